@@ -98,8 +98,16 @@ typedef enum {
   MGG_OP_GROUPED_GEMM = 3,
   MGG_OP_MASKED = 4,
   MGG_OP_FFN_FORWARD = 5,
-  MGG_OP_FFN_BACKWARD = 6
+  MGG_OP_FFN_BACKWARD = 6,
+  MGG_OP_LAYER_NORM_BACKWARD = 7,
+  MGG_OP_LINEAR_BACKWARD = 8
 } mgg_op;
+
+/* How mgg_select_experts scores the logits. */
+typedef enum { MGG_SCORE_SOFTMAX = 0, MGG_SCORE_SIGMOID = 1 } mgg_scoring;
+
+/* Activation of mgg_linear_forward: GELU is z (1 + erf(z / sqrt 2)) / 2. */
+typedef enum { MGG_ACT_NONE = 0, MGG_ACT_RELU = 1, MGG_ACT_SILU = 2, MGG_ACT_GELU = 3 } mgg_activation;
 
 /* Bits the kernels OR into *dev_status. */
 #define MGG_DEV_BAD_EXPERT_ID 0x1 /* an expert id outside [0, E): assignment skipped */
@@ -164,6 +172,8 @@ mgg_status mgg_tile_config(mgg_op op, mgg_dtype dtype, int* BM, int* BN, int* BK
  *   MGG_OP_MASKED                : 0 (no workspace)
  *   MGG_OP_FFN_FORWARD           : T, k, E (N = H, K = F unused)
  *   MGG_OP_FFN_BACKWARD          : T, k, E, N = H, K = F, dtype (bf16)
+ *   MGG_OP_LAYER_NORM_BACKWARD   : T, K
+ *   MGG_OP_LINEAR_BACKWARD       : T, N
  */
 size_t mgg_workspace_bytes(mgg_op op, int T, int k, int E, int N, int K, mgg_dtype dtype);
 
@@ -538,6 +548,137 @@ mgg_status mgg_debug_wait_timeout(int32_t* dev_status, long long limit_cycles, v
  * n > 8.
  */
 mgg_status mgg_set_kernel_events(void* const* events, int n);
+
+/* ------------------------------------------------------------------------
+ * The layers around the experts of a MoE transformer block: layer norm, the
+ * choice of the experts from the gate's logits, and dense products (the gate
+ * itself, a shared expert, the residual stream).  The pages have no
+ * counterpart; the conventions above hold, with these additions: a matrix
+ * argument named with an ld has rows ld elements apart (ld >= its columns),
+ * the others are dense; T = 0 is accepted (nothing is read; weight and bias
+ * gradients become zero).
+ */
+
+/*
+ * Layer norm over the last dimension:
+ *   mean[t] = sum_k x[t, k] / K
+ *   rstd[t] = 1 / sqrt(sum_k (x[t, k] - mean[t])^2 / K + eps)
+ *   y[t, k] = (x[t, k] - mean[t]) * rstd[t] * weight[k] + bias[k]
+ *   x [T, K] (x_dtype, rows ldx apart), weight and bias [K] (w_dtype; bias
+ *   may be NULL), y [T, K] (y_dtype), mean and rstd [T] f32 (the backward's
+ *   saved context).  Dtypes: MGG_BF16 or MGG_F32 each.  Any K >= 1 and any
+ *   element-aligned pointers; rows on 16-byte boundaries move in 16-byte
+ *   pieces.  Sums are f32.
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, K < 1, ldx < K, eps negative or
+ * not finite), MGG_ERR_DTYPE, MGG_ERR_ALIGNMENT (a pointer not aligned to
+ * its element), MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
+ */
+mgg_status mgg_layer_norm_forward(const void* x, mgg_dtype x_dtype, int64_t ldx, const void* weight,
+                                  const void* bias, mgg_dtype w_dtype, int T, int K, float eps,
+                                  void* y, mgg_dtype y_dtype, float* mean, float* rstd,
+                                  void* stream);
+
+/*
+ * Gradient of L = sum(dy * y), with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx[t, k]   = rstd[t] * (g[t, k] - sum_k g[t, k] / K - xh[t, k] * sum_k (g xh)[t, k] / K)
+ *   dweight[k] = sum_t dy[t, k] * xh[t, k],   dbias[k] = sum_t dy[t, k]
+ *   dy [T, K] (y_dtype), dx [T, K] (x_dtype), dweight and dbias [K]
+ *   (w_dtype; dbias may be NULL).  Overwritten.  The column sums are formed
+ *   in a fixed order: equal inputs give equal bits.
+ * ws: mgg_workspace_bytes(MGG_OP_LAYER_NORM_BACKWARD, T, 0, 0, 0, K, ...).
+ * Errors as for the forward, and MGG_ERR_WORKSPACE.
+ */
+mgg_status mgg_layer_norm_backward(const void* dy, mgg_dtype y_dtype, const void* x,
+                                   mgg_dtype x_dtype, int64_t ldx, const void* weight,
+                                   mgg_dtype w_dtype, const float* mean, const float* rstd, int T,
+                                   int K, void* dx, void* dweight, void* dbias, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Most experts per token mgg_select_experts chooses. */
+#define MGG_MAX_TOPK 32
+
+/*
+ * The choice of k experts per token and their weights, from the gate's
+ * logits [T, E] (dtype MGG_BF16 or MGG_F32, rows ldl apart):
+ *   softmax: p = softmax over the token's unmasked logits; the experts are
+ *            ordered by logit (with a bias: by p + bias)
+ *   sigmoid: p = 1 / (1 + exp(-logit)); ordered by p (+ bias)
+ *   bias [E] f32 or NULL: moves the order only, never the weights.
+ *   groups > 1: the experts form `groups` equal runs; a group's score is its
+ *   best expert's key (softmax) or the sum of its two best (sigmoid), and
+ *   only the topk_groups best groups take part.
+ *   expert_ids   [T, k] int32: the k best, best first; equal keys (and equal
+ *                group scores) go to the lowest index
+ *   topk_weights [T, k] f32: scale * p, or scale * p / (sum of the chosen p)
+ *                with renormalize
+ * A logit that is NaN, -inf or its type's lowest finite value masks the
+ * expert; +inf counts as the largest finite f32.  When fewer than k experts
+ * are left, masked ones (and those of other groups) fill the row, lowest
+ * index first, with weight 0: the ids of a row are always valid and distinct.
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, E < 1, E > MGG_MAX_EXPERTS,
+ * k < 1, k > MGG_MAX_TOPK, k > experts in topk_groups groups, ldl < E,
+ * groups < 1 or > 32 or not dividing E, topk_groups outside 1..groups, scale
+ * not finite or not positive, unknown scoring), MGG_ERR_DTYPE,
+ * MGG_ERR_ALIGNMENT, MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
+ */
+mgg_status mgg_select_experts(const void* logits, mgg_dtype dtype, int64_t ldl, int T, int E, int k,
+                              mgg_scoring scoring, const float* bias, int groups, int topk_groups,
+                              int renormalize, float scale, int32_t* expert_ids,
+                              float* topk_weights, void* stream);
+
+/*
+ * Gradient of L = sum(dtopk * topk_weights) to the logits, the choice held
+ * fixed (the order has no gradient, and so neither has the bias):
+ *   dlogits [T, E] (dtype, dense), overwritten whole.
+ * expert_ids and topk_weights are the forward's; a choice of weight 0 takes
+ * no part, and its dtopk may hold anything.  An id outside [0, E) sets
+ * MGG_DEV_BAD_EXPERT_ID and takes no part.
+ */
+mgg_status mgg_select_experts_backward(const float* dtopk, const void* logits, mgg_dtype dtype,
+                                       int64_t ldl, const int32_t* expert_ids,
+                                       const float* topk_weights, int T, int E, int k,
+                                       mgg_scoring scoring, int renormalize, float scale,
+                                       void* dlogits, int32_t* dev_status, void* stream);
+
+/*
+ * Dense product with its epilogue:
+ *   z[t, n] = sum_k x[t, k] W[n, k] + bias[n]
+ *   out     = act(z) + residual
+ *   x [T, K] bf16 (rows ldx apart), W [N, K] bf16 stored like nn.Linear, bias
+ *   [N] (bias_dtype) or NULL, residual [T, N] (residual_dtype, rows ldr apart)
+ *   or NULL, out [T, N] (out_dtype), pre [T, N] bf16 or NULL: z rounded, the
+ *   backward's saved context.  residual may be out itself (same dtype, ldr =
+ *   N); no other argument may overlap an output.
+ * K % 8 == 0, ldx % 8 == 0 and x, W 16-byte aligned (MGG_ERR_ALIGNMENT); any
+ * N >= 1.  f32 accumulation; equal inputs give equal bits.
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, K < 1, N < 1, ldx < K, ldr < N,
+ * unknown activation), MGG_ERR_DTYPE, MGG_ERR_ALIGNMENT,
+ * MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.  A pipeline wait that runs out sets
+ * MGG_DEV_TIMEOUT in *dev_status.
+ */
+mgg_status mgg_linear_forward(const void* x, int64_t ldx, const void* W, const void* bias,
+                              mgg_dtype bias_dtype, const void* residual, mgg_dtype residual_dtype,
+                              int64_t ldr, int T, int K, int N, mgg_activation activation,
+                              void* out, mgg_dtype out_dtype, void* pre, int32_t* dev_status,
+                              void* stream);
+
+/*
+ * Gradient of L = sum(dy * out) (the residual's gradient is dy itself):
+ *   dz = dy * act'(pre)
+ *   dx [T, K] bf16 = dz W,  dW [N, K] bf16 = dz^T x,  dbias [N] (bias_dtype)
+ *   = sum_t dz; each may be NULL and is then not computed.
+ *   dy [T, N] (dy_dtype, rows lddy apart); pre [T, N] bf16, the forward's
+ *   (NULL with MGG_ACT_NONE).  The products' operand is bf16(dz), as in the
+ *   library's other backward GEMMs; dbias sums the unrounded dz in f32.
+ * Alignment as for the forward.  ws: mgg_workspace_bytes(
+ * MGG_OP_LINEAR_BACKWARD, T, 0, 0, N, ...).  Errors as for the forward, and
+ * MGG_ERR_WORKSPACE.
+ */
+mgg_status mgg_linear_backward(const void* dy, mgg_dtype dy_dtype, int64_t lddy, const void* x,
+                               int64_t ldx, const void* W, const void* pre,
+                               mgg_activation activation, int T, int K, int N, void* dx, void* dW,
+                               void* dbias, mgg_dtype bias_dtype, int32_t* dev_status, void* ws,
+                               size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,4 +13,8 @@ from .ops import (  # noqa: F401
     quantize_fp8, moe_forward_fp8, grouped_gemm_fp8, grouped_gemm_masked_fp8,
     quantize_fp8_cols, moe_backward_dx_fp8,
 )
+from .block import (  # noqa: F401
+    layer_norm, layer_norm_backward, layer_norm_forward, linear, linear_backward, linear_forward,
+    router, select_experts, select_experts_backward,
+)
 from . import _lib  # noqa: F401

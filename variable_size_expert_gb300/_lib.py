@@ -35,11 +35,22 @@ MGG_OP_GROUPED_GEMM = 3
 MGG_OP_MASKED = 4
 MGG_OP_FFN_FORWARD = 5
 MGG_OP_FFN_BACKWARD = 6
+MGG_OP_LAYER_NORM_BACKWARD = 7
+MGG_OP_LINEAR_BACKWARD = 8
+# mgg_scoring
+MGG_SCORE_SOFTMAX = 0
+MGG_SCORE_SIGMOID = 1
+# mgg_activation
+MGG_ACT_NONE = 0
+MGG_ACT_RELU = 1
+MGG_ACT_SILU = 2
+MGG_ACT_GELU = 3
 # device status bits
 MGG_DEV_BAD_EXPERT_ID = 0x1
 MGG_DEV_BAD_OFFSETS = 0x2
 MGG_DEV_TIMEOUT = 0x4
 MGG_MAX_EXPERTS = 1024
+MGG_MAX_TOPK = 32
 MGG_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 # every exported symbol of include/mgg.h
@@ -49,7 +60,9 @@ EXPORTS = (
     "mgg_set_kernel_events", "mgg_route_noalloc", "mgg_moe_ffn_forward", "mgg_quantize_fp8",
     "mgg_grouped_gemm_fp8", "mgg_moe_forward_fp8", "mgg_moe_ffn_backward",
     "mgg_debug_wait_timeout", "mgg_debug_row_tile", "mgg_quantize_fp8_cols",
-    "mgg_moe_backward_dx_fp8",
+    "mgg_moe_backward_dx_fp8", "mgg_layer_norm_forward", "mgg_layer_norm_backward",
+    "mgg_select_experts", "mgg_select_experts_backward", "mgg_linear_forward",
+    "mgg_linear_backward",
 )
 
 
@@ -69,6 +82,8 @@ class Routing(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_int64
+_F = ctypes.c_float
 _RP = ctypes.POINTER(Routing)
 
 _SIGS = {
@@ -96,6 +111,19 @@ _SIGS = {
     "mgg_moe_forward_fp8": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _RP, _P, _P, _SZ,
                                  _P]),
 }
+
+_SIGS.update({
+    "mgg_layer_norm_forward": (_I, [_P, _I, _LL, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P, _P]),
+    "mgg_layer_norm_backward": (_I, [_P, _I, _P, _I, _LL, _P, _I, _P, _P, _I, _I, _P, _P, _P, _P,
+                                     _SZ, _P]),
+    "mgg_select_experts": (_I, [_P, _I, _LL, _I, _I, _I, _I, _P, _I, _I, _I, _F, _P, _P, _P]),
+    "mgg_select_experts_backward": (_I, [_P, _P, _I, _LL, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P,
+                                         _P]),
+    "mgg_linear_forward": (_I, [_P, _LL, _P, _P, _I, _P, _I, _LL, _I, _I, _I, _I, _P, _I, _P, _P,
+                                _P]),
+    "mgg_linear_backward": (_I, [_P, _I, _LL, _P, _LL, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P,
+                                 _P, _SZ, _P]),
+})
 
 _lib = None
 

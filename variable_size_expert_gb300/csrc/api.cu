@@ -25,28 +25,6 @@ int g_arch_ok[kMaxDevices] = {};  // 0 unknown, 1 sm_103, -1 other
 
 bool current_device(int* dev) { return cudaGetDevice(dev) == cudaSuccess && *dev >= 0 && *dev < kMaxDevices; }
 
-mgg_status check_arch() {
-  int dev = 0;
-  if (!current_device(&dev)) return MGG_ERR_CUDA;
-  if (g_arch_ok[dev] == 0) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-      return MGG_ERR_CUDA;
-    g_arch_ok[dev] = (major == 10 && minor == 3) ? 1 : -1;
-  }
-  return g_arch_ok[dev] == 1 ? MGG_OK : MGG_ERR_UNSUPPORTED_ARCH;
-}
-
-long long wait_limit() {
-  static long long lim = [] {
-    const char* s = getenv("MGG_WAIT_LIMIT");
-    const long long v = s ? atoll(s) : 0;
-    return v > 0 ? v : kDefaultWaitLimit;
-  }();
-  return lim;
-}
-
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -311,6 +289,28 @@ mgg_status check_moe_sizes(int T, int K, int N, int E, int k, mgg_dtype dt) {
 
 }  // namespace
 
+mgg_status check_arch() {
+  int dev = 0;
+  if (!current_device(&dev)) return MGG_ERR_CUDA;
+  if (g_arch_ok[dev] == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+      return MGG_ERR_CUDA;
+    g_arch_ok[dev] = (major == 10 && minor == 3) ? 1 : -1;
+  }
+  return g_arch_ok[dev] == 1 ? MGG_OK : MGG_ERR_UNSUPPORTED_ARCH;
+}
+
+long long wait_limit() {
+  static long long lim = [] {
+    const char* s = getenv("MGG_WAIT_LIMIT");
+    const long long v = s ? atoll(s) : 0;
+    return v > 0 ? v : kDefaultWaitLimit;
+  }();
+  return lim;
+}
+
 int num_sms() {
   int dev = 0;
   if (!current_device(&dev)) return 1;
@@ -339,6 +339,20 @@ bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* d
          const_cast<void*>(base), d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
+  if (!fn) return false;
+  cuuint64_t d[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t st[1] = {static_cast<cuuint64_t>(cols) * (f32 ? 4 : 2)};
+  cuuint32_t b[2] = {f32 ? 32u : 64u, 32};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d,
+         st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -419,6 +433,14 @@ mgg_status mgg_tile_config(mgg_op op, mgg_dtype dtype, int* BM, int* BN, int* BK
       *BN = kPairBN;
       *BK = kBK;
       return MGG_OK;
+    case MGG_OP_LAYER_NORM_BACKWARD:  // no tiles
+      return MGG_ERR_DTYPE;
+    case MGG_OP_LINEAR_BACKWARD:
+      if (!bf) return MGG_ERR_DTYPE;
+      *BM = kPairBM;
+      *BN = kPairBN;
+      *BK = kBK;
+      return MGG_OK;
   }
   return MGG_ERR_DTYPE;
 }
@@ -446,6 +468,12 @@ size_t mgg_workspace_bytes(mgg_op op, int T, int k, int E, int N, int K, mgg_dty
       if (T < 1 || k < 1 || E < 1 || E > kMaxExperts || N < 1 || K < 1) return 0;
       if (dtype != MGG_BF16) return 0;
       return ffn_bwd_layout(T, k, E, N, K).total;
+    case MGG_OP_LAYER_NORM_BACKWARD:
+      if (T < 1 || K < 1) return 0;
+      return round256(static_cast<size_t>(2) * norm_bwd_blocks() * K * 4);
+    case MGG_OP_LINEAR_BACKWARD:
+      if (T < 1 || N < 1) return 0;
+      return dense_bwd_ws_bytes(T, N);
   }
   return 0;
 }

@@ -9,6 +9,8 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "../../include/mgg.h"
+
 namespace mgg {
 
 // An NVTX range over one C-ABI call, named after the entry point, so that
@@ -160,12 +162,88 @@ struct MaskedParams {
   long long wait_limit;
 };
 
+// Activations of the dense products (the values of mgg_activation).
+enum DenseAct { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+
+// A bf16 operand [rows][cols], row stride ld elements.
+struct DenseOperand {
+  const void* ptr;
+  int rows, cols;
+  long long ld;
+};
+// D[M, N] = sum_k A[m, k] B[n, k]; a_mn / b_mn: the operand lies [k][m] / [k][n].
+struct DenseProduct {
+  int M, N, Kc;
+  bool a_mn, b_mn;
+  void* out;        // [M, N] dense
+  bool out_f32;     // else bf16
+  bool out_tma;     // rows of out start on 16-byte boundaries (set by the launcher)
+  bool epilogue;    // bias, activation, residual, z kept
+  int tiles;        // set by the launcher
+};
+struct DenseParams {
+  DenseProduct pr[2];
+  const void* bias;      // [N] or null
+  bool bias_f32;
+  int act;
+  const void* residual;  // [M, ldr] or null
+  bool res_f32, res_vec; // res_vec: 16-byte loads
+  long long ldr;
+  void* pre;             // bf16 z [M, N] or null
+  bool pre_tma;          // set by the launcher
+  int32_t* dev_status;
+  long long wait_limit;
+};
+struct DenseBackward {
+  const void* dy;
+  bool dy_f32;
+  long long lddy;
+  const void* x;
+  long long ldx;
+  const void* W;
+  const void* pre;
+  int act;
+  int T, K, N;
+  void *dx, *dW, *db;    // any may be null
+  bool db_f32;
+  int32_t* dev_status;
+  long long wait_limit;
+};
+
 // device properties
 int num_sms();
+// null-safe argument checks shared by the C-ABI translation units
+mgg_status check_arch();
+long long wait_limit();
 
 // tensor maps
 bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box);
+
+// [rows][cols] bf16 or f32 output for TMA stores of 32 rows x 128 bytes, 128-byte swizzle
+bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols);
+
+// norm.cu
+int norm_bwd_blocks();  // partial rows of the weight and bias gradients
+cudaError_t launch_norm_fwd(const void* x, bool x_f32, long long ldx, const void* w, const void* b,
+                            bool w_f32, int T, int K, float eps, void* y, bool y_f32, float* mean,
+                            float* rstd, cudaStream_t st);
+cudaError_t launch_norm_bwd(const void* dy, bool y_f32, const void* x, bool x_f32, long long ldx,
+                            const void* w, bool w_f32, const float* mean, const float* rstd, int T,
+                            int K, void* dx, void* dw, void* db, float* part, cudaStream_t st);
+// select.cu
+cudaError_t launch_select(const void* logits, bool f32, long long ldl, int T, int E, int k,
+                          bool softmax, const float* bias, int groups, int topk_groups,
+                          bool renorm, float scale, int32_t* ids, float* weights, cudaStream_t st);
+cudaError_t launch_select_bwd(const float* g, const void* logits, bool f32, long long ldl,
+                              const int32_t* ids, const float* w, int T, int E, int k,
+                              bool softmax, bool renorm, float scale, void* out,
+                              int32_t* dev_status, cudaStream_t st);
+// linear.cu
+size_t dense_bwd_ws_bytes(int T, int N);
+cudaError_t launch_dense_forward(const DenseParams& p, const DenseOperand& x,
+                                 const DenseOperand& W, cudaStream_t st);
+cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t st);
 
 // router.cu
 cudaError_t launch_route(const int32_t* ids, const float* w, int T, int k, int E, int BM,

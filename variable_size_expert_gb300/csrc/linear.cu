@@ -1,0 +1,988 @@
+// Dense products on the tensor cores (tcgen05, bf16 operands, f32
+// accumulation in tensor memory) for the layers around the experts:
+//   forward   z = x W^T + b;  out = act(z) + residual
+//   backward  dz = dy act'(z) (bf16);  dx = dz W;  dW = dz^T x;  db = sum_t dz
+//
+// Every product is D[M, N] = sum_k A[m, k] B[n, k] over operands that lie in
+// memory either with k contiguous ("K-major": x and W in the forward, dz in
+// dx) or with m / n contiguous ("MN-major": W in dx, dz and x in dW); TMA
+// loads both kinds as 128-byte-swizzled blocks of 64 and the matrix
+// descriptors say which it is.  No operand is transposed in memory.
+//
+// Two kernels:
+//  dense_pair_kernel  persistent, one cluster of two CTAs per SM pair, tiles
+//    of 256 x 256 (MMA M = 256, N = 256, cta_group::2: each SM holds 128 rows
+//    of A and of B, so a tile costs each SM half the bytes of a single-CTA
+//    tile).  Two accumulators in tensor memory, so the epilogue of a tile
+//    runs under the next tile's MMAs.  A launch takes the tiles of up to two
+//    products: the backward runs dx and dW as one tile space, whose last
+//    round is the only partly filled one.
+//  dense_cta_kernel  one tile of 128 x BN (BN 16..256) per cluster of S CTAs,
+//    which split the contraction and add their partial accumulators through
+//    distributed shared memory in rank order (the same bits every time).  For
+//    products with too few 256 x 256 tiles to fill the GPU: a decode step's
+//    few tokens, the gate's few columns.  The longer of the two output sides
+//    lies on the MMA's 128 rows, so that the shorter costs only its own width.
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mgg {
+namespace {
+
+constexpr int BK = kBK;                 // contraction step: one 128-byte row of bf16
+constexpr int kHalf = 128;              // rows of A, and of B, per CTA and stage of a pair
+constexpr int STAGES = 6;
+constexpr int OPER = kHalf * BK * 2;    // 16 KB
+constexpr int CHUNK = 64 * BK * 2;      // 8 KB: 64 wide MN-major block of one stage
+constexpr int EPI_BUF = 32 * 128;       // one warp's staged block: 32 rows x 128 bytes
+constexpr int kThreads = 192;           // warps 0-3 epilogue, 4 MMA, 5 TMA
+constexpr int kMeta = 512;
+constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + 8 * EPI_BUF + kMeta;
+static_assert(kPairSmem <= 232448, "shared memory per block");
+constexpr long long DRAIN_LIMIT = 200000000LL;
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::
+                   "l"(map),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// ---------------------------------------------------------------- epilogue math
+// z -> act(z).  expf / erff are CUDA's own, the divisions IEEE: f32 outputs
+// keep f32 accuracy.
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+  if constexpr (ACT == kActRelu) return fmaxf(z, 0.f);
+  if constexpr (ACT == kActSilu) return z / (1.f + expf(-z));
+  if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  return z;
+}
+// act'(z)
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
+  if constexpr (ACT == kActSilu) {
+    const float s = 1.f / (1.f + expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  if constexpr (ACT == kActGelu)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
+           z * (0.39894228040143268f * expf(-0.5f * z * z));
+  return 1.f;
+}
+
+template <int N>
+__device__ __forceinline__ void act_all(int act, float (&v)[N]) {
+  if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_f<kActRelu>(v[i]);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_f<kActSilu>(v[i]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_f<kActGelu>(v[i]);
+  }
+}
+
+__device__ __forceinline__ float load_any(const void* p, bool f32, long long i) {
+  return f32 ? static_cast<const float*>(p)[i]
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// ---------------------------------------------------------------- pair kernel
+struct PairMaps {
+  CUtensorMap a[2], b[2], out[2], pre;
+};
+
+struct PSmem {
+  uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, issued;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+};
+__device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
+  PSmem m;
+  const uint32_t raw_addr = smem_u32(raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* g = raw + (base - raw_addr);
+  m.sA = base;
+  m.sB = m.sA + STAGES * OPER;
+  m.sEpi = m.sB + STAGES * OPER;
+  m.full = m.sEpi + 8 * EPI_BUF;
+  m.empty = m.full + 8 * STAGES;
+  m.acc_full = m.empty + 8 * STAGES;
+  m.acc_empty = m.acc_full + 16;
+  m.drain = m.acc_empty + 16;
+  m.pdone = m.drain + 8;
+  m.issued = m.pdone + 8;
+  m.tmem_slot = reinterpret_cast<uint32_t*>(g + (m.issued + 8 - base));
+  m.abort_flag = reinterpret_cast<volatile int*>(m.tmem_slot + 1);
+  return m;
+}
+
+struct PTile {
+  int q;           // product
+  int m0, n0;      // first row and column
+  int nkb;
+};
+// Tiles are walked in bands of kBand row blocks, down the band first: the
+// tiles in flight at one time then cover about kBand x 9 blocks, the squarest
+// set of operand rows for the L2 to hold.
+constexpr int kBand = 8;
+__device__ __forceinline__ PTile decode_pair(const DenseParams& p, int tau) {
+  PTile t;
+  t.q = tau >= p.pr[0].tiles ? 1 : 0;
+  const DenseProduct& d = p.pr[t.q];
+  const int local = tau - (t.q ? p.pr[0].tiles : 0);
+  const int tm = cdiv(d.M, 256), tn = cdiv(d.N, 256);
+  const int band = local / (kBand * tn);
+  const int r = local - band * kBand * tn;
+  const int rows = min(kBand, tm - band * kBand);
+  t.n0 = (r / rows) * 256;
+  t.m0 = (band * kBand + r % rows) * 256;
+  t.nkb = cdiv(d.Kc, BK);
+  return t;
+}
+
+// One operand's rows of a stage: 128 rows from r0, contraction step kb.
+__device__ __forceinline__ void load_oper(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                          bool mn, int r0, int kb) {
+  if (mn) {
+    tma_load_2d_cg2(dst, map, bar, r0, kb * BK);
+    tma_load_2d_cg2(dst + CHUNK, map, bar, r0 + 64, kb * BK);
+  } else {
+    tma_load_2d_cg2(dst, map, bar, kb * BK, r0);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ DenseParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const PSmem m = carve_pair(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (warp == 5 && lane == 0) {
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
+  }
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(m.full + 8 * s, 2);  // both TMA threads announce their own bytes
+      mbar_init(m.empty + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(m.acc_full + 8 * a, 1);
+      mbar_init(m.acc_empty + 8 * a, 8);  // the epilogue warps of both CTAs
+    }
+    mbar_init(m.drain, 1);
+    mbar_init(m.pdone, 1);
+    *m.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc_cg2(smem_u32(m.tmem_slot), 512);
+    tmem_relinquish_cg2();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *m.tmem_slot;
+  pdl_wait();
+  const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
+  const int total = p.pr[0].tiles + p.pr[1].tiles;
+  const uint32_t full_l = mapa_shared(m.full, 0);
+  const uint32_t acc_empty_l = mapa_shared(m.acc_empty, 0);
+
+  if (warp == 5) {
+    // ------------------------------------------------ TMA
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tau = pair; ok && tau < total; tau += npairs) {
+        const PTile t = decode_pair(p, tau);
+        const DenseProduct& d = p.pr[t.q];
+        const int ar = t.m0 + static_cast<int>(rank) * kHalf;
+        const int br = t.n0 + static_cast<int>(rank) * kHalf;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          const int s = it % STAGES;
+          if (!wait_bar(m.empty + 8 * s, ((it / STAGES) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = full_l + 8 * s;
+          if (leader) mbar_arrive_expect_tx(m.full + 8 * s, 2 * OPER);
+          load_oper(m.sA + s * OPER, &maps.a[t.q], fb, d.a_mn, ar, kb);
+          load_oper(m.sB + s * OPER, &maps.b[t.q], fb, d.b_mn, br, kb);
+          if (!leader) mbar_arrive_expect_tx_cluster(fb, 2 * OPER);
+          ++it;
+        }
+      }
+      // Every copy lands before either CTA may exit: the peer reports how
+      // many stages it issued; for the stages that one side did not issue
+      // (only after a timeout) the leader makes that side's arrival and
+      // waits for the phase, which completes once the issued copies landed.
+      if (!leader) {
+        st_cluster_s32(mapa_shared(m.issued, 0), it);
+        mbar_arrive_cluster(mapa_shared(m.pdone, 0));
+      } else {
+        const bool rep = wait_bar_cluster_drain(m.pdone, 0, DRAIN_LIMIT);
+        const int other = rep ? ld_shared_s32(m.issued) : it;
+        const int hi = std::max(it, other);
+        for (int j = std::max(0, hi - STAGES); j < hi; ++j) {
+          const uint32_t b = m.full + 8 * (j % STAGES);
+          if (j >= it) mbar_arrive(b);
+          if (j >= other) mbar_arrive(b);
+          wait_bar_drain(b, (j / STAGES) & 1, DRAIN_LIMIT);
+        }
+      }
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------ MMA issue
+    if (leader && lane == 0) {
+      int it = 0, tcount = 0;
+      bool ok = true;
+      for (int tau = pair; ok && tau < total; tau += npairs) {
+        const PTile t = decode_pair(p, tau);
+        const DenseProduct& d = p.pr[t.q];
+        const uint32_t idesc = idesc_bf16_f32(256, 256, d.a_mn, d.b_mn);
+        // per 16 of the contraction: 32 bytes along a K-major row, 16 rows
+        // of 128 bytes down an MN-major block
+        const uint32_t a_step = d.a_mn ? 16 * 128 : 32, b_step = d.b_mn ? 16 * 128 : 32;
+        const uint32_t a_lbo = d.a_mn ? CHUNK : 16, b_lbo = d.b_mn ? CHUNK : 16;
+        const int acc = tcount & 1;
+        if (!wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)) break;
+        tc_fence_after();
+        const uint32_t dt = tmem_base + acc * 256;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          const int s = it % STAGES;
+          if (!wait_bar(m.full + 8 * s, (it / STAGES) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = m.sA + s * OPER, b0 = m.sB + s * OPER;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc_mma_bf16_cg2(dt, sw128_desc(a0 + kk * a_step, a_lbo, 1024),
+                            sw128_desc(b0 + kk * b_step, b_lbo, 1024), idesc, (kb | kk) != 0);
+          tc_commit_cg2_mc(m.empty + 8 * s, 0x3);
+          ++it;
+        }
+        if (!ok) break;
+        tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
+        ++tcount;
+      }
+      tc_commit_cg2(m.drain);
+      wait_bar_drain(m.drain, 0, DRAIN_LIMIT);
+    }
+  } else {
+    // ------------------------------------------------ epilogue
+    // Warp w holds rows 32 w .. +31 of this CTA's 128, lane i row i.  A block
+    // of 128 bytes per row (64 bf16 or 32 f32 columns) is staged in the TMA
+    // store's 128-byte swizzle (conflict-free: the lanes of a quarter warp
+    // write eight different 16-byte columns) and leaves with one store
+    // instruction; two buffers per warp alternate.
+    const uint32_t stg = m.sEpi + warp * 2 * EPI_BUF;
+    const int row_w = static_cast<int>(rank) * kHalf + warp * 32;
+    int tcount = 0, nst = 0;
+    for (int tau = pair; tau < total; tau += npairs) {
+      const PTile t = decode_pair(p, tau);
+      const DenseProduct& d = p.pr[t.q];
+      const int row0 = t.m0 + row_w;
+      const int row = row0 + lane;
+      const int acc = tcount & 1;
+      if (!__all_sync(0xffffffffu, wait_bar(m.acc_full + 8 * acc, (tcount >> 1) & 1, wc))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + acc * 256;
+      const int nblk = std::min(8, cdiv(d.N - t.n0, 32));  // 32-column blocks
+      // stage 32 columns of v as bf16 (half a block) or f32 (a block)
+      auto put = [&](uint32_t buf, const float(&v)[32], bool f32, int half) {
+        if (f32) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared_v4(buf + sw128_offset(lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2],
+                         v[4 * c + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_shared_v4(buf + sw128_offset(lane, half * 4 + c),
+                         __uint_as_float(pack_bf16x2_rn(v[8 * c], v[8 * c + 1])),
+                         __uint_as_float(pack_bf16x2_rn(v[8 * c + 2], v[8 * c + 3])),
+                         __uint_as_float(pack_bf16x2_rn(v[8 * c + 4], v[8 * c + 5])),
+                         __uint_as_float(pack_bf16x2_rn(v[8 * c + 6], v[8 * c + 7])));
+        }
+      };
+      // a staged block to columns c0.. of rows row0..
+      auto flush = [&](uint32_t buf, const CUtensorMap* map, bool tma, void* base, int ld, bool f32,
+                       int c0) {
+        if (tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row0 < d.M) {
+            tma_store_2d(map, buf, c0, row0);
+          }
+          if (lane == 0) bulk_commit();
+        } else {
+          // rows that do not start on 16-byte boundaries: element by element,
+          // a row at a time
+          __syncwarp();
+          const int per = f32 ? 32 : 64;
+          for (int r = 0; r < 32 && row0 + r < d.M; ++r)
+            for (int c = lane; c < per; c += 32) {
+              if (c0 + c >= d.N) continue;
+              const uint32_t at = buf + sw128_offset(r, c / (per / 8));
+              const long long o = static_cast<long long>(row0 + r) * ld + c0 + c;
+              if (f32) {
+                static_cast<float*>(base)[o] = __int_as_float(ld_shared_s32(at + (c & 3) * 4));
+              } else {
+                const uint32_t u = static_cast<uint32_t>(ld_shared_s32(at + ((c & 7) >> 1) * 4));
+                static_cast<unsigned short*>(base)[o] =
+                    static_cast<unsigned short>(c & 1 ? u >> 16 : u);
+              }
+            }
+          __syncwarp();
+        }
+      };
+      // With z kept, its block lies in the first buffer and the output's in
+      // the second; else the output's blocks alternate.
+      const bool keep = d.epilogue && p.pre;
+      auto next_buf = [&](bool is_pre) {
+        uint32_t b = stg;
+        if (keep) {
+          if (!is_pre) b += EPI_BUF;
+          if (lane == 0) bulk_wait_read<0>();
+        } else {
+          b += (nst & 1) * EPI_BUF;
+          ++nst;
+          if (lane == 0) bulk_wait_read<1>();  // the store two blocks ago has read it
+        }
+        __syncwarp();
+        return b;
+      };
+      uint32_t obuf = 0, pbuf = 0;
+#pragma unroll 1
+      for (int b = 0; b < nblk; ++b) {
+        float v[32];
+        tmem_ld32(taddr + b * 32, v);
+        tmem_ld_wait();
+        if (b == nblk - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
+        }
+        const int c0 = t.n0 + b * 32;
+        const bool last = b == nblk - 1;
+        if (d.epilogue) {
+          if (p.bias) {
+            const float bl = c0 + lane < d.N ? load_any(p.bias, p.bias_f32, c0 + lane) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bl, i);
+          }
+          if (keep) {
+            if ((b & 1) == 0) pbuf = next_buf(true);
+            put(pbuf, v, false, b & 1);
+            if ((b & 1) || last) flush(pbuf, &maps.pre, p.pre_tma, p.pre, d.N, false, c0 - (b & 1) * 32);
+          }
+          act_all<32>(p.act, v);
+          if (p.residual && row < d.M) {
+            const long long ro = static_cast<long long>(row) * p.ldr + c0;
+            if (p.res_vec && c0 + 32 <= d.N) {
+              if (p.res_f32) {
+                const float4* r4 = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + ro);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 x = r4[i];
+                  v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+                }
+              } else {
+                const uint4* r4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint4 x = r4[i];
+                  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    v[8 * i + 2 * j] += __uint_as_float(u[j] << 16);
+                    v[8 * i + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c0 + i < d.N) v[i] += load_any(p.residual, p.res_f32, ro + i);
+            }
+          }
+        }
+        if (d.out_f32) {
+          obuf = next_buf(false);
+          put(obuf, v, true, 0);
+          flush(obuf, &maps.out[t.q], d.out_tma, d.out, d.N, true, c0);
+        } else {
+          if ((b & 1) == 0) obuf = next_buf(false);
+          put(obuf, v, false, b & 1);
+          if ((b & 1) || last)
+            flush(obuf, &maps.out[t.q], d.out_tma, d.out, d.N, false, c0 - (b & 1) * 32);
+        }
+      }
+      ++tcount;
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_cg2(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- single-CTA tiles, split contraction
+struct CtaMaps {
+  CUtensorMap a, b;
+};
+struct CtaParams {
+  DenseProduct d;
+  int swap;        // the tile's 128 rows run along the output's columns
+  int Mr, Nc;      // extents along the tile's rows and columns
+  int BN;          // tile columns (16..256, a multiple of 16)
+  int splits;      // CTAs per cluster: pieces of the contraction
+  int stages;
+  int b_bytes;     // B bytes per stage
+  int tmem_cols;
+  int vec_out, vec_pre;  // 16-byte stores of 8 columns
+};
+
+__global__ void __launch_bounds__(kThreads)
+    dense_cta_kernel(const __grid_constant__ CtaMaps maps, const __grid_constant__ CtaParams c,
+                     const __grid_constant__ DenseParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw_addr);
+  const int stage_bytes = OPER + c.b_bytes;
+  const uint32_t meta = base + std::max(c.stages * stage_bytes, c.splits > 1 ? c.BN * 512 : 0);
+  const uint32_t full = meta, empty = meta + 64, acc_full = meta + 128;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (meta + 136 - base));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = c.splits;
+  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / S;
+  const int tr = cdiv(c.Mr, 128);
+  const int m0 = (tile % tr) * 128, n0 = (tile / tr) * c.BN;
+  const int nkb = cdiv(c.d.Kc, BK);
+  const int kb0 = static_cast<int>(static_cast<long long>(rank) * nkb / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(rank + 1) * nkb / S);
+
+  if (warp == 5 && lane == 0) {
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+  }
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < c.stages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), c.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
+
+  if (warp == 5) {
+    if (lane == 0) {
+      int issued = 0, s = 0, ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bar(empty + 8 * s, ph ^ 1, wc)) break;
+        const uint32_t fb = full + 8 * s;
+        const uint32_t a = base + s * stage_bytes, b = a + OPER;
+        mbar_arrive_expect_tx(fb, stage_bytes);
+        if (c.d.a_mn) {
+          tma_load_2d(a, &maps.a, fb, m0, kb * BK);
+          tma_load_2d(a + CHUNK, &maps.a, fb, m0 + 64, kb * BK);
+        } else {
+          tma_load_2d(a, &maps.a, fb, kb * BK, m0);
+        }
+        if (c.d.b_mn) {
+          for (int j = 0; j * 64 < c.BN; ++j)
+            tma_load_2d(b + j * CHUNK, &maps.b, fb, n0 + 64 * j, kb * BK);
+        } else {
+          tma_load_2d(b, &maps.b, fb, kb * BK, n0);
+        }
+        ++issued;
+        if (++s == c.stages) s = 0, ph ^= 1;
+      }
+      // the copies land before the block may exit
+      for (int j = std::max(0, issued - c.stages); j < issued; ++j)
+        wait_bar_drain(full + 8 * (j % c.stages), (j / c.stages) & 1, DRAIN_LIMIT);
+    }
+    __syncwarp();
+  } else if (warp == 4) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(128, c.BN, c.d.a_mn, c.d.b_mn);
+      const uint32_t a_step = c.d.a_mn ? 16 * 128 : 32, b_step = c.d.b_mn ? 16 * 128 : 32;
+      const uint32_t a_lbo = c.d.a_mn ? CHUNK : 16, b_lbo = c.d.b_mn ? CHUNK : 16;
+      int s = 0, ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bar(full + 8 * s, ph, wc)) break;
+        tc_fence_after();
+        const uint32_t a0 = base + s * stage_bytes, b0 = a0 + OPER;
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_bf16(tmem_base, sw128_desc(a0 + kk * a_step, a_lbo, 1024),
+                      sw128_desc(b0 + kk * b_step, b_lbo, 1024), idesc, kb > kb0 || kk > 0);
+        tc_commit(empty + 8 * s);
+        if (++s == c.stages) s = 0, ph ^= 1;
+      }
+      tc_commit(acc_full);
+      wait_bar_drain(acc_full, 0, DRAIN_LIMIT);
+    }
+    __syncwarp();
+  }
+
+  // ------------------------------------------------ epilogue
+  // thread = tile row (tensor memory lane); 8 columns at a time
+  const int row = m0 + warp * 32 + lane;  // along the tile's rows
+  auto finish = [&](int j0, float(&v)[8]) {
+    // v: columns n0 + j0 .. + 7 of this row, added up over the contraction
+    if (row >= c.Mr) return;
+    const DenseProduct& d = c.d;
+    const int col0 = n0 + j0;
+    if (c.swap) {
+      // output[col, row]: consecutive lanes write consecutive elements
+      const float bv = d.epilogue && p.bias ? load_any(p.bias, p.bias_f32, row) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += bv;
+      if (d.epilogue && p.pre) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col0 + i < c.Nc)
+            static_cast<__nv_bfloat16*>(p.pre)[static_cast<long long>(col0 + i) * d.N + row] =
+                __float2bfloat16_rn(v[i]);
+      }
+      if (d.epilogue) act_all<8>(p.act, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (col0 + i >= c.Nc) continue;
+        if (d.epilogue && p.residual)
+          v[i] += load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row);
+        const long long o = static_cast<long long>(col0 + i) * d.N + row;
+        if (d.out_f32)
+          static_cast<float*>(d.out)[o] = v[i];
+        else
+          static_cast<__nv_bfloat16*>(d.out)[o] = __float2bfloat16_rn(v[i]);
+      }
+      return;
+    }
+    const int nv = std::min(8, c.Nc - col0);
+    if (nv <= 0) return;
+    auto store8 = [&](void* out, bool f32, bool vec) {
+      const long long o = static_cast<long long>(row) * d.N + col0;
+      if (vec && nv == 8) {
+        if (f32) {
+          float4* q = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+          q[0] = make_float4(v[0], v[1], v[2], v[3]);
+          q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + o) =
+              make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                         pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= nv) continue;
+          if (f32)
+            static_cast<float*>(out)[o + i] = v[i];
+          else
+            static_cast<__nv_bfloat16*>(out)[o + i] = __float2bfloat16_rn(v[i]);
+        }
+      }
+    };
+    if (d.epilogue) {
+      if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < nv) v[i] += load_any(p.bias, p.bias_f32, col0 + i);
+      }
+      if (p.pre) store8(p.pre, false, c.vec_pre);
+      act_all<8>(p.act, v);
+      if (p.residual) {
+        const long long ro = static_cast<long long>(row) * p.ldr + col0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < nv) v[i] += load_any(p.residual, p.res_f32, ro + i);
+      }
+    }
+    store8(d.out, d.out_f32, c.vec_out);
+  };
+
+  bool ok = true;
+  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  if (warp < 4) {
+    ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
+    tc_fence_after();
+    if (S == 1) {
+      if (ok)
+#pragma unroll 1
+        for (int j = 0; j < c.BN && n0 + j < c.Nc; j += 16) {
+          float v[16], h[8];
+          tmem_ld16(taddr + j, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = v[i];
+          finish(j, h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = v[8 + i];
+          finish(j + 8, h);
+        }
+    } else {
+      // the partial tile, column by column (128 consecutive floats each),
+      // over the pipeline's buffers: every MMA that read them is done
+#pragma unroll 1
+      for (int j = 0; j < c.BN; j += 16) {
+        float v[16];
+        tmem_ld16(taddr + j, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          st_shared_f32(base + (j + i) * 512 + (warp * 32 + lane) * 4, v[i]);
+      }
+    }
+  }
+  if (S > 1) {
+    cluster_sync_all();
+    if (warp < 4) {
+      // this CTA finishes columns [j0, j1): sums over the ranks in order
+      const int per = (cdiv(c.BN, S) + 7) & ~7;
+      const int j1 = std::min(c.BN, (rank + 1) * per);
+#pragma unroll 1
+      for (int j = rank * per; j < j1 && n0 + j < c.Nc; j += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        for (int q = 0; q < S; ++q) {
+          const uint32_t src = mapa_shared(base + j * 512 + (warp * 32 + lane) * 4, q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(src + i * 512) : "memory");
+            v[i] += x;
+          }
+        }
+        finish(j, v);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while its partial tile is being read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, c.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------- backward prep
+// dz = bf16(dy act'(pre)) [T, ldz], and the partial column sums of the
+// unrounded dz over `rows` rows per block: part[blockIdx.y][N].
+template <int ACT>
+__global__ void __launch_bounds__(256)
+    dense_dz_kernel(const void* dy, bool dy_f32, long long lddy, const __nv_bfloat16* pre, int T,
+                    int N, int rows, __nv_bfloat16* dz, int ldz, float* part) {
+  pdl_trigger();
+  pdl_wait();
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int t = t0; t < t1; ++t) {
+    float v = load_any(dy, dy_f32, t * lddy + n);
+    if constexpr (ACT != kActNone)
+      v *= act_slope<ACT>(__bfloat162float(pre[static_cast<long long>(t) * N + n]));
+    sum += v;
+    if (dz) dz[static_cast<long long>(t) * ldz + n] = __float2bfloat16_rn(v);
+  }
+  if (part) part[static_cast<long long>(blockIdx.y) * N + n] = sum;
+}
+
+// db[n] = sum over the partial rows, in order
+__global__ void __launch_bounds__(256)
+    dense_db_kernel(const float* part, int nb, int N, void* db, bool db_f32) {
+  pdl_trigger();
+  pdl_wait();
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float v = 0.f;
+  for (int i = 0; i < nb; ++i) v += part[static_cast<long long>(i) * N + n];
+  if (db_f32)
+    static_cast<float*>(db)[n] = v;
+  else
+    static_cast<__nv_bfloat16*>(db)[n] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------- host
+template <typename K>
+cudaError_t allow_smem(K kern, size_t smem, bool* done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && done[dev]) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
+// Co-resident clusters of two (persistent grid).
+int pair_count() {
+  static int cache[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && cache[dev]) return cache[dev];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms() & ~1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel, &cfg) != cudaSuccess || n < 1)
+    n = num_sms() / 2;
+  n = std::min(n, num_sms() / 2);
+  if (dev < 64) cache[dev] = n;
+  return n;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// bf16 operand [rows][cols] with row stride ld: K-major boxes of 64 columns x
+// `box_rows` rows, MN-major boxes of 64 columns x 64 rows.
+bool tmap_operand(CUtensorMap* m, const DenseOperand& o, bool mn, int box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(o.cols), static_cast<uint64_t>(o.rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(o.ld) * 2};
+  const uint32_t box[2] = {64, static_cast<uint32_t>(mn ? 64 : box_rows)};
+  return encode_tmap(m, o.ptr, 2, dims, strides, box);
+}
+
+bool use_pairs(const DenseProduct& d) {
+  // enough 256 x 256 tiles to give most pairs one
+  return static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256) * 5 >= 4LL * (num_sms() / 2);
+}
+
+bool out_by_tma(const void* out, int N, bool f32) {
+  return aligned16(out) && (static_cast<long long>(N) * (f32 ? 4 : 2)) % 16 == 0;
+}
+
+cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperand* b, int n,
+                         cudaStream_t st) {
+  PairMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  int total = 0;
+  for (int q = 0; q < 2; ++q) {
+    DenseProduct& d = p.pr[q];
+    if (q >= n) {
+      d.tiles = 0;
+      continue;
+    }
+    d.tiles = cdiv(d.M, 256) * cdiv(d.N, 256);
+    total += d.tiles;
+    d.out_tma = out_by_tma(d.out, d.N, d.out_f32);
+    if (!tmap_operand(&maps.a[q], a[q], d.a_mn, kHalf) ||
+        !tmap_operand(&maps.b[q], b[q], d.b_mn, kHalf))
+      return cudaErrorInvalidValue;
+    if (d.out_tma && !encode_tmap_out(&maps.out[q], d.out, d.out_f32, d.M, d.N))
+      return cudaErrorInvalidValue;
+  }
+  if (p.pre) {
+    p.pre_tma = out_by_tma(p.pre, p.pr[0].N, false);
+    if (p.pre_tma && !encode_tmap_out(&maps.pre, p.pre, false, p.pr[0].M, p.pr[0].N))
+      return cudaErrorInvalidValue;
+  }
+  static bool done[64] = {};
+  cudaError_t e = allow_smem(dense_pair_kernel, kPairSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(dense_pair_kernel, dim3(2 * std::min(pair_count(), total)), dim3(kThreads),
+                    kPairSmem, st, maps, p);
+}
+
+// Tile columns, orientation and contraction pieces of a product on
+// single-CTA tiles, by estimated time: rounds of clusters x (contraction
+// steps of a piece x cycles per step + the start and end of a tile).  A step
+// costs what its bytes take at the SM's share of the memory rate.
+struct CtaPlan {
+  bool swap;
+  int BN, splits;
+};
+CtaPlan plan_cta(const DenseProduct& d) {
+  CtaPlan best{false, 16, 1};
+  double best_t = 1e30;
+  const int nkb = cdiv(d.Kc, BK);
+  const int sms = num_sms();
+  for (int swap = 0; swap < 2; ++swap) {
+    const int mr = swap ? d.N : d.M, nc = swap ? d.M : d.N;
+    for (int bn : {16, 32, 64, 128, 256}) {
+      if (bn > 16 && nc <= bn / 2) break;
+      const long long tiles = static_cast<long long>(cdiv(mr, 128)) * cdiv(nc, bn);
+      for (int s = 1; s <= 8 && s <= nkb; s *= 2) {
+        const double steps = static_cast<double>(cdiv(nkb, s));
+        const long long rounds = (tiles * s + sms - 1) / sms;
+        const double step = std::max(2.0 * bn, (16384.0 + 128.0 * bn) / 32.0);
+        const double t =
+            static_cast<double>(rounds) * (steps * step + 2500.0 + 8.0 * bn + (s > 1 ? 1500.0 : 0.0));
+        if (t < best_t) {
+          best_t = t;
+          best = CtaPlan{swap != 0, bn, s};
+        }
+      }
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const DenseOperand& b,
+                       cudaStream_t st) {
+  const CtaPlan plan = plan_cta(p.pr[q]);
+  CtaParams c{};
+  c.d = p.pr[q];
+  c.swap = plan.swap;
+  c.Mr = plan.swap ? c.d.N : c.d.M;
+  c.Nc = plan.swap ? c.d.M : c.d.N;
+  const DenseOperand& ra = plan.swap ? b : a;
+  const DenseOperand& rb = plan.swap ? a : b;
+  if (plan.swap) std::swap(c.d.a_mn, c.d.b_mn);
+  c.BN = plan.BN;
+  c.splits = plan.splits;
+  c.b_bytes = c.d.b_mn ? cdiv(c.BN, 64) * CHUNK : c.BN * 128;
+  const int nkb = cdiv(c.d.Kc, BK);
+  // two blocks on an SM where the stages are small
+  const int room = (c.BN <= 128 ? 100 : 200) * 1024;
+  c.stages = std::max(2, std::min({8, room / (OPER + c.b_bytes), cdiv(nkb, c.splits)}));
+  c.tmem_cols = 32;
+  while (c.tmem_cols < c.BN) c.tmem_cols *= 2;
+  c.vec_out = out_by_tma(c.d.out, c.d.N, c.d.out_f32) && c.d.N % 8 == 0;
+  c.vec_pre = p.pre && out_by_tma(p.pre, c.d.N, false);
+  CtaMaps maps;
+  if (!tmap_operand(&maps.a, ra, c.d.a_mn, 128) || !tmap_operand(&maps.b, rb, c.d.b_mn, c.BN))
+    return cudaErrorInvalidValue;
+  const size_t smem = 1024 + std::max(c.stages * (OPER + c.b_bytes), c.splits > 1 ? c.BN * 512 : 0) + 256;
+  static bool done[64] = {};
+  cudaError_t e = allow_smem(dense_cta_kernel, 232448, done);
+  if (e != cudaSuccess) return e;
+  const int tiles = cdiv(c.Mr, 128) * cdiv(c.Nc, c.BN);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * c.splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = c.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, dense_cta_kernel, maps, c, p);
+}
+
+constexpr int kDbRows = 64;  // rows per partial sum of db
+
+template <int ACT>
+cudaError_t launch_dz(const DenseBackward& a, __nv_bfloat16* dz, int ldz, float* part,
+                      cudaStream_t st) {
+  return launch_pdl(dense_dz_kernel<ACT>, dim3(cdiv(a.N, 256), cdiv(a.T, kDbRows)), dim3(256), 0, st,
+                    a.dy, a.dy_f32, a.lddy, static_cast<const __nv_bfloat16*>(a.pre), a.T, a.N,
+                    kDbRows, dz, ldz, part);
+}
+
+bool dy_is_operand(const DenseBackward& a) {
+  return a.act == kActNone && !a.dy_f32 && a.lddy % 8 == 0 && aligned16(a.dy);
+}
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+int dz_ld(int N) { return (N + 7) / 8 * 8; }
+
+}  // namespace
+
+size_t dense_bwd_ws_bytes(int T, int N) {
+  return round256(static_cast<size_t>(T) * dz_ld(N) * 2) +
+         round256(static_cast<size_t>(cdiv(T, kDbRows)) * N * 4);
+}
+
+cudaError_t launch_dense_forward(const DenseParams& p0, const DenseOperand& x,
+                                 const DenseOperand& W, cudaStream_t st) {
+  DenseParams p = p0;
+  return use_pairs(p.pr[0]) ? launch_pairs(p, &x, &W, 1, st) : launch_cta(p, 0, x, W, st);
+}
+
+cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t st) {
+  const bool direct = dy_is_operand(a);
+  const int ldz = dz_ld(a.N);
+  __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                         round256(static_cast<size_t>(a.T) * ldz * 2));
+  const bool gemm = a.dx || a.dW;
+  __nv_bfloat16* dz_out = direct || !gemm ? nullptr : dz;
+  float* part_out = a.db ? part : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (dz_out || part_out) {
+    if (a.act == kActRelu) e = launch_dz<kActRelu>(a, dz_out, ldz, part_out, st);
+    else if (a.act == kActSilu) e = launch_dz<kActSilu>(a, dz_out, ldz, part_out, st);
+    else if (a.act == kActGelu) e = launch_dz<kActGelu>(a, dz_out, ldz, part_out, st);
+    else e = launch_dz<kActNone>(a, dz_out, ldz, part_out, st);
+    if (e == cudaSuccess && part_out)
+      e = launch_pdl(dense_db_kernel, dim3(cdiv(a.N, 256)), dim3(256), 0, st, part,
+                     cdiv(a.T, kDbRows), a.N, a.db, a.db_f32);
+    if (e != cudaSuccess) return e;
+  }
+  const DenseOperand z = direct ? DenseOperand{a.dy, a.T, a.N, a.lddy} : DenseOperand{dz, a.T, a.N, ldz};
+  const DenseOperand x{a.x, a.T, a.K, a.ldx}, W{a.W, a.N, a.K, a.K};
+  DenseParams p{};
+  p.dev_status = a.dev_status;
+  p.wait_limit = a.wait_limit;
+  DenseOperand pa[2], pb[2];
+  int n = 0;
+  auto add = [&](int M, int N, int Kc, bool a_mn, void* out, const DenseOperand& oa,
+                 const DenseOperand& ob) {
+    DenseProduct d{};
+    d.M = M, d.N = N, d.Kc = Kc, d.a_mn = a_mn, d.b_mn = true, d.out = out;
+    p.pr[n] = d;
+    pa[n] = oa, pb[n] = ob;
+    if (!use_pairs(d)) return launch_cta(p, n, oa, ob, st);
+    ++n;
+    return cudaSuccess;
+  };
+  if (a.dx) e = add(a.T, a.K, a.N, false, a.dx, z, W);
+  if (e == cudaSuccess && a.dW) e = add(a.N, a.K, a.T, true, a.dW, z, x);
+  if (e == cudaSuccess && n) e = launch_pairs(p, pa, pb, n, st);
+  return e;
+}
+
+}  // namespace mgg
