@@ -231,6 +231,9 @@ cudaError_t launch_norm_fwd(const void* x, bool x_f32, long long ldx, const void
 cudaError_t launch_norm_bwd(const void* dy, bool y_f32, const void* x, bool x_f32, long long ldx,
                             const void* w, bool w_f32, const float* mean, const float* rstd, int T,
                             int K, void* dx, void* dw, void* db, float* part, cudaStream_t st);
+// out0[K] = column sums of part[0][nb][K], out1 (or null) of part[1][nb][K], in a fixed order
+cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
+                               bool out_f32, cudaStream_t st);
 // select.cu
 cudaError_t launch_select(const void* logits, bool f32, long long ldl, int T, int E, int k,
                           bool softmax, const float* bias, int groups, int topk_groups,

@@ -34,13 +34,15 @@ namespace {
 
 constexpr int BK = kBK;                 // contraction step: one 128-byte row of bf16
 constexpr int kHalf = 128;              // rows of A, and of B, per CTA and stage of a pair
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int OPER = kHalf * BK * 2;    // 16 KB
 constexpr int CHUNK = 64 * BK * 2;      // 8 KB: 64 wide MN-major block of one stage
 constexpr int EPI_BUF = 32 * 128;       // one warp's staged block: 32 rows x 128 bytes
-constexpr int kThreads = 192;           // warps 0-3 epilogue, 4 MMA, 5 TMA
+constexpr int kThreads = 192;           // single-CTA tiles: warps 0-3 epilogue, 4 MMA, 5 TMA
+constexpr int kEpiWarps = 8;            // pairs: warps 0-3 and 6-9 epilogue, 4 MMA, 5 TMA
+constexpr int kPairThreads = 320;
 constexpr int kMeta = 512;
-constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + 8 * EPI_BUF + kMeta;
+constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + 2 * kEpiWarps * EPI_BUF + kMeta;
 static_assert(kPairSmem <= 232448, "shared memory per block");
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
@@ -52,13 +54,35 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
 }
 
 // ---------------------------------------------------------------- epilogue math
-// z -> act(z).  expf / erff are CUDA's own, the divisions IEEE: f32 outputs
-// keep f32 accuracy.
+// The activations run once per output element on the few warps that empty the
+// accumulators, so their instruction count matters (CUDA's erff and expf with
+// IEEE divisions took the GELU epilogue past the MMAs it should hide under:
+// 246 us against 180 for 8192 x 2048 x 8192).  sigmoid by the fast
+// exponential and divide, both within a few f32 ulp; exp(-z) = inf gives 0.
+__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// Phi(z) = (1 + erf(z / sqrt 2)) / 2 with Abramowitz & Stegun 7.1.26,
+//   erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0,
+// absolute error at most 1.5e-7.  *e receives exp(-z^2 / 2), which is the
+// exp(-x^2) of the formula and the density's exponential in the gradient.
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  *e = __expf(-x * x);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q = 0.5f * q * t * *e;  // Phi(-|z|)
+  return z < 0.f ? q : 1.f - q;
+}
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
   if constexpr (ACT == kActRelu) return fmaxf(z, 0.f);
-  if constexpr (ACT == kActSilu) return z / (1.f + expf(-z));
-  if constexpr (ACT == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return z * normal_cdf(z, &e);
+  }
   return z;
 }
 // act'(z)
@@ -66,12 +90,14 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
   if constexpr (ACT == kActSilu) {
-    const float s = 1.f / (1.f + expf(-z));
-    return s * (1.f + z * (1.f - s));
+    const float s = sigmoid_f(z);
+    return s * fmaf(z, 1.f - s, 1.f);
   }
-  if constexpr (ACT == kActGelu)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
-           z * (0.39894228040143268f * expf(-0.5f * z * z));
+  if constexpr (ACT == kActGelu) {
+    float e;
+    const float c = normal_cdf(z, &e);
+    return fmaf(z * 0.39894228040143268f, e, c);
+  }
   return 1.f;
 }
 
@@ -112,7 +138,7 @@ __device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
   m.sA = base;
   m.sB = m.sA + STAGES * OPER;
   m.sEpi = m.sB + STAGES * OPER;
-  m.full = m.sEpi + 8 * EPI_BUF;
+  m.full = m.sEpi + 2 * kEpiWarps * EPI_BUF;
   m.empty = m.full + 8 * STAGES;
   m.acc_full = m.empty + 8 * STAGES;
   m.acc_empty = m.acc_full + 16;
@@ -159,7 +185,7 @@ __device__ __forceinline__ void load_oper(uint32_t dst, const CUtensorMap* map, 
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ DenseParams p) {
   extern __shared__ uint8_t smem_raw[];
   const PSmem m = carve_pair(smem_raw);
@@ -180,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(m.acc_full + 8 * a, 1);
-      mbar_init(m.acc_empty + 8 * a, 8);  // the epilogue warps of both CTAs
+      mbar_init(m.acc_empty + 8 * a, 2 * kEpiWarps);  // the epilogue warps of both CTAs
     }
     mbar_init(m.drain, 1);
     mbar_init(m.pdone, 1);
@@ -285,13 +311,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------ epilogue
-    // Warp w holds rows 32 w .. +31 of this CTA's 128, lane i row i.  A block
+    // Eight warps: warps 0-3 take the tile's first 128 columns, 6-9 the second;
+    // a warp holds rows 32 (w % 4) .. +31 of this CTA's 128 (the quarter of
+    // tensor memory that it can read), lane i row i.  A block
     // of 128 bytes per row (64 bf16 or 32 f32 columns) is staged in the TMA
     // store's 128-byte swizzle (conflict-free: the lanes of a quarter warp
     // write eight different 16-byte columns) and leaves with one store
     // instruction; two buffers per warp alternate.
-    const uint32_t stg = m.sEpi + warp * 2 * EPI_BUF;
-    const int row_w = static_cast<int>(rank) * kHalf + warp * 32;
+    const int quad = warp & 3, half = warp >= 6 ? 1 : 0;
+    const uint32_t stg = m.sEpi + (half * 4 + quad) * 2 * EPI_BUF;
+    const int row_w = static_cast<int>(rank) * kHalf + quad * 32;
     int tcount = 0, nst = 0;
     for (int tau = pair; tau < total; tau += npairs) {
       const PTile t = decode_pair(p, tau);
@@ -301,8 +330,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int acc = tcount & 1;
       if (!__all_sync(0xffffffffu, wait_bar(m.acc_full + 8 * acc, (tcount >> 1) & 1, wc))) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + acc * 256;
-      const int nblk = std::min(8, cdiv(d.N - t.n0, 32));  // 32-column blocks
+      const int col_w = t.n0 + half * 128;  // first column of this warp
+      const uint32_t taddr =
+          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
+      const int nblk = std::max(0, std::min(4, cdiv(d.N - col_w, 32)));  // 32-column blocks
+      if (nblk == 0) {  // nothing of the tile here
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
+      }
       // stage 32 columns of v as bf16 (half a block) or f32 (a block)
       auto put = [&](uint32_t buf, const float(&v)[32], bool f32, int half) {
         if (f32) {
@@ -378,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
         }
-        const int c0 = t.n0 + b * 32;
+        const int c0 = col_w + b * 32;
         const bool last = b == nblk - 1;
         if (d.epilogue) {
           if (p.bias) {
@@ -707,42 +743,84 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------- backward prep
-// dz = bf16(dy act'(pre)) [T, ldz], and the partial column sums of the
-// unrounded dz over `rows` rows per block: part[blockIdx.y][N].
-template <int ACT>
-__global__ void __launch_bounds__(256)
-    dense_dz_kernel(const void* dy, bool dy_f32, long long lddy, const __nv_bfloat16* pre, int T,
-                    int N, int rows, __nv_bfloat16* dz, int ldz, float* part) {
-  pdl_trigger();
-  pdl_wait();
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int t = t0; t < t1; ++t) {
-    float v = load_any(dy, dy_f32, t * lddy + n);
-    if constexpr (ACT != kActNone)
-      v *= act_slope<ACT>(__bfloat162float(pre[static_cast<long long>(t) * N + n]));
-    sum += v;
-    if (dz) dz[static_cast<long long>(t) * ldz + n] = __float2bfloat16_rn(v);
+// dz = bf16(dy act'(pre)) [T, ldz] in one pass, and the column sums of the
+// unrounded dz over each block's rows: part[blockIdx.y][N].  Bound by its
+// bytes: 16-byte pieces of eight columns per thread (VEC = 8) wherever rows
+// start on 16-byte boundaries.  A block is `lanes` threads along the columns
+// and 256 / lanes rows; its partial sums add up in shared memory in row order.
+struct DzArgs {
+  const void* dy;
+  bool dy_f32;
+  long long lddy;
+  const __nv_bfloat16* pre;
+  int T, N, rows, lanes;
+  __nv_bfloat16* dz;  // null: sums only
+  int ldz;
+  float* part;        // null: no sums
+};
+template <int VEC>
+__device__ __forceinline__ void load_row(const void* p, bool f32, long long i, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = load_any(p, f32, i);
+  } else if (f32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(u[j] << 16);
+      v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+    }
   }
-  if (part) part[static_cast<long long>(blockIdx.y) * N + n] = sum;
 }
-
-// db[n] = sum over the partial rows, in order
-__global__ void __launch_bounds__(256)
-    dense_db_kernel(const float* part, int nb, int N, void* db, bool db_f32) {
+template <int ACT, int VEC>
+__global__ void __launch_bounds__(256) dense_dz_kernel(const DzArgs a) {
+  __shared__ float acc[256 * VEC];
   pdl_trigger();
   pdl_wait();
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  float v = 0.f;
-  for (int i = 0; i < nb; ++i) v += part[static_cast<long long>(i) * N + n];
-  if (db_f32)
-    static_cast<float*>(db)[n] = v;
-  else
-    static_cast<__nv_bfloat16*>(db)[n] = __float2bfloat16_rn(v);
+  const int cx = threadIdx.x % a.lanes, ry = threadIdx.x / a.lanes, nr = 256 / a.lanes;
+  const int n = (blockIdx.x * a.lanes + cx) * VEC;
+  const int t0 = blockIdx.y * a.rows, t1 = min(a.T, t0 + a.rows);
+  float sum[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sum[i] = 0.f;
+  if (n < a.N) {
+#pragma unroll 4
+    for (int t = t0 + ry; t < t1; t += nr) {
+      float v[VEC], z[VEC];
+      load_row<VEC>(a.dy, a.dy_f32, t * a.lddy + n, v);
+      if constexpr (ACT != kActNone) {
+        load_row<VEC>(a.pre, false, static_cast<long long>(t) * a.N + n, z);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] *= act_slope<ACT>(z[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sum[i] += v[i];
+      if (a.dz) {
+        __nv_bfloat16* o = a.dz + static_cast<long long>(t) * a.ldz + n;
+        if constexpr (VEC == 1)
+          *o = __float2bfloat16_rn(v[0]);
+        else
+          *reinterpret_cast<uint4*>(o) =
+              make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                         pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+      }
+    }
+  }
+  if (!a.part) return;
+  const int width = a.lanes * VEC;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[ry * width + cx * VEC + i] = sum[i];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < width && blockIdx.x * width + c < a.N) {
+    float v = 0.f;
+    for (int r = 0; r < nr; ++r) v += acc[r * width + c];
+    a.part[static_cast<long long>(blockIdx.y) * a.N + blockIdx.x * width + c] = v;
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -765,7 +843,7 @@ int pair_count() {
   if (dev < 64 && cache[dev]) return cache[dev];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms() & ~1);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kPairSmem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -829,7 +907,7 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
   static bool done[64] = {};
   cudaError_t e = allow_smem(dense_pair_kernel, kPairSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(dense_pair_kernel, dim3(2 * std::min(pair_count(), total)), dim3(kThreads),
+  return launch_pdl(dense_pair_kernel, dim3(2 * std::min(pair_count(), total)), dim3(kPairThreads),
                     kPairSmem, st, maps, p);
 }
 
@@ -913,14 +991,32 @@ cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const
   return cudaLaunchKernelEx(&cfg, dense_cta_kernel, maps, c, p);
 }
 
-constexpr int kDbRows = 64;  // rows per partial sum of db
+// Blocks of the dz pass: columns first, then enough row ranges for two blocks
+// per SM.
+struct DzPlan {
+  int vec, lanes, bx, by, rows;
+};
+DzPlan plan_dz(int T, int N, bool vec) {
+  DzPlan p;
+  p.vec = vec ? 8 : 1;
+  p.lanes = 32;
+  while (p.lanes > 1 && (p.lanes / 2) * p.vec >= N) p.lanes /= 2;
+  p.bx = cdiv(N, p.lanes * p.vec);
+  const int per = 256 / p.lanes;  // rows of one step of a block
+  p.by = std::max(1, std::min(cdiv(T, per), cdiv(4 * num_sms(), p.bx)));
+  p.rows = cdiv(cdiv(T, p.by), per) * per;
+  p.by = cdiv(T, p.rows);
+  return p;
+}
+int max_partials(int T, int N) {
+  return std::max(plan_dz(T, N, true).by, plan_dz(T, N, false).by);
+}
 
 template <int ACT>
-cudaError_t launch_dz(const DenseBackward& a, __nv_bfloat16* dz, int ldz, float* part,
-                      cudaStream_t st) {
-  return launch_pdl(dense_dz_kernel<ACT>, dim3(cdiv(a.N, 256), cdiv(a.T, kDbRows)), dim3(256), 0, st,
-                    a.dy, a.dy_f32, a.lddy, static_cast<const __nv_bfloat16*>(a.pre), a.T, a.N,
-                    kDbRows, dz, ldz, part);
+cudaError_t launch_dz(const DzPlan& pl, const DzArgs& a, cudaStream_t st) {
+  const dim3 grid(pl.bx, pl.by), block(256);
+  return pl.vec == 8 ? launch_pdl(dense_dz_kernel<ACT, 8>, grid, block, 0, st, a)
+                     : launch_pdl(dense_dz_kernel<ACT, 1>, grid, block, 0, st, a);
 }
 
 bool dy_is_operand(const DenseBackward& a) {
@@ -933,7 +1029,7 @@ int dz_ld(int N) { return (N + 7) / 8 * 8; }
 
 size_t dense_bwd_ws_bytes(int T, int N) {
   return round256(static_cast<size_t>(T) * dz_ld(N) * 2) +
-         round256(static_cast<size_t>(cdiv(T, kDbRows)) * N * 4);
+         round256(static_cast<size_t>(max_partials(T, N)) * N * 4);
 }
 
 cudaError_t launch_dense_forward(const DenseParams& p0, const DenseOperand& x,
@@ -953,13 +1049,16 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
   float* part_out = a.db ? part : nullptr;
   cudaError_t e = cudaSuccess;
   if (dz_out || part_out) {
-    if (a.act == kActRelu) e = launch_dz<kActRelu>(a, dz_out, ldz, part_out, st);
-    else if (a.act == kActSilu) e = launch_dz<kActSilu>(a, dz_out, ldz, part_out, st);
-    else if (a.act == kActGelu) e = launch_dz<kActGelu>(a, dz_out, ldz, part_out, st);
-    else e = launch_dz<kActNone>(a, dz_out, ldz, part_out, st);
+    const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && aligned16(a.dy) && aligned16(a.pre);
+    const DzPlan pl = plan_dz(a.T, a.N, vec);
+    const DzArgs z{a.dy,    a.dy_f32, a.lddy,   static_cast<const __nv_bfloat16*>(a.pre), a.T,
+                   a.N,     pl.rows,  pl.lanes, dz_out, ldz, part_out};
+    if (a.act == kActRelu) e = launch_dz<kActRelu>(pl, z, st);
+    else if (a.act == kActSilu) e = launch_dz<kActSilu>(pl, z, st);
+    else if (a.act == kActGelu) e = launch_dz<kActGelu>(pl, z, st);
+    else e = launch_dz<kActNone>(pl, z, st);
     if (e == cudaSuccess && part_out)
-      e = launch_pdl(dense_db_kernel, dim3(cdiv(a.N, 256)), dim3(256), 0, st, part,
-                     cdiv(a.T, kDbRows), a.N, a.db, a.db_f32);
+      e = launch_column_sums(part, pl.by, a.N, a.db, nullptr, a.db_f32, st);
     if (e != cudaSuccess) return e;
   }
   const DenseOperand z = direct ? DenseOperand{a.dy, a.T, a.N, a.lddy} : DenseOperand{dz, a.T, a.N, ldz};

@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(256)
 // Partial rows part[2][nb][K] -> dw, db, added in block order: 32 columns
 // per block, 32 row lanes each summing every 32nd partial, then a tree.
 __global__ void __launch_bounds__(1024)
-    norm_bwd_reduce_kernel(const float* part, int nb, int K, void* dw, void* db, bool w_f32) {
+    column_sums_kernel(const float* part, int nb, int K, void* dw, void* db, bool w_f32) {
   __shared__ float s[32][33];
   pdl_trigger();
   pdl_wait();
@@ -521,13 +521,18 @@ cudaError_t bwd(const BwdArgs& a, bool vec, cudaStream_t st) {
     else e = bwd_t<XT, YT, 1, 1024, 16>(a, &nb, st);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_bwd_reduce_kernel, dim3(cdiv(K, 32), a.db ? 2 : 1), dim3(1024), 0, st,
-                    static_cast<const float*>(a.part), nb, K, a.dw, a.db, a.w_f32);
+  return launch_column_sums(a.part, nb, K, a.dw, a.db, a.w_f32, st);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
+
+cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
+                               bool out_f32, cudaStream_t st) {
+  return launch_pdl(column_sums_kernel, dim3(cdiv(K, 32), out1 ? 2 : 1), dim3(1024), 0, st, part,
+                    nb, K, out0, out1, out_f32);
+}
 
 int norm_bwd_blocks() { return num_sms(); }
 
