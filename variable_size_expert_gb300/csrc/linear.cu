@@ -174,15 +174,75 @@ __device__ __forceinline__ PTile decode_pair(const DenseParams& p, int tau) {
   return t;
 }
 
-// One operand's rows of a stage: 128 rows from r0, contraction step kb.
-__device__ __forceinline__ void load_oper(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                          bool mn, int r0, int kb) {
-  if (mn) {
-    tma_load_2d_cg2(dst, map, bar, r0, kb * BK);
-    tma_load_2d_cg2(dst + CHUNK, map, bar, r0 + 64, kb * BK);
+// One operand's rows of a stage: 128 rows from r0, contraction from k.
+template <bool MN>
+__device__ __forceinline__ void load_oper(uint32_t dst, const CUtensorMap* map, uint32_t bar, int r0,
+                                          int k) {
+  if constexpr (MN) {
+    tma_load_2d_cg2(dst, map, bar, r0, k);
+    tma_load_2d_cg2(dst + CHUNK, map, bar, r0 + 64, k);
   } else {
-    tma_load_2d_cg2(dst, map, bar, kb * BK, r0);
+    tma_load_2d_cg2(dst, map, bar, k, r0);
   }
+}
+
+// Ring position of a pipeline role: stage and the parity its next wait takes.
+struct Ring {
+  int s;
+  uint32_t ph;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) s = 0, ph ^= 1;
+  }
+};
+
+// The producer's and the MMA thread's loops over a tile's contraction.  One
+// thread runs each, an iteration has the 512 cycles of a stage's MMAs, and an
+// instruction costs a lone thread 4 to 6 of them: the layouts are template
+// arguments, the descriptors advance by one addition, and nothing in the loops
+// is read from the parameters.
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ bool produce(const PSmem& m, const CUtensorMap* ma,
+                                        const CUtensorMap* mb, uint32_t full_l, bool leader, int ar,
+                                        int br, int nkb, Ring& r, int& issued, const WaitCtl& wc) {
+#pragma unroll 1
+  for (int k = 0; k < nkb * BK; k += BK) {
+    if (!wait_bar(m.empty + 8 * r.s, r.ph ^ 1, wc)) return false;
+    const uint32_t fb = full_l + 8 * r.s;
+    // the leader announces its bytes first; the peer issues its copies first
+    // (the phase cannot complete before its arrival)
+    if (leader) mbar_arrive_expect_tx(m.full + 8 * r.s, 2 * OPER);
+    load_oper<A_MN>(m.sA + r.s * OPER, ma, fb, ar, k);
+    load_oper<B_MN>(m.sB + r.s * OPER, mb, fb, br, k);
+    if (!leader) mbar_arrive_expect_tx_cluster(fb, 2 * OPER);
+    ++issued;
+    r.next(STAGES);
+  }
+  return true;
+}
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ bool multiply(const PSmem& m, uint32_t dt, int nkb, Ring& r,
+                                         const WaitCtl& wc) {
+  constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256, A_MN, B_MN);
+  // per 16 of the contraction: 32 bytes along a K-major row, 16 rows of 128
+  // bytes down an MN-major block (descriptors count 16-byte units)
+  constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
+  const uint64_t a0 = sw128_desc(m.sA, A_MN ? CHUNK : 16, 1024);
+  const uint64_t b0 = sw128_desc(m.sB, B_MN ? CHUNK : 16, 1024);
+  uint32_t accumulate = 0;
+#pragma unroll 1
+  for (int kb = 0; kb < nkb; ++kb) {
+    if (!wait_bar(m.full + 8 * r.s, r.ph, wc)) return false;
+    tc_fence_after();
+    const uint64_t ad = a0 + r.s * (OPER >> 4), bd = b0 + r.s * (OPER >> 4);
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk) {
+      tc_mma_bf16_cg2(dt, ad + kk * kA, bd + kk * kB, kIdesc, accumulate);
+      accumulate = 1;
+    }
+    tc_commit_cg2_mc(m.empty + 8 * r.s, 0x3);
+    r.next(STAGES);
+  }
+  return true;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -231,25 +291,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ TMA
     if (lane == 0) {
       int it = 0;
+      Ring r{0, 0};
       bool ok = true;
       for (int tau = pair; ok && tau < total; tau += npairs) {
         const PTile t = decode_pair(p, tau);
         const DenseProduct& d = p.pr[t.q];
         const int ar = t.m0 + static_cast<int>(rank) * kHalf;
         const int br = t.n0 + static_cast<int>(rank) * kHalf;
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          const int s = it % STAGES;
-          if (!wait_bar(m.empty + 8 * s, ((it / STAGES) & 1) ^ 1, wc)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = full_l + 8 * s;
-          if (leader) mbar_arrive_expect_tx(m.full + 8 * s, 2 * OPER);
-          load_oper(m.sA + s * OPER, &maps.a[t.q], fb, d.a_mn, ar, kb);
-          load_oper(m.sB + s * OPER, &maps.b[t.q], fb, d.b_mn, br, kb);
-          if (!leader) mbar_arrive_expect_tx_cluster(fb, 2 * OPER);
-          ++it;
-        }
+        const CUtensorMap *ma = &maps.a[t.q], *mb = &maps.b[t.q];
+        // (the three layouts of the forward, dx and dW)
+        if (d.a_mn)
+          ok = produce<true, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, it, wc);
+        else if (d.b_mn)
+          ok = produce<false, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, it, wc);
+        else
+          ok = produce<false, false>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, it, wc);
       }
       // Every copy lands before either CTA may exit: the peer reports how
       // many stages it issued; for the stages that one side did not issue
@@ -273,35 +329,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 4) {
     // ------------------------------------------------ MMA issue
     if (leader && lane == 0) {
-      int it = 0, tcount = 0;
+      int tcount = 0;
+      Ring r{0, 0};
       bool ok = true;
       for (int tau = pair; ok && tau < total; tau += npairs) {
         const PTile t = decode_pair(p, tau);
         const DenseProduct& d = p.pr[t.q];
-        const uint32_t idesc = idesc_bf16_f32(256, 256, d.a_mn, d.b_mn);
-        // per 16 of the contraction: 32 bytes along a K-major row, 16 rows
-        // of 128 bytes down an MN-major block
-        const uint32_t a_step = d.a_mn ? 16 * 128 : 32, b_step = d.b_mn ? 16 * 128 : 32;
-        const uint32_t a_lbo = d.a_mn ? CHUNK : 16, b_lbo = d.b_mn ? CHUNK : 16;
         const int acc = tcount & 1;
         if (!wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)) break;
         tc_fence_after();
         const uint32_t dt = tmem_base + acc * 256;
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          const int s = it % STAGES;
-          if (!wait_bar(m.full + 8 * s, (it / STAGES) & 1, wc)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = m.sA + s * OPER, b0 = m.sB + s * OPER;
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_bf16_cg2(dt, sw128_desc(a0 + kk * a_step, a_lbo, 1024),
-                            sw128_desc(b0 + kk * b_step, b_lbo, 1024), idesc, (kb | kk) != 0);
-          tc_commit_cg2_mc(m.empty + 8 * s, 0x3);
-          ++it;
-        }
+        if (d.a_mn)
+          ok = multiply<true, true>(m, dt, t.nkb, r, wc);
+        else if (d.b_mn)
+          ok = multiply<false, true>(m, dt, t.nkb, r, wc);
+        else
+          ok = multiply<false, false>(m, dt, t.nkb, r, wc);
         if (!ok) break;
         tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
         ++tcount;
