@@ -347,12 +347,12 @@ bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols)
   if (!fn) return false;
   cuuint64_t d[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t st[1] = {static_cast<cuuint64_t>(cols) * (f32 ? 4 : 2)};
-  cuuint32_t b[2] = {f32 ? 32u : 64u, 32};
+  cuuint32_t b[2] = {32, 32};
   cuuint32_t estr[2] = {1, 1};
   const CUresult r =
       fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d,
-         st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+         st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

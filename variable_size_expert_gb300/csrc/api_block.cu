@@ -163,6 +163,7 @@ mgg_status mgg_linear_forward(const void* x, int64_t ldx, const void* W, const v
   d.epilogue = bias || residual || pre || activation != MGG_ACT_NONE;
   p.bias = bias;
   p.bias_f32 = bias_dtype == MGG_F32;
+  p.bias_vec = bias && aligned(bias, 16);
   p.act = activation;
   p.residual = residual;
   p.res_f32 = residual_dtype == MGG_F32;

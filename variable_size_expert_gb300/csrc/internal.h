@@ -184,7 +184,7 @@ struct DenseProduct {
 struct DenseParams {
   DenseProduct pr[2];
   const void* bias;      // [N] or null
-  bool bias_f32;
+  bool bias_f32, bias_vec;  // bias_vec: 16-byte loads
   int act;
   const void* residual;  // [M, ldr] or null
   bool res_f32, res_vec; // res_vec: 16-byte loads
@@ -220,7 +220,8 @@ long long wait_limit();
 bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box);
 
-// [rows][cols] bf16 or f32 output for TMA stores of 32 rows x 128 bytes, 128-byte swizzle
+// [rows][cols] bf16 or f32 output for TMA stores of 32 rows x 32 columns
+// (bf16: 64-byte swizzle, f32: 128-byte)
 bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols);
 
 // norm.cu

@@ -37,12 +37,13 @@ constexpr int kHalf = 128;              // rows of A, and of B, per CTA and stag
 constexpr int STAGES = 5;
 constexpr int OPER = kHalf * BK * 2;    // 16 KB
 constexpr int CHUNK = 64 * BK * 2;      // 8 KB: 64 wide MN-major block of one stage
-constexpr int EPI_BUF = 32 * 128;       // one warp's staged block: 32 rows x 128 bytes
+constexpr int EPI_BUF = 32 * 64;        // staging unit: 32 rows x 64 bytes (32 bf16 columns)
+constexpr int EPI_WARP = 4 * EPI_BUF;   // per epilogue warp
 constexpr int kThreads = 192;           // single-CTA tiles: warps 0-3 epilogue, 4 MMA, 5 TMA
 constexpr int kEpiWarps = 8;            // pairs: warps 0-3 and 6-9 epilogue, 4 MMA, 5 TMA
 constexpr int kPairThreads = 320;
 constexpr int kMeta = 512;
-constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + 2 * kEpiWarps * EPI_BUF + kMeta;
+constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + kEpiWarps * EPI_WARP + kMeta;
 static_assert(kPairSmem <= 232448, "shared memory per block");
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
@@ -57,67 +58,152 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
 // The activations run once per output element on the few warps that empty the
 // accumulators, so their instruction count matters (CUDA's erff and expf with
 // IEEE divisions took the GELU epilogue past the MMAs it should hide under:
-// 246 us against 180 for 8192 x 2048 x 8192).  sigmoid by the fast
-// exponential and divide, both within a few f32 ulp; exp(-z) = inf gives 0.
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 246 us against 197 for 8192 x 2048 x 8192).  The approximate exponential
+// and reciprocal are each one instruction, within 2 ulp, denormals flushed
+// (values under 1e-38); exp(-z) = inf gives a sigmoid of 0.
+__device__ __forceinline__ float exp2_f(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_f(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return rcp_f(1.f + exp2_f(z * -1.4426950408889634f));
+}
+// Two f32 values in one register pair: the FMA pipe takes both in one
+// instruction.
+struct F2 {
+  uint64_t u;
+};
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.u));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+  return r;
+}
+__device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
+
 // Phi(z) = (1 + erf(z / sqrt 2)) / 2 with Abramowitz & Stegun 7.1.26,
 //   erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0,
-// absolute error at most 1.5e-7.  *e receives exp(-z^2 / 2), which is the
+// absolute error at most 1.5e-7; here x = |z| / sqrt 2, with the 1 / sqrt 2
+// in p and the half in the a's.  *e receives exp(-z^2 / 2), which is the
 // exp(-x^2) of the formula and the density's exponential in the gradient.
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-  *e = __expf(-x * x);
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  q = 0.5f * q * t * *e;  // Phi(-|z|)
-  return z < 0.f ? q : 1.f - q;
+__device__ __forceinline__ F2 normal_cdf2(float z0, float z1, F2* e) {
+  const F2 z = pack2(z0, z1);
+  float x0, x1;
+  unpack2(mul2(mul2(z, z), both(-0.72134752044448170f)), x0, x1);  // log2(e) / 2
+  *e = pack2(exp2_f(x0), exp2_f(x1));
+  const F2 t = pack2(rcp_f(fmaf(0.23164189f, fabsf(z0), 1.f)), rcp_f(fmaf(0.23164189f, fabsf(z1), 1.f)));
+  F2 q = fma2(both(0.5307027145f), t, both(-0.7265760135f));
+  q = fma2(q, t, both(0.7107068705f));
+  q = fma2(q, t, both(-0.142248368f));
+  q = fma2(q, t, both(0.127414796f));
+  q = mul2(q, mul2(t, *e));  // Phi(-|z|)
+  float q0, q1;
+  unpack2(q, q0, q1);
+  return pack2(z0 < 0.f ? q0 : 1.f - q0, z1 < 0.f ? q1 : 1.f - q1);
 }
-template <int ACT>
-__device__ __forceinline__ float act_f(float z) {
-  if constexpr (ACT == kActRelu) return fmaxf(z, 0.f);
-  if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
-  if constexpr (ACT == kActGelu) {
-    float e;
-    return z * normal_cdf(z, &e);
+
+// v = act(v)
+template <int ACT, int N>
+__device__ __forceinline__ void act_n(float (&v)[N]) {
+  static_assert(N % 2 == 0, "");
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    if constexpr (ACT == kActRelu) {
+      v[i] = fmaxf(v[i], 0.f);
+      v[i + 1] = fmaxf(v[i + 1], 0.f);
+    } else if constexpr (ACT == kActSilu) {
+      v[i] *= sigmoid_f(v[i]);
+      v[i + 1] *= sigmoid_f(v[i + 1]);
+    } else if constexpr (ACT == kActGelu) {
+      F2 e;
+      unpack2(mul2(pack2(v[i], v[i + 1]), normal_cdf2(v[i], v[i + 1], &e)), v[i], v[i + 1]);
+    }
   }
-  return z;
 }
-// act'(z)
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == kActSilu) {
-    const float s = sigmoid_f(z);
-    return s * fmaf(z, 1.f - s, 1.f);
+// g = g act'(z)
+template <int ACT, int N>
+__device__ __forceinline__ void slope_n(float (&g)[N], const float (&z)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float z0 = z[i], z1 = N > 1 ? z[i + (N > 1)] : 0.f;
+    float s0, s1;
+    if constexpr (ACT == kActRelu) {
+      s0 = z0 > 0.f ? 1.f : 0.f, s1 = z1 > 0.f ? 1.f : 0.f;
+    } else if constexpr (ACT == kActSilu) {
+      const float a = sigmoid_f(z0), b = sigmoid_f(z1);
+      s0 = a * fmaf(z0, 1.f - a, 1.f), s1 = b * fmaf(z1, 1.f - b, 1.f);
+    } else if constexpr (ACT == kActGelu) {
+      F2 e;
+      const F2 c = normal_cdf2(z0, z1, &e);
+      unpack2(fma2(mul2(pack2(z0, z1), both(0.39894228040143268f)), e, c), s0, s1);
+    } else {
+      s0 = s1 = 1.f;
+    }
+    g[i] *= s0;
+    if constexpr (N > 1) g[i + 1] *= s1;
   }
-  if constexpr (ACT == kActGelu) {
-    float e;
-    const float c = normal_cdf(z, &e);
-    return fmaf(z * 0.39894228040143268f, e, c);
-  }
-  return 1.f;
 }
 
 template <int N>
 __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
-  if (act == kActRelu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_f<kActRelu>(v[i]);
-  } else if (act == kActSilu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_f<kActSilu>(v[i]);
-  } else if (act == kActGelu) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = act_f<kActGelu>(v[i]);
-  }
+  if (act == kActRelu) act_n<kActRelu>(v);
+  else if (act == kActSilu) act_n<kActSilu>(v);
+  else if (act == kActGelu) act_n<kActGelu>(v);
 }
 
 __device__ __forceinline__ float load_any(const void* p, bool f32, long long i) {
   return f32 ? static_cast<const float*>(p)[i]
              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// v += bias[c0 .. c0 + 31]: the same addresses in every lane, so a 16-byte
+// load serves the warp with one L1 access (32 shuffles of a lane's own column
+// took longer than the addition hides).
+__device__ __forceinline__ void add_bias(const DenseParams& p, int c0, int N, float (&v)[32]) {
+  if (p.bias_vec && c0 + 32 <= N) {
+    if (p.bias_f32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + c0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = q[i];
+        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+      }
+    } else {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.bias) + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = q[i];
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] += __uint_as_float(u[j] << 16);
+          v[8 * i + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c0 + i < N) v[i] += load_any(p.bias, p.bias_f32, c0 + i);
+  }
 }
 
 // ---------------------------------------------------------------- pair kernel
@@ -138,7 +224,7 @@ __device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
   m.sA = base;
   m.sB = m.sA + STAGES * OPER;
   m.sEpi = m.sB + STAGES * OPER;
-  m.full = m.sEpi + 2 * kEpiWarps * EPI_BUF;
+  m.full = m.sEpi + kEpiWarps * EPI_WARP;
   m.empty = m.full + 8 * STAGES;
   m.acc_full = m.empty + 8 * STAGES;
   m.acc_empty = m.acc_full + 16;
@@ -245,6 +331,10 @@ __device__ __forceinline__ bool multiply(const PSmem& m, uint32_t dt, int nkb, R
   return true;
 }
 
+// ACT is a template argument and the column loop is not unrolled: with the
+// activations as runtime branches of an unrolled loop the epilogue's code
+// outgrew the instruction cache, which the lone producer and MMA threads share.
+template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ DenseParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -356,97 +446,119 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ epilogue
     // Eight warps: warps 0-3 take the tile's first 128 columns, 6-9 the second;
     // a warp holds rows 32 (w % 4) .. +31 of this CTA's 128 (the quarter of
-    // tensor memory that it can read), lane i row i.  A block
-    // of 128 bytes per row (64 bf16 or 32 f32 columns) is staged in the TMA
-    // store's 128-byte swizzle (conflict-free: the lanes of a quarter warp
-    // write eight different 16-byte columns) and leaves with one store
-    // instruction; two buffers per warp alternate.
+    // tensor memory that it can read), lane i row i.  32 columns at a time are
+    // staged in the TMA store's swizzle (64-byte rows for bf16, 128 for f32;
+    // conflict-free: the lanes of a quarter warp write eight different 16-byte
+    // columns) and leave with one store instruction.  The warp's four 2 KB
+    // units rotate, so a store is waited for only when its unit comes round.
     const int quad = warp & 3, half = warp >= 6 ? 1 : 0;
-    const uint32_t stg = m.sEpi + (half * 4 + quad) * 2 * EPI_BUF;
+    const uint32_t stg = m.sEpi + (half * 4 + quad) * EPI_WARP;
     const int row_w = static_cast<int>(rank) * kHalf + quad * 32;
-    int tcount = 0, nst = 0;
+    const int kq = lane & 7, rq = lane >> 3;  // residual: this lane's 16-byte column and first row
+    int tcount = 0, unit = 0;
     for (int tau = pair; tau < total; tau += npairs) {
       const PTile t = decode_pair(p, tau);
       const DenseProduct& d = p.pr[t.q];
       const int row0 = t.m0 + row_w;
       const int row = row0 + lane;
       const int acc = tcount & 1;
+      const int col_w = t.n0 + half * 128;  // first column of this warp
+      const int nblk = std::max(0, std::min(4, cdiv(d.N - col_w, 32)));  // 32-column blocks
+      const bool epi = d.epilogue;
+      // With aligned rows the residual is read four rows x 128 bytes per
+      // instruction (lane: 4 columns of rows rq + 4 j), one block ahead, and
+      // the sum stored the same way; the staged block is f32.
+      const bool res_fast = epi && p.residual && p.res_vec && d.out_tma;
+      float4 rf[8];
+      auto fetch_res = [&](int b) {
+        const int c = col_w + b * 32 + 4 * kq;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = row0 + rq + 4 * j;
+          if (r >= d.M || c >= d.N) continue;
+          const long long o = static_cast<long long>(r) * p.ldr + c;
+          if (p.res_f32) {
+            rf[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + o);
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + o);
+            rf[j] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+          }
+        }
+      };
+      if (res_fast && nblk > 0) fetch_res(0);
       if (!__all_sync(0xffffffffu, wait_bar(m.acc_full + 8 * acc, (tcount >> 1) & 1, wc))) break;
       tc_fence_after();
-      const int col_w = t.n0 + half * 128;  // first column of this warp
       const uint32_t taddr =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
-      const int nblk = std::max(0, std::min(4, cdiv(d.N - col_w, 32)));  // 32-column blocks
       if (nblk == 0) {  // nothing of the tile here
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
       }
-      // stage 32 columns of v as bf16 (half a block) or f32 (a block)
-      auto put = [&](uint32_t buf, const float(&v)[32], bool f32, int half) {
-        if (f32) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_shared_v4(buf + sw128_offset(lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2],
-                         v[4 * c + 3]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            st_shared_v4(buf + sw128_offset(lane, half * 4 + c),
-                         __uint_as_float(pack_bf16x2_rn(v[8 * c], v[8 * c + 1])),
-                         __uint_as_float(pack_bf16x2_rn(v[8 * c + 2], v[8 * c + 3])),
-                         __uint_as_float(pack_bf16x2_rn(v[8 * c + 4], v[8 * c + 5])),
-                         __uint_as_float(pack_bf16x2_rn(v[8 * c + 6], v[8 * c + 7])));
+      // Room for a block of 1 (bf16) or 2 (f32) units: blocks of one size wait
+      // for the store four units back; where both sizes mix (z kept beside an
+      // f32 output) an f32 block waits for every store before it.
+      auto room = [&](int units) {
+        if (units == 2) {
+          unit = (unit + 1) & 2;
+          if (lane == 0) {
+            if (p.pre)
+              bulk_wait_read<0>();
+            else
+              bulk_wait_read<1>();
+          }
+        } else if (lane == 0) {
+          bulk_wait_read<3>();
         }
+        __syncwarp();
+        const uint32_t buf = stg + unit * EPI_BUF;
+        unit = (unit + units) & 3;
+        return buf;
+      };
+      auto put_f32 = [&](uint32_t buf, const float(&v)[32]) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(buf + sw128_offset(lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      };
+      auto put_bf16 = [&](uint32_t buf, const float(&v)[32]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st_shared_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4),
+                       __uint_as_float(pack_bf16x2_rn(v[8 * c], v[8 * c + 1])),
+                       __uint_as_float(pack_bf16x2_rn(v[8 * c + 2], v[8 * c + 3])),
+                       __uint_as_float(pack_bf16x2_rn(v[8 * c + 4], v[8 * c + 5])),
+                       __uint_as_float(pack_bf16x2_rn(v[8 * c + 6], v[8 * c + 7])));
       };
       // a staged block to columns c0.. of rows row0..
-      auto flush = [&](uint32_t buf, const CUtensorMap* map, bool tma, void* base, int ld, bool f32,
-                       int c0) {
+      auto flush = [&](uint32_t buf, const CUtensorMap* map, bool tma, void* base, bool f32, int c0) {
         if (tma) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && row0 < d.M) {
-            tma_store_2d(map, buf, c0, row0);
+          if (lane == 0) {
+            if (row0 < d.M) tma_store_2d(map, buf, c0, row0);
+            bulk_commit();
           }
-          if (lane == 0) bulk_commit();
         } else {
-          // rows that do not start on 16-byte boundaries: element by element,
-          // a row at a time
+          // rows that do not start on 16-byte boundaries: a row at a time,
+          // lane = column
           __syncwarp();
-          const int per = f32 ? 32 : 64;
-          for (int r = 0; r < 32 && row0 + r < d.M; ++r)
-            for (int c = lane; c < per; c += 32) {
-              if (c0 + c >= d.N) continue;
-              const uint32_t at = buf + sw128_offset(r, c / (per / 8));
-              const long long o = static_cast<long long>(row0 + r) * ld + c0 + c;
+          if (c0 + lane < d.N)
+            for (int r = 0; r < 32 && row0 + r < d.M; ++r) {
+              const long long o = static_cast<long long>(row0 + r) * d.N + c0 + lane;
               if (f32) {
-                static_cast<float*>(base)[o] = __int_as_float(ld_shared_s32(at + (c & 3) * 4));
+                static_cast<float*>(base)[o] =
+                    __int_as_float(ld_shared_s32(buf + sw128_offset(r, lane >> 2) + (lane & 3) * 4));
               } else {
-                const uint32_t u = static_cast<uint32_t>(ld_shared_s32(at + ((c & 7) >> 1) * 4));
+                const uint32_t at = buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4);
+                const uint32_t u = static_cast<uint32_t>(ld_shared_s32(at + ((lane & 7) >> 1) * 4));
                 static_cast<unsigned short*>(base)[o] =
-                    static_cast<unsigned short>(c & 1 ? u >> 16 : u);
+                    static_cast<unsigned short>(lane & 1 ? u >> 16 : u);
               }
             }
           __syncwarp();
         }
       };
-      // With z kept, its block lies in the first buffer and the output's in
-      // the second; else the output's blocks alternate.
-      const bool keep = d.epilogue && p.pre;
-      auto next_buf = [&](bool is_pre) {
-        uint32_t b = stg;
-        if (keep) {
-          if (!is_pre) b += EPI_BUF;
-          if (lane == 0) bulk_wait_read<0>();
-        } else {
-          b += (nst & 1) * EPI_BUF;
-          ++nst;
-          if (lane == 0) bulk_wait_read<1>();  // the store two blocks ago has read it
-        }
-        __syncwarp();
-        return b;
-      };
-      uint32_t obuf = 0, pbuf = 0;
 #pragma unroll 1
       for (int b = 0; b < nblk; ++b) {
         float v[32];
@@ -458,59 +570,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
         }
         const int c0 = col_w + b * 32;
-        const bool last = b == nblk - 1;
-        if (d.epilogue) {
-          if (p.bias) {
-            const float bl = c0 + lane < d.N ? load_any(p.bias, p.bias_f32, c0 + lane) : 0.f;
+        if (epi) {
+          if (p.bias) add_bias(p, c0, d.N, v);
+          if (p.pre) {
+            const uint32_t buf = room(1);
+            put_bf16(buf, v);
+            flush(buf, &maps.pre, p.pre_tma, p.pre, false, c0);
+          }
+          act_n<ACT>(v);
+          if (res_fast) {
+            const uint32_t buf = room(2);
+            put_f32(buf, v);
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bl, i);
+            for (int j = 0; j < 8; ++j) {
+              const int r = rq + 4 * j;
+              float4 x = ld_shared_v4(buf + sw128_offset(r, kq));
+              x.x += rf[j].x, x.y += rf[j].y, x.z += rf[j].z, x.w += rf[j].w;
+              if (row0 + r >= d.M || c0 + 4 * kq >= d.N) continue;
+              const long long o = static_cast<long long>(row0 + r) * d.N + c0 + 4 * kq;
+              if (d.out_f32)
+                *reinterpret_cast<float4*>(static_cast<float*>(d.out) + o) = x;
+              else
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(d.out) + o) =
+                    make_uint2(pack_bf16x2_rn(x.x, x.y), pack_bf16x2_rn(x.z, x.w));
+            }
+            if (b + 1 < nblk) fetch_res(b + 1);
+            continue;
           }
-          if (keep) {
-            if ((b & 1) == 0) pbuf = next_buf(true);
-            put(pbuf, v, false, b & 1);
-            if ((b & 1) || last) flush(pbuf, &maps.pre, p.pre_tma, p.pre, d.N, false, c0 - (b & 1) * 32);
-          }
-          act_all<32>(p.act, v);
           if (p.residual && row < d.M) {
             const long long ro = static_cast<long long>(row) * p.ldr + c0;
-            if (p.res_vec && c0 + 32 <= d.N) {
-              if (p.res_f32) {
-                const float4* r4 = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + ro);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 x = r4[i];
-                  v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
-                }
-              } else {
-                const uint4* r4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint4 x = r4[i];
-                  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    v[8 * i + 2 * j] += __uint_as_float(u[j] << 16);
-                    v[8 * i + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
-                  }
-                }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c0 + i < d.N) v[i] += load_any(p.residual, p.res_f32, ro + i);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (c0 + i < d.N) v[i] += load_any(p.residual, p.res_f32, ro + i);
           }
         }
-        if (d.out_f32) {
-          obuf = next_buf(false);
-          put(obuf, v, true, 0);
-          flush(obuf, &maps.out[t.q], d.out_tma, d.out, d.N, true, c0);
-        } else {
-          if ((b & 1) == 0) obuf = next_buf(false);
-          put(obuf, v, false, b & 1);
-          if ((b & 1) || last)
-            flush(obuf, &maps.out[t.q], d.out_tma, d.out, d.N, false, c0 - (b & 1) * 32);
-        }
+        const uint32_t buf = room(d.out_f32 ? 2 : 1);
+        if (d.out_f32)
+          put_f32(buf, v);
+        else
+          put_bf16(buf, v);
+        flush(buf, &maps.out[t.q], d.out_tma, d.out, d.out_f32, c0);
       }
       ++tcount;
     }
@@ -793,7 +893,6 @@ __global__ void __launch_bounds__(kThreads)
 // and 256 / lanes rows; its partial sums add up in shared memory in row order.
 struct DzArgs {
   const void* dy;
-  bool dy_f32;
   long long lddy;
   const __nv_bfloat16* pre;
   int T, N, rows, lanes;
@@ -801,26 +900,50 @@ struct DzArgs {
   int ldz;
   float* part;        // null: no sums
 };
-template <int VEC>
-__device__ __forceinline__ void load_row(const void* p, bool f32, long long i, float (&v)[VEC]) {
+// VEC consecutive elements as they lie in memory
+template <typename T, int VEC>
+struct Piece {
+  T v;
+};
+template <>
+struct Piece<__nv_bfloat16, 8> {
+  uint4 q;
+};
+template <>
+struct Piece<float, 8> {
+  float4 q[2];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Piece<T, VEC> load_piece(const T* p) {
+  Piece<T, VEC> r;
   if constexpr (VEC == 1) {
-    v[0] = load_any(p, f32, i);
-  } else if (f32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    r.v = *p;
+  } else if constexpr (sizeof(T) == 2) {
+    r.q = *reinterpret_cast<const uint4*>(p);
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+    r.q[0] = reinterpret_cast<const float4*>(p)[0];
+    r.q[1] = reinterpret_cast<const float4*>(p)[1];
+  }
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void floats(const Piece<T, VEC>& r, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = static_cast<float>(r.v);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t u[4] = {r.q.x, r.q.y, r.q.z, r.q.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(u[j] << 16);
       v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
     }
+  } else {
+    v[0] = r.q[0].x, v[1] = r.q[0].y, v[2] = r.q[0].z, v[3] = r.q[0].w;
+    v[4] = r.q[1].x, v[5] = r.q[1].y, v[6] = r.q[1].z, v[7] = r.q[1].w;
   }
 }
-template <int ACT, int VEC>
-__global__ void __launch_bounds__(256) dense_dz_kernel(const DzArgs a) {
+template <int ACT, typename DT, int VEC>
+__global__ void __launch_bounds__(256, 4) dense_dz_kernel(const DzArgs a) {
   __shared__ float acc[256 * VEC];
   pdl_trigger();
   pdl_wait();
@@ -831,25 +954,41 @@ __global__ void __launch_bounds__(256) dense_dz_kernel(const DzArgs a) {
 #pragma unroll
   for (int i = 0; i < VEC; ++i) sum[i] = 0.f;
   if (n < a.N) {
-#pragma unroll 4
-    for (int t = t0 + ry; t < t1; t += nr) {
-      float v[VEC], z[VEC];
-      load_row<VEC>(a.dy, a.dy_f32, t * a.lddy + n, v);
-      if constexpr (ACT != kActNone) {
-        load_row<VEC>(a.pre, false, static_cast<long long>(t) * a.N + n, z);
+    // rows in batches whose loads are all issued before the first is used
+    // (the stores to dz keep the compiler from moving later loads up)
+    constexpr int U = sizeof(DT) == 4 && VEC == 8 ? 2 : 4;
+    for (int tb = t0 + ry; tb < t1; tb += U * nr) {
+      Piece<DT, VEC> dy[U];
+      Piece<__nv_bfloat16, VEC> pre[U];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] *= act_slope<ACT>(z[i]);
+      for (int u = 0; u < U; ++u) {
+        const int t = min(tb + u * nr, t1 - 1);  // (past the end: a row that is not used)
+        dy[u] = load_piece<DT, VEC>(static_cast<const DT*>(a.dy) + t * a.lddy + n);
+        if constexpr (ACT != kActNone)
+          pre[u] = load_piece<__nv_bfloat16, VEC>(a.pre + static_cast<long long>(t) * a.N + n);
       }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) sum[i] += v[i];
-      if (a.dz) {
-        __nv_bfloat16* o = a.dz + static_cast<long long>(t) * a.ldz + n;
-        if constexpr (VEC == 1)
-          *o = __float2bfloat16_rn(v[0]);
-        else
-          *reinterpret_cast<uint4*>(o) =
-              make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
-                         pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+      for (int u = 0; u < U; ++u) {
+        const int t = tb + u * nr;
+        if (t >= t1) break;
+        float v[VEC];
+        floats<DT, VEC>(dy[u], v);
+        if constexpr (ACT != kActNone) {
+          float z[VEC];
+          floats<__nv_bfloat16, VEC>(pre[u], z);
+          slope_n<ACT>(v, z);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum[i] += v[i];
+        if (a.dz) {
+          __nv_bfloat16* o = a.dz + static_cast<long long>(t) * a.ldz + n;
+          if constexpr (VEC == 1)
+            *o = __float2bfloat16_rn(v[0]);
+          else
+            *reinterpret_cast<uint4*>(o) =
+                make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                           pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+        }
       }
     }
   }
@@ -879,7 +1018,7 @@ cudaError_t allow_smem(K kern, size_t smem, bool* done) {
 }
 
 // Co-resident clusters of two (persistent grid).
-int pair_count() {
+int pair_count() {  // (one block per SM, whatever the activation)
   static int cache[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -895,7 +1034,7 @@ int pair_count() {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel, &cfg) != cudaSuccess || n < 1)
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<kActNone>, &cfg) != cudaSuccess || n < 1)
     n = num_sms() / 2;
   n = std::min(n, num_sms() / 2);
   if (dev < 64) cache[dev] = n;
@@ -920,6 +1059,16 @@ bool use_pairs(const DenseProduct& d) {
 
 bool out_by_tma(const void* out, int N, bool f32) {
   return aligned16(out) && (static_cast<long long>(N) * (f32 ? 4 : 2)) % 16 == 0;
+}
+
+template <int ACT>
+cudaError_t launch_pairs_act(const PairMaps& maps, const DenseParams& p, int total,
+                             cudaStream_t st) {
+  static bool done[64] = {};
+  cudaError_t e = allow_smem(dense_pair_kernel<ACT>, kPairSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(dense_pair_kernel<ACT>, dim3(2 * std::min(pair_count(), total)),
+                    dim3(kPairThreads), kPairSmem, st, maps, p);
 }
 
 cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperand* b, int n,
@@ -947,11 +1096,10 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
     if (p.pre_tma && !encode_tmap_out(&maps.pre, p.pre, false, p.pr[0].M, p.pr[0].N))
       return cudaErrorInvalidValue;
   }
-  static bool done[64] = {};
-  cudaError_t e = allow_smem(dense_pair_kernel, kPairSmem, done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(dense_pair_kernel, dim3(2 * std::min(pair_count(), total)), dim3(kPairThreads),
-                    kPairSmem, st, maps, p);
+  if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, total, st);
+  if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, total, st);
+  if (p.act == kActGelu) return launch_pairs_act<kActGelu>(maps, p, total, st);
+  return launch_pairs_act<kActNone>(maps, p, total, st);
 }
 
 // Tile columns, orientation and contraction pieces of a product on
@@ -1056,10 +1204,14 @@ int max_partials(int T, int N) {
 }
 
 template <int ACT>
-cudaError_t launch_dz(const DzPlan& pl, const DzArgs& a, cudaStream_t st) {
+cudaError_t launch_dz(const DzPlan& pl, const DzArgs& a, bool dy_f32, cudaStream_t st) {
   const dim3 grid(pl.bx, pl.by), block(256);
-  return pl.vec == 8 ? launch_pdl(dense_dz_kernel<ACT, 8>, grid, block, 0, st, a)
-                     : launch_pdl(dense_dz_kernel<ACT, 1>, grid, block, 0, st, a);
+  using B = __nv_bfloat16;
+  if (pl.vec == 8)
+    return dy_f32 ? launch_pdl(dense_dz_kernel<ACT, float, 8>, grid, block, 0, st, a)
+                  : launch_pdl(dense_dz_kernel<ACT, B, 8>, grid, block, 0, st, a);
+  return dy_f32 ? launch_pdl(dense_dz_kernel<ACT, float, 1>, grid, block, 0, st, a)
+                : launch_pdl(dense_dz_kernel<ACT, B, 1>, grid, block, 0, st, a);
 }
 
 bool dy_is_operand(const DenseBackward& a) {
@@ -1094,12 +1246,12 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
   if (dz_out || part_out) {
     const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && aligned16(a.dy) && aligned16(a.pre);
     const DzPlan pl = plan_dz(a.T, a.N, vec);
-    const DzArgs z{a.dy,    a.dy_f32, a.lddy,   static_cast<const __nv_bfloat16*>(a.pre), a.T,
-                   a.N,     pl.rows,  pl.lanes, dz_out, ldz, part_out};
-    if (a.act == kActRelu) e = launch_dz<kActRelu>(pl, z, st);
-    else if (a.act == kActSilu) e = launch_dz<kActSilu>(pl, z, st);
-    else if (a.act == kActGelu) e = launch_dz<kActGelu>(pl, z, st);
-    else e = launch_dz<kActNone>(pl, z, st);
+    const DzArgs z{a.dy, a.lddy,  static_cast<const __nv_bfloat16*>(a.pre), a.T, a.N, pl.rows,
+                   pl.lanes, dz_out, ldz, part_out};
+    if (a.act == kActRelu) e = launch_dz<kActRelu>(pl, z, a.dy_f32, st);
+    else if (a.act == kActSilu) e = launch_dz<kActSilu>(pl, z, a.dy_f32, st);
+    else if (a.act == kActGelu) e = launch_dz<kActGelu>(pl, z, a.dy_f32, st);
+    else e = launch_dz<kActNone>(pl, z, a.dy_f32, st);
     if (e == cudaSuccess && part_out)
       e = launch_column_sums(part, pl.by, a.N, a.db, nullptr, a.db_f32, st);
     if (e != cudaSuccess) return e;
