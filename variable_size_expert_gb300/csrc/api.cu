@@ -342,11 +342,11 @@ bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* d
   return r == CUDA_SUCCESS;
 }
 
-bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols) {
+bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols, long long ld) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
   if (!fn) return false;
   cuuint64_t d[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t st[1] = {static_cast<cuuint64_t>(cols) * (f32 ? 4 : 2)};
+  cuuint64_t st[1] = {static_cast<cuuint64_t>(ld) * (f32 ? 4 : 2)};
   cuuint32_t b[2] = {32, 32};
   cuuint32_t estr[2] = {1, 1};
   const CUresult r =

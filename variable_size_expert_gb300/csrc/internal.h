@@ -187,7 +187,8 @@ struct DenseParams {
   bool bias_f32, bias_vec;  // bias_vec: 16-byte loads
   int act;
   const void* residual;  // [M, ldr] or null
-  bool res_f32, res_vec; // res_vec: 16-byte loads
+  bool res_f32, res_vec; // res_vec: base and rows on 16-byte boundaries
+  bool res_tma;          // set by the launcher
   long long ldr;
   void* pre;             // bf16 z [M, N] or null
   bool pre_tma;          // set by the launcher
@@ -220,9 +221,9 @@ long long wait_limit();
 bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box);
 
-// [rows][cols] bf16 or f32 output for TMA stores of 32 rows x 32 columns
+// [rows][cols] bf16 or f32, row stride ld elements, for TMA stores (and loads) of 32 rows x 32 columns
 // (bf16: 64-byte swizzle, f32: 128-byte)
-bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols);
+bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols, long long ld);
 
 // norm.cu
 int norm_bwd_blocks();  // partial rows of the weight and bias gradients

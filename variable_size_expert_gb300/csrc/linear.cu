@@ -38,10 +38,13 @@ constexpr int STAGES = 5;
 constexpr int OPER = kHalf * BK * 2;    // 16 KB
 constexpr int CHUNK = 64 * BK * 2;      // 8 KB: 64 wide MN-major block of one stage
 constexpr int EPI_BUF = 32 * 64;        // staging unit: 32 rows x 64 bytes (32 bf16 columns)
-constexpr int EPI_WARP = 4 * EPI_BUF;   // per epilogue warp
+constexpr int EPI_WARP = 2 * EPI_BUF;   // per epilogue warp
 constexpr int kThreads = 192;           // single-CTA tiles: warps 0-3 epilogue, 4 MMA, 5 TMA
-constexpr int kEpiWarps = 8;            // pairs: warps 0-3 and 6-9 epilogue, 4 MMA, 5 TMA
-constexpr int kPairThreads = 320;
+// pairs: warps 0-3 and 6-17 epilogue, 4 MMA, 5 TMA.  Sixteen epilogue warps
+// hide one another's latencies (tensor memory, exponentials, store fences):
+// with eight, bias + GELU + kept z took 9.1 us a tile, half of it stalled.
+constexpr int kEpiWarps = 16;
+constexpr int kPairThreads = 32 * (kEpiWarps + 2);
 constexpr int kMeta = 512;
 constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + kEpiWarps * EPI_WARP + kMeta;
 static_assert(kPairSmem <= 232448, "shared memory per block");
@@ -208,11 +211,11 @@ __device__ __forceinline__ void add_bias(const DenseParams& p, int c0, int N, fl
 
 // ---------------------------------------------------------------- pair kernel
 struct PairMaps {
-  CUtensorMap a[2], b[2], out[2], pre;
+  CUtensorMap a[2], b[2], out[2], pre, res;
 };
 
 struct PSmem {
-  uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, issued;
+  uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, res_full, issued;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
 };
@@ -230,7 +233,8 @@ __device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
   m.acc_empty = m.acc_full + 16;
   m.drain = m.acc_empty + 16;
   m.pdone = m.drain + 8;
-  m.issued = m.pdone + 8;
+  m.res_full = m.pdone + 8;  // one per epilogue warp
+  m.issued = m.res_full + 8 * kEpiWarps;
   m.tmem_slot = reinterpret_cast<uint32_t*>(g + (m.issued + 8 - base));
   m.abort_flag = reinterpret_cast<volatile int*>(m.tmem_slot + 1);
   return m;
@@ -360,6 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(m.drain, 1);
     mbar_init(m.pdone, 1);
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(m.res_full + 8 * w, 1);
     *m.abort_flag = 0;
     fence_mbar_init();
   }
@@ -444,76 +449,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ------------------------------------------------ epilogue
-    // Eight warps: warps 0-3 take the tile's first 128 columns, 6-9 the second;
-    // a warp holds rows 32 (w % 4) .. +31 of this CTA's 128 (the quarter of
-    // tensor memory that it can read), lane i row i.  32 columns at a time are
-    // staged in the TMA store's swizzle (64-byte rows for bf16, 128 for f32;
-    // conflict-free: the lanes of a quarter warp write eight different 16-byte
-    // columns) and leave with one store instruction.  The warp's four 2 KB
-    // units rotate, so a store is waited for only when its unit comes round.
-    const int quad = warp & 3, half = warp >= 6 ? 1 : 0;
-    const uint32_t stg = m.sEpi + (half * 4 + quad) * EPI_WARP;
+    // Four warps per 64 columns of the tile; a warp holds rows 32 (w % 4) ..
+    // +31 of this CTA's 128 (the quarter of tensor memory that it can read),
+    // lane i row i.  32 columns at a time are staged in the TMA store's swizzle
+    // (64-byte rows for bf16, 128 for f32; conflict-free: the lanes of a
+    // quarter warp write eight different 16-byte columns) and leave with one
+    // store instruction.  A bf16 block takes one of the warp's two 2 KB units
+    // in turn, an f32 block both.
+    const int quad = warp & 3, group = warp < 4 ? 0 : (warp - 2) >> 2;
+    const int ew = group * 4 + quad;
+    const uint32_t stg = m.sEpi + ew * EPI_WARP;
+    const uint32_t res_bar = m.res_full + 8 * ew;
     const int row_w = static_cast<int>(rank) * kHalf + quad * 32;
-    const int kq = lane & 7, rq = lane >> 3;  // residual: this lane's 16-byte column and first row
-    int tcount = 0, unit = 0;
+    int tcount = 0, unit = 0, res_n = 0;
+    bool res_open = false;  // a residual block is on its way
     for (int tau = pair; tau < total; tau += npairs) {
       const PTile t = decode_pair(p, tau);
       const DenseProduct& d = p.pr[t.q];
       const int row0 = t.m0 + row_w;
       const int row = row0 + lane;
       const int acc = tcount & 1;
-      const int col_w = t.n0 + half * 128;  // first column of this warp
-      const int nblk = std::max(0, std::min(4, cdiv(d.N - col_w, 32)));  // 32-column blocks
+      const int col_w = t.n0 + group * 64;  // first column of this warp
+      const int nblk = std::max(0, std::min(2, cdiv(d.N - col_w, 32)));  // 32-column blocks
       const bool epi = d.epilogue;
-      // With aligned rows the residual is read four rows x 128 bytes per
-      // instruction (lane: 4 columns of rows rq + 4 j), one block ahead, and
-      // the sum stored the same way; the staged block is f32.
-      const bool res_fast = epi && p.residual && p.res_vec && d.out_tma;
-      float4 rf[8];
-      auto fetch_res = [&](int b) {
-        const int c = col_w + b * 32 + 4 * kq;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = row0 + rq + 4 * j;
-          if (r >= d.M || c >= d.N) continue;
-          const long long o = static_cast<long long>(r) * p.ldr + c;
-          if (p.res_f32) {
-            rf[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + o);
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + o);
-            rf[j] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-          }
+      // The residual's block comes by TMA into the staging area that the
+      // result then takes: the first one while the tile is multiplied.
+      const bool res_tma = epi && p.res_tma && row0 < d.M;
+      auto fetch_res = [&](int c0) {
+        if (lane == 0) {
+          bulk_wait_read<0>();  // the stores before have left the staging area
+          mbar_arrive_expect_tx(res_bar, p.res_f32 ? 4096 : 2048);
+          tma_load_2d(stg, &maps.res, res_bar, c0, row0);
         }
+        res_open = true;
       };
-      if (res_fast && nblk > 0) fetch_res(0);
+      if (res_tma && nblk > 0) {
+        __syncwarp();
+        fetch_res(col_w);
+      }
       if (!__all_sync(0xffffffffu, wait_bar(m.acc_full + 8 * acc, (tcount >> 1) & 1, wc))) break;
       tc_fence_after();
       const uint32_t taddr =
-          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + half * 128;
+          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + group * 64;
       if (nblk == 0) {  // nothing of the tile here
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
       }
-      // Room for a block of 1 (bf16) or 2 (f32) units: blocks of one size wait
-      // for the store four units back; where both sizes mix (z kept beside an
-      // f32 output) an f32 block waits for every store before it.
+      // room for a block of 1 or 2 units
       auto room = [&](int units) {
-        if (units == 2) {
-          unit = (unit + 1) & 2;
-          if (lane == 0) {
-            if (p.pre)
-              bulk_wait_read<0>();
-            else
-              bulk_wait_read<1>();
-          }
-        } else if (lane == 0) {
-          bulk_wait_read<3>();
+        if (lane == 0) {
+          if (units == 2)
+            bulk_wait_read<0>();
+          else
+            bulk_wait_read<1>();
         }
         __syncwarp();
+        if (units == 2) unit = 0;
         const uint32_t buf = stg + unit * EPI_BUF;
-        unit = (unit + units) & 3;
+        if (units == 1) unit ^= 1;
         return buf;
       };
       auto put_f32 = [&](uint32_t buf, const float(&v)[32]) {
@@ -578,27 +572,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             flush(buf, &maps.pre, p.pre_tma, p.pre, false, c0);
           }
           act_n<ACT>(v);
-          if (res_fast) {
-            const uint32_t buf = room(2);
-            put_f32(buf, v);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int r = rq + 4 * j;
-              float4 x = ld_shared_v4(buf + sw128_offset(r, kq));
-              x.x += rf[j].x, x.y += rf[j].y, x.z += rf[j].z, x.w += rf[j].w;
-              if (row0 + r >= d.M || c0 + 4 * kq >= d.N) continue;
-              const long long o = static_cast<long long>(row0 + r) * d.N + c0 + 4 * kq;
-              if (d.out_f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(d.out) + o) = x;
-              else
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(d.out) + o) =
-                    make_uint2(pack_bf16x2_rn(x.x, x.y), pack_bf16x2_rn(x.z, x.w));
+          if (res_tma) {
+            if (b > 0) {
+              __syncwarp();
+              fetch_res(c0);
             }
-            if (b + 1 < nblk) fetch_res(b + 1);
-            continue;
-          }
-          if (p.residual && row < d.M) {
+            const bool ok = __all_sync(0xffffffffu, wait_bar(res_bar, res_n & 1, wc));
+            res_open = !ok;
+            ++res_n;
+            if (p.res_f32) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float4 x = ld_shared_v4(stg + sw128_offset(lane, c));
+                v[4 * c] += x.x, v[4 * c + 1] += x.y, v[4 * c + 2] += x.z, v[4 * c + 3] += x.w;
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float4 x = ld_shared_v4(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+                const uint32_t u[4] = {__float_as_uint(x.x), __float_as_uint(x.y),
+                                       __float_as_uint(x.z), __float_as_uint(x.w)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  v[8 * c + 2 * j] += __uint_as_float(u[j] << 16);
+                  v[8 * c + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+                }
+              }
+            }
+            __syncwarp();  // every lane has read its row before any writes
+          } else if (p.residual && row < d.M) {
             const long long ro = static_cast<long long>(row) * p.ldr + c0;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -613,6 +615,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         flush(buf, &maps.out[t.q], d.out_tma, d.out, d.out_f32, c0);
       }
       ++tcount;
+    }
+    if (lane == 0) {
+      if (res_open) wait_bar_drain(res_bar, res_n & 1, DRAIN_LIMIT);
+      bulk_wait<0>();
     }
     if (lane == 0) bulk_wait<0>();
   }
@@ -1088,14 +1094,20 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
     if (!tmap_operand(&maps.a[q], a[q], d.a_mn, kHalf) ||
         !tmap_operand(&maps.b[q], b[q], d.b_mn, kHalf))
       return cudaErrorInvalidValue;
-    if (d.out_tma && !encode_tmap_out(&maps.out[q], d.out, d.out_f32, d.M, d.N))
+    if (d.out_tma && !encode_tmap_out(&maps.out[q], d.out, d.out_f32, d.M, d.N, d.N))
       return cudaErrorInvalidValue;
   }
   if (p.pre) {
     p.pre_tma = out_by_tma(p.pre, p.pr[0].N, false);
-    if (p.pre_tma && !encode_tmap_out(&maps.pre, p.pre, false, p.pr[0].M, p.pr[0].N))
+    if (p.pre_tma && !encode_tmap_out(&maps.pre, p.pre, false, p.pr[0].M, p.pr[0].N, p.pr[0].N))
       return cudaErrorInvalidValue;
   }
+  // the residual by TMA, where its rows allow and z does not need the staging
+  // area at the same time
+  p.res_tma = p.residual && p.res_vec && !p.pre;
+  if (p.res_tma && !encode_tmap_out(&maps.res, const_cast<void*>(p.residual), p.res_f32, p.pr[0].M,
+                                    p.pr[0].N, p.ldr))
+    return cudaErrorInvalidValue;
   if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, total, st);
   if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, total, st);
   if (p.act == kActGelu) return launch_pairs_act<kActGelu>(maps, p, total, st);
