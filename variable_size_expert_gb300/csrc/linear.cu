@@ -643,12 +643,129 @@ struct CtaParams {
   int Mr, Nc;      // extents along the tile's rows and columns
   int BN;          // tile columns (16..256, a multiple of 16)
   int splits;      // CTAs per cluster: pieces of the contraction
+  int per;         // columns that each CTA of a cluster finishes (a multiple of 4)
   int stages;
   int b_bytes;     // B bytes per stage
   int tmem_cols;
-  int vec_out, vec_pre;  // 16-byte stores of 8 columns
+  int vec_out, vec_pre, vec_res;  // accesses of 4 columns at once
 };
+constexpr int kCtaMeta = 256;
+size_t cta_smem(const CtaParams& c) {
+  return 1024 + static_cast<size_t>(c.stages) * (OPER + c.b_bytes) +
+         (c.splits > 1 ? static_cast<size_t>(c.splits) * c.per * 512 : 0) + kCtaMeta;
+}
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// 16 bytes into the shared memory of any CTA of the cluster, counted on that
+// CTA's mbarrier (both cluster addresses).
+__device__ __forceinline__ void st_async_v4(uint32_t dst, uint32_t bar, float a, float b, float c,
+                                            float d) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::
+          "r"(dst),
+      "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+      : "memory");
+}
+
+// Finish four columns of one tile row: v holds the contraction's sum for
+// output column(s) / row(s) j0 .. j0 + 3 along the tile's columns.
+__device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p, int row, int col0,
+                                        float (&v)[4]) {
+  const DenseProduct& d = c.d;
+  if (row >= c.Mr) return;
+  const int nv = std::min(4, c.Nc - col0);
+  if (nv <= 0) return;
+  if (c.swap) {
+    // output[col, row]: consecutive lanes write consecutive elements
+    if (d.epilogue) {
+      if (p.bias) {
+        const float bv = load_any(p.bias, p.bias_f32, row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += bv;
+      }
+      if (p.pre) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < nv)
+            static_cast<__nv_bfloat16*>(p.pre)[static_cast<long long>(col0 + i) * d.N + row] =
+                __float2bfloat16_rn(v[i]);
+      }
+      float r[4] = {0.f, 0.f, 0.f, 0.f};
+      if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < nv) r[i] = load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row);
+      }
+      act_all<4>(p.act, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += r[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= nv) continue;
+      const long long o = static_cast<long long>(col0 + i) * d.N + row;
+      if (d.out_f32)
+        static_cast<float*>(d.out)[o] = v[i];
+      else
+        static_cast<__nv_bfloat16*>(d.out)[o] = __float2bfloat16_rn(v[i]);
+    }
+    return;
+  }
+  auto store4 = [&](void* out, bool f32, bool vec) {
+    const long long o = static_cast<long long>(row) * d.N + col0;
+    if (vec && nv == 4) {
+      if (f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
+            make_uint2(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= nv) continue;
+        if (f32)
+          static_cast<float*>(out)[o + i] = v[i];
+        else
+          static_cast<__nv_bfloat16*>(out)[o + i] = __float2bfloat16_rn(v[i]);
+      }
+    }
+  };
+  if (d.epilogue) {
+    float r[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.residual) {
+      const long long ro = static_cast<long long>(row) * p.ldr + col0;
+      if (c.vec_res && p.res_f32 && nv == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + ro);
+        r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
+      } else if (c.vec_res && nv == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
+        r[0] = __uint_as_float(u.x << 16), r[1] = __uint_as_float(u.x & 0xffff0000u);
+        r[2] = __uint_as_float(u.y << 16), r[3] = __uint_as_float(u.y & 0xffff0000u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < nv) r[i] = load_any(p.residual, p.res_f32, ro + i);
+      }
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < nv) v[i] += load_any(p.bias, p.bias_f32, col0 + i);
+    }
+    if (p.pre) store4(p.pre, false, c.vec_pre);
+    act_all<4>(p.act, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += r[i];
+  }
+  store4(d.out, d.out_f32, c.vec_out);
+}
+
+template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads)
     dense_cta_kernel(const __grid_constant__ CtaMaps maps, const __grid_constant__ CtaParams c,
                      const __grid_constant__ DenseParams p) {
@@ -656,13 +773,15 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw_addr);
-  const int stage_bytes = OPER + c.b_bytes;
-  const uint32_t meta = base + std::max(c.stages * stage_bytes, c.splits > 1 ? c.BN * 512 : 0);
-  const uint32_t full = meta, empty = meta + 64, acc_full = meta + 128;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (meta + 136 - base));
+  const int b_bytes = c.b_bytes, stages = c.stages;
+  const uint32_t stage_bytes = OPER + b_bytes;
+  const int S = c.splits;
+  const uint32_t recv = base + stages * stage_bytes;  // partial sums from the cluster
+  const uint32_t meta = recv + (S > 1 ? S * c.per * 512 : 0);
+  const uint32_t full = meta, empty = meta + 64, acc_full = meta + 128, got = meta + 136;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (meta + 144 - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = c.splits;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / S;
   const int tr = cdiv(c.Mr, 128);
@@ -670,6 +789,7 @@ __global__ void __launch_bounds__(kThreads)
   const int nkb = cdiv(c.d.Kc, BK);
   const int kb0 = static_cast<int>(static_cast<long long>(rank) * nkb / S);
   const int kb1 = static_cast<int>(static_cast<long long>(rank + 1) * nkb / S);
+  const int own0 = rank * c.per, own1 = std::min(c.BN, own0 + c.per);  // columns finished here
 
   if (warp == 5 && lane == 0) {
     tma_prefetch_desc(&maps.a);
@@ -677,13 +797,15 @@ __global__ void __launch_bounds__(kThreads)
   }
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < c.stages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(got, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (S > 1 && own1 > own0) mbar_arrive_expect_tx(got, S * (own1 - own0) * 512);
   }
   if (warp == 4) {
     tmem_alloc(smem_u32(tmem_slot), c.tmem_cols);
@@ -691,6 +813,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   tc_fence_before();
   __syncthreads();
+  if (S > 1) cluster_arrive();  // this CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
@@ -698,48 +821,55 @@ __global__ void __launch_bounds__(kThreads)
 
   if (warp == 5) {
     if (lane == 0) {
-      int issued = 0, s = 0, ph = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_bar(empty + 8 * s, ph ^ 1, wc)) break;
-        const uint32_t fb = full + 8 * s;
-        const uint32_t a = base + s * stage_bytes, b = a + OPER;
+      int issued = 0;
+      Ring r{0, 0};
+#pragma unroll 1
+      for (int k = kb0 * BK; k < kb1 * BK; k += BK) {
+        if (!wait_bar(empty + 8 * r.s, r.ph ^ 1, wc)) break;
+        const uint32_t fb = full + 8 * r.s;
+        const uint32_t a = base + r.s * stage_bytes, b = a + OPER;
         mbar_arrive_expect_tx(fb, stage_bytes);
-        if (c.d.a_mn) {
-          tma_load_2d(a, &maps.a, fb, m0, kb * BK);
-          tma_load_2d(a + CHUNK, &maps.a, fb, m0 + 64, kb * BK);
+        if constexpr (A_MN) {
+          tma_load_2d(a, &maps.a, fb, m0, k);
+          tma_load_2d(a + CHUNK, &maps.a, fb, m0 + 64, k);
         } else {
-          tma_load_2d(a, &maps.a, fb, kb * BK, m0);
+          tma_load_2d(a, &maps.a, fb, k, m0);
         }
-        if (c.d.b_mn) {
-          for (int j = 0; j * 64 < c.BN; ++j)
-            tma_load_2d(b + j * CHUNK, &maps.b, fb, n0 + 64 * j, kb * BK);
+        if constexpr (B_MN) {
+          for (int j = 0; j * CHUNK < b_bytes; ++j)
+            tma_load_2d(b + j * CHUNK, &maps.b, fb, n0 + 64 * j, k);
         } else {
-          tma_load_2d(b, &maps.b, fb, kb * BK, n0);
+          tma_load_2d(b, &maps.b, fb, k, n0);
         }
         ++issued;
-        if (++s == c.stages) s = 0, ph ^= 1;
+        r.next(stages);
       }
       // the copies land before the block may exit
-      for (int j = std::max(0, issued - c.stages); j < issued; ++j)
-        wait_bar_drain(full + 8 * (j % c.stages), (j / c.stages) & 1, DRAIN_LIMIT);
+      for (int j = std::max(0, issued - stages); j < issued; ++j)
+        wait_bar_drain(full + 8 * (j % stages), (j / stages) & 1, DRAIN_LIMIT);
     }
     __syncwarp();
   } else if (warp == 4) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, c.BN, c.d.a_mn, c.d.b_mn);
-      const uint32_t a_step = c.d.a_mn ? 16 * 128 : 32, b_step = c.d.b_mn ? 16 * 128 : 32;
-      const uint32_t a_lbo = c.d.a_mn ? CHUNK : 16, b_lbo = c.d.b_mn ? CHUNK : 16;
-      int s = 0, ph = 0;
+      const uint32_t idesc = idesc_bf16_f32(128, c.BN, A_MN, B_MN);
+      constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
+      const uint64_t a0 = sw128_desc(base, A_MN ? CHUNK : 16, 1024);
+      const uint64_t b0 = sw128_desc(base + OPER, B_MN ? CHUNK : 16, 1024);
+      const uint32_t adv = stage_bytes >> 4;
+      Ring r{0, 0};
+      uint32_t accumulate = 0;
+#pragma unroll 1
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_bar(full + 8 * s, ph, wc)) break;
+        if (!wait_bar(full + 8 * r.s, r.ph, wc)) break;
         tc_fence_after();
-        const uint32_t a0 = base + s * stage_bytes, b0 = a0 + OPER;
+        const uint64_t ad = a0 + r.s * adv, bd = b0 + r.s * adv;
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          tc_mma_bf16(tmem_base, sw128_desc(a0 + kk * a_step, a_lbo, 1024),
-                      sw128_desc(b0 + kk * b_step, b_lbo, 1024), idesc, kb > kb0 || kk > 0);
-        tc_commit(empty + 8 * s);
-        if (++s == c.stages) s = 0, ph ^= 1;
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          tc_mma_bf16(tmem_base, ad + kk * kA, bd + kk * kB, idesc, accumulate);
+          accumulate = 1;
+        }
+        tc_commit(empty + 8 * r.s);
+        r.next(stages);
       }
       tc_commit(acc_full);
       wait_bar_drain(acc_full, 0, DRAIN_LIMIT);
@@ -748,139 +878,67 @@ __global__ void __launch_bounds__(kThreads)
   }
 
   // ------------------------------------------------ epilogue
-  // thread = tile row (tensor memory lane); 8 columns at a time
-  const int row = m0 + warp * 32 + lane;  // along the tile's rows
-  auto finish = [&](int j0, float(&v)[8]) {
-    // v: columns n0 + j0 .. + 7 of this row, added up over the contraction
-    if (row >= c.Mr) return;
-    const DenseProduct& d = c.d;
-    const int col0 = n0 + j0;
-    if (c.swap) {
-      // output[col, row]: consecutive lanes write consecutive elements
-      const float bv = d.epilogue && p.bias ? load_any(p.bias, p.bias_f32, row) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += bv;
-      if (d.epilogue && p.pre) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col0 + i < c.Nc)
-            static_cast<__nv_bfloat16*>(p.pre)[static_cast<long long>(col0 + i) * d.N + row] =
-                __float2bfloat16_rn(v[i]);
-      }
-      if (d.epilogue) act_all<8>(p.act, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (col0 + i >= c.Nc) continue;
-        if (d.epilogue && p.residual)
-          v[i] += load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row);
-        const long long o = static_cast<long long>(col0 + i) * d.N + row;
-        if (d.out_f32)
-          static_cast<float*>(d.out)[o] = v[i];
-        else
-          static_cast<__nv_bfloat16*>(d.out)[o] = __float2bfloat16_rn(v[i]);
-      }
-      return;
-    }
-    const int nv = std::min(8, c.Nc - col0);
-    if (nv <= 0) return;
-    auto store8 = [&](void* out, bool f32, bool vec) {
-      const long long o = static_cast<long long>(row) * d.N + col0;
-      if (vec && nv == 8) {
-        if (f32) {
-          float4* q = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
-          q[0] = make_float4(v[0], v[1], v[2], v[3]);
-          q[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + o) =
-              make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
-                         pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= nv) continue;
-          if (f32)
-            static_cast<float*>(out)[o + i] = v[i];
-          else
-            static_cast<__nv_bfloat16*>(out)[o + i] = __float2bfloat16_rn(v[i]);
-        }
-      }
-    };
-    if (d.epilogue) {
-      if (p.bias) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < nv) v[i] += load_any(p.bias, p.bias_f32, col0 + i);
-      }
-      if (p.pre) store8(p.pre, false, c.vec_pre);
-      act_all<8>(p.act, v);
-      if (p.residual) {
-        const long long ro = static_cast<long long>(row) * p.ldr + col0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < nv) v[i] += load_any(p.residual, p.res_f32, ro + i);
-      }
-    }
-    store8(d.out, d.out_f32, c.vec_out);
-  };
-
-  bool ok = true;
+  // thread = tile row (tensor memory lane); 4 columns at a time
+  const int tl = warp * 32 + lane;
+  const int row = m0 + tl;
   const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  if (S > 1) cluster_wait();  // every CTA's barriers exist
   if (warp < 4) {
-    ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
+    const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
     tc_fence_after();
     if (S == 1) {
       if (ok)
 #pragma unroll 1
         for (int j = 0; j < c.BN && n0 + j < c.Nc; j += 16) {
-          float v[16], h[8];
+          float v[16];
           tmem_ld16(taddr + j, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] = v[i];
-          finish(j, h);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] = v[8 + i];
-          finish(j + 8, h);
+          for (int i = 0; i < 4; ++i) {
+            float h[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            finish4(c, p, row, n0 + j + 4 * i, h);
+          }
         }
     } else {
-      // the partial tile, column by column (128 consecutive floats each),
-      // over the pipeline's buffers: every MMA that read them is done
+      // Each CTA finishes `per` of the tile's columns: every CTA sends it its
+      // partial sums of them, straight from registers, counted on its barrier
+      // (and goes on: nothing of the sender's is read later).
 #pragma unroll 1
       for (int j = 0; j < c.BN; j += 16) {
         float v[16];
         tmem_ld16(taddr + j, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          st_shared_f32(base + (j + i) * 512 + (warp * 32 + lane) * 4, v[i]);
+        for (int i = 0; i < 4; ++i) {
+          const int col = j + 4 * i;
+          const int owner = col / c.per;
+          const uint32_t dst = recv + (((rank * c.per + col - owner * c.per) >> 2) * 128 + tl) * 16;
+          st_async_v4(mapa_shared(dst, owner), mapa_shared(got, owner), v[4 * i], v[4 * i + 1],
+                      v[4 * i + 2], v[4 * i + 3]);
+        }
       }
     }
   }
   if (S > 1) {
-    cluster_sync_all();
-    if (warp < 4) {
-      // this CTA finishes columns [j0, j1): sums over the ranks in order
-      const int per = (cdiv(c.BN, S) + 7) & ~7;
-      const int j1 = std::min(c.BN, (rank + 1) * per);
+    cluster_arrive();  // this CTA has sent everything
+    if (warp < 4 && own1 > own0) {
+      if (__all_sync(0xffffffffu, wait_bar_cluster(got, 0, wc))) {
 #pragma unroll 1
-      for (int j = rank * per; j < j1 && n0 + j < c.Nc; j += 8) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        for (int q = 0; q < S; ++q) {
-          const uint32_t src = mapa_shared(base + j * 512 + (warp * 32 + lane) * 4, q);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float x;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(src + i * 512) : "memory");
-            v[i] += x;
+        for (int j = own0; j < own1 && n0 + j < c.Nc; j += 4) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t src = recv + (((j - own0) >> 2) * 128 + tl) * 16;
+#pragma unroll 8
+          for (int q = 0; q < S; ++q) {  // in rank order: the same bits every time
+            const float4 x = ld_shared_v4(src + q * c.per * 512);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
           }
+          finish4(c, p, row, n0 + j, v);
         }
-        finish(j, v);
       }
     }
-    cluster_sync_all();  // no CTA leaves while its partial tile is being read
+    // no CTA leaves before the others have sent (on the normal path they
+    // have: what was received here came from all of them)
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -1115,9 +1173,9 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
 }
 
 // Tile columns, orientation and contraction pieces of a product on
-// single-CTA tiles, by estimated time: rounds of clusters x (contraction
-// steps of a piece x cycles per step + the start and end of a tile).  A step
-// costs what its bytes take at the SM's share of the memory rate.
+// single-CTA tiles, by estimated time in SM cycles: rounds of clusters x
+// (contraction steps of a piece x the cycles its bytes take at an SM's share
+// of the L2 rate + the start and end of a tile, which grow with its columns).
 struct CtaPlan {
   bool swap;
   int BN, splits;
@@ -1132,12 +1190,12 @@ CtaPlan plan_cta(const DenseProduct& d) {
     for (int bn : {16, 32, 64, 128, 256}) {
       if (bn > 16 && nc <= bn / 2) break;
       const long long tiles = static_cast<long long>(cdiv(mr, 128)) * cdiv(nc, bn);
-      for (int s = 1; s <= 8 && s <= nkb; s *= 2) {
+      for (int s = 1; s <= 8 && s <= nkb && (s == 1 || bn <= 128); s *= 2) {
         const double steps = static_cast<double>(cdiv(nkb, s));
         const long long rounds = (tiles * s + sms - 1) / sms;
-        const double step = std::max(2.0 * bn, (16384.0 + 128.0 * bn) / 32.0);
-        const double t =
-            static_cast<double>(rounds) * (steps * step + 2500.0 + 8.0 * bn + (s > 1 ? 1500.0 : 0.0));
+        const double step = std::max(2.0 * bn, (16384.0 + 128.0 * bn) / 48.0);
+        const double t = static_cast<double>(rounds) *
+                         (steps * step + 2500.0 + 12.0 * bn + (s > 1 ? 1000.0 + 6.0 * bn : 0.0));
         if (t < best_t) {
           best_t = t;
           best = CtaPlan{swap != 0, bn, s};
@@ -1146,6 +1204,29 @@ CtaPlan plan_cta(const DenseProduct& d) {
     }
   }
   return best;
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t launch_cta_t(const CtaMaps& maps, const CtaParams& c, const DenseParams& p,
+                         cudaStream_t st) {
+  static bool done[64] = {};
+  auto kern = dense_cta_kernel<A_MN, B_MN>;
+  cudaError_t e = allow_smem(kern, 232448, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cdiv(c.Mr, 128) * cdiv(c.Nc, c.BN) * c.splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = cta_smem(c);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = c.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, c, p);
 }
 
 cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const DenseOperand& b,
@@ -1161,37 +1242,27 @@ cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const
   if (plan.swap) std::swap(c.d.a_mn, c.d.b_mn);
   c.BN = plan.BN;
   c.splits = plan.splits;
+  c.per = (cdiv(c.BN, c.splits) + 3) & ~3;
   c.b_bytes = c.d.b_mn ? cdiv(c.BN, 64) * CHUNK : c.BN * 128;
-  const int nkb = cdiv(c.d.Kc, BK);
-  // two blocks on an SM where the stages are small
-  const int room = (c.BN <= 128 ? 100 : 200) * 1024;
-  c.stages = std::max(2, std::min({8, room / (OPER + c.b_bytes), cdiv(nkb, c.splits)}));
+  // two blocks on an SM where the tile is small
+  const int room = (c.BN <= 64 ? 112 : 225) * 1024 - 1024 - kCtaMeta -
+                   (c.splits > 1 ? c.splits * c.per * 512 : 0);
+  c.stages = std::max(2, std::min({8, room / (OPER + c.b_bytes), cdiv(cdiv(c.d.Kc, BK), c.splits)}));
   c.tmem_cols = 32;
   while (c.tmem_cols < c.BN) c.tmem_cols *= 2;
-  c.vec_out = out_by_tma(c.d.out, c.d.N, c.d.out_f32) && c.d.N % 8 == 0;
-  c.vec_pre = p.pre && out_by_tma(p.pre, c.d.N, false);
+  auto vec4 = [](const void* ptr, long long ld, bool f32) {
+    const int bytes = f32 ? 16 : 8;
+    return reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && ld % 4 == 0;
+  };
+  c.vec_out = vec4(c.d.out, c.d.N, c.d.out_f32);
+  c.vec_pre = p.pre && vec4(p.pre, c.d.N, false);
+  c.vec_res = p.residual && vec4(p.residual, p.ldr, p.res_f32);
   CtaMaps maps;
   if (!tmap_operand(&maps.a, ra, c.d.a_mn, 128) || !tmap_operand(&maps.b, rb, c.d.b_mn, c.BN))
     return cudaErrorInvalidValue;
-  const size_t smem = 1024 + std::max(c.stages * (OPER + c.b_bytes), c.splits > 1 ? c.BN * 512 : 0) + 256;
-  static bool done[64] = {};
-  cudaError_t e = allow_smem(dense_cta_kernel, 232448, done);
-  if (e != cudaSuccess) return e;
-  const int tiles = cdiv(c.Mr, 128) * cdiv(c.Nc, c.BN);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * c.splits);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = c.splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = c.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, dense_cta_kernel, maps, c, p);
+  if (c.d.a_mn)
+    return c.d.b_mn ? launch_cta_t<true, true>(maps, c, p, st) : launch_cta_t<true, false>(maps, c, p, st);
+  return c.d.b_mn ? launch_cta_t<false, true>(maps, c, p, st) : launch_cta_t<false, false>(maps, c, p, st);
 }
 
 // Blocks of the dz pass: columns first, then enough row ranges for two blocks
