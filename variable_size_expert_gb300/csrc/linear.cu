@@ -214,6 +214,7 @@ struct PairMaps {
   CUtensorMap a[2], b[2], out[2], pre, res;
 };
 
+constexpr int kGroups = 4;  // release barriers of a ring
 struct PSmem {
   uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, res_full, issued;
   uint32_t* tmem_slot;
@@ -229,7 +230,7 @@ __device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
   m.sEpi = m.sB + STAGES * OPER;
   m.full = m.sEpi + kEpiWarps * EPI_WARP;
   m.empty = m.full + 8 * STAGES;
-  m.acc_full = m.empty + 8 * STAGES;
+  m.acc_full = m.empty + 8 * kGroups;
   m.acc_empty = m.acc_full + 16;
   m.drain = m.acc_empty + 16;
   m.pdone = m.drain + 8;
@@ -276,35 +277,64 @@ __device__ __forceinline__ void load_oper(uint32_t dst, const CUtensorMap* map, 
   }
 }
 
-// Ring position of a pipeline role: stage and the parity its next wait takes.
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
+// The producer's and the MMA warp's loops.  Blocks of the contraction pass
+// through a ring of `stages` slots: full[s] tells that a block has landed, and
+// every 2^lg blocks one commit tells through empty[q % kGroups] that group q of
+// blocks has been read.  The pair kernel's blocks take their MMAs 512 cycles
+// and are released one by one (by twos its ring of five runs short: gradients
+// of 8192 x 2048 x 8192 1650 instead of 1800 TFLOP/s); the handshake of a
+// small single-CTA tile costs more than its MMAs and is shared by 2 or 4.
+// Both loops run with the whole warp converged, one elected lane issuing:
+// inside a divergent branch every operand of an MMA or a copy costs extra
+// moves into uniform registers (15% of a loop of small tiles).
 struct Ring {
-  int s;
+  int it, s;
   uint32_t ph;
   __device__ __forceinline__ void next(int stages) {
+    ++it;
     if (++s == stages) s = 0, ph ^= 1;
   }
 };
+// Producer: the slot of block r.it is free.  (log2 of the group size given.)
+__device__ __forceinline__ bool slot_free(uint32_t empty, const Ring& r, int stages, int lg,
+                                          const WaitCtl& wc) {
+  const int u = r.it - stages;
+  if (u < 0 || (u & ((1 << lg) - 1))) return true;  // never used, or freed with its group
+  const int q = u >> lg;
+  return __all_sync(0xffffffffu, wait_bar(empty + 8 * (q % kGroups), (q / kGroups) & 1, wc));
+}
+// MMA: the barrier to commit to after block `it`, 0 where its group goes on.
+__device__ __forceinline__ uint32_t release_bar(uint32_t empty, int it, int lg) {
+  return ((it + 1) & ((1 << lg) - 1)) ? 0u : empty + 8 * ((it >> lg) % kGroups);
+}
 
-// The producer's and the MMA thread's loops over a tile's contraction.  One
-// thread runs each, an iteration has the 512 cycles of a stage's MMAs, and an
-// instruction costs a lone thread 4 to 6 of them: the layouts are template
-// arguments, the descriptors advance by one addition, and nothing in the loops
-// is read from the parameters.
 template <bool A_MN, bool B_MN>
 __device__ __forceinline__ bool produce(const PSmem& m, const CUtensorMap* ma,
                                         const CUtensorMap* mb, uint32_t full_l, bool leader, int ar,
-                                        int br, int nkb, Ring& r, int& issued, const WaitCtl& wc) {
+                                        int br, int nkb, Ring& r, const WaitCtl& wc) {
 #pragma unroll 1
   for (int k = 0; k < nkb * BK; k += BK) {
-    if (!wait_bar(m.empty + 8 * r.s, r.ph ^ 1, wc)) return false;
-    const uint32_t fb = full_l + 8 * r.s;
-    // the leader announces its bytes first; the peer issues its copies first
-    // (the phase cannot complete before its arrival)
-    if (leader) mbar_arrive_expect_tx(m.full + 8 * r.s, 2 * OPER);
-    load_oper<A_MN>(m.sA + r.s * OPER, ma, fb, ar, k);
-    load_oper<B_MN>(m.sB + r.s * OPER, mb, fb, br, k);
-    if (!leader) mbar_arrive_expect_tx_cluster(fb, 2 * OPER);
-    ++issued;
+    if (!slot_free(m.empty, r, STAGES, 0, wc)) return false;
+    if (elect_one()) {
+      const uint32_t fb = full_l + 8 * r.s;
+      // the leader announces its bytes first; the peer issues its copies first
+      // (the phase cannot complete before its arrival)
+      if (leader) mbar_arrive_expect_tx(m.full + 8 * r.s, 2 * OPER);
+      load_oper<A_MN>(m.sA + r.s * OPER, ma, fb, ar, k);
+      load_oper<B_MN>(m.sB + r.s * OPER, mb, fb, br, k);
+      if (!leader) mbar_arrive_expect_tx_cluster(fb, 2 * OPER);
+    }
     r.next(STAGES);
   }
   return true;
@@ -318,18 +348,18 @@ __device__ __forceinline__ bool multiply(const PSmem& m, uint32_t dt, int nkb, R
   constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
   const uint64_t a0 = sw128_desc(m.sA, A_MN ? CHUNK : 16, 1024);
   const uint64_t b0 = sw128_desc(m.sB, B_MN ? CHUNK : 16, 1024);
-  uint32_t accumulate = 0;
 #pragma unroll 1
   for (int kb = 0; kb < nkb; ++kb) {
-    if (!wait_bar(m.full + 8 * r.s, r.ph, wc)) return false;
+    if (!__all_sync(0xffffffffu, wait_bar(m.full + 8 * r.s, r.ph, wc))) return false;
     tc_fence_after();
     const uint64_t ad = a0 + r.s * (OPER >> 4), bd = b0 + r.s * (OPER >> 4);
+    const uint32_t rel = release_bar(m.empty, r.it, 0);
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      tc_mma_bf16_cg2(dt, ad + kk * kA, bd + kk * kB, kIdesc, accumulate);
-      accumulate = 1;
+      for (int kk = 0; kk < BK / 16; ++kk)
+        tc_mma_bf16_cg2(dt, ad + kk * kA, bd + kk * kB, kIdesc, (kb | kk) != 0);
+      if (rel) tc_commit_cg2_mc(rel, 0x3);
     }
-    tc_commit_cg2_mc(m.empty + 8 * r.s, 0x3);
     r.next(STAGES);
   }
   return true;
@@ -354,10 +384,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s)
       mbar_init(m.full + 8 * s, 2);  // both TMA threads announce their own bytes
-      mbar_init(m.empty + 8 * s, 1);
-    }
+    for (int q = 0; q < kGroups; ++q) mbar_init(m.empty + 8 * q, 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(m.acc_full + 8 * a, 1);
       mbar_init(m.acc_empty + 8 * a, 2 * kEpiWarps);  // the epilogue warps of both CTAs
@@ -384,28 +413,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (warp == 5) {
     // ------------------------------------------------ TMA
+    Ring r{0, 0, 0};
+    bool ok = true;
+    for (int tau = pair; ok && tau < total; tau += npairs) {
+      const PTile t = decode_pair(p, tau);
+      const DenseProduct& d = p.pr[t.q];
+      const int ar = t.m0 + static_cast<int>(rank) * kHalf;
+      const int br = t.n0 + static_cast<int>(rank) * kHalf;
+      const CUtensorMap *ma = &maps.a[t.q], *mb = &maps.b[t.q];
+      // (the three layouts of the forward, dx and dW)
+      if (d.a_mn)
+        ok = produce<true, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
+      else if (d.b_mn)
+        ok = produce<false, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
+      else
+        ok = produce<false, false>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
+    }
+    // Every copy lands before either CTA may exit: the peer reports how
+    // many blocks it issued; for the blocks that one side did not issue
+    // (only after a timeout) the leader makes that side's arrival and
+    // waits for the phase, which completes once the issued copies landed.
     if (lane == 0) {
-      int it = 0;
-      Ring r{0, 0};
-      bool ok = true;
-      for (int tau = pair; ok && tau < total; tau += npairs) {
-        const PTile t = decode_pair(p, tau);
-        const DenseProduct& d = p.pr[t.q];
-        const int ar = t.m0 + static_cast<int>(rank) * kHalf;
-        const int br = t.n0 + static_cast<int>(rank) * kHalf;
-        const CUtensorMap *ma = &maps.a[t.q], *mb = &maps.b[t.q];
-        // (the three layouts of the forward, dx and dW)
-        if (d.a_mn)
-          ok = produce<true, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, it, wc);
-        else if (d.b_mn)
-          ok = produce<false, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, it, wc);
-        else
-          ok = produce<false, false>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, it, wc);
-      }
-      // Every copy lands before either CTA may exit: the peer reports how
-      // many stages it issued; for the stages that one side did not issue
-      // (only after a timeout) the leader makes that side's arrival and
-      // waits for the phase, which completes once the issued copies landed.
+      const int it = r.it;
       if (!leader) {
         st_cluster_s32(mapa_shared(m.issued, 0), it);
         mbar_arrive_cluster(mapa_shared(m.pdone, 0));
@@ -421,17 +450,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
     }
+    __syncwarp();
   } else if (warp == 4) {
     // ------------------------------------------------ MMA issue
-    if (leader && lane == 0) {
+    if (leader) {
       int tcount = 0;
-      Ring r{0, 0};
+      Ring r{0, 0, 0};
       bool ok = true;
       for (int tau = pair; ok && tau < total; tau += npairs) {
         const PTile t = decode_pair(p, tau);
         const DenseProduct& d = p.pr[t.q];
         const int acc = tcount & 1;
-        if (!wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)) break;
+        if (!__all_sync(0xffffffffu, wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)))
+          break;
         tc_fence_after();
         const uint32_t dt = tmem_base + acc * 256;
         if (d.a_mn)
@@ -441,11 +472,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         else
           ok = multiply<false, false>(m, dt, t.nkb, r, wc);
         if (!ok) break;
-        tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
+        if (elect_one()) tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
         ++tcount;
       }
-      tc_commit_cg2(m.drain);
-      wait_bar_drain(m.drain, 0, DRAIN_LIMIT);
+      if (elect_one()) {
+        tc_commit_cg2(m.drain);
+        wait_bar_drain(m.drain, 0, DRAIN_LIMIT);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------ epilogue
@@ -644,12 +678,15 @@ struct CtaParams {
   int BN;          // tile columns (16..256, a multiple of 16)
   int splits;      // CTAs per cluster: pieces of the contraction
   int per;         // columns that each CTA of a cluster finishes (a multiple of 4)
-  int stages;
-  int b_bytes;     // B bytes per stage
+  int stages, lg;  // ring slots, log2 of the blocks per release
+  int b_bytes;     // B bytes per block
+  int nacc;        // accumulators (1, 2 or 4), see the MMA loop
   int tmem_cols;
   int vec_out, vec_pre, vec_res;  // accesses of 4 columns at once
 };
 constexpr int kCtaMeta = 256;
+constexpr int kMaxStages = 12;
+static_assert(8 * (kMaxStages + kGroups + 2) + 8 <= kCtaMeta, "barrier area");
 size_t cta_smem(const CtaParams& c) {
   return 1024 + static_cast<size_t>(c.stages) * (OPER + c.b_bytes) +
          (c.splits > 1 ? static_cast<size_t>(c.splits) * c.per * 512 : 0) + kCtaMeta;
@@ -778,8 +815,9 @@ __global__ void __launch_bounds__(kThreads)
   const int S = c.splits;
   const uint32_t recv = base + stages * stage_bytes;  // partial sums from the cluster
   const uint32_t meta = recv + (S > 1 ? S * c.per * 512 : 0);
-  const uint32_t full = meta, empty = meta + 64, acc_full = meta + 128, got = meta + 136;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (meta + 144 - base));
+  const uint32_t full = meta, empty = meta + 8 * kMaxStages, acc_full = empty + 8 * kGroups,
+                 got = acc_full + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (got + 8 - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -797,10 +835,8 @@ __global__ void __launch_bounds__(kThreads)
   }
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, 1);
-    }
+    for (int s = 0; s < stages; ++s) mbar_init(full + 8 * s, 1);
+    for (int q = 0; q < kGroups; ++q) mbar_init(empty + 8 * q, 1);
     mbar_init(acc_full, 1);
     mbar_init(got, 1);
     *abort_flag = 0;
@@ -820,12 +856,11 @@ __global__ void __launch_bounds__(kThreads)
   const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
 
   if (warp == 5) {
-    if (lane == 0) {
-      int issued = 0;
-      Ring r{0, 0};
+    Ring r{0, 0, 0};
 #pragma unroll 1
-      for (int k = kb0 * BK; k < kb1 * BK; k += BK) {
-        if (!wait_bar(empty + 8 * r.s, r.ph ^ 1, wc)) break;
+    for (int k = kb0 * BK; k < kb1 * BK; k += BK) {
+      if (!slot_free(empty, r, stages, c.lg, wc)) break;
+      if (elect_one()) {
         const uint32_t fb = full + 8 * r.s;
         const uint32_t a = base + r.s * stage_bytes, b = a + OPER;
         mbar_arrive_expect_tx(fb, stage_bytes);
@@ -841,36 +876,42 @@ __global__ void __launch_bounds__(kThreads)
         } else {
           tma_load_2d(b, &maps.b, fb, k, n0);
         }
-        ++issued;
-        r.next(stages);
       }
-      // the copies land before the block may exit
-      for (int j = std::max(0, issued - stages); j < issued; ++j)
-        wait_bar_drain(full + 8 * (j % stages), (j / stages) & 1, DRAIN_LIMIT);
+      r.next(stages);
     }
+    // the copies land before the block may exit
+    for (int j = std::max(0, r.it - stages); j < r.it; ++j)
+      wait_bar_drain(full + 8 * (j % stages), (j / stages) & 1, DRAIN_LIMIT);
     __syncwarp();
   } else if (warp == 4) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, c.BN, A_MN, B_MN);
-      constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
-      const uint64_t a0 = sw128_desc(base, A_MN ? CHUNK : 16, 1024);
-      const uint64_t b0 = sw128_desc(base + OPER, B_MN ? CHUNK : 16, 1024);
-      const uint32_t adv = stage_bytes >> 4;
-      Ring r{0, 0};
-      uint32_t accumulate = 0;
-#pragma unroll 1
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_bar(full + 8 * r.s, r.ph, wc)) break;
-        tc_fence_after();
-        const uint64_t ad = a0 + r.s * adv, bd = b0 + r.s * adv;
+    const uint32_t idesc = idesc_bf16_f32(128, c.BN, A_MN, B_MN);
+    constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
+    const uint64_t a0 = sw128_desc(base, A_MN ? CHUNK : 16, 1024);
+    const uint64_t b0 = sw128_desc(base + OPER, B_MN ? CHUNK : 16, 1024);
+    const uint32_t adv = stage_bytes >> 4;
+    // The four MMAs of a block go to up to four accumulators, which the
+    // epilogue adds up: one that adds onto the accumulator of the one before
+    // it waits for it (6% of 16 x 7168 x 2048 in one piece).
+    const int nacc = c.nacc;
+    uint32_t dt[BK / 16];
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          tc_mma_bf16(tmem_base, ad + kk * kA, bd + kk * kB, idesc, accumulate);
-          accumulate = 1;
-        }
-        tc_commit(empty + 8 * r.s);
-        r.next(stages);
+    for (int kk = 0; kk < BK / 16; ++kk) dt[kk] = tmem_base + (kk & (nacc - 1)) * c.BN;
+    Ring r{0, 0, 0};
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!__all_sync(0xffffffffu, wait_bar(full + 8 * r.s, r.ph, wc))) break;
+      tc_fence_after();
+      const uint64_t ad = a0 + r.s * adv, bd = b0 + r.s * adv;
+      const uint32_t rel = release_bar(empty, r.it, c.lg);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_bf16(dt[kk], ad + kk * kA, bd + kk * kB, idesc, kb > kb0 || kk >= nacc);
+        if (rel) tc_commit(rel);
       }
+      r.next(stages);
+    }
+    if (elect_one()) {
       tc_commit(acc_full);
       wait_bar_drain(acc_full, 0, DRAIN_LIMIT);
     }
@@ -882,6 +923,18 @@ __global__ void __launch_bounds__(kThreads)
   const int tl = warp * 32 + lane;
   const int row = m0 + tl;
   const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  // 16 columns from j, the accumulators added up
+  auto load16 = [&](int j, float(&v)[16]) {
+    tmem_ld16(taddr + j, v);
+    tmem_ld_wait();
+    for (int a = 1; a < c.nacc; ++a) {
+      float x[16];
+      tmem_ld16(taddr + a * c.BN + j, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += x[i];
+    }
+  };
   if (S > 1) cluster_wait();  // every CTA's barriers exist
   if (warp < 4) {
     const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
@@ -891,8 +944,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
         for (int j = 0; j < c.BN && n0 + j < c.Nc; j += 16) {
           float v[16];
-          tmem_ld16(taddr + j, v);
-          tmem_ld_wait();
+          load16(j, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float h[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
@@ -906,8 +958,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
       for (int j = 0; j < c.BN; j += 16) {
         float v[16];
-        tmem_ld16(taddr + j, v);
-        tmem_ld_wait();
+        load16(j, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int col = j + 4 * i;
@@ -1116,11 +1167,6 @@ bool tmap_operand(CUtensorMap* m, const DenseOperand& o, bool mn, int box_rows) 
   return encode_tmap(m, o.ptr, 2, dims, strides, box);
 }
 
-bool use_pairs(const DenseProduct& d) {
-  // enough 256 x 256 tiles to give most pairs one
-  return static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256) * 5 >= 4LL * (num_sms() / 2);
-}
-
 bool out_by_tma(const void* out, int N, bool f32) {
   return aligned16(out) && (static_cast<long long>(N) * (f32 ? 4 : 2)) % 16 == 0;
 }
@@ -1172,17 +1218,23 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
   return launch_pairs_act<kActNone>(maps, p, total, st);
 }
 
-// Tile columns, orientation and contraction pieces of a product on
-// single-CTA tiles, by estimated time in SM cycles: rounds of clusters x
-// (contraction steps of a piece x the cycles its bytes take at an SM's share
-// of the L2 rate + the start and end of a tile, which grow with its columns).
+// The kernel for a product, by estimated time in us: start-up + rounds x
+// contraction blocks x the time of a block, fitted to sweeps of 16 to 4096 x
+// 2048 x 2048 and 16 x 7168 x 2048 (a tile of 128 x BN takes 0.18 us + 1.7 ns
+// per column and block, 1.2 times that with two CTAs on an SM; joining the
+// pieces of a contraction costs 0.4 us + 36 ns per column, storing a tile
+// 0.5 us + 40 ns per column; a 256 x 256 tile on a pair 0.275 us a block and 1.85 us to
+// store).  BN up to 64 leaves room for two CTAs an SM.
+// Clusters of eight CTAs that fill an SM each found too few places (128 x
+// 2048 x 2048: 16 us against 8), so wider tiles split at most four ways, and
+// the widest not at all (its partial sums do not fit beside the ring).
 struct CtaPlan {
   bool swap;
   int BN, splits;
+  double us;
 };
 CtaPlan plan_cta(const DenseProduct& d) {
-  CtaPlan best{false, 16, 1};
-  double best_t = 1e30;
+  CtaPlan best{false, 16, 1, 1e30};
   const int nkb = cdiv(d.Kc, BK);
   const int sms = num_sms();
   for (int swap = 0; swap < 2; ++swap) {
@@ -1190,20 +1242,24 @@ CtaPlan plan_cta(const DenseProduct& d) {
     for (int bn : {16, 32, 64, 128, 256}) {
       if (bn > 16 && nc <= bn / 2) break;
       const long long tiles = static_cast<long long>(cdiv(mr, 128)) * cdiv(nc, bn);
-      for (int s = 1; s <= 8 && s <= nkb && (s == 1 || bn <= 128); s *= 2) {
-        const double steps = static_cast<double>(cdiv(nkb, s));
-        const long long rounds = (tiles * s + sms - 1) / sms;
-        const double step = std::max(2.0 * bn, (16384.0 + 128.0 * bn) / 48.0);
-        const double t = static_cast<double>(rounds) *
-                         (steps * step + 2500.0 + 12.0 * bn + (s > 1 ? 1000.0 + 6.0 * bn : 0.0));
-        if (t < best_t) {
-          best_t = t;
-          best = CtaPlan{swap != 0, bn, s};
-        }
+      const int most = bn <= 64 ? 8 : bn == 128 ? 4 : 1;
+      for (int s = 1; s <= most && s <= nkb; s *= 2) {
+        const long long ctas = tiles * s, slots = bn <= 64 ? 2LL * sms : sms;
+        const double rounds = static_cast<double>((ctas + slots - 1) / slots);
+        const double block = (0.18 + 0.0017 * bn) * (ctas > sms && bn <= 64 ? 1.2 : 1.0);
+        const double us = 2.2 + rounds * (cdiv(nkb, s) * block + 0.5 + 0.04 * bn) +
+                          (s > 1 ? 0.4 + 0.036 * bn : 0.0);
+        if (us < best.us) best = CtaPlan{swap != 0, bn, s, us};
       }
     }
   }
   return best;
+}
+bool use_pairs(const DenseProduct& d) {
+  const long long tiles = static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256);
+  const long long pairs = num_sms() / 2;
+  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * (cdiv(d.Kc, BK) * 0.275 + 1.85);
+  return us <= plan_cta(d).us;
 }
 
 template <bool A_MN, bool B_MN>
@@ -1247,9 +1303,11 @@ cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const
   // two blocks on an SM where the tile is small
   const int room = (c.BN <= 64 ? 112 : 225) * 1024 - 1024 - kCtaMeta -
                    (c.splits > 1 ? c.splits * c.per * 512 : 0);
-  c.stages = std::max(2, std::min({8, room / (OPER + c.b_bytes), cdiv(cdiv(c.d.Kc, BK), c.splits)}));
+  c.stages = std::max(2, std::min({kMaxStages, room / (OPER + c.b_bytes), cdiv(cdiv(c.d.Kc, BK), c.splits)}));
+  c.lg = c.stages >= 8 ? 2 : c.stages >= 4 ? 1 : 0;
+  c.nacc = c.BN <= 64 ? 4 : c.BN <= 128 ? 2 : 1;
   c.tmem_cols = 32;
-  while (c.tmem_cols < c.BN) c.tmem_cols *= 2;
+  while (c.tmem_cols < c.nacc * c.BN) c.tmem_cols *= 2;
   auto vec4 = [](const void* ptr, long long ld, bool f32) {
     const int bytes = f32 ? 16 : 8;
     return reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && ld % 4 == 0;

@@ -43,8 +43,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// VEC consecutive elements as they lie in memory: 16-byte accesses for
-// VEC = 8, single elements for VEC = 1 (odd widths, unaligned rows).
+// VEC consecutive elements as they lie in memory: 8 where both sides are bf16
+// and 4 where one is f32 (16 bytes of the wider), single elements for VEC = 1.
 template <typename T, int VEC>
 struct Raw {
   T v[VEC];
@@ -54,59 +54,67 @@ struct Raw<__nv_bfloat16, 8> {
   uint4 q;
 };
 template <>
-struct Raw<float, 8> {
-  float4 q[2];
+struct Raw<__nv_bfloat16, 4> {
+  uint2 q;
+};
+template <>
+struct Raw<float, 4> {
+  float4 q;
 };
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> load_raw(const T* p) {
   Raw<T, VEC> r;
-  if constexpr (VEC == 1) {
+  if constexpr (VEC == 1)
     r.v[0] = *p;
-  } else if constexpr (sizeof(T) == 2) {
-    r.q = *reinterpret_cast<const uint4*>(p);
-  } else {
-    r.q[0] = reinterpret_cast<const float4*>(p)[0];
-    r.q[1] = reinterpret_cast<const float4*>(p)[1];
-  }
+  else
+    r = *reinterpret_cast<const Raw<T, VEC>*>(p);
   return r;
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void unpack(const Raw<T, VEC>& r, float (&f)[VEC]) {
   if constexpr (VEC == 1) {
     f[0] = to_f<T>(r.v[0]);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint32_t u[4] = {r.q.x, r.q.y, r.q.z, r.q.w};
+  } else if constexpr (sizeof(T) == 4) {
+    f[0] = r.q.x, f[1] = r.q.y, f[2] = r.q.z, f[3] = r.q.w;
+  } else {
+    uint32_t u[VEC / 2];
+    u[0] = r.q.x, u[1] = r.q.y;
+    if constexpr (VEC == 8) u[2] = r.q.z, u[3] = r.q.w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < VEC / 2; ++i) {
       f[2 * i] = __uint_as_float(u[i] << 16);
       f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
-  } else {
-    f[0] = r.q[0].x, f[1] = r.q[0].y, f[2] = r.q[0].z, f[3] = r.q[0].w;
-    f[4] = r.q[1].x, f[5] = r.q[1].y, f[6] = r.q[1].z, f[7] = r.q[1].w;
   }
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void store_f(T* p, const float (&f)[VEC]) {
   if constexpr (VEC == 1) {
     *p = from_f<T>(f[0]);
-  } else if constexpr (sizeof(T) == 2) {
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
+  } else {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]),
                    pack_bf16x2_rn(f[4], f[5]), pack_bf16x2_rn(f[6], f[7]));
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
   }
 }
 // the weight or bias (f32 or bf16), VEC elements from column c
 template <int VEC>
 __device__ __forceinline__ void load_param(const void* w, bool w_f32, int c, float (&f)[VEC]) {
-  if (w_f32)
-    unpack<float, VEC>(load_raw<float, VEC>(static_cast<const float*>(w) + c), f);
-  else
+  if (!w_f32) {
     unpack<__nv_bfloat16, VEC>(
         load_raw<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w) + c), f);
+  } else if constexpr (VEC == 8) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+    const float4 a = q[0], b = q[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    unpack<float, VEC>(load_raw<float, VEC>(static_cast<const float*>(w) + c), f);
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -359,6 +367,178 @@ __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
   }
 }
 
+// The same with the rows to come on their way through shared memory: each
+// thread copies its own pieces of the next rows (cp.async, D rows ahead) into
+// slots that only it reads, so the copies need no barrier and the loads of D
+// rows are in flight whatever the reduction waits for.  The register version
+// above keeps one row in flight: 135 us instead of 68 for 8191 x 7163 bf16.
+//
+// SHIFT: rows that do not start on VEC-element boundaries (odd widths).  Where
+// x, dy and dx share each row's residue m (row t starts m = t K mod VEC
+// elements past a boundary), a thread reads the aligned pieces that cover the
+// row, whose columns start at -m; pieces at the row's ends overlap the rows
+// beside it (never another 16-byte word than the row's own) and their foreign
+// elements are left out.  The residue repeats every VEC / gcd(K, VEC) rows, a
+// divisor of 8: each group takes rows of one residue, so that its threads keep
+// their columns and the column sums stay in registers.
+// Row slots: three of two f32 rows fill the shared memory, four of less.
+template <typename XT, typename YT>
+__host__ __device__ constexpr int pipe_depth() {
+  return sizeof(XT) + sizeof(YT) == 8 ? 3 : 4;
+}
+template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
+__global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
+    norm_bwd_pipe_kernel(const YT* dy, const XT* x, long long ldx, const void* w, bool w_f32,
+                         const float* mean, const float* rstd, int T, int K, XT* dx, float* part,
+                         int period) {
+  constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
+  constexpr int kGroups = kThreads / TPR;
+  constexpr int XB = VEC * sizeof(XT), YB = VEC * sizeof(YT);
+  __shared__ float slots[2][2][kGroups][TPR / 32];
+  extern __shared__ __align__(16) uint8_t ring[];  // [depth][NV]([threads] x, [threads] dy)
+  const int group = threadIdx.x / TPR, tig = threadIdx.x % TPR;
+  constexpr int kRow = kThreads * (XB + YB);  // bytes of one j of one row slot
+  const uint32_t mine_x = smem_u32(ring) + threadIdx.x * XB;
+  const uint32_t mine_y = smem_u32(ring) + kThreads * XB + threadIdx.x * YB;
+  pdl_trigger();
+  pdl_wait();
+  const int gid = blockIdx.x * kGroups + group, gn = gridDim.x * kGroups;
+  // this group's rows: gid mod period, then every gn-th (gn is a multiple of period)
+  const int first = SHIFT ? gid % period + period * (gid / period) : gid;
+  const int step = gn;
+  const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
+  float wv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + tig) * VEC - m;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) wv[j][i] = aw[j][i] = ab[j][i] = 0.f;
+    if constexpr (!SHIFT) {
+      if (c < K) load_param<VEC>(w, w_f32, c, wv[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (c + i >= 0 && c + i < K) {
+          float one[1];
+          load_param<1>(w, w_f32, c + i, one);
+          wv[j][i] = one[0];
+        }
+    }
+  }
+  auto copy = [&](long long t, int slot) {
+    if (t < T) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + tig) * VEC - m;
+        if (c >= K) continue;
+        const uint32_t o = (slot * NV + j) * kRow;
+        const XT* xs = x + t * ldx + c;
+        const YT* ys = dy + t * K + c;
+        if constexpr (XB == 16)
+          cp_async_16_full(mine_x + o, xs);
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(mine_x + o), "l"(xs) : "memory");
+        if constexpr (YB == 16)
+          cp_async_16_full(mine_y + o, ys);
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(mine_y + o), "l"(ys) : "memory");
+      }
+    }
+    cp_async_commit();  // (an empty group past the last row keeps the count)
+  };
+  constexpr int depth = pipe_depth<XT, YT>(), D = depth - 1;  // slots, rows ahead
+  long long t = first;
+#pragma unroll
+  for (int i = 0; i < D; ++i) copy(t + static_cast<long long>(i) * step, i);
+  int slot = 0;
+  for (int par = 0; t < T; t += step, par ^= 1) {
+    copy(t + static_cast<long long>(D) * step, slot + D >= depth ? slot + D - depth : slot + D);
+    const float mu = mean[t], rs = rstd[t];
+    cp_async_wait<D>();
+    float xh[NV][VEC], g[NV][VEC];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + tig) * VEC - m;
+      const uint8_t* at = ring + (slot * NV + j) * kRow;
+      if (c < K) {
+        unpack<XT, VEC>(*reinterpret_cast<const Raw<XT, VEC>*>(at + threadIdx.x * XB), xh[j]);
+        unpack<YT, VEC>(*reinterpret_cast<const Raw<YT, VEC>*>(at + kThreads * XB + threadIdx.x * YB), g[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        if (c >= K || (SHIFT && (c + i < 0 || c + i >= K))) xh[j][i] = g[j][i] = 0.f;
+        else xh[j][i] = (xh[j][i] - mu) * rs;
+        aw[j][i] = fmaf(g[j][i], xh[j][i], aw[j][i]);
+        ab[j][i] += g[j][i];
+        g[j][i] *= wv[j][i];
+        s1 += g[j][i];
+        s2 = fmaf(g[j][i], xh[j][i], s2);
+      }
+    }
+    if (++slot == depth) slot = 0;
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (TPR > 32) {
+      // two sums, one barrier: the slots alternate, so the next row's writes
+      // cannot meet this row's reads
+      if ((tig & 31) == 0) {
+        slots[par][0][group][tig >> 5] = s1;
+        slots[par][1][group][tig >> 5] = s2;
+      }
+      bar_named(1 + group, TPR);
+      s1 = s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / 32; ++i) {
+        s1 += slots[par][0][group][i];
+        s2 += slots[par][1][group][i];
+      }
+    }
+    s1 /= K;
+    s2 /= K;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + tig) * VEC - m;
+      if (c >= K) continue;
+      float o[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] = rs * (g[j][i] - s1 - xh[j][i] * s2);
+      if (!SHIFT || (c >= 0 && c + VEC <= K)) {
+        store_f<XT, VEC>(dx + t * K + c, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (c + i >= 0 && c + i < K) dx[t * K + c + i] = from_f<XT>(o[i]);
+      }
+    }
+  }
+  // the block's partial row: groups added in order, over the ring
+  cp_async_wait<0>();
+  __syncthreads();
+  float* acc = reinterpret_cast<float*>(ring);  // [2][K]
+  float* pw = part + static_cast<long long>(blockIdx.x) * K;
+  float* pb = part + static_cast<long long>(gridDim.x + blockIdx.x) * K;
+  for (int gi = 0; gi < kGroups; ++gi) {
+    if (group == gi) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * TPR + tig) * VEC - m;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          if (c + i < 0 || c + i >= K) continue;
+          acc[c + i] = gi ? acc[c + i] + aw[j][i] : aw[j][i];
+          acc[K + c + i] = gi ? acc[K + c + i] + ab[j][i] : ab[j][i];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < K; c += kThreads) {
+    pw[c] = acc[c];
+    pb[c] = acc[K + c];
+  }
+}
+
 // Rows longer than the registers hold: dx row by row (two passes), and the
 // column sums by blocks of 32 columns over a range of rows each.
 template <typename XT, typename YT>
@@ -431,6 +611,16 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+}  // namespace
+
+cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
+                               bool out_f32, cudaStream_t st) {
+  return launch_pdl(column_sums_kernel, dim3(cdiv(K, 32), out1 ? 2 : 1), dim3(1024), 0, st, part,
+                    nb, K, out0, out1, out_f32);
+}
+
+namespace {
+
 struct FwdArgs {
   const void* x;
   long long ldx;
@@ -458,12 +648,16 @@ cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t st) {
                       static_cast<const XT*>(a.x), a.ldx, a.w, a.b, a.w_f32, a.T, K, a.eps,
                       static_cast<YT*>(a.y), a.mean, a.rstd);
   if (vec) {
-    if (K <= 512) return fwd_t<XT, YT, 8, 32, 2>(a, st);
-    if (K <= 1024) return fwd_t<XT, YT, 8, 32, 4>(a, st);
-    if (K <= 2048) return fwd_t<XT, YT, 8, 128, 2>(a, st);
-    if (K <= 4096) return fwd_t<XT, YT, 8, 256, 2>(a, st);
-    if (K <= 8192) return fwd_t<XT, YT, 8, 512, 2>(a, st);
-    return fwd_t<XT, YT, 8, 1024, 2>(a, st);
+    // a warp per row up to 2048 columns (64 values a lane, no barrier), then
+    // 16 values a thread
+    constexpr int V = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
+    if (K <= 512) return fwd_t<XT, YT, V, 32, 16 / V>(a, st);
+    if (K <= 1024) return fwd_t<XT, YT, V, 32, 32 / V>(a, st);
+    if (K <= 2048 && a.T >= 4 * num_sms()) return fwd_t<XT, YT, V, 32, 64 / V>(a, st);
+    if (K <= 2048) return fwd_t<XT, YT, V, 128, 16 / V>(a, st);
+    if (K <= 4096) return fwd_t<XT, YT, V, 256, 16 / V>(a, st);
+    if (K <= 8192) return fwd_t<XT, YT, V, 512, 16 / V>(a, st);
+    return fwd_t<XT, YT, V, 1024, 16 / V>(a, st);
   }
   if (K <= 512) return fwd_t<XT, YT, 1, 32, 16>(a, st);
   if (K <= 4096) return fwd_t<XT, YT, 1, 256, 16>(a, st);
@@ -482,8 +676,9 @@ struct BwdArgs {
   float* part;
 };
 
-template <typename XT, typename YT, int VEC, int TPR, int NV>
+template <typename XT, typename YT, int TPR>
 cudaError_t bwd_t(const BwdArgs& a, int* nb, cudaStream_t st) {
+  constexpr int VEC = 1, NV = 16;
   constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   *nb = std::min(norm_bwd_blocks(), cdiv(a.T, kGroups));
@@ -493,8 +688,48 @@ cudaError_t bwd_t(const BwdArgs& a, int* nb, cudaStream_t st) {
                     a.mean, a.rstd, a.T, a.K, static_cast<XT*>(a.dx), a.part);
 }
 
+template <typename XT, typename YT, int TPR, bool SHIFT>
+cudaError_t bwd_pipe_t(const BwdArgs& a, int* nb, cudaStream_t st) {
+  constexpr int VEC = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
+  constexpr int NV = 16 / VEC;
+  constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
+  constexpr int kGroups = kThreads / TPR;
+  constexpr size_t kRing = static_cast<size_t>(pipe_depth<XT, YT>()) * NV * kThreads * VEC * (sizeof(XT) + sizeof(YT));
+  int period = 1;
+  if (SHIFT)
+    for (period = VEC; period > 1 && (static_cast<long long>(a.K) * (period / 2)) % VEC == 0;) period /= 2;
+  // a multiple of eight blocks, so that the groups divide by any period
+  *nb = std::max(8, std::min(norm_bwd_blocks(), cdiv(cdiv(a.T, kGroups), 8) * 8));
+  const size_t smem = std::max(kRing, static_cast<size_t>(2) * a.K * 4);
+  static bool done[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  auto kern = norm_bwd_pipe_kernel<XT, YT, VEC, TPR, NV, SHIFT>;
+  if (dev >= 64 || !done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = true;
+  }
+  return launch_pdl(kern, dim3(*nb), dim3(kThreads), smem, st, static_cast<const YT*>(a.dy),
+                    static_cast<const XT*>(a.x), a.ldx, a.w, a.w_f32, a.mean, a.rstd, a.T, a.K,
+                    static_cast<XT*>(a.dx), a.part, period);
+}
+// K: the row's columns, with SHIFT those of the pieces that cover it
+template <typename XT, typename YT, bool SHIFT>
+cudaError_t bwd_pipe(const BwdArgs& a, int* nb, cudaStream_t st) {
+  constexpr int VEC = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
+  const int K = a.K + (SHIFT ? VEC - 1 : 0);
+  if (K <= 512) return bwd_pipe_t<XT, YT, 32, SHIFT>(a, nb, st);
+  if (K <= 1024) return bwd_pipe_t<XT, YT, 64, SHIFT>(a, nb, st);
+  if (K <= 2048) return bwd_pipe_t<XT, YT, 128, SHIFT>(a, nb, st);
+  if (K <= 4096) return bwd_pipe_t<XT, YT, 256, SHIFT>(a, nb, st);
+  return bwd_pipe_t<XT, YT, 512, SHIFT>(a, nb, st);
+}
+
+enum BwdPath { kByElement, kAligned, kShifted };
+
 template <typename XT, typename YT>
-cudaError_t bwd(const BwdArgs& a, bool vec, cudaStream_t st) {
+cudaError_t bwd(const BwdArgs& a, BwdPath path, cudaStream_t st) {
   const int K = a.K;
   int nb = 0;
   cudaError_t e;
@@ -507,18 +742,15 @@ cudaError_t bwd(const BwdArgs& a, bool vec, cudaStream_t st) {
     e = launch_pdl(norm_bwd_long_cols_kernel<XT, YT>, dim3(cdiv(K, 256), nb), dim3(256), 0, st,
                    static_cast<const YT*>(a.dy), static_cast<const XT*>(a.x), a.ldx, a.mean,
                    a.rstd, a.T, K, a.part);
-  } else if (vec) {
-    if (K <= 512) e = bwd_t<XT, YT, 8, 32, 2>(a, &nb, st);
-    else if (K <= 1024) e = bwd_t<XT, YT, 8, 64, 2>(a, &nb, st);
-    else if (K <= 2048) e = bwd_t<XT, YT, 8, 128, 2>(a, &nb, st);
-    else if (K <= 4096) e = bwd_t<XT, YT, 8, 256, 2>(a, &nb, st);
-    else if (K <= 8192) e = bwd_t<XT, YT, 8, 512, 2>(a, &nb, st);
-    else e = bwd_t<XT, YT, 8, 1024, 2>(a, &nb, st);
+  } else if (path == kAligned && K <= 8192) {
+    e = bwd_pipe<XT, YT, false>(a, &nb, st);
+  } else if (path == kShifted && K <= 8192 - 7) {
+    e = bwd_pipe<XT, YT, true>(a, &nb, st);
   } else {
-    if (K <= 512) e = bwd_t<XT, YT, 1, 32, 16>(a, &nb, st);
-    else if (K <= 2048) e = bwd_t<XT, YT, 1, 128, 16>(a, &nb, st);
-    else if (K <= 8192) e = bwd_t<XT, YT, 1, 512, 16>(a, &nb, st);
-    else e = bwd_t<XT, YT, 1, 1024, 16>(a, &nb, st);
+    if (K <= 512) e = bwd_t<XT, YT, 32>(a, &nb, st);
+    else if (K <= 2048) e = bwd_t<XT, YT, 128>(a, &nb, st);
+    else if (K <= 8192) e = bwd_t<XT, YT, 512>(a, &nb, st);
+    else e = bwd_t<XT, YT, 1024>(a, &nb, st);
   }
   if (e != cudaSuccess) return e;
   return launch_column_sums(a.part, nb, K, a.dw, a.db, a.w_f32, st);
@@ -528,13 +760,8 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 }  // namespace
 
-cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
-                               bool out_f32, cudaStream_t st) {
-  return launch_pdl(column_sums_kernel, dim3(cdiv(K, 32), out1 ? 2 : 1), dim3(1024), 0, st, part,
-                    nb, K, out0, out1, out_f32);
-}
 
-int norm_bwd_blocks() { return num_sms(); }
+int norm_bwd_blocks() { return std::max(8, num_sms() / 8 * 8); }
 
 // 16-byte accesses where every row of every operand starts on a 16-byte
 // boundary, else element by element.
@@ -552,12 +779,16 @@ cudaError_t launch_norm_fwd(const void* x, bool x_f32, long long ldx, const void
 cudaError_t launch_norm_bwd(const void* dy, bool y_f32, const void* x, bool x_f32, long long ldx,
                             const void* w, bool w_f32, const float* mean, const float* rstd, int T,
                             int K, void* dx, void* dw, void* db, float* part, cudaStream_t st) {
-  const bool vec = K % 8 == 0 && ldx % 8 == 0 && aligned16(x) && aligned16(w) && aligned16(dy) &&
-                   aligned16(dx);
+  const int vec = x_f32 || y_f32 ? 4 : 8;
+  BwdPath path = kByElement;
+  if (aligned16(x) && aligned16(dy) && aligned16(dx)) {
+    if (K % vec == 0 && ldx % vec == 0 && aligned16(w)) path = kAligned;
+    else if (ldx % vec == K % vec) path = kShifted;
+  }
   const BwdArgs a{dy, x, ldx, w, w_f32, mean, rstd, T, K, dx, dw, db, part};
   using B = __nv_bfloat16;
-  if (x_f32) return y_f32 ? bwd<float, float>(a, vec, st) : bwd<float, B>(a, vec, st);
-  return y_f32 ? bwd<B, float>(a, vec, st) : bwd<B, B>(a, vec, st);
+  if (x_f32) return y_f32 ? bwd<float, float>(a, path, st) : bwd<float, B>(a, path, st);
+  return y_f32 ? bwd<B, float>(a, path, st) : bwd<B, B>(a, path, st);
 }
 
 }  // namespace mgg
