@@ -77,31 +77,6 @@ __device__ __forceinline__ float rcp_f(float v) {
 __device__ __forceinline__ float sigmoid_f(float z) {
   return rcp_f(1.f + exp2_f(z * -1.4426950408889634f));
 }
-// Two f32 values in one register pair: the FMA pipe takes both in one
-// instruction.
-struct F2 {
-  uint64_t u;
-};
-__device__ __forceinline__ F2 pack2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.u) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(F2 a, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.u));
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
-  return r;
-}
-__device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
-
 // Phi(z) = (1 + erf(z / sqrt 2)) / 2 with Abramowitz & Stegun 7.1.26,
 //   erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0,
 // absolute error at most 1.5e-7; here x = |z| / sqrt 2, with the 1 / sqrt 2
@@ -553,10 +528,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           st_shared_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4),
-                       __uint_as_float(pack_bf16x2_rn(v[8 * c], v[8 * c + 1])),
-                       __uint_as_float(pack_bf16x2_rn(v[8 * c + 2], v[8 * c + 3])),
-                       __uint_as_float(pack_bf16x2_rn(v[8 * c + 4], v[8 * c + 5])),
-                       __uint_as_float(pack_bf16x2_rn(v[8 * c + 6], v[8 * c + 7])));
+                       __uint_as_float(cvt_bf16x2(v[8 * c], v[8 * c + 1])),
+                       __uint_as_float(cvt_bf16x2(v[8 * c + 2], v[8 * c + 3])),
+                       __uint_as_float(cvt_bf16x2(v[8 * c + 4], v[8 * c + 5])),
+                       __uint_as_float(cvt_bf16x2(v[8 * c + 6], v[8 * c + 7])));
       };
       // a staged block to columns c0.. of rows row0..
       auto flush = [&](uint32_t buf, const CUtensorMap* map, bool tma, void* base, bool f32, int c0) {
@@ -760,7 +735,7 @@ __device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p
         *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(v[0], v[1], v[2], v[3]);
       else
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
-            make_uint2(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]));
+            make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -1101,8 +1076,8 @@ __global__ void __launch_bounds__(256, 4) dense_dz_kernel(const DzArgs a) {
             *o = __float2bfloat16_rn(v[0]);
           else
             *reinterpret_cast<uint4*>(o) =
-                make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
-                           pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+                make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                           cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
         }
       }
     }

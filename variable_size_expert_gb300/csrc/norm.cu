@@ -95,11 +95,39 @@ __device__ __forceinline__ void store_f(T* p, const float (&f)[VEC]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   } else if constexpr (VEC == 4) {
     *reinterpret_cast<uint2*>(p) =
-        make_uint2(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]));
+        make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
   } else {
     *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]),
-                   pack_bf16x2_rn(f[4], f[5]), pack_bf16x2_rn(f[6], f[7]));
+        make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
+                   cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
+  }
+}
+// the same as packed pairs
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack2v(const Raw<T, VEC>& r, F2 (&f)[VEC / 2]) {
+  float v[VEC];
+  unpack<T, VEC>(r, v);
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) f[i] = pack2(v[2 * i], v[2 * i + 1]);
+}
+// keeps the elements i of a piece with lo <= i < hi, zeroes the others
+template <typename T, int VEC>
+__device__ __forceinline__ void keep_range(Raw<T, VEC>& r, int lo, int hi) {
+  if constexpr (sizeof(T) == 4) {
+    r.q.x = 0 >= lo && 0 < hi ? r.q.x : 0.f;
+    r.q.y = 1 >= lo && 1 < hi ? r.q.y : 0.f;
+    r.q.z = 2 >= lo && 2 < hi ? r.q.z : 0.f;
+    r.q.w = 3 >= lo && 3 < hi ? r.q.w : 0.f;
+  } else {
+    auto word = [&](int i) {
+      return (i >= lo && i < hi ? 0x0000ffffu : 0u) | (i + 1 >= lo && i + 1 < hi ? 0xffff0000u : 0u);
+    };
+    r.q.x &= word(0);
+    r.q.y &= word(2);
+    if constexpr (VEC == 8) {
+      r.q.z &= word(4);
+      r.q.w &= word(6);
+    }
   }
 }
 // the weight or bias (f32 or bf16), VEC elements from column c
@@ -123,18 +151,29 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the TPR threads of a row group (TPR a multiple of 32); the result
-// in every thread.  `slots` holds TPR/32 values per call site and parity.
+// Sum over the TPR threads of a row group (TPR a power of two); the result in
+// every thread.  `slots` holds TPR/32 values per call site and parity; every
+// warp adds them up with one read per lane.
 template <int TPR>
 __device__ __forceinline__ float group_sum(float v, float* slots, int group, int tig) {
   v = warp_sum(v);
   if constexpr (TPR > 32) {
+    constexpr int NW = TPR / 32;
     if ((tig & 31) == 0) slots[tig >> 5] = v;
     bar_named(1 + group, TPR);
-    v = 0.f;
+    v = slots[tig & (NW - 1)];
 #pragma unroll
-    for (int w = 0; w < TPR / 32; ++w) v += slots[w];
+    for (int o = NW / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
+  return v;
+}
+// Two sums over a warp in five shuffles: lanes 0-15 get a's, 16-31 b's.
+__device__ __forceinline__ float warp_sum2(float a, float b) {
+  const bool hi = threadIdx.x & 16;
+  float v = hi ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -367,150 +406,212 @@ __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
   }
 }
 
-// The same with the rows to come on their way through shared memory: each
-// thread copies its own pieces of the next rows (cp.async, D rows ahead) into
-// slots that only it reads, so the copies need no barrier and the loads of D
-// rows are in flight whatever the reduction waits for.  The register version
-// above keeps one row in flight: 135 us instead of 68 for 8191 x 7163 bf16.
+// ---------------------------------------------------------------- rows through shared memory
+// The persistent kernels below keep the next rows on their way through shared
+// memory: each thread copies its own pieces (cp.async) into slots that only it
+// reads, so the copies need no barrier and several rows are in flight whatever
+// the reductions wait for.
 //
 // SHIFT: rows that do not start on VEC-element boundaries (odd widths).  Where
-// x, dy and dx share each row's residue m (row t starts m = t K mod VEC
-// elements past a boundary), a thread reads the aligned pieces that cover the
+// all matrices share each row's residue m (row t starts m = t K mod VEC
+// elements past a boundary), a thread takes the aligned pieces that cover the
 // row, whose columns start at -m; pieces at the row's ends overlap the rows
 // beside it (never another 16-byte word than the row's own) and their foreign
-// elements are left out.  The residue repeats every VEC / gcd(K, VEC) rows, a
-// divisor of 8: each group takes rows of one residue, so that its threads keep
-// their columns and the column sums stay in registers.
-// Row slots: three of two f32 rows fill the shared memory, four of less.
-template <typename XT, typename YT>
-__host__ __device__ constexpr int pipe_depth() {
-  return sizeof(XT) + sizeof(YT) == 8 ? 3 : 4;
+// elements are zeroed on reading.  The residue repeats every VEC / gcd(K, VEC)
+// rows, a divisor of 8: each group takes rows of one residue, so that its
+// threads keep their columns, the weights of them in registers.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_piece(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    cp_async_16_full(dst, src);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
-__global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
-    norm_bwd_pipe_kernel(const YT* dy, const XT* x, long long ldx, const void* w, bool w_f32,
-                         const float* mean, const float* rstd, int T, int K, XT* dx, float* part,
-                         int period) {
-  constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
-  constexpr int kGroups = kThreads / TPR;
-  constexpr int XB = VEC * sizeof(XT), YB = VEC * sizeof(YT);
-  __shared__ float slots[2][2][kGroups][TPR / 32];
-  extern __shared__ __align__(16) uint8_t ring[];  // [depth][NV]([threads] x, [threads] dy)
-  const int group = threadIdx.x / TPR, tig = threadIdx.x % TPR;
-  constexpr int kRow = kThreads * (XB + YB);  // bytes of one j of one row slot
-  const uint32_t mine_x = smem_u32(ring) + threadIdx.x * XB;
-  const uint32_t mine_y = smem_u32(ring) + kThreads * XB + threadIdx.x * YB;
-  pdl_trigger();
-  pdl_wait();
-  const int gid = blockIdx.x * kGroups + group, gn = gridDim.x * kGroups;
-  // this group's rows: gid mod period, then every gn-th (gn is a multiple of period)
-  const int first = SHIFT ? gid % period + period * (gid / period) : gid;
-  const int step = gn;
-  const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
-  float wv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+
+// weights (or biases) of this thread's columns, zero outside the row
+template <int VEC, int TPR, int NV, bool SHIFT>
+__device__ __forceinline__ void load_columns(const void* w, bool w_f32, int tig, int m, int K,
+                                             F2 (&out)[NV][VEC / 2]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = (j * TPR + tig) * VEC - m;
+    float v[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) wv[j][i] = aw[j][i] = ab[j][i] = 0.f;
-    if constexpr (!SHIFT) {
-      if (c < K) load_param<VEC>(w, w_f32, c, wv[j]);
+    for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+    if (!SHIFT) {
+      if (c < K) load_param<VEC>(w, w_f32, c, v);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         if (c + i >= 0 && c + i < K) {
           float one[1];
           load_param<1>(w, w_f32, c + i, one);
-          wv[j][i] = one[0];
+          v[i] = one[0];
         }
     }
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) out[j][i] = pack2(v[2 * i], v[2 * i + 1]);
   }
-  auto copy = [&](long long t, int slot) {
-    if (t < T) {
+}
+
+// store a piece of a row, whole or (at the ends of a shifted row) by element
+template <typename T, int VEC, bool SHIFT>
+__device__ __forceinline__ void store_piece(T* at, int c, int K, const F2 (&v)[VEC / 2]) {
+  float o[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) unpack2(v[i], o[2 * i], o[2 * i + 1]);
+  if (!SHIFT || (c >= 0 && c + VEC <= K)) {
+    store_f<T, VEC>(at, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (c + i >= 0 && c + i < K) at[i] = from_f<T>(o[i]);
+  }
+}
+
+// Backward.  The sums of row i + 1 are formed before row i is finished, from
+// the row's slot both times: one barrier per row, with a whole row of other
+// work between a sum's parts and its use.  Packed f32 arithmetic.
+// Row slots: three of two f32 rows fill the shared memory, four of less.
+template <typename XT, typename YT>
+__host__ __device__ constexpr int pipe_depth() {
+  return sizeof(XT) + sizeof(YT) == 8 ? 3 : 4;
+}
+template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
+__global__ void __launch_bounds__(kBwdThreads)
+    norm_bwd_pipe_kernel(const YT* dy, const XT* x, long long ldx, const void* w, bool w_f32,
+                         const float* mean, const float* rstd, int T, int K, XT* dx, float* part,
+                         int period) {
+  constexpr int kThreads = kBwdThreads;
+  constexpr int kGroups = kThreads / TPR;
+  constexpr int XB = VEC * sizeof(XT), YB = VEC * sizeof(YT), H = VEC / 2;
+  constexpr int NW = TPR / 32;
+  __shared__ float slots[2][kGroups][2][NW];
+  extern __shared__ __align__(16) uint8_t ring[];  // [depth][NV]([threads] x, [threads] dy)
+  const int group = threadIdx.x / TPR, tig = threadIdx.x % TPR;
+  constexpr int kRow = kThreads * (XB + YB);  // bytes of one j of one row slot
+  uint8_t* mine_x = ring + threadIdx.x * XB;
+  uint8_t* mine_y = ring + kThreads * XB + threadIdx.x * YB;
+  pdl_trigger();
+  pdl_wait();
+  const int gid = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
+  // this group's rows: gid mod period, then every step-th (a multiple of period)
+  const int first = SHIFT ? gid % period + period * (gid / period) : gid;
+  const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
+  const int rows = first < T ? (T - 1 - first) / step + 1 : 0;
+  const int c0 = tig * VEC - m;      // column of the first piece; piece j: + j * kStride
+  constexpr int kStride = TPR * VEC;
+  F2 wv[NV][H], aw[NV][H], ab[NV][H];
+  load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < H; ++i) aw[j][i] = ab[j][i] = both(0.f);
+  // pointers that advance by a row of this group
+  const XT* xs = x + first * ldx + c0;
+  const YT* ys = dy + static_cast<long long>(first) * K + c0;
+  XT* out = dx + static_cast<long long>(first) * K + c0;
+  const long long sx = step * ldx, sk = static_cast<long long>(step) * K;
+  auto copy = [&](int i, int slot) {  // row i of this group, the rows in order
+    if (i < rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + tig) * VEC - m;
-        if (c >= K) continue;
-        const uint32_t o = (slot * NV + j) * kRow;
-        const XT* xs = x + t * ldx + c;
-        const YT* ys = dy + t * K + c;
-        if constexpr (XB == 16)
-          cp_async_16_full(mine_x + o, xs);
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(mine_x + o), "l"(xs) : "memory");
-        if constexpr (YB == 16)
-          cp_async_16_full(mine_y + o, ys);
-        else
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(mine_y + o), "l"(ys) : "memory");
+        if (c0 + j * kStride >= K) continue;
+        const int o = slot * (NV * kRow) + j * kRow;
+        cp_async_piece<XB>(smem_u32(mine_x + o), xs + j * kStride);
+        cp_async_piece<YB>(smem_u32(mine_y + o), ys + j * kStride);
       }
+      xs += sx;
+      ys += sk;
     }
     cp_async_commit();  // (an empty group past the last row keeps the count)
   };
+  // xh and dy of piece j of a landed row
+  auto fetch = [&](int slot, int j, F2 nmu, F2 rs, F2 (&xh)[H], F2 (&gy)[H]) {
+    const int c = c0 + j * kStride;
+    const int o = slot * (NV * kRow) + j * kRow;
+    Raw<XT, VEC> rx = *reinterpret_cast<const Raw<XT, VEC>*>(mine_x + o);
+    Raw<YT, VEC> ry = *reinterpret_cast<const Raw<YT, VEC>*>(mine_y + o);
+    if (SHIFT && (c < 0 || c + VEC > K)) {
+      keep_range<XT, VEC>(rx, -c, K - c);
+      keep_range<YT, VEC>(ry, -c, K - c);
+    }
+    unpack2v<XT, VEC>(rx, xh);
+    unpack2v<YT, VEC>(ry, gy);
+#pragma unroll
+    for (int i = 0; i < H; ++i) xh[i] = mul2(add2(xh[i], nmu), rs);
+  };
   constexpr int depth = pipe_depth<XT, YT>(), D = depth - 1;  // slots, rows ahead
-  long long t = first;
 #pragma unroll
-  for (int i = 0; i < D; ++i) copy(t + static_cast<long long>(i) * step, i);
-  int slot = 0;
-  for (int par = 0; t < T; t += step, par ^= 1) {
-    copy(t + static_cast<long long>(D) * step, slot + D >= depth ? slot + D - depth : slot + D);
-    const float mu = mean[t], rs = rstd[t];
-    cp_async_wait<D>();
-    float xh[NV][VEC], g[NV][VEC];
-    float s1 = 0.f, s2 = 0.f;
+  for (int i = 0; i < D; ++i) copy(i, i);
+  // the sums of a landed row: into slots[par], or (a warp per row) returned
+  const float inv_k = 1.f / K;
+  auto sums = [&](int slot, float mu, float rs, int par) -> float {
+    F2 s1 = both(0.f), s2 = both(0.f);
+    const F2 nmu = both(-mu), rs2 = both(rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + tig) * VEC - m;
-      const uint8_t* at = ring + (slot * NV + j) * kRow;
-      if (c < K) {
-        unpack<XT, VEC>(*reinterpret_cast<const Raw<XT, VEC>*>(at + threadIdx.x * XB), xh[j]);
-        unpack<YT, VEC>(*reinterpret_cast<const Raw<YT, VEC>*>(at + kThreads * XB + threadIdx.x * YB), g[j]);
-      }
+      if (c0 + j * kStride >= K) continue;
+      F2 xh[H], g[H];
+      fetch(slot, j, nmu, rs2, xh, g);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (c >= K || (SHIFT && (c + i < 0 || c + i >= K))) xh[j][i] = g[j][i] = 0.f;
-        else xh[j][i] = (xh[j][i] - mu) * rs;
-        aw[j][i] = fmaf(g[j][i], xh[j][i], aw[j][i]);
-        ab[j][i] += g[j][i];
-        g[j][i] *= wv[j][i];
-        s1 += g[j][i];
-        s2 = fmaf(g[j][i], xh[j][i], s2);
+      for (int i = 0; i < H; ++i) {
+        aw[j][i] = fma2(g[i], xh[i], aw[j][i]);
+        ab[j][i] = add2(ab[j][i], g[i]);
+        g[i] = mul2(g[i], wv[j][i]);
+        s1 = add2(s1, g[i]);
+        s2 = fma2(g[i], xh[i], s2);
       }
     }
-    if (++slot == depth) slot = 0;
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    float a, b, c, d;
+    unpack2(s1, a, b);
+    unpack2(s2, c, d);
+    a = warp_sum2(a + b, c + d);
+    if (TPR > 32 && (tig & 15) == 0) slots[par][group][(tig >> 4) & 1][tig >> 5] = a;
+    return a;
+  };
+  const float *pm = mean + first, *pr = rstd + first;
+  float mu = 0.f, rs = 0.f, held = 0.f;
+  int slot = 0, ahead = D, par = 0;
+  if (rows > 0) {
+    mu = *pm, rs = *pr;
+    cp_async_wait<D - 1>();
+    held = sums(0, mu, rs, 0);
+  }
+#pragma unroll 1
+  for (int r = 0; r < rows; ++r, par ^= 1) {
+    const bool more = r + 1 < rows;
+    pm += step, pr += step;
+    const float mu1 = more ? *pm : 0.f, rs1 = more ? *pr : 0.f;
+    float v = held;
     if constexpr (TPR > 32) {
-      // two sums, one barrier: the slots alternate, so the next row's writes
-      // cannot meet this row's reads
-      if ((tig & 31) == 0) {
-        slots[par][0][group][tig >> 5] = s1;
-        slots[par][1][group][tig >> 5] = s2;
-      }
-      bar_named(1 + group, TPR);
-      s1 = s2 = 0.f;
+      bar_named(1 + group, TPR);  // the parts of this row's sums are there
+      v = slots[par][group][(tig >> 4) & 1][tig & (NW - 1)];
 #pragma unroll
-      for (int i = 0; i < TPR / 32; ++i) {
-        s1 += slots[par][0][group][i];
-        s2 += slots[par][1][group][i];
-      }
+      for (int o = NW / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
-    s1 /= K;
-    s2 /= K;
+    const float s1 = __shfl_sync(0xffffffffu, v, 0), s2 = __shfl_sync(0xffffffffu, v, 16);
+    const int next = slot + 1 == depth ? 0 : slot + 1;
+    // the next row's sums, then this row's gradient
+    copy(r + D, ahead);
+    if (++ahead == depth) ahead = 0;
+    cp_async_wait<D - 1>();  // the next row has landed
+    if (more) held = sums(next, mu1, rs1, par ^ 1);
+    const F2 n1 = both(-s1 * inv_k), n2 = both(-s2 * inv_k), nmu = both(-mu), rs2 = both(rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + tig) * VEC - m;
+      const int c = c0 + j * kStride;
       if (c >= K) continue;
-      float o[VEC];
+      F2 xh[H], g[H];
+      fetch(slot, j, nmu, rs2, xh, g);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) o[i] = rs * (g[j][i] - s1 - xh[j][i] * s2);
-      if (!SHIFT || (c >= 0 && c + VEC <= K)) {
-        store_f<XT, VEC>(dx + t * K + c, o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (c + i >= 0 && c + i < K) dx[t * K + c + i] = from_f<XT>(o[i]);
-      }
+      for (int i = 0; i < H; ++i)
+        g[i] = mul2(rs2, fma2(xh[i], n2, fma2(g[i], wv[j][i], n1)));
+      store_piece<XT, VEC, SHIFT>(out + j * kStride, c, K, g);
     }
+    out += sk;
+    mu = mu1, rs = rs1;
+    slot = next;
   }
   // the block's partial row: groups added in order, over the ring
   cp_async_wait<0>();
@@ -526,8 +627,12 @@ __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           if (c + i < 0 || c + i >= K) continue;
-          acc[c + i] = gi ? acc[c + i] + aw[j][i] : aw[j][i];
-          acc[K + c + i] = gi ? acc[K + c + i] + ab[j][i] : ab[j][i];
+          float w0, w1, b0, b1;
+          unpack2(aw[j][i / 2], w0, w1);
+          unpack2(ab[j][i / 2], b0, b1);
+          const float vw = i & 1 ? w1 : w0, vb = i & 1 ? b1 : b0;
+          acc[c + i] = gi ? acc[c + i] + vw : vw;
+          acc[K + c + i] = gi ? acc[K + c + i] + vb : vb;
         }
       }
     }
@@ -537,6 +642,123 @@ __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
     pw[c] = acc[c];
     pb[c] = acc[K + c];
   }
+}
+
+// Forward, for many rows: six row slots (32 KB each in f32), weights and
+// biases of a thread's 16 columns in registers; a row leaves its slot for
+// registers before its first reduction.
+constexpr int kFwdDepth = 6;
+template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
+__global__ void __launch_bounds__(kBwdThreads)
+    norm_fwd_pipe_kernel(const XT* x, long long ldx, const void* w, const void* b, bool w_f32,
+                         int T, int K, float eps, YT* y, float* mean_out, float* rstd_out,
+                         int period) {
+  constexpr int kThreads = kBwdThreads;
+  constexpr int kGroups = kThreads / TPR;
+  constexpr int XB = VEC * sizeof(XT), H = VEC / 2;
+  constexpr int depth = kFwdDepth, D = depth - 1;
+  __shared__ float slots[4][kGroups][TPR / 32];
+  extern __shared__ __align__(16) uint8_t ring[];  // [depth][NV][threads]
+  const int group = threadIdx.x / TPR, tig = threadIdx.x % TPR;
+  uint8_t* mine = ring + threadIdx.x * XB;
+  pdl_trigger();
+  pdl_wait();
+  const int gid = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
+  const int first = SHIFT ? gid % period + period * (gid / period) : gid;
+  const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
+  F2 wv[NV][H], bv[NV][H];
+  load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
+  if (b) {
+    load_columns<VEC, TPR, NV, SHIFT>(b, w_f32, tig, m, K, bv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < H; ++i) bv[j][i] = both(0.f);
+  }
+  const float inv_k = 1.f / K;
+  const int rows = first < T ? (T - 1 - first) / step + 1 : 0;
+  const int c0 = tig * VEC - m;
+  constexpr int kStride = TPR * VEC, kPiece = kThreads * XB;
+  const XT* xs = x + first * ldx + c0;
+  YT* out = y + static_cast<long long>(first) * K + c0;
+  const long long sx = step * ldx, sk = static_cast<long long>(step) * K;
+  auto copy = [&](int i, int slot) {
+    if (i < rows) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (c0 + j * kStride < K)
+          cp_async_piece<XB>(smem_u32(mine + slot * (NV * kPiece) + j * kPiece), xs + j * kStride);
+      xs += sx;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) copy(i, i);
+  float *pm = mean_out + first, *pr = rstd_out + first;
+  int slot = 0, ahead = D;
+#pragma unroll 1
+  for (int row = 0, par = 0; row < rows; ++row, par ^= 2) {
+    copy(row + D, ahead);
+    if (++ahead == depth) ahead = 0;
+    cp_async_wait<D>();
+    F2 f[NV][H];
+    F2 s = both(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = c0 + j * kStride;
+      if (c >= K) continue;
+      Raw<XT, VEC> r = *reinterpret_cast<const Raw<XT, VEC>*>(mine + slot * (NV * kPiece) + j * kPiece);
+      if (SHIFT && (c < 0 || c + VEC > K)) keep_range<XT, VEC>(r, -c, K - c);
+      unpack2v<XT, VEC>(r, f[j]);
+#pragma unroll
+      for (int i = 0; i < H; ++i) s = add2(s, f[j][i]);
+    }
+    if (++slot == depth) slot = 0;
+    float lo, hi;
+    unpack2(s, lo, hi);
+    // (the slots of even and odd rows alternate: a row's writes cannot meet
+    // the reads of the row before)
+    const float mean = group_sum<TPR>(lo + hi, slots[par][group], group, tig) * inv_k;
+    const F2 nm = both(-mean);
+    F2 q = both(0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = c0 + j * kStride;
+      if (c >= K) continue;
+      const bool edge = SHIFT && (c < 0 || c + VEC > K);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        f[j][i] = add2(f[j][i], nm);
+        if (edge) {  // outside the row: no part in the variance
+          float a, d;
+          unpack2(f[j][i], a, d);
+          f[j][i] = pack2(c + 2 * i >= 0 && c + 2 * i < K ? a : 0.f,
+                          c + 2 * i + 1 >= 0 && c + 2 * i + 1 < K ? d : 0.f);
+        }
+        q = fma2(f[j][i], f[j][i], q);
+      }
+    }
+    unpack2(q, lo, hi);
+    const float rstd = 1.f / sqrtf(group_sum<TPR>(lo + hi, slots[par + 1][group], group, tig) * inv_k + eps);
+    if (tig == 0) {
+      *pm = mean;
+      *pr = rstd;
+    }
+    pm += step, pr += step;
+    const F2 rs = both(rstd);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = c0 + j * kStride;
+      if (c >= K) continue;
+      F2 o[H];
+#pragma unroll
+      for (int i = 0; i < H; ++i) o[i] = fma2(mul2(f[j][i], rs), wv[j][i], bv[j][i]);
+      store_piece<YT, VEC, SHIFT>(out + j * kStride, c, K, o);
+    }
+    out += sk;
+  }
+  cp_async_wait<0>();
 }
 
 // Rows longer than the registers hold: dx row by row (two passes), and the
@@ -640,20 +862,66 @@ cudaError_t fwd_t(const FwdArgs& a, cudaStream_t st) {
                     a.T, a.K, a.eps, static_cast<YT*>(a.y), a.mean, a.rstd);
 }
 
+// How the rows lie: element by element, all on piece boundaries, or all with
+// the same residue per row.
+enum RowPath { kByElement, kAligned, kShifted };
+
+// Rows between repeats of the residue: VEC / gcd(K, VEC).
+int residue_period(int K, int vec) {
+  int p = vec;
+  while (p > 1 && (static_cast<long long>(K) * (p / 2)) % vec == 0) p /= 2;
+  return p;
+}
+
+template <typename K>
+cudaError_t allow_ring(K kern, bool* done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && done[dev]) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <typename XT, typename YT, int TPR, bool SHIFT>
+cudaError_t fwd_pipe_t(const FwdArgs& a, cudaStream_t st) {
+  constexpr int VEC = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4, NV = 16 / VEC;
+  constexpr int kGroups = kBwdThreads / TPR;
+  constexpr size_t smem = static_cast<size_t>(kFwdDepth) * NV * kBwdThreads * VEC * sizeof(XT);
+  auto kern = norm_fwd_pipe_kernel<XT, YT, VEC, TPR, NV, SHIFT>;
+  static bool done[64] = {};
+  const cudaError_t e = allow_ring(kern, done);
+  if (e != cudaSuccess) return e;
+  const int blocks = std::max(8, std::min(num_sms() / 8 * 8, cdiv(cdiv(a.T, kGroups), 8) * 8));
+  return launch_pdl(kern, dim3(blocks), dim3(kBwdThreads), smem, st, static_cast<const XT*>(a.x),
+                    a.ldx, a.w, a.b, a.w_f32, a.T, a.K, a.eps, static_cast<YT*>(a.y), a.mean, a.rstd,
+                    SHIFT ? residue_period(a.K, VEC) : 1);
+}
+template <typename XT, typename YT, bool SHIFT>
+cudaError_t fwd_pipe(const FwdArgs& a, cudaStream_t st) {
+  const int K = a.K + (SHIFT ? 7 : 0);
+  if (K <= 512) return fwd_pipe_t<XT, YT, 32, SHIFT>(a, st);
+  if (K <= 1024) return fwd_pipe_t<XT, YT, 64, SHIFT>(a, st);
+  if (K <= 2048) return fwd_pipe_t<XT, YT, 128, SHIFT>(a, st);
+  if (K <= 4096) return fwd_pipe_t<XT, YT, 256, SHIFT>(a, st);
+  return fwd_pipe_t<XT, YT, 512, SHIFT>(a, st);
+}
+
 template <typename XT, typename YT>
-cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t st) {
+cudaError_t fwd(const FwdArgs& a, RowPath path, cudaStream_t st) {
   const int K = a.K;
   if (K > kRegRow)
     return launch_pdl(norm_fwd_long_kernel<XT, YT>, dim3(a.T), dim3(512), 0, st,
                       static_cast<const XT*>(a.x), a.ldx, a.w, a.b, a.w_f32, a.T, K, a.eps,
                       static_cast<YT*>(a.y), a.mean, a.rstd);
-  if (vec) {
-    // a warp per row up to 2048 columns (64 values a lane, no barrier), then
-    // 16 values a thread
-    constexpr int V = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
+  // The ring pays once it turns over: more rows than two to a group.
+  const bool many = static_cast<long long>(a.T) * K > 2LL * num_sms() * kBwdThreads * 16;
+  if (many && path == kAligned && K <= 8192) return fwd_pipe<XT, YT, false>(a, st);
+  if (many && path == kShifted && K <= 8192 - 7) return fwd_pipe<XT, YT, true>(a, st);
+  if (path == kAligned) {
+    constexpr int V = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;  // 16 values a thread
     if (K <= 512) return fwd_t<XT, YT, V, 32, 16 / V>(a, st);
-    if (K <= 1024) return fwd_t<XT, YT, V, 32, 32 / V>(a, st);
-    if (K <= 2048 && a.T >= 4 * num_sms()) return fwd_t<XT, YT, V, 32, 64 / V>(a, st);
     if (K <= 2048) return fwd_t<XT, YT, V, 128, 16 / V>(a, st);
     if (K <= 4096) return fwd_t<XT, YT, V, 256, 16 / V>(a, st);
     if (K <= 8192) return fwd_t<XT, YT, V, 512, 16 / V>(a, st);
@@ -692,33 +960,25 @@ template <typename XT, typename YT, int TPR, bool SHIFT>
 cudaError_t bwd_pipe_t(const BwdArgs& a, int* nb, cudaStream_t st) {
   constexpr int VEC = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
   constexpr int NV = 16 / VEC;
-  constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
+  constexpr int kThreads = kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   constexpr size_t kRing = static_cast<size_t>(pipe_depth<XT, YT>()) * NV * kThreads * VEC * (sizeof(XT) + sizeof(YT));
-  int period = 1;
-  if (SHIFT)
-    for (period = VEC; period > 1 && (static_cast<long long>(a.K) * (period / 2)) % VEC == 0;) period /= 2;
   // a multiple of eight blocks, so that the groups divide by any period
   *nb = std::max(8, std::min(norm_bwd_blocks(), cdiv(cdiv(a.T, kGroups), 8) * 8));
   const size_t smem = std::max(kRing, static_cast<size_t>(2) * a.K * 4);
-  static bool done[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
   auto kern = norm_bwd_pipe_kernel<XT, YT, VEC, TPR, NV, SHIFT>;
-  if (dev >= 64 || !done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) done[dev] = true;
-  }
+  static bool done[64] = {};
+  const cudaError_t e = allow_ring(kern, done);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(*nb), dim3(kThreads), smem, st, static_cast<const YT*>(a.dy),
                     static_cast<const XT*>(a.x), a.ldx, a.w, a.w_f32, a.mean, a.rstd, a.T, a.K,
-                    static_cast<XT*>(a.dx), a.part, period);
+                    static_cast<XT*>(a.dx), a.part,
+                    SHIFT ? residue_period(a.K, VEC) : 1);
 }
 // K: the row's columns, with SHIFT those of the pieces that cover it
 template <typename XT, typename YT, bool SHIFT>
 cudaError_t bwd_pipe(const BwdArgs& a, int* nb, cudaStream_t st) {
-  constexpr int VEC = sizeof(XT) == 2 && sizeof(YT) == 2 ? 8 : 4;
-  const int K = a.K + (SHIFT ? VEC - 1 : 0);
+  const int K = a.K + (SHIFT ? 7 : 0);
   if (K <= 512) return bwd_pipe_t<XT, YT, 32, SHIFT>(a, nb, st);
   if (K <= 1024) return bwd_pipe_t<XT, YT, 64, SHIFT>(a, nb, st);
   if (K <= 2048) return bwd_pipe_t<XT, YT, 128, SHIFT>(a, nb, st);
@@ -726,10 +986,8 @@ cudaError_t bwd_pipe(const BwdArgs& a, int* nb, cudaStream_t st) {
   return bwd_pipe_t<XT, YT, 512, SHIFT>(a, nb, st);
 }
 
-enum BwdPath { kByElement, kAligned, kShifted };
-
 template <typename XT, typename YT>
-cudaError_t bwd(const BwdArgs& a, BwdPath path, cudaStream_t st) {
+cudaError_t bwd(const BwdArgs& a, RowPath path, cudaStream_t st) {
   const int K = a.K;
   int nb = 0;
   cudaError_t e;
@@ -763,28 +1021,32 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 int norm_bwd_blocks() { return std::max(8, num_sms() / 8 * 8); }
 
-// 16-byte accesses where every row of every operand starts on a 16-byte
-// boundary, else element by element.
+// Pieces (16 bytes of the wider type) where the bases are aligned and either
+// every row starts on a piece boundary or all matrices share the rows'
+// residues; else element by element.
+static RowPath row_path(bool any_f32, int K, long long ldx, bool bases, bool params) {
+  const int vec = any_f32 ? 4 : 8;
+  if (!bases) return kByElement;
+  if (K % vec == 0 && ldx % vec == 0 && params) return kAligned;
+  return ldx % vec == K % vec ? kShifted : kByElement;
+}
+
 cudaError_t launch_norm_fwd(const void* x, bool x_f32, long long ldx, const void* w, const void* b,
                             bool w_f32, int T, int K, float eps, void* y, bool y_f32, float* mean,
                             float* rstd, cudaStream_t st) {
-  const bool vec = K % 8 == 0 && ldx % 8 == 0 && aligned16(x) && aligned16(w) &&
-                   (!b || aligned16(b)) && aligned16(y);
+  const RowPath path = row_path(x_f32 || y_f32, K, ldx, aligned16(x) && aligned16(y),
+                                aligned16(w) && aligned16(b));
   const FwdArgs a{x, ldx, w, b, w_f32, T, K, eps, y, mean, rstd};
   using B = __nv_bfloat16;
-  if (x_f32) return y_f32 ? fwd<float, float>(a, vec, st) : fwd<float, B>(a, vec, st);
-  return y_f32 ? fwd<B, float>(a, vec, st) : fwd<B, B>(a, vec, st);
+  if (x_f32) return y_f32 ? fwd<float, float>(a, path, st) : fwd<float, B>(a, path, st);
+  return y_f32 ? fwd<B, float>(a, path, st) : fwd<B, B>(a, path, st);
 }
 
 cudaError_t launch_norm_bwd(const void* dy, bool y_f32, const void* x, bool x_f32, long long ldx,
                             const void* w, bool w_f32, const float* mean, const float* rstd, int T,
                             int K, void* dx, void* dw, void* db, float* part, cudaStream_t st) {
-  const int vec = x_f32 || y_f32 ? 4 : 8;
-  BwdPath path = kByElement;
-  if (aligned16(x) && aligned16(dy) && aligned16(dx)) {
-    if (K % vec == 0 && ldx % vec == 0 && aligned16(w)) path = kAligned;
-    else if (ldx % vec == K % vec) path = kShifted;
-  }
+  const RowPath path = row_path(x_f32 || y_f32, K, ldx,
+                                aligned16(x) && aligned16(dy) && aligned16(dx), aligned16(w));
   const BwdArgs a{dy, x, ldx, w, w_f32, mean, rstd, T, K, dx, dw, db, part};
   using B = __nv_bfloat16;
   if (x_f32) return y_f32 ? bwd<float, float>(a, path, st) : bwd<float, B>(a, path, st);
