@@ -15,7 +15,9 @@
 // the k ids are always valid and distinct.
 //
 // Each lane holds V consecutive experts in registers.  The kernel is bound by
-// instruction issue, not by its bytes (a few KB per token).
+// instruction issue, not by its bytes (1 KB per token at E = 256), so the work
+// per round of the top-k is what counts: up to V = 8 a lane sorts its keys once
+// and a round pops the winner's list.
 #include "common.cuh"
 #include "internal.h"
 
@@ -26,9 +28,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 8;
 
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (!(f > -INFINITY)) return 1u;  // -inf, NaN
-  const uint32_t u = __float_as_uint(f + 0.f);  // -0 -> +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const int u = __float_as_int(f + 0.f);  // -0 -> +0
+  const uint32_t k = static_cast<uint32_t>(u ^ ((u >> 31) | 0x80000000));
+  return f > -INFINITY ? k : 1u;  // -inf, NaN
 }
 __device__ __forceinline__ float key_value(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
@@ -62,7 +64,17 @@ __device__ __forceinline__ float open_logit<__nv_bfloat16>(__nv_bfloat16 b) {
 template <typename T, int V>
 __device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool vec, float (&l)[V]) {
   constexpr int PER = 16 / sizeof(T);
-  if constexpr (V % PER == 0) {
+  if constexpr (V == 4 && PER == 8) {
+    if (vec) {  // 8 bytes a lane
+      uint2 q = make_uint2(0xff80ff80u, 0xff80ff80u);  // -inf
+      if (e0 < E) q = *reinterpret_cast<const uint2*>(row + e0);
+      const uint32_t u[2] = {q.x, q.y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        l[j] = open_logit<T>(__ushort_as_bfloat16(static_cast<unsigned short>(u[j / 2] >> (16 * (j & 1)))));
+      return;
+    }
+  } else if constexpr (V % PER == 0) {
     if (vec) {  // E a multiple of V's 16-byte pieces, rows 16-byte aligned
 #pragma unroll
       for (int i = 0; i < V; i += PER) {
@@ -101,11 +113,76 @@ struct SelectArgs {
   float scale;
   int32_t* ids;
   float* weights;
-  bool vec;
+  bool vec, vec_bias;  // 16-byte loads
 };
+
+// Keys of the experts outside the topk_groups best groups become 1.
+template <int V>
+__device__ __forceinline__ void keep_groups(const SelectArgs& a, int e0, int lane,
+                                            uint32_t (&key)[V]) {
+  const int gs = a.E / a.groups;
+  const int L = gs / V;  // lanes per group, where that divides evenly
+  auto score = [&](uint32_t b1, uint32_t b2) {
+    return !a.softmax && b1 > 1u && b2 > 1u ? order_key(key_value(b1) + key_value(b2)) : b1;
+  };
+  if (gs % V == 0 && (L & (L - 1)) == 0) {
+    // a lane's experts are of one group and the group's lanes an aligned
+    // power of two: two best keys per lane, then over the group's lanes
+    uint32_t x = 0u, y = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      y = max(y, min(x, key[i]));
+      x = max(x, key[i]);
+    }
+    for (int o = 1; o < L; o <<= 1) {
+      const uint32_t x2 = __shfl_xor_sync(kFull, x, o), y2 = __shfl_xor_sync(kFull, y, o);
+      y = max(min(x, x2), max(y, y2));
+      x = max(x, x2);
+    }
+    const int lg = __ffs(L) - 1, mine_g = lane >> lg;
+    uint32_t mine = e0 < a.E ? score(x, y) : 0u;
+    bool kept = false;
+    for (int r = 0; r < a.topk_groups; ++r) {
+      const uint32_t b = __reduce_max_sync(kFull, mine);
+      const int g = (__ffs(__ballot_sync(kFull, mine == b)) - 1) >> lg;
+      if (g == mine_g) mine = 0u, kept = true;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!kept && e0 + i < a.E) key[i] = 1u;
+    return;
+  }
+  // any other size: group by group, lane g keeps the score of group g
+  uint32_t mine = 0u;
+  for (int g = 0; g < a.groups; ++g) {
+    uint32_t x = 0u, y = 0u;  // the lane's best two keys in the group
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = e0 + i;
+      const uint32_t u = e >= g * gs && e < (g + 1) * gs ? key[i] : 0u;
+      y = max(y, min(x, u));
+      x = max(x, u);
+    }
+    const uint32_t b1 = __reduce_max_sync(kFull, x);
+    const int owner = __ffs(__ballot_sync(kFull, x == b1)) - 1;
+    const uint32_t b2 = __reduce_max_sync(kFull, lane == owner ? y : x);
+    if (lane == g) mine = score(b1, b2);
+  }
+  uint32_t kept = 0u;
+  for (int r = 0; r < a.topk_groups; ++r) {
+    const uint32_t b = __reduce_max_sync(kFull, mine);
+    const int g = __ffs(__ballot_sync(kFull, mine == b)) - 1;
+    kept |= 1u << g;
+    if (lane == g) mine = 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (e0 + i < a.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 1u;
+}
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a) {
+  extern __shared__ float scores[];  // [kWarps][32 V]
   const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   pdl_trigger();
@@ -115,6 +192,28 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a)
   float p[V];
   uint32_t key[V];
   load_logits<T, V>(static_cast<const T*>(a.logits) + t * a.ldl, e0, E, a.vec, p);
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = 0.f;
+  if (a.bias) {
+    bool done = false;
+    if constexpr (V % 4 == 0) {
+      if (a.vec_bias) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          if (e0 + i < E) {
+            const float4 v = *reinterpret_cast<const float4*>(a.bias + e0 + i);
+            bias[i] = v.x, bias[i + 1] = v.y, bias[i + 2] = v.z, bias[i + 3] = v.w;
+          }
+        done = true;
+      }
+    }
+    if (!done) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) bias[i] = a.bias[e0 + i];
+    }
+  }
   if (a.softmax) {
     float top = p[0];
 #pragma unroll
@@ -132,90 +231,92 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       p[i] *= inv;
-      if (a.bias && key[i] > 1u) key[i] = order_key(p[i] + a.bias[e0 + i]);
+      if (a.bias && key[i] > 1u) key[i] = order_key(p[i] + bias[i]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool open = p[i] > -INFINITY;
+      const float l = p[i];
+      p[i] = __frcp_rn(1.f + expf(-l));  // (correctly rounded, as the division)
       // below -87 exp(-logit) nears f32's end, and 1 + exp(-logit) has long
       // been exp(-logit): exp(logit) itself, down to the denormals, so that a
       // row of very low logits keeps its proportions; 0 where masked
-      p[i] = p[i] < -87.f ? expf(p[i]) : 1.f / (1.f + expf(-p[i]));
-      key[i] = open ? order_key(a.bias ? p[i] + a.bias[e0 + i] : p[i]) : 1u;
+      if (l < -87.f) p[i] = expf(l);
+      key[i] = order_key(l > -INFINITY ? p[i] + bias[i] : l);
     }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if (e0 + i >= E) key[i] = 0u;  // no expert here
 
-  if (a.groups > 1) {
-    // lane g keeps the score of group g
-    const int gs = E / a.groups;
-    uint32_t mine = 0u;
-    for (int g = 0; g < a.groups; ++g) {
-      uint32_t x = 0u, y = 0u;  // the lane's best two keys in the group
+  if (a.groups > 1) keep_groups<V>(a, e0, lane, key);
+
+  // the scores where every lane can read them
+  float* row = scores + (threadIdx.x >> 5) * (32 * V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = e0 + i;
-        const uint32_t u = e >= g * gs && e < (g + 1) * gs ? key[i] : 0u;
-        y = max(y, min(x, u));
-        x = max(x, u);
-      }
-      const uint32_t b1 = __reduce_max_sync(kFull, x);
-      uint32_t score = b1;
-      if (!a.softmax) {
-        const int owner = __ffs(__ballot_sync(kFull, x == b1)) - 1;
-        const uint32_t b2 = __reduce_max_sync(kFull, lane == owner ? y : x);
-        if (b1 > 1u && b2 > 1u) score = order_key(key_value(b1) + key_value(b2));
-      }
-      if (lane == g) mine = score;
-    }
-    uint32_t kept = 0u;
-    for (int r = 0; r < a.topk_groups; ++r) {
-      const uint32_t b = __reduce_max_sync(kFull, mine);
-      const int g = __ffs(__ballot_sync(kFull, mine == b)) - 1;
-      kept |= 1u << g;
-      if (lane == g) mine = 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i < E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 1u;
-  }
+  for (int i = 0; i < V; ++i) row[e0 + i] = p[i];
 
   // k rounds: the largest key, the lowest expert among equals
   int id_mine = 0;
-  float w_mine = 0.f;
-  uint32_t best = 0u;
-  int slot = 0;
-  auto rescan = [&]() {
-    best = key[0];
-    slot = 0;
+  uint32_t key_mine = 0u;
+  if constexpr (V <= 8) {
+    // Each lane's keys in descending order (odd-even transposition with strict
+    // comparisons: equal keys keep their order), their places as 4-bit digits.
+    uint32_t place[V];
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > best) best = key[i], slot = i;
-  };
-  rescan();
-  for (int r = 0; r < a.k; ++r) {
-    const uint32_t b = __reduce_max_sync(kFull, best);
-    const int owner = __ffs(__ballot_sync(kFull, best == b)) - 1;
-    float w = 0.f;
-    const int id = __shfl_sync(kFull, e0 + slot, owner);
-    if (lane == owner) {
+    for (int i = 0; i < V; ++i) place[i] = i;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == slot) {
-          w = b > 1u ? p[i] : 0.f;
-          key[i] = 0u;
-        }
-      rescan();
+    for (int r = 0; r < V; ++r)
+#pragma unroll
+      for (int i = r & 1; i + 1 < V; i += 2) {
+        const bool swap = key[i + 1] > key[i];
+        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+        const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
+        key[i] = hi, key[i + 1] = lo;
+        place[i] = ph, place[i + 1] = pl;
+      }
+    uint32_t places = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) places |= place[i] << (4 * i);
+    for (int r = 0; r < a.k; ++r) {
+      const uint32_t b = __reduce_max_sync(kFull, key[0]);
+      const int owner = __ffs(__ballot_sync(kFull, key[0] == b)) - 1;
+      const int id = __shfl_sync(kFull, e0 + static_cast<int>(places & 15u), owner);
+      if (lane == owner) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+        key[V - 1] = 0u;
+        places >>= 4;
+      }
+      if (lane == r) id_mine = id, key_mine = b;
     }
-    w = __shfl_sync(kFull, w, owner);
-    if (lane == r) {
-      id_mine = id;
-      w_mine = w;
+  } else {
+    uint32_t best = 0u;
+    auto rescan = [&]() {
+      best = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    };
+    rescan();
+    for (int r = 0; r < a.k; ++r) {
+      const uint32_t b = __reduce_max_sync(kFull, best);
+      const int owner = __ffs(__ballot_sync(kFull, best == b)) - 1;
+      int slot = 0;
+      if (lane == owner) {
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == b) slot = i;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i == slot) key[i] = 0u;
+        rescan();
+      }
+      const int id = __shfl_sync(kFull, e0 + slot, owner);
+      if (lane == r) id_mine = id, key_mine = b;
     }
   }
+  __syncwarp();
+  float w_mine = lane < a.k && key_mine > 1u ? row[id_mine] : 0.f;
   if (a.renorm) {
     const float tot = warp_sum(w_mine);
     w_mine = tot > 0.f ? w_mine / tot : 0.f;
@@ -247,7 +348,7 @@ struct SelectBwdArgs {
   float scale;
   void* out;
   int32_t* dev_status;
-  bool vec;
+  bool vec, vec_out;
 };
 
 template <typename T>
@@ -323,6 +424,26 @@ __global__ void __launch_bounds__(kWarps * 32) select_bwd_kernel(const SelectBwd
   }
   __syncwarp();
   T* out = static_cast<T*>(a.out) + t * E;
+  if constexpr (V % 4 == 0) {
+    // four consecutive experts per access, lane after lane
+    if (a.vec_out) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const int e = dense ? lane * V + i : (i / 4) * 128 + lane * 4;
+        if (e >= E) continue;
+        float4 v = *reinterpret_cast<const float4*>(row + e);
+        if (dense) {
+          v.x -= p[i] * dot, v.y -= p[i + 1] * dot;
+          v.z -= p[i + 2] * dot, v.w -= p[i + 3] * dot;
+        }
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(out + e) = v;
+        else
+          *reinterpret_cast<uint2*>(out + e) = make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
+      }
+      return;
+    }
+  }
   if (dense) {
 #pragma unroll
     for (int i = 0; i < V; ++i) row[lane * V + i] -= p[i] * dot;
@@ -335,26 +456,26 @@ __global__ void __launch_bounds__(kWarps * 32) select_bwd_kernel(const SelectBwd
   }
 }
 
+size_t row_smem(int v) { return static_cast<size_t>(kWarps) * 32 * v * 4; }
 template <typename T>
 cudaError_t select_t(const SelectArgs& a, cudaStream_t st) {
   const dim3 grid(cdiv(a.T, kWarps)), block(kWarps * 32);
-  if (a.E <= 32) return launch_pdl(select_kernel<T, 1>, grid, block, 0, st, a);
-  if (a.E <= 64) return launch_pdl(select_kernel<T, 2>, grid, block, 0, st, a);
-  if (a.E <= 128) return launch_pdl(select_kernel<T, 4>, grid, block, 0, st, a);
-  if (a.E <= 256) return launch_pdl(select_kernel<T, 8>, grid, block, 0, st, a);
-  if (a.E <= 512) return launch_pdl(select_kernel<T, 16>, grid, block, 0, st, a);
-  return launch_pdl(select_kernel<T, 32>, grid, block, 0, st, a);
+  if (a.E <= 32) return launch_pdl(select_kernel<T, 1>, grid, block, row_smem(1), st, a);
+  if (a.E <= 64) return launch_pdl(select_kernel<T, 2>, grid, block, row_smem(2), st, a);
+  if (a.E <= 128) return launch_pdl(select_kernel<T, 4>, grid, block, row_smem(4), st, a);
+  if (a.E <= 256) return launch_pdl(select_kernel<T, 8>, grid, block, row_smem(8), st, a);
+  if (a.E <= 512) return launch_pdl(select_kernel<T, 16>, grid, block, row_smem(16), st, a);
+  return launch_pdl(select_kernel<T, 32>, grid, block, row_smem(32), st, a);
 }
 template <typename T>
 cudaError_t select_bwd_t(const SelectBwdArgs& a, cudaStream_t st) {
   const dim3 grid(cdiv(a.T, kWarps)), block(kWarps * 32);
-  auto smem = [](int v) { return static_cast<size_t>(kWarps) * 32 * v * 4; };
-  if (a.E <= 32) return launch_pdl(select_bwd_kernel<T, 1>, grid, block, smem(1), st, a);
-  if (a.E <= 64) return launch_pdl(select_bwd_kernel<T, 2>, grid, block, smem(2), st, a);
-  if (a.E <= 128) return launch_pdl(select_bwd_kernel<T, 4>, grid, block, smem(4), st, a);
-  if (a.E <= 256) return launch_pdl(select_bwd_kernel<T, 8>, grid, block, smem(8), st, a);
-  if (a.E <= 512) return launch_pdl(select_bwd_kernel<T, 16>, grid, block, smem(16), st, a);
-  return launch_pdl(select_bwd_kernel<T, 32>, grid, block, smem(32), st, a);
+  if (a.E <= 32) return launch_pdl(select_bwd_kernel<T, 1>, grid, block, row_smem(1), st, a);
+  if (a.E <= 64) return launch_pdl(select_bwd_kernel<T, 2>, grid, block, row_smem(2), st, a);
+  if (a.E <= 128) return launch_pdl(select_bwd_kernel<T, 4>, grid, block, row_smem(4), st, a);
+  if (a.E <= 256) return launch_pdl(select_bwd_kernel<T, 8>, grid, block, row_smem(8), st, a);
+  if (a.E <= 512) return launch_pdl(select_bwd_kernel<T, 16>, grid, block, row_smem(16), st, a);
+  return launch_pdl(select_bwd_kernel<T, 32>, grid, block, row_smem(32), st, a);
 }
 
 // 16-byte loads of the logits: rows on 16-byte boundaries and whole pieces.
@@ -370,7 +491,8 @@ cudaError_t launch_select(const void* logits, bool f32, long long ldl, int T, in
                           bool renorm, float scale, int32_t* ids, float* weights,
                           cudaStream_t st) {
   const SelectArgs a{logits, ldl,         bias,   T,     E,   k,       softmax,
-                     groups, topk_groups, renorm, scale, ids, weights, vec_logits(logits, ldl, E, f32)};
+                     groups, topk_groups, renorm, scale, ids, weights, vec_logits(logits, ldl, E, f32),
+                     reinterpret_cast<uintptr_t>(bias) % 16 == 0 && E % 4 == 0};
   return f32 ? select_t<float>(a, st) : select_t<__nv_bfloat16>(a, st);
 }
 
@@ -379,7 +501,8 @@ cudaError_t launch_select_bwd(const float* g, const void* logits, bool f32, long
                               bool softmax, bool renorm, float scale, void* out,
                               int32_t* dev_status, cudaStream_t st) {
   const SelectBwdArgs a{g,       logits, ldl,   ids, w,          T, E, k,
-                        softmax, renorm, scale, out, dev_status, vec_logits(logits, ldl, E, f32)};
+                        softmax, renorm, scale, out, dev_status, vec_logits(logits, ldl, E, f32),
+                        reinterpret_cast<uintptr_t>(out) % 16 == 0 && E % 4 == 0};
   return f32 ? select_bwd_t<float>(a, st) : select_bwd_t<__nv_bfloat16>(a, st);
 }
 
