@@ -357,7 +357,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&maps.a[0]);
     tma_prefetch_desc(&maps.b[0]);
   }
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s)
       mbar_init(m.full + 8 * s, 2);  // both TMA threads announce their own bytes
@@ -380,7 +379,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *m.tmem_slot;
-  pdl_wait();
+  if (!p.late) pdl_wait();
+  pdl_trigger();  // (after the wait: see launch_dense_backward)
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
   const int total = p.pr[0].tiles + p.pr[1].tiles;
   const uint32_t full_l = mapa_shared(m.full, 0);
@@ -640,6 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     tmem_dealloc_cg2(tmem_base, 512);
   }
+  if (p.late) pdl_wait();
 }
 
 // ---------------------------------------------------------------- single-CTA tiles, split contraction
@@ -808,7 +809,6 @@ __global__ void __launch_bounds__(kThreads)
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
   }
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(full + 8 * s, 1);
     for (int q = 0; q < kGroups; ++q) mbar_init(empty + 8 * q, 1);
@@ -827,7 +827,8 @@ __global__ void __launch_bounds__(kThreads)
   if (S > 1) cluster_arrive();  // this CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();
+  if (!p.late) pdl_wait();
+  pdl_trigger();  // (after the wait: see launch_dense_backward)
   const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
 
   if (warp == 5) {
@@ -973,6 +974,7 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_after();
     tmem_dealloc(tmem_base, c.tmem_cols);
   }
+  if (p.late) pdl_wait();
 }
 
 // ---------------------------------------------------------------- backward prep
@@ -1349,6 +1351,12 @@ cudaError_t launch_dense_forward(const DenseParams& p0, const DenseOperand& x,
   return use_pairs(p.pr[0]) ? launch_pairs(p, &x, &W, 1, st) : launch_cta(p, 0, x, W, st);
 }
 
+// Up to four launches: dz, then dx and dW (one launch where both take 256 x
+// 256 tiles), then the bias gradient's sums.  All but dz depend on dz alone,
+// so only the first of them waits for what is before it; the later ones start
+// as soon as every block of the one before has passed its own wait (a kernel
+// lets its successor in after its wait, so dz is complete by then) and wait at
+// their end, which keeps the order of completion for whatever follows.
 cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t st) {
   const bool direct = dy_is_operand(a);
   const int ldz = dz_ld(a.N);
@@ -1359,17 +1367,17 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
   __nv_bfloat16* dz_out = direct || !gemm ? nullptr : dz;
   float* part_out = a.db ? part : nullptr;
   cudaError_t e = cudaSuccess;
+  int parts = 0;
   if (dz_out || part_out) {
     const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && aligned16(a.dy) && aligned16(a.pre);
     const DzPlan pl = plan_dz(a.T, a.N, vec);
+    parts = pl.by;
     const DzArgs z{a.dy, a.lddy,  static_cast<const __nv_bfloat16*>(a.pre), a.T, a.N, pl.rows,
                    pl.lanes, dz_out, ldz, part_out};
     if (a.act == kActRelu) e = launch_dz<kActRelu>(pl, z, a.dy_f32, st);
     else if (a.act == kActSilu) e = launch_dz<kActSilu>(pl, z, a.dy_f32, st);
     else if (a.act == kActGelu) e = launch_dz<kActGelu>(pl, z, a.dy_f32, st);
     else e = launch_dz<kActNone>(pl, z, a.dy_f32, st);
-    if (e == cudaSuccess && part_out)
-      e = launch_column_sums(part, pl.by, a.N, a.db, nullptr, a.db_f32, st);
     if (e != cudaSuccess) return e;
   }
   const DenseOperand z = direct ? DenseOperand{a.dy, a.T, a.N, a.lddy} : DenseOperand{dz, a.T, a.N, ldz};
@@ -1385,13 +1393,19 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
     d.M = M, d.N = N, d.Kc = Kc, d.a_mn = a_mn, d.b_mn = true, d.out = out;
     p.pr[n] = d;
     pa[n] = oa, pb[n] = ob;
-    if (!use_pairs(d)) return launch_cta(p, n, oa, ob, st);
-    ++n;
-    return cudaSuccess;
+    if (use_pairs(d)) {
+      ++n;
+      return cudaSuccess;
+    }
+    const cudaError_t r = launch_cta(p, n, oa, ob, st);
+    p.late = true;
+    return r;
   };
   if (a.dx) e = add(a.T, a.K, a.N, false, a.dx, z, W);
   if (e == cudaSuccess && a.dW) e = add(a.N, a.K, a.T, true, a.dW, z, x);
   if (e == cudaSuccess && n) e = launch_pairs(p, pa, pb, n, st);
+  if (e == cudaSuccess && part_out)
+    e = launch_column_sums(part, parts, a.N, a.db, nullptr, a.db_f32, gemm, st);
   return e;
 }
 

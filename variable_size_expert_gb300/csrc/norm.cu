@@ -469,9 +469,9 @@ __device__ __forceinline__ void store_piece(T* at, int c, int K, const F2 (&v)[V
   }
 }
 
-// Backward.  The sums of row i + 1 are formed before row i is finished, from
-// the row's slot both times: one barrier per row, with a whole row of other
-// work between a sum's parts and its use.  Packed f32 arithmetic.
+// Backward: one barrier per row (the sums' slots alternate); a row's xh and
+// g w stay in registers between its sums and its gradient.  Packed f32
+// arithmetic.
 // Row slots: three of two f32 rows fill the shared memory, four of less.
 template <typename XT, typename YT>
 __host__ __device__ constexpr int pipe_depth() {
@@ -526,41 +526,37 @@ __global__ void __launch_bounds__(kBwdThreads)
     }
     cp_async_commit();  // (an empty group past the last row keeps the count)
   };
-  // xh and dy of piece j of a landed row
-  auto fetch = [&](int slot, int j, F2 nmu, F2 rs, F2 (&xh)[H], F2 (&gy)[H]) {
-    const int c = c0 + j * kStride;
-    const int o = slot * (NV * kRow) + j * kRow;
-    Raw<XT, VEC> rx = *reinterpret_cast<const Raw<XT, VEC>*>(mine_x + o);
-    Raw<YT, VEC> ry = *reinterpret_cast<const Raw<YT, VEC>*>(mine_y + o);
-    if (SHIFT && (c < 0 || c + VEC > K)) {
-      keep_range<XT, VEC>(rx, -c, K - c);
-      keep_range<YT, VEC>(ry, -c, K - c);
-    }
-    unpack2v<XT, VEC>(rx, xh);
-    unpack2v<YT, VEC>(ry, gy);
-#pragma unroll
-    for (int i = 0; i < H; ++i) xh[i] = mul2(add2(xh[i], nmu), rs);
-  };
   constexpr int depth = pipe_depth<XT, YT>(), D = depth - 1;  // slots, rows ahead
 #pragma unroll
   for (int i = 0; i < D; ++i) copy(i, i);
-  // the sums of a landed row: into slots[par], or (a warp per row) returned
+  // xh and g w of a landed row, and its sums: into slots[par], or (a warp per
+  // row) returned
   const float inv_k = 1.f / K;
+  F2 xh[NV][H], g[NV][H];
   auto sums = [&](int slot, float mu, float rs, int par) -> float {
     F2 s1 = both(0.f), s2 = both(0.f);
     const F2 nmu = both(-mu), rs2 = both(rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (c0 + j * kStride >= K) continue;
-      F2 xh[H], g[H];
-      fetch(slot, j, nmu, rs2, xh, g);
+      const int c = c0 + j * kStride;
+      if (c >= K) continue;
+      const int o = slot * (NV * kRow) + j * kRow;
+      Raw<XT, VEC> rx = *reinterpret_cast<const Raw<XT, VEC>*>(mine_x + o);
+      Raw<YT, VEC> ry = *reinterpret_cast<const Raw<YT, VEC>*>(mine_y + o);
+      if (SHIFT && (c < 0 || c + VEC > K)) {
+        keep_range<XT, VEC>(rx, -c, K - c);
+        keep_range<YT, VEC>(ry, -c, K - c);
+      }
+      unpack2v<XT, VEC>(rx, xh[j]);
+      unpack2v<YT, VEC>(ry, g[j]);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
-        aw[j][i] = fma2(g[i], xh[i], aw[j][i]);
-        ab[j][i] = add2(ab[j][i], g[i]);
-        g[i] = mul2(g[i], wv[j][i]);
-        s1 = add2(s1, g[i]);
-        s2 = fma2(g[i], xh[i], s2);
+        xh[j][i] = mul2(add2(xh[j][i], nmu), rs2);
+        aw[j][i] = fma2(g[j][i], xh[j][i], aw[j][i]);
+        ab[j][i] = add2(ab[j][i], g[j][i]);
+        g[j][i] = mul2(g[j][i], wv[j][i]);
+        s1 = add2(s1, g[j][i]);
+        s2 = fma2(g[j][i], xh[j][i], s2);
       }
     }
     float a, b, c, d;
@@ -571,12 +567,12 @@ __global__ void __launch_bounds__(kBwdThreads)
     return a;
   };
   const float *pm = mean + first, *pr = rstd + first;
-  float mu = 0.f, rs = 0.f, held = 0.f;
+  float rs = 0.f, held = 0.f;
   int slot = 0, ahead = D, par = 0;
   if (rows > 0) {
-    mu = *pm, rs = *pr;
+    rs = *pr;
     cp_async_wait<D - 1>();
-    held = sums(0, mu, rs, 0);
+    held = sums(0, *pm, rs, 0);
   }
 #pragma unroll 1
   for (int r = 0; r < rows; ++r, par ^= 1) {
@@ -591,27 +587,23 @@ __global__ void __launch_bounds__(kBwdThreads)
       for (int o = NW / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     }
     const float s1 = __shfl_sync(0xffffffffu, v, 0), s2 = __shfl_sync(0xffffffffu, v, 16);
-    const int next = slot + 1 == depth ? 0 : slot + 1;
-    // the next row's sums, then this row's gradient
-    copy(r + D, ahead);
-    if (++ahead == depth) ahead = 0;
-    cp_async_wait<D - 1>();  // the next row has landed
-    if (more) held = sums(next, mu1, rs1, par ^ 1);
-    const F2 n1 = both(-s1 * inv_k), n2 = both(-s2 * inv_k), nmu = both(-mu), rs2 = both(rs);
+    const F2 n1 = both(-s1 * inv_k), n2 = both(-s2 * inv_k), rs2 = both(rs);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = c0 + j * kStride;
       if (c >= K) continue;
-      F2 xh[H], g[H];
-      fetch(slot, j, nmu, rs2, xh, g);
+      F2 o[H];
 #pragma unroll
-      for (int i = 0; i < H; ++i)
-        g[i] = mul2(rs2, fma2(xh[i], n2, fma2(g[i], wv[j][i], n1)));
-      store_piece<XT, VEC, SHIFT>(out + j * kStride, c, K, g);
+      for (int i = 0; i < H; ++i) o[i] = mul2(rs2, fma2(xh[j][i], n2, add2(g[j][i], n1)));
+      store_piece<XT, VEC, SHIFT>(out + j * kStride, c, K, o);
     }
     out += sk;
-    mu = mu1, rs = rs1;
-    slot = next;
+    copy(r + D, ahead);
+    if (++ahead == depth) ahead = 0;
+    if (++slot == depth) slot = 0;
+    cp_async_wait<D - 1>();  // the next row has landed
+    if (more) held = sums(slot, mu1, rs1, par ^ 1);
+    rs = rs1;
   }
   // the block's partial row: groups added in order, over the ring
   cp_async_wait<0>();
@@ -810,10 +802,10 @@ __global__ void __launch_bounds__(256)
 // Partial rows part[2][nb][K] -> dw, db, added in block order: 32 columns
 // per block, 32 row lanes each summing every 32nd partial, then a tree.
 __global__ void __launch_bounds__(1024)
-    column_sums_kernel(const float* part, int nb, int K, void* dw, void* db, bool w_f32) {
+    column_sums_kernel(const float* part, int nb, int K, void* dw, void* db, bool w_f32, bool late) {
   __shared__ float s[32][33];
+  if (!late) pdl_wait();
   pdl_trigger();
-  pdl_wait();
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   const float* p = part + static_cast<long long>(blockIdx.y) * nb * K;
@@ -831,14 +823,15 @@ __global__ void __launch_bounds__(1024)
     else
       static_cast<__nv_bfloat16*>(out)[co] = __float2bfloat16_rn(v);
   }
+  if (late) pdl_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
-                               bool out_f32, cudaStream_t st) {
+                               bool out_f32, bool late, cudaStream_t st) {
   return launch_pdl(column_sums_kernel, dim3(cdiv(K, 32), out1 ? 2 : 1), dim3(1024), 0, st, part,
-                    nb, K, out0, out1, out_f32);
+                    nb, K, out0, out1, out_f32, late);
 }
 
 namespace {
@@ -1011,7 +1004,7 @@ cudaError_t bwd(const BwdArgs& a, RowPath path, cudaStream_t st) {
     else e = bwd_t<XT, YT, 1024>(a, &nb, st);
   }
   if (e != cudaSuccess) return e;
-  return launch_column_sums(a.part, nb, K, a.dw, a.db, a.w_f32, st);
+  return launch_column_sums(a.part, nb, K, a.dw, a.db, a.w_f32, false, st);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
