@@ -203,6 +203,18 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
       for (int i = 0; i < VEC; ++i) f[j][i] = 0.f;
     }
   }
+  // the parameters are on their way while the sums are formed
+  float wv[NV][VEC], bv[NV][VEC];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + tig) * VEC;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bv[j][i] = 0.f;
+    if (c < K) {
+      load_param<VEC>(w, w_f32, c, wv[j]);
+      if (b) load_param<VEC>(b, w_f32, c, bv[j]);
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -228,15 +240,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   for (int j = 0; j < NV; ++j) {
     const int c = (j * TPR + tig) * VEC;
     if (c < K) {
-      float wv[VEC], o[VEC];
-      load_param<VEC>(w, w_f32, c, wv);
+      float o[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) o[i] = f[j][i] * rstd * wv[i];
-      if (b) {
-        load_param<VEC>(b, w_f32, c, wv);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] += wv[i];
-      }
+      for (int i = 0; i < VEC; ++i) o[i] = fmaf(f[j][i] * rstd, wv[j][i], bv[j][i]);
       store_f<YT, VEC>(yr + c, o);
     }
   }
@@ -501,12 +507,6 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int rows = first < T ? (T - 1 - first) / step + 1 : 0;
   const int c0 = tig * VEC - m;      // column of the first piece; piece j: + j * kStride
   constexpr int kStride = TPR * VEC;
-  F2 wv[NV][H], aw[NV][H], ab[NV][H];
-  load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < H; ++i) aw[j][i] = ab[j][i] = both(0.f);
   // pointers that advance by a row of this group
   const XT* xs = x + first * ldx + c0;
   const YT* ys = dy + static_cast<long long>(first) * K + c0;
@@ -529,6 +529,12 @@ __global__ void __launch_bounds__(kBwdThreads)
   constexpr int depth = pipe_depth<XT, YT>(), D = depth - 1;  // slots, rows ahead
 #pragma unroll
   for (int i = 0; i < D; ++i) copy(i, i);
+  F2 wv[NV][H], aw[NV][H], ab[NV][H];
+  load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < H; ++i) aw[j][i] = ab[j][i] = both(0.f);
   // xh and g w of a landed row, and its sums: into slots[par], or (a warp per
   // row) returned
   const float inv_k = 1.f / K;
@@ -605,34 +611,37 @@ __global__ void __launch_bounds__(kBwdThreads)
     if (more) held = sums(slot, mu1, rs1, par ^ 1);
     rs = rs1;
   }
-  // the block's partial row: groups added in order, over the ring
+  // the block's partial row: every group's sums over the ring (64 KB at most),
+  // then added in group order
   cp_async_wait<0>();
   __syncthreads();
-  float* acc = reinterpret_cast<float*>(ring);  // [2][K]
+  float* acc = reinterpret_cast<float*>(ring);  // [groups][2][K]
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = c0 + j * kStride;
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      float w0, w1, b0, b1;
+      unpack2(aw[j][i], w0, w1);
+      unpack2(ab[j][i], b0, b1);
+      const int k = c + 2 * i;
+      float* at = acc + group * 2 * K + k;
+      if (k >= 0 && k < K) at[0] = w0, at[K] = b0;
+      if (k + 1 >= 0 && k + 1 < K) at[1] = w1, at[K + 1] = b1;
+    }
+  }
+  __syncthreads();
   float* pw = part + static_cast<long long>(blockIdx.x) * K;
   float* pb = part + static_cast<long long>(gridDim.x + blockIdx.x) * K;
-  for (int gi = 0; gi < kGroups; ++gi) {
-    if (group == gi) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * TPR + tig) * VEC - m;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          if (c + i < 0 || c + i >= K) continue;
-          float w0, w1, b0, b1;
-          unpack2(aw[j][i / 2], w0, w1);
-          unpack2(ab[j][i / 2], b0, b1);
-          const float vw = i & 1 ? w1 : w0, vb = i & 1 ? b1 : b0;
-          acc[c + i] = gi ? acc[c + i] + vw : vw;
-          acc[K + c + i] = gi ? acc[K + c + i] + vb : vb;
-        }
-      }
-    }
-    __syncthreads();
-  }
   for (int c = threadIdx.x; c < K; c += kThreads) {
-    pw[c] = acc[c];
-    pb[c] = acc[K + c];
+    float vw = 0.f, vb = 0.f;
+#pragma unroll 4
+    for (int gi = 0; gi < kGroups; ++gi) {
+      vw += acc[gi * 2 * K + c];
+      vb += acc[gi * 2 * K + K + c];
+    }
+    pw[c] = vw;
+    pb[c] = vb;
   }
 }
 
@@ -658,16 +667,6 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int gid = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
   const int first = SHIFT ? gid % period + period * (gid / period) : gid;
   const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
-  F2 wv[NV][H], bv[NV][H];
-  load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
-  if (b) {
-    load_columns<VEC, TPR, NV, SHIFT>(b, w_f32, tig, m, K, bv);
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < H; ++i) bv[j][i] = both(0.f);
-  }
   const float inv_k = 1.f / K;
   const int rows = first < T ? (T - 1 - first) / step + 1 : 0;
   const int c0 = tig * VEC - m;
@@ -687,6 +686,16 @@ __global__ void __launch_bounds__(kBwdThreads)
   };
 #pragma unroll
   for (int i = 0; i < D; ++i) copy(i, i);
+  F2 wv[NV][H], bv[NV][H];
+  load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
+  if (b) {
+    load_columns<VEC, TPR, NV, SHIFT>(b, w_f32, tig, m, K, bv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < H; ++i) bv[j][i] = both(0.f);
+  }
   float *pm = mean_out + first, *pr = rstd_out + first;
   int slot = 0, ahead = D;
 #pragma unroll 1
@@ -958,7 +967,7 @@ cudaError_t bwd_pipe_t(const BwdArgs& a, int* nb, cudaStream_t st) {
   constexpr size_t kRing = static_cast<size_t>(pipe_depth<XT, YT>()) * NV * kThreads * VEC * (sizeof(XT) + sizeof(YT));
   // a multiple of eight blocks, so that the groups divide by any period
   *nb = std::max(8, std::min(norm_bwd_blocks(), cdiv(cdiv(a.T, kGroups), 8) * 8));
-  const size_t smem = std::max(kRing, static_cast<size_t>(2) * a.K * 4);
+  const size_t smem = std::max(kRing, static_cast<size_t>(2) * kGroups * a.K * 4);
   auto kern = norm_bwd_pipe_kernel<XT, YT, VEC, TPR, NV, SHIFT>;
   static bool done[64] = {};
   const cudaError_t e = allow_ring(kern, done);

@@ -375,8 +375,16 @@ __global__ void __launch_bounds__(kWarps * 32) select_bwd_kernel(const SelectBwd
   const T* lr = static_cast<const T*>(a.logits) + t * a.ldl;
   float p[V];
   const bool dense = a.softmax && !a.renorm;
+  if (dense) load_logits<T, V>(lr, lane * V, E, a.vec, p);
+  // (loaded beside the logits: one latency for all)
+  int id = -1 - lane;  // lanes without a choice: all different, none an expert
+  float w = 0.f, g = 0.f;
+  if (lane < a.k) {
+    id = a.ids[t * a.k + lane];
+    w = a.w[t * a.k + lane];
+    g = a.g[t * a.k + lane];
+  }
   if (dense) {
-    load_logits<T, V>(lr, lane * V, E, a.vec, p);
     float top = p[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) top = fmaxf(top, p[i]);
@@ -392,12 +400,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_bwd_kernel(const SelectBwd
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] *= inv;
   }
-  int id = -1 - lane;  // lanes without a choice: all different, none an expert
-  float w = 0.f, g = 0.f;
   if (lane < a.k) {
-    id = a.ids[t * a.k + lane];
-    w = a.w[t * a.k + lane];
-    g = a.g[t * a.k + lane];
     if (id < 0 || id >= E) {
       atomicOr(a.dev_status, kDevBadExpertId);
       id = -1 - lane;
