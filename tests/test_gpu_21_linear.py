@@ -120,6 +120,31 @@ def test_many_tiles_backward(T, K, N):
     _check_backward(dy, x, W, None, "none", F)
 
 
+@pytest.mark.parametrize("K", [64, 320, 384, 512, 576, 1024, 4096])
+def test_long_runs_of_tiles(K):
+    """Thirteen tiles per CTA pair, over and over, with contractions shorter and
+    longer than the ring of blocks: no wait may run out, and every pass gives
+    the same bits, whichever of the copies and the products is ahead."""
+    T, N = 8192, 8192
+    x, W, b, _, g = _inputs(T, K, N, K, BF)
+    st = mgg.new_status(DEV)
+    ref = mgg.linear_forward(x, W, b, "gelu", status=st)
+    dy = torch.randn(T, N, generator=g, device=DEV).to(BF)
+    rdx, rdW, _ = mgg.linear_backward(dy, x, W, status=st)
+    for _ in range(12):
+        assert torch.equal(mgg.linear_forward(x, W, b, "gelu", status=st), ref)
+        dx, dW, _ = mgg.linear_backward(dy, x, W, status=st)
+        assert torch.equal(dx, rdx) and torch.equal(dW, rdW)
+        mgg.linear_forward(x, W, status=st)
+        mgg.linear_forward(x, W, out_dtype=F, status=st)
+    assert mgg.read_status(st) == 0
+    rows = torch.randint(0, T, (64,), generator=g, device=DEV)
+    z = R.d(x[rows]) @ R.d(W).t() + R.d(b)
+    tol = SLOPE * R.dot_bound(R.d(x[rows]), R.d(W)) + 16 * R.U * z.abs()
+    want = R.act(z, "gelu")
+    R.within(ref[rows], want, tol + R.rounding(BF, want) * 1.01, "rows")
+
+
 @pytest.mark.parametrize("T", [40, 2400])
 def test_slices_and_in_place_residual(T):
     K, N = 128, 2304 if T > 2000 else 72

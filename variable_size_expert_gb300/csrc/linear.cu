@@ -189,7 +189,12 @@ struct PairMaps {
   CUtensorMap a[2], b[2], out[2], pre, res;
 };
 
-constexpr int kGroups = 4;  // release barriers of a ring
+constexpr int kGroups = 8;  // release barriers of a ring
+// When the producer waits for a group, the MMAs may have released every group
+// up to the last block it issued: a barrier must not come round again by then
+// (a second completion would turn the parity it waits for).
+constexpr bool releases_fit(int stages, int lg) { return ((stages - 1) >> lg) < kGroups; }
+static_assert(releases_fit(STAGES, 0), "release barriers");
 struct PSmem {
   uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, res_full, issued;
   uint32_t* tmem_slot;
@@ -663,6 +668,8 @@ struct CtaParams {
 constexpr int kCtaMeta = 256;
 constexpr int kMaxStages = 12;
 static_assert(8 * (kMaxStages + kGroups + 2) + 8 <= kCtaMeta, "barrier area");
+static_assert(releases_fit(kMaxStages, 2) && releases_fit(7, 1) && releases_fit(3, 0),
+              "release barriers");  // (the group sizes that launch_cta picks)
 size_t cta_smem(const CtaParams& c) {
   return 1024 + static_cast<size_t>(c.stages) * (OPER + c.b_bytes) +
          (c.splits > 1 ? static_cast<size_t>(c.splits) * c.per * 512 : 0) + kCtaMeta;
