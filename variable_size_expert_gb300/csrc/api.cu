@@ -342,7 +342,8 @@ bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* d
   return r == CUDA_SUCCESS;
 }
 
-bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols, long long ld) {
+bool encode_tmap_residual(CUtensorMap* map, const void* base, bool f32, int rows, int cols,
+                          long long ld) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_encoder();
   if (!fn) return false;
   cuuint64_t d[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -350,7 +351,7 @@ bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols,
   cuuint32_t b[2] = {32, 32};
   cuuint32_t estr[2] = {1, 1};
   const CUresult r =
-      fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, d,
+      fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), d,
          st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
          f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;

@@ -177,7 +177,7 @@ struct DenseProduct {
   bool a_mn, b_mn;
   void* out;        // [M, N] dense
   bool out_f32;     // else bf16
-  bool out_tma;     // rows of out start on 16-byte boundaries (set by the launcher)
+  bool out_vec;     // rows of out start on 16-byte boundaries (set by the launcher)
   bool epilogue;    // bias, activation, residual, z kept
   int tiles;        // set by the launcher
 };
@@ -191,7 +191,7 @@ struct DenseParams {
   bool res_tma;          // set by the launcher
   long long ldr;
   void* pre;             // bf16 z [M, N] or null
-  bool pre_tma;          // set by the launcher
+  bool pre_vec;          // rows on 16-byte boundaries (set by the launcher)
   bool late;             // operands complete at the start: wait for the kernel before at the end
   int32_t* dev_status;
   long long wait_limit;
@@ -222,9 +222,10 @@ long long wait_limit();
 bool encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box);
 
-// [rows][cols] bf16 or f32, row stride ld elements, for TMA stores (and loads) of 32 rows x 32 columns
-// (bf16: 64-byte swizzle, f32: 128-byte)
-bool encode_tmap_out(CUtensorMap* map, void* base, bool f32, int rows, int cols, long long ld);
+// [rows][cols] bf16 or f32, row stride ld elements, for TMA loads of 32 rows x
+// 32 columns (bf16: 64-byte swizzle, f32: 128-byte)
+bool encode_tmap_residual(CUtensorMap* map, const void* base, bool f32, int rows, int cols,
+                          long long ld);
 
 // norm.cu
 int norm_bwd_blocks();  // partial rows of the weight and bias gradients
