@@ -231,3 +231,29 @@ def test_router_feeds_moe():
     (rw * per).sum().backward()
     err = (R.d(l.grad) - z.grad).norm() / z.grad.norm()
     assert err <= 1e-5, err
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,tg,k", [(128, 8, 4, 8), (256, 8, 2, 16), (256, 32, 16, 8), (512, 16, 8, 12),
+                                           (192, 8, 4, 8)])
+def test_groups_with_masks(E, groups, tg, k, scoring):
+    """Kept groups with fewer than k experts left: the row fills up from all
+    experts, lowest first, with weight 0; ties across and within groups."""
+    l, g = _logits(40, E, F, E + k, coarse=True)
+    gs = E // groups
+    low = torch.finfo(F).min
+    l[0] = NINF
+    l[1, 3:] = low                                     # three experts left
+    l[2] = NINF
+    l[2, E - 2:] = 1.0                                 # two, at the end
+    l[3, gs:] = float("nan")                           # one group left
+    for r in range(4, 20):                             # a random few left
+        keep = torch.randperm(E, generator=torch.Generator().manual_seed(r))[:r - 3]
+        row = torch.full((E,), low, device=DEV)
+        row[keep.to(DEV)] = l[r, keep.to(DEV)]
+        l[r] = row
+    ids, w = _check(l, k, scoring, groups=groups, topk_groups=tg)
+    if scoring == "softmax":
+        rid = R.select(l, k, scoring, None, groups, tg, True, 1.0)[0]
+        assert torch.equal(ids.cpu().long(), rid)
+    assert torch.equal(ids[0].cpu(), torch.arange(k, dtype=torch.int32)) and not w[0].any()

@@ -176,6 +176,90 @@ __device__ __forceinline__ void add_bias(const DenseParams& p, int c0, int N, fl
   }
 }
 
+// ---------------------------------------------------------------- staged stores
+// A warp's block of 32 rows x 128 bytes (64 bf16 or 32 f32 columns) in shared
+// memory, 16-byte columns XOR-ed by row: written a row per lane, read four rows
+// x 128 bytes per store instruction, without bank conflicts both ways.
+__device__ __forceinline__ void stage_f32(uint32_t stg, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st_shared_v4(stg + sw128_offset(lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+__device__ __forceinline__ void stage_bf16(uint32_t stg, int lane, int half, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    st_shared_v4(stg + sw128_offset(lane, 4 * half + c),
+                 __uint_as_float(cvt_bf16x2(v[8 * c], v[8 * c + 1])),
+                 __uint_as_float(cvt_bf16x2(v[8 * c + 2], v[8 * c + 3])),
+                 __uint_as_float(cvt_bf16x2(v[8 * c + 4], v[8 * c + 5])),
+                 __uint_as_float(cvt_bf16x2(v[8 * c + 6], v[8 * c + 7])));
+}
+// The staged block to columns c0 .. cend - 1 of rows row0.. (of M) of base [M, N].
+// vec: rows start on 16-byte boundaries.
+__device__ __forceinline__ void stage_flush(uint32_t stg, int lane, bool vec, void* base, bool f32,
+                                            int row0, int M, int N, int c0, int cend) {
+  __syncwarp();
+  const int per = f32 ? 32 : 64, size = f32 ? 4 : 2;
+  if (vec) {
+    const int kq = lane & 7, rq = lane >> 3;  // 16-byte column, first row
+    const int c = c0 + kq * (per / 8);
+    uint8_t* at = static_cast<uint8_t*>(base) + (static_cast<long long>(row0 + rq) * N + c) * size;
+    const long long step = 4LL * N * size;
+#pragma unroll
+    for (int j = 0; j < 8; ++j, at += step)
+      if (row0 + rq + 4 * j < M && c < cend)
+        *reinterpret_cast<float4*>(at) = ld_shared_v4(stg + sw128_offset(rq + 4 * j, kq));
+  } else {
+    // a row at a time, four bytes a lane (bf16: two elements, stored together
+    // where the rows start on 4-byte boundaries)
+    const bool even = !(N & 1) && (reinterpret_cast<uintptr_t>(base) & 3) == 0;
+    const int c = c0 + (f32 ? lane : 2 * lane);
+    if (c < cend) {
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        if (row0 + r >= M) break;
+        const uint32_t u = static_cast<uint32_t>(
+            ld_shared_s32(stg + sw128_offset(r, lane >> 2) + (lane & 3) * 4));
+        const long long o = static_cast<long long>(row0 + r) * N + c;
+        if (f32) {
+          static_cast<uint32_t*>(base)[o] = u;
+        } else {
+          unsigned short* at = static_cast<unsigned short*>(base) + o;
+          if (even && c + 1 < cend) {
+            *reinterpret_cast<uint32_t*>(at) = u;
+          } else {
+            at[0] = static_cast<unsigned short>(u);
+            if (c + 1 < cend) at[1] = static_cast<unsigned short>(u >> 16);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();  // the staging area is free again
+}
+// v += residual row `row`, columns c0.., read by the row's own lane
+__device__ __forceinline__ void add_residual_row(const DenseParams& p, int row, int c0, int N,
+                                                 float (&v)[32]) {
+  const long long ro = static_cast<long long>(row) * p.ldr + c0;
+  if (p.res_vec && !p.res_f32 && c0 + 32 <= N) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 x = q[c];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * c + 2 * j] += __uint_as_float(u[j] << 16);
+        v[8 * c + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (c0 + i < N) v[i] += load_any(p.residual, p.res_f32, ro + i);
+  }
+}
+
 // ---------------------------------------------------------------- pair kernel
 struct PairMaps {
   CUtensorMap a[2], b[2], res;
@@ -457,17 +541,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ epilogue
     // Four warps per 64 columns of the tile; a warp holds rows 32 (w % 4) ..
     // +31 of this CTA's 128 (the quarter of tensor memory that it can read),
-    // lane i row i.  A block of 128 bytes per row (64 bf16 or 32 f32 columns)
-    // is staged with its 16-byte columns XOR-ed by row (conflict-free both
-    // ways) and stored four rows x 128 bytes per instruction.  (Plain stores:
-    // TMA stores waited for the staging area to be read, 96 against 82 us for
-    // bias + GELU + z of 8192 x 64 x 8192; no difference at K = 2048.)
+    // lane i row i.  The results leave through staged blocks by plain stores
+    // (TMA stores waited for the staging area to be read, 96 against 82 us for
+    // bias + GELU + z of 8192 x 64 x 8192; no difference at K = 2048).
     const int quad = warp & 3, group = warp < 4 ? 0 : (warp - 2) >> 2;
     const int ew = group * 4 + quad;
     const uint32_t stg = m.sEpi + ew * EPI_WARP;
     const uint32_t res_bar = m.res_full + 8 * ew;
     const int row_w = static_cast<int>(rank) * kHalf + quad * 32;
-    const int kq = lane & 7, rq = lane >> 3;  // stores: 16-byte column, first row
     int tcount = 0, res_n = 0;
     bool res_open = false;  // a residual block is on its way
     for (int tau = pair; tau < total; tau += npairs) {
@@ -537,76 +618,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
         } else if (epi && p.residual && row < d.M) {
-          const long long ro = static_cast<long long>(row) * p.ldr + c0;
-          if (p.res_vec && !p.res_f32 && c0 + 32 <= d.N) {
-            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 x = q[c];
-              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                v[8 * c + 2 * j] += __uint_as_float(u[j] << 16);
-                v[8 * c + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c0 + i < d.N) v[i] += load_any(p.residual, p.res_f32, ro + i);
-          }
+          add_residual_row(p, row, c0, d.N, v);
         }
-      };
-      // lane's row, 16-byte columns c0.. of the staged block
-      auto put = [&](int c, uint32_t a, uint32_t b, uint32_t e, uint32_t f) {
-        st_shared_v4(stg + sw128_offset(lane, c), __uint_as_float(a), __uint_as_float(b),
-                     __uint_as_float(e), __uint_as_float(f));
-      };
-      auto put_bf16 = [&](int b, const float(&v)[32]) {  // half b of a block
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          put(4 * b + c, cvt_bf16x2(v[8 * c], v[8 * c + 1]), cvt_bf16x2(v[8 * c + 2], v[8 * c + 3]),
-              cvt_bf16x2(v[8 * c + 4], v[8 * c + 5]), cvt_bf16x2(v[8 * c + 6], v[8 * c + 7]));
-      };
-      // the staged block to columns c0.. (of `per` in the block) of rows row0..
-      auto flush = [&](bool vec, void* base, bool f32, int c0) {
-        __syncwarp();
-        const int per = f32 ? 32 : 64, size = f32 ? 4 : 2;
-        if (vec) {
-          const int c = c0 + kq * (per / 8);
-          uint8_t* at = static_cast<uint8_t*>(base) +
-                        (static_cast<long long>(row0 + rq) * d.N + c) * size;
-          const long long step = 4LL * d.N * size;
-#pragma unroll
-          for (int j = 0; j < 8; ++j, at += step)
-            if (row0 + rq + 4 * j < d.M && c < d.N)
-              *reinterpret_cast<float4*>(at) = ld_shared_v4(stg + sw128_offset(rq + 4 * j, kq));
-        } else {
-          // rows that do not start on 16-byte boundaries: a row at a time,
-          // consecutive elements in consecutive lanes
-          for (int r = 0; r < 32 && row0 + r < d.M; ++r)
-            for (int c = lane; c < per && c0 + c < d.N; c += 32) {
-              const long long o = static_cast<long long>(row0 + r) * d.N + c0 + c;
-              const uint32_t at = stg + sw128_offset(r, c / (per / 8));
-              if (f32) {
-                static_cast<float*>(base)[o] = __int_as_float(ld_shared_s32(at + (c & 3) * 4));
-              } else {
-                const uint32_t u = static_cast<uint32_t>(ld_shared_s32(at + ((c & 7) >> 1) * 4));
-                static_cast<unsigned short*>(base)[o] =
-                    static_cast<unsigned short>(c & 1 ? u >> 16 : u);
-              }
-            }
-        }
-        __syncwarp();  // the staging area is free again
       };
       if (epi && p.pre && nblk > 0) {
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
           float v[32];
           load(b, v);
-          put_bf16(b, v);
+          stage_bf16(stg, lane, b, v);
         }
-        flush(p.pre_vec, p.pre, false, col_w);
+        stage_flush(stg, lane, p.pre_vec, p.pre, false, row0, d.M, d.N, col_w, d.N);
       }
       if (d.out_f32) {
 #pragma unroll 1
@@ -616,11 +638,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (b == nblk - 1) release();
           act_res(b, v);
           __syncwarp();  // every lane has read its residual row
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            put(c, __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-          flush(d.out_vec, d.out, true, col_w + b * 32);
+          stage_f32(stg, lane, v);
+          stage_flush(stg, lane, d.out_vec, d.out, true, row0, d.M, d.N, col_w + b * 32, d.N);
         }
       } else if (nblk > 0) {
 #pragma unroll 1
@@ -629,9 +648,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           load(b, v);
           if (b == nblk - 1) release();
           act_res(b, v);
-          put_bf16(b, v);
+          stage_bf16(stg, lane, b, v);
         }
-        flush(d.out_vec, d.out, false, col_w);
+        stage_flush(stg, lane, d.out_vec, d.out, false, row0, d.M, d.N, col_w, d.N);
       }
       ++tcount;
     }
@@ -665,7 +684,7 @@ struct CtaParams {
   int b_bytes;     // B bytes per block
   int nacc;        // accumulators (1, 2 or 4), see the MMA loop
   int tmem_cols;
-  int vec_out, vec_pre, vec_res;  // accesses of 4 columns at once
+  int vec_out, vec_pre, vec_res;  // whole rows: 16-byte pieces; split tiles: 4 columns at once
 };
 constexpr int kCtaMeta = 256;
 constexpr int kMaxStages = 12;
@@ -924,7 +943,55 @@ __global__ void __launch_bounds__(kThreads)
   if (warp < 4) {
     const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
     tc_fence_after();
-    if (S == 1) {
+    if (S == 1 && !c.swap) {
+      // rows of the output: through staged blocks, over the pipeline's buffers
+      // (every MMA that read them is done)
+      const DenseProduct& d = c.d;
+      const uint32_t stg = base + warp * 4096;
+      const int row0 = m0 + warp * 32, cend = std::min(d.N, n0 + c.BN);
+      auto load32 = [&](int j, float(&v)[32]) {  // columns n0 + j .. with the bias
+        float h[16];
+        load16(j, h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = h[i], v[16 + i] = 0.f;
+        if (j + 16 < c.BN) {
+          load16(j + 16, h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[16 + i] = h[i];
+        }
+        if (d.epilogue && p.bias) add_bias(p, n0 + j, d.N, v);
+      };
+      const int per = d.out_f32 ? 32 : 64;
+      if (ok)
+#pragma unroll 1
+        for (int j0 = 0; j0 < c.BN && n0 + j0 < d.N; j0 += per) {
+          const int halves = std::min(per / 32, cdiv(c.BN - j0, 32));
+          if (d.epilogue && p.pre) {
+#pragma unroll 1
+            for (int h = 0; h < halves; ++h) {
+              float v[32];
+              load32(j0 + 32 * h, v);
+              stage_bf16(stg, lane, h, v);
+            }
+            stage_flush(stg, lane, c.vec_pre, p.pre, false, row0, d.M, d.N, n0 + j0,
+                        std::min(cend, n0 + j0 + per));
+          }
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {
+            float v[32];
+            load32(j0 + 32 * h, v);
+            if (d.epilogue) {
+              act_all<32>(p.act, v);
+              if (p.residual && row < d.M) add_residual_row(p, row, n0 + j0 + 32 * h, d.N, v);
+            }
+            if (d.out_f32)
+              stage_f32(stg, lane, v);
+            else
+              stage_bf16(stg, lane, h, v);
+          }
+          stage_flush(stg, lane, c.vec_out, d.out, d.out_f32, row0, d.M, d.N, n0 + j0, cend);
+        }
+    } else if (S == 1) {
       if (ok)
 #pragma unroll 1
         for (int j = 0; j < c.BN && n0 + j < c.Nc; j += 16) {
@@ -1201,8 +1268,9 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
 // 2048 x 2048 and 16 x 7168 x 2048 (a tile of 128 x BN takes 0.18 us + 1.7 ns
 // per column and block, 1.2 times that with two CTAs on an SM; joining the
 // pieces of a contraction costs 0.4 us + 36 ns per column, storing a tile
-// 0.5 us + 40 ns per column; a 256 x 256 tile on a pair 0.275 us a block and 1.85 us to
-// store).  BN up to 64 leaves room for two CTAs an SM.
+// 0.5 us + 40 ns per column, 0.4 us + 19 ns through staged blocks; a 256 x 256
+// tile on a pair 0.275 us a block and 1.2 us to store).  BN up to 64, or a few
+// blocks in all, leave room for two CTAs an SM.
 // Clusters of eight CTAs that fill an SM each found too few places (128 x
 // 2048 x 2048: 16 us against 8), so wider tiles split at most four ways, and
 // the widest not at all (its partial sums do not fit beside the ring).
@@ -1222,10 +1290,12 @@ CtaPlan plan_cta(const DenseProduct& d) {
       const long long tiles = static_cast<long long>(cdiv(mr, 128)) * cdiv(nc, bn);
       const int most = bn <= 64 ? 8 : bn == 128 ? 4 : 1;
       for (int s = 1; s <= most && s <= nkb; s *= 2) {
-        const long long ctas = tiles * s, slots = bn <= 64 ? 2LL * sms : sms;
+        const bool two = bn <= 64 || cdiv(nkb, s) * (OPER + 128 * bn) <= 110 * 1024;
+        const long long ctas = tiles * s, slots = two ? 2LL * sms : sms;
         const double rounds = static_cast<double>((ctas + slots - 1) / slots);
-        const double block = (0.18 + 0.0017 * bn) * (ctas > sms && bn <= 64 ? 1.2 : 1.0);
-        const double us = 2.2 + rounds * (cdiv(nkb, s) * block + 0.5 + 0.04 * bn) +
+        const double block = (0.18 + 0.0017 * bn) * (ctas > sms && two ? 1.2 : 1.0);
+        const double store = s == 1 && !swap ? 0.4 + 0.019 * bn : 0.5 + 0.04 * bn;
+        const double us = 2.2 + rounds * (cdiv(nkb, s) * block + store) +
                           (s > 1 ? 0.4 + 0.036 * bn : 0.0);
         if (us < best.us) best = CtaPlan{swap != 0, bn, s, us};
       }
@@ -1236,7 +1306,7 @@ CtaPlan plan_cta(const DenseProduct& d) {
 bool use_pairs(const DenseProduct& d) {
   const long long tiles = static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256);
   const long long pairs = num_sms() / 2;
-  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * (cdiv(d.Kc, BK) * 0.275 + 1.85);
+  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * (cdiv(d.Kc, BK) * 0.275 + 1.2);
   return us <= plan_cta(d).us;
 }
 
@@ -1290,8 +1360,9 @@ cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const
     const int bytes = f32 ? 16 : 8;
     return reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && ld % 4 == 0;
   };
-  c.vec_out = vec4(c.d.out, c.d.N, c.d.out_f32);
-  c.vec_pre = p.pre && vec4(p.pre, c.d.N, false);
+  const bool staged = c.splits == 1 && !c.swap;
+  c.vec_out = staged ? vec_rows(c.d.out, c.d.N, c.d.out_f32) : vec4(c.d.out, c.d.N, c.d.out_f32);
+  c.vec_pre = p.pre && (staged ? vec_rows(p.pre, c.d.N, false) : vec4(p.pre, c.d.N, false));
   c.vec_res = p.residual && vec4(p.residual, p.ldr, p.res_f32);
   CtaMaps maps;
   if (!tmap_operand(&maps.a, ra, c.d.a_mn, 128) || !tmap_operand(&maps.b, rb, c.d.b_mn, c.BN))

@@ -116,10 +116,11 @@ struct SelectArgs {
   bool vec, vec_bias;  // 16-byte loads
 };
 
-// Keys of the experts outside the topk_groups best groups become 1.
+// Keys of the experts outside the topk_groups best groups become 1.  Returns
+// the lanes whose experts stay, or 0 where the groups share lanes.
 template <int V>
-__device__ __forceinline__ void keep_groups(const SelectArgs& a, int e0, int lane,
-                                            uint32_t (&key)[V]) {
+__device__ __forceinline__ uint32_t keep_groups(const SelectArgs& a, int e0, int lane,
+                                                uint32_t (&key)[V]) {
   const int gs = a.E / a.groups;
   const int L = gs / V;  // lanes per group, where that divides evenly
   auto score = [&](uint32_t b1, uint32_t b2) {
@@ -150,7 +151,7 @@ __device__ __forceinline__ void keep_groups(const SelectArgs& a, int e0, int lan
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (!kept && e0 + i < a.E) key[i] = 1u;
-    return;
+    return __ballot_sync(kFull, kept);
   }
   // any other size: group by group, lane g keeps the score of group g
   uint32_t mine = 0u;
@@ -178,11 +179,84 @@ __device__ __forceinline__ void keep_groups(const SelectArgs& a, int e0, int lan
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if (e0 + i < a.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 1u;
+  return 0u;
 }
+
+// k rounds: the largest key, the lowest expert among equals; lane r keeps round
+// r's expert and key.  Returns the last round's key (the same in every lane).
+// e0: the lane's first expert, lanes in expert order.
+template <int V>
+__device__ __forceinline__ uint32_t top_k(uint32_t (&key)[V], int e0, int k, int lane, int& id_mine,
+                                          uint32_t& key_mine) {
+  uint32_t b = 0u;
+  if constexpr (V <= 8) {
+    // Each lane's keys in descending order (odd-even transposition with strict
+    // comparisons: equal keys keep their order), their places as 4-bit digits.
+    uint32_t place[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) place[i] = i;
+#pragma unroll
+    for (int r = 0; r < V; ++r)
+#pragma unroll
+      for (int i = r & 1; i + 1 < V; i += 2) {
+        const bool swap = key[i + 1] > key[i];
+        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+        const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
+        key[i] = hi, key[i + 1] = lo;
+        place[i] = ph, place[i + 1] = pl;
+      }
+    uint32_t places = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) places |= place[i] << (4 * i);
+    for (int r = 0; r < k; ++r) {
+      b = __reduce_max_sync(kFull, key[0]);
+      const int owner = __ffs(__ballot_sync(kFull, key[0] == b)) - 1;
+      const int id = __shfl_sync(kFull, e0 + static_cast<int>(places & 15u), owner);
+      if (lane == owner) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+        key[V - 1] = 0u;
+        places >>= 4;
+      }
+      if (lane == r) id_mine = id, key_mine = b;
+    }
+  } else {
+    uint32_t best = 0u;
+    auto rescan = [&]() {
+      best = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    };
+    rescan();
+    for (int r = 0; r < k; ++r) {
+      b = __reduce_max_sync(kFull, best);
+      const int owner = __ffs(__ballot_sync(kFull, best == b)) - 1;
+      int slot = 0;
+      if (lane == owner) {
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == b) slot = i;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i == slot) key[i] = 0u;
+        rescan();
+      }
+      const int id = __shfl_sync(kFull, e0 + slot, owner);
+      if (lane == r) id_mine = id, key_mine = b;
+    }
+  }
+  return b;
+}
+
+// Per warp: 32 V scores, and room to spread half of the keys.
+template <int V>
+constexpr bool kSpread = V >= 4 && V <= 16;  // (V = 32 would pass 48 KB a block)
+template <int V>
+constexpr int kRowFloats = 32 * V + (kSpread<V> ? 16 * V + 16 : 0);
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a) {
-  extern __shared__ float scores[];  // [kWarps][32 V]
+  extern __shared__ float scores[];  // [kWarps][kRowFloats]
   const int lane = threadIdx.x & 31;
   const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   pdl_trigger();
@@ -249,72 +323,40 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a)
   for (int i = 0; i < V; ++i)
     if (e0 + i >= E) key[i] = 0u;  // no expert here
 
-  if (a.groups > 1) keep_groups<V>(a, e0, lane, key);
+  const uint32_t kept = a.groups > 1 ? keep_groups<V>(a, e0, lane, key) : 0u;
 
   // the scores where every lane can read them
-  float* row = scores + (threadIdx.x >> 5) * (32 * V);
+  float* row = scores + (threadIdx.x >> 5) * kRowFloats<V>;
 #pragma unroll
   for (int i = 0; i < V; ++i) row[e0 + i] = p[i];
 
-  // k rounds: the largest key, the lowest expert among equals
   int id_mine = 0;
   uint32_t key_mine = 0u;
-  if constexpr (V <= 8) {
-    // Each lane's keys in descending order (odd-even transposition with strict
-    // comparisons: equal keys keep their order), their places as 4-bit digits.
-    uint32_t place[V];
+  bool done = false;
+  if constexpr (kSpread<V>) {
+    if (kept && __popc(kept) <= 16) {
+      // At most half of the lanes hold experts that stay: spread those over all
+      // of them, half as many keys each.
+      constexpr int VC = V / 2;
+      uint32_t* keys = reinterpret_cast<uint32_t*>(row + 32 * V);
+      int* first = reinterpret_cast<int*>(keys + 16 * V);
+      const int rank = __popc(kept & ((1u << lane) - 1u)), n = __popc(kept);
+      if ((kept >> lane) & 1u) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) place[i] = i;
-#pragma unroll
-    for (int r = 0; r < V; ++r)
-#pragma unroll
-      for (int i = r & 1; i + 1 < V; i += 2) {
-        const bool swap = key[i + 1] > key[i];
-        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
-        const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
-        key[i] = hi, key[i + 1] = lo;
-        place[i] = ph, place[i + 1] = pl;
+        for (int i = 0; i < V; ++i) keys[rank * V + i] = key[i];
+        first[rank] = e0;
       }
-    uint32_t places = 0u;
+      __syncwarp();
+      uint32_t half[VC];
+      const bool has = lane / 2 < n;
 #pragma unroll
-    for (int i = 0; i < V; ++i) places |= place[i] << (4 * i);
-    for (int r = 0; r < a.k; ++r) {
-      const uint32_t b = __reduce_max_sync(kFull, key[0]);
-      const int owner = __ffs(__ballot_sync(kFull, key[0] == b)) - 1;
-      const int id = __shfl_sync(kFull, e0 + static_cast<int>(places & 15u), owner);
-      if (lane == owner) {
-#pragma unroll
-        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-        key[V - 1] = 0u;
-        places >>= 4;
-      }
-      if (lane == r) id_mine = id, key_mine = b;
-    }
-  } else {
-    uint32_t best = 0u;
-    auto rescan = [&]() {
-      best = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) best = max(best, key[i]);
-    };
-    rescan();
-    for (int r = 0; r < a.k; ++r) {
-      const uint32_t b = __reduce_max_sync(kFull, best);
-      const int owner = __ffs(__ballot_sync(kFull, best == b)) - 1;
-      int slot = 0;
-      if (lane == owner) {
-#pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-          if (key[i] == b) slot = i;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i == slot) key[i] = 0u;
-        rescan();
-      }
-      const int id = __shfl_sync(kFull, e0 + slot, owner);
-      if (lane == r) id_mine = id, key_mine = b;
+      for (int i = 0; i < VC; ++i) half[i] = has ? keys[lane * VC + i] : 0u;
+      const int h0 = has ? first[lane / 2] + (lane & 1) * VC : 0;
+      // (fewer than k that can be chosen on their merits: over all experts below)
+      done = top_k<VC>(half, h0, a.k, lane, id_mine, key_mine) > 1u;
     }
   }
+  if (!done) top_k<V>(key, e0, a.k, lane, id_mine, key_mine);
   __syncwarp();
   float w_mine = lane < a.k && key_mine > 1u ? row[id_mine] : 0.f;
   if (a.renorm) {
@@ -460,15 +502,19 @@ __global__ void __launch_bounds__(kWarps * 32) select_bwd_kernel(const SelectBwd
 }
 
 size_t row_smem(int v) { return static_cast<size_t>(kWarps) * 32 * v * 4; }
+template <typename T, int V>
+cudaError_t select_tv(const SelectArgs& a, cudaStream_t st) {
+  return launch_pdl(select_kernel<T, V>, dim3(cdiv(a.T, kWarps)), dim3(kWarps * 32),
+                    kWarps * kRowFloats<V> * sizeof(float), st, a);
+}
 template <typename T>
 cudaError_t select_t(const SelectArgs& a, cudaStream_t st) {
-  const dim3 grid(cdiv(a.T, kWarps)), block(kWarps * 32);
-  if (a.E <= 32) return launch_pdl(select_kernel<T, 1>, grid, block, row_smem(1), st, a);
-  if (a.E <= 64) return launch_pdl(select_kernel<T, 2>, grid, block, row_smem(2), st, a);
-  if (a.E <= 128) return launch_pdl(select_kernel<T, 4>, grid, block, row_smem(4), st, a);
-  if (a.E <= 256) return launch_pdl(select_kernel<T, 8>, grid, block, row_smem(8), st, a);
-  if (a.E <= 512) return launch_pdl(select_kernel<T, 16>, grid, block, row_smem(16), st, a);
-  return launch_pdl(select_kernel<T, 32>, grid, block, row_smem(32), st, a);
+  if (a.E <= 32) return select_tv<T, 1>(a, st);
+  if (a.E <= 64) return select_tv<T, 2>(a, st);
+  if (a.E <= 128) return select_tv<T, 4>(a, st);
+  if (a.E <= 256) return select_tv<T, 8>(a, st);
+  if (a.E <= 512) return select_tv<T, 16>(a, st);
+  return select_tv<T, 32>(a, st);
 }
 template <typename T>
 cudaError_t select_bwd_t(const SelectBwdArgs& a, cudaStream_t st) {
