@@ -237,27 +237,49 @@ __device__ __forceinline__ void stage_flush(uint32_t stg, int lane, bool vec, vo
   }
   __syncwarp();  // the staging area is free again
 }
-// v += residual row `row`, columns c0.., read by the row's own lane
-__device__ __forceinline__ void add_residual_row(const DenseParams& p, int row, int c0, int N,
-                                                 float (&v)[32]) {
-  const long long ro = static_cast<long long>(row) * p.ldr + c0;
-  if (p.res_vec && !p.res_f32 && c0 + 32 <= N) {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
+// v += residual, rows row0.. (of M), columns c0 .. c0 + 31 (below N): read with
+// consecutive lanes on consecutive elements into the staging area as f32, then
+// each lane takes its own row.
+__device__ __forceinline__ void add_residual(const DenseParams& p, uint32_t stg, int lane, int row0,
+                                             int M, int c0, int N, float (&v)[32]) {
+  if (p.res_vec && N % 4 == 0) {
+    // four columns a lane, four rows per instruction
+    const int kq = lane & 7, c = c0 + 4 * kq, rq = lane >> 3;
+    const long long o = static_cast<long long>(row0 + rq) * p.ldr + c;
+    float4 x[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint4 x = q[c];
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * c + 2 * j] += __uint_as_float(u[j] << 16);
-        v[8 * c + 2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+    for (int j = 0; j < 8; ++j) {
+      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row0 + rq + 4 * j < M && c < N) {
+        if (p.res_f32) {
+          x[j] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + o + 4 * j * p.ldr);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(
+              static_cast<const __nv_bfloat16*>(p.residual) + o + 4 * j * p.ldr);
+          x[j] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                             __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+        }
       }
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c0 + i < N) v[i] += load_any(p.residual, p.res_f32, ro + i);
+    for (int j = 0; j < 8; ++j)
+      st_shared_v4(stg + sw128_offset(rq + 4 * j, kq), x[j].x, x[j].y, x[j].z, x[j].w);
+  } else {
+    const int c = c0 + lane;
+    const long long o = static_cast<long long>(row0) * p.ldr + c;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const float x = row0 + r < M && c < N ? load_any(p.residual, p.res_f32, o + r * p.ldr) : 0.f;
+      st_shared_f32(stg + sw128_offset(r, lane >> 2) + (lane & 3) * 4, x);
+    }
   }
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float4 x = ld_shared_v4(stg + sw128_offset(lane, c));
+    v[4 * c] += x.x, v[4 * c + 1] += x.y, v[4 * c + 2] += x.z, v[4 * c + 3] += x.w;
+  }
+  __syncwarp();  // the staging area is free again
 }
 
 // ---------------------------------------------------------------- pair kernel
@@ -555,15 +577,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const PTile t = decode_pair(p, tau);
       const DenseProduct& d = p.pr[t.q];
       const int row0 = t.m0 + row_w;
-      const int row = row0 + lane;
       const int acc = tcount & 1;
       const int col_w = t.n0 + group * 64;  // first column of this warp
       const int nblk = std::max(0, std::min(2, cdiv(d.N - col_w, 32)));  // 32-column blocks
       const bool epi = d.epilogue;
       // To an f32 output the residual's 32 x 32 block comes by TMA into the
       // staging area that the result then takes: the first one while the tile
-      // is multiplied, unless z passes through the staging area before.  (A
-      // bf16 block holds two of them, so there each lane reads its own row.)
+      // is multiplied, unless z passes through the staging area before.  A
+      // bf16 output with a residual leaves 32 columns at a time (the residual's
+      // block takes the whole staging area).
       const bool res_tma = epi && p.res_tma && row0 < d.M;
       auto fetch_res = [&](int c0) {
         __syncwarp();  // the staging area has been read
@@ -617,8 +639,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               }
             }
           }
-        } else if (epi && p.residual && row < d.M) {
-          add_residual_row(p, row, c0, d.N, v);
+        } else if (epi && p.residual) {
+          add_residual(p, stg, lane, row0, d.M, c0, d.N, v);
         }
       };
       if (epi && p.pre && nblk > 0) {
@@ -642,15 +664,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           stage_flush(stg, lane, d.out_vec, d.out, true, row0, d.M, d.N, col_w + b * 32, d.N);
         }
       } else if (nblk > 0) {
+        const bool by_half = epi && p.residual;
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
           float v[32];
           load(b, v);
           if (b == nblk - 1) release();
           act_res(b, v);
-          stage_bf16(stg, lane, b, v);
+          stage_bf16(stg, lane, by_half ? 0 : b, v);
+          if (by_half)
+            stage_flush(stg, lane, d.out_vec, d.out, false, row0, d.M, d.N, col_w + 32 * b,
+                        std::min(d.N, col_w + 32 * b + 32));
         }
-        stage_flush(stg, lane, d.out_vec, d.out, false, row0, d.M, d.N, col_w, d.N);
+        if (!by_half)
+          stage_flush(stg, lane, d.out_vec, d.out, false, row0, d.M, d.N, col_w, d.N);
       }
       ++tcount;
     }
@@ -807,7 +834,7 @@ __device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p
 }
 
 template <bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     dense_cta_kernel(const __grid_constant__ CtaMaps maps, const __grid_constant__ CtaParams c,
                      const __grid_constant__ DenseParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -945,7 +972,7 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_after();
     if (S == 1 && !c.swap) {
       // rows of the output: through staged blocks, over the pipeline's buffers
-      // (every MMA that read them is done)
+      // (every MMA that read them is done); the residual's blocks beside them
       const DenseProduct& d = c.d;
       const uint32_t stg = base + warp * 4096;
       const int row0 = m0 + warp * 32, cend = std::min(d.N, n0 + c.BN);
@@ -982,7 +1009,8 @@ __global__ void __launch_bounds__(kThreads)
             load32(j0 + 32 * h, v);
             if (d.epilogue) {
               act_all<32>(p.act, v);
-              if (p.residual && row < d.M) add_residual_row(p, row, n0 + j0 + 32 * h, d.N, v);
+              if (p.residual)
+                add_residual(p, stg + 16384, lane, row0, d.M, n0 + j0 + 32 * h, d.N, v);
             }
             if (d.out_f32)
               stage_f32(stg, lane, v);
@@ -1056,8 +1084,8 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------- backward prep
 // dz = bf16(dy act'(pre)) [T, ldz] in one pass, and the column sums of the
 // unrounded dz over each block's rows: part[blockIdx.y][N].  Bound by its
-// bytes: 16-byte pieces of eight columns per thread (VEC = 8) wherever rows
-// start on 16-byte boundaries.  A block is `lanes` threads along the columns
+// bytes: pieces of eight columns per thread (VEC = 8) where rows start on their
+// boundaries, else of four, two or one.  A block is `lanes` threads along the columns
 // and 256 / lanes rows; its partial sums add up in shared memory in row order.
 struct DzArgs {
   const void* dy;
@@ -1074,6 +1102,22 @@ struct Piece {
   T v;
 };
 template <>
+struct Piece<__nv_bfloat16, 2> {
+  uint32_t q;
+};
+template <>
+struct Piece<float, 2> {
+  float2 q;
+};
+template <>
+struct Piece<__nv_bfloat16, 4> {
+  uint2 q;
+};
+template <>
+struct Piece<float, 4> {
+  float4 q;
+};
+template <>
 struct Piece<__nv_bfloat16, 8> {
   uint4 q;
 };
@@ -1084,13 +1128,11 @@ struct Piece<float, 8> {
 template <typename T, int VEC>
 __device__ __forceinline__ Piece<T, VEC> load_piece(const T* p) {
   Piece<T, VEC> r;
-  if constexpr (VEC == 1) {
-    r.v = *p;
-  } else if constexpr (sizeof(T) == 2) {
-    r.q = *reinterpret_cast<const uint4*>(p);
-  } else {
+  if constexpr (VEC == 8 && sizeof(T) == 4) {
     r.q[0] = reinterpret_cast<const float4*>(p)[0];
     r.q[1] = reinterpret_cast<const float4*>(p)[1];
+  } else {
+    r = *reinterpret_cast<const Piece<T, VEC>*>(p);
   }
   return r;
 }
@@ -1099,16 +1141,29 @@ __device__ __forceinline__ void floats(const Piece<T, VEC>& r, float (&v)[VEC]) 
   if constexpr (VEC == 1) {
     v[0] = static_cast<float>(r.v);
   } else if constexpr (sizeof(T) == 2) {
-    const uint32_t u[4] = {r.q.x, r.q.y, r.q.z, r.q.w};
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < VEC / 2; ++j) {
       v[2 * j] = __uint_as_float(u[j] << 16);
       v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
     }
   } else {
-    v[0] = r.q[0].x, v[1] = r.q[0].y, v[2] = r.q[0].z, v[3] = r.q[0].w;
-    v[4] = r.q[1].x, v[5] = r.q[1].y, v[6] = r.q[1].z, v[7] = r.q[1].w;
+    const float* f = reinterpret_cast<const float*>(&r);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = f[j];
   }
+}
+template <int VEC>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* o, const float (&v)[VEC]) {
+  if constexpr (VEC == 1)
+    *o = __float2bfloat16_rn(v[0]);
+  else if constexpr (VEC == 2)
+    *reinterpret_cast<uint32_t*>(o) = cvt_bf16x2(v[0], v[1]);
+  else if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(o) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+  else
+    *reinterpret_cast<uint4*>(o) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                              cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
 }
 template <int ACT, typename DT, int VEC>
 __global__ void __launch_bounds__(256, 4) dense_dz_kernel(const DzArgs a) {
@@ -1124,7 +1179,7 @@ __global__ void __launch_bounds__(256, 4) dense_dz_kernel(const DzArgs a) {
   if (n < a.N) {
     // rows in batches whose loads are all issued before the first is used
     // (the stores to dz keep the compiler from moving later loads up)
-    constexpr int U = sizeof(DT) == 4 && VEC == 8 ? 2 : 4;
+    constexpr int U = VEC == 1 ? 8 : sizeof(DT) == 4 && VEC == 8 ? 2 : 4;
     for (int tb = t0 + ry; tb < t1; tb += U * nr) {
       Piece<DT, VEC> dy[U];
       Piece<__nv_bfloat16, VEC> pre[U];
@@ -1148,15 +1203,7 @@ __global__ void __launch_bounds__(256, 4) dense_dz_kernel(const DzArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum[i] += v[i];
-        if (a.dz) {
-          __nv_bfloat16* o = a.dz + static_cast<long long>(t) * a.ldz + n;
-          if constexpr (VEC == 1)
-            *o = __float2bfloat16_rn(v[0]);
-          else
-            *reinterpret_cast<uint4*>(o) =
-                make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
-                           cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
-        }
+        if (a.dz) store_bf16<VEC>(a.dz + static_cast<long long>(t) * a.ldz + n, v);
       }
     }
   }
@@ -1377,9 +1424,9 @@ cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const
 struct DzPlan {
   int vec, lanes, bx, by, rows;
 };
-DzPlan plan_dz(int T, int N, bool vec) {
+DzPlan plan_dz(int T, int N, int vec) {
   DzPlan p;
-  p.vec = vec ? 8 : 1;
+  p.vec = vec;
   p.lanes = 32;
   while (p.lanes > 1 && (p.lanes / 2) * p.vec >= N) p.lanes /= 2;
   p.bx = cdiv(N, p.lanes * p.vec);
@@ -1390,18 +1437,23 @@ DzPlan plan_dz(int T, int N, bool vec) {
   return p;
 }
 int max_partials(int T, int N) {
-  return std::max(plan_dz(T, N, true).by, plan_dz(T, N, false).by);
+  int n = 1;
+  for (int vec : {1, 2, 4, 8}) n = std::max(n, plan_dz(T, N, vec).by);
+  return n;
 }
 
+template <int ACT, int VEC>
+cudaError_t launch_dz_v(const DzPlan& pl, const DzArgs& a, bool dy_f32, cudaStream_t st) {
+  const dim3 grid(pl.bx, pl.by), block(256);
+  return dy_f32 ? launch_pdl(dense_dz_kernel<ACT, float, VEC>, grid, block, 0, st, a)
+                : launch_pdl(dense_dz_kernel<ACT, __nv_bfloat16, VEC>, grid, block, 0, st, a);
+}
 template <int ACT>
 cudaError_t launch_dz(const DzPlan& pl, const DzArgs& a, bool dy_f32, cudaStream_t st) {
-  const dim3 grid(pl.bx, pl.by), block(256);
-  using B = __nv_bfloat16;
-  if (pl.vec == 8)
-    return dy_f32 ? launch_pdl(dense_dz_kernel<ACT, float, 8>, grid, block, 0, st, a)
-                  : launch_pdl(dense_dz_kernel<ACT, B, 8>, grid, block, 0, st, a);
-  return dy_f32 ? launch_pdl(dense_dz_kernel<ACT, float, 1>, grid, block, 0, st, a)
-                : launch_pdl(dense_dz_kernel<ACT, B, 1>, grid, block, 0, st, a);
+  if (pl.vec == 8) return launch_dz_v<ACT, 8>(pl, a, dy_f32, st);
+  if (pl.vec == 4) return launch_dz_v<ACT, 4>(pl, a, dy_f32, st);
+  if (pl.vec == 2) return launch_dz_v<ACT, 2>(pl, a, dy_f32, st);
+  return launch_dz_v<ACT, 1>(pl, a, dy_f32, st);
 }
 
 bool dy_is_operand(const DenseBackward& a) {
@@ -1441,7 +1493,9 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
   cudaError_t e = cudaSuccess;
   int parts = 0;
   if (dz_out || part_out) {
-    const bool vec = a.N % 8 == 0 && a.lddy % 8 == 0 && aligned16(a.dy) && aligned16(a.pre);
+    // the widest pieces that every row of dy and z starts on
+    int vec = 8;
+    while (vec > 1 && (a.N % vec || a.lddy % vec || !aligned16(a.dy) || !aligned16(a.pre))) vec /= 2;
     const DzPlan pl = plan_dz(a.T, a.N, vec);
     parts = pl.by;
     const DzArgs z{a.dy, a.lddy,  static_cast<const __nv_bfloat16*>(a.pre), a.T, a.N, pl.rows,

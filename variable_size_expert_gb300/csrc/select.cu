@@ -14,7 +14,7 @@
 // only when nothing else is left, lowest index first, with weight 0, so that
 // the k ids are always valid and distinct.
 //
-// Each lane holds V consecutive experts in registers.  The kernel is bound by
+// Up to 256 experts each lane holds V consecutive ones in registers.  The kernel is bound by
 // instruction issue, not by its bytes (1 KB per token at E = 256), so the work
 // per round of the top-k is what counts: up to V = 8 a lane sorts its keys once
 // and a round pops the winner's list.
@@ -188,69 +188,44 @@ __device__ __forceinline__ uint32_t keep_groups(const SelectArgs& a, int e0, int
 template <int V>
 __device__ __forceinline__ uint32_t top_k(uint32_t (&key)[V], int e0, int k, int lane, int& id_mine,
                                           uint32_t& key_mine) {
+  static_assert(V <= 8, "4-bit places");
   uint32_t b = 0u;
-  if constexpr (V <= 8) {
-    // Each lane's keys in descending order (odd-even transposition with strict
-    // comparisons: equal keys keep their order), their places as 4-bit digits.
-    uint32_t place[V];
+  // Each lane's keys in descending order (odd-even transposition with strict
+  // comparisons: equal keys keep their order), their places as 4-bit digits.
+  uint32_t place[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) place[i] = i;
+  for (int i = 0; i < V; ++i) place[i] = i;
 #pragma unroll
-    for (int r = 0; r < V; ++r)
+  for (int r = 0; r < V; ++r)
 #pragma unroll
-      for (int i = r & 1; i + 1 < V; i += 2) {
-        const bool swap = key[i + 1] > key[i];
-        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
-        const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
-        key[i] = hi, key[i + 1] = lo;
-        place[i] = ph, place[i + 1] = pl;
-      }
-    uint32_t places = 0u;
-#pragma unroll
-    for (int i = 0; i < V; ++i) places |= place[i] << (4 * i);
-    for (int r = 0; r < k; ++r) {
-      b = __reduce_max_sync(kFull, key[0]);
-      const int owner = __ffs(__ballot_sync(kFull, key[0] == b)) - 1;
-      const int id = __shfl_sync(kFull, e0 + static_cast<int>(places & 15u), owner);
-      if (lane == owner) {
-#pragma unroll
-        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-        key[V - 1] = 0u;
-        places >>= 4;
-      }
-      if (lane == r) id_mine = id, key_mine = b;
+    for (int i = r & 1; i + 1 < V; i += 2) {
+      const bool swap = key[i + 1] > key[i];
+      const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+      const uint32_t ph = swap ? place[i + 1] : place[i], pl = swap ? place[i] : place[i + 1];
+      key[i] = hi, key[i + 1] = lo;
+      place[i] = ph, place[i + 1] = pl;
     }
-  } else {
-    uint32_t best = 0u;
-    auto rescan = [&]() {
-      best = key[0];
+  uint32_t places = 0u;
 #pragma unroll
-      for (int i = 1; i < V; ++i) best = max(best, key[i]);
-    };
-    rescan();
-    for (int r = 0; r < k; ++r) {
-      b = __reduce_max_sync(kFull, best);
-      const int owner = __ffs(__ballot_sync(kFull, best == b)) - 1;
-      int slot = 0;
-      if (lane == owner) {
+  for (int i = 0; i < V; ++i) places |= place[i] << (4 * i);
+  for (int r = 0; r < k; ++r) {
+    b = __reduce_max_sync(kFull, key[0]);
+    const int owner = __ffs(__ballot_sync(kFull, key[0] == b)) - 1;
+    const int id = __shfl_sync(kFull, e0 + static_cast<int>(places & 15u), owner);
+    if (lane == owner) {
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-          if (key[i] == b) slot = i;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i == slot) key[i] = 0u;
-        rescan();
-      }
-      const int id = __shfl_sync(kFull, e0 + slot, owner);
-      if (lane == r) id_mine = id, key_mine = b;
+      for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+      key[V - 1] = 0u;
+      places >>= 4;
     }
+    if (lane == r) id_mine = id, key_mine = b;
   }
   return b;
 }
 
 // Per warp: 32 V scores, and room to spread half of the keys.
 template <int V>
-constexpr bool kSpread = V >= 4 && V <= 16;  // (V = 32 would pass 48 KB a block)
+constexpr bool kSpread = V >= 4;
 template <int V>
 constexpr int kRowFloats = 32 * V + (kSpread<V> ? 16 * V + 16 : 0);
 
@@ -366,6 +341,114 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a)
   if (lane < a.k) {
     a.ids[t * a.k + lane] = id_mine;
     a.weights[t * a.k + lane] = w_mine * a.scale;
+  }
+}
+
+// More than 256 experts: the scores and keys of a token in shared memory, lane l
+// with experts l, l + 32, ...  Loops instead of unrolled registers: the code of
+// 32 experts per lane did not fit the instruction cache (13 us for 32 tokens).
+constexpr int kWideWarps = 4;
+template <typename T>
+__global__ void __launch_bounds__(kWideWarps * 32) select_wide_kernel(const SelectArgs a) {
+  extern __shared__ float wide[];  // [kWideWarps][2][E]
+  const int lane = threadIdx.x & 31, E = a.E;
+  const long long t = static_cast<long long>(blockIdx.x) * kWideWarps + (threadIdx.x >> 5);
+  pdl_trigger();
+  pdl_wait();
+  if (t >= a.T) return;
+  float* p = wide + (threadIdx.x >> 5) * 2 * E;
+  uint32_t* key = reinterpret_cast<uint32_t*>(p + E);
+  const T* lr = static_cast<const T*>(a.logits) + t * a.ldl;
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {
+    const float l = open_logit<T>(lr[e]);
+    p[e] = l;
+    top = fmaxf(top, l);
+  }
+  float inv = 1.f;
+  if (a.softmax) {
+    top = warp_max(top);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32) sum += p[e] > -INFINITY ? expf(p[e] - top) : 0.f;
+    sum = warp_sum(sum);
+    inv = sum > 0.f ? 1.f / sum : 0.f;
+  }
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {
+    const float l = p[e], bias = a.bias ? a.bias[e] : 0.f;
+    float s;
+    if (a.softmax) {
+      s = l > -INFINITY ? expf(l - top) * inv : 0.f;
+    } else {
+      s = __frcp_rn(1.f + expf(-l));
+      if (l < -87.f) s = expf(l);  // (as above)
+    }
+    p[e] = s;
+    key[e] = order_key(l > -INFINITY ? (a.softmax && !a.bias ? l : s + bias) : l);
+  }
+  __syncwarp();
+  if (a.groups > 1) {
+    // group by group, lane g keeps the score of group g
+    const int gs = E / a.groups;
+    uint32_t mine = 0u;
+    for (int g = 0; g < a.groups; ++g) {
+      uint32_t x = 0u, y = 0u;
+      for (int i = lane; i < gs; i += 32) {
+        const uint32_t u = key[g * gs + i];
+        y = max(y, min(x, u));
+        x = max(x, u);
+      }
+      const uint32_t b1 = __reduce_max_sync(kFull, x);
+      const int owner = __ffs(__ballot_sync(kFull, x == b1)) - 1;
+      const uint32_t b2 = __reduce_max_sync(kFull, lane == owner ? y : x);
+      if (lane == g)
+        mine = !a.softmax && b1 > 1u && b2 > 1u ? order_key(key_value(b1) + key_value(b2)) : b1;
+    }
+    uint32_t kept = 0u;
+    for (int r = 0; r < a.topk_groups; ++r) {
+      const uint32_t b = __reduce_max_sync(kFull, mine);
+      const int g = __ffs(__ballot_sync(kFull, mine == b)) - 1;
+      kept |= 1u << g;
+      if (lane == g) mine = 0u;
+    }
+    for (int g = 0; g < a.groups; ++g)
+      if (!((kept >> g) & 1u))
+        for (int i = lane; i < gs; i += 32) key[g * gs + i] = 1u;
+    __syncwarp();
+  }
+  // k rounds; a lane's best: its largest key, the lowest expert among equals
+  uint32_t best = 0u;
+  int at = 0;
+  auto rescan = [&]() {
+    best = 0u;
+#pragma unroll 8
+    for (int e = lane; e < E; e += 32) {
+      const uint32_t u = key[e];
+      if (u > best) best = u, at = e;
+    }
+  };
+  rescan();
+  int id_mine = 0;
+  uint32_t key_mine = 0u;
+  for (int r = 0; r < a.k; ++r) {
+    const uint32_t b = __reduce_max_sync(kFull, best);
+    const int id = static_cast<int>(__reduce_min_sync(kFull, best == b ? static_cast<unsigned>(at) : ~0u));
+    if (lane == (id & 31)) {
+      key[id] = 0u;
+      rescan();
+    }
+    if (lane == r) id_mine = id, key_mine = b;
+  }
+  float w = lane < a.k && key_mine > 1u ? p[id_mine] : 0.f;
+  if (a.renorm) {
+    const float tot = warp_sum(w);
+    w = tot > 0.f ? w / tot : 0.f;
+  }
+  if (lane < a.k) {
+    a.ids[t * a.k + lane] = id_mine;
+    a.weights[t * a.k + lane] = w * a.scale;
   }
 }
 
@@ -513,8 +596,8 @@ cudaError_t select_t(const SelectArgs& a, cudaStream_t st) {
   if (a.E <= 64) return select_tv<T, 2>(a, st);
   if (a.E <= 128) return select_tv<T, 4>(a, st);
   if (a.E <= 256) return select_tv<T, 8>(a, st);
-  if (a.E <= 512) return select_tv<T, 16>(a, st);
-  return select_tv<T, 32>(a, st);
+  return launch_pdl(select_wide_kernel<T>, dim3(cdiv(a.T, kWideWarps)), dim3(kWideWarps * 32),
+                    static_cast<size_t>(kWideWarps) * 2 * a.E * sizeof(float), st, a);
 }
 template <typename T>
 cudaError_t select_bwd_t(const SelectBwdArgs& a, cudaStream_t st) {
