@@ -215,21 +215,32 @@ __device__ __forceinline__ void stage_flush(uint32_t stg, int lane, bool vec, vo
     const bool even = !(N & 1) && (reinterpret_cast<uintptr_t>(base) & 3) == 0;
     const int c = c0 + (f32 ? lane : 2 * lane);
     if (c < cend) {
-#pragma unroll 8
-      for (int r = 0; r < 32; ++r) {
-        if (row0 + r >= M) break;
-        const uint32_t u = static_cast<uint32_t>(
-            ld_shared_s32(stg + sw128_offset(r, lane >> 2) + (lane & 3) * 4));
-        const long long o = static_cast<long long>(row0 + r) * N + c;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32 && row0 + r0 < M; r0 += 8) {
+        uint32_t u[8];  // (read together: a store holds the next read back)
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          u[r] = static_cast<uint32_t>(
+              ld_shared_s32(stg + sw128_offset(r0 + r, lane >> 2) + (lane & 3) * 4));
+        const long long o = static_cast<long long>(row0 + r0) * N + c;
+        const int rows = std::min(8, M - row0 - r0);
         if (f32) {
-          static_cast<uint32_t*>(base)[o] = u;
+          uint32_t* at = static_cast<uint32_t*>(base) + o;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < rows) at[static_cast<long long>(r) * N] = u[r];
         } else {
           unsigned short* at = static_cast<unsigned short*>(base) + o;
-          if (even && c + 1 < cend) {
-            *reinterpret_cast<uint32_t*>(at) = u;
-          } else {
-            at[0] = static_cast<unsigned short>(u);
-            if (c + 1 < cend) at[1] = static_cast<unsigned short>(u >> 16);
+          const bool two = c + 1 < cend;
+#pragma unroll
+          for (int r = 0; r < 8; ++r, at += N) {
+            if (r >= rows) continue;
+            if (even && two) {
+              *reinterpret_cast<uint32_t*>(at) = u[r];
+            } else {
+              at[0] = static_cast<unsigned short>(u[r]);
+              if (two) at[1] = static_cast<unsigned short>(u[r] >> 16);
+            }
           }
         }
       }
@@ -267,10 +278,15 @@ __device__ __forceinline__ void add_residual(const DenseParams& p, uint32_t stg,
   } else {
     const int c = c0 + lane;
     const long long o = static_cast<long long>(row0) * p.ldr + c;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-      const float x = row0 + r < M && c < N ? load_any(p.residual, p.res_f32, o + r * p.ldr) : 0.f;
-      st_shared_f32(stg + sw128_offset(r, lane >> 2) + (lane & 3) * 4, x);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      float x[16];  // (loaded together: a shared store holds the next load back)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        x[r] = row0 + r0 + r < M && c < N ? load_any(p.residual, p.res_f32, o + (r0 + r) * p.ldr) : 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        st_shared_f32(stg + sw128_offset(r0 + r, lane >> 2) + (lane & 3) * 4, x[r]);
     }
   }
   __syncwarp();
@@ -713,9 +729,9 @@ struct CtaParams {
   int tmem_cols;
   int vec_out, vec_pre, vec_res;  // whole rows: 16-byte pieces; split tiles: 4 columns at once
 };
-constexpr int kCtaMeta = 256;
+constexpr int kCtaMeta = 256 + 1024;  // barriers, the tile's biases
 constexpr int kMaxStages = 12;
-static_assert(8 * (kMaxStages + kGroups + 2) + 8 <= kCtaMeta, "barrier area");
+static_assert(8 * (kMaxStages + kGroups + 2) + 8 <= 256, "barrier area");
 static_assert(releases_fit(kMaxStages, 2) && releases_fit(7, 1) && releases_fit(3, 0),
               "release barriers");  // (the group sizes that launch_cta picks)
 size_t cta_smem(const CtaParams& c) {
@@ -742,8 +758,41 @@ __device__ __forceinline__ void st_async_v4(uint32_t dst, uint32_t bar, float a,
 
 // Finish four columns of one tile row: v holds the contraction's sum for
 // output column(s) / row(s) j0 .. j0 + 3 along the tile's columns.
-__device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p, int row, int col0,
-                                        float (&v)[4]) {
+// bias: of the tile's columns in shared memory, or (swapped) of this row.
+struct Extra {
+  uint32_t bias;   // shared-memory address of the tile's first column's
+  float bias_row;
+};
+// Residual of the four values.
+__device__ __forceinline__ void residual4(const CtaParams& c, const DenseParams& p, int row, int col0,
+                                          float (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = 0.f;
+  if (!c.d.epilogue || !p.residual || row >= c.Mr || col0 >= c.Nc) return;
+  const int nv = std::min(4, c.Nc - col0);
+  if (c.swap) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < nv) r[i] = load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row);
+    return;
+  }
+  const long long ro = static_cast<long long>(row) * p.ldr + col0;
+  if (c.vec_res && p.res_f32 && nv == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + ro);
+    r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
+  } else if (c.vec_res && nv == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
+    r[0] = __uint_as_float(u.x << 16), r[1] = __uint_as_float(u.x & 0xffff0000u);
+    r[2] = __uint_as_float(u.y << 16), r[3] = __uint_as_float(u.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < nv) r[i] = load_any(p.residual, p.res_f32, ro + i);
+  }
+}
+__device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p, const Extra& x,
+                                        int row, int n0, int j, float (&v)[4], const float (&r)[4]) {
+  const int col0 = n0 + j;
   const DenseProduct& d = c.d;
   if (row >= c.Mr) return;
   const int nv = std::min(4, c.Nc - col0);
@@ -751,23 +800,14 @@ __device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p
   if (c.swap) {
     // output[col, row]: consecutive lanes write consecutive elements
     if (d.epilogue) {
-      if (p.bias) {
-        const float bv = load_any(p.bias, p.bias_f32, row);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += bv;
-      }
+      for (int i = 0; i < 4; ++i) v[i] += x.bias_row;
       if (p.pre) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (i < nv)
             static_cast<__nv_bfloat16*>(p.pre)[static_cast<long long>(col0 + i) * d.N + row] =
                 __float2bfloat16_rn(v[i]);
-      }
-      float r[4] = {0.f, 0.f, 0.f, 0.f};
-      if (p.residual) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < nv) r[i] = load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row);
       }
       act_all<4>(p.act, v);
 #pragma unroll
@@ -804,26 +844,9 @@ __device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p
     }
   };
   if (d.epilogue) {
-    float r[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.residual) {
-      const long long ro = static_cast<long long>(row) * p.ldr + col0;
-      if (c.vec_res && p.res_f32 && nv == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + ro);
-        r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
-      } else if (c.vec_res && nv == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
-        r[0] = __uint_as_float(u.x << 16), r[1] = __uint_as_float(u.x & 0xffff0000u);
-        r[2] = __uint_as_float(u.y << 16), r[3] = __uint_as_float(u.y & 0xffff0000u);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < nv) r[i] = load_any(p.residual, p.res_f32, ro + i);
-      }
-    }
     if (p.bias) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < nv) v[i] += load_any(p.bias, p.bias_f32, col0 + i);
+      const float4 bv = ld_shared_v4(x.bias + 4 * j);
+      v[0] += bv.x, v[1] += bv.y, v[2] += bv.z, v[3] += bv.w;
     }
     if (p.pre) store4(p.pre, false, c.vec_pre);
     act_all<4>(p.act, v);
@@ -966,6 +989,21 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int i = 0; i < 16; ++i) v[i] += x[i];
     }
   };
+  // the biases, and for a split tile the first residuals, while the tile is
+  // multiplied (each is an L2 latency that would follow the accumulators)
+  Extra extra{meta + 256, 0.f};
+  float res[4] = {0.f, 0.f, 0.f, 0.f};
+  if (warp < 4 && c.d.epilogue) {
+    if (p.bias && c.swap) {
+      if (row < c.Mr) extra.bias_row = load_any(p.bias, p.bias_f32, row);
+    } else if (p.bias) {
+      for (int j = threadIdx.x; j < c.BN; j += 128)
+        st_shared_f32(extra.bias + 4 * j,
+                      n0 + j < c.Nc ? load_any(p.bias, p.bias_f32, n0 + j) : 0.f);
+      bar_named(1, 128);
+    }
+    if (S > 1 && own1 > own0) residual4(c, p, row, n0 + own0, res);
+  }
   if (S > 1) cluster_wait();  // every CTA's barriers exist
   if (warp < 4) {
     const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
@@ -986,7 +1024,13 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[16 + i] = h[i];
         }
-        if (d.epilogue && p.bias) add_bias(p, n0 + j, d.N, v);
+        if (d.epilogue && p.bias) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // (past BN: columns that are not stored)
+            const float4 bv = ld_shared_v4(extra.bias + 4 * j + 16 * i);
+            v[4 * i] += bv.x, v[4 * i + 1] += bv.y, v[4 * i + 2] += bv.z, v[4 * i + 3] += bv.w;
+          }
+        }
       };
       const int per = d.out_f32 ? 32 : 64;
       if (ok)
@@ -1028,7 +1072,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float h[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-            finish4(c, p, row, n0 + j + 4 * i, h);
+            residual4(c, p, row, n0 + j + 4 * i, res);
+            finish4(c, p, extra, row, n0, j + 4 * i, h, res);
           }
         }
     } else {
@@ -1063,7 +1108,8 @@ __global__ void __launch_bounds__(kThreads, 3)
             const float4 x = ld_shared_v4(src + q * c.per * 512);
             v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
           }
-          finish4(c, p, row, n0 + j, v);
+          if (j > own0) residual4(c, p, row, n0 + j, res);
+          finish4(c, p, extra, row, n0, j, v, res);
         }
       }
     }
@@ -1332,6 +1378,9 @@ CtaPlan plan_cta(const DenseProduct& d) {
   const int sms = num_sms();
   for (int swap = 0; swap < 2; ++swap) {
     const int mr = swap ? d.N : d.M, nc = swap ? d.M : d.N;
+    // (a few rows on the 128-row side would be read by every tile at once:
+    // 6 x 216 x 4248 9 us against 5)
+    if (mr < 128 && nc > mr) continue;
     for (int bn : {16, 32, 64, 128, 256}) {
       if (bn > 16 && nc <= bn / 2) break;
       const long long tiles = static_cast<long long>(cdiv(mr, 128)) * cdiv(nc, bn);
@@ -1341,7 +1390,7 @@ CtaPlan plan_cta(const DenseProduct& d) {
         const long long ctas = tiles * s, slots = two ? 2LL * sms : sms;
         const double rounds = static_cast<double>((ctas + slots - 1) / slots);
         const double block = (0.18 + 0.0017 * bn) * (ctas > sms && two ? 1.2 : 1.0);
-        const double store = s == 1 && !swap ? 0.4 + 0.019 * bn : 0.5 + 0.04 * bn;
+        const double store = s == 1 && !swap ? 0.4 + 0.019 * std::max(bn, 32) : 0.5 + 0.04 * bn;
         const double us = 2.2 + rounds * (cdiv(nkb, s) * block + store) +
                           (s > 1 ? 0.4 + 0.036 * bn : 0.0);
         if (us < best.us) best = CtaPlan{swap != 0, bn, s, us};
