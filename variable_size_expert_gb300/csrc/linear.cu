@@ -23,6 +23,9 @@
 //    products with too few 256 x 256 tiles to fill the GPU: a decode step's
 //    few tokens, the gate's few columns.  The longer of the two output sides
 //    lies on the MMA's 128 rows, so that the shorter costs only its own width.
+//    Two warps load and two multiply: 1024 x 8192 x 1024 21 us, 35 with one of
+//    each.  A decode step's 16 x 7168 x 2048 7.0 us (29 MB of weights, 62% of
+//    the measured copy rate): start-up, the first loads and the join take 3 us.
 #include <algorithm>
 #include <cstring>
 
@@ -38,7 +41,6 @@ constexpr int STAGES = 5;
 constexpr int OPER = kHalf * BK * 2;    // 16 KB
 constexpr int CHUNK = 64 * BK * 2;      // 8 KB: 64 wide MN-major block of one stage
 constexpr int EPI_WARP = 32 * 128;      // staging of an epilogue warp: 32 rows x 128 bytes
-constexpr int kThreads = 192;           // single-CTA tiles: warps 0-3 epilogue, 4 MMA, 5 TMA
 // pairs: warps 0-3 and 6-17 epilogue, 4 MMA, 5 TMA.  Sixteen epilogue warps
 // hide one another's latencies (tensor memory, exponentials, store fences):
 // with eight, bias + GELU + kept z took 9.1 us a tile, half of it stalled.
@@ -303,12 +305,6 @@ struct PairMaps {
   CUtensorMap a[2], b[2], res;
 };
 
-constexpr int kGroups = 8;  // release barriers of a ring
-// When the producer waits for a group, the MMAs may have released every group
-// up to the last block it issued: a barrier must not come round again by then
-// (a second completion would turn the parity it waits for).
-constexpr bool releases_fit(int stages, int lg) { return ((stages - 1) >> lg) < kGroups; }
-static_assert(releases_fit(STAGES, 0), "release barriers");
 struct PSmem {
   uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, res_full, issued;
   uint32_t* tmem_slot;
@@ -324,7 +320,7 @@ __device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
   m.sEpi = m.sB + STAGES * OPER;
   m.full = m.sEpi + kEpiWarps * EPI_WARP;
   m.empty = m.full + 8 * STAGES;
-  m.acc_full = m.empty + 8 * kGroups;
+  m.acc_full = m.empty + 8 * STAGES;
   m.acc_empty = m.acc_full + 16;
   m.drain = m.acc_empty + 16;
   m.pdone = m.drain + 8;
@@ -383,15 +379,12 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The producer's and the MMA warp's loops.  Blocks of the contraction pass
-// through a ring of `stages` slots: full[s] tells that a block has landed, and
-// every 2^lg blocks one commit tells through empty[q % kGroups] that group q of
-// blocks has been read.  The pair kernel's blocks take their MMAs 512 cycles
-// and are released one by one (by twos its ring of five runs short: gradients
-// of 8192 x 2048 x 8192 1650 instead of 1800 TFLOP/s); the handshake of a
-// small single-CTA tile costs more than its MMAs and is shared by 2 or 4.
-// Both loops run with the whole warp converged, one elected lane issuing:
-// inside a divergent branch every operand of an MMA or a copy costs extra
-// moves into uniform registers (15% of a loop of small tiles).
+// through a ring of slots: full[s] tells that a block has landed, empty[s] that
+// its MMAs have read it (slots released by twos, the ring of five runs short:
+// gradients of 8192 x 2048 x 8192 1650 instead of 1800 TFLOP/s).  Both loops run
+// with the whole warp converged, one elected lane issuing: inside a divergent
+// branch every operand of an MMA or a copy costs extra moves into uniform
+// registers (15% of a loop of small tiles).
 struct Ring {
   int it, s;
   uint32_t ph;
@@ -400,26 +393,15 @@ struct Ring {
     if (++s == stages) s = 0, ph ^= 1;
   }
 };
-// Producer: the slot of block r.it is free.  (log2 of the group size given.)
-__device__ __forceinline__ bool slot_free(uint32_t empty, const Ring& r, int stages, int lg,
-                                          const WaitCtl& wc) {
-  const int u = r.it - stages;
-  if (u < 0 || (u & ((1 << lg) - 1))) return true;  // never used, or freed with its group
-  const int q = u >> lg;
-  return __all_sync(0xffffffffu, wait_bar(empty + 8 * (q % kGroups), (q / kGroups) & 1, wc));
-}
-// MMA: the barrier to commit to after block `it`, 0 where its group goes on.
-__device__ __forceinline__ uint32_t release_bar(uint32_t empty, int it, int lg) {
-  return ((it + 1) & ((1 << lg) - 1)) ? 0u : empty + 8 * ((it >> lg) % kGroups);
-}
-
 template <bool A_MN, bool B_MN>
 __device__ __forceinline__ bool produce(const PSmem& m, const CUtensorMap* ma,
                                         const CUtensorMap* mb, uint32_t full_l, bool leader, int ar,
                                         int br, int nkb, Ring& r, const WaitCtl& wc) {
 #pragma unroll 1
   for (int k = 0; k < nkb * BK; k += BK) {
-    if (!slot_free(m.empty, r, STAGES, 0, wc)) return false;
+    // (the first round of the slots was never used)
+    if (r.it >= STAGES && !__all_sync(0xffffffffu, wait_bar(m.empty + 8 * r.s, r.ph ^ 1, wc)))
+      return false;
     if (elect_one()) {
       const uint32_t fb = full_l + 8 * r.s;
       // the leader announces its bytes first; the peer issues its copies first
@@ -447,12 +429,11 @@ __device__ __forceinline__ bool multiply(const PSmem& m, uint32_t dt, int nkb, R
     if (!__all_sync(0xffffffffu, wait_bar(m.full + 8 * r.s, r.ph, wc))) return false;
     tc_fence_after();
     const uint64_t ad = a0 + r.s * (OPER >> 4), bd = b0 + r.s * (OPER >> 4);
-    const uint32_t rel = release_bar(m.empty, r.it, 0);
     if (elect_one()) {
 #pragma unroll
       for (int kk = 0; kk < BK / 16; ++kk)
         tc_mma_bf16_cg2(dt, ad + kk * kA, bd + kk * kB, kIdesc, (kb | kk) != 0);
-      if (rel) tc_commit_cg2_mc(rel, 0x3);
+      tc_commit_cg2_mc(m.empty + 8 * r.s, 0x3);
     }
     r.next(STAGES);
   }
@@ -477,9 +458,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&maps.b[0]);
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s)
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(m.full + 8 * s, 2);  // both TMA threads announce their own bytes
-    for (int q = 0; q < kGroups; ++q) mbar_init(m.empty + 8 * q, 1);
+      mbar_init(m.empty + 8 * s, 1);
+    }
     for (int a = 0; a < 2; ++a) {
       mbar_init(m.acc_full + 8 * a, 1);
       mbar_init(m.acc_empty + 8 * a, 2 * kEpiWarps);  // the epilogue warps of both CTAs
@@ -698,7 +680,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ++tcount;
     }
     if (lane == 0 && res_open) wait_bar_drain(res_bar, res_n & 1, DRAIN_LIMIT);
-    if (lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();
@@ -722,20 +703,20 @@ struct CtaParams {
   int Mr, Nc;      // extents along the tile's rows and columns
   int BN;          // tile columns (16..256, a multiple of 16)
   int splits;      // CTAs per cluster: pieces of the contraction
-  int per;         // columns that each CTA of a cluster finishes (a multiple of 4)
-  int stages, lg;  // ring slots, log2 of the blocks per release
+  int per;         // columns that each CTA of a cluster finishes (a multiple of 4, or of 8
+                   // along the output's rows)
+  int slots;       // of the ring, an even number
   int b_bytes;     // B bytes per block
-  int nacc;        // accumulators (1, 2 or 4), see the MMA loop
+  int nacc;        // accumulators (2 or 4), see the MMA loop
   int tmem_cols;
-  int vec_out, vec_pre, vec_res;  // whole rows: 16-byte pieces; split tiles: 4 columns at once
+  int vec_out, vec_pre;  // stores in 16-byte pieces
 };
+constexpr int kCtaThreads = 256;  // warps 0-3 epilogue, 4 and 6 multiply, 5 and 7 load
 constexpr int kCtaMeta = 256 + 1024;  // barriers, the tile's biases
-constexpr int kMaxStages = 12;
-static_assert(8 * (kMaxStages + kGroups + 2) + 8 <= 256, "barrier area");
-static_assert(releases_fit(kMaxStages, 2) && releases_fit(7, 1) && releases_fit(3, 0),
-              "release barriers");  // (the group sizes that launch_cta picks)
+constexpr int kMaxSlots = 12;
+static_assert(8 * (2 * kMaxSlots + 2) + 8 <= 256, "barrier area");
 size_t cta_smem(const CtaParams& c) {
-  return 1024 + static_cast<size_t>(c.stages) * (OPER + c.b_bytes) +
+  return 1024 + static_cast<size_t>(c.slots) * (OPER + c.b_bytes) +
          (c.splits > 1 ? static_cast<size_t>(c.splits) * c.per * 512 : 0) + kCtaMeta;
 }
 
@@ -745,131 +726,68 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// 16 bytes into the shared memory of any CTA of the cluster, counted on that
+// A piece of shared memory into that of any CTA of the cluster, counted on that
 // CTA's mbarrier (both cluster addresses).
-__device__ __forceinline__ void st_async_v4(uint32_t dst, uint32_t bar, float a, float b, float c,
-                                            float d) {
+__device__ __forceinline__ void bulk_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
   asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
           "r"(dst),
-      "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+      "r"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 
-// Finish four columns of one tile row: v holds the contraction's sum for
-// output column(s) / row(s) j0 .. j0 + 3 along the tile's columns.
-// bias: of the tile's columns in shared memory, or (swapped) of this row.
-struct Extra {
-  uint32_t bias;   // shared-memory address of the tile's first column's
-  float bias_row;
-};
-// Residual of the four values.
-__device__ __forceinline__ void residual4(const CtaParams& c, const DenseParams& p, int row, int col0,
-                                          float (&r)[4]) {
+// Sixteen columns of one row of a swapped tile, which are output[col, row]:
+// consecutive lanes read and write consecutive elements.
+__device__ __forceinline__ void residual16(const CtaParams& c, const DenseParams& p, int row, int col0,
+                                           int end, float (&r)[16]) {
+  const bool any = c.d.epilogue && p.residual && row < c.Mr;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = 0.f;
-  if (!c.d.epilogue || !p.residual || row >= c.Mr || col0 >= c.Nc) return;
-  const int nv = std::min(4, c.Nc - col0);
-  if (c.swap) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < nv) r[i] = load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row);
-    return;
-  }
-  const long long ro = static_cast<long long>(row) * p.ldr + col0;
-  if (c.vec_res && p.res_f32 && nv == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + ro);
-    r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
-  } else if (c.vec_res && nv == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + ro);
-    r[0] = __uint_as_float(u.x << 16), r[1] = __uint_as_float(u.x & 0xffff0000u);
-    r[2] = __uint_as_float(u.y << 16), r[3] = __uint_as_float(u.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < nv) r[i] = load_any(p.residual, p.res_f32, ro + i);
-  }
+  for (int i = 0; i < 16; ++i)
+    r[i] = any && col0 + i < end
+               ? load_any(p.residual, p.res_f32, static_cast<long long>(col0 + i) * p.ldr + row)
+               : 0.f;
 }
-__device__ __forceinline__ void finish4(const CtaParams& c, const DenseParams& p, const Extra& x,
-                                        int row, int n0, int j, float (&v)[4], const float (&r)[4]) {
-  const int col0 = n0 + j;
-  const DenseProduct& d = c.d;
+__device__ __forceinline__ void finish16(const CtaParams& c, const DenseParams& p, float bias, int row,
+                                         int col0, int end, float (&v)[16], const float (&r)[16]) {
   if (row >= c.Mr) return;
-  const int nv = std::min(4, c.Nc - col0);
-  if (nv <= 0) return;
-  if (c.swap) {
-    // output[col, row]: consecutive lanes write consecutive elements
-    if (d.epilogue) {
+  const DenseProduct& d = c.d;
+  const long long o = static_cast<long long>(col0) * d.N + row;
+  const int nv = end - col0;
+  auto store = [&](void* out, bool f32) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += x.bias_row;
-      if (p.pre) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < nv)
-            static_cast<__nv_bfloat16*>(p.pre)[static_cast<long long>(col0 + i) * d.N + row] =
-                __float2bfloat16_rn(v[i]);
-      }
-      act_all<4>(p.act, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += r[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 16; ++i) {
       if (i >= nv) continue;
-      const long long o = static_cast<long long>(col0 + i) * d.N + row;
-      if (d.out_f32)
-        static_cast<float*>(d.out)[o] = v[i];
-      else
-        static_cast<__nv_bfloat16*>(d.out)[o] = __float2bfloat16_rn(v[i]);
-    }
-    return;
-  }
-  auto store4 = [&](void* out, bool f32, bool vec) {
-    const long long o = static_cast<long long>(row) * d.N + col0;
-    if (vec && nv == 4) {
       if (f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+        static_cast<float*>(out)[o + static_cast<long long>(i) * d.N] = v[i];
       else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
-            make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= nv) continue;
-        if (f32)
-          static_cast<float*>(out)[o + i] = v[i];
-        else
-          static_cast<__nv_bfloat16*>(out)[o + i] = __float2bfloat16_rn(v[i]);
-      }
+        static_cast<__nv_bfloat16*>(out)[o + static_cast<long long>(i) * d.N] = __float2bfloat16_rn(v[i]);
     }
   };
   if (d.epilogue) {
-    if (p.bias) {
-      const float4 bv = ld_shared_v4(x.bias + 4 * j);
-      v[0] += bv.x, v[1] += bv.y, v[2] += bv.z, v[3] += bv.w;
-    }
-    if (p.pre) store4(p.pre, false, c.vec_pre);
-    act_all<4>(p.act, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += r[i];
+    for (int i = 0; i < 16; ++i) v[i] += bias;
+    if (p.pre) store(p.pre, false);
+    act_all<16>(p.act, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += r[i];
   }
-  store4(d.out, d.out_f32, c.vec_out);
+  store(d.out, d.out_f32);
 }
 
-template <bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 3)
+template <bool A_MN, bool B_MN, bool SPLIT>
+__global__ void __launch_bounds__(kCtaThreads, 2)
     dense_cta_kernel(const __grid_constant__ CtaMaps maps, const __grid_constant__ CtaParams c,
                      const __grid_constant__ DenseParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw_addr);
-  const int b_bytes = c.b_bytes, stages = c.stages;
+  const int b_bytes = c.b_bytes, slots = c.slots;
   const uint32_t stage_bytes = OPER + b_bytes;
-  const int S = c.splits;
-  const uint32_t recv = base + stages * stage_bytes;  // partial sums from the cluster
+  const int S = SPLIT ? c.splits : 1;
+  const uint32_t recv = base + slots * stage_bytes;  // partial sums from the cluster
   const uint32_t meta = recv + (S > 1 ? S * c.per * 512 : 0);
-  const uint32_t full = meta, empty = meta + 8 * kMaxStages, acc_full = empty + 8 * kGroups,
+  const uint32_t full = meta, empty = meta + 8 * kMaxSlots, acc_full = empty + 8 * kMaxSlots,
                  got = acc_full + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (got + 8 - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -888,9 +806,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     tma_prefetch_desc(&maps.b);
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(full + 8 * s, 1);
-    for (int q = 0; q < kGroups; ++q) mbar_init(empty + 8 * q, 1);
-    mbar_init(acc_full, 1);
+    for (int s = 0; s < slots; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
+    mbar_init(acc_full, 2);
     mbar_init(got, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -909,65 +826,76 @@ __global__ void __launch_bounds__(kThreads, 3)
   pdl_trigger();  // (after the wait: see launch_dense_backward)
   const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
 
-  if (warp == 5) {
-    Ring r{0, 0, 0};
+  // Warps 5 and 7 load, and warps 4 and 6 multiply, the even and the odd blocks:
+  // waiting, issuing and committing take one warp 250 ns a block, a tile of 128
+  // columns' MMAs 130 (1024 x 8192 x 1024 in whole tiles 35 us with one warp
+  // of each kind, 22 with two).  The number of slots is even, so that a slot
+  // has one warp on either side.  As above, the warps stay converged and
+  // elected lanes issue.
+  if (warp >= 4) {
+    const int first = (warp - 4) >> 1;
+    int s = first, it = first;
+    uint32_t ph = 0;
+    auto next = [&]() {
+      it += 2;
+      if ((s += 2) >= slots) s -= slots, ph ^= 1;
+    };
+    if (warp & 1) {
 #pragma unroll 1
-    for (int k = kb0 * BK; k < kb1 * BK; k += BK) {
-      if (!slot_free(empty, r, stages, c.lg, wc)) break;
-      if (elect_one()) {
-        const uint32_t fb = full + 8 * r.s;
-        const uint32_t a = base + r.s * stage_bytes, b = a + OPER;
-        mbar_arrive_expect_tx(fb, stage_bytes);
-        if constexpr (A_MN) {
-          tma_load_2d(a, &maps.a, fb, m0, k);
-          tma_load_2d(a + CHUNK, &maps.a, fb, m0 + 64, k);
-        } else {
-          tma_load_2d(a, &maps.a, fb, k, m0);
+      for (int k = (kb0 + first) * BK; k < kb1 * BK; k += 2 * BK) {
+        if (it >= slots && !__all_sync(0xffffffffu, wait_bar(empty + 8 * s, ph ^ 1, wc))) break;
+        if (elect_one()) {
+          const uint32_t fb = full + 8 * s;
+          const uint32_t a = base + s * stage_bytes, b = a + OPER;
+          mbar_arrive_expect_tx(fb, stage_bytes);
+          if constexpr (A_MN) {
+            tma_load_2d(a, &maps.a, fb, m0, k);
+            tma_load_2d(a + CHUNK, &maps.a, fb, m0 + 64, k);
+          } else {
+            tma_load_2d(a, &maps.a, fb, k, m0);
+          }
+          if constexpr (B_MN) {
+            for (int j = 0; j * CHUNK < b_bytes; ++j)
+              tma_load_2d(b + j * CHUNK, &maps.b, fb, n0 + 64 * j, k);
+          } else {
+            tma_load_2d(b, &maps.b, fb, k, n0);
+          }
         }
-        if constexpr (B_MN) {
-          for (int j = 0; j * CHUNK < b_bytes; ++j)
-            tma_load_2d(b + j * CHUNK, &maps.b, fb, n0 + 64 * j, k);
-        } else {
-          tma_load_2d(b, &maps.b, fb, k, n0);
-        }
+        next();
       }
-      r.next(stages);
-    }
-    // the copies land before the block may exit
-    for (int j = std::max(0, r.it - stages); j < r.it; ++j)
-      wait_bar_drain(full + 8 * (j % stages), (j / stages) & 1, DRAIN_LIMIT);
-    __syncwarp();
-  } else if (warp == 4) {
-    const uint32_t idesc = idesc_bf16_f32(128, c.BN, A_MN, B_MN);
-    constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
-    const uint64_t a0 = sw128_desc(base, A_MN ? CHUNK : 16, 1024);
-    const uint64_t b0 = sw128_desc(base + OPER, B_MN ? CHUNK : 16, 1024);
-    const uint32_t adv = stage_bytes >> 4;
-    // The four MMAs of a block go to up to four accumulators, which the
-    // epilogue adds up: one that adds onto the accumulator of the one before
-    // it waits for it (6% of 16 x 7168 x 2048 in one piece).
-    const int nacc = c.nacc;
-    uint32_t dt[BK / 16];
+      // the copies land before the block may exit
+      for (int j = it - 2; j >= first && j > it - 2 - slots; j -= 2)
+        wait_bar_drain(full + 8 * (j % slots), (j / slots) & 1, DRAIN_LIMIT);
+    } else {
+      const uint32_t idesc = idesc_bf16_f32(128, c.BN, A_MN, B_MN);
+      constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
+      const uint64_t a0 = sw128_desc(base, A_MN ? CHUNK : 16, 1024);
+      const uint64_t b0 = sw128_desc(base + OPER, B_MN ? CHUNK : 16, 1024);
+      const uint32_t adv = stage_bytes >> 4;
+      // Each warp has an accumulator of its own, or two where the tile is
+      // narrow (an MMA that adds onto the accumulator of the one before waits
+      // for it); the epilogue adds them up.
+      const int own = c.nacc / 2;
+      uint32_t dt[BK / 16];
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) dt[kk] = tmem_base + (kk & (nacc - 1)) * c.BN;
-    Ring r{0, 0, 0};
+      for (int kk = 0; kk < BK / 16; ++kk) dt[kk] = tmem_base + (first + (kk & (own - 1)) * 2) * c.BN;
 #pragma unroll 1
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!__all_sync(0xffffffffu, wait_bar(full + 8 * r.s, r.ph, wc))) break;
-      tc_fence_after();
-      const uint64_t ad = a0 + r.s * adv, bd = b0 + r.s * adv;
-      const uint32_t rel = release_bar(empty, r.it, c.lg);
-      if (elect_one()) {
+      for (int kb = kb0 + first; kb < kb1; kb += 2) {
+        if (!__all_sync(0xffffffffu, wait_bar(full + 8 * s, ph, wc))) break;
+        tc_fence_after();
+        const uint64_t ad = a0 + s * adv, bd = b0 + s * adv;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          tc_mma_bf16(dt[kk], ad + kk * kA, bd + kk * kB, idesc, kb > kb0 || kk >= nacc);
-        if (rel) tc_commit(rel);
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc_mma_bf16(dt[kk], ad + kk * kA, bd + kk * kB, idesc, it > first || kk >= own);
+          tc_commit(empty + 8 * s);
+        }
+        next();
       }
-      r.next(stages);
-    }
-    if (elect_one()) {
-      tc_commit(acc_full);
-      wait_bar_drain(acc_full, 0, DRAIN_LIMIT);
+      if (elect_one()) {
+        tc_commit(acc_full);
+        wait_bar_drain(acc_full, 0, DRAIN_LIMIT);
+      }
     }
     __syncwarp();
   }
@@ -977,146 +905,160 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int tl = warp * 32 + lane;
   const int row = m0 + tl;
   const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-  // 16 columns from j, the accumulators added up
+  // 16 columns from j, the accumulators added up (of a single block only the
+  // first warp's are written)
   auto load16 = [&](int j, float(&v)[16]) {
+    const int step = kb1 - kb0 > 1 ? 1 : 2;
+    const bool two = step < c.nacc;
+    float x[16];
     tmem_ld16(taddr + j, v);
+    if (two) tmem_ld16(taddr + step * c.BN + j, x);
     tmem_ld_wait();
-    for (int a = 1; a < c.nacc; ++a) {
-      float x[16];
+    if (two)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += x[i];
+    for (int a = 2 * step; a < c.nacc; a += step) {
       tmem_ld16(taddr + a * c.BN + j, x);
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] += x[i];
     }
   };
-  // the biases, and for a split tile the first residuals, while the tile is
+  // the same over the cluster's pieces, in rank order (the same bits every time)
+  auto sum16 = [&](int j, float(&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    const uint32_t src = recv + (((j - own0) >> 2) * 128 + tl) * 16;
+    for (int q = 0; q < S; ++q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (j + 4 * i >= own1) continue;
+        const float4 x = ld_shared_v4(src + q * c.per * 512 + i * 2048);
+        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+      }
+    }
+  };
+  // the biases, and a swapped tile's first residuals, while the tile is
   // multiplied (each is an L2 latency that would follow the accumulators)
-  Extra extra{meta + 256, 0.f};
-  float res[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint32_t biases = meta + 256;
+  float bias_row = 0.f, res[16];
+  const int cend = std::min(c.Nc, n0 + own1);
   if (warp < 4 && c.d.epilogue) {
     if (p.bias && c.swap) {
-      if (row < c.Mr) extra.bias_row = load_any(p.bias, p.bias_f32, row);
+      if (row < c.Mr) bias_row = load_any(p.bias, p.bias_f32, row);
     } else if (p.bias) {
       for (int j = threadIdx.x; j < c.BN; j += 128)
-        st_shared_f32(extra.bias + 4 * j,
-                      n0 + j < c.Nc ? load_any(p.bias, p.bias_f32, n0 + j) : 0.f);
+        st_shared_f32(biases + 4 * j, n0 + j < c.Nc ? load_any(p.bias, p.bias_f32, n0 + j) : 0.f);
       bar_named(1, 128);
     }
-    if (S > 1 && own1 > own0) residual4(c, p, row, n0 + own0, res);
   }
+  if (warp < 4 && c.swap) residual16(c, p, row, n0 + own0, cend, res);
   if (S > 1) cluster_wait();  // every CTA's barriers exist
+  bool ok = false;
   if (warp < 4) {
-    const bool ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
+    ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
     tc_fence_after();
-    if (S == 1 && !c.swap) {
-      // rows of the output: through staged blocks, over the pipeline's buffers
-      // (every MMA that read them is done); the residual's blocks beside them
-      const DenseProduct& d = c.d;
-      const uint32_t stg = base + warp * 4096;
-      const int row0 = m0 + warp * 32, cend = std::min(d.N, n0 + c.BN);
-      auto load32 = [&](int j, float(&v)[32]) {  // columns n0 + j .. with the bias
-        float h[16];
-        load16(j, h);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = h[i], v[16 + i] = 0.f;
-        if (j + 16 < c.BN) {
-          load16(j + 16, h);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[16 + i] = h[i];
-        }
-        if (d.epilogue && p.bias) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {  // (past BN: columns that are not stored)
-            const float4 bv = ld_shared_v4(extra.bias + 4 * j + 16 * i);
-            v[4 * i] += bv.x, v[4 * i + 1] += bv.y, v[4 * i + 2] += bv.z, v[4 * i + 3] += bv.w;
-          }
-        }
-      };
-      const int per = d.out_f32 ? 32 : 64;
-      if (ok)
-#pragma unroll 1
-        for (int j0 = 0; j0 < c.BN && n0 + j0 < d.N; j0 += per) {
-          const int halves = std::min(per / 32, cdiv(c.BN - j0, 32));
-          if (d.epilogue && p.pre) {
-#pragma unroll 1
-            for (int h = 0; h < halves; ++h) {
-              float v[32];
-              load32(j0 + 32 * h, v);
-              stage_bf16(stg, lane, h, v);
-            }
-            stage_flush(stg, lane, c.vec_pre, p.pre, false, row0, d.M, d.N, n0 + j0,
-                        std::min(cend, n0 + j0 + per));
-          }
-#pragma unroll 1
-          for (int h = 0; h < halves; ++h) {
-            float v[32];
-            load32(j0 + 32 * h, v);
-            if (d.epilogue) {
-              act_all<32>(p.act, v);
-              if (p.residual)
-                add_residual(p, stg + 16384, lane, row0, d.M, n0 + j0 + 32 * h, d.N, v);
-            }
-            if (d.out_f32)
-              stage_f32(stg, lane, v);
-            else
-              stage_bf16(stg, lane, h, v);
-          }
-          stage_flush(stg, lane, c.vec_out, d.out, d.out_f32, row0, d.M, d.N, n0 + j0, cend);
-        }
-    } else if (S == 1) {
-      if (ok)
-#pragma unroll 1
-        for (int j = 0; j < c.BN && n0 + j < c.Nc; j += 16) {
-          float v[16];
-          load16(j, v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float h[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-            residual4(c, p, row, n0 + j + 4 * i, res);
-            finish4(c, p, extra, row, n0, j + 4 * i, h, res);
-          }
-        }
-    } else {
-      // Each CTA finishes `per` of the tile's columns: every CTA sends it its
-      // partial sums of them, straight from registers, counted on its barrier
-      // (and goes on: nothing of the sender's is read later).
+    if (S > 1) {
+      // Each CTA finishes `per` of the tile's columns: every CTA lays its partial
+      // sums down over the ring (every MMA that read it is done) and sends each
+      // its columns in one copy, counted on its barrier.  (Sixteen bytes at a
+      // time from registers the receiver's count takes longer than the copy.)
 #pragma unroll 1
       for (int j = 0; j < c.BN; j += 16) {
         float v[16];
         load16(j, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = j + 4 * i;
-          const int owner = col / c.per;
-          const uint32_t dst = recv + (((rank * c.per + col - owner * c.per) >> 2) * 128 + tl) * 16;
-          st_async_v4(mapa_shared(dst, owner), mapa_shared(got, owner), v[4 * i], v[4 * i + 1],
-                      v[4 * i + 2], v[4 * i + 3]);
-        }
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(base + (((j >> 2) + i) * 128 + tl) * 16, v[4 * i], v[4 * i + 1], v[4 * i + 2],
+                       v[4 * i + 3]);
       }
+      fence_proxy_async_smem();
+      bar_named(1, 128);
+      const int cols = min(c.per, c.BN - lane * c.per);  // of the CTA of rank `lane`
+      if (warp == 0 && lane < S && cols > 0)
+        bulk_to_cta(mapa_shared(recv + rank * c.per * 512, lane), base + lane * c.per * 512, cols * 512,
+                    mapa_shared(got, lane));
+      __syncwarp();
+      if (own1 > own0) ok = __all_sync(0xffffffffu, wait_bar(got, 0, wc)) && ok;
     }
   }
-  if (S > 1) {
-    cluster_arrive();  // this CTA has sent everything
-    if (warp < 4 && own1 > own0) {
-      if (__all_sync(0xffffffffu, wait_bar_cluster(got, 0, wc))) {
+  // After this barrier what the CTA sent has arrived (every CTA has waited for
+  // all that was sent to it): its ring is free, and it may leave.
+  if (S > 1) cluster_arrive();
+  if (S > 1 && !c.swap) cluster_wait();
+  if (ok && c.swap) {
 #pragma unroll 1
-        for (int j = own0; j < own1 && n0 + j < c.Nc; j += 4) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t src = recv + (((j - own0) >> 2) * 128 + tl) * 16;
-#pragma unroll 8
-          for (int q = 0; q < S; ++q) {  // in rank order: the same bits every time
-            const float4 x = ld_shared_v4(src + q * c.per * 512);
-            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-          }
-          if (j > own0) residual4(c, p, row, n0 + j, res);
-          finish4(c, p, extra, row, n0, j, v, res);
+    for (int j = own0; j < own1 && n0 + j < c.Nc; j += 16) {
+      float v[16];
+      if (S > 1)
+        sum16(j, v);
+      else
+        load16(j, v);
+      if (j > own0) residual16(c, p, row, n0 + j, cend, res);
+      finish16(c, p, bias_row, row, n0 + j, cend, v, res);
+    }
+  } else if (ok) {
+    // rows of the output: through staged blocks, over the pipeline's buffers;
+    // the residual's blocks beside them
+    const DenseProduct& d = c.d;
+    const uint32_t stg = base + warp * 4096;
+    const int row0 = m0 + warp * 32;
+    auto load32 = [&](int j, float(&v)[32]) {  // columns n0 + j .. with the bias
+      float h[16];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (j + 16 * k >= own1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[16 * k + i] = 0.f;
+          continue;
+        }
+        if (S > 1)
+          sum16(j + 16 * k, h);
+        else
+          load16(j + 16 * k, h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[16 * k + i] = h[i];
+      }
+      if (d.epilogue && p.bias) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // (past BN: columns that are not stored)
+          const float4 bv = ld_shared_v4(biases + 4 * j + 16 * i);
+          v[4 * i] += bv.x, v[4 * i + 1] += bv.y, v[4 * i + 2] += bv.z, v[4 * i + 3] += bv.w;
         }
       }
+    };
+    const int per = d.out_f32 ? 32 : 64;
+#pragma unroll 1
+    for (int j0 = own0; j0 < own1 && n0 + j0 < d.N; j0 += per) {
+      const int halves = std::min(per / 32, cdiv(own1 - j0, 32));
+      if (d.epilogue && p.pre) {
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          float v[32];
+          load32(j0 + 32 * h, v);
+          stage_bf16(stg, lane, h, v);
+        }
+        stage_flush(stg, lane, c.vec_pre, p.pre, false, row0, d.M, d.N, n0 + j0,
+                    std::min(cend, n0 + j0 + per));
+      }
+#pragma unroll 1
+      for (int h = 0; h < halves; ++h) {
+        float v[32];
+        load32(j0 + 32 * h, v);
+        if (d.epilogue) {
+          act_all<32>(p.act, v);
+          if (p.residual)
+            add_residual(p, stg + 16384, lane, row0, d.M, n0 + j0 + 32 * h, d.N, v);
+        }
+        if (d.out_f32)
+          stage_f32(stg, lane, v);
+        else
+          stage_bf16(stg, lane, h, v);
+      }
+      stage_flush(stg, lane, c.vec_out, d.out, d.out_f32, row0, d.M, d.N, n0 + j0, cend);
     }
-    // no CTA leaves before the others have sent (on the normal path they
-    // have: what was received here came from all of them)
-    cluster_wait();
   }
+  if (S > 1 && c.swap) cluster_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
@@ -1356,22 +1298,29 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
   return launch_pairs_act<kActNone>(maps, p, total, st);
 }
 
-// The kernel for a product, by estimated time in us: start-up + rounds x
-// contraction blocks x the time of a block, fitted to sweeps of 16 to 4096 x
-// 2048 x 2048 and 16 x 7168 x 2048 (a tile of 128 x BN takes 0.18 us + 1.7 ns
-// per column and block, 1.2 times that with two CTAs on an SM; joining the
-// pieces of a contraction costs 0.4 us + 36 ns per column, storing a tile
-// 0.5 us + 40 ns per column, 0.4 us + 19 ns through staged blocks; a 256 x 256
-// tile on a pair 0.275 us a block and 1.2 us to store).  BN up to 64, or a few
-// blocks in all, leave room for two CTAs an SM.
-// Clusters of eight CTAs that fill an SM each found too few places (128 x
-// 2048 x 2048: 16 us against 8), so wider tiles split at most four ways, and
-// the widest not at all (its partial sums do not fit beside the ring).
+// The kernel for a product, by estimated time in us, fitted to sweeps of 16 to
+// 8192 rows, 64 to 2048 columns and contractions of 512 to 8192 over every tile
+// width and split (within 10% of most).  A tile of 128 x BN takes 0.125 us a
+// block of the contraction up to 32 columns (the handshakes), 0.19 at 128, 0.28
+// at 256 (its MMAs and operands); two CTAs on an SM share that rate.  Storing
+// it takes 0.4 us + 17 ns a column (45 with its rows along the output's columns,
+// 70 where rows do not start on 16-byte boundaries), joining S pieces 0.5 us a
+// piece, 12 ns a column of the tile and 55 of a CTA's own; a 256 x 256 tile on a
+// pair 0.275 us a block and 1.2 us to store (4.6).  Measured on both sides:
+// 4096 x 2048 x 64 in tiles of 32 columns 6.9 us, of 128 8.3; 64 x 4096 x 2048
+// in four pieces of 32 columns 7.0, in eight 7.9, whole 11; 4096 x 4096 x 1024
+// in tiles of 256 24.7, of 128 30.2, on pairs 25.4; 5135 x 1928 x 626 on pairs
+// 19.5, in tiles of 256 28.5; 16 x 7168 x 2048 in four pieces 7.0, in six 7.35,
+// in eight 7.3.
+// Clusters of eight CTAs that fill an SM each find too few places; tiles wider
+// than 64 split at most four ways, wider than 128 not at all (their partial
+// sums would not fit over the ring).
 struct CtaPlan {
   bool swap;
   int BN, splits;
   double us;
 };
+bool whole_rows(const DenseProduct& d) { return vec_rows(d.out, d.N, d.out_f32); }
 CtaPlan plan_cta(const DenseProduct& d) {
   CtaPlan best{false, 16, 1, 1e30};
   const int nkb = cdiv(d.Kc, BK);
@@ -1381,18 +1330,21 @@ CtaPlan plan_cta(const DenseProduct& d) {
     // (a few rows on the 128-row side would be read by every tile at once:
     // 6 x 216 x 4248 9 us against 5)
     if (mr < 128 && nc > mr) continue;
-    for (int bn : {16, 32, 64, 128, 256}) {
-      if (bn > 16 && nc <= bn / 2) break;
+    const double column = swap ? 0.045 : whole_rows(d) ? 0.017 : 0.07;
+    int last = 0;
+    for (int bn : {16, 32, 64, 96, 128, 192, 256}) {
+      if (bn > 16 && nc <= last) break;
+      last = bn;
       const long long tiles = static_cast<long long>(cdiv(mr, 128)) * cdiv(nc, bn);
-      const int most = bn <= 64 ? 8 : bn == 128 ? 4 : 1;
-      for (int s = 1; s <= most && s <= nkb; s *= 2) {
-        const bool two = bn <= 64 || cdiv(nkb, s) * (OPER + 128 * bn) <= 110 * 1024;
+      for (int s : {1, 2, 3, 4, 8}) {
+        if (s > nkb || s > (bn <= 64 ? 8 : bn <= 128 ? 4 : 1)) break;
+        const int blocks = cdiv(nkb, s);
+        const bool two = bn <= 64 || (bn <= 128 && (blocks + 1) * (OPER + 128 * bn) <= 110 * 1024);
         const long long ctas = tiles * s, slots = two ? 2LL * sms : sms;
         const double rounds = static_cast<double>((ctas + slots - 1) / slots);
-        const double block = (0.18 + 0.0017 * bn) * (ctas > sms && two ? 1.2 : 1.0);
-        const double store = s == 1 && !swap ? 0.4 + 0.019 * std::max(bn, 32) : 0.5 + 0.04 * bn;
-        const double us = 2.2 + rounds * (cdiv(nkb, s) * block + store) +
-                          (s > 1 ? 0.4 + 0.036 * bn : 0.0);
+        const double block = std::max(0.125, 0.1 + 0.0007 * bn) * (ctas > sms && two ? 2.05 : 1.0);
+        const double join = s > 1 ? 0.5 * s + 0.012 * bn + 0.055 * cdiv(bn, s) : 0.0;
+        const double us = 2.0 + rounds * (blocks * block + 0.4 + column * bn + join);
         if (us < best.us) best = CtaPlan{swap != 0, bn, s, us};
       }
     }
@@ -1402,20 +1354,20 @@ CtaPlan plan_cta(const DenseProduct& d) {
 bool use_pairs(const DenseProduct& d) {
   const long long tiles = static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256);
   const long long pairs = num_sms() / 2;
-  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * (cdiv(d.Kc, BK) * 0.275 + 1.2);
+  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * (cdiv(d.Kc, BK) * 0.275 + (whole_rows(d) ? 1.2 : 4.6));
   return us <= plan_cta(d).us;
 }
 
-template <bool A_MN, bool B_MN>
-cudaError_t launch_cta_t(const CtaMaps& maps, const CtaParams& c, const DenseParams& p,
+template <bool A_MN, bool B_MN, bool SPLIT>
+cudaError_t launch_cta_s(const CtaMaps& maps, const CtaParams& c, const DenseParams& p,
                          cudaStream_t st) {
   static bool done[64] = {};
-  auto kern = dense_cta_kernel<A_MN, B_MN>;
+  auto kern = dense_cta_kernel<A_MN, B_MN, SPLIT>;
   cudaError_t e = allow_smem(kern, 232448, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cdiv(c.Mr, 128) * cdiv(c.Nc, c.BN) * c.splits);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kCtaThreads);
   cfg.dynamicSmemBytes = cta_smem(c);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1425,8 +1377,14 @@ cudaError_t launch_cta_t(const CtaMaps& maps, const CtaParams& c, const DensePar
   attr[1].val.clusterDim.x = c.splits;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = c.splits > 1 ? 2 : 1;
+  cfg.numAttrs = SPLIT ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, maps, c, p);
+}
+template <bool A_MN, bool B_MN>
+cudaError_t launch_cta_t(const CtaMaps& maps, const CtaParams& c, const DenseParams& p,
+                         cudaStream_t st) {
+  return c.splits > 1 ? launch_cta_s<A_MN, B_MN, true>(maps, c, p, st)
+                      : launch_cta_s<A_MN, B_MN, false>(maps, c, p, st);
 }
 
 cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const DenseOperand& b,
@@ -1442,24 +1400,22 @@ cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const
   if (plan.swap) std::swap(c.d.a_mn, c.d.b_mn);
   c.BN = plan.BN;
   c.splits = plan.splits;
-  c.per = (cdiv(c.BN, c.splits) + 3) & ~3;
+  c.per = c.swap ? (cdiv(c.BN, c.splits) + 3) & ~3 : (cdiv(c.BN, c.splits) + 7) & ~7;
   c.b_bytes = c.d.b_mn ? cdiv(c.BN, 64) * CHUNK : c.BN * 128;
-  // two blocks on an SM where the tile is small
-  const int room = (c.BN <= 64 ? 112 : 225) * 1024 - 1024 - kCtaMeta -
-                   (c.splits > 1 ? c.splits * c.per * 512 : 0);
-  c.stages = std::max(2, std::min({kMaxStages, room / (OPER + c.b_bytes), cdiv(cdiv(c.d.Kc, BK), c.splits)}));
-  c.lg = c.stages >= 8 ? 2 : c.stages >= 4 ? 1 : 0;
-  c.nacc = c.BN <= 64 ? 4 : c.BN <= 128 ? 2 : 1;
+  // The ring has an SM's room where every CTA has an SM of its own (512 x 2048 x
+  // 2048 in tiles of 64 columns 7.8 us against 8.9), else half of it for narrow
+  // tiles.  Clusters of eight leave the other half free: they find too few
+  // places else (16 x 7168 x 2048 in eight pieces 10 us against 7).
+  const long long ctas = static_cast<long long>(cdiv(c.Mr, 128)) * cdiv(c.Nc, c.BN) * c.splits;
+  const bool alone = c.BN > 64 || (ctas <= num_sms() && c.splits <= 4);
+  const int room = (alone ? 225 : 112) * 1024 - 1024 - kCtaMeta - (c.splits > 1 ? c.splits * c.per * 512 : 0);
+  const int fit = std::min({kMaxSlots, room / (OPER + c.b_bytes), cdiv(cdiv(c.d.Kc, BK), c.splits) + 1});
+  c.slots = std::max(2, fit & ~1);
+  c.nacc = c.BN <= 64 ? 4 : 2;
   c.tmem_cols = 32;
   while (c.tmem_cols < c.nacc * c.BN) c.tmem_cols *= 2;
-  auto vec4 = [](const void* ptr, long long ld, bool f32) {
-    const int bytes = f32 ? 16 : 8;
-    return reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && ld % 4 == 0;
-  };
-  const bool staged = c.splits == 1 && !c.swap;
-  c.vec_out = staged ? vec_rows(c.d.out, c.d.N, c.d.out_f32) : vec4(c.d.out, c.d.N, c.d.out_f32);
-  c.vec_pre = p.pre && (staged ? vec_rows(p.pre, c.d.N, false) : vec4(p.pre, c.d.N, false));
-  c.vec_res = p.residual && vec4(p.residual, p.ldr, p.res_f32);
+  c.vec_out = vec_rows(c.d.out, c.d.N, c.d.out_f32);
+  c.vec_pre = p.pre && vec_rows(p.pre, c.d.N, false);
   CtaMaps maps;
   if (!tmap_operand(&maps.a, ra, c.d.a_mn, 128) || !tmap_operand(&maps.b, rb, c.d.b_mn, c.BN))
     return cudaErrorInvalidValue;
