@@ -646,8 +646,12 @@ __global__ void __launch_bounds__(kBwdThreads)
 }
 
 // Forward, for many rows: six row slots (32 KB each in f32), weights and
-// biases of a thread's 16 columns in registers; a row leaves its slot for
-// registers before its first reduction.
+// biases of a thread's 16 columns in registers.  A group takes its rows in
+// pairs with one barrier a pair: what bounds a group is the chain from a row's
+// copy to its store.  So that one exchange is enough, each warp finds mean and
+// squares of its own columns around its own mean, and the warps' are joined,
+//   M2 = sum_w M2_w + n_w (mean_w - mean)^2,
+// which loses nothing to a large mean either.
 constexpr int kFwdDepth = 6;
 template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kBwdThreads)
@@ -657,8 +661,9 @@ __global__ void __launch_bounds__(kBwdThreads)
   constexpr int kThreads = kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   constexpr int XB = VEC * sizeof(XT), H = VEC / 2;
-  constexpr int depth = kFwdDepth, D = depth - 1;
-  __shared__ float slots[4][kGroups][TPR / 32];
+  constexpr int NW = TPR / 32, R = 2;  // rows at a time
+  __shared__ float2 slots[2][kGroups][NW][R];
+  __shared__ float counts[kGroups][NW];
   extern __shared__ __align__(16) uint8_t ring[];  // [depth][NV][threads]
   const int group = threadIdx.x / TPR, tig = threadIdx.x % TPR;
   uint8_t* mine = ring + threadIdx.x * XB;
@@ -674,18 +679,25 @@ __global__ void __launch_bounds__(kBwdThreads)
   const XT* xs = x + first * ldx + c0;
   YT* out = y + static_cast<long long>(first) * K + c0;
   const long long sx = step * ldx, sk = static_cast<long long>(step) * K;
-  auto copy = [&](int i, int slot) {
-    if (i < rows) {
+  int next = 0;  // row to copy, its slot
+  int to = 0;
+  auto copy = [&]() {
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (c0 + j * kStride < K)
-          cp_async_piece<XB>(smem_u32(mine + slot * (NV * kPiece) + j * kPiece), xs + j * kStride);
-      xs += sx;
+    for (int i = 0; i < R; ++i, ++next) {
+      if (next < rows) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (c0 + j * kStride < K)
+            cp_async_piece<XB>(smem_u32(mine + to * (NV * kPiece) + j * kPiece), xs + j * kStride);
+        xs += sx;
+      }
+      if (++to == kFwdDepth) to = 0;
     }
     cp_async_commit();
   };
+  constexpr int D = kFwdDepth / R - 1;  // pairs ahead
 #pragma unroll
-  for (int i = 0; i < D; ++i) copy(i, i);
+  for (int i = 0; i < D; ++i) copy();
   F2 wv[NV][H], bv[NV][H];
   load_columns<VEC, TPR, NV, SHIFT>(w, w_f32, tig, m, K, wv);
   if (b) {
@@ -696,68 +708,135 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
       for (int i = 0; i < H; ++i) bv[j][i] = both(0.f);
   }
+  // columns of this warp, and of warp (lane mod NW), whose sums the lane joins
+  float own = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    own += static_cast<float>(max(0, min(c0 + j * kStride + VEC, K) - max(c0 + j * kStride, 0)));
+  own = warp_sum(own);
+  const float inv_own = own > 0.f ? 1.f / own : 0.f;
+  float n = own, inv_n = inv_own;
+  if constexpr (NW > 1) {
+    if ((tig & 31) == 0) counts[group][tig >> 5] = own;
+    bar_named(1 + group, TPR);
+    n = counts[group][tig & (NW - 1)];
+    inv_n = n > 0.f ? 1.f / n : 0.f;
+  }
   float *pm = mean_out + first, *pr = rstd_out + first;
-  int slot = 0, ahead = D;
+  int slot = 0;
 #pragma unroll 1
-  for (int row = 0, par = 0; row < rows; ++row, par ^= 2) {
-    copy(row + D, ahead);
-    if (++ahead == depth) ahead = 0;
+  for (int row = 0, par = 0; row < rows; row += R, par ^= 1) {
+    copy();
     cp_async_wait<D>();
-    F2 f[NV][H];
-    F2 s = both(0.f);
+    F2 f[R][NV][H];
+    float mine_mean[R], sq[R], sums[R], mean[R], rstd[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = c0 + j * kStride;
-      if (c >= K) continue;
-      Raw<XT, VEC> r = *reinterpret_cast<const Raw<XT, VEC>*>(mine + slot * (NV * kPiece) + j * kPiece);
-      if (SHIFT && (c < 0 || c + VEC > K)) keep_range<XT, VEC>(r, -c, K - c);
-      unpack2v<XT, VEC>(r, f[j]);
+    for (int r = 0; r < R; ++r) {
+      F2 s = both(0.f);
 #pragma unroll
-      for (int i = 0; i < H; ++i) s = add2(s, f[j][i]);
-    }
-    if (++slot == depth) slot = 0;
-    float lo, hi;
-    unpack2(s, lo, hi);
-    // (the slots of even and odd rows alternate: a row's writes cannot meet
-    // the reads of the row before)
-    const float mean = group_sum<TPR>(lo + hi, slots[par][group], group, tig) * inv_k;
-    const F2 nm = both(-mean);
-    F2 q = both(0.f);
+      for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * kStride;
+        if (c >= K) continue;
+        Raw<XT, VEC> q = *reinterpret_cast<const Raw<XT, VEC>*>(mine + slot * (NV * kPiece) + j * kPiece);
+        if (SHIFT && (c < 0 || c + VEC > K)) keep_range<XT, VEC>(q, -c, K - c);
+        unpack2v<XT, VEC>(q, f[r][j]);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = c0 + j * kStride;
-      if (c >= K) continue;
-      const bool edge = SHIFT && (c < 0 || c + VEC > K);
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        f[j][i] = add2(f[j][i], nm);
-        if (edge) {  // outside the row: no part in the variance
-          float a, d;
-          unpack2(f[j][i], a, d);
-          f[j][i] = pack2(c + 2 * i >= 0 && c + 2 * i < K ? a : 0.f,
-                          c + 2 * i + 1 >= 0 && c + 2 * i + 1 < K ? d : 0.f);
-        }
-        q = fma2(f[j][i], f[j][i], q);
+        for (int i = 0; i < H; ++i) s = add2(s, f[r][j][i]);
       }
+      if (++slot == kFwdDepth) slot = 0;
+      float lo, hi;
+      unpack2(s, lo, hi);
+      sums[r] = lo + hi;
     }
-    unpack2(q, lo, hi);
-    const float rstd = 1.f / sqrtf(group_sum<TPR>(lo + hi, slots[par + 1][group], group, tig) * inv_k + eps);
-    if (tig == 0) {
-      *pm = mean;
-      *pr = rstd;
-    }
-    pm += step, pr += step;
-    const F2 rs = both(rstd);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = c0 + j * kStride;
-      if (c >= K) continue;
-      F2 o[H];
+    for (int o = 16; o; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < H; ++i) o[i] = fma2(mul2(f[j][i], rs), wv[j][i], bv[j][i]);
-      store_piece<YT, VEC, SHIFT>(out + j * kStride, c, K, o);
+      for (int r = 0; r < R; ++r) sums[r] += __shfl_xor_sync(0xffffffffu, sums[r], o);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mine_mean[r] = sums[r] * inv_own;
+      const F2 nm = both(-mine_mean[r]);
+      F2 q = both(0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * kStride;
+        if (c >= K) continue;
+        const bool edge = SHIFT && (c < 0 || c + VEC > K);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          f[r][j][i] = add2(f[r][j][i], nm);
+          F2 v = f[r][j][i];
+          if (edge) {  // outside the row: no part in the variance
+            float a, d;
+            unpack2(v, a, d);
+            v = pack2(c + 2 * i >= 0 && c + 2 * i < K ? a : 0.f,
+                      c + 2 * i + 1 >= 0 && c + 2 * i + 1 < K ? d : 0.f);
+          }
+          q = fma2(v, v, q);
+        }
+      }
+      float lo, hi;
+      unpack2(q, lo, hi);
+      sq[r] = lo + hi;
     }
-    out += sk;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+    if constexpr (NW > 1) {
+      // (the slots of even and odd pairs alternate: a pair's writes cannot meet
+      // the reads of the pair before)
+      if ((tig & 31) == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) slots[par][group][tig >> 5][r] = make_float2(sums[r], sq[r]);
+      bar_named(1 + group, TPR);
+      float all[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2 v = slots[par][group][tig & (NW - 1)][r];
+        all[r] = sums[r] = v.x;
+        sq[r] = v.y;
+      }
+#pragma unroll
+      for (int o = NW / 2; o; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) all[r] += __shfl_xor_sync(0xffffffffu, all[r], o);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mean[r] = all[r] * inv_k;
+        const float d = sums[r] * inv_n - mean[r];
+        sq[r] = fmaf(n * d, d, sq[r]);
+      }
+#pragma unroll
+      for (int o = NW / 2; o; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) mean[r] = mine_mean[r];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (row + r >= rows) break;
+      rstd[r] = 1.f / sqrtf(sq[r] * inv_k + eps);
+      if (tig == 0) {
+        *pm = mean[r];
+        *pr = rstd[r];
+      }
+      pm += step, pr += step;
+      const F2 shift = both(mine_mean[r] - mean[r]), rs = both(rstd[r]);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * kStride;
+        if (c >= K) continue;
+        F2 o[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+          o[i] = fma2(mul2(add2(f[r][j][i], shift), rs), wv[j][i], bv[j][i]);
+        store_piece<YT, VEC, SHIFT>(out + j * kStride, c, K, o);
+      }
+      out += sk;
+    }
   }
   cp_async_wait<0>();
 }
