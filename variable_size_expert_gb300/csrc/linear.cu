@@ -598,10 +598,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + group * 64;
-      auto release = [&]() {  // the accumulator has been read
+      // The accumulator has been read (into registers, by loads that are done:
+      // no other memory is handed over, and a release at cluster scope would
+      // wait 0.5 us for this warp's stores in flight).
+      auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty_l + 8 * acc);
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_l + 8 * acc);
       };
       if (nblk == 0) release();  // nothing of the tile here
       // columns 32 b .. of the tile with the bias, v
@@ -1306,7 +1309,7 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
 // it takes 0.4 us + 17 ns a column (45 with its rows along the output's columns,
 // 70 where rows do not start on 16-byte boundaries), joining S pieces 0.5 us a
 // piece, 12 ns a column of the tile and 55 of a CTA's own; a 256 x 256 tile on a
-// pair 0.275 us a block and 1.2 us to store (4.6).  Measured on both sides:
+// pair 0.275 us a block and 1.2 us to store (4.6), 2.5 at least.  Both sides:
 // 4096 x 2048 x 64 in tiles of 32 columns 6.9 us, of 128 8.3; 64 x 4096 x 2048
 // in four pieces of 32 columns 7.0, in eight 7.9, whole 11; 4096 x 4096 x 1024
 // in tiles of 256 24.7, of 128 30.2, on pairs 25.4; 5135 x 1928 x 626 on pairs
@@ -1354,7 +1357,8 @@ CtaPlan plan_cta(const DenseProduct& d) {
 bool use_pairs(const DenseProduct& d) {
   const long long tiles = static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256);
   const long long pairs = num_sms() / 2;
-  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * (cdiv(d.Kc, BK) * 0.275 + (whole_rows(d) ? 1.2 : 4.6));
+  const double tile = std::max(cdiv(d.Kc, BK) * 0.275 + (whole_rows(d) ? 1.2 : 4.6), 2.5);
+  const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * tile;
   return us <= plan_cta(d).us;
 }
 
