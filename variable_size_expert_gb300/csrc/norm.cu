@@ -18,6 +18,15 @@
 // the end the groups of a block add up in shared memory in group order and
 // the block writes one partial row; a second kernel adds the partial rows in
 // block order.  No atomics: equal inputs give equal bits.
+//
+// Which kernel: few rows take a block per row (or rows) in the forward; many, and
+// all in the backward, the rings of the second half where rows are aligned or
+// shifted alike; rows of differing alignment or of more than 8192 elements the
+// kernels that keep a row in registers, of more than 16384 those that read a row
+// again.
+// Measured (inputs from HBM): forward 16384 x 2048 f32 to bf16 35.4 us (5.7 TB/s,
+// 84% of the measured copy rate), 16 x 7168 5.2 us (latency); backward 4096 x
+// 2048 20.6 us, 4.4 of it the column sums, 8191 x 7163 bf16 74.7 us (4.7 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -283,10 +292,14 @@ __global__ void __launch_bounds__(512)
 // ---------------------------------------------------------------- backward
 constexpr int kBwdThreads = 512;
 
-template <typename XT, typename YT, int VEC, int TPR, int NV>
+// By element, in registers: rows of differing alignment, and rows of more than
+// 8192 elements (8191 x 7163 bf16 with rows padded to 7170 133 us; shifted alike,
+// through the ring below, 75).
+template <typename XT, typename YT, int TPR, int NV>
 __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
     norm_bwd_kernel(const YT* dy, const XT* x, long long ldx, const void* w, bool w_f32,
                     const float* mean, const float* rstd, int T, int K, XT* dx, float* part) {
+  constexpr int VEC = 1;
   constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   __shared__ float slots[2][2][kGroups][TPR / 32];
@@ -996,8 +1009,15 @@ cudaError_t fwd(const FwdArgs& a, RowPath path, cudaStream_t st) {
     return launch_pdl(norm_fwd_long_kernel<XT, YT>, dim3(a.T), dim3(512), 0, st,
                       static_cast<const XT*>(a.x), a.ldx, a.w, a.b, a.w_f32, a.T, K, a.eps,
                       static_cast<YT*>(a.y), a.mean, a.rstd);
-  // The ring pays once it turns over: more rows than two to a group.
-  const bool many = static_cast<long long>(a.T) * K > 2LL * num_sms() * kBwdThreads * 16;
+  // The ring pays once it has turned over, counted in elements per thread and 16
+  // columns: after two rounds of rows, eight at the widths where a block takes
+  // two rows and hides one behind the other, one for shifted rows, which are
+  // read by element else.  Measured, block per row against ring, inputs in L2:
+  // 512 x 7168 bf16 7.5 and 6.1 us, 4096 x 7168 58 and 28; 4096 x 2048 f32 9.3
+  // and 11.2, 8192 x 2048 20.7 and 19.3; 8192 x 512 bf16 5.7 and 5.2; 1024 x 2047
+  // 7.3 and 6.9.
+  const int turns = path == kShifted ? 1 : K > 512 && K <= 2048 ? 8 : 2;
+  const bool many = static_cast<long long>(a.T) * K > static_cast<long long>(turns) * num_sms() * kBwdThreads * 16;
   if (many && path == kAligned && K <= 8192) return fwd_pipe<XT, YT, false>(a, st);
   if (many && path == kShifted && K <= 8192 - 7) return fwd_pipe<XT, YT, true>(a, st);
   if (path == kAligned) {
@@ -1027,12 +1047,12 @@ struct BwdArgs {
 
 template <typename XT, typename YT, int TPR>
 cudaError_t bwd_t(const BwdArgs& a, int* nb, cudaStream_t st) {
-  constexpr int VEC = 1, NV = 16;
+  constexpr int NV = 16;
   constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   *nb = std::min(norm_bwd_blocks(), cdiv(a.T, kGroups));
   const size_t smem = kGroups > 1 ? static_cast<size_t>(2) * a.K * 4 : 0;
-  return launch_pdl(norm_bwd_kernel<XT, YT, VEC, TPR, NV>, dim3(*nb), dim3(kThreads), smem, st,
+  return launch_pdl(norm_bwd_kernel<XT, YT, TPR, NV>, dim3(*nb), dim3(kThreads), smem, st,
                     static_cast<const YT*>(a.dy), static_cast<const XT*>(a.x), a.ldx, a.w, a.w_f32,
                     a.mean, a.rstd, a.T, a.K, static_cast<XT*>(a.dx), a.part);
 }
