@@ -210,10 +210,12 @@ __device__ __forceinline__ void stage_flush(uint32_t stg, int lane, bool vec, vo
     const int c = c0 + kq * (per / 8);
     uint8_t* at = static_cast<uint8_t*>(base) + (static_cast<long long>(row0 + rq) * N + c) * size;
     const long long step = 4LL * N * size;
+    float4 q[8];  // (read together: a store holds the next read back)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = ld_shared_v4(stg + sw128_offset(rq + 4 * j, kq));
 #pragma unroll
     for (int j = 0; j < 8; ++j, at += step)
-      if (row0 + rq + 4 * j < M && c < cend)
-        *reinterpret_cast<float4*>(at) = ld_shared_v4(stg + sw128_offset(rq + 4 * j, kq));
+      if (row0 + rq + 4 * j < M && c < cend) *reinterpret_cast<float4*>(at) = q[j];
   } else {
     // a row at a time, four bytes a lane (bf16: two elements, stored together
     // where the rows start on 4-byte boundaries)
@@ -222,7 +224,7 @@ __device__ __forceinline__ void stage_flush(uint32_t stg, int lane, bool vec, vo
     if (c < cend) {
 #pragma unroll 1
       for (int r0 = 0; r0 < 32 && row0 + r0 < M; r0 += 8) {
-        uint32_t u[8];  // (read together: a store holds the next read back)
+        uint32_t u[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
           u[r] = static_cast<uint32_t>(
@@ -811,8 +813,12 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
   }
+  if (threadIdx.x < slots) {
+    mbar_init(full + 8 * threadIdx.x, 1);
+    mbar_init(empty + 8 * threadIdx.x, 1);
+    fence_mbar_init();
+  }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < slots; ++s) mbar_init(full + 8 * s, 1), mbar_init(empty + 8 * s, 1);
     mbar_init(acc_full, 2);
     mbar_init(got, 1);
     *abort_flag = 0;
