@@ -719,7 +719,7 @@ struct CtaParams {
   int tmem_cols;
   int vec_out, vec_pre;  // stores in 16-byte pieces
 };
-constexpr int kCtaThreads = 256;  // warps 0-3 epilogue, 4 and 6 multiply, 5 and 7 load
+constexpr int kCtaThreads = 256;  // warps 4 and 6 multiply, 5 and 7 load; 0-3 or all finish
 constexpr int kCtaMeta = 256 + 1024;  // barriers, the tile's biases
 constexpr int kMaxSlots = 12;
 static_assert(8 * (2 * kMaxSlots + 2) + 8 <= 256, "barrier area");
@@ -913,10 +913,22 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
   }
 
   // ------------------------------------------------ epilogue
-  // thread = tile row (tensor memory lane); 4 columns at a time
-  const int tl = warp * 32 + lane;
+  // Thread = tile row (tensor memory lane).  Warps w and w + 4 can read the same
+  // quarter of tensor memory: for wide tiles they share its columns (2048 x 2048 x
+  // 2048 with a residual 22.7 to 19.0 us); of narrow ones, or with the tile's
+  // rows along the output's columns, warps 0-3 finish alone, without waiting for
+  // the others (16 x 7168 x 2048 8.0 to 7.1).
+  const int quad = warp & 3, half = warp >> 2;
+  const bool both = !c.swap && c.BN >= 128, epi_warp = both || warp < 4;
+  auto sync_epi = [&]() {
+    if (both)
+      __syncthreads();
+    else
+      bar_named(1, 128);
+  };
+  const int tl = quad * 32 + lane;
   const int row = m0 + tl;
-  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
   // 16 columns from j, the accumulators added up (of a single block only the
   // first warp's are written)
   auto load16 = [&](int j, float(&v)[16]) {
@@ -955,44 +967,44 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
   const uint32_t biases = meta + 256;
   float bias_row = 0.f, res[16];
   const int cend = std::min(c.Nc, n0 + own1);
-  if (warp < 4 && c.d.epilogue) {
-    if (p.bias && c.swap) {
+  if (epi_warp && c.d.epilogue && p.bias) {
+    if (c.swap) {
       if (row < c.Mr) bias_row = load_any(p.bias, p.bias_f32, row);
-    } else if (p.bias) {
-      for (int j = threadIdx.x; j < c.BN; j += 128)
+    } else {
+      for (int j = threadIdx.x; j < c.BN && warp < 4; j += 128)
         st_shared_f32(biases + 4 * j, n0 + j < c.Nc ? load_any(p.bias, p.bias_f32, n0 + j) : 0.f);
-      bar_named(1, 128);
+      sync_epi();
     }
   }
-  if (warp < 4 && c.swap) residual16(c, p, row, n0 + own0, cend, res);
+  if (c.swap && epi_warp) residual16(c, p, row, n0 + own0, cend, res);
   if (S > 1) cluster_wait();  // every CTA's barriers exist
   bool ok = false;
-  if (warp < 4) {
+  if (epi_warp) {
     ok = __all_sync(0xffffffffu, wait_bar(acc_full, 0, wc));
     tc_fence_after();
-    if (S > 1) {
-      // Each CTA finishes `per` of the tile's columns: every CTA lays its partial
-      // sums down over the ring (every MMA that read it is done) and sends each
-      // its columns in one copy, counted on its barrier.  (Sixteen bytes at a
-      // time from registers the receiver's count takes longer than the copy.)
+  }
+  if (S > 1 && epi_warp) {
+    // Each CTA finishes `per` of the tile's columns: every CTA lays its partial
+    // sums down over the ring (every MMA that read it is done) and sends each
+    // its columns in one copy, counted on its barrier.  (Sixteen bytes at a
+    // time from registers the receiver's count takes longer than the copy.)
 #pragma unroll 1
-      for (int j = 0; j < c.BN; j += 16) {
-        float v[16];
-        load16(j, v);
+    for (int j = 16 * half; j < c.BN; j += both ? 32 : 16) {
+      float v[16];
+      load16(j, v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          st_shared_v4(base + (((j >> 2) + i) * 128 + tl) * 16, v[4 * i], v[4 * i + 1], v[4 * i + 2],
-                       v[4 * i + 3]);
-      }
-      fence_proxy_async_smem();
-      bar_named(1, 128);
-      const int cols = min(c.per, c.BN - lane * c.per);  // of the CTA of rank `lane`
-      if (warp == 0 && lane < S && cols > 0)
-        bulk_to_cta(mapa_shared(recv + rank * c.per * 512, lane), base + lane * c.per * 512, cols * 512,
-                    mapa_shared(got, lane));
-      __syncwarp();
-      if (own1 > own0) ok = __all_sync(0xffffffffu, wait_bar(got, 0, wc)) && ok;
+      for (int i = 0; i < 4; ++i)
+        st_shared_v4(base + (((j >> 2) + i) * 128 + tl) * 16, v[4 * i], v[4 * i + 1], v[4 * i + 2],
+                     v[4 * i + 3]);
     }
+    fence_proxy_async_smem();
+    sync_epi();
+    const int cols = min(c.per, c.BN - lane * c.per);  // of the CTA of rank `lane`
+    if (warp == 0 && lane < S && cols > 0)
+      bulk_to_cta(mapa_shared(recv + rank * c.per * 512, lane), base + lane * c.per * 512, cols * 512,
+                  mapa_shared(got, lane));
+    __syncwarp();
+    if (own1 > own0) ok = __all_sync(0xffffffffu, wait_bar(got, 0, wc)) && ok;
   }
   // After this barrier what the CTA sent has arrived (every CTA has waited for
   // all that was sent to it): its ring is free, and it may leave.
@@ -1013,8 +1025,8 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
     // rows of the output: through staged blocks, over the pipeline's buffers;
     // the residual's blocks beside them
     const DenseProduct& d = c.d;
-    const uint32_t stg = base + warp * 4096;
-    const int row0 = m0 + warp * 32;
+    const uint32_t stg = base + warp * 4096, stg_res = stg + (both ? 32768 : 16384);
+    const int row0 = m0 + quad * 32;
     auto load32 = [&](int j, float(&v)[32]) {  // columns n0 + j .. with the bias
       float h[16];
 #pragma unroll
@@ -1041,7 +1053,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
     };
     const int per = d.out_f32 ? 32 : 64;
 #pragma unroll 1
-    for (int j0 = own0; j0 < own1 && n0 + j0 < d.N; j0 += per) {
+    for (int j0 = own0 + half * per; j0 < own1 && n0 + j0 < d.N; j0 += both ? 2 * per : per) {
       const int halves = std::min(per / 32, cdiv(own1 - j0, 32));
       if (d.epilogue && p.pre) {
 #pragma unroll 1
@@ -1060,7 +1072,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
         if (d.epilogue) {
           act_all<32>(p.act, v);
           if (p.residual)
-            add_residual(p, stg + 16384, lane, row0, d.M, n0 + j0 + 32 * h, d.N, v);
+            add_residual(p, stg_res, lane, row0, d.M, n0 + j0 + 32 * h, d.N, v);
         }
         if (d.out_f32)
           stage_f32(stg, lane, v);
@@ -1315,15 +1327,17 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
 // width and split (within 10% of most).  A tile of 128 x BN takes 0.125 us a
 // block of the contraction up to 32 columns (the handshakes), 0.19 at 128, 0.28
 // at 256 (its MMAs and operands); two CTAs on an SM share that rate.  Storing
-// it takes 0.4 us + 17 ns a column (45 with its rows along the output's columns,
-// 70 where rows do not start on 16-byte boundaries), joining S pieces 0.5 us a
-// piece, 12 ns a column of the tile and 55 of a CTA's own; a 256 x 256 tile on a
-// pair 0.275 us a block and 1.2 us to store (4.6), 2.5 at least.  Both sides:
-// 4096 x 2048 x 64 in tiles of 32 columns 6.9 us, of 128 8.3; 64 x 4096 x 2048
-// in four pieces of 32 columns 7.0, in eight 7.9, whole 11; 4096 x 4096 x 1024
-// in tiles of 256 24.7, of 128 30.2, on pairs 25.4; 5135 x 1928 x 626 on pairs
-// 19.5, in tiles of 256 28.5; 16 x 7168 x 2048 in four pieces 7.0, in six 7.35,
-// in eight 7.3.
+// it takes 0.4 us + 17 ns a column (14 a column of whole 128 where eight warps
+// store it; 45 and 90 with its rows along the output's columns; 70 and 56 where
+// rows do not start on 16-byte boundaries), joining S pieces 0.5 us a piece, 12
+// ns a column of the tile and 55 of a CTA's own; a further round of CTAs that have
+// an SM each starts 1.5 us late.  A 256 x 256 tile on a pair takes 0.275 us a
+// block and 1.2 us to store (4.6), 2.5 at least.  Measured on both sides: 4096 x
+// 2048 x 64 in tiles of 32 columns 6.9 us, of 128 8.3; 64 x 4096 x 2048 in four
+// pieces of 32 columns 7.0, in eight 7.9, whole 11; 4096 x 4096 x 1024 in tiles
+// of 256 24.7, of 128 30.2, on pairs 25.4; 13314 x 456 x 456 in tiles of 64 15.0,
+// of 128 20.4; 5135 x 1928 x 626 on pairs 18.9, in tiles of 256 28.5; 16 x 7168 x
+// 2048 in four pieces 7.0, in six 7.35, in eight 7.3.
 // Clusters of eight CTAs that fill an SM each find too few places; tiles wider
 // than 64 split at most four ways, wider than 128 not at all (their partial
 // sums would not fit over the ring).
@@ -1342,7 +1356,6 @@ CtaPlan plan_cta(const DenseProduct& d) {
     // (a few rows on the 128-row side would be read by every tile at once:
     // 6 x 216 x 4248 9 us against 5)
     if (mr < 128 && nc > mr) continue;
-    const double column = swap ? 0.045 : whole_rows(d) ? 0.017 : 0.07;
     int last = 0;
     for (int bn : {16, 32, 64, 96, 128, 192, 256}) {
       if (bn > 16 && nc <= last) break;
@@ -1351,12 +1364,15 @@ CtaPlan plan_cta(const DenseProduct& d) {
       for (int s : {1, 2, 3, 4, 8}) {
         if (s > nkb || s > (bn <= 64 ? 8 : bn <= 128 ? 4 : 1)) break;
         const int blocks = cdiv(nkb, s);
+        const double column = swap ? (bn <= 64 ? 0.045 : 0.09) : whole_rows(d) ? 0.017 : 0.07;
+        const double store = swap || bn < 128 ? column * bn : 0.8 * column * (128 * cdiv(bn, 128));
         const bool two = bn <= 64 || (bn <= 128 && (blocks + 1) * (OPER + 128 * bn) <= 110 * 1024);
         const long long ctas = tiles * s, slots = two ? 2LL * sms : sms;
         const double rounds = static_cast<double>((ctas + slots - 1) / slots);
         const double block = std::max(0.125, 0.1 + 0.0007 * bn) * (ctas > sms && two ? 2.05 : 1.0);
         const double join = s > 1 ? 0.5 * s + 0.012 * bn + 0.055 * cdiv(bn, s) : 0.0;
-        const double us = 2.0 + rounds * (blocks * block + 0.4 + column * bn + join);
+        const double us = 2.0 + rounds * (blocks * block + 0.4 + store + join) +
+                          (two ? 0.0 : 1.5 * (rounds - 1));
         if (us < best.us) best = CtaPlan{swap != 0, bn, s, us};
       }
     }
