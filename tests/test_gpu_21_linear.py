@@ -266,3 +266,26 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(y, ref) and all(torch.equal(i, j) for i, j in zip(got, want))
     assert mgg.read_status(st) == 0
+
+
+@pytest.mark.parametrize("T,K,N,act,bias,res,out", [
+    (2050, 8, 1000, "gelu", BF, F, BF),       # one block of the contraction: half of the accumulators
+    (1000, 72, 640, "silu", F, BF, F),        # two blocks, the second ragged
+    (1280, 2048, 96, "none", BF, F, F),       # narrow: pieces of the contraction
+    (1219, 2168, 360, "relu", F, BF, BF),
+    (2720, 5832, 224, "none", None, None, BF),
+    (1024, 1096, 1200, "gelu", BF, BF, BF),   # wide single tiles, finished by every warp
+    (1030, 1096, 1201, "silu", F, BF, BF),    # the same off 16-byte boundaries
+    (1000, 2056, 1208, "none", F, F, F),
+    (48, 4096, 2048, "gelu", BF, BF, BF),     # rows along the output's columns, in pieces
+    (8, 5000, 3000, "silu", F, F, F),
+])
+def test_tile_choices(T, K, N, act, bias, res, out):
+    x, W, b, r, g = _inputs(T, K, N, T + K, bias, res)
+    _, pre = _check_forward(x, W, b, r, act, out)
+    again, _ = _check_forward(x, W, b, r, act, out, save_pre=True)
+    assert torch.equal(again, _check_forward(x, W, b, r, act, out, save_pre=False)[0])
+    dy = torch.randn(T, N, generator=g, device=DEV).to(out)
+    dx, dW, _ = _check_backward(dy, x, W, pre, act, bias)
+    dx2, dW2, _ = _check_backward(dy, x, W, pre, act, bias)
+    assert torch.equal(dx, dx2) and torch.equal(dW, dW2)

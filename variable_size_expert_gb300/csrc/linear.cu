@@ -734,16 +734,6 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// A piece of shared memory into that of any CTA of the cluster, counted on that
-// CTA's mbarrier (both cluster addresses).
-__device__ __forceinline__ void bulk_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "r"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // Sixteen columns of one row of a swapped tile, which are output[col, row]:
 // consecutive lanes read and write consecutive elements.
 __device__ __forceinline__ void residual16(const CtaParams& c, const DenseParams& p, int row, int col0,
@@ -1001,8 +991,8 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
     sync_epi();
     const int cols = min(c.per, c.BN - lane * c.per);  // of the CTA of rank `lane`
     if (warp == 0 && lane < S && cols > 0)
-      bulk_to_cta(mapa_shared(recv + rank * c.per * 512, lane), base + lane * c.per * 512, cols * 512,
-                  mapa_shared(got, lane));
+      dsmem_copy(mapa_shared(recv + rank * c.per * 512, lane), base + lane * c.per * 512, cols * 512,
+                 mapa_shared(got, lane));
     __syncwarp();
     if (own1 > own0) ok = __all_sync(0xffffffffu, wait_bar(got, 0, wc)) && ok;
   }
