@@ -192,7 +192,6 @@ struct DenseParams {
   long long ldr;
   void* pre;             // bf16 z [M, N] or null
   bool pre_vec;          // rows on 16-byte boundaries (set by the launcher)
-  bool late;             // operands complete at the start: wait for the kernel before at the end
   int32_t* dev_status;
   long long wait_limit;
 };
@@ -235,10 +234,9 @@ cudaError_t launch_norm_fwd(const void* x, bool x_f32, long long ldx, const void
 cudaError_t launch_norm_bwd(const void* dy, bool y_f32, const void* x, bool x_f32, long long ldx,
                             const void* w, bool w_f32, const float* mean, const float* rstd, int T,
                             int K, void* dx, void* dw, void* db, float* part, cudaStream_t st);
-// out0[K] = column sums of part[0][nb][K], out1 (or null) of part[1][nb][K], in a fixed order;
-// late: part is complete when the kernel launched before this one has let it in
+// out0[K] = column sums of part[0][nb][K], out1 (or null) of part[1][nb][K], in a fixed order
 cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
-                               bool out_f32, bool late, cudaStream_t st);
+                               bool out_f32, cudaStream_t st);
 // select.cu
 cudaError_t launch_select(const void* logits, bool f32, long long ldl, int T, int E, int k,
                           bool softmax, const float* bias, int groups, int topk_groups,

@@ -485,8 +485,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *m.tmem_slot;
-  if (!p.late) pdl_wait();
-  pdl_trigger();  // (after the wait: see launch_dense_backward)
+  pdl_wait();
+  pdl_trigger();
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
   const int total = p.pr[0].tiles + p.pr[1].tiles;
   const uint32_t full_l = mapa_shared(m.full, 0);
@@ -698,7 +698,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     tmem_dealloc_cg2(tmem_base, 512);
   }
-  if (p.late) pdl_wait();
 }
 
 // ---------------------------------------------------------------- single-CTA tiles, split contraction
@@ -824,8 +823,8 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
   if (S > 1) cluster_arrive();  // this CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  if (!p.late) pdl_wait();
-  pdl_trigger();  // (after the wait: see launch_dense_backward)
+  pdl_wait();
+  pdl_trigger();
   const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
 
   // Warps 5 and 7 load, and warps 4 and 6 multiply, the even and the odd blocks:
@@ -1080,7 +1079,6 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem_base, c.tmem_cols);
   }
-  if (p.late) pdl_wait();
 }
 
 // ---------------------------------------------------------------- backward prep
@@ -1500,11 +1498,9 @@ cudaError_t launch_dense_forward(const DenseParams& p0, const DenseOperand& x,
 }
 
 // Up to four launches: dz, then dx and dW (one launch where both take 256 x
-// 256 tiles), then the bias gradient's sums.  All but dz depend on dz alone,
-// so only the first of them waits for what is before it; the later ones start
-// as soon as every block of the one before has passed its own wait (a kernel
-// lets its successor in after its wait, so dz is complete by then) and wait at
-// their end, which keeps the order of completion for whatever follows.
+// 256 tiles), then the bias gradient's sums.  Each waits for the one before:
+// dx, dW and the sums depend on dz alone, but only a grid's own wait makes an
+// earlier grid's writes visible to it.
 cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t st) {
   const bool direct = dy_is_operand(a);
   const int ldz = dz_ld(a.N);
@@ -1547,15 +1543,13 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
       ++n;
       return cudaSuccess;
     }
-    const cudaError_t r = launch_cta(p, n, oa, ob, st);
-    p.late = true;
-    return r;
+    return launch_cta(p, n, oa, ob, st);
   };
   if (a.dx) e = add(a.T, a.K, a.N, false, a.dx, z, W);
   if (e == cudaSuccess && a.dW) e = add(a.N, a.K, a.T, true, a.dW, z, x);
   if (e == cudaSuccess && n) e = launch_pairs(p, pa, pb, n, st);
   if (e == cudaSuccess && part_out)
-    e = launch_column_sums(part, parts, a.N, a.db, nullptr, a.db_f32, gemm, st);
+    e = launch_column_sums(part, parts, a.N, a.db, nullptr, a.db_f32, st);
   return e;
 }
 

@@ -903,10 +903,10 @@ __global__ void __launch_bounds__(256)
 // Partial rows part[2][nb][K] -> dw, db, added in block order: 32 columns
 // per block, 32 row lanes each summing every 32nd partial, then a tree.
 __global__ void __launch_bounds__(1024)
-    column_sums_kernel(const float* part, int nb, int K, void* dw, void* db, bool w_f32, bool late) {
+    column_sums_kernel(const float* part, int nb, int K, void* dw, void* db, bool w_f32) {
   __shared__ float s[32][33];
-  if (!late) pdl_wait();
   pdl_trigger();
+  pdl_wait();
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   const float* p = part + static_cast<long long>(blockIdx.y) * nb * K;
@@ -924,15 +924,14 @@ __global__ void __launch_bounds__(1024)
     else
       static_cast<__nv_bfloat16*>(out)[co] = __float2bfloat16_rn(v);
   }
-  if (late) pdl_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, void* out1,
-                               bool out_f32, bool late, cudaStream_t st) {
+                               bool out_f32, cudaStream_t st) {
   return launch_pdl(column_sums_kernel, dim3(cdiv(K, 32), out1 ? 2 : 1), dim3(1024), 0, st, part,
-                    nb, K, out0, out1, out_f32, late);
+                    nb, K, out0, out1, out_f32);
 }
 
 namespace {
@@ -1112,7 +1111,7 @@ cudaError_t bwd(const BwdArgs& a, RowPath path, cudaStream_t st) {
     else e = bwd_t<XT, YT, 1024>(a, &nb, st);
   }
   if (e != cudaSuccess) return e;
-  return launch_column_sums(a.part, nb, K, a.dw, a.db, a.w_f32, false, st);
+  return launch_column_sums(a.part, nb, K, a.dw, a.db, a.w_f32, st);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
