@@ -591,7 +591,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // block takes the whole staging area).
       const bool res_tma = epi && p.res_tma && row0 < d.M;
       auto fetch_res = [&](int c0) {
-        __syncwarp();  // the staging area has been read
+        // Every lane's reads and writes of the staging area come before the
+        // copy that overwrites it: they are ordinary accesses, the copy is of
+        // the async proxy, so the warp's barrier alone does not order them.
+        fence_proxy_async_smem();
+        __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(res_bar, p.res_f32 ? 4096 : 2048);
           tma_load_2d(stg, &maps.res, res_bar, c0, row0);
