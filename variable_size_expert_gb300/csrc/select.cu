@@ -540,7 +540,9 @@ __global__ void __launch_bounds__(kWarps * 32) select_bwd_kernel(const SelectBwd
   if (a.renorm) d = w * (g - dot / a.scale);
   if (!a.softmax && id >= 0) {
     const float l = open_logit<T>(lr[id]);
-    d *= 1.f - 1.f / (1.f + expf(-l));
+    // 1 - p = 1 / (1 + exp(l)): from a rounded p it has three digits left at a
+    // logit of 10 and none from 17 on
+    d *= 1.f / (1.f + expf(l));
   }
   __syncwarp();
   const unsigned same = __match_any_sync(kFull, id);
