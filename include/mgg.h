@@ -106,7 +106,8 @@ typedef enum {
 /* How mgg_select_experts scores the logits. */
 typedef enum { MGG_SCORE_SOFTMAX = 0, MGG_SCORE_SIGMOID = 1 } mgg_scoring;
 
-/* Activation of mgg_linear_forward: GELU is z (1 + erf(z / sqrt 2)) / 2. */
+/* Activation of mgg_linear_forward: GELU is z (1 + erf(z / sqrt 2)) / 2.  A NaN
+ * in z stays one through every activation. */
 typedef enum { MGG_ACT_NONE = 0, MGG_ACT_RELU = 1, MGG_ACT_SILU = 2, MGG_ACT_GELU = 3 } mgg_activation;
 
 /* Bits the kernels OR into *dev_status. */

@@ -102,8 +102,8 @@ __device__ __forceinline__ void act_n(float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     if constexpr (ACT == kActRelu) {
-      v[i] = fmaxf(v[i], 0.f);
-      v[i + 1] = fmaxf(v[i + 1], 0.f);
+      v[i] = v[i] < 0.f ? 0.f : v[i];  // (fmaxf would turn NaN into 0)
+      v[i + 1] = v[i + 1] < 0.f ? 0.f : v[i + 1];
     } else if constexpr (ACT == kActSilu) {
       v[i] *= sigmoid_f(v[i]);
       v[i + 1] *= sigmoid_f(v[i + 1]);
