@@ -665,7 +665,7 @@ mgg_status mgg_linear_forward(const void* x, int64_t ldx, const void* W, const v
 
 /*
  * Gradient of L = sum(dy * out) (the residual's gradient is dy itself):
- *   dz = dy * act'(pre)
+ *   dz = dy * act'(pre)   (ReLU: dy where pre > 0, else 0, whatever dy holds)
  *   dx [T, K] bf16 = dz W,  dW [N, K] bf16 = dz^T x,  dbias [N] (bias_dtype)
  *   = sum_t dz; each may be NULL and is then not computed.
  *   dy [T, N] (dy_dtype, rows lddy apart); pre [T, N] bf16, the forward's

@@ -35,3 +35,23 @@ def test_forward_keeps_nan(T, K, N, out):
     want = torch.where(z < 0, torch.zeros_like(z), z)
     assert torch.equal(torch.isnan(got[T - 1][cols]), torch.isnan(want))
     assert torch.equal(got[T - 1][cols].float().nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("T,K,N", SIZES + [(40, 64, 36), (40, 64, 38)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_backward_of_closed_units(T, K, N, dtype):
+    """An infinite or NaN dy at a closed unit (pre <= 0) is no part of any
+    gradient: the same bits as with dy = 0 there."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    x = torch.randn(T, K, generator=g, device=DEV).to(BF)
+    W = (torch.randn(N, K, generator=g, device=DEV) / K ** 0.5).to(BF)
+    pre = torch.randn(T, N, generator=g, device=DEV).to(BF)
+    pre[:, 0] = -0.0
+    dy = torch.randn(T, N, generator=g, device=DEV).to(dtype)
+    wild = torch.tensor([float("nan"), float("inf"), -float("inf")], device=DEV).to(dtype)
+    wild = wild[torch.randint(0, 3, (T, N), generator=g, device=DEV)]
+    closed = pre <= 0
+    want = mgg.linear_backward(torch.where(closed, torch.zeros_like(dy), dy), x, W, pre, "relu", F)
+    got = mgg.linear_backward(torch.where(closed, wild, dy), x, W, pre, "relu", F)
+    assert all(torch.isfinite(t).all() for t in want)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

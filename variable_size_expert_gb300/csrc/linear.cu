@@ -113,16 +113,20 @@ __device__ __forceinline__ void act_n(float (&v)[N]) {
     }
   }
 }
-// g = g act'(z)
+// g = g act'(z); of ReLU a choice, not a product: a closed unit passes nothing on,
+// whatever its g holds
 template <int ACT, int N>
 __device__ __forceinline__ void slope_n(float (&g)[N], const float (&z)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float z0 = z[i], z1 = N > 1 ? z[i + (N > 1)] : 0.f;
-    float s0, s1;
     if constexpr (ACT == kActRelu) {
-      s0 = z0 > 0.f ? 1.f : 0.f, s1 = z1 > 0.f ? 1.f : 0.f;
-    } else if constexpr (ACT == kActSilu) {
+      g[i] = z0 > 0.f ? g[i] : 0.f;
+      if constexpr (N > 1) g[i + 1] = z1 > 0.f ? g[i + 1] : 0.f;
+      continue;
+    }
+    float s0, s1;
+    if constexpr (ACT == kActSilu) {
       const float a = sigmoid_f(z0), b = sigmoid_f(z1);
       s0 = a * fmaf(z0, 1.f - a, 1.f), s1 = b * fmaf(z1, 1.f - b, 1.f);
     } else if constexpr (ACT == kActGelu) {
