@@ -10,11 +10,13 @@ last dimension contiguous); everything else is contiguous.
   layer_norm(x, weight, bias)              differentiable
   router(logits, k, ...)                   differentiable expert choice
   linear(x, W, bias, activation, residual) differentiable
-plus the *_forward / *_backward calls under them.
+plus the *_forward / *_backward calls under them.  The gradients have no
+gradients of their own: asking for them (create_graph) is an error.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 from .ops import _ids_i32, new_status
@@ -70,6 +72,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, ctx.bias)
@@ -122,6 +125,7 @@ class _Router(torch.autograd.Function):
         return ids, w
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, dw):
         logits, ids, w = ctx.saved_tensors
         d = select_experts_backward(dw.contiguous(), logits, ids, w, *ctx.opts)
@@ -182,6 +186,7 @@ class _Linear(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, W, pre = ctx.saved_tensors
         nx, nw, nb = ctx.needs_input_grad[:3]

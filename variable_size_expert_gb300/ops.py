@@ -19,6 +19,7 @@ import ctypes
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -292,6 +293,7 @@ class _MoEFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, W = ctx.saved_tensors
         dx, dW, dtopk = moe_backward(dy, x, W, ctx.routing, ctx.k)
