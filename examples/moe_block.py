@@ -47,16 +47,18 @@ class MoEBlock(torch.nn.Module):
         self.up, self.up_b = weight(shared, hidden), torch.nn.Parameter(torch.zeros(shared, device=device))
         self.down = weight(hidden, shared)
         self.register_buffer("balance", torch.zeros(experts, device=device))
+        # the word that every layer's kernels report errors in
+        self.register_buffer("status", mgg.new_status(device), persistent=False)
 
     def forward(self, x: torch.Tensor):
         """x [T, hidden] float32 (the residual stream) -> (out, expert_ids)."""
         h = mgg.layer_norm(x, self.norm_w, self.norm_b, out_dtype=torch.bfloat16)
-        logits = mgg.linear(h, self.gate, out_dtype=torch.float32)
+        logits = mgg.linear(h, self.gate, out_dtype=torch.float32, status=self.status)
         ids, w = mgg.router(logits, self.k, scoring="sigmoid", bias=self.balance, groups=self.groups,
-                            topk_groups=self.topk_groups)
-        y = mgg.moe(h, self.experts, ids, w)
-        s = mgg.linear(h, self.up, self.up_b, "gelu")
-        return mgg.linear(s, self.down, residual=x + y, out_dtype=torch.float32), ids
+                            topk_groups=self.topk_groups, status=self.status)
+        y = mgg.moe(h, self.experts, ids, w, status=self.status)
+        s = mgg.linear(h, self.up, self.up_b, "gelu", status=self.status)
+        return mgg.linear(s, self.down, residual=x + y, out_dtype=torch.float32, status=self.status), ids
 
     @torch.no_grad()
     def rebalance(self, ids: torch.Tensor, rate: float = 1e-3) -> torch.Tensor:
@@ -84,6 +86,8 @@ def train(tokens=4096, hidden=2048, shared=2048, experts=8, k=2, steps=20, lr=0.
                 p.grad = None
         load = block.rebalance(ids)
         losses.append(loss.item())
+        if error := mgg.read_status(block.status):
+            raise RuntimeError(f"step {step}: the kernels report error bits {error:#x}")
         log(f"step {step:3d}  loss {losses[-1]:.4f}  load {int(load.min())}..{int(load.max())}")
     return losses
 

@@ -68,9 +68,9 @@ def test_second_gradients_are_refused(host, monkeypatch):
     x = torch.randn(5, 8, generator=g, requires_grad=True)
     w, b = torch.randn(8, generator=g), torch.randn(8, generator=g)
     W = torch.randn(3, 8, generator=g)
-    monkeypatch.setattr(ops, "moe_forward", lambda x, W, ids, tw: (x @ W[0].t(), None))
-    monkeypatch.setattr(ops, "moe_backward", lambda dy, x, W, r, k: (dy @ W[0], torch.zeros_like(W),
-                                                                   torch.zeros(5, 1)))
+    monkeypatch.setattr(ops, "moe_forward", lambda x, W, ids, tw, **_: (x @ W[0].t(), None))
+    monkeypatch.setattr(ops, "moe_backward", lambda dy, x, W, r, k, **_: (dy @ W[0], torch.zeros_like(W),
+                                                                        torch.zeros(5, 1)))
     ids, tw = torch.zeros(5, 1, dtype=torch.int32), torch.ones(5, 1)
     for f in (lambda v: mgg.layer_norm(v, w, b), lambda v: mgg.router(v, 2)[1],
               lambda v: mgg.linear(v, W, None, "gelu"), lambda v: mgg.moe(v, W[None], ids, tw)):
@@ -83,3 +83,27 @@ def test_first_gradients(host):
     W = torch.ones(3, 8, requires_grad=True)
     mgg.linear(x, W).sum().backward()
     assert torch.equal(x.grad, torch.full((5, 8), 3.0)) and W.grad.shape == (3, 8)
+
+
+def test_one_status_word_serves_both_directions(host, monkeypatch):
+    """The word a caller gives reaches every kernel call that can report an
+    error, and no other word is made."""
+    st = torch.zeros(1, dtype=torch.int32)
+    made = []
+    for m in (block, ops):
+        monkeypatch.setattr(m, "new_status", lambda dev: made.append(dev) or torch.zeros(1).int())
+    seen = []
+    monkeypatch.setattr(ops, "moe_forward",
+                        lambda x, W, ids, tw, status=None: seen.append(status) or (x @ W[0].t(), None))
+    monkeypatch.setattr(ops, "moe_backward",
+                        lambda dy, x, W, r, k, status=None: seen.append(status) or
+                        (dy @ W[0], torch.zeros_like(W), torch.zeros(5, 1)))
+    x = torch.randn(5, 8, generator=torch.Generator().manual_seed(2), requires_grad=True)
+    W = torch.ones(8, 8)
+    mgg.linear(x, W, None, "gelu", status=st).sum().backward()
+    mgg.router(x, 2, status=st)[1].sum().backward()
+    mgg.moe(x, W[None], torch.zeros(5, 1).int(), torch.ones(5, 1), status=st).sum().backward()
+    words = host.status + seen
+    assert len(words) == 5 and all(w is st for w in words) and not made
+    mgg.linear(x, W).sum().backward()
+    assert len(made) == 2       # without one: a word for each direction

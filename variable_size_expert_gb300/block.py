@@ -117,10 +117,10 @@ def select_experts_backward(dtopk: torch.Tensor, logits: torch.Tensor, expert_id
 
 class _Router(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, k, scoring, bias, groups, topk_groups, renormalize, scale):
+    def forward(ctx, logits, k, scoring, bias, groups, topk_groups, renormalize, scale, status):
         ids, w = select_experts(logits, k, scoring, bias, groups, topk_groups, renormalize, scale)
         ctx.save_for_backward(logits, ids, w)
-        ctx.opts = (scoring, renormalize, scale)
+        ctx.opts = (scoring, renormalize, scale, status)
         ctx.mark_non_differentiable(ids)
         return ids, w
 
@@ -129,15 +129,17 @@ class _Router(torch.autograd.Function):
     def backward(ctx, _, dw):
         logits, ids, w = ctx.saved_tensors
         d = select_experts_backward(dw.contiguous(), logits, ids, w, *ctx.opts)
-        return d, None, None, None, None, None, None, None
+        return d, None, None, None, None, None, None, None, None
 
 
 def router(logits: torch.Tensor, k: int, scoring: str = "softmax",
            bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int = 1,
-           renormalize: bool = True, scale: float = 1.0):
+           renormalize: bool = True, scale: float = 1.0, status: torch.Tensor | None = None):
     """select_experts, its weights differentiable to the logits: the
-    expert_ids and topk_weights that ``moe`` takes."""
-    return _Router.apply(logits, k, scoring, bias, groups, topk_groups, renormalize, scale)
+    expert_ids and topk_weights that ``moe`` takes.  ``status``: the word the
+    backward reports errors in (without one they are dropped, and each
+    backward zeroes a word of its own)."""
+    return _Router.apply(logits, k, scoring, bias, groups, topk_groups, renormalize, scale, status)
 
 
 # ---------------------------------------------------------------- dense products
@@ -175,12 +177,13 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor,
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, bias, activation, residual, out_dtype):
+    def forward(ctx, x, W, bias, activation, residual, out_dtype, status):
         keep = activation != "none" and any(ctx.needs_input_grad[:3])
-        out = linear_forward(x, W, bias, activation, residual, out_dtype, save_pre=keep)
+        out = linear_forward(x, W, bias, activation, residual, out_dtype, save_pre=keep,
+                             status=status)
         out, pre = out if keep else (out, None)
         ctx.save_for_backward(x, W, pre)
-        ctx.activation = activation
+        ctx.activation, ctx.status = activation, status
         ctx.bias_dtype = bias.dtype if bias is not None and ctx.needs_input_grad[2] else None
         ctx.residual_dtype = residual.dtype if residual is not None else None
         return out
@@ -193,13 +196,17 @@ class _Linear(torch.autograd.Function):
         dx = dW = db = None
         if nx or nw or nb:
             dx, dW, db = linear_backward(dy.contiguous(), x, W, pre, ctx.activation,
-                                         ctx.bias_dtype, need_dx=nx, need_dW=nw)
+                                         ctx.bias_dtype, need_dx=nx, need_dW=nw,
+                                         status=ctx.status)
         dr = dy.to(ctx.residual_dtype) if ctx.needs_input_grad[4] else None
-        return dx, dW, db, None, dr, None
+        return dx, dW, db, None, dr, None, None
 
 
 def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
            activation: str = "none", residual: torch.Tensor | None = None,
-           out_dtype: torch.dtype | None = None) -> torch.Tensor:
-    """act(x W^T + bias) + residual, differentiable to x, W, bias and residual."""
-    return _Linear.apply(x, W, bias, activation, residual, out_dtype)
+           out_dtype: torch.dtype | None = None,
+           status: torch.Tensor | None = None) -> torch.Tensor:
+    """act(x W^T + bias) + residual, differentiable to x, W, bias and residual.
+    ``status``: the word that forward and backward report errors in (without
+    one they are dropped, and each call zeroes a word of its own)."""
+    return _Linear.apply(x, W, bias, activation, residual, out_dtype, status)

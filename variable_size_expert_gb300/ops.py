@@ -284,27 +284,29 @@ def moe_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, routing: Ro
 
 class _MoEFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, expert_ids, topk_weights):
-        y, r = moe_forward(x.detach(), W.detach(), expert_ids, topk_weights.detach())
+    def forward(ctx, x, W, expert_ids, topk_weights, status):
+        y, r = moe_forward(x.detach(), W.detach(), expert_ids, topk_weights.detach(), status=status)
         ctx.save_for_backward(x.detach(), W.detach())
         ctx.routing = r
         ctx.k = expert_ids.shape[1]
         ctx.w_dtype = topk_weights.dtype
+        ctx.status = status
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         x, W = ctx.saved_tensors
-        dx, dW, dtopk = moe_backward(dy, x, W, ctx.routing, ctx.k)
-        return dx.to(x.dtype), dW.to(W.dtype), None, dtopk.to(ctx.w_dtype)
+        dx, dW, dtopk = moe_backward(dy, x, W, ctx.routing, ctx.k, status=ctx.status)
+        return dx.to(x.dtype), dW.to(W.dtype), None, dtopk.to(ctx.w_dtype), None
 
 
 def moe(x: torch.Tensor, W: torch.Tensor, expert_ids: torch.Tensor,
-        topk_weights: torch.Tensor) -> torch.Tensor:
+        topk_weights: torch.Tensor, status: torch.Tensor | None = None) -> torch.Tensor:
     """Fused MoE layer y[t] = sum_j w[t,j] x[t] W_{ids[t,j]}^T, differentiable to
-    x, W and topk_weights ("grouped-gemm-moe", §Usage)."""
-    return _MoEFunction.apply(x, W, expert_ids, topk_weights)
+    x, W and topk_weights ("grouped-gemm-moe", §Usage).  ``status``: the word
+    that forward and backward report errors in."""
+    return _MoEFunction.apply(x, W, expert_ids, topk_weights, status)
 
 
 def grouped_gemm(a: torch.Tensor, W: torch.Tensor, group_sizes: torch.Tensor | None = None,
