@@ -6,7 +6,10 @@
 
 #include <initializer_list>
 
+#include <utility>
+
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -45,6 +48,21 @@ ScalarType dtype_or(PyObject* o, ScalarType otherwise) {
 void on_gpu(const Tensor& t) {
   if (!t.is_cuda()) fail(PyExc_ValueError, "%s must live on a CUDA device", "tensors");
 }
+
+// A call's tensors live on one GPU, that of its first argument, and the call
+// runs there whichever device is current: the library launches, asks for sizes
+// and zeroes on the current device.  Built before anything else is read off the
+// arguments (what is no tensor is refused later, by name).
+struct OnDevice {
+  OnDevice(const Tensor& x, std::initializer_list<std::pair<PyObject*, const char*>> others) {
+    if (!x.is_cuda()) return;  // (refused by its own check)
+    for (const auto& [o, what] : others)
+      if (THPVariable_Check(o) && THPVariable_Unpack(o).device() != x.device())
+        fail(PyExc_ValueError, "%s must be on the first argument's device", what);
+    guard.set_index(x.device().index());
+  }
+  c10::cuda::OptionalCUDAGuard guard;
+};
 
 // A matrix with contiguous rows, rows ld elements apart.
 struct Rows {
@@ -167,7 +185,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // x, weight, bias, eps, out_dtype
 PyObject* layer_norm_forward(PyObject* const* a) {
-  const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
+  const Tensor& x = tensor(a[0], "x");
+  const OnDevice dev(x, {{a[1], "weight"}, {a[2], "bias"}});
+  const Tensor& w = tensor(a[1], "weight");
   const Rows r = rows_of(x, "x");
   const void* wp = dense(w, {r.cols}, "weight");
   const void* bp = nullptr;
@@ -191,7 +211,9 @@ PyObject* layer_norm_forward(PyObject* const* a) {
 
 // dy, x, weight, mean, rstd, bias, workspace
 PyObject* layer_norm_backward(PyObject* const* a) {
-  const Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &w = tensor(a[2], "weight");
+  const Tensor& dy = tensor(a[0], "dy");
+  const OnDevice dev(dy, {{a[1], "x"}, {a[2], "weight"}, {a[3], "mean"}, {a[4], "rstd"}, {a[6], "workspace"}});
+  const Tensor &x = tensor(a[1], "x"), &w = tensor(a[2], "weight");
   const Rows r = rows_of(x, "x");
   const void* gp = dense(dy, {r.rows, r.cols}, "dy");
   const void* wp = dense(w, {r.cols}, "weight");
@@ -211,6 +233,7 @@ PyObject* layer_norm_backward(PyObject* const* a) {
 // logits, k, scoring, bias, groups, topk_groups, renormalize, scale
 PyObject* select_experts(PyObject* const* a) {
   const Tensor& l = tensor(a[0], "logits");
+  const OnDevice dev(l, {{a[3], "bias"}});
   const Rows r = rows_of(l, "logits");
   const int k = static_cast<int>(integer(a[1], "k"));
   const float* bp = a[3] == Py_None ? nullptr : dense_f32(tensor(a[3], "bias"), {r.cols}, "bias");
@@ -229,7 +252,9 @@ PyObject* select_experts(PyObject* const* a) {
 
 // dtopk, logits, expert_ids, topk_weights, scoring, renormalize, scale, status
 PyObject* select_experts_backward(PyObject* const* a) {
-  const Tensor &g = tensor(a[0], "dtopk"), &l = tensor(a[1], "logits"), &ids = tensor(a[2], "expert_ids"),
+  const Tensor& g = tensor(a[0], "dtopk");
+  const OnDevice dev(g, {{a[1], "logits"}, {a[2], "expert_ids"}, {a[3], "topk_weights"}, {a[7], "status"}});
+  const Tensor &l = tensor(a[1], "logits"), &ids = tensor(a[2], "expert_ids"),
                &w = tensor(a[3], "topk_weights");
   const Rows r = rows_of(l, "logits");
   if (ids.dim() != 2 || ids.scalar_type() != at::kInt)
@@ -264,7 +289,9 @@ LinearArgs linear_args(const Tensor& x, const Tensor& W) {
 
 // x, W, bias, activation, residual, out_dtype, save_pre, status, out
 PyObject* linear_forward(PyObject* const* a) {
-  const Tensor &x = tensor(a[0], "x"), &W = tensor(a[1], "W");
+  const Tensor& x = tensor(a[0], "x");
+  const OnDevice dev(x, {{a[1], "W"}, {a[2], "bias"}, {a[4], "residual"}, {a[7], "status"}, {a[8], "out"}});
+  const Tensor& W = tensor(a[1], "W");
   const LinearArgs l = linear_args(x, W);
   const int T = l.x.rows;
   const void* bp = nullptr;
@@ -306,7 +333,9 @@ PyObject* linear_forward(PyObject* const* a) {
 
 // dy, x, W, pre, activation, bias_dtype, need_dx, need_dW, status, workspace
 PyObject* linear_backward(PyObject* const* a) {
-  const Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &W = tensor(a[2], "W");
+  const Tensor& dy = tensor(a[0], "dy");
+  const OnDevice dev(dy, {{a[1], "x"}, {a[2], "W"}, {a[3], "pre"}, {a[8], "status"}, {a[9], "workspace"}});
+  const Tensor &x = tensor(a[1], "x"), &W = tensor(a[2], "W");
   const LinearArgs l = linear_args(x, W);
   const int T = l.x.rows, K = l.x.cols;
   const Rows g = rows_of(dy, "dy");
