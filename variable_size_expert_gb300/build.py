@@ -62,11 +62,13 @@ def _compile(src: str, extra: list[str], verbose_ptxas: bool) -> str:
 
 
 def _compile_host() -> str:
-    """csrc/host.cpp against torch's headers -> _build/host.o"""
+    """csrc/host.cpp against torch's headers -> _build/host-<torch>-<python>.o:
+    an object is good for the versions that it was compiled against alone."""
     import sysconfig
 
     import torch
-    src, obj = os.path.join(CSRC, "host.cpp"), os.path.join(BUILD, "host.o")
+    versions = f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}"
+    src, obj = os.path.join(CSRC, "host.cpp"), os.path.join(BUILD, f"host-{versions}.o")
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "mgg.h")))
     if os.path.exists(obj) and os.path.getmtime(obj) > newest:
         return obj
