@@ -436,9 +436,10 @@ __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
 // elements past a boundary), a thread takes the aligned pieces that cover the
 // row, whose columns start at -m; pieces at the row's ends overlap the rows
 // beside it (never another 16-byte word than the row's own) and their foreign
-// elements are zeroed on reading.  The residue repeats every VEC / gcd(K, VEC)
-// rows, a divisor of 8: each group takes rows of one residue, so that its
-// threads keep their columns, the weights of them in registers.
+// elements are zeroed on reading.  The groups of all blocks take the rows in
+// turn and blocks come in eights (ring_blocks), so a group's rows lie a multiple
+// of 8 apart, hence of VEC: they share one residue, and its threads keep their
+// columns, the weights of them in registers.
 template <int BYTES>
 __device__ __forceinline__ void cp_async_piece(uint32_t dst, const void* src) {
   if constexpr (BYTES == 16)
@@ -499,8 +500,7 @@ __host__ __device__ constexpr int pipe_depth() {
 template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kBwdThreads)
     norm_bwd_pipe_kernel(const YT* dy, const XT* x, long long ldx, const void* w, bool w_f32,
-                         const float* mean, const float* rstd, int T, int K, XT* dx, float* part,
-                         int period) {
+                         const float* mean, const float* rstd, int T, int K, XT* dx, float* part) {
   constexpr int kThreads = kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   constexpr int XB = VEC * sizeof(XT), YB = VEC * sizeof(YT), H = VEC / 2;
@@ -513,9 +513,8 @@ __global__ void __launch_bounds__(kBwdThreads)
   uint8_t* mine_y = ring + kThreads * XB + threadIdx.x * YB;
   pdl_trigger();
   pdl_wait();
-  const int gid = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
-  // this group's rows: gid mod period, then every step-th (a multiple of period)
-  const int first = SHIFT ? gid % period + period * (gid / period) : gid;
+  // this group's rows: first, then every step-th
+  const int first = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
   const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
   const int rows = first < T ? (T - 1 - first) / step + 1 : 0;
   const int c0 = tig * VEC - m;      // column of the first piece; piece j: + j * kStride
@@ -669,8 +668,7 @@ constexpr int kFwdDepth = 6;
 template <typename XT, typename YT, int VEC, int TPR, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kBwdThreads)
     norm_fwd_pipe_kernel(const XT* x, long long ldx, const void* w, const void* b, bool w_f32,
-                         int T, int K, float eps, YT* y, float* mean_out, float* rstd_out,
-                         int period) {
+                         int T, int K, float eps, YT* y, float* mean_out, float* rstd_out) {
   constexpr int kThreads = kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   constexpr int XB = VEC * sizeof(XT), H = VEC / 2;
@@ -682,8 +680,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   uint8_t* mine = ring + threadIdx.x * XB;
   pdl_trigger();
   pdl_wait();
-  const int gid = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
-  const int first = SHIFT ? gid % period + period * (gid / period) : gid;
+  const int first = blockIdx.x * kGroups + group, step = gridDim.x * kGroups;
   const int m = SHIFT ? static_cast<int>((static_cast<long long>(first) * K) % VEC) : 0;
   const float inv_k = 1.f / K;
   const int rows = first < T ? (T - 1 - first) / step + 1 : 0;
@@ -959,11 +956,10 @@ cudaError_t fwd_t(const FwdArgs& a, cudaStream_t st) {
 // the same residue per row.
 enum RowPath { kByElement, kAligned, kShifted };
 
-// Rows between repeats of the residue: VEC / gcd(K, VEC).
-int residue_period(int K, int vec) {
-  int p = vec;
-  while (p > 1 && (static_cast<long long>(K) * (p / 2)) % vec == 0) p /= 2;
-  return p;
+// Blocks of the rings: a multiple of eight (see SHIFT above), one an SM at most,
+// no more than the rows need.
+int ring_blocks(int T, int groups) {
+  return std::min(norm_bwd_blocks(), cdiv(cdiv(T, groups), 8) * 8);
 }
 
 template <typename K>
@@ -986,10 +982,9 @@ cudaError_t fwd_pipe_t(const FwdArgs& a, cudaStream_t st) {
   static bool done[64] = {};
   const cudaError_t e = allow_ring(kern, done);
   if (e != cudaSuccess) return e;
-  const int blocks = std::max(8, std::min(num_sms() / 8 * 8, cdiv(cdiv(a.T, kGroups), 8) * 8));
-  return launch_pdl(kern, dim3(blocks), dim3(kBwdThreads), smem, st, static_cast<const XT*>(a.x),
-                    a.ldx, a.w, a.b, a.w_f32, a.T, a.K, a.eps, static_cast<YT*>(a.y), a.mean, a.rstd,
-                    SHIFT ? residue_period(a.K, VEC) : 1);
+  return launch_pdl(kern, dim3(ring_blocks(a.T, kGroups)), dim3(kBwdThreads), smem, st,
+                    static_cast<const XT*>(a.x), a.ldx, a.w, a.b, a.w_f32, a.T, a.K, a.eps,
+                    static_cast<YT*>(a.y), a.mean, a.rstd);
 }
 template <typename XT, typename YT, bool SHIFT>
 cudaError_t fwd_pipe(const FwdArgs& a, cudaStream_t st) {
@@ -1063,8 +1058,7 @@ cudaError_t bwd_pipe_t(const BwdArgs& a, int* nb, cudaStream_t st) {
   constexpr int kThreads = kBwdThreads;
   constexpr int kGroups = kThreads / TPR;
   constexpr size_t kRing = static_cast<size_t>(pipe_depth<XT, YT>()) * NV * kThreads * VEC * (sizeof(XT) + sizeof(YT));
-  // a multiple of eight blocks, so that the groups divide by any period
-  *nb = std::max(8, std::min(norm_bwd_blocks(), cdiv(cdiv(a.T, kGroups), 8) * 8));
+  *nb = ring_blocks(a.T, kGroups);
   const size_t smem = std::max(kRing, static_cast<size_t>(2) * kGroups * a.K * 4);
   auto kern = norm_bwd_pipe_kernel<XT, YT, VEC, TPR, NV, SHIFT>;
   static bool done[64] = {};
@@ -1072,8 +1066,7 @@ cudaError_t bwd_pipe_t(const BwdArgs& a, int* nb, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(*nb), dim3(kThreads), smem, st, static_cast<const YT*>(a.dy),
                     static_cast<const XT*>(a.x), a.ldx, a.w, a.w_f32, a.mean, a.rstd, a.T, a.K,
-                    static_cast<XT*>(a.dx), a.part,
-                    SHIFT ? residue_period(a.K, VEC) : 1);
+                    static_cast<XT*>(a.dx), a.part);
 }
 // K: the row's columns, with SHIFT those of the pieces that cover it
 template <typename XT, typename YT, bool SHIFT>
