@@ -1375,12 +1375,12 @@ CtaPlan plan_cta(const DenseProduct& d) {
   }
   return best;
 }
-bool use_pairs(const DenseProduct& d) {
+bool use_pairs(const DenseProduct& d, const CtaPlan& cta) {
   const long long tiles = static_cast<long long>(cdiv(d.M, 256)) * cdiv(d.N, 256);
   const long long pairs = num_sms() / 2;
   const double tile = std::max(cdiv(d.Kc, BK) * 0.275 + (whole_rows(d) ? 1.2 : 4.6), 2.5);
   const double us = 6.4 + static_cast<double>((tiles + pairs - 1) / pairs) * tile;
-  return us <= plan_cta(d).us;
+  return us <= cta.us;
 }
 
 template <bool A_MN, bool B_MN, bool SPLIT>
@@ -1412,9 +1412,8 @@ cudaError_t launch_cta_t(const CtaMaps& maps, const CtaParams& c, const DensePar
                       : launch_cta_s<A_MN, B_MN, false>(maps, c, p, st);
 }
 
-cudaError_t launch_cta(const DenseParams& p, int q, const DenseOperand& a, const DenseOperand& b,
-                       cudaStream_t st) {
-  const CtaPlan plan = plan_cta(p.pr[q]);
+cudaError_t launch_cta(const DenseParams& p, int q, const CtaPlan& plan, const DenseOperand& a,
+                       const DenseOperand& b, cudaStream_t st) {
   CtaParams c{};
   c.d = p.pr[q];
   c.swap = plan.swap;
@@ -1499,10 +1498,11 @@ size_t dense_bwd_ws_bytes(int T, int N) {
          round256(static_cast<size_t>(max_partials(T, N)) * N * 4);
 }
 
-cudaError_t launch_dense_forward(const DenseParams& p0, const DenseOperand& x,
+cudaError_t launch_dense_forward(const DenseParams& p, const DenseOperand& x,
                                  const DenseOperand& W, cudaStream_t st) {
-  DenseParams p = p0;
-  return use_pairs(p.pr[0]) ? launch_pairs(p, &x, &W, 1, st) : launch_cta(p, 0, x, W, st);
+  const CtaPlan plan = plan_cta(p.pr[0]);
+  return use_pairs(p.pr[0], plan) ? launch_pairs(p, &x, &W, 1, st)
+                                  : launch_cta(p, 0, plan, x, W, st);
 }
 
 // Up to four launches: dz, then dx and dW (one launch where both take 256 x
@@ -1547,11 +1547,12 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
     d.M = M, d.N = N, d.Kc = Kc, d.a_mn = a_mn, d.b_mn = true, d.out = out;
     p.pr[n] = d;
     pa[n] = oa, pb[n] = ob;
-    if (use_pairs(d)) {
+    const CtaPlan plan = plan_cta(d);
+    if (use_pairs(d, plan)) {
       ++n;
       return cudaSuccess;
     }
-    return launch_cta(p, n, oa, ob, st);
+    return launch_cta(p, n, plan, oa, ob, st);
   };
   if (a.dx) e = add(a.T, a.K, a.N, false, a.dx, z, W);
   if (e == cudaSuccess && a.dW) e = add(a.N, a.K, a.T, true, a.dW, z, x);
