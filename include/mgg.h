@@ -103,8 +103,15 @@ typedef enum {
   MGG_OP_LINEAR_BACKWARD = 8
 } mgg_op;
 
-/* How mgg_select_experts scores the logits. */
-typedef enum { MGG_SCORE_SOFTMAX = 0, MGG_SCORE_SIGMOID = 1 } mgg_scoring;
+/* How mgg_select_experts scores the logits.  One of the MGG_GROUP_ values may be
+ * or-ed into the scoring and says how a group of experts is scored; without one
+ * sigmoid takes the sum of the group's two best keys, softmax its best. */
+typedef enum {
+  MGG_SCORE_SOFTMAX = 0,
+  MGG_SCORE_SIGMOID = 1,
+  MGG_GROUP_BEST = 0x100,
+  MGG_GROUP_TWO_BEST = 0x200
+} mgg_scoring;
 
 /* Activation of mgg_linear_forward: GELU is z (1 + erf(z / sqrt 2)) / 2.  A NaN
  * in z stays one through every activation. */
@@ -602,12 +609,14 @@ mgg_status mgg_layer_norm_backward(const void* dy, mgg_dtype y_dtype, const void
  * The choice of k experts per token and their weights, from the gate's
  * logits [T, E] (dtype MGG_BF16 or MGG_F32, rows ldl apart):
  *   softmax: p = softmax over the token's unmasked logits; the experts are
- *            ordered by logit (with a bias: by p + bias)
+ *            ordered by logit (with a bias or MGG_GROUP_TWO_BEST over groups: by
+ *            p + bias)
  *   sigmoid: p = 1 / (1 + exp(-logit)); ordered by p (+ bias)
  *   bias [E] f32 or NULL: moves the order only, never the weights.
  *   groups > 1: the experts form `groups` equal runs; a group's score is its
- *   best expert's key (softmax) or the sum of its two best (sigmoid), and
- *   only the topk_groups best groups take part.
+ *   best expert's key (softmax, MGG_GROUP_BEST) or the sum of its two best
+ *   (sigmoid, MGG_GROUP_TWO_BEST; of one where no other is left), and only the
+ *   topk_groups best groups take part.
  *   expert_ids   [T, k] int32: the k best, best first; equal keys (and equal
  *                group scores) go to the lowest index
  *   topk_weights [T, k] f32: scale * p, or scale * p / (sum of the chosen p)
@@ -619,7 +628,8 @@ mgg_status mgg_layer_norm_backward(const void* dy, mgg_dtype y_dtype, const void
  * Errors: MGG_ERR_INVALID_ARG (null, T < 0, E < 1, E > MGG_MAX_EXPERTS,
  * k < 1, k > MGG_MAX_TOPK, k > experts in topk_groups groups, ldl < E,
  * groups < 1 or > 32 or not dividing E, topk_groups outside 1..groups, scale
- * not finite or not positive, unknown scoring), MGG_ERR_DTYPE,
+ * not finite or not positive, unknown scoring, both MGG_GROUP_ values),
+ * MGG_ERR_DTYPE,
  * MGG_ERR_ALIGNMENT, MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
  */
 mgg_status mgg_select_experts(const void* logits, mgg_dtype dtype, int64_t ldl, int T, int E, int k,

@@ -40,6 +40,8 @@ MGG_OP_LINEAR_BACKWARD = 8
 # mgg_scoring
 MGG_SCORE_SOFTMAX = 0
 MGG_SCORE_SIGMOID = 1
+MGG_GROUP_BEST = 0x100
+MGG_GROUP_TWO_BEST = 0x200
 # mgg_activation
 MGG_ACT_NONE = 0
 MGG_ACT_RELU = 1

@@ -27,6 +27,7 @@ __all__ = [
 ]
 
 _SCORING = {"softmax": L.MGG_SCORE_SOFTMAX, "sigmoid": L.MGG_SCORE_SIGMOID}
+_GROUP_SCORE = {None: 0, "best": L.MGG_GROUP_BEST, "two best": L.MGG_GROUP_TWO_BEST}
 _ACTIVATION = {"none": L.MGG_ACT_NONE, "relu": L.MGG_ACT_RELU, "silu": L.MGG_ACT_SILU,
                "gelu": L.MGG_ACT_GELU}
 
@@ -94,14 +95,18 @@ def _scoring(name: str) -> int:
 
 def select_experts(logits: torch.Tensor, k: int, scoring: str = "softmax",
                    bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int = 1,
-                   renormalize: bool = True, scale: float = 1.0):
+                   renormalize: bool = True, scale: float = 1.0, group_score: str | None = None):
     """The k experts of every token and their weights, from the gate's logits
     [T, E].  Returns (expert_ids [T, k] int32, topk_weights [T, k] float32),
     best first, equal keys to the lowest expert; ``bias`` [E] float32 moves
     the choice, not the weights.  -inf, NaN or the dtype's lowest value mask
-    an expert (mgg_select_experts)."""
-    return _host.select_experts(logits, k, _scoring(scoring), bias, groups, topk_groups, renormalize,
-                                scale)
+    an expert.  ``group_score``: a group counts by its "best" key or the sum
+    of its "two best" (with softmax of the scores, not the logits); None:
+    two best with sigmoid, best with softmax (mgg_select_experts)."""
+    if group_score not in _GROUP_SCORE:
+        raise ValueError("group_score must be 'best', 'two best' or None")
+    return _host.select_experts(logits, k, _scoring(scoring) | _GROUP_SCORE[group_score], bias, groups,
+                                topk_groups, renormalize, scale)
 
 
 def select_experts_backward(dtopk: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor,
@@ -117,8 +122,10 @@ def select_experts_backward(dtopk: torch.Tensor, logits: torch.Tensor, expert_id
 
 class _Router(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, k, scoring, bias, groups, topk_groups, renormalize, scale, status):
-        ids, w = select_experts(logits, k, scoring, bias, groups, topk_groups, renormalize, scale)
+    def forward(ctx, logits, k, scoring, bias, groups, topk_groups, renormalize, scale, status,
+                group_score):
+        ids, w = select_experts(logits, k, scoring, bias, groups, topk_groups, renormalize, scale,
+                                group_score)
         ctx.save_for_backward(logits, ids, w)
         ctx.opts = (scoring, renormalize, scale, status)
         ctx.mark_non_differentiable(ids)
@@ -129,17 +136,19 @@ class _Router(torch.autograd.Function):
     def backward(ctx, _, dw):
         logits, ids, w = ctx.saved_tensors
         d = select_experts_backward(dw.contiguous(), logits, ids, w, *ctx.opts)
-        return d, None, None, None, None, None, None, None, None
+        return d, None, None, None, None, None, None, None, None, None
 
 
 def router(logits: torch.Tensor, k: int, scoring: str = "softmax",
            bias: torch.Tensor | None = None, groups: int = 1, topk_groups: int = 1,
-           renormalize: bool = True, scale: float = 1.0, status: torch.Tensor | None = None):
+           renormalize: bool = True, scale: float = 1.0, status: torch.Tensor | None = None,
+           group_score: str | None = None):
     """select_experts, its weights differentiable to the logits: the
     expert_ids and topk_weights that ``moe`` takes.  ``status``: the word the
     backward reports errors in (without one they are dropped, and each
     backward zeroes a word of its own)."""
-    return _Router.apply(logits, k, scoring, bias, groups, topk_groups, renormalize, scale, status)
+    return _Router.apply(logits, k, scoring, bias, groups, topk_groups, renormalize, scale, status,
+                         group_score)
 
 
 # ---------------------------------------------------------------- dense products

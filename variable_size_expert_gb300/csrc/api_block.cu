@@ -89,8 +89,13 @@ mgg_status mgg_select_experts(const void* logits, mgg_dtype dtype, int64_t ldl, 
                               int renormalize, float scale, int32_t* expert_ids,
                               float* topk_weights, void* stream) {
   const NvtxRange nvtx("mgg_select_experts");
+  const int group_score = scoring & (MGG_GROUP_BEST | MGG_GROUP_TWO_BEST);
+  scoring = static_cast<mgg_scoring>(scoring & ~(MGG_GROUP_BEST | MGG_GROUP_TWO_BEST));
   mgg_status s = check_select(dtype, ldl, T, E, k, scoring, scale);
   if (s != MGG_OK) return s;
+  if (group_score == (MGG_GROUP_BEST | MGG_GROUP_TWO_BEST)) return MGG_ERR_INVALID_ARG;
+  const bool two_best =
+      groups > 1 && (group_score ? group_score == MGG_GROUP_TWO_BEST : scoring == MGG_SCORE_SIGMOID);
   if (groups < 1 || groups > 32 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
       k > topk_groups * (E / groups))
     return MGG_ERR_INVALID_ARG;
@@ -102,7 +107,7 @@ mgg_status mgg_select_experts(const void* logits, mgg_dtype dtype, int64_t ldl, 
   s = check_arch();
   if (s != MGG_OK) return s;
   return from_cuda(launch_select(logits, dtype == MGG_F32, ldl, T, E, k,
-                                 scoring == MGG_SCORE_SOFTMAX, bias, groups, topk_groups,
+                                 scoring == MGG_SCORE_SOFTMAX, bias, groups, topk_groups, two_best,
                                  renormalize != 0, scale, expert_ids, topk_weights,
                                  static_cast<cudaStream_t>(stream)));
 }

@@ -240,7 +240,8 @@ cudaError_t launch_column_sums(const float* part, int nb, int K, void* out0, voi
 // select.cu
 cudaError_t launch_select(const void* logits, bool f32, long long ldl, int T, int E, int k,
                           bool softmax, const float* bias, int groups, int topk_groups,
-                          bool renorm, float scale, int32_t* ids, float* weights, cudaStream_t st);
+                          bool two_best, bool renorm, float scale, int32_t* ids, float* weights,
+                          cudaStream_t st);
 cudaError_t launch_select_bwd(const float* g, const void* logits, bool f32, long long ldl,
                               const int32_t* ids, const float* w, int T, int E, int k,
                               bool softmax, bool renorm, float scale, void* out,

@@ -3,7 +3,8 @@
 // Per token (one warp): scores p_e, selection keys, the best topk_groups
 // groups, the k best keys, the weights of the chosen.
 //   softmax: p = softmax over the unmasked logits; key = logit, or p + bias
-//            with a bias (the logit orders as p does, without p's rounding)
+//            with a bias (the logit orders as p does, without p's rounding) or
+//            where two keys are added up
 //   sigmoid: p = 1 / (1 + exp(-logit)); key = p (+ bias)
 // A logit that is NaN, -inf or its type's lowest value masks the expert; +inf
 // counts as the largest finite value.  Keys are compared as order-preserving
@@ -111,6 +112,7 @@ struct SelectArgs {
   int T, E, k;
   bool softmax;
   int groups, topk_groups;
+  bool two_best;  // a group's score: the sum of its two best keys, else its best
   bool renorm;
   float scale;
   int32_t* ids;
@@ -126,7 +128,7 @@ __device__ __forceinline__ uint32_t keep_groups(const SelectArgs& a, int e0, int
   const int gs = a.E / a.groups;
   const int L = gs / V;  // lanes per group, where that divides evenly
   auto score = [&](uint32_t b1, uint32_t b2) {
-    return !a.softmax && b1 > 1u && b2 > 1u ? order_key(key_value(b1) + key_value(b2)) : b1;
+    return a.two_best && b1 > 1u && b2 > 1u ? order_key(key_value(b1) + key_value(b2)) : b1;
   };
   if (gs % V == 0 && (L & (L - 1)) == 0) {
     // a lane's experts are of one group and the group's lanes an aligned
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const SelectArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       p[i] *= inv;
-      if (a.bias && key[i] > 1u) key[i] = order_key(p[i] + bias[i]);
+      if ((a.bias || a.two_best) && key[i] > 1u) key[i] = order_key(p[i] + bias[i]);
     }
   } else {
 #pragma unroll
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(kWideWarps * 32) select_wide_kernel(const Sele
     top = fmaxf(top, l);
   }
   float inv = 1.f;
+  const bool by_logit = a.softmax && !a.bias && !a.two_best;
   if (a.softmax) {
     top = warp_max(top);
     float sum = 0.f;
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kWideWarps * 32) select_wide_kernel(const Sele
       if (l < -87.f) s = expf(l);  // (as above)
     }
     p[e] = s;
-    key[e] = order_key(l > -INFINITY ? (a.softmax && !a.bias ? l : s + bias) : l);
+    key[e] = order_key(l > -INFINITY ? (by_logit ? l : s + bias) : l);
   }
   __syncwarp();
   if (a.groups > 1) {
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kWideWarps * 32) select_wide_kernel(const Sele
       const int owner = __ffs(__ballot_sync(kFull, x == b1)) - 1;
       const uint32_t b2 = __reduce_max_sync(kFull, lane == owner ? y : x);
       if (lane == g)
-        mine = !a.softmax && b1 > 1u && b2 > 1u ? order_key(key_value(b1) + key_value(b2)) : b1;
+        mine = a.two_best && b1 > 1u && b2 > 1u ? order_key(key_value(b1) + key_value(b2)) : b1;
     }
     uint32_t kept = 0u;
     for (int r = 0; r < a.topk_groups; ++r) {
@@ -624,10 +627,10 @@ bool vec_logits(const void* p, long long ldl, int E, bool f32) {
 
 cudaError_t launch_select(const void* logits, bool f32, long long ldl, int T, int E, int k,
                           bool softmax, const float* bias, int groups, int topk_groups,
-                          bool renorm, float scale, int32_t* ids, float* weights,
+                          bool two_best, bool renorm, float scale, int32_t* ids, float* weights,
                           cudaStream_t st) {
-  const SelectArgs a{logits, ldl,         bias,   T,     E,   k,       softmax,
-                     groups, topk_groups, renorm, scale, ids, weights, vec_logits(logits, ldl, E, f32),
+  const SelectArgs a{logits,   ldl,    bias,  T,   E,       k, softmax, groups, topk_groups,
+                     two_best, renorm, scale, ids, weights, vec_logits(logits, ldl, E, f32),
                      reinterpret_cast<uintptr_t>(bias) % 16 == 0 && E % 4 == 0};
   return f32 ? select_t<float>(a, st) : select_t<__nv_bfloat16>(a, st);
 }
