@@ -36,3 +36,24 @@ def test_sigmoid_gradient_of_sure_choices(dtype, E, renorm):
     tol = torch.zeros(T, E).double().scatter_(1, i, 16 * R.U * slope * (gd.abs() + mag))
     R.within(got, ref, tol + R.rounding(dtype, ref) * 1.01, "dlogits")
     assert (got.gather(1, ids.long()) != 0).float().mean() > 0.9    # a sure choice still learns
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [16, 200, 600])
+def test_bias_that_is_no_number(scoring, E):
+    """An expert whose key is NaN or -inf by its bias fills a row only after all
+    others, lowest index first, with weight 0."""
+    T, k = 33, 8
+    g = torch.Generator(device=DEV).manual_seed(E)
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    bias = torch.full((E,), float("nan"), device=DEV)
+    bias[::2] = -float("inf")
+    bias[3], bias[E - 2], bias[E // 2] = 0.0, 0.1, -0.2
+    ids, w = mgg.select_experts(logits, k, scoring, bias, renormalize=False)
+    live = torch.tensor([3, E // 2, E - 2])
+    assert torch.equal(ids[:, :3].cpu().long().sort(1).values, live.expand(T, 3))
+    p, _, _ = R.scores(logits, scoring)
+    R.within(w[:, :3], p.gather(1, ids[:, :3].cpu().long()), 16 * R.U, "weights")
+    rest = [e for e in range(E) if e not in live.tolist()][:k - 3]
+    assert torch.equal(ids[:, 3:].cpu(), torch.tensor(rest).int().expand(T, k - 3))
+    assert not w[:, 3:].any()
