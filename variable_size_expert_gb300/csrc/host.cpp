@@ -1,7 +1,8 @@
 // Python entry to the C ABI of the layers around the experts (block.py): the
 // argument checks, output allocation and the call, in one C function each.  A
-// decode step's calls take the GPU 4 to 8 us; the same steps in Python and
-// ctypes took the host 11 to 25 us a call.  No computation happens here.
+// decode step's calls take the GPU 4 to 8 us; these take the host 3.6 to 5 (the
+// products' gradients 8 to 9), where the same steps in Python and ctypes took 11
+// to 13.5.  No computation happens here.
 #include <Python.h>
 
 #include <initializer_list>

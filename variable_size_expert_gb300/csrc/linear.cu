@@ -20,6 +20,11 @@
 //    Bound by the matrix units at the power limit: 8192 x 2048 x 8192 171 us
 //    (1610 TFLOP/s sustained), with bias, GELU and kept z 196; dx and dW 338;
 //    with little to contract by its stores (8192 x 64 x 8192 40 us, 3.4 TB/s).
+//    A product's operands are bf16, so dz is rounded to it, as in the library's
+//    other backward products: dx and dW are off by 2.35e-3 (relative, root mean
+//    square) where the rounding of the result alone gives 1.66e-3.  A second
+//    product with the rest of dz would remove that and double the operations of
+//    kernels that the matrix units bound.  dbias sums dz before it is rounded.
 //  dense_cta_kernel  one tile of 128 x BN (BN 16..256) per cluster of S CTAs,
 //    which split the contraction and add their partial accumulators through
 //    distributed shared memory in rank order (the same bits every time).  For
@@ -27,8 +32,8 @@
 //    few tokens, the gate's few columns.  The longer of the two output sides
 //    lies on the MMA's 128 rows, so that the shorter costs only its own width.
 //    Two warps load and two multiply: 1024 x 8192 x 1024 21 us, 35 with one of
-//    each.  A decode step's 16 x 7168 x 2048 7.0 us (29 MB of weights, 62% of
-//    the measured copy rate): start-up, the first loads and the join take 3 us.
+//    each.  A decode step's 16 x 7168 x 2048 7.0 us (30 MB, 63% of the measured
+//    copy rate): start-up, the first loads and the join take 2.6 us.
 #include <algorithm>
 #include <cstring>
 
@@ -77,7 +82,9 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 // Phi(z) = (1 + erf(z / sqrt 2)) / 2 with Abramowitz & Stegun 7.1.26,
 //   erf(x) = 1 - (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x), x >= 0,
 // absolute error at most 1.5e-7; here x = |z| / sqrt 2, with the 1 / sqrt 2
-// in p and the half in the a's.  *e receives exp(-z^2 / 2), which is the
+// in p and the half in the a's.  The error falls with exp(-z^2 / 2) but slower
+// than Phi: z Phi(z) is right to 3e-7 |z| everywhere, which a bf16 output does not
+// show; of its own value to 4e-6 at z = -2, 5e-4 at -4, 4e-3 at -6.  *e receives exp(-z^2 / 2), which is the
 // exp(-x^2) of the formula and the density's exponential in the gradient.
 __device__ __forceinline__ F2 normal_cdf2(float z0, float z1, F2* e) {
   const F2 z = pack2(z0, z1);

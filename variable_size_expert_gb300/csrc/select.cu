@@ -8,9 +8,10 @@
 //   sigmoid: p = 1 / (1 + exp(-logit)); key = p (+ bias)
 // A logit that is NaN, -inf or its type's lowest value masks the expert; +inf
 // counts as the largest finite value.  Keys are compared as order-preserving
-// 32-bit integers (monotone map of the f32 bits), so a round of the top-k is
-// two integer warp reductions: the largest key, then the lowest expert that
-// holds it.  0 marks a chosen expert, 1 an expert that cannot be chosen on
+// 32-bit integers (monotone map of the f32 bits), so a round of the top-k is an
+// integer warp reduction for the largest key and a ballot (lanes in expert order)
+// or a second reduction (beyond 256 experts) for the lowest expert that holds
+// it.  0 marks a chosen expert, 1 an expert that cannot be chosen on
 // its merits (masked, or outside the kept groups): such experts are taken
 // only when nothing else is left, lowest index first, with weight 0, so that
 // the k ids are always valid and distinct.
@@ -19,8 +20,9 @@
 // instruction issue, not by its bytes (1 KB per token at E = 256), so the work
 // per round of the top-k is what counts: up to V = 8 a lane sorts its keys once
 // and a round pops the winner's list.
-// Measured: 64 x 128 bf16, k = 8 5.1 us (latency); 16384 x 256 f32 sigmoid with
-// bias, 4 of 8 groups 16.4 us (1.1 TB/s); gradient 16384 x 256 10.3 us (3.4 TB/s).
+// Measured: 64 x 128 bf16, k = 8 5 to 6 us (latency); 16384 x 256 f32 sigmoid with
+// bias, 4 of 8 groups 16.4 us (1.1 TB/s); gradient, dense, 16384 x 256 10.3 us
+// (3.4 TB/s).
 #include "common.cuh"
 #include "internal.h"
 
