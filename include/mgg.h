@@ -100,7 +100,10 @@ typedef enum {
   MGG_OP_FFN_FORWARD = 5,
   MGG_OP_FFN_BACKWARD = 6,
   MGG_OP_LAYER_NORM_BACKWARD = 7,
-  MGG_OP_LINEAR_BACKWARD = 8
+  MGG_OP_LINEAR_BACKWARD = 8,
+  MGG_OP_BALANCE = 9,
+  MGG_OP_VOCAB_FORWARD = 10,
+  MGG_OP_VOCAB_BACKWARD = 11
 } mgg_op;
 
 /* How mgg_select_experts scores the logits.  One of the MGG_GROUP_ values may be
@@ -118,10 +121,14 @@ typedef enum {
  * 3e-7 |z| (SiLU: a few units in the last place); below 1e-38 it may be 0. */
 typedef enum { MGG_ACT_NONE = 0, MGG_ACT_RELU = 1, MGG_ACT_SILU = 2, MGG_ACT_GELU = 3 } mgg_activation;
 
+/* What becomes of the tokens' losses. */
+typedef enum { MGG_REDUCE_NONE = 0, MGG_REDUCE_SUM = 1, MGG_REDUCE_MEAN = 2 } mgg_reduction;
+
 /* Bits the kernels OR into *dev_status. */
 #define MGG_DEV_BAD_EXPERT_ID 0x1 /* an expert id outside [0, E): assignment skipped */
 #define MGG_DEV_BAD_OFFSETS 0x2   /* end offsets decreasing / beyond rows, or masked_m > M_max */
 #define MGG_DEV_TIMEOUT 0x4       /* a pipeline wait exceeded its limit; the kernel gave up */
+#define MGG_DEV_BAD_TARGET 0x8    /* a target outside the vocabulary: its token does not count */
 
 /* Largest expert count the device router handles. */
 #define MGG_MAX_EXPERTS 1024
@@ -692,6 +699,144 @@ mgg_status mgg_linear_backward(const void* dy, mgg_dtype dy_dtype, int64_t lddy,
                                mgg_activation activation, int T, int K, int N, void* dx, void* dW,
                                void* dbias, mgg_dtype bias_dtype, int32_t* dev_status, void* ws,
                                size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * What a training step needs around the blocks: the balance loss of a gate,
+ * the cross entropy over a vocabulary, and the optimiser's step.  The pages
+ * have no counterpart; the conventions of the layers above hold.
+ */
+
+/*
+ * Balance loss of a gate over logits [T, E] and the chosen experts, with the
+ * experts' counts.  The T tokens are `sequences` equal runs (1: the whole batch):
+ *   p[t, e]      = softmax of the token's logits, or sigmoid(logit) over the sum
+ *                  of the token's sigmoids
+ *   n[b]         = tokens of run b that count;  counts[b, e] = their choices of e
+ *   slope[b, e]  = E counts[b, e] / (k n[b]^2 B'),  B' = runs with n[b] > 0
+ *   loss         = sum_b sum_e slope[b, e] sum_t p[t, e]
+ *                = mean over the runs of sum_e (E counts / (k n)) (mean_t p)
+ *   logits (dtype, rows ldl apart), expert_ids [T, k] int32, mask [T] bytes or
+ *   NULL: not 0 where the token counts (what a token that does not count holds
+ *   is not used).  loss [1] f32, counts [sequences, E] int32, slope [sequences,
+ *   E] f32 (the backward's context).  No token that counts: zeros.
+ * Logits mask experts as in mgg_select_experts (p = 0; a token with no expert
+ * left adds nothing to p, its choices count).  An id outside [0, E) sets
+ * MGG_DEV_BAD_EXPERT_ID and is not counted.  Sums are f32, in a fixed order.
+ * ws: mgg_workspace_bytes(MGG_OP_BALANCE, T, sequences, E, 0, 0, ...).
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, E < 1, E > MGG_MAX_EXPERTS, k < 1,
+ * k > MGG_MAX_TOPK, ldl < E, sequences < 1 or not dividing T, a scoring other
+ * than MGG_SCORE_SOFTMAX and MGG_SCORE_SIGMOID), MGG_ERR_DTYPE,
+ * MGG_ERR_ALIGNMENT, MGG_ERR_WORKSPACE, MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
+ */
+mgg_status mgg_balance_loss(const void* logits, mgg_dtype dtype, int64_t ldl,
+                            const int32_t* expert_ids, const uint8_t* mask, int T, int E, int k,
+                            int sequences, mgg_scoring scoring, float* loss, int32_t* counts,
+                            float* slope, int32_t* dev_status, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * Gradient of dloss * loss to the logits, the counts held fixed:
+ *   dlogits[t, e] = dloss p[t, e] (slope[b, e] - sum_j p[t, j] slope[b, j])
+ *   (sigmoid: times 1 - sigmoid(logit)); 0 for tokens that do not count and for
+ *   masked experts.
+ *   dloss [1] f32 on the device; dlogits [T, E] (dtype, dense), overwritten
+ *   whole; the rest as the forward had or filled it.
+ */
+mgg_status mgg_balance_loss_backward(const float* dloss, const void* logits, mgg_dtype dtype,
+                                     int64_t ldl, const float* slope, const uint8_t* mask, int T,
+                                     int E, int sequences, mgg_scoring scoring, void* dlogits,
+                                     void* stream);
+
+/*
+ * Cross entropy over a vocabulary of V from hidden states, the logits
+ * z = x W^T [T, V] not kept:
+ *   lse[t]  = log sum_v exp z[t, v]
+ *   l[t]    = lse[t] - z[t, targets[t]] + z_loss lse[t]^2, 0 for a token whose
+ *             target is ignore_index
+ *   loss    = l [T] (MGG_REDUCE_NONE), sum_t l [1] (SUM), or that over the number
+ *             of tokens that count [1] (MEAN; 0 where none does)
+ *   weight  = [1] f32: 1 / tokens that count (MEAN; at least one), else 1
+ *   x [T, K] bf16 (rows ldx apart), W [V, K] bf16, targets [T] int32 or int64
+ *   (targets_i64).  A target outside [0, V) that is not ignore_index sets
+ *   MGG_DEV_BAD_TARGET and its token does not count.
+ * K % 8 == 0, ldx % 8 == 0, x and W 16-byte aligned; any V >= 1.  f32
+ * accumulation and statistics; equal inputs give equal bits.
+ * ws: mgg_workspace_bytes(MGG_OP_VOCAB_FORWARD, T, 0, 0, V, K, MGG_BF16).
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, K < 1, V < 1, ldx < K, z_loss
+ * negative or not finite, unknown reduction), MGG_ERR_ALIGNMENT,
+ * MGG_ERR_WORKSPACE, MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
+ */
+mgg_status mgg_linear_cross_entropy(const void* x, int64_t ldx, const void* W, const void* targets,
+                                    int targets_i64, int64_t ignore_index, int T, int K, int V,
+                                    mgg_reduction reduction, float z_loss, float* loss, float* lse,
+                                    float* weight, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/*
+ * Its gradients, from the forward's lse and weight:
+ *   d[t, v] = exp(z[t, v] - lse[t]) (1 + 2 z_loss lse[t]) - [v = targets[t]],
+ *             0 for tokens that do not count
+ *   dx [T, K] bf16 = g d W,  dW [V, K] bf16 = g d^T x; either may be NULL
+ *   g = dloss[0] weight[0], or with per_token dloss[t] weight[0] (dloss [T])
+ * The vocabulary is taken in pieces: the logits again, d in bf16 (the products'
+ * operand), both products; dx is summed in f32 over the pieces.  dloss and weight
+ * are read on the device.
+ * ws: mgg_workspace_bytes(MGG_OP_VOCAB_BACKWARD, T, 0, 0, V, K, MGG_BF16).
+ * Errors as for the forward.
+ */
+mgg_status mgg_linear_cross_entropy_backward(const float* dloss, int per_token, const float* weight,
+                                             const void* x, int64_t ldx, const void* W,
+                                             const void* targets, int targets_i64,
+                                             int64_t ignore_index, const float* lse, int T, int K,
+                                             int V, float z_loss, void* dx, void* dW,
+                                             int32_t* dev_status, void* ws, size_t ws_bytes,
+                                             void* stream);
+
+/* Elements that share a scale of the 8-bit moments. */
+#define MGG_ADAMW_BLOCK 256
+
+/* One tensor of n elements (0 is accepted), dense; device pointers. */
+typedef struct {
+  void* param;           /* p_dtype */
+  float* master;         /* f32 copy of a bf16 param that the step updates, or NULL */
+  const void* grad;      /* g_dtype */
+  void* exp_avg;         /* f32, or e4m3 codes */
+  void* exp_avg_sq;      /* f32, or e4m3 codes of its root */
+  float* exp_avg_scale;  /* [ceil(n / 256)] f32 with codes, else NULL */
+  float* exp_avg_sq_scale;
+  int64_t n;
+} mgg_adamw_tensor;
+
+/*
+ * One AdamW step (decoupled weight decay) over `count` tensors; t = step:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in f32; p is the master where there is one, and param receives it rounded.
+ * bits = 8: m and sqrt(v) are held as e4m3 codes times a scale for each 256
+ * elements (largest magnitude / 448), the step itself uses them unrounded.  With
+ * y = |value| / scale and u = ((index * 0x9E3779B1 + t * 0xC13FA9A9 + salt) mod
+ * 2^32) / 2^32, salt 0 for m and 2^31 for sqrt(v), y goes down to the code below
+ * y + u steps of the code: the threshold walks over the steps, so that changes
+ * of less than a code add up.  A sqrt(v) that is not 0 is held as one code at
+ * least; a value that is not finite as NaN, its neighbours are not touched by it.
+ *   tensors   [count], in host memory (read before the call returns).  All have a
+ *             master or none (bf16 params alone have one).  No two may overlap.
+ *   lr, step  as given, or read on the device at lr_dev [1] f32 / step_dev [1]
+ *             int32 where those are not NULL (a captured call follows them).
+ *             step counts from 1.
+ *   grad_scale [1] f32 on the device, or NULL: 1
+ * Up to 400 tensors take one launch.  No workspace.
+ * Errors: MGG_ERR_INVALID_ARG (null, count < 0, n < 0, beta1 or beta2 outside [0,
+ * 1), eps, lr or decay negative or not finite, step < 1 without step_dev, bits
+ * other than 8 and 32, masters of some tensors only or of f32 params),
+ * MGG_ERR_DTYPE, MGG_ERR_ALIGNMENT (a pointer not aligned to its element),
+ * MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
+ */
+mgg_status mgg_adamw_step(const mgg_adamw_tensor* tensors, int count, mgg_dtype p_dtype,
+                          mgg_dtype g_dtype, int bits, double lr, const float* lr_dev, double beta1,
+                          double beta2, double eps, double decay, int64_t step,
+                          const int32_t* step_dev, const float* grad_scale, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,4 +17,8 @@ from .block import (  # noqa: F401
     layer_norm, layer_norm_backward, layer_norm_forward, linear, linear_backward, linear_forward,
     router, select_experts, select_experts_backward,
 )
+from .step import (  # noqa: F401
+    AdamW, adamw_state, adamw_step, balance_loss, balance_loss_backward, balance_loss_forward,
+    linear_cross_entropy, linear_cross_entropy_backward, linear_cross_entropy_forward,
+)
 from . import _lib  # noqa: F401

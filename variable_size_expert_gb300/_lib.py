@@ -37,6 +37,9 @@ MGG_OP_FFN_FORWARD = 5
 MGG_OP_FFN_BACKWARD = 6
 MGG_OP_LAYER_NORM_BACKWARD = 7
 MGG_OP_LINEAR_BACKWARD = 8
+MGG_OP_BALANCE = 9
+MGG_OP_VOCAB_FORWARD = 10
+MGG_OP_VOCAB_BACKWARD = 11
 # mgg_scoring
 MGG_SCORE_SOFTMAX = 0
 MGG_SCORE_SIGMOID = 1
@@ -47,12 +50,18 @@ MGG_ACT_NONE = 0
 MGG_ACT_RELU = 1
 MGG_ACT_SILU = 2
 MGG_ACT_GELU = 3
+# mgg_reduction
+MGG_REDUCE_NONE = 0
+MGG_REDUCE_SUM = 1
+MGG_REDUCE_MEAN = 2
 # device status bits
 MGG_DEV_BAD_EXPERT_ID = 0x1
 MGG_DEV_BAD_OFFSETS = 0x2
 MGG_DEV_TIMEOUT = 0x4
+MGG_DEV_BAD_TARGET = 0x8
 MGG_MAX_EXPERTS = 1024
 MGG_MAX_TOPK = 32
+MGG_ADAMW_BLOCK = 256
 MGG_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 # every exported symbol of include/mgg.h
@@ -64,7 +73,8 @@ EXPORTS = (
     "mgg_debug_wait_timeout", "mgg_debug_row_tile", "mgg_quantize_fp8_cols",
     "mgg_moe_backward_dx_fp8", "mgg_layer_norm_forward", "mgg_layer_norm_backward",
     "mgg_select_experts", "mgg_select_experts_backward", "mgg_linear_forward",
-    "mgg_linear_backward",
+    "mgg_linear_backward", "mgg_balance_loss", "mgg_balance_loss_backward",
+    "mgg_linear_cross_entropy", "mgg_linear_cross_entropy_backward", "mgg_adamw_step",
 )
 
 
@@ -79,6 +89,12 @@ class Routing(ctypes.Structure):
         ("row_weight", ctypes.c_void_p),
         ("assign_row", ctypes.c_void_p),
     ]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "param", "master", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
+    ] + [("n", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -125,6 +141,17 @@ _SIGS.update({
                                 _P]),
     "mgg_linear_backward": (_I, [_P, _I, _LL, _P, _LL, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P,
                                  _P, _SZ, _P]),
+})
+_D = ctypes.c_double
+_SIGS.update({
+    "mgg_balance_loss": (_I, [_P, _I, _LL, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "mgg_balance_loss_backward": (_I, [_P, _P, _I, _LL, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "mgg_linear_cross_entropy": (_I, [_P, _LL, _P, _P, _I, _LL, _I, _I, _I, _I, _F, _P, _P, _P, _P,
+                                      _P, _SZ, _P]),
+    "mgg_linear_cross_entropy_backward": (_I, [_P, _I, _P, _P, _LL, _P, _P, _I, _LL, _P, _I, _I, _I,
+                                               _F, _P, _P, _P, _P, _SZ, _P]),
+    "mgg_adamw_step": (_I, [ctypes.POINTER(AdamwTensor), _I, _I, _I, _I, _D, _P, _D, _D, _D, _D, _LL,
+                            _P, _P, _P]),
 })
 
 _lib = None

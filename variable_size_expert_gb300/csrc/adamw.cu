@@ -1,0 +1,342 @@
+// AdamW over many tensors in one launch (decoupled decay):
+//   g = grad * scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+// Bound by its bytes (28 an element with bfloat16 weights, float32 masters and
+// moments; 12 with float32 weights, bfloat16 gradients and 8-bit moments).
+//
+// The tensors' addresses travel as kernel parameters: no table in device memory,
+// nothing to copy, and a captured call replays as it was.  The tensors are cut into
+// pieces of 2048 elements; a block takes a run of pieces, so that it looks its first
+// tensor up once and then walks on.  A warp's 256 elements are a block of the 8-bit
+// states: its largest value is one redux.sync.
+//
+// 8-bit moments: m and sqrt(v) as e4m3 codes times a float32 scale for each 256
+// elements of a tensor (largest magnitude / 448).  Rounding to nearest would never
+// move a second moment whose change in one step is smaller than half a code (one in a
+// thousand against one in sixteen); instead an element's rounding threshold walks a
+// Weyl sequence over the steps, (index * A + t * B + salt) mod 2^32 over 2^32, so
+// that in the mean over steps nothing is lost: sqrt(v) of gradients of constant size
+// is off by 15% (root mean square) and 0.5% on average at b2 = 0.999, 22% and 9%
+// rounded to nearest.  sqrt(v), not v: half the exponents.  A sqrt(v) that is not zero
+// does not become zero (m / eps would follow).
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mgg {
+namespace {
+
+constexpr int kThreads = 256, kPiece = kThreads * 8;
+constexpr int kFew = 24, kMany = 400;  // tensors of a launch, by parameter size
+constexpr uint32_t kWalkI = 0x9E3779B1u, kWalkT = 0xC13FA9A9u, kSaltV = 0x80000000u;
+
+struct Entry {
+  void* p;
+  float* master;
+  const void* g;
+  void *m, *v;
+  float *ms, *vs;
+  long long n;
+  int first;  // its first piece
+  int wide;   // every address allows vectors of eight elements
+};
+template <int N>
+struct AdamwParams {
+  int count, pieces;
+  float b1, c1, b2, c2, eps;  // c: 1 - b
+  float lr, decay;            // lr where lr_dev is null; weight decay
+  double lnb1, lnb2;
+  long long step;
+  const float* lr_dev;
+  const int32_t* step_dev;
+  const float* grad_scale;
+  Entry e[N];
+};
+static_assert(sizeof(AdamwParams<kMany>) <= 32764, "kernel parameters");
+
+// Eight elements from i on, `wide` as one access, else those below n, 32 apart.
+template <bool WIDE>
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  static_assert(WIDE, "");
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                 "=f"(v[7])
+               : "l"(p));
+}
+template <bool WIDE>
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  static_assert(WIDE, "");
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                            cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+}
+template <bool WIDE, typename T>
+__device__ __forceinline__ void get(const T* base, long long i, long long n, float (&v)[8]) {
+  if constexpr (WIDE) {
+    load8<true>(base + i, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + 32 * j < n ? static_cast<float>(base[i + 32 * j]) : 0.f;
+  }
+}
+template <bool WIDE, typename T>
+__device__ __forceinline__ void put(T* base, long long i, long long n, const float (&v)[8]) {
+  if constexpr (WIDE) {
+    store8(base + i, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + 32 * j < n) base[i + 32 * j] = static_cast<T>(v[j]);
+  }
+}
+
+// ---------------------------------------------------------------- 8-bit states
+// Two e4m3 codes (low half) as floats.
+__device__ __forceinline__ void decode2(uint32_t c, float& a, float& b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(c)));
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\t"
+      "cvt.f32.f16 %1, hi;\n\t}\n"
+      : "=f"(a), "=f"(b)
+      : "r"(h));
+}
+template <bool WIDE>
+__device__ __forceinline__ void get_codes(const void* base, long long i, long long n, float scale,
+                                          float (&v)[8]) {
+  const uint8_t* q = static_cast<const uint8_t*>(base);
+  if constexpr (WIDE) {
+    const uint2 w = *reinterpret_cast<const uint2*>(q + i);
+    decode2(w.x, v[0], v[1]);
+    decode2(w.x >> 16, v[2], v[3]);
+    decode2(w.y, v[4], v[5]);
+    decode2(w.y >> 16, v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t a = i + 32 * j < n ? q[i + 32 * j] : 0;
+      const uint32_t b = i + 32 * j + 32 < n ? q[i + 32 * j + 32] : 0;
+      decode2(a | b << 8, v[j], v[j + 1]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], scale);
+}
+// v's codes, and the block's scale.  The arithmetic is the formula's step by step
+// (no contraction): |v| / scale as the bits of a number with four exponent and three
+// mantissa bits (times 2^-120, so that e4m3's denormals are float's), 20 bits below
+// them, the threshold's 20 bits added, cut off.
+template <bool WIDE, bool ROOT>
+__device__ __forceinline__ void put_codes(void* base, long long i, long long n, float* scale,
+                                          uint32_t walk, const float (&v)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(fabsf(v[j])));
+  top = __reduce_max_sync(0xffffffffu, top);
+  // An element that is not finite becomes NaN and leaves its neighbours alone.
+  const bool odd = top >= 0x7f800000u;  // (the same in every lane)
+  if (odd) {
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = __float_as_uint(fabsf(v[j]));
+      if (b < 0x7f800000u) top = max(top, b);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  const float amax = __uint_as_float(top);
+  const float inv = amax > 0x1p-110f ? __fdiv_rn(448.f, amax) : 0.f;
+  uint32_t code[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a = fabsf(v[j]);
+    const uint32_t u = (walk + static_cast<uint32_t>(WIDE ? j : 32 * j) * kWalkI) >> 12;
+    const float y = __fmul_rn(__fmul_rn(a, inv), 0x1p-120f);
+    uint32_t c = min((__float_as_uint(y) + u) >> 20, 0x7eu);
+    if (ROOT && y > 0.f) c = max(c, 1u);
+    if (odd && __float_as_uint(a) >= 0x7f800000u) c = 0x7f;
+    if (!ROOT) c |= (__float_as_uint(v[j]) >> 24) & 0x80u;
+    code[j] = c;
+  }
+  uint8_t* q = static_cast<uint8_t*>(base);
+  if constexpr (WIDE) {
+    *reinterpret_cast<uint2*>(q + i) =
+        make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
+                   code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + 32 * j < n) q[i + 32 * j] = static_cast<uint8_t>(code[j]);
+  }
+  if ((threadIdx.x & 31) == 0) *scale = __fdiv_rn(amax, 448.f);
+}
+
+// ---------------------------------------------------------------- the step
+struct Rates {
+  float b1, c1, b2, c2, eps, keep, rate, root, gs;
+  uint32_t walk;
+};
+
+// Eight elements of this lane, of the warp's 256 from `at` on.
+template <typename P, typename G, bool MASTER, bool BITS8, bool WIDE>
+__device__ __forceinline__ void step8(const Entry& e, long long at, const Rates& r) {
+  const int lane = threadIdx.x & 31;
+  const long long i = at + (WIDE ? 8 * lane : lane), n = e.n;
+  float p[8], g[8], m[8], v[8];
+  get<WIDE>(static_cast<const G*>(e.g), i, n, g);
+  if constexpr (MASTER)
+    get<WIDE>(static_cast<const float*>(e.master), i, n, p);
+  else
+    get<WIDE>(static_cast<const P*>(e.p), i, n, p);
+  if constexpr (BITS8) {
+    get_codes<WIDE>(e.m, i, n, e.ms[at >> 8], m);
+    get_codes<WIDE>(e.v, i, n, e.vs[at >> 8], v);
+  } else {
+    get<WIDE>(static_cast<const float*>(e.m), i, n, m);
+    get<WIDE>(static_cast<const float*>(e.v), i, n, v);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = __fmul_rn(g[j], r.gs);
+    m[j] = __fadd_rn(__fmul_rn(m[j], r.b1), __fmul_rn(x, r.c1));
+    float root;
+    if constexpr (BITS8) {
+      root = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(v[j], v[j]), r.b2), __fmul_rn(__fmul_rn(x, x), r.c2)));
+      v[j] = root;
+    } else {
+      v[j] = __fadd_rn(__fmul_rn(v[j], r.b2), __fmul_rn(__fmul_rn(x, x), r.c2));
+      root = sqrtf(v[j]);
+    }
+    p[j] = fmaf(-r.rate * m[j], __frcp_rn(fmaf(root, r.root, r.eps)), p[j] * r.keep);
+  }
+  if constexpr (MASTER) put<WIDE>(e.master, i, n, p);
+  put<WIDE>(static_cast<P*>(e.p), i, n, p);
+  if constexpr (BITS8) {
+    const uint32_t walk = r.walk + static_cast<uint32_t>(i) * kWalkI;
+    put_codes<WIDE, false>(e.m, i, n, e.ms + (at >> 8), walk, m);
+    put_codes<WIDE, true>(e.v, i, n, e.vs + (at >> 8), walk + kSaltV, v);
+  } else {
+    put<WIDE>(static_cast<float*>(e.m), i, n, m);
+    put<WIDE>(static_cast<float*>(e.v), i, n, v);
+  }
+}
+
+template <typename P, typename G, bool MASTER, bool BITS8, int N>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwParams<N> a) {
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5;
+  const long long t = a.step_dev ? static_cast<long long>(*a.step_dev) : a.step;
+  const float lr = a.lr_dev ? *a.lr_dev : a.lr;
+  // 1 - b^t = -expm1(t ln b): no cancellation in the first steps
+  const float bc1 = -expm1f(static_cast<float>(static_cast<double>(t) * a.lnb1));
+  const float bc2 = -expm1f(static_cast<float>(static_cast<double>(t) * a.lnb2));
+  Rates r;
+  r.b1 = a.b1, r.c1 = a.c1, r.b2 = a.b2, r.c2 = a.c2, r.eps = a.eps;
+  r.keep = 1.f - lr * a.decay;
+  r.rate = lr / bc1;
+  r.root = rsqrtf(bc2);
+  r.gs = a.grad_scale ? *a.grad_scale : 1.f;
+  r.walk = static_cast<uint32_t>(t) * kWalkT;
+  const int lo = static_cast<int>(static_cast<long long>(blockIdx.x) * a.pieces / gridDim.x);
+  const int hi = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * a.pieces / gridDim.x);
+  // the tensor of the first piece: the last one that starts at or before it
+  int k = 0, end = a.count;
+  while (end - k > 1) {
+    const int mid = (k + end) >> 1;
+    if (a.e[mid].first <= lo) k = mid;
+    else end = mid;
+  }
+  for (int piece = lo; piece < hi; ++piece) {
+    while (k + 1 < a.count && a.e[k + 1].first <= piece) ++k;
+    const Entry& e = a.e[k];
+    const long long at = static_cast<long long>(piece - e.first) * kPiece + warp * 256;
+    if (at >= e.n) continue;
+    if (e.wide && at + 256 <= e.n)
+      step8<P, G, MASTER, BITS8, true>(e, at, r);
+    else
+      step8<P, G, MASTER, BITS8, false>(e, at, r);
+  }
+}
+
+// ---------------------------------------------------------------- host
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <typename P, typename G, bool MASTER, bool BITS8, int N>
+cudaError_t launch_n(const AdamwArgs& a, const AdamwParams<1>& common, int from, int count,
+                     cudaStream_t st) {
+  AdamwParams<N> p;
+  p.count = 0;
+  p.b1 = common.b1, p.c1 = common.c1, p.b2 = common.b2, p.c2 = common.c2, p.eps = common.eps;
+  p.lr = common.lr, p.decay = common.decay, p.lnb1 = common.lnb1, p.lnb2 = common.lnb2;
+  p.step = common.step, p.lr_dev = common.lr_dev, p.step_dev = common.step_dev;
+  p.grad_scale = common.grad_scale;
+  long long pieces = 0;
+  for (int i = from; i < from + count; ++i) {
+    const mgg_adamw_tensor& t = a.tensors[i];
+    if (t.n == 0) continue;
+    Entry& e = p.e[p.count++];
+    e.p = t.param, e.master = t.master, e.g = t.grad, e.m = t.exp_avg, e.v = t.exp_avg_sq;
+    e.ms = t.exp_avg_scale, e.vs = t.exp_avg_sq_scale, e.n = t.n;
+    e.first = static_cast<int>(pieces);
+    e.wide = aligned(t.param, 8 * sizeof(P)) && aligned(t.grad, 8 * sizeof(G)) &&
+             (!MASTER || aligned(t.master, 32)) && aligned(t.exp_avg, BITS8 ? 8 : 32) &&
+             aligned(t.exp_avg_sq, BITS8 ? 8 : 32);
+    pieces += (t.n + kPiece - 1) / kPiece;
+  }
+  if (pieces == 0) return cudaSuccess;
+  if (pieces > 0x7fffffff) return cudaErrorInvalidValue;
+  p.pieces = static_cast<int>(pieces);
+  const int blocks = static_cast<int>(std::min<long long>(pieces, 16LL * num_sms()));
+  return launch_pdl(adamw_kernel<P, G, MASTER, BITS8, N>, dim3(blocks), dim3(kThreads), 0, st, p);
+}
+
+template <typename P, typename G, bool MASTER, bool BITS8>
+cudaError_t launch_t(const AdamwArgs& a, const AdamwParams<1>& common, cudaStream_t st) {
+  if (a.count <= kFew) return launch_n<P, G, MASTER, BITS8, kFew>(a, common, 0, a.count, st);
+  for (int from = 0; from < a.count; from += kMany) {
+    const cudaError_t e =
+        launch_n<P, G, MASTER, BITS8, kMany>(a, common, from, std::min(kMany, a.count - from), st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+template <typename P, bool MASTER>
+cudaError_t launch_p(const AdamwArgs& a, const AdamwParams<1>& c, cudaStream_t st) {
+  if (a.g_f32)
+    return a.bits8 ? launch_t<P, float, MASTER, true>(a, c, st) : launch_t<P, float, MASTER, false>(a, c, st);
+  return a.bits8 ? launch_t<P, __nv_bfloat16, MASTER, true>(a, c, st)
+                 : launch_t<P, __nv_bfloat16, MASTER, false>(a, c, st);
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t st) {
+  AdamwParams<1> c{};
+  c.b1 = static_cast<float>(a.beta1), c.c1 = static_cast<float>(1.0 - a.beta1);
+  c.b2 = static_cast<float>(a.beta2), c.c2 = static_cast<float>(1.0 - a.beta2);
+  c.eps = static_cast<float>(a.eps), c.lr = static_cast<float>(a.lr), c.decay = static_cast<float>(a.decay);
+  c.lnb1 = log(a.beta1), c.lnb2 = log(a.beta2);  // (-inf for 0: 1 - 0^t = 1)
+  c.step = a.step, c.lr_dev = a.lr_dev, c.step_dev = a.step_dev, c.grad_scale = a.grad_scale;
+  if (a.p_f32) return launch_p<float, false>(a, c, st);
+  return a.master ? launch_p<__nv_bfloat16, true>(a, c, st) : launch_p<__nv_bfloat16, false>(a, c, st);
+}
+
+}  // namespace mgg

@@ -1,0 +1,447 @@
+// Balance loss of the gate, with the experts' counts:
+//   p_te  = softmax_e(z_t), or sigmoid(z_te) / sum_j sigmoid(z_tj)
+//   n_b   = tokens of sequence b that count; count_be = their choices of expert e
+//   loss  = 1/B' sum_b sum_e (E count_be / (k n_b)) (1/n_b sum_t p_te),  B' the
+//           sequences with tokens
+//         = sum_be slope_be sum_t p_te,  slope_be = E count_be / (k n_b^2 B')
+//   dz_te = dloss p_te (slope_be - sum_j p_tj slope_bj)   (sigmoid: times 1 - a_te)
+//
+// Bound by the logits' bytes, and below some megabytes by the launches.  Forward:
+// blocks over runs of a sequence's tokens leave their column sums of p and their
+// counts; a second kernel adds these up in the blocks' order (the same bits every
+// time), forms the slopes and the loss.  A token's logits lie in the registers of
+// `lanes` lanes (a power of two, 32 from 128 experts on), so that a softmax is
+// log2(lanes) shuffles and small gates fill their warps with tokens.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mgg {
+namespace {
+
+constexpr int kFwdThreads = 512, kBwdThreads = 256, kJoinThreads = 256;
+
+struct BalanceParams {
+  const void* logits;
+  long long ldl;
+  const int32_t* ids;
+  const uint8_t* mask;
+  int T, E, k, len, sequences;  // len: tokens of a sequence
+  int lanes;
+  int chunks, rows;             // of a sequence: blocks, and tokens of one
+  float* sums;                  // [sequences * chunks][E]
+  int32_t* hits;                // [sequences * chunks][E]
+  int32_t* tokens;              // [sequences * chunks]
+  int* ticket;
+  float* loss;
+  int32_t* counts;
+  float* slope;
+  float* parts;                 // the joining blocks' shares of the loss
+  const float* dloss;
+  void* dlogits;
+  int32_t* dev_status;
+};
+
+// VEC elements at p, as floats; 16-byte aligned where VEC > 1
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float* v) {
+  if constexpr (VEC == 1) {
+    v[0] = static_cast<float>(*p);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const float* v) {
+  if constexpr (VEC == 1) {
+    *p = static_cast<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                              cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+  }
+}
+
+// A token's logits (NV pieces of VEC in each of its lanes) to probabilities;
+// rest[]: of sigmoid scores 1 - a_te, else left.  As in the choice of the experts
+// NaN, -inf and the type's lowest value mask an expert (p = 0) and +inf is the
+// largest finite number.  Sigmoids are taken relative to the token's largest where
+// that is below a half (c = min(0, top)): a e^-c = 1 / (e^c + e^(c - z)), so that a
+// token whose scores all vanish in f32 keeps its distribution.
+template <typename T, bool SOFTMAX, int N>
+__device__ __forceinline__ void probabilities(float (&z)[N], float (&rest)[SOFTMAX ? 1 : N], int lanes) {
+  constexpr float kLow = sizeof(T) == 4 ? -3.402823466e38f : -3.389531390e38f;
+  constexpr float kMost = 3.402823466e38f;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    z[i] = z[i] > kLow ? fminf(z[i], kMost) : -INFINITY;
+    top = fmaxf(top, z[i]);
+  }
+  for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if constexpr (SOFTMAX) {
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      z[i] = expf(z[i] - ref);
+      sum += z[i];
+    }
+  } else {
+    const float c = top == -INFINITY ? 0.f : fminf(top, 0.f), ec = expf(c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = expf(c - z[i]);
+      z[i] = 1.f / (ec + e);
+      rest[i] = e == INFINITY ? 1.f : e * z[i];  // 1 - a without its cancellation
+      sum += z[i];
+    }
+  }
+  for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float r = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) z[i] *= r;
+}
+
+template <typename T, bool SOFTMAX, int VEC, int NV>
+__global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const BalanceParams p) {
+  constexpr int N = VEC * NV, U = N >= 16 ? 1 : N >= 8 ? 2 : 4;
+  constexpr int kWarps = kFwdThreads / 32;
+  __shared__ float sums[kWarps / 2 * 1024];
+  __shared__ int hits[1024];
+  __shared__ int tokens;
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seq = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int t0 = seq * p.len + chunk * p.rows, t1 = min(t0 + p.rows, (seq + 1) * p.len);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+  for (int e = threadIdx.x; e < p.E; e += kFwdThreads) hits[e] = 0;
+  if (threadIdx.x == 0) tokens = 0;
+  const int sub = lane & (p.lanes - 1), per = 32 / p.lanes;  // place in the token, tokens of a warp
+  const int step = kWarps * per;
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  int mine = 0;
+  for (int tb = t0 + warp * per; tb < t1; tb += U * step) {  // (the same in every lane of a warp)
+    float z[U][N];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * step + lane / p.lanes;
+      on[u] = t < t1 && (!p.mask || p.mask[t]);
+      const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * p.lanes + sub) * VEC;
+        if (t < t1 && e < p.E) {
+          load_vec<T, VEC>(row + e, &z[u][j * VEC]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) z[u][j * VEC + i] = -INFINITY;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float rest[SOFTMAX ? 1 : N];
+      probabilities<T, SOFTMAX, N>(z[u], rest, p.lanes);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += on[u] ? z[u][i] : 0.f;
+      mine += on[u] && sub == 0;
+    }
+  }
+  for (int o = p.lanes; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  __syncthreads();  // (hits, tokens are zero)
+  if (lane == 0 && mine) atomicAdd(&tokens, mine);
+  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kFwdThreads) {
+    const int t = t0 + i / p.k;
+    const int e = p.ids[static_cast<long long>(t0) * p.k + i];
+    if (p.mask && !p.mask[t]) continue;
+    if (e < 0 || e >= p.E)
+      atomicOr(p.dev_status, kDevBadExpertId);
+    else
+      atomicAdd(&hits[e], 1);
+  }
+  // the warps' sums meet in two steps, in the warps' order
+  auto put = [&](int w) {
+    if (lane < p.lanes)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = ((i / VEC) * p.lanes + sub) * VEC + i % VEC;
+        if (e < p.E) sums[w * p.E + e] = acc[i];
+      }
+  };
+  if (warp >= kWarps / 2) put(warp - kWarps / 2);
+  __syncthreads();
+  if (warp < kWarps / 2 && lane < p.lanes) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = ((i / VEC) * p.lanes + sub) * VEC + i % VEC;
+      if (e < p.E) acc[i] += sums[warp * p.E + e];
+    }
+  }
+  __syncthreads();
+  if (warp < kWarps / 2) put(warp);
+  __syncthreads();
+  const long long out = static_cast<long long>(blockIdx.x) * p.E;
+  for (int e = threadIdx.x; e < p.E; e += kFwdThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps / 2; ++w) s += sums[w * p.E + e];
+    p.sums[out + e] = s;
+    p.hits[out + e] = hits[e];
+  }
+  if (threadIdx.x == 0) p.tokens[blockIdx.x] = tokens;
+}
+
+// An item is 32 experts of one sequence: a lane each, the chunks dealt out to the
+// eight warps.
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const BalanceParams p) {
+  __shared__ float s_sum[8][32];
+  __shared__ int s_hit[8][32];
+  __shared__ int s_n[8], s_live[8];
+  __shared__ bool last;
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cols = cdiv(p.E, 32), items = cols * p.sequences;
+  int live = 0;
+  for (int b = threadIdx.x; b < p.sequences; b += kJoinThreads) {
+    int n = 0;
+    for (int c = 0; c < p.chunks; ++c) n |= p.tokens[b * p.chunks + c];
+    live += n != 0;
+  }
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) s_live[warp] = live;
+  float share = 0.f;
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const int b = it / cols, e = (it % cols) * 32 + lane;
+    float sum = 0.f;
+    int hit = 0, n = 0;
+    for (int c = warp; c < p.chunks; c += 32) {
+      float f[4];
+      int h[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool any = c + 8 * u < p.chunks && e < p.E;
+        const long long at = (static_cast<long long>(b) * p.chunks + c + 8 * u) * p.E + e;
+        f[u] = any ? p.sums[at] : 0.f;
+        h[u] = any ? p.hits[at] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += f[u], hit += h[u];
+    }
+    for (int c = threadIdx.x; c < p.chunks; c += kJoinThreads) n += p.tokens[b * p.chunks + c];
+    n = __reduce_add_sync(0xffffffffu, n);
+    s_sum[warp][lane] = sum;
+    s_hit[warp][lane] = hit;
+    if (lane == 0) s_n[warp] = n;
+    __syncthreads();
+    if (warp == 0) {
+      live = 0, n = 0, sum = 0.f, hit = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        live += s_live[w], n += s_n[w], sum += s_sum[w][lane], hit += s_hit[w][lane];
+      float slope = 0.f;
+      if (n > 0)
+        slope = static_cast<float>(hit) * (static_cast<float>(p.E) / static_cast<float>(p.k)) /
+                (static_cast<float>(n) * static_cast<float>(n)) / static_cast<float>(live);
+      if (e < p.E) {
+        p.counts[static_cast<long long>(b) * p.E + e] = hit;
+        p.slope[static_cast<long long>(b) * p.E + e] = slope;
+        share += slope * sum;
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) share += __shfl_xor_sync(0xffffffffu, share, o);
+    if (lane == 0) {
+      p.parts[blockIdx.x] = share;
+      __threadfence();
+      last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+    }
+  }
+  __syncthreads();
+  if (!last || warp) return;
+  __threadfence();
+  float sum = 0.f;
+  for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) sum += __ldcg(p.parts + i);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) *p.loss = sum;
+}
+
+template <typename T, bool SOFTMAX, int VEC, int NV>
+__global__ void __launch_bounds__(kBwdThreads) balance_grad_kernel(const BalanceParams p) {
+  constexpr int N = VEC * NV, U = N >= 8 ? 1 : 2;
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane & (p.lanes - 1), per = 32 / p.lanes;
+  const int warps = gridDim.x * (kBwdThreads / 32), step = warps * per;
+  const float g = *p.dloss;
+  for (int tb = (blockIdx.x * (kBwdThreads / 32) + warp) * per; tb < p.T; tb += U * step) {
+    float z[U][N], s[U][N];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * step + lane / p.lanes;
+      const bool any = t < p.T;
+      on[u] = any && (!p.mask || p.mask[t]);
+      const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
+      const float* slope = p.slope + static_cast<long long>(any ? t / p.len : 0) * p.E;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * p.lanes + sub) * VEC;
+        if (any && e < p.E) {
+          load_vec<T, VEC>(row + e, &z[u][j * VEC]);
+#pragma unroll
+          for (int i = 0; i < VEC; i += VEC > 1 ? 4 : 1)
+            load_vec<float, (VEC > 1 ? 4 : 1)>(slope + e + i, &s[u][j * VEC + i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) z[u][j * VEC + i] = -INFINITY, s[u][j * VEC + i] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * step + lane / p.lanes;
+      float rest[SOFTMAX ? 1 : N];
+      probabilities<T, SOFTMAX, N>(z[u], rest, p.lanes);
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) dot = fmaf(z[u][i], s[u][i], dot);
+      for (int o = p.lanes >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (t >= p.T) continue;
+      T* out = static_cast<T*>(p.dlogits) + static_cast<long long>(t) * p.E;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float d = z[u][i] * (s[u][i] - dot);
+        if constexpr (!SOFTMAX) d *= rest[i];
+        z[u][i] = on[u] && z[u][i] > 0.f ? d * g : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * p.lanes + sub) * VEC;
+        if (e < p.E) store_vec<T, VEC>(out + e, &z[u][j * VEC]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Blocks of the sums: one an SM, at least 32 tokens each.
+int plan_chunks(int T, int sequences) {
+  const int len = T / sequences;
+  return std::max(1, std::min(cdiv(num_sms(), sequences), cdiv(len, 32)));
+}
+
+// The widest pieces that every row starts on; then the lanes of a token.
+template <typename F>
+cudaError_t by_layout(const BalanceArgs& a, bool grads, int* lanes, F&& f) {
+  const int wide = a.f32 ? 4 : 8;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) |
+                       (grads ? reinterpret_cast<uintptr_t>(a.dlogits) | reinterpret_cast<uintptr_t>(a.slope) : 0);
+  const int vec = at % 16 == 0 && a.ldl % wide == 0 && a.E % wide == 0 ? wide : 1;
+  *lanes = 1;
+  while (*lanes < 32 && *lanes * vec < a.E) *lanes *= 2;
+  const int nv = cdiv(a.E, *lanes * vec);
+  if (vec == 1) {
+    if (nv <= 1) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    if (nv <= 2) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 2>());
+    if (nv <= 4) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
+    if (nv <= 8) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
+    if (nv <= 16) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 16>());
+    return f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>());
+  }
+  if (nv <= 1) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
+  if (nv <= 2) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
+  if (nv <= 4) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, 2>(), std::integral_constant<int, 8>());
+}
+
+// f(type, scoring) for the logits' type and the scoring
+template <typename F>
+cudaError_t by_type(const BalanceArgs& a, F&& f) {
+  if (a.f32) return a.softmax ? f(float(), std::true_type()) : f(float(), std::false_type());
+  return a.softmax ? f(__nv_bfloat16(), std::true_type()) : f(__nv_bfloat16(), std::false_type());
+}
+
+BalanceParams params(const BalanceArgs& a) {
+  BalanceParams p{};
+  p.logits = a.logits, p.ldl = a.ldl, p.ids = a.ids, p.mask = a.mask;
+  p.T = a.T, p.E = a.E, p.k = a.k, p.sequences = a.sequences, p.len = a.T / a.sequences;
+  p.loss = a.loss, p.counts = a.counts, p.slope = a.slope;
+  p.dloss = a.dloss, p.dlogits = a.dlogits, p.dev_status = a.dev_status;
+  return p;
+}
+
+}  // namespace
+
+constexpr int kJoinBlocks = 1024;  // at most
+
+size_t balance_ws_bytes(int T, int E, int sequences) {
+  const size_t blocks = static_cast<size_t>(sequences) * plan_chunks(T, sequences);
+  return 2 * round256(blocks * E * 4) + round256(blocks * 4) + round256(kJoinBlocks * 4) + 256;
+}
+
+cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st) {
+  BalanceParams p = params(a);
+  p.chunks = plan_chunks(a.T, a.sequences);
+  p.rows = cdiv(p.len, p.chunks);
+  const size_t blocks = static_cast<size_t>(a.sequences) * p.chunks;
+  char* at = static_cast<char*>(ws);
+  p.sums = reinterpret_cast<float*>(at), at += round256(blocks * a.E * 4);
+  p.hits = reinterpret_cast<int32_t*>(at), at += round256(blocks * a.E * 4);
+  p.tokens = reinterpret_cast<int32_t*>(at), at += round256(blocks * 4);
+  p.parts = reinterpret_cast<float*>(at), at += round256(kJoinBlocks * 4);
+  p.ticket = reinterpret_cast<int*>(at);
+  cudaError_t e = by_type(a, [&](auto type, auto softmax) {
+    using T = decltype(type);
+    return by_layout(a, false, &p.lanes, [&](auto wide, auto nv) {
+      constexpr int VEC = wide() == 1 ? 1 : 16 / sizeof(T), NV = VEC == 8 && nv() > 4 ? 4 : nv();
+      return launch_pdl(balance_sums_kernel<T, softmax(), VEC, NV>, dim3(static_cast<unsigned>(blocks)),
+                        dim3(kFwdThreads), 0, st, p);
+    });
+  });
+  if (e != cudaSuccess) return e;
+  const long long items = static_cast<long long>(cdiv(a.E, 32)) * a.sequences;
+  return launch_pdl(balance_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(items, kJoinBlocks))),
+                    dim3(kJoinThreads), 0, st, p);
+}
+
+cudaError_t launch_balance_bwd(const BalanceArgs& a, cudaStream_t st) {
+  BalanceParams p = params(a);
+  return by_type(a, [&](auto type, auto softmax) {
+    using T = decltype(type);
+    return by_layout(a, true, &p.lanes, [&](auto wide, auto nv) {
+      constexpr int VEC = wide() == 1 ? 1 : 16 / sizeof(T), NV = VEC == 8 && nv() > 4 ? 4 : nv();
+      const int per = kBwdThreads / p.lanes;  // tokens of a block and step
+      const int blocks = std::max(1, std::min(cdiv(a.T, per), 8 * num_sms()));
+      return launch_pdl(balance_grad_kernel<T, softmax(), VEC, NV>, dim3(blocks), dim3(kBwdThreads), 0, st, p);
+    });
+  });
+}
+
+}  // namespace mgg

@@ -14,6 +14,7 @@ namespace mgg {
 constexpr int kDevBadExpertId = 0x1;
 constexpr int kDevBadOffsets = 0x2;
 constexpr int kDevTimeout = 0x4;
+constexpr int kDevBadTarget = 0x8;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -391,6 +392,11 @@ __device__ __forceinline__ bool bar_and(int id, int count, bool pred) {
 
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // Two floats -> packed bfloat16x2 (round to nearest even), lo in the low half.

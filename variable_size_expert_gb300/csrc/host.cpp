@@ -1,13 +1,14 @@
-// Python entry to the C ABI of the layers around the experts (block.py): the
-// argument checks, output allocation and the call, in one C function each.  A
+// Python entry to the C ABI of the layers around the experts (block.py) and of a
+// training step's losses and optimiser (step.py): the argument checks, output allocation and the call, in one C function each.  A
 // decode step's calls take the GPU 4 to 8 us; these take the host 3.6 to 5 (the
 // products' gradients 8 to 9), where the same steps in Python and ctypes took 11
 // to 13.5.  No computation happens here.
 #include <Python.h>
 
+#include <algorithm>
 #include <initializer_list>
-
 #include <utility>
+#include <vector>
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -363,6 +364,207 @@ PyObject* linear_backward(PyObject* const* a) {
   return tuple({dx, dW, db});
 }
 
+// [T] bools, or none: every token counts.
+const uint8_t* token_mask(PyObject* o, int T) {
+  if (o == Py_None) return nullptr;
+  const Tensor& t = tensor(o, "mask");
+  if (t.scalar_type() != at::kBool) fail(PyExc_TypeError, "%s must be bool", "mask");
+  return static_cast<const uint8_t*>(dense(t, {T}, "mask"));
+}
+const float* scalar_f32(const Tensor& t, const char* what) {
+  if (t.scalar_type() != at::kFloat || t.numel() != 1) fail(PyExc_ValueError, "%s must be float32 [1]", what);
+  on_gpu(t);
+  return static_cast<const float*>(t.data_ptr());
+}
+int runs_of(PyObject* o, int T) {
+  const long n = integer(o, "sequences");
+  if (n < 1 || T % n != 0) fail(PyExc_ValueError, "%s must divide the tokens", "sequences");
+  return static_cast<int>(n);
+}
+
+// logits, expert_ids, scoring, mask, sequences, status, workspace
+PyObject* balance_loss_forward(PyObject* const* a) {
+  const Tensor& l = tensor(a[0], "logits");
+  const OnDevice dev(l, {{a[1], "expert_ids"}, {a[3], "mask"}, {a[5], "status"}, {a[6], "workspace"}});
+  const Tensor& ids = tensor(a[1], "expert_ids");
+  const Rows r = rows_of(l, "logits");
+  if (ids.dim() != 2 || ids.scalar_type() != at::kInt)
+    fail(PyExc_ValueError, "%s must be int32 [T, k]", "expert_ids");
+  const int k = small(ids.size(1), "expert_ids");
+  const void* ip = dense(ids, {r.rows, k}, "expert_ids");
+  const uint8_t* mp = token_mask(a[3], r.rows);
+  const int runs = runs_of(a[4], r.rows);
+  const mgg_dtype lc = code(l.scalar_type());
+  Tensor loss = empty({}, at::kFloat, l), counts = empty({runs, r.cols}, at::kInt, l),
+         slope = empty({runs, r.cols}, at::kFloat, l);
+  Tensor ws = room(a[6], mgg_workspace_bytes(MGG_OP_BALANCE, r.rows, runs, r.cols, 0, 0, lc), l);
+  check(mgg_balance_loss(r.ptr, lc, r.ld, static_cast<const int32_t*>(ip), mp, r.rows, r.cols, k, runs,
+                         static_cast<mgg_scoring>(integer(a[2], "scoring")),
+                         static_cast<float*>(loss.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
+                         static_cast<float*>(slope.data_ptr()), status_word(a[5]), ws.data_ptr(), ws.nbytes(),
+                         stream(l)),
+        "mgg_balance_loss");
+  return tuple({loss, counts, slope});
+}
+
+// dloss, logits, slope, scoring, mask
+PyObject* balance_loss_backward(PyObject* const* a) {
+  const Tensor& g = tensor(a[0], "dloss");
+  const OnDevice dev(g, {{a[1], "logits"}, {a[2], "slope"}, {a[4], "mask"}});
+  const Tensor &l = tensor(a[1], "logits"), &slope = tensor(a[2], "slope");
+  const Rows r = rows_of(l, "logits");
+  const float* gp = scalar_f32(g, "dloss");
+  const int runs = slope.dim() == 2 ? small(slope.size(0), "slope") : 0;
+  const float* sp = dense_f32(slope, {runs, r.cols}, "slope");
+  if (runs < 1 || r.rows % runs != 0) fail(PyExc_ValueError, "%s must be [sequences, E]", "slope");
+  const uint8_t* mp = token_mask(a[4], r.rows);
+  const mgg_dtype lc = code(l.scalar_type());
+  Tensor d = empty({r.rows, r.cols}, l.scalar_type(), l);
+  check(mgg_balance_loss_backward(gp, r.ptr, lc, r.ld, sp, mp, r.rows, r.cols, runs,
+                                  static_cast<mgg_scoring>(integer(a[3], "scoring")), d.data_ptr(), stream(l)),
+        "mgg_balance_loss_backward");
+  return wrap(d);
+}
+
+// The tokens' targets: int64 or int32 [T].
+const void* targets_of(const Tensor& t, int T, bool* i64) {
+  *i64 = t.scalar_type() == at::kLong;
+  if (!*i64 && t.scalar_type() != at::kInt) fail(PyExc_TypeError, "%s must be int64 or int32", "targets");
+  return dense(t, {T}, "targets");
+}
+long long wide_integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+// x, W, targets, ignore_index, reduction, z_loss, status, workspace
+PyObject* linear_cross_entropy_forward(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x");
+  const OnDevice dev(x, {{a[1], "W"}, {a[2], "targets"}, {a[6], "status"}, {a[7], "workspace"}});
+  const LinearArgs l = linear_args(x, tensor(a[1], "W"));
+  const int T = l.x.rows;
+  bool i64;
+  const void* tp = targets_of(tensor(a[2], "targets"), T, &i64);
+  const int reduction = static_cast<int>(integer(a[4], "reduction"));
+  Tensor loss = reduction == MGG_REDUCE_NONE ? empty({T}, at::kFloat, x) : empty({}, at::kFloat, x);
+  Tensor lse = empty({T}, at::kFloat, x), weight = empty({1}, at::kFloat, x);
+  Tensor ws = room(a[7], mgg_workspace_bytes(MGG_OP_VOCAB_FORWARD, T, 0, 0, l.N, l.x.cols, MGG_BF16), x);
+  check(mgg_linear_cross_entropy(l.x.ptr, l.x.ld, l.W, tp, i64, wide_integer(a[3]), T, l.x.cols, l.N,
+                                 static_cast<mgg_reduction>(reduction), static_cast<float>(number(a[5])),
+                                 static_cast<float*>(loss.data_ptr()), static_cast<float*>(lse.data_ptr()),
+                                 static_cast<float*>(weight.data_ptr()), status_word(a[6]), ws.data_ptr(),
+                                 ws.nbytes(), stream(x)),
+        "mgg_linear_cross_entropy");
+  return tuple({loss, lse, weight});
+}
+
+// dloss, x, W, targets, lse, weight, ignore_index, z_loss, need_dx, need_dW, status, workspace
+PyObject* linear_cross_entropy_backward(PyObject* const* a) {
+  const Tensor& g = tensor(a[0], "dloss");
+  const OnDevice dev(g, {{a[1], "x"}, {a[2], "W"}, {a[3], "targets"}, {a[4], "lse"}, {a[5], "weight"},
+                         {a[10], "status"}, {a[11], "workspace"}});
+  const Tensor& x = tensor(a[1], "x");
+  const LinearArgs l = linear_args(x, tensor(a[2], "W"));
+  const int T = l.x.rows, K = l.x.cols;
+  bool i64;
+  const void* tp = targets_of(tensor(a[3], "targets"), T, &i64);
+  const float* lp = dense_f32(tensor(a[4], "lse"), {T}, "lse");
+  const float* wp = scalar_f32(tensor(a[5], "weight"), "weight");
+  const bool per_token = g.dim() == 1 && g.size(0) == T;
+  const float* gp = per_token ? dense_f32(g, {T}, "dloss") : scalar_f32(g, "dloss");
+  Tensor dx, dW;
+  if (truth(a[8])) dx = empty({T, K}, at::kBFloat16, x);
+  if (truth(a[9])) dW = empty({l.N, K}, at::kBFloat16, x);
+  Tensor ws = room(a[11], mgg_workspace_bytes(MGG_OP_VOCAB_BACKWARD, T, 0, 0, l.N, K, MGG_BF16), x);
+  check(mgg_linear_cross_entropy_backward(gp, per_token, wp, l.x.ptr, l.x.ld, l.W, tp, i64, wide_integer(a[6]),
+                                          lp, T, K, l.N, static_cast<float>(number(a[7])),
+                                          dx.defined() ? dx.data_ptr() : nullptr,
+                                          dW.defined() ? dW.data_ptr() : nullptr, status_word(a[10]),
+                                          ws.data_ptr(), ws.nbytes(), stream(x)),
+        "mgg_linear_cross_entropy_backward");
+  return tuple({dx, dW});
+}
+
+// A list or tuple of n tensors (n < 0: of any length), or none where that is allowed.
+struct List {
+  List(PyObject* o, const char* name, Py_ssize_t n, bool optional) : what(name) {
+    if (optional && o == Py_None) return;
+    fast = PySequence_Fast(o, "tensors come in lists");
+    if (!fast) throw Raised{};
+    count = PySequence_Fast_GET_SIZE(fast);
+    if (n >= 0 && count != n) {
+      Py_DECREF(fast);
+      fail(PyExc_ValueError, "%s must hold a tensor for each of params", what);
+    }
+  }
+  ~List() { Py_XDECREF(fast); }
+  List(const List&) = delete;
+  List& operator=(const List&) = delete;
+  bool given() const { return fast != nullptr; }
+  // the i-th: of this dtype and number of elements, dense, on the device
+  void* at(Py_ssize_t i, ScalarType t, int64_t n, const at::Device& dev) const {
+    const Tensor& x = tensor(PySequence_Fast_GET_ITEM(fast, i), what);
+    if (x.scalar_type() != t) fail(PyExc_TypeError, "%s: the tensors' dtype differs or is not supported", what);
+    if (x.numel() != n) fail(PyExc_ValueError, "%s: a tensor has %ld elements, not %ld", what, x.numel(), n);
+    if (x.device() != dev) fail(PyExc_ValueError, "%s must be on the first parameter's device", what);
+    if (!x.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", what);
+    return x.data_ptr();
+  }
+  PyObject* fast = nullptr;
+  Py_ssize_t count = 0;
+  const char* what;
+};
+
+// params, grads, exp_avg, exp_avg_sq, step, lr, beta1, beta2, eps, weight_decay, masters,
+// exp_avg_scale, exp_avg_sq_scale, grad_scale
+PyObject* adamw_step(PyObject* const* a) {
+  const List params(a[0], "params", -1, false);
+  const Py_ssize_t n = params.count;
+  const List grads(a[1], "grads", n, false), m(a[2], "exp_avg", n, false), v(a[3], "exp_avg_sq", n, false),
+      masters(a[10], "masters", n, true), ms(a[11], "exp_avg_scale", n, true), vs(a[12], "exp_avg_sq_scale", n, true);
+  if (ms.given() != vs.given()) fail(PyExc_ValueError, "%s go together", "exp_avg_scale and exp_avg_sq_scale");
+  const double lr = THPVariable_Check(a[5]) ? 0.0 : number(a[5]);
+  const long long step = THPVariable_Check(a[4]) ? 0 : wide_integer(a[4]);
+  if (n == 0) return none();
+  const Tensor& first = tensor(PySequence_Fast_GET_ITEM(params.fast, 0), "params");
+  on_gpu(first);
+  const at::Device dev = first.device();
+  const OnDevice on(first, {{a[4], "step"}, {a[5], "lr"}, {a[13], "grad_scale"}});
+  const float* lr_dev = THPVariable_Check(a[5]) ? scalar_f32(tensor(a[5], "lr"), "lr") : nullptr;
+  const int32_t* step_dev = THPVariable_Check(a[4]) ? status_word(a[4]) : nullptr;
+  const float* gs = a[13] == Py_None ? nullptr : scalar_f32(tensor(a[13], "grad_scale"), "grad_scale");
+  const ScalarType pt = first.scalar_type(),
+                   gt = tensor(PySequence_Fast_GET_ITEM(grads.fast, 0), "grads").scalar_type();
+  const mgg_dtype pc = code(pt), gc = code(gt);
+  const ScalarType state = ms.given() ? at::kFloat8_e4m3fn : at::kFloat;
+  std::vector<mgg_adamw_tensor> t(static_cast<size_t>(n));
+  std::vector<std::pair<const char*, int64_t>> spans;
+  spans.reserve(t.size());
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const int64_t size = tensor(PySequence_Fast_GET_ITEM(params.fast, i), "params").numel();
+    const int64_t blocks = (size + MGG_ADAMW_BLOCK - 1) / MGG_ADAMW_BLOCK;
+    mgg_adamw_tensor& e = t[static_cast<size_t>(i)];
+    e.n = size;
+    e.param = params.at(i, pt, size, dev);
+    e.grad = grads.at(i, gt, size, dev);
+    e.exp_avg = m.at(i, state, size, dev);
+    e.exp_avg_sq = v.at(i, state, size, dev);
+    e.master = masters.given() ? static_cast<float*>(masters.at(i, at::kFloat, size, dev)) : nullptr;
+    e.exp_avg_scale = ms.given() ? static_cast<float*>(ms.at(i, at::kFloat, blocks, dev)) : nullptr;
+    e.exp_avg_sq_scale = ms.given() ? static_cast<float*>(vs.at(i, at::kFloat, blocks, dev)) : nullptr;
+    if (size) spans.emplace_back(static_cast<const char*>(e.param), size * (pt == at::kFloat ? 4 : 2));
+  }
+  std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i - 1].first + spans[i - 1].second > spans[i].first)
+      fail(PyExc_ValueError, "%s must not overlap (is one of them listed twice?)", "params");
+  check(mgg_adamw_step(t.data(), static_cast<int>(n), pc, gc, ms.given() ? 8 : 32, lr, lr_dev, number(a[6]),
+                       number(a[7]), number(a[8]), number(a[9]), step, step_dev, gs, stream(first)),
+        "mgg_adamw_step");
+  return none();
+}
+
 #define MGG_ENTRY(f, n)                                                               \
   {                                                                                   \
     #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)),    \
@@ -374,6 +576,11 @@ PyMethodDef methods[] = {MGG_ENTRY(layer_norm_forward, 5),
                          MGG_ENTRY(select_experts_backward, 8),
                          MGG_ENTRY(linear_forward, 9),
                          MGG_ENTRY(linear_backward, 10),
+                         MGG_ENTRY(balance_loss_forward, 7),
+                         MGG_ENTRY(balance_loss_backward, 5),
+                         MGG_ENTRY(linear_cross_entropy_forward, 8),
+                         MGG_ENTRY(linear_cross_entropy_backward, 12),
+                         MGG_ENTRY(adamw_step, 14),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", nullptr, -1, methods};
 

@@ -162,8 +162,9 @@ struct MaskedParams {
   long long wait_limit;
 };
 
-// Activations of the dense products (the values of mgg_activation).
-enum DenseAct { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
+// Activations of the dense products (the values of mgg_activation; the last one,
+// for the library's own calls, multiplies every product by *scale0 * *scale1).
+enum DenseAct { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActScale = 4 };
 
 // A bf16 operand [rows][cols], row stride ld elements.
 struct DenseOperand {
@@ -192,6 +193,7 @@ struct DenseParams {
   long long ldr;
   void* pre;             // bf16 z [M, N] or null
   bool pre_vec;          // rows on 16-byte boundaries (set by the launcher)
+  const float *scale0, *scale1;  // of kActScale
   int32_t* dev_status;
   long long wait_limit;
 };
@@ -250,7 +252,80 @@ cudaError_t launch_select_bwd(const float* g, const void* logits, bool f32, long
 size_t dense_bwd_ws_bytes(int T, int N);
 cudaError_t launch_dense_forward(const DenseParams& p, const DenseOperand& x,
                                  const DenseOperand& W, cudaStream_t st);
+cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, const DenseOperand* a,
+                                  const DenseOperand* b, cudaStream_t st);
 cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t st);
+
+int dense_pair_count();  // co-resident clusters of two (persistent grid)
+
+// vocab.cu
+struct VocabForward {
+  const void* x;
+  long long ldx;
+  const void* W;
+  const void* targets;
+  bool i64;
+  long long ignore;
+  int T, K, V, reduction;
+  float z_loss;
+  float *loss, *lse, *weight;
+  int32_t* dev_status;
+  long long wait_limit;
+};
+struct VocabBackward {
+  const float* dloss;
+  bool per_token;
+  const float* weight;
+  const void* x;
+  long long ldx;
+  const void* W;
+  const void* targets;
+  bool i64;
+  long long ignore;
+  const float* lse;
+  int T, K, V;
+  float z_loss;
+  void *dx, *dW;  // either may be null
+  int32_t* dev_status;
+  long long wait_limit;
+};
+size_t vocab_fwd_ws_bytes(int T, int V);
+size_t vocab_bwd_ws_bytes(int T, int K, int V);
+cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t st);
+cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t st);
+
+// balance.cu
+struct BalanceArgs {
+  const void* logits;
+  bool f32;
+  long long ldl;
+  const int32_t* ids;    // [T, k] (forward)
+  const uint8_t* mask;   // [T] or null
+  int T, E, k, sequences;
+  bool softmax;
+  float* loss;           // [1]
+  int32_t* counts;       // [sequences, E]
+  float* slope;          // [sequences, E]
+  const float* dloss;    // [1] (backward)
+  void* dlogits;         // [T, E]
+  int32_t* dev_status;
+};
+size_t balance_ws_bytes(int T, int E, int sequences);
+cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st);
+cudaError_t launch_balance_bwd(const BalanceArgs& a, cudaStream_t st);
+
+// adamw.cu
+struct AdamwArgs {
+  const mgg_adamw_tensor* tensors;  // host memory
+  int count;
+  bool p_f32, g_f32, master, bits8;
+  double lr, beta1, beta2, eps, decay;
+  long long step;
+  const float* lr_dev;       // or null
+  const int32_t* step_dev;   // or null
+  const float* grad_scale;   // or null
+};
+cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t st);
 
 // router.cu
 cudaError_t launch_route(const int32_t* ids, const float* w, int T, int k, int E, int BM,

@@ -34,30 +34,10 @@
 //    Two warps load and two multiply: 1024 x 8192 x 1024 21 us, 35 with one of
 //    each.  A decode step's 16 x 7168 x 2048 7.0 us (30 MB, 63% of the measured
 //    copy rate): start-up, the first loads and the join take 2.6 us.
-#include <algorithm>
-#include <cstring>
-
-#include "common.cuh"
-#include "internal.h"
+#include "pair.cuh"
 
 namespace mgg {
 namespace {
-
-constexpr int BK = kBK;                 // contraction step: one 128-byte row of bf16
-constexpr int kHalf = 128;              // rows of A, and of B, per CTA and stage of a pair
-constexpr int STAGES = 5;
-constexpr int OPER = kHalf * BK * 2;    // 16 KB
-constexpr int CHUNK = 64 * BK * 2;      // 8 KB: 64 wide MN-major block of one stage
-constexpr int EPI_WARP = 32 * 128;      // staging of an epilogue warp: 32 rows x 128 bytes
-// pairs: warps 0-3 and 6-17 epilogue, 4 MMA, 5 TMA.  Sixteen epilogue warps
-// hide one another's latencies (tensor memory, exponentials, store fences):
-// with eight, bias + GELU + kept z took 9.1 us a tile, half of it stalled.
-constexpr int kEpiWarps = 16;
-constexpr int kPairThreads = 32 * (kEpiWarps + 2);
-constexpr int kMeta = 512;
-constexpr size_t kPairSmem = 1024 + static_cast<size_t>(STAGES) * 2 * OPER + kEpiWarps * EPI_WARP + kMeta;
-static_assert(kPairSmem <= 232448, "shared memory per block");
-constexpr long long DRAIN_LIMIT = 200000000LL;
 
 // ---------------------------------------------------------------- epilogue math
 // The activations run once per output element on the few warps that empty the
@@ -66,16 +46,6 @@ constexpr long long DRAIN_LIMIT = 200000000LL;
 // 246 us against 197 for 8192 x 2048 x 8192).  The approximate exponential
 // and reciprocal are each one instruction, within 2 ulp, denormals flushed
 // (values under 1e-38); exp(-z) = inf gives a sigmoid of 0.
-__device__ __forceinline__ float exp2_f(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp_f(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ float sigmoid_f(float z) {
   return rcp_f(1.f + exp2_f(z * -1.4426950408889634f));
 }
@@ -155,6 +125,15 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
   else if (act == kActGelu) act_n<kActGelu>(v);
 }
 
+// The factor of every product (kActScale): two words, as a loss's gradient and
+// its tokens' weight come.
+__device__ __forceinline__ float factor(const DenseParams& p) { return *p.scale0 * *p.scale1; }
+template <int N>
+__device__ __forceinline__ void scale_all(float scale, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] *= scale;
+}
+
 __device__ __forceinline__ float load_any(const void* p, bool f32, long long i) {
   return f32 ? static_cast<const float*>(p)[i]
              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -192,80 +171,6 @@ __device__ __forceinline__ void add_bias(const DenseParams& p, int c0, int N, fl
   }
 }
 
-// ---------------------------------------------------------------- staged stores
-// A warp's block of 32 rows x 128 bytes (64 bf16 or 32 f32 columns) in shared
-// memory, 16-byte columns XOR-ed by row: written a row per lane, read four rows
-// x 128 bytes per store instruction, without bank conflicts both ways.
-__device__ __forceinline__ void stage_f32(uint32_t stg, int lane, const float (&v)[32]) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    st_shared_v4(stg + sw128_offset(lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-}
-__device__ __forceinline__ void stage_bf16(uint32_t stg, int lane, int half, const float (&v)[32]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    st_shared_v4(stg + sw128_offset(lane, 4 * half + c),
-                 __uint_as_float(cvt_bf16x2(v[8 * c], v[8 * c + 1])),
-                 __uint_as_float(cvt_bf16x2(v[8 * c + 2], v[8 * c + 3])),
-                 __uint_as_float(cvt_bf16x2(v[8 * c + 4], v[8 * c + 5])),
-                 __uint_as_float(cvt_bf16x2(v[8 * c + 6], v[8 * c + 7])));
-}
-// The staged block to columns c0 .. cend - 1 of rows row0.. (of M) of base [M, N].
-// vec: rows start on 16-byte boundaries.
-__device__ __forceinline__ void stage_flush(uint32_t stg, int lane, bool vec, void* base, bool f32,
-                                            int row0, int M, int N, int c0, int cend) {
-  __syncwarp();
-  const int per = f32 ? 32 : 64, size = f32 ? 4 : 2;
-  if (vec) {
-    const int kq = lane & 7, rq = lane >> 3;  // 16-byte column, first row
-    const int c = c0 + kq * (per / 8);
-    uint8_t* at = static_cast<uint8_t*>(base) + (static_cast<long long>(row0 + rq) * N + c) * size;
-    const long long step = 4LL * N * size;
-    float4 q[8];  // (read together: a store holds the next read back)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = ld_shared_v4(stg + sw128_offset(rq + 4 * j, kq));
-#pragma unroll
-    for (int j = 0; j < 8; ++j, at += step)
-      if (row0 + rq + 4 * j < M && c < cend) *reinterpret_cast<float4*>(at) = q[j];
-  } else {
-    // a row at a time, four bytes a lane (bf16: two elements, stored together
-    // where the rows start on 4-byte boundaries)
-    const bool even = !(N & 1) && (reinterpret_cast<uintptr_t>(base) & 3) == 0;
-    const int c = c0 + (f32 ? lane : 2 * lane);
-    if (c < cend) {
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32 && row0 + r0 < M; r0 += 8) {
-        uint32_t u[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          u[r] = static_cast<uint32_t>(
-              ld_shared_s32(stg + sw128_offset(r0 + r, lane >> 2) + (lane & 3) * 4));
-        const long long o = static_cast<long long>(row0 + r0) * N + c;
-        const int rows = std::min(8, M - row0 - r0);
-        if (f32) {
-          uint32_t* at = static_cast<uint32_t*>(base) + o;
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (r < rows) at[static_cast<long long>(r) * N] = u[r];
-        } else {
-          unsigned short* at = static_cast<unsigned short*>(base) + o;
-          const bool two = c + 1 < cend;
-#pragma unroll
-          for (int r = 0; r < 8; ++r, at += N) {
-            if (r >= rows) continue;
-            if (even && two) {
-              *reinterpret_cast<uint32_t*>(at) = u[r];
-            } else {
-              at[0] = static_cast<unsigned short>(u[r]);
-              if (two) at[1] = static_cast<unsigned short>(u[r] >> 16);
-            }
-          }
-        }
-      }
-    }
-  }
-  __syncwarp();  // the staging area is free again
-}
 // v += residual, rows row0.. (of M), columns c0 .. c0 + 31 (below N): read with
 // consecutive lanes on consecutive elements into the staging area as f32, then
 // each lane takes its own row.
@@ -321,139 +226,19 @@ struct PairMaps {
   CUtensorMap a[2], b[2], res;
 };
 
-struct PSmem {
-  uint32_t sA, sB, sEpi, full, empty, acc_full, acc_empty, drain, pdone, res_full, issued;
-  uint32_t* tmem_slot;
-  volatile int* abort_flag;
-};
-__device__ __forceinline__ PSmem carve_pair(uint8_t* raw) {
-  PSmem m;
-  const uint32_t raw_addr = smem_u32(raw);
-  const uint32_t base = (raw_addr + 1023u) & ~1023u;
-  uint8_t* g = raw + (base - raw_addr);
-  m.sA = base;
-  m.sB = m.sA + STAGES * OPER;
-  m.sEpi = m.sB + STAGES * OPER;
-  m.full = m.sEpi + kEpiWarps * EPI_WARP;
-  m.empty = m.full + 8 * STAGES;
-  m.acc_full = m.empty + 8 * STAGES;
-  m.acc_empty = m.acc_full + 16;
-  m.drain = m.acc_empty + 16;
-  m.pdone = m.drain + 8;
-  m.res_full = m.pdone + 8;  // one per epilogue warp
-  m.issued = m.res_full + 8 * kEpiWarps;
-  m.tmem_slot = reinterpret_cast<uint32_t*>(g + (m.issued + 8 - base));
-  m.abort_flag = reinterpret_cast<volatile int*>(m.tmem_slot + 1);
-  return m;
-}
-
 struct PTile {
   int q;           // product
   int m0, n0;      // first row and column
   int nkb;
 };
-// Tiles are walked in bands of kBand row blocks, down the band first: the
-// tiles in flight at one time then cover about kBand x 9 blocks, the squarest
-// set of operand rows for the L2 to hold.
-constexpr int kBand = 8;
 __device__ __forceinline__ PTile decode_pair(const DenseParams& p, int tau) {
   PTile t;
   t.q = tau >= p.pr[0].tiles ? 1 : 0;
   const DenseProduct& d = p.pr[t.q];
   const int local = tau - (t.q ? p.pr[0].tiles : 0);
-  const int tm = cdiv(d.M, 256), tn = cdiv(d.N, 256);
-  const int band = local / (kBand * tn);
-  const int r = local - band * kBand * tn;
-  const int rows = min(kBand, tm - band * kBand);
-  t.n0 = (r / rows) * 256;
-  t.m0 = (band * kBand + r % rows) * 256;
+  band_tile(local, d.M, d.N, t.m0, t.n0);
   t.nkb = cdiv(d.Kc, BK);
   return t;
-}
-
-// One operand's rows of a stage: 128 rows from r0, contraction from k.
-template <bool MN>
-__device__ __forceinline__ void load_oper(uint32_t dst, const CUtensorMap* map, uint32_t bar, int r0,
-                                          int k) {
-  if constexpr (MN) {
-    tma_load_2d_cg2(dst, map, bar, r0, k);
-    tma_load_2d_cg2(dst + CHUNK, map, bar, r0 + 64, k);
-  } else {
-    tma_load_2d_cg2(dst, map, bar, k, r0);
-  }
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r));
-  return r != 0;
-}
-
-// The producer's and the MMA warp's loops.  Blocks of the contraction pass
-// through a ring of slots: full[s] tells that a block has landed, empty[s] that
-// its MMAs have read it (slots released by twos, the ring of five runs short:
-// gradients of 8192 x 2048 x 8192 1650 instead of 1800 TFLOP/s).  Both loops run
-// with the whole warp converged, one elected lane issuing: inside a divergent
-// branch every operand of an MMA or a copy costs extra moves into uniform
-// registers (15% of a loop of small tiles).
-struct Ring {
-  int it, s;
-  uint32_t ph;
-  __device__ __forceinline__ void next(int stages) {
-    ++it;
-    if (++s == stages) s = 0, ph ^= 1;
-  }
-};
-template <bool A_MN, bool B_MN>
-__device__ __forceinline__ bool produce(const PSmem& m, const CUtensorMap* ma,
-                                        const CUtensorMap* mb, uint32_t full_l, bool leader, int ar,
-                                        int br, int nkb, Ring& r, const WaitCtl& wc) {
-#pragma unroll 1
-  for (int k = 0; k < nkb * BK; k += BK) {
-    // (the first round of the slots was never used)
-    if (r.it >= STAGES && !__all_sync(0xffffffffu, wait_bar(m.empty + 8 * r.s, r.ph ^ 1, wc)))
-      return false;
-    if (elect_one()) {
-      const uint32_t fb = full_l + 8 * r.s;
-      // the leader announces its bytes first; the peer issues its copies first
-      // (the phase cannot complete before its arrival)
-      if (leader) mbar_arrive_expect_tx(m.full + 8 * r.s, 2 * OPER);
-      load_oper<A_MN>(m.sA + r.s * OPER, ma, fb, ar, k);
-      load_oper<B_MN>(m.sB + r.s * OPER, mb, fb, br, k);
-      if (!leader) mbar_arrive_expect_tx_cluster(fb, 2 * OPER);
-    }
-    r.next(STAGES);
-  }
-  return true;
-}
-template <bool A_MN, bool B_MN>
-__device__ __forceinline__ bool multiply(const PSmem& m, uint32_t dt, int nkb, Ring& r,
-                                         const WaitCtl& wc) {
-  constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256, A_MN, B_MN);
-  // per 16 of the contraction: 32 bytes along a K-major row, 16 rows of 128
-  // bytes down an MN-major block (descriptors count 16-byte units)
-  constexpr uint64_t kA = (A_MN ? 16 * 128 : 32) >> 4, kB = (B_MN ? 16 * 128 : 32) >> 4;
-  const uint64_t a0 = sw128_desc(m.sA, A_MN ? CHUNK : 16, 1024);
-  const uint64_t b0 = sw128_desc(m.sB, B_MN ? CHUNK : 16, 1024);
-#pragma unroll 1
-  for (int kb = 0; kb < nkb; ++kb) {
-    if (!__all_sync(0xffffffffu, wait_bar(m.full + 8 * r.s, r.ph, wc))) return false;
-    tc_fence_after();
-    const uint64_t ad = a0 + r.s * (OPER >> 4), bd = b0 + r.s * (OPER >> 4);
-    if (elect_one()) {
-#pragma unroll
-      for (int kk = 0; kk < BK / 16; ++kk)
-        tc_mma_bf16_cg2(dt, ad + kk * kA, bd + kk * kB, kIdesc, (kb | kk) != 0);
-      tc_commit_cg2_mc(m.empty + 8 * r.s, 0x3);
-    }
-    r.next(STAGES);
-  }
-  return true;
 }
 
 // ACT is a template argument and the column loop is not unrolled: with the
@@ -474,19 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&maps.b[0]);
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(m.full + 8 * s, 2);  // both TMA threads announce their own bytes
-      mbar_init(m.empty + 8 * s, 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(m.acc_full + 8 * a, 1);
-      mbar_init(m.acc_empty + 8 * a, 2 * kEpiWarps);  // the epilogue warps of both CTAs
-    }
-    mbar_init(m.drain, 1);
-    mbar_init(m.pdone, 1);
-    for (int w = 0; w < kEpiWarps; ++w) mbar_init(m.res_full + 8 * w, 1);
-    *m.abort_flag = 0;
-    fence_mbar_init();
+    init_pair(m);
   }
   if (warp == 4) {
     tmem_alloc_cg2(smem_u32(m.tmem_slot), 512);
@@ -521,27 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       else
         ok = produce<false, false>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
     }
-    // Every copy lands before either CTA may exit: the peer reports how
-    // many blocks it issued; for the blocks that one side did not issue
-    // (only after a timeout) the leader makes that side's arrival and
-    // waits for the phase, which completes once the issued copies landed.
-    if (lane == 0) {
-      const int it = r.it;
-      if (!leader) {
-        st_cluster_s32(mapa_shared(m.issued, 0), it);
-        mbar_arrive_cluster(mapa_shared(m.pdone, 0));
-      } else {
-        const bool rep = wait_bar_cluster_drain(m.pdone, 0, DRAIN_LIMIT);
-        const int other = rep ? ld_shared_s32(m.issued) : it;
-        const int hi = std::max(it, other);
-        for (int j = std::max(0, hi - STAGES); j < hi; ++j) {
-          const uint32_t b = m.full + 8 * (j % STAGES);
-          if (j >= it) mbar_arrive(b);
-          if (j >= other) mbar_arrive(b);
-          wait_bar_drain(b, (j / STAGES) & 1, DRAIN_LIMIT);
-        }
-      }
-    }
+    if (lane == 0) drain_copies(m, r.it, leader);
     __syncwarp();
   } else if (warp == 4) {
     // ------------------------------------------------ MMA issue
@@ -587,6 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int row_w = static_cast<int>(rank) * kHalf + quad * 32;
     int tcount = 0, res_n = 0;
     bool res_open = false;  // a residual block is on its way
+    const float scale = ACT == kActScale ? factor(p) : 1.f;
     for (int tau = pair; tau < total; tau += npairs) {
       const PTile t = decode_pair(p, tau);
       const DenseProduct& d = p.pr[t.q];
@@ -631,6 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       auto load = [&](int b, float(&v)[32]) {
         tmem_ld32(taddr + b * 32, v);
         tmem_ld_wait();
+        if constexpr (ACT == kActScale) scale_all<32>(scale, v);
         if (epi && p.bias) add_bias(p, col_w + b * 32, d.N, v);
       };
       auto act_res = [&](int b, float(&v)[32]) {
@@ -765,6 +520,7 @@ __device__ __forceinline__ void finish16(const CtaParams& c, const DenseParams& 
   const DenseProduct& d = c.d;
   const long long o = static_cast<long long>(col0) * d.N + row;
   const int nv = end - col0;
+  if (p.act == kActScale) scale_all<16>(factor(p), v);
   auto store = [&](void* out, bool f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -1047,6 +803,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[16 * k + i] = h[i];
       }
+      if (p.act == kActScale) scale_all<32>(factor(p), v);
       if (d.epilogue && p.bias) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // (past BN: columns that are not stored)
@@ -1236,19 +993,10 @@ __global__ void __launch_bounds__(256, 4) dense_dz_kernel(const DzArgs a) {
 }
 
 // ---------------------------------------------------------------- host
-template <typename K>
-cudaError_t allow_smem(K kern, size_t smem, bool* done) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && done[dev]) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e == cudaSuccess && dev < 64) done[dev] = true;
-  return e;
-}
+}  // namespace
 
 // Co-resident clusters of two (persistent grid).
-int pair_count() {  // (one block per SM, whatever the activation)
+int dense_pair_count() {  // (one block per SM, whatever the activation)
   static int cache[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1271,21 +1019,7 @@ int pair_count() {  // (one block per SM, whatever the activation)
   return n;
 }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-// bf16 operand [rows][cols] with row stride ld: K-major boxes of 64 columns x
-// `box_rows` rows, MN-major boxes of 64 columns x 64 rows.
-bool tmap_operand(CUtensorMap* m, const DenseOperand& o, bool mn, int box_rows) {
-  const uint64_t dims[2] = {static_cast<uint64_t>(o.cols), static_cast<uint64_t>(o.rows)};
-  const uint64_t strides[1] = {static_cast<uint64_t>(o.ld) * 2};
-  const uint32_t box[2] = {64, static_cast<uint32_t>(mn ? 64 : box_rows)};
-  return encode_tmap(m, o.ptr, 2, dims, strides, box);
-}
-
-// Rows of an output start on 16-byte boundaries.
-bool vec_rows(const void* out, int N, bool f32) {
-  return aligned16(out) && (static_cast<long long>(N) * (f32 ? 4 : 2)) % 16 == 0;
-}
+namespace {
 
 template <int ACT>
 cudaError_t launch_pairs_act(const PairMaps& maps, const DenseParams& p, int total,
@@ -1293,7 +1027,7 @@ cudaError_t launch_pairs_act(const PairMaps& maps, const DenseParams& p, int tot
   static bool done[64] = {};
   cudaError_t e = allow_smem(dense_pair_kernel<ACT>, kPairSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(dense_pair_kernel<ACT>, dim3(2 * std::min(pair_count(), total)),
+  return launch_pdl(dense_pair_kernel<ACT>, dim3(2 * std::min(dense_pair_count(), total)),
                     dim3(kPairThreads), kPairSmem, st, maps, p);
 }
 
@@ -1322,6 +1056,7 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
   if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, total, st);
   if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, total, st);
   if (p.act == kActGelu) return launch_pairs_act<kActGelu>(maps, p, total, st);
+  if (p.act == kActScale) return launch_pairs_act<kActScale>(maps, p, total, st);
   return launch_pairs_act<kActNone>(maps, p, total, st);
 }
 
@@ -1512,6 +1247,28 @@ cudaError_t launch_dense_forward(const DenseParams& p, const DenseOperand& x,
                                   : launch_cta(p, 0, plan, x, W, st);
 }
 
+// Up to two products (those with an output): one launch where both take 256 x
+// 256 tiles.  The epilogue's operands in p are the first one's.
+cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, const DenseOperand* a,
+                                  const DenseOperand* b, cudaStream_t st) {
+  DenseParams p = q;
+  DenseOperand pa[2], pb[2];
+  int n = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (!pr[i].out) continue;
+    p.pr[n] = pr[i];
+    const CtaPlan plan = plan_cta(pr[i]);
+    if (use_pairs(pr[i], plan)) {
+      pa[n] = a[i], pb[n] = b[i];
+      ++n;
+      continue;
+    }
+    const cudaError_t e = launch_cta(p, n, plan, a[i], b[i], st);
+    if (e != cudaSuccess) return e;
+  }
+  return n ? launch_pairs(p, pa, pb, n, st) : cudaSuccess;
+}
+
 // Up to four launches: dz, then dx and dW (one launch where both take 256 x
 // 256 tiles), then the bias gradient's sums.  Each waits for the one before:
 // dx, dW and the sums depend on dz alone, but only a grid's own wait makes an
@@ -1546,24 +1303,12 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
   DenseParams p{};
   p.dev_status = a.dev_status;
   p.wait_limit = a.wait_limit;
-  DenseOperand pa[2], pb[2];
-  int n = 0;
-  auto add = [&](int M, int N, int Kc, bool a_mn, void* out, const DenseOperand& oa,
-                 const DenseOperand& ob) {
-    DenseProduct d{};
-    d.M = M, d.N = N, d.Kc = Kc, d.a_mn = a_mn, d.b_mn = true, d.out = out;
-    p.pr[n] = d;
-    pa[n] = oa, pb[n] = ob;
-    const CtaPlan plan = plan_cta(d);
-    if (use_pairs(d, plan)) {
-      ++n;
-      return cudaSuccess;
-    }
-    return launch_cta(p, n, plan, oa, ob, st);
-  };
-  if (a.dx) e = add(a.T, a.K, a.N, false, a.dx, z, W);
-  if (e == cudaSuccess && a.dW) e = add(a.N, a.K, a.T, true, a.dW, z, x);
-  if (e == cudaSuccess && n) e = launch_pairs(p, pa, pb, n, st);
+  DenseProduct dx{}, dW{};
+  dx.M = a.T, dx.N = a.K, dx.Kc = a.N, dx.b_mn = true, dx.out = a.dx;
+  dW.M = a.N, dW.N = a.K, dW.Kc = a.T, dW.a_mn = dW.b_mn = true, dW.out = a.dW;
+  const DenseProduct pr[2] = {dx, dW};
+  const DenseOperand oa[2] = {z, z}, ob[2] = {W, x};
+  if (e == cudaSuccess) e = launch_dense_products(p, pr, oa, ob, st);
   if (e == cudaSuccess && part_out)
     e = launch_column_sums(part, parts, a.N, a.db, nullptr, a.db_f32, st);
   return e;
