@@ -180,6 +180,8 @@ struct DenseProduct {
   bool out_f32;     // else bf16
   bool out_vec;     // rows of out start on 16-byte boundaries (set by the launcher)
   bool epilogue;    // bias, activation, residual, z kept
+  int slices;       // pieces of the contraction, each with an f32 output [M, N] of its own,
+                    // one behind the other (0: one)
   int tiles;        // set by the launcher
 };
 struct DenseParams {
@@ -194,6 +196,7 @@ struct DenseParams {
   void* pre;             // bf16 z [M, N] or null
   bool pre_vec;          // rows on 16-byte boundaries (set by the launcher)
   const float *scale0, *scale1;  // of kActScale
+  int longer, deal_pairs, deal;  // the tiles' order, set by the launcher
   int32_t* dev_status;
   long long wait_limit;
 };

@@ -229,16 +229,47 @@ struct PairMaps {
 struct PTile {
   int q;           // product
   int m0, n0;      // first row and column
-  int nkb;
+  int slice;       // of the contraction
+  int kb0, nkb;    // its blocks
 };
 __device__ __forceinline__ PTile decode_pair(const DenseParams& p, int tau) {
   PTile t;
   t.q = tau >= p.pr[0].tiles ? 1 : 0;
   const DenseProduct& d = p.pr[t.q];
-  const int local = tau - (t.q ? p.pr[0].tiles : 0);
+  int local = tau - (t.q ? p.pr[0].tiles : 0);
+  const int blocks = cdiv(d.Kc, BK);
+  t.slice = 0, t.kb0 = 0, t.nkb = blocks;
+  if (d.slices > 1) {
+    const int per = d.tiles / d.slices;
+    t.slice = local / per;
+    local -= t.slice * per;
+    t.kb0 = static_cast<int>(static_cast<long long>(t.slice) * blocks / d.slices);
+    t.nkb = static_cast<int>(static_cast<long long>(t.slice + 1) * blocks / d.slices) - t.kb0;
+  }
   band_tile(local, d.M, d.N, t.m0, t.n0);
-  t.nkb = cdiv(d.Kc, BK);
   return t;
+}
+// The i-th tile of a pair, -1 after its last.  The tiles of the product with the
+// longer contraction are dealt out one after the other; the pairs left with one
+// fewer of them (from p.deal_pairs on) then take p.deal tiles of the other product,
+// about as long as that one, before those are dealt out in turn too.  (Dealt out by
+// their number alone, 128 tiles of 128 blocks and 256 of 64 gave four pairs 512
+// blocks of 431 on average; so none has more than 448.)
+__device__ __forceinline__ int tile_of(const DenseParams& p, int pair, int npairs, int i) {
+  const int f = p.longer, head = p.pr[f].tiles, tail = p.pr[1 - f].tiles;
+  const int base0 = f ? p.pr[0].tiles : 0, base1 = f ? 0 : p.pr[0].tiles;
+  const int mine = pair < head ? (head - 1 - pair) / npairs + 1 : 0;
+  if (i < mine) return base0 + pair + i * npairs;
+  i -= mine;
+  const int few = npairs - p.deal_pairs;  // pairs with one fewer
+  int t;
+  if (pair >= p.deal_pairs && i < p.deal) {
+    t = i * few + pair - p.deal_pairs;
+  } else {
+    if (pair >= p.deal_pairs) i -= p.deal;
+    t = p.deal * few + i * npairs + pair;
+  }
+  return t < tail ? base1 + t : -1;
 }
 
 // ACT is a template argument and the column loop is not unrolled: with the
@@ -272,7 +303,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_wait();
   pdl_trigger();
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
-  const int total = p.pr[0].tiles + p.pr[1].tiles;
   const uint32_t full_l = mapa_shared(m.full, 0);
   const uint32_t acc_empty_l = mapa_shared(m.acc_empty, 0);
 
@@ -280,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ TMA
     Ring r{0, 0, 0};
     bool ok = true;
-    for (int tau = pair; ok && tau < total; tau += npairs) {
+    for (int i = 0, tau; ok && (tau = tile_of(p, pair, npairs, i)) >= 0; ++i) {
       const PTile t = decode_pair(p, tau);
       const DenseProduct& d = p.pr[t.q];
       const int ar = t.m0 + static_cast<int>(rank) * kHalf;
@@ -288,11 +318,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const CUtensorMap *ma = &maps.a[t.q], *mb = &maps.b[t.q];
       // (the three layouts of the forward, dx and dW)
       if (d.a_mn)
-        ok = produce<true, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
+        ok = produce<true, true>(m, ma, mb, full_l, leader, ar, br, t.kb0, t.nkb, r, wc);
       else if (d.b_mn)
-        ok = produce<false, true>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
+        ok = produce<false, true>(m, ma, mb, full_l, leader, ar, br, t.kb0, t.nkb, r, wc);
       else
-        ok = produce<false, false>(m, ma, mb, full_l, leader, ar, br, t.nkb, r, wc);
+        ok = produce<false, false>(m, ma, mb, full_l, leader, ar, br, t.kb0, t.nkb, r, wc);
     }
     if (lane == 0) drain_copies(m, r.it, leader);
     __syncwarp();
@@ -302,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int tcount = 0;
       Ring r{0, 0, 0};
       bool ok = true;
-      for (int tau = pair; ok && tau < total; tau += npairs) {
+      for (int i = 0, tau; ok && (tau = tile_of(p, pair, npairs, i)) >= 0; ++i) {
         const PTile t = decode_pair(p, tau);
         const DenseProduct& d = p.pr[t.q];
         const int acc = tcount & 1;
@@ -341,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int tcount = 0, res_n = 0;
     bool res_open = false;  // a residual block is on its way
     const float scale = ACT == kActScale ? factor(p) : 1.f;
-    for (int tau = pair; tau < total; tau += npairs) {
+    for (int i = 0, tau; (tau = tile_of(p, pair, npairs, i)) >= 0; ++i) {
       const PTile t = decode_pair(p, tau);
       const DenseProduct& d = p.pr[t.q];
       const int row0 = t.m0 + row_w;
@@ -363,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_expect_tx(res_bar, p.res_f32 ? 4096 : 2048);
-          tma_load_2d(stg, &maps.res, res_bar, c0, row0);
+          tma_load_2d(stg, &maps.res, res_bar, c0, t.slice * d.M + row0);
         }
         res_open = true;
       };
@@ -437,7 +467,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           act_res(b, v);
           __syncwarp();  // every lane has read its residual row
           stage_f32(stg, lane, v);
-          stage_flush(stg, lane, d.out_vec, d.out, true, row0, d.M, d.N, col_w + b * 32, d.N);
+          stage_flush(stg, lane, d.out_vec, static_cast<float*>(d.out) + static_cast<long long>(t.slice) * d.M * d.N,
+                      true, row0, d.M, d.N, col_w + b * 32, d.N);
         }
       } else if (nblk > 0) {
         const bool by_half = epi && p.residual;
@@ -1042,7 +1073,8 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
       d.tiles = 0;
       continue;
     }
-    d.tiles = cdiv(d.M, 256) * cdiv(d.N, 256);
+    d.slices = std::max(1, d.slices);
+    d.tiles = cdiv(d.M, 256) * cdiv(d.N, 256) * d.slices;
     total += d.tiles;
     d.out_vec = vec_rows(d.out, d.N, d.out_f32);
     if (!tmap_operand(&maps.a[q], a[q], d.a_mn, kHalf) ||
@@ -1050,8 +1082,13 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
       return cudaErrorInvalidValue;
   }
   p.pre_vec = p.pre && vec_rows(p.pre, p.pr[0].N, false);
+  const int pairs = std::min(dense_pair_count(), total);
+  auto blocks = [&](int q) { return q < n ? cdiv(cdiv(p.pr[q].Kc, BK), p.pr[q].slices) : 0; };
+  p.longer = blocks(1) > blocks(0);
+  p.deal_pairs = p.pr[p.longer].tiles % pairs;
+  p.deal = n > 1 && p.deal_pairs ? (2 * blocks(p.longer) + blocks(1 - p.longer)) / (2 * blocks(1 - p.longer)) : 0;
   p.res_tma = p.residual && p.res_vec && p.pr[0].out_f32;
-  if (p.res_tma && !encode_tmap_residual(&maps.res, p.residual, p.res_f32, p.pr[0].M, p.pr[0].N, p.ldr))
+  if (p.res_tma && !encode_tmap_residual(&maps.res, p.residual, p.res_f32, p.pr[0].slices * p.pr[0].M, p.pr[0].N, p.ldr))
     return cudaErrorInvalidValue;
   if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, total, st);
   if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, total, st);
@@ -1258,7 +1295,7 @@ cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, 
     if (!pr[i].out) continue;
     p.pr[n] = pr[i];
     const CtaPlan plan = plan_cta(pr[i]);
-    if (use_pairs(pr[i], plan)) {
+    if (pr[i].slices > 1 || use_pairs(pr[i], plan)) {
       pa[n] = a[i], pb[n] = b[i];
       ++n;
       continue;

@@ -215,9 +215,9 @@ struct Ring {
 template <bool A_MN, bool B_MN>
 __device__ __forceinline__ bool produce(const PSmem& m, const CUtensorMap* ma,
                                         const CUtensorMap* mb, uint32_t full_l, bool leader, int ar,
-                                        int br, int nkb, Ring& r, const WaitCtl& wc) {
+                                        int br, int kb0, int nkb, Ring& r, const WaitCtl& wc) {
 #pragma unroll 1
-  for (int k = 0; k < nkb * BK; k += BK) {
+  for (int k = kb0 * BK; k < (kb0 + nkb) * BK; k += BK) {
     // (the first round of the slots was never used)
     if (r.it >= STAGES && !__all_sync(0xffffffffu, wait_bar(m.empty + 8 * r.s, r.ph ^ 1, wc)))
       return false;

@@ -30,6 +30,13 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The matrix units cut every sum they add to off: over 2048 terms a logit loses 1.3e-5
+// of 6 or so, always towards zero, and a loss, which averages many, keeps that (1.6e-6
+// of it, ten times the error of f32 sums).  The forward therefore has them add up eight
+// blocks (512 terms) at a time and adds those sums in f32, in the registers of the
+// epilogue, under the next eight blocks' products.  (For d a logit need not be as good.)
+constexpr int kRunBlocks = 8;
+
 struct VocabMaps {
   CUtensorMap a, b;
 };
@@ -40,7 +47,7 @@ struct VocabParams {
   bool i64;
   long long ignore;
   // forward
-  float2* part;         // [cdiv(V, 256)][T]: (c, sum)
+  float2* part;         // [tiles along V][T]: (c, sum)
   float* target_z;      // [T]
   int* ticket;          // zeroed for the joining kernel
   // backward
@@ -99,6 +106,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_trigger();
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
   const int total = cdiv(p.T, 256) * cdiv(p.V, 256), nkb = cdiv(p.K, BK);
+  // blocks of the contraction that one accumulator adds up
+  const int kRun = BACK ? nkb : kRunBlocks;
   const uint32_t full_l = mapa_shared(m.full, 0);
   const uint32_t acc_empty_l = mapa_shared(m.acc_empty, 0);
   if (!BACK && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
@@ -111,7 +120,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int m0, n0;
       band_tile(tau, p.T, p.V, m0, n0);
       const int half = static_cast<int>(rank) * kHalf;
-      ok = produce<false, false>(m, &maps.a, &maps.b, full_l, leader, m0 + half, n0 + half, nkb, r, wc);
+      ok = produce<false, false>(m, &maps.a, &maps.b, full_l, leader, m0 + half, n0 + half, 0, nkb, r, wc);
     }
     if (lane == 0) drain_copies(m, r.it, leader);
     __syncwarp();
@@ -120,14 +129,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (leader) {
       int tcount = 0;
       Ring r{0, 0, 0};
-      for (int tau = pair; tau < total; tau += npairs) {
-        const int acc = tcount & 1;
-        if (!__all_sync(0xffffffffu, wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)))
-          break;
-        tc_fence_after();
-        if (!multiply<false, false>(m, tmem_base + acc * 256, nkb, r, wc)) break;
-        if (elect_one()) tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
-        ++tcount;
+      bool ok = true;
+      for (int tau = pair; ok && tau < total; tau += npairs) {
+        for (int kb = 0; ok && kb < nkb; kb += kRun, ++tcount) {
+          const int acc = tcount & 1;
+          ok = __all_sync(0xffffffffu, wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+          ok = multiply<false, false>(m, tmem_base + acc * 256, min(kRun, nkb - kb), r, wc);
+          if (ok && elect_one()) tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
+        }
       }
       if (elect_one()) {
         tc_commit_cg2(m.drain);
@@ -143,12 +154,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t stg = m.sEpi + ew * EPI_WARP;
     // (forward) the groups' statistics, two tiles' in turn: [tile][group][row]
     const uint32_t stat = m.sEpi + quad * 2048 + lane * 8;
-    int tcount = 0;
-    for (int tau = pair; tau < total; tau += npairs) {
+    int tcount = 0, parity = 0;
+    for (int tau = pair; tau < total; tau += npairs, parity ^= 1) {
       int m0, n0;
       band_tile(tau, p.T, p.V, m0, n0);
       const int row0 = m0 + static_cast<int>(rank) * kHalf + quad * 32, row = row0 + lane;
-      const int acc = tcount & 1;
       const int col_w = n0 + group * 64;
       const int nv = p.V - col_w;  // columns from col_w on (may be none)
       // while the tile is multiplied: the row's target, of this warp's columns
@@ -163,19 +173,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         one = g;
         if (y == -2 && p.v0 + col_w == 0) atomicOr(p.dev_status, kDevBadTarget);
       }
-      bool ok = __all_sync(0xffffffffu, wait_bar(m.acc_full + 8 * acc, (tcount >> 1) & 1, wc));
-      // the four groups of a quarter meet below: they leave together
-      if (!BACK) ok = bar_and(1 + quad, 128, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr =
-          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + group * 64;
+      auto arrived = [&]() {
+        const bool ok = __all_sync(0xffffffffu, wait_bar(m.acc_full + 8 * (tcount & 1), (tcount >> 1) & 1, wc));
+        tc_fence_after();
+        return ok;
+      };
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_l + 8 * acc);
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_l + 8 * (tcount & 1));
       };
+      const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + group * 64;
       if constexpr (BACK) {
+        if (!arrived()) break;
+        const uint32_t taddr = taddr0 + (tcount & 1) * 256;
         if (nv <= 0) release();
         // (few tokens) d in two parts: rounded, and what the rounding left
         const int parts = nv <= 0 ? 0 : p.split ? 2 : 1;
@@ -210,14 +221,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       } else {
         float v[64];
-        {
-          float(&lo)[32] = *reinterpret_cast<float(*)[32]>(v);
-          float(&hi)[32] = *reinterpret_cast<float(*)[32]>(v + 32);
-          tmem_ld32(taddr, lo);
-          tmem_ld32(taddr + 32, hi);
+        bool ok = true;
+        for (int kb = 0; ok && kb < nkb; kb += kRun) {
+          ok = arrived();
+          if (!ok) break;
+          const uint32_t taddr = taddr0 + (tcount & 1) * 256;
+          float x[32];
+          tmem_ld32(taddr, x);
           tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = kb ? v[i] + x[i] : x[i];
+          tmem_ld32(taddr + 32, x);
+          tmem_ld_wait();
+          release();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[32 + i] = kb ? v[32 + i] + x[i] : x[i];
+          ++tcount;
         }
-        release();
+        // the four groups of a quarter meet below: they leave together
+        if (!bar_and(1 + quad, 128, ok)) break;
         if (nv < 64) {
 #pragma unroll
           for (int i = 0; i < 64; ++i)
@@ -255,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // the four groups of a quarter meet in shared memory: one barrier a tile,
         // as the first group reads this tile's half while the others write the
         // next tile's
-        const uint32_t mine = stat + (tcount & 1) * 1024;
+        const uint32_t mine = stat + parity * 1024;
         if (group) {
           st_shared_f32(mine + group * 256, cc);
           st_shared_f32(mine + group * 256 + 4, s);
@@ -268,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           p.part[static_cast<long long>(n0 >> 8) * p.T + row] = make_float2(cc, s);
         }
       }
-      ++tcount;
+      if (BACK) ++tcount;
     }
   }
 
@@ -282,9 +304,186 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- few tokens
+// Up to 64 tokens the weights' bytes are the bound: tiles of 128 rows of W by N
+// tokens (16..64), W's rows on the rows of the accumulator, two blocks an SM with a
+// ring each, so that 190 KB an SM are in flight.  (Pair tiles, whose 256 token rows
+// are mostly empty, take 42 us for 16 x 2048 x 32768.)  A lane then holds a vocabulary
+// entry, not a token: the forward turns the tile through shared memory and reduces a
+// token with a warp, the backward stores d as it lies.  Runs of the contraction have
+// an accumulator each and meet in f32 (see kRunBlocks).
+constexpr int kFewTokens = 64, kFewThreads = 192, kFewSlots = 6;
+constexpr int kFewMeta = 256;
+struct FewParams {
+  int N;          // tokens, rounded up to 16
+  int slots, run, runs, tmem_cols;
+};
+size_t few_smem(int N, int slots) {
+  return 1024 + std::max(static_cast<size_t>(slots) * (OPER + N * 128), static_cast<size_t>(N) * 132 * 4) + kFewMeta;
+}
+template <bool BACK>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    vocab_few_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabParams p,
+                     const __grid_constant__ FewParams f) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw_addr);
+  const uint32_t stage = OPER + f.N * 128;
+  const uint32_t ring = max(f.slots * stage, f.N * 132u * 4);
+  const uint32_t full = base + ring, empty = full + 8 * kFewSlots, done = empty + 8 * kFewSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ring + 16 * kFewSlots + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * 128, nkb = cdiv(p.K, BK);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < f.slots; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), f.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
+  if (!BACK && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+
+  if (warp == 4) {
+    Ring r{0, 0, 0};
+#pragma unroll 1
+    for (int k = 0; k < nkb * BK; k += BK) {
+      if (r.it >= f.slots && !__all_sync(0xffffffffu, wait_bar(empty + 8 * r.s, r.ph ^ 1, wc))) break;
+      if (elect_one()) {
+        const uint32_t a = base + r.s * stage;
+        mbar_arrive_expect_tx(full + 8 * r.s, stage);
+        tma_load_2d(a, &maps.b, full + 8 * r.s, k, n0);
+        tma_load_2d(a + OPER, &maps.a, full + 8 * r.s, k, 0);
+      }
+      r.next(f.slots);
+    }
+    // the copies land before the block may exit
+    for (int j = max(0, r.it - f.slots); j < r.it; ++j)
+      wait_bar_drain(full + 8 * (j % f.slots), (j / f.slots) & 1, DRAIN_LIMIT);
+    __syncwarp();
+  } else if (warp == 5) {
+    const uint32_t idesc = idesc_bf16_f32(128, f.N, false, false);
+    const uint64_t a0 = sw128_desc(base, 16, 1024), b0 = sw128_desc(base + OPER, 16, 1024);
+    Ring r{0, 0, 0};
+    bool ok = true;
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bar(full + 8 * r.s, r.ph, wc));
+      if (!ok) break;
+      tc_fence_after();
+      const int run = kb / f.run;
+      const uint64_t ad = a0 + r.s * (stage >> 4), bd = b0 + r.s * (stage >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_bf16(tmem_base + run * f.N, ad + kk * 2, bd + kk * 2, idesc, kb != run * f.run || kk);
+        tc_commit(empty + 8 * r.s);
+      }
+      r.next(f.slots);
+    }
+    if (elect_one()) {
+      tc_commit(done);
+      wait_bar_drain(done, 0, DRAIN_LIMIT);
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  }
+  // ------------------------------------------------ epilogue
+  __syncthreads();  // every MMA is done; all warps, no wait of their own
+  tc_fence_after();
+  const bool ok = *abort_flag == 0;
+  const int tl = warp * 32 + lane, row = n0 + tl;
+  if (ok && warp < 4) {
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+    for (int j = 0; j < f.N; j += 16) {
+      float v[16], x[16];
+      tmem_ld16(taddr + j, v);
+      tmem_ld_wait();
+      for (int k = 1; k < f.runs; ++k) {
+        tmem_ld16(taddr + k * f.N + j, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += x[i];
+      }
+      if constexpr (BACK) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int t = j + i;
+          if (t >= p.T) break;
+          const int y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
+          const float lse = p.lse[t];
+          const float g = y < 0 ? 0.f : p.gtok ? p.gtok[t] * *p.weight : 1.f;
+          if (y == -2 && p.v0 + row == 0) atomicOr(p.dev_status, kDevBadTarget);
+          float d = exp2_f(fmaf(v[i], kLog2e, -lse * kLog2e)) * ((1.f + p.z2 * lse) * g);
+          if (y == p.v0 + row) d -= g;
+          if (y < 0) d = 0.f;
+          if (row < p.V) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(d);
+            p.d[static_cast<long long>(t) * p.ldd + row] = hi;
+            if (p.split)
+              p.d[static_cast<long long>(p.T + t) * p.ldd + row] = __float2bfloat16_rn(d - __bfloat162float(hi));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st_shared_f32(base + ((j + i) * 132 + tl) * 4, row < p.V ? v[i] : -INFINITY);
+      }
+    }
+  }
+  if (!BACK) {
+    __syncthreads();
+    for (int t = warp; ok && t < p.T; t += kFewThreads / 32) {
+      float v[4], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = ld_shared_f32(base + (t * 132 + 32 * i + lane) * 4);
+        top = fmaxf(top, v[i]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float c = top * kLog2e, r = c == -INFINITY ? 0.f : c;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += exp2_f(fmaf(v[i], kLog2e, -r));
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) {
+        p.part[static_cast<long long>(blockIdx.x) * p.T + t] = make_float2(c, s);
+        const int at = target_of(p.targets, p.i64, p.ignore, p.vocab, t) - n0;
+        if (at >= 0 && at < 128) p.target_z[t] = ld_shared_f32(base + (t * 132 + at) * 4);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, f.tmem_cols);
+  }
+}
+
 // ---------------------------------------------------------------- joining the tiles
 // A block joins the pairs of 32 tokens (a lane each, the tiles dealt out to its
-// eight warps), and the block that ends last adds up the blocks' losses in their
+// warps; then a warp each), and the block that ends last adds up the blocks' losses in their
 // order: the same bits every time.
 struct JoinParams {
   const float2* part;
@@ -303,33 +502,39 @@ struct JoinParams {
   int* ticket;
   int32_t* dev_status;
 };
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinParams p) {
-  __shared__ float2 sh[8][32];
+  __shared__ float2 sh[kJoinWarps][33];
+  __shared__ float2 each[kJoinWarps];
   __shared__ bool last;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 32 + lane;
+  int t = blockIdx.x * 32 + lane;
   float c = -INFINITY, s = 0.f;
   if (t < p.T) {
-    for (int i = warp; i < p.tiles; i += 32) {
+    for (int i = warp; i < p.tiles; i += 4 * kJoinWarps) {
       float2 q[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        q[u] = i + 8 * u < p.tiles ? p.part[static_cast<long long>(i + 8 * u) * p.T + t]
-                                   : make_float2(-INFINITY, 0.f);
+        q[u] = i + kJoinWarps * u < p.tiles ? p.part[static_cast<long long>(i + kJoinWarps * u) * p.T + t]
+                                            : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int u = 0; u < 4; ++u) join(c, s, q[u].x, q[u].y);
     }
   }
   sh[warp][lane] = make_float2(c, s);
   __syncthreads();
-  if (warp == 0) {
+  // warp w: the block's token w
+  t = blockIdx.x * 32 + warp;
+  const float2 q = sh[lane][warp];
+  c = q.x, s = q.y;
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2)
+    join(c, s, __shfl_xor_sync(0xffffffffu, c, o), __shfl_xor_sync(0xffffffffu, s, o));
+  if (lane == 0) {
     float loss = 0.f, n = 0.f;
     if (t < p.T) {
-#pragma unroll
-      for (int w = 1; w < 8; ++w) join(c, s, sh[w][lane].x, sh[w][lane].y);
       const float lse = kLn2 * (c + log2f(s));
       p.lse[t] = lse;
       const int y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
@@ -341,13 +546,18 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinPara
       }
       if (p.reduction == MGG_REDUCE_NONE) p.losses[t] = loss;
     }
+    each[warp] = make_float2(loss, n);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float2 e = each[lane];
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
-      loss += __shfl_xor_sync(0xffffffffu, loss, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
+      e.x += __shfl_xor_sync(0xffffffffu, e.x, o);
+      e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
     }
     if (lane == 0) {
-      p.blocks[blockIdx.x] = make_float2(loss, n);
+      p.blocks[blockIdx.x] = e;
       __threadfence();
       last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
     }
@@ -355,24 +565,30 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinPara
   __syncthreads();
   if (!last) return;
   __threadfence();
-  float loss = 0.f, n = 0.f;
+  float2 e = make_float2(0.f, 0.f);
   for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kJoinThreads) {
-    const float2 q = __ldcg(p.blocks + i);
-    loss += q.x, n += q.y;
+    const float2 b = __ldcg(p.blocks + i);
+    e.x += b.x, e.y += b.y;
   }
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) {
-    loss += __shfl_xor_sync(0xffffffffu, loss, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
+    e.x += __shfl_xor_sync(0xffffffffu, e.x, o);
+    e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
   }
-  if (lane == 0) sh[0][warp] = make_float2(loss, n);
+  if (lane == 0) each[warp] = e;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    loss = 0.f, n = 0.f;
-    for (int w = 0; w < 8; ++w) loss += sh[0][w].x, n += sh[0][w].y;
-    const float w = p.reduction == MGG_REDUCE_MEAN ? 1.f / fmaxf(n, 1.f) : 1.f;
-    if (p.reduction != MGG_REDUCE_NONE) *p.total = loss * w;
-    *p.weight = w;
+  if (warp == 0) {
+    e = each[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+      e.x += __shfl_xor_sync(0xffffffffu, e.x, o);
+      e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
+    }
+    if (lane == 0) {
+      const float w = p.reduction == MGG_REDUCE_MEAN ? 1.f / fmaxf(e.y, 1.f) : 1.f;
+      if (p.reduction != MGG_REDUCE_NONE) *p.total = e.x * w;
+      *p.weight = w;
+    }
   }
 }
 
@@ -381,9 +597,34 @@ __global__ void vocab_empty_kernel(float* total, float* weight) {
   *weight = 1.f;
 }
 
+// Rows of W that one pair (c, s) of the forward stands for.
+int tile_columns(int T) { return T <= kFewTokens ? 128 : 256; }
+
+template <bool BACK>
+cudaError_t launch_few(const DenseOperand& x, const DenseOperand& W, const VocabParams& p, cudaStream_t st) {
+  static bool done[64] = {};
+  cudaError_t e = allow_smem(vocab_few_kernel<BACK>, 116 * 1024, done);
+  if (e != cudaSuccess) return e;
+  FewParams f;
+  f.N = (p.T + 15) / 16 * 16;
+  const int nkb = cdiv(p.K, BK);
+  // half of an SM's shared memory and tensor memory
+  f.slots = std::min({kFewSlots, (112 * 1024 - 1024 - kFewMeta) / (OPER + f.N * 128), nkb});
+  f.run = std::max(BACK ? nkb : cdiv(nkb, 256 / f.N), 1);
+  if (!BACK) f.run = std::max(f.run, std::min(nkb, 4));
+  f.runs = cdiv(nkb, f.run);
+  f.tmem_cols = 32;
+  while (f.tmem_cols < f.runs * f.N) f.tmem_cols *= 2;
+  VocabMaps maps;
+  if (!tmap_operand(&maps.a, x, false, f.N) || !tmap_operand(&maps.b, W, false, 128)) return cudaErrorInvalidValue;
+  return launch_pdl(vocab_few_kernel<BACK>, dim3(cdiv(p.V, 128)), dim3(kFewThreads), few_smem(f.N, f.slots), st,
+                    maps, p, f);
+}
+
 template <bool BACK>
 cudaError_t launch_tiles(const DenseOperand& x, const DenseOperand& W, const VocabParams& p,
                          cudaStream_t st) {
+  if (p.T <= kFewTokens) return launch_few<BACK>(x, W, p, st);
   static bool done[64] = {};
   cudaError_t e = allow_smem(vocab_pair_kernel<BACK>, kPairSmem, done);
   if (e != cudaSuccess) return e;
@@ -412,15 +653,18 @@ __global__ void __launch_bounds__(256) vocab_twice_kernel(const uint4* x, long l
     out[T * K8 + i] = v;
   }
 }
-// dx = scale (rows t + rows T + t of sum)
-__global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, const float* scale0,
-                                                            const float* scale1, int n4, uint2* dx) {
+// dx = the sum of its parts, [parts][T K]
+__global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, int parts, long long n4,
+                                                            uint2* dx) {
   pdl_trigger();
   pdl_wait();
-  const float g = scale0 ? *scale0 * *scale1 : 1.f;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n4; i += gridDim.x * 256) {
-    const float4 a = sum[i], b = sum[n4 + i];
-    dx[i] = make_uint2(cvt_bf16x2((a.x + b.x) * g, (a.y + b.y) * g), cvt_bf16x2((a.z + b.z) * g, (a.w + b.w) * g));
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < n4; i += gridDim.x * 256) {
+    float4 a = sum[i];
+    for (int k = 1; k < parts; ++k) {
+      const float4 b = sum[k * n4 + i];
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    dx[i] = make_uint2(cvt_bf16x2(a.x, a.y), cvt_bf16x2(a.z, a.w));
   }
 }
 
@@ -431,20 +675,30 @@ int piece_columns(int T, int V) {
   const long long cols = std::max<long long>(2048, most / (2LL * rows) / 256 * 256);
   return static_cast<int>(std::min<long long>(cols, (V + 7) / 8 * 8));
 }
-// What the backward keeps: d; the f32 sum of dx (over pieces or parts); [x; x].
+// What the backward keeps: d; f32 sums of dx (over pieces, of its slices and parts);
+// [x; x].
 struct BackLayout {
   int cols;
   bool split;
+  int slices;                // of dx's contraction in a piece
   size_t sum, twice, total;  // offsets of the second and third
 };
 BackLayout back_layout(int T, int K, int V) {
   BackLayout l;
   l.cols = piece_columns(T, V);
   l.split = T <= kSplitTokens;
-  const size_t rows = l.split ? 2 * static_cast<size_t>(T) : T;
-  l.sum = round256(rows * l.cols * 2);
-  l.twice = l.sum + (l.split || l.cols < V ? round256(rows * K * 4) : 0);
-  l.total = l.twice + (l.split ? round256(rows * K * 2) : 0);
+  const int rows = l.split ? 2 * T : T;
+  // dx has few tiles and a long contraction where there are few tokens: cut so that
+  // no tile takes longer than half of what a pair has to do (1111 x 1160 over 50257:
+  // 25 tiles, 240 us on single-CTA tiles)
+  const long long blocks = cdiv(l.cols, BK), tk = cdiv(K, 256);
+  const long long work = cdiv(rows, 256) * tk * blocks + cdiv(l.cols, 256) * tk * (cdiv(rows, BK) + 4);
+  const long long most = std::max<long long>(16, work / (num_sms() / 2) / 2);
+  l.slices = static_cast<int>(std::min<long long>(32, (blocks + most - 1) / most));
+  const size_t sums = static_cast<size_t>(rows) * l.slices;
+  l.sum = round256(static_cast<size_t>(rows) * l.cols * 2);
+  l.twice = l.sum + (l.split || l.slices > 1 || l.cols < V ? round256(sums * K * 4) : 0);
+  l.total = l.twice + (l.split ? round256(static_cast<size_t>(rows) * K * 2) : 0);
   return l;
 }
 
@@ -452,7 +706,7 @@ BackLayout back_layout(int T, int K, int V) {
 
 // forward: the tiles' pairs, the targets' logits, the joining blocks' sums, their ticket
 size_t vocab_fwd_ws_bytes(int T, int V) {
-  return round256(static_cast<size_t>(cdiv(V, 256)) * T * 8) + round256(static_cast<size_t>(T) * 4) +
+  return round256(static_cast<size_t>(cdiv(V, tile_columns(T))) * T * 8) + round256(static_cast<size_t>(T) * 4) +
          round256(static_cast<size_t>(cdiv(T, 32)) * 8) + 256;
 }
 size_t vocab_bwd_ws_bytes(int T, int K, int V) { return back_layout(T, K, V).total; }
@@ -468,7 +722,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t s
     at += round256(bytes);
     return r;
   };
-  const int tn = cdiv(a.V, 256);
+  const int tn = cdiv(a.V, tile_columns(a.T));
   VocabParams p{};
   p.T = a.T, p.V = a.V, p.K = a.K, p.vocab = a.V;
   p.targets = a.targets, p.i64 = a.i64, p.ignore = a.ignore;
@@ -516,9 +770,9 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     const DenseOperand Wp{W, n, a.K, a.K}, dp{d, rows, n, l.cols};
     e = launch_tiles<true>(x, Wp, p, st);
     if (e != cudaSuccess) return e;
-    const bool first = v0 == 0, direct = v0 + n == a.V && !l.split;  // dx in place
-    // Every product is multiplied by the loss's gradient as it leaves, but dx's
-    // parts, which meet first.
+    const bool parts = l.split || l.slices > 1;
+    const bool first = v0 == 0, direct = v0 + n == a.V && !parts;  // dx in place
+    // every product is multiplied by the loss's gradient as it leaves
     DenseParams q{};
     q.scale0 = scale, q.scale1 = a.weight;
     q.dev_status = a.dev_status, q.wait_limit = a.wait_limit;
@@ -526,6 +780,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     dx.M = rows, dx.N = a.K, dx.Kc = n, dx.b_mn = true;
     dx.out = !a.dx ? nullptr : direct ? a.dx : sum;
     dx.out_f32 = !direct, dx.epilogue = !first;
+    dx.slices = std::min(l.slices, cdiv(n, BK));  // (a last piece may be narrow)
     dW.M = n, dW.N = a.K, dW.Kc = rows, dW.a_mn = dW.b_mn = true;
     dW.out = a.dW ? static_cast<char*>(a.dW) + static_cast<size_t>(v0) * a.K * 2 : nullptr;
     if (!first) {
@@ -535,24 +790,15 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     }
     q.act = scale ? kActScale : kActNone;
     const DenseOperand oa[2] = {dp, dp}, ob[2] = {Wp, xd};
-    if (l.split && scale) {
-      const DenseProduct none{}, only_dx[2] = {dx, none}, only_dW[2] = {none, dW};
-      DenseParams plain = q;
-      plain.act = kActNone;
-      e = launch_dense_products(plain, only_dx, oa, ob, st);
-      if (e == cudaSuccess) {
-        q.residual = nullptr;
-        e = launch_dense_products(q, only_dW, oa, ob, st);
-      }
-    } else {
-      const DenseProduct pr[2] = {dx, dW};
-      e = launch_dense_products(q, pr, oa, ob, st);
-    }
+    const DenseProduct pr[2] = {dx, dW};
+    e = launch_dense_products(q, pr, oa, ob, st);
   }
-  if (e == cudaSuccess && l.split && a.dx)
-    e = launch_pdl(vocab_join_dx_kernel, dim3(cdiv(a.T * a.K / 4, 256)), dim3(256), 0, st,
-                   reinterpret_cast<const float4*>(sum), scale, a.weight, a.T * a.K / 4,
-                   static_cast<uint2*>(a.dx));
+  if (e == cudaSuccess && (l.split || l.slices > 1) && a.dx) {
+    const long long n4 = static_cast<long long>(a.T) * a.K / 4;
+    e = launch_pdl(vocab_join_dx_kernel, dim3(static_cast<unsigned>(std::min<long long>((n4 + 255) / 256, 16 * num_sms()))),
+                   dim3(256), 0, st, reinterpret_cast<const float4*>(sum), (l.split ? 2 : 1) * l.slices, n4,
+                    static_cast<uint2*>(a.dx));
+  }
   return e;
 }
 
