@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256, kPiece = kThreads * 8;
 constexpr int kFew = 24, kMany = 400;  // tensors of a launch, by parameter size
+constexpr int kGroups = 128;
 constexpr uint32_t kWalkI = 0x9E3779B1u, kWalkT = 0xC13FA9A9u, kSaltV = 0x80000000u;
 
 struct Entry {
@@ -40,8 +41,7 @@ struct Entry {
   void *m, *v;
   float *ms, *vs;
   long long n;
-  int first;  // its first piece
-  int wide;   // every address allows vectors of eight elements
+  int wide;  // every address allows vectors of eight elements
 };
 template <int N>
 struct AdamwParams {
@@ -53,6 +53,11 @@ struct AdamwParams {
   const float* lr_dev;
   const int32_t* step_dev;
   const float* grad_scale;
+  // Each block reads these at its start, one after the other, from memory (they are
+  // cold): the tensor that holds the first piece of its group of blocks, then the
+  // tensors' first pieces from there on.
+  unsigned short hint[kGroups];
+  int first[N + 1];
   Entry e[N];
 };
 static_assert(sizeof(AdamwParams<kMany>) <= 32764, "kernel parameters");
@@ -139,41 +144,55 @@ __device__ __forceinline__ void get_codes(const void* base, long long i, long lo
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], scale);
 }
-// v's codes, and the block's scale.  The arithmetic is the formula's step by step
-// (no contraction): |v| / scale as the bits of a number with four exponent and three
-// mantissa bits (times 2^-120, so that e4m3's denormals are float's), 20 bits below
-// them, the threshold's 20 bits added, cut off.
-template <bool WIDE, bool ROOT>
-__device__ __forceinline__ void put_codes(void* base, long long i, long long n, float* scale,
-                                          uint32_t walk, const float (&v)[8]) {
+// The largest magnitude of the block, as bits; odd: some value is not finite, and
+// the largest is that of the others (an element that is not finite becomes NaN and
+// leaves its neighbours alone).  SIGNED: the values may be negative.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t largest(const float (&v)[8], bool& odd) {
+  auto bits = [](float x) { return __float_as_uint(SIGNED ? fabsf(x) : x); };
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(fabsf(v[j])));
+  for (int j = 0; j < 8; ++j) top = max(top, bits(v[j]));
   top = __reduce_max_sync(0xffffffffu, top);
-  // An element that is not finite becomes NaN and leaves its neighbours alone.
-  const bool odd = top >= 0x7f800000u;  // (the same in every lane)
+  odd = top >= 0x7f800000u;  // (the same in every lane)
   if (odd) {
     top = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = __float_as_uint(fabsf(v[j]));
-      if (b < 0x7f800000u) top = max(top, b);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (bits(v[j]) < 0x7f800000u) top = max(top, bits(v[j]));
     top = __reduce_max_sync(0xffffffffu, top);
   }
-  const float amax = __uint_as_float(top);
-  const float inv = amax > 0x1p-110f ? __fdiv_rn(448.f, amax) : 0.f;
+  return top;
+}
+// v's codes.  The arithmetic is the formula's step by step: |v| / scale as the bits
+// of a number with four exponent and three mantissa bits (times 2^-120, so that
+// e4m3's denormals are float's), 20 bits below them, the threshold's 20 bits added,
+// cut off.
+template <bool WIDE, bool ROOT>
+__device__ __forceinline__ void put_codes(void* base, long long i, long long n, float inv, bool odd,
+                                          uint32_t walk, const float (&v)[8]) {
+  // one product where the factor is a normal number (up to 28672 as the largest)
+  const float tiny = __fmul_rn(inv, 0x1p-120f);
+  const bool one = tiny >= 0x1p-126f || inv == 0.f;
   uint32_t code[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float a = fabsf(v[j]);
     const uint32_t u = (walk + static_cast<uint32_t>(WIDE ? j : 32 * j) * kWalkI) >> 12;
-    const float y = __fmul_rn(__fmul_rn(a, inv), 0x1p-120f);
-    uint32_t c = min((__float_as_uint(y) + u) >> 20, 0x7eu);
-    if (ROOT && y > 0.f) c = max(c, 1u);
-    if (odd && __float_as_uint(a) >= 0x7f800000u) c = 0x7f;
-    if (!ROOT) c |= (__float_as_uint(v[j]) >> 24) & 0x80u;
+    float y = __fmul_rn(fabsf(v[j]), tiny);
+    if (!one) y = __fmul_rn(__fmul_rn(fabsf(v[j]), inv), 0x1p-120f);
+    const uint32_t b = __float_as_uint(y);
+    uint32_t c = min((b + u) >> 20, 0x7eu);
+    if (ROOT) c = max(c, min(b, 1u));
     code[j] = c;
+  }
+  if (odd) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if ((__float_as_uint(v[j]) & 0x7fffffffu) >= 0x7f800000u) code[j] = 0x7f;
+  }
+  if (!ROOT) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) code[j] |= (__float_as_uint(v[j]) >> 24) & 0x80u;
   }
   uint8_t* q = static_cast<uint8_t*>(base);
   if constexpr (WIDE) {
@@ -185,7 +204,23 @@ __device__ __forceinline__ void put_codes(void* base, long long i, long long n, 
     for (int j = 0; j < 8; ++j)
       if (i + 32 * j < n) q[i + 32 * j] = static_cast<uint8_t>(code[j]);
   }
-  if ((threadIdx.x & 31) == 0) *scale = __fdiv_rn(amax, 448.f);
+}
+// Both moments' codes and scales.  The four divisions (a scale and its inverse each)
+// are one: lanes 0 to 3 take one each.
+template <bool WIDE>
+__device__ __forceinline__ void put_moments(const Entry& e, long long at, long long i, uint32_t walk,
+                                            const float (&m)[8], const float (&r)[8]) {
+  bool odd_m, odd_r;
+  const float tm = __uint_as_float(largest<true>(m, odd_m)), tr = __uint_as_float(largest<false>(r, odd_r));
+  const int lane = threadIdx.x & 31;
+  const float t = lane & 1 ? tr : tm;
+  const float q = __fdiv_rn(lane & 2 ? 448.f : t, lane & 2 ? t : 448.f);
+  if (lane < 2) (lane ? e.vs : e.ms)[at >> 8] = q;
+  float im = __shfl_sync(0xffffffffu, q, 2), ir = __shfl_sync(0xffffffffu, q, 3);
+  im = tm > 0x1p-110f ? im : 0.f;
+  ir = tr > 0x1p-110f ? ir : 0.f;
+  put_codes<WIDE, false>(e.m, i, e.n, im, odd_m, walk, m);
+  put_codes<WIDE, true>(e.v, i, e.n, ir, odd_r, walk + kSaltV, r);
 }
 
 // ---------------------------------------------------------------- the step
@@ -224,14 +259,12 @@ __device__ __forceinline__ void step8(const Entry& e, long long at, const Rates&
       v[j] = __fadd_rn(__fmul_rn(v[j], r.b2), __fmul_rn(__fmul_rn(x, x), r.c2));
       root = sqrtf(v[j]);
     }
-    p[j] = fmaf(-r.rate * m[j], __frcp_rn(fmaf(root, r.root, r.eps)), p[j] * r.keep);
+    p[j] = fmaf(-r.rate, __fdividef(m[j], fmaf(root, r.root, r.eps)), p[j] * r.keep);
   }
   if constexpr (MASTER) put<WIDE>(e.master, i, n, p);
   put<WIDE>(static_cast<P*>(e.p), i, n, p);
   if constexpr (BITS8) {
-    const uint32_t walk = r.walk + static_cast<uint32_t>(i) * kWalkI;
-    put_codes<WIDE, false>(e.m, i, n, e.ms + (at >> 8), walk, m);
-    put_codes<WIDE, true>(e.v, i, n, e.vs + (at >> 8), walk + kSaltV, v);
+    put_moments<WIDE>(e, at, i, r.walk + static_cast<uint32_t>(i) * kWalkI, m, v);
   } else {
     put<WIDE>(static_cast<float*>(e.m), i, n, m);
     put<WIDE>(static_cast<float*>(e.v), i, n, v);
@@ -257,17 +290,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   r.walk = static_cast<uint32_t>(t) * kWalkT;
   const int lo = static_cast<int>(static_cast<long long>(blockIdx.x) * a.pieces / gridDim.x);
   const int hi = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * a.pieces / gridDim.x);
-  // the tensor of the first piece: the last one that starts at or before it
-  int k = 0, end = a.count;
-  while (end - k > 1) {
-    const int mid = (k + end) >> 1;
-    if (a.e[mid].first <= lo) k = mid;
-    else end = mid;
-  }
+  int k = a.hint[static_cast<int>(static_cast<long long>(blockIdx.x) * kGroups / gridDim.x)];
   for (int piece = lo; piece < hi; ++piece) {
-    while (k + 1 < a.count && a.e[k + 1].first <= piece) ++k;
+    while (a.first[k + 1] <= piece) ++k;
     const Entry& e = a.e[k];
-    const long long at = static_cast<long long>(piece - e.first) * kPiece + warp * 256;
+    const long long at = static_cast<long long>(piece - a.first[k]) * kPiece + warp * 256;
     if (at >= e.n) continue;
     if (e.wide && at + 256 <= e.n)
       step8<P, G, MASTER, BITS8, true>(e, at, r);
@@ -295,7 +322,7 @@ cudaError_t launch_n(const AdamwArgs& a, const AdamwParams<1>& common, int from,
     Entry& e = p.e[p.count++];
     e.p = t.param, e.master = t.master, e.g = t.grad, e.m = t.exp_avg, e.v = t.exp_avg_sq;
     e.ms = t.exp_avg_scale, e.vs = t.exp_avg_sq_scale, e.n = t.n;
-    e.first = static_cast<int>(pieces);
+    p.first[p.count - 1] = static_cast<int>(pieces);
     e.wide = aligned(t.param, 8 * sizeof(P)) && aligned(t.grad, 8 * sizeof(G)) &&
              (!MASTER || aligned(t.master, 32)) && aligned(t.exp_avg, BITS8 ? 8 : 32) &&
              aligned(t.exp_avg_sq, BITS8 ? 8 : 32);
@@ -304,7 +331,15 @@ cudaError_t launch_n(const AdamwArgs& a, const AdamwParams<1>& common, int from,
   if (pieces == 0) return cudaSuccess;
   if (pieces > 0x7fffffff) return cudaErrorInvalidValue;
   p.pieces = static_cast<int>(pieces);
+  p.first[p.count] = p.pieces;
   const int blocks = static_cast<int>(std::min<long long>(pieces, 16LL * num_sms()));
+  for (int g = 0, k = 0; g < kGroups; ++g) {
+    // the first block b of the group has b * kGroups / blocks = g
+    const long long b = (static_cast<long long>(g) * blocks + kGroups - 1) / kGroups;
+    const long long piece = b * pieces / blocks;
+    while (k + 1 < p.count && p.first[k + 1] <= piece) ++k;
+    p.hint[g] = static_cast<unsigned short>(k);
+  }
   return launch_pdl(adamw_kernel<P, G, MASTER, BITS8, N>, dim3(blocks), dim3(kThreads), 0, st, p);
 }
 

@@ -11,7 +11,8 @@
 // counts; a second kernel adds these up in the blocks' order (the same bits every
 // time), forms the slopes and the loss.  A token's logits lie in the registers of
 // `lanes` lanes (a power of two, 32 from 128 experts on), so that a softmax is
-// log2(lanes) shuffles and small gates fill their warps with tokens.
+// log2(lanes) shuffles and small gates fill their warps with tokens.  A call that one
+// block gets through in two steps (512 tokens of 8 experts) is one launch.
 #include <algorithm>
 
 #include "common.cuh"
@@ -30,6 +31,7 @@ struct BalanceParams {
   int T, E, k, len, sequences;  // len: tokens of a sequence
   int lanes;
   int chunks, rows;             // of a sequence: blocks, and tokens of one
+  bool alone;                   // one block, which finishes by itself
   float* sums;                  // [sequences * chunks][E]
   int32_t* hits;                // [sequences * chunks][E]
   int32_t* tokens;              // [sequences * chunks]
@@ -73,6 +75,20 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
   }
 }
 
+// One instruction each, within 2 ulp (a probability is as good as its logit's f32
+// rounding; with expf and a division the sigmoids took 35 instructions an element,
+// 14 us of 16384 x 256).
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // A token's logits (NV pieces of VEC in each of its lanes) to probabilities;
 // rest[]: of sigmoid scores 1 - a_te, else left.  As in the choice of the experts
 // NaN, -inf and the type's lowest value mask an expert (p = 0) and +inf is the
@@ -83,6 +99,7 @@ template <typename T, bool SOFTMAX, int N>
 __device__ __forceinline__ void probabilities(float (&z)[N], float (&rest)[SOFTMAX ? 1 : N], int lanes) {
   constexpr float kLow = sizeof(T) == 4 ? -3.402823466e38f : -3.389531390e38f;
   constexpr float kMost = 3.402823466e38f;
+  constexpr float kLog2e = 1.4426950408889634f;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -94,16 +111,19 @@ __device__ __forceinline__ void probabilities(float (&z)[N], float (&rest)[SOFTM
     const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      z[i] = expf(z[i] - ref);
+      z[i] = ex2((z[i] - ref) * kLog2e);
       sum += z[i];
     }
   } else {
-    const float c = top == -INFINITY ? 0.f : fminf(top, 0.f), ec = expf(c);
+    const float c = top == -INFINITY ? 0.f : fminf(top, 0.f), ec = ex2(c * kLog2e);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float e = expf(c - z[i]);
-      z[i] = 1.f / (ec + e);
-      rest[i] = e == INFINITY ? 1.f : e * z[i];  // 1 - a without its cancellation
+      const bool open = z[i] != -INFINITY;
+      // (2^126 stands for all that is larger: its reciprocal is still a number)
+      const float e = ex2(fminf((c - z[i]) * kLog2e, 126.f));
+      const float r = rcp(ec + e);
+      rest[i] = e * r;  // 1 - a without its cancellation
+      z[i] = open ? r : 0.f;
       sum += z[i];
     }
   }
@@ -113,9 +133,20 @@ __device__ __forceinline__ void probabilities(float (&z)[N], float (&rest)[SOFTM
   for (int i = 0; i < N; ++i) z[i] *= r;
 }
 
+// E hits / (k n^2 live), 0 of a sequence without tokens
+__device__ __forceinline__ float slope_of(int hits, int E, int k, int n, int live) {
+  if (n == 0) return 0.f;
+  return static_cast<float>(hits) * (static_cast<float>(E) / static_cast<float>(k)) /
+         (static_cast<float>(n) * static_cast<float>(n)) / static_cast<float>(live);
+}
+
+// tokens that a lane has in flight
+template <int N>
+constexpr int kUnroll = N >= 32 ? 1 : N >= 16 ? 2 : 4;
+
 template <typename T, bool SOFTMAX, int VEC, int NV>
 __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const BalanceParams p) {
-  constexpr int N = VEC * NV, U = N >= 16 ? 1 : N >= 8 ? 2 : 4;
+  constexpr int N = VEC * NV, U = kUnroll<N>;
   constexpr int kWarps = kFwdThreads / 32;
   __shared__ float sums[kWarps / 2 * 1024];
   __shared__ int hits[1024];
@@ -125,7 +156,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seq = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int t0 = seq * p.len + chunk * p.rows, t1 = min(t0 + p.rows, (seq + 1) * p.len);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.alone) *p.ticket = 0;
   for (int e = threadIdx.x; e < p.E; e += kFwdThreads) hits[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
   const int sub = lane & (p.lanes - 1), per = 32 / p.lanes;  // place in the token, tokens of a warp
@@ -200,14 +231,35 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   if (warp < kWarps / 2) put(warp);
   __syncthreads();
   const long long out = static_cast<long long>(blockIdx.x) * p.E;
+  float share = 0.f;
   for (int e = threadIdx.x; e < p.E; e += kFwdThreads) {
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps / 2; ++w) s += sums[w * p.E + e];
-    p.sums[out + e] = s;
-    p.hits[out + e] = hits[e];
+    if (p.alone) {
+      const float slope = slope_of(hits[e], p.E, p.k, tokens, 1);
+      p.counts[e] = hits[e];
+      p.slope[e] = slope;
+      share += slope * s;
+    } else {
+      p.sums[out + e] = s;
+      p.hits[out + e] = hits[e];
+    }
   }
-  if (threadIdx.x == 0) p.tokens[blockIdx.x] = tokens;
+  if (p.alone) {
+    __shared__ float shares[kWarps];
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) share += __shfl_xor_sync(0xffffffffu, share, o);
+    if (lane == 0) shares[warp] = share;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      share = 0.f;
+      for (int w = 0; w < kWarps; ++w) share += shares[w];
+      *p.loss = share;
+    }
+  } else if (threadIdx.x == 0) {
+    p.tokens[blockIdx.x] = tokens;
+  }
 }
 
 // An item is 32 experts of one sequence: a lane each, the chunks dealt out to the
@@ -258,10 +310,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
 #pragma unroll
       for (int w = 0; w < 8; ++w)
         live += s_live[w], n += s_n[w], sum += s_sum[w][lane], hit += s_hit[w][lane];
-      float slope = 0.f;
-      if (n > 0)
-        slope = static_cast<float>(hit) * (static_cast<float>(p.E) / static_cast<float>(p.k)) /
-                (static_cast<float>(n) * static_cast<float>(n)) / static_cast<float>(live);
+      const float slope = slope_of(hit, p.E, p.k, n, live);
       if (e < p.E) {
         p.counts[static_cast<long long>(b) * p.E + e] = hit;
         p.slope[static_cast<long long>(b) * p.E + e] = slope;
@@ -291,7 +340,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
 
 template <typename T, bool SOFTMAX, int VEC, int NV>
 __global__ void __launch_bounds__(kBwdThreads) balance_grad_kernel(const BalanceParams p) {
-  constexpr int N = VEC * NV, U = N >= 8 ? 1 : 2;
+  constexpr int N = VEC * NV, U = N >= 16 ? 1 : 2;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -351,10 +400,13 @@ __global__ void __launch_bounds__(kBwdThreads) balance_grad_kernel(const Balance
 // ---------------------------------------------------------------- host
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Blocks of the sums: one an SM, at least 32 tokens each.
-int plan_chunks(int T, int sequences) {
+// Blocks of a sequence's sums: two an SM in all, of at least 32 tokens each; one
+// alone where it needs no more than two steps of its 512 threads' lanes (512 x 8
+// in one launch 3 us less than in two).
+int plan_chunks(int T, int E, int sequences) {
   const int len = T / sequences;
-  return std::max(1, std::min(cdiv(num_sms(), sequences), cdiv(len, 32)));
+  if (sequences == 1 && static_cast<long long>(T) * E <= 8192) return 1;
+  return std::max(1, std::min(cdiv(2 * num_sms(), sequences), cdiv(len, 32)));
 }
 
 // The widest pieces that every row starts on; then the lanes of a token.
@@ -402,15 +454,16 @@ BalanceParams params(const BalanceArgs& a) {
 constexpr int kJoinBlocks = 1024;  // at most
 
 size_t balance_ws_bytes(int T, int E, int sequences) {
-  const size_t blocks = static_cast<size_t>(sequences) * plan_chunks(T, sequences);
+  const size_t blocks = static_cast<size_t>(sequences) * plan_chunks(T, E, sequences);
   return 2 * round256(blocks * E * 4) + round256(blocks * 4) + round256(kJoinBlocks * 4) + 256;
 }
 
 cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st) {
   BalanceParams p = params(a);
-  p.chunks = plan_chunks(a.T, a.sequences);
+  p.chunks = plan_chunks(a.T, a.E, a.sequences);
   p.rows = cdiv(p.len, p.chunks);
   const size_t blocks = static_cast<size_t>(a.sequences) * p.chunks;
+  p.alone = blocks == 1;
   char* at = static_cast<char*>(ws);
   p.sums = reinterpret_cast<float*>(at), at += round256(blocks * a.E * 4);
   p.hits = reinterpret_cast<int32_t*>(at), at += round256(blocks * a.E * 4);
@@ -425,7 +478,7 @@ cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st) {
                         dim3(kFwdThreads), 0, st, p);
     });
   });
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.alone) return e;
   const long long items = static_cast<long long>(cdiv(a.E, 32)) * a.sequences;
   return launch_pdl(balance_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(items, kJoinBlocks))),
                     dim3(kJoinThreads), 0, st, p);

@@ -226,16 +226,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           ok = arrived();
           if (!ok) break;
           const uint32_t taddr = taddr0 + (tcount & 1) * 256;
-          float x[32];
-          tmem_ld32(taddr, x);
-          tmem_ld_wait();
+          // (sixteen columns at a time: 64 sums and 32 more do not fit a thread's 96
+          // registers, and spilled ones cost 876 us instead of 6xx)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = kb ? v[i] + x[i] : x[i];
-          tmem_ld32(taddr + 32, x);
-          tmem_ld_wait();
-          release();
+          for (int q = 0; q < 4; ++q) {
+            float x[16];
+            tmem_ld16(taddr + 16 * q, x);
+            tmem_ld_wait();
+            if (q == 3) release();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[32 + i] = kb ? v[32 + i] + x[i] : x[i];
+            for (int i = 0; i < 16; ++i) v[16 * q + i] = kb ? v[16 * q + i] + x[i] : x[i];
+          }
           ++tcount;
         }
         // the four groups of a quarter meet below: they leave together
