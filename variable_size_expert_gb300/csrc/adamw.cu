@@ -6,9 +6,12 @@
 //
 // The tensors' addresses travel as kernel parameters: no table in device memory,
 // nothing to copy, and a captured call replays as it was.  The tensors are cut into
-// pieces of 2048 elements; a block takes a run of pieces, so that it looks its first
-// tensor up once and then walks on.  A warp's 256 elements are a block of the 8-bit
-// states: its largest value is one redux.sync.
+// pieces, a warp takes one; a block takes a run of pieces, so that it looks its first
+// tensor up once and then walks on.  256 elements, eight a lane, are a block of the
+// 8-bit states: its largest value is one redux.sync.  With 8-bit states a piece is
+// eight blocks where there are enough of them: their scales are then one 32-byte
+// sector, read and written once (one scale at a time, each 4-byte store into a sector
+// held the loads of its neighbours up: 348 us for 120M elements, 265 without scales).
 //
 // 8-bit moments: m and sqrt(v) as e4m3 codes times a float32 scale for each 256
 // elements of a tensor (largest magnitude / 448).  Rounding to nearest would never
@@ -29,7 +32,7 @@
 namespace mgg {
 namespace {
 
-constexpr int kThreads = 256, kPiece = kThreads * 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kFew = 24, kMany = 400;  // tensors of a launch, by parameter size
 constexpr int kGroups = 128;
 constexpr uint32_t kWalkI = 0x9E3779B1u, kWalkT = 0xC13FA9A9u, kSaltV = 0x80000000u;
@@ -46,6 +49,7 @@ struct Entry {
 template <int N>
 struct AdamwParams {
   int count, pieces;
+  int span;                   // blocks of 256 elements in a piece
   float b1, c1, b2, c2, eps;  // c: 1 - b
   float lr, decay;            // lr where lr_dev is null; weight decay
   double lnb1, lnb2;
@@ -62,6 +66,14 @@ struct AdamwParams {
 };
 static_assert(sizeof(AdamwParams<kMany>) <= 32764, "kernel parameters");
 
+__device__ __forceinline__ void bf16s(const uint4& q, float (&v)[8]) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
 // Eight elements from i on, `wide` as one access, else those below n, 32 apart.
 template <bool WIDE>
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
@@ -74,13 +86,7 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 template <bool WIDE>
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   static_assert(WIDE, "");
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+  bf16s(*reinterpret_cast<const uint4*>(p), v);
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
@@ -123,26 +129,27 @@ __device__ __forceinline__ void decode2(uint32_t c, float& a, float& b) {
       : "=f"(a), "=f"(b)
       : "r"(h));
 }
+// Eight codes, as they lie (WIDE) or gathered.
 template <bool WIDE>
-__device__ __forceinline__ void get_codes(const void* base, long long i, long long n, float scale,
-                                          float (&v)[8]) {
+__device__ __forceinline__ uint2 get_codes(const void* base, long long i, long long n) {
   const uint8_t* q = static_cast<const uint8_t*>(base);
   if constexpr (WIDE) {
-    const uint2 w = *reinterpret_cast<const uint2*>(q + i);
-    decode2(w.x, v[0], v[1]);
-    decode2(w.x >> 16, v[2], v[3]);
-    decode2(w.y, v[4], v[5]);
-    decode2(w.y >> 16, v[6], v[7]);
+    return *reinterpret_cast<const uint2*>(q + i);
   } else {
+    uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint32_t a = i + 32 * j < n ? q[i + 32 * j] : 0;
-      const uint32_t b = i + 32 * j + 32 < n ? q[i + 32 * j + 32] : 0;
-      decode2(a | b << 8, v[j], v[j + 1]);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (i + 32 * j < n) w[j / 4] |= static_cast<uint32_t>(q[i + 32 * j]) << (8 * (j % 4));
+    return make_uint2(w[0], w[1]);
   }
+}
+__device__ __forceinline__ void decode8(uint2 w, float scale, float (&v)[8]) {
+  decode2(w.x, v[0], v[1]);
+  decode2(w.x >> 16, v[2], v[3]);
+  decode2(w.y, v[4], v[5]);
+  decode2(w.y >> 16, v[6], v[7]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], scale);
+  for (int j = 0; j < 8; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), both(scale)), v[j], v[j + 1]);
 }
 // The largest magnitude of the block, as bits; odd: some value is not finite, and
 // the largest is that of the others (an element that is not finite becomes NaN and
@@ -164,115 +171,179 @@ __device__ __forceinline__ uint32_t largest(const float (&v)[8], bool& odd) {
   }
   return top;
 }
-// v's codes.  The arithmetic is the formula's step by step: |v| / scale as the bits
-// of a number with four exponent and three mantissa bits (times 2^-120, so that
-// e4m3's denormals are float's), 20 bits below them, the threshold's 20 bits added,
-// cut off.
-template <bool WIDE, bool ROOT>
-__device__ __forceinline__ void put_codes(void* base, long long i, long long n, float inv, bool odd,
-                                          uint32_t walk, const float (&v)[8]) {
-  // one product where the factor is a normal number (up to 28672 as the largest)
-  const float tiny = __fmul_rn(inv, 0x1p-120f);
-  const bool one = tiny >= 0x1p-126f || inv == 0.f;
-  uint32_t code[8];
+// v's codes: |v| / scale as the bits of a number with four exponent and three
+// mantissa bits (times 2^-120, so that e4m3's denormals are float's), 20 bits below
+// them, the threshold's 20 bits added, cut off.  The code's eight bits are left on
+// the top byte and gathered from there.
+template <bool ROOT, bool ONE>
+__device__ __forceinline__ uint2 codes(float inv, float tiny, bool odd, const uint32_t (&walk)[8],
+                                       const float (&v)[8]) {
+  uint32_t b[8], c[8], low = 0xffffffffu;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    float y0, y1;
+    if (ONE) {
+      unpack2(mul2(pack2(fabsf(v[j]), fabsf(v[j + 1])), both(tiny)), y0, y1);
+    } else {
+      y0 = (fabsf(v[j]) * inv) * 0x1p-120f, y1 = (fabsf(v[j + 1]) * inv) * 0x1p-120f;
+    }
+    b[j] = __float_as_uint(y0), b[j + 1] = __float_as_uint(y1);
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t u = (walk + static_cast<uint32_t>(WIDE ? j : 32 * j) * kWalkI) >> 12;
-    float y = __fmul_rn(fabsf(v[j]), tiny);
-    if (!one) y = __fmul_rn(__fmul_rn(fabsf(v[j]), inv), 0x1p-120f);
-    const uint32_t b = __float_as_uint(y);
-    uint32_t c = min((b + u) >> 20, 0x7eu);
-    if (ROOT) c = max(c, min(b, 1u));
-    code[j] = c;
+    if (ROOT) low = min(low, b[j]);
+    c[j] = min(walk[j] + b[j], 0x07efffffu);
+  }
+  if (ROOT && __any_sync(0xffffffffu, low < 0x100000u)) {  // (a root below one code)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (b[j]) c[j] = max(c[j], 0x100000u);
   }
   if (odd) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if ((__float_as_uint(v[j]) & 0x7fffffffu) >= 0x7f800000u) code[j] = 0x7f;
+      if ((__float_as_uint(v[j]) & 0x7fffffffu) >= 0x7f800000u) c[j] = 0x07f00000u;
   }
-  if (!ROOT) {
+  uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) code[j] |= (__float_as_uint(v[j]) >> 24) & 0x80u;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t* q = c + 4 * h;
+    const uint32_t lo = __byte_perm(q[0] << 4, q[1] << 4, 0x0073), hi = __byte_perm(q[2] << 4, q[3] << 4, 0x0073);
+    w[h] = __byte_perm(lo, hi, 0x5410) & 0x7f7f7f7fu;
+    if (!ROOT) {
+      const float* f = v + 4 * h;
+      const uint32_t s0 = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0073),
+                     s1 = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0073);
+      w[h] |= __byte_perm(s0, s1, 0x5410) & 0x80808080u;
+    }
   }
+  return make_uint2(w[0], w[1]);
+}
+template <bool WIDE, bool ROOT>
+__device__ __forceinline__ void put_codes(void* base, long long i, long long n, float inv, bool odd,
+                                          const uint32_t (&walk)[8], const float (&v)[8]) {
+  // one product where the factor is a normal number (up to 28672 as the largest)
+  const float tiny = inv * 0x1p-120f;
+  const uint2 w = tiny >= 0x1p-126f || inv == 0.f ? codes<ROOT, true>(inv, tiny, odd, walk, v)
+                                                  : codes<ROOT, false>(inv, tiny, odd, walk, v);
   uint8_t* q = static_cast<uint8_t*>(base);
   if constexpr (WIDE) {
-    *reinterpret_cast<uint2*>(q + i) =
-        make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                   code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+    *reinterpret_cast<uint2*>(q + i) = w;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + 32 * j < n) q[i + 32 * j] = static_cast<uint8_t>(code[j]);
+      if (i + 32 * j < n) q[i + 32 * j] = static_cast<uint8_t>((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
   }
 }
-// Both moments' codes and scales.  The four divisions (a scale and its inverse each)
-// are one: lanes 0 to 3 take one each.
+// Both moments' codes; returns their scales in lanes 0 and 1.  The four divisions (a
+// scale and its inverse each) are one: lanes 0 to 3 take one each.
 template <bool WIDE>
-__device__ __forceinline__ void put_moments(const Entry& e, long long at, long long i, uint32_t walk,
-                                            const float (&m)[8], const float (&r)[8]) {
+__device__ __forceinline__ float put_moments(const Entry& e, long long i, uint32_t walk, const float (&m)[8],
+                                             const float (&r)[8]) {
   bool odd_m, odd_r;
   const float tm = __uint_as_float(largest<true>(m, odd_m)), tr = __uint_as_float(largest<false>(r, odd_r));
   const int lane = threadIdx.x & 31;
   const float t = lane & 1 ? tr : tm;
   const float q = __fdiv_rn(lane & 2 ? 448.f : t, lane & 2 ? t : 448.f);
-  if (lane < 2) (lane ? e.vs : e.ms)[at >> 8] = q;
   float im = __shfl_sync(0xffffffffu, q, 2), ir = __shfl_sync(0xffffffffu, q, 3);
   im = tm > 0x1p-110f ? im : 0.f;
   ir = tr > 0x1p-110f ? ir : 0.f;
-  put_codes<WIDE, false>(e.m, i, e.n, im, odd_m, walk, m);
-  put_codes<WIDE, true>(e.v, i, e.n, ir, odd_r, walk + kSaltV, r);
+  // the thresholds' 20 bits; the salt turns the first of them
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = (walk + static_cast<uint32_t>(WIDE ? j : 32 * j) * kWalkI) >> 12;
+  put_codes<WIDE, false>(e.m, i, e.n, im, odd_m, w, m);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] ^= kSaltV >> 12;
+  put_codes<WIDE, true>(e.v, i, e.n, ir, odd_r, w, r);
+  return q;
 }
 
 // ---------------------------------------------------------------- the step
+// One instruction each, within 2 ulp; second moments below 1e-38 count as 0.
+__device__ __forceinline__ float root(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float inverse(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 struct Rates {
   float b1, c1, b2, c2, eps, keep, rate, root, gs;
   uint32_t walk;
 };
 
-// Eight elements of this lane, of the warp's 256 from `at` on.
-template <typename P, typename G, bool MASTER, bool BITS8, bool WIDE>
-__device__ __forceinline__ void step8(const Entry& e, long long at, const Rates& r) {
-  const int lane = threadIdx.x & 31;
-  const long long i = at + (WIDE ? 8 * lane : lane), n = e.n;
+// Eight elements of this lane, of the warp's 256 from `at` on: what is read, then
+// the step on it.
+template <typename P, typename G, bool MASTER, bool BITS8>
+struct Held {
   float p[8], g[8], m[8], v[8];
-  get<WIDE>(static_cast<const G*>(e.g), i, n, g);
-  if constexpr (MASTER)
-    get<WIDE>(static_cast<const float*>(e.master), i, n, p);
-  else
-    get<WIDE>(static_cast<const P*>(e.p), i, n, p);
-  if constexpr (BITS8) {
-    get_codes<WIDE>(e.m, i, n, e.ms[at >> 8], m);
-    get_codes<WIDE>(e.v, i, n, e.vs[at >> 8], v);
-  } else {
-    get<WIDE>(static_cast<const float*>(e.m), i, n, m);
-    get<WIDE>(static_cast<const float*>(e.v), i, n, v);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float x = __fmul_rn(g[j], r.gs);
-    m[j] = __fadd_rn(__fmul_rn(m[j], r.b1), __fmul_rn(x, r.c1));
-    float root;
+  uint4 gc;  // eight bfloat16 gradients as they lie
+  uint2 mc, vc;
+  template <bool WIDE>
+  __device__ __forceinline__ void read(const Entry& e, long long at) {
+    const int lane = threadIdx.x & 31;
+    const long long i = at + (WIDE ? 8 * lane : lane), n = e.n;
+    if constexpr (WIDE && sizeof(G) == 2)
+      gc = *reinterpret_cast<const uint4*>(static_cast<const G*>(e.g) + i);
+    else
+      get<WIDE>(static_cast<const G*>(e.g), i, n, g);
+    if constexpr (MASTER)
+      get<WIDE>(static_cast<const float*>(e.master), i, n, p);
+    else
+      get<WIDE>(static_cast<const P*>(e.p), i, n, p);
     if constexpr (BITS8) {
-      root = __fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(v[j], v[j]), r.b2), __fmul_rn(__fmul_rn(x, x), r.c2)));
-      v[j] = root;
+      mc = get_codes<WIDE>(e.m, i, n), vc = get_codes<WIDE>(e.v, i, n);
     } else {
-      v[j] = __fadd_rn(__fmul_rn(v[j], r.b2), __fmul_rn(__fmul_rn(x, x), r.c2));
-      root = sqrtf(v[j]);
+      get<WIDE>(static_cast<const float*>(e.m), i, n, m);
+      get<WIDE>(static_cast<const float*>(e.v), i, n, v);
     }
-    p[j] = fmaf(-r.rate, __fdividef(m[j], fmaf(root, r.root, r.eps)), p[j] * r.keep);
   }
-  if constexpr (MASTER) put<WIDE>(e.master, i, n, p);
-  put<WIDE>(static_cast<P*>(e.p), i, n, p);
-  if constexpr (BITS8) {
-    put_moments<WIDE>(e, at, i, r.walk + static_cast<uint32_t>(i) * kWalkI, m, v);
-  } else {
-    put<WIDE>(static_cast<float*>(e.m), i, n, m);
-    put<WIDE>(static_cast<float*>(e.v), i, n, v);
+  // ms, vs: the block's scales; returns the new ones in lanes 0 and 1
+  template <bool WIDE>
+  __device__ __forceinline__ float step(const Entry& e, long long at, const Rates& r, float ms, float vs) {
+    const int lane = threadIdx.x & 31;
+    const long long i = at + (WIDE ? 8 * lane : lane), n = e.n;
+    if constexpr (WIDE && sizeof(G) == 2) bf16s(gc, g);
+    if constexpr (BITS8) {
+      decode8(mc, ms * r.b1, m);  // b1 m
+      decode8(vc, vs, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const F2 x = mul2(pack2(g[j], g[j + 1]), both(r.gs));
+      F2 mm = pack2(m[j], m[j + 1]), vv = pack2(v[j], v[j + 1]);
+      if constexpr (!BITS8) mm = mul2(mm, both(r.b1));
+      mm = fma2(x, both(r.c1), mm);
+      if constexpr (BITS8) vv = mul2(vv, vv);
+      vv = fma2(mul2(x, x), both(r.c2), mul2(vv, both(r.b2)));
+      float v0, v1, d0, d1, p0, p1;
+      unpack2(vv, v0, v1);
+      const float r0 = root(v0), r1 = root(v1);
+      unpack2(fma2(pack2(r0, r1), both(r.root), both(r.eps)), d0, d1);
+      const F2 u = mul2(mm, pack2(inverse(d0), inverse(d1)));
+      unpack2(fma2(both(-r.rate), u, mul2(pack2(p[j], p[j + 1]), both(r.keep))), p0, p1);
+      p[j] = p0, p[j + 1] = p1;
+      unpack2(mm, m[j], m[j + 1]);
+      v[j] = BITS8 ? r0 : v0, v[j + 1] = BITS8 ? r1 : v1;
+    }
+    if constexpr (MASTER) put<WIDE>(e.master, i, n, p);
+    put<WIDE>(static_cast<P*>(e.p), i, n, p);
+    if constexpr (BITS8) {
+      return put_moments<WIDE>(e, i, r.walk + static_cast<uint32_t>(i) * kWalkI, m, v);
+    } else {
+      put<WIDE>(static_cast<float*>(e.m), i, n, m);
+      put<WIDE>(static_cast<float*>(e.v), i, n, v);
+      return 0.f;
+    }
   }
-}
+};
 
 template <typename P, typename G, bool MASTER, bool BITS8, int N>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwParams<N> a) {
+__global__ void __launch_bounds__(kThreads, BITS8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamwParams<N> a) {
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5;
@@ -291,15 +362,40 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const int lo = static_cast<int>(static_cast<long long>(blockIdx.x) * a.pieces / gridDim.x);
   const int hi = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * a.pieces / gridDim.x);
   int k = a.hint[static_cast<int>(static_cast<long long>(blockIdx.x) * kGroups / gridDim.x)];
-  for (int piece = lo; piece < hi; ++piece) {
+  const int lane = threadIdx.x & 31;
+  Held<P, G, MASTER, BITS8> held;
+  for (int piece = lo + warp; piece < hi; piece += kWarps) {
     while (a.first[k + 1] <= piece) ++k;
-    const Entry& e = a.e[k];
-    const long long at = static_cast<long long>(piece - a.first[k]) * kPiece + warp * 256;
-    if (at >= e.n) continue;
-    if (e.wide && at + 256 <= e.n)
-      step8<P, G, MASTER, BITS8, true>(e, at, r);
-    else
-      step8<P, G, MASTER, BITS8, false>(e, at, r);
+    const Entry e = a.e[k];
+    long long at = static_cast<long long>(piece - a.first[k]) * a.span * 256;
+    if constexpr (BITS8) {
+      const int blocks = static_cast<int>(min(static_cast<long long>(a.span), (e.n - at + 255) >> 8));
+      float ms = 0.f, vs = 0.f;  // the piece's scales, a lane each
+      if (lane < blocks) ms = e.ms[(at >> 8) + lane], vs = e.vs[(at >> 8) + lane];
+      const long long first = at >> 8;
+      // lane b's scales become the ones that the step on block b returns
+      auto renew = [&](int b, float q) {
+        const float m = __shfl_sync(0xffffffffu, q, 0), v = __shfl_sync(0xffffffffu, q, 1);
+        if (lane == b) ms = m, vs = v;
+      };
+      auto of = [&](float s, int b) { return __shfl_sync(0xffffffffu, s, b); };
+      for (int b = 0; b < blocks; ++b, at += 256) {
+        if (e.wide && at + 256 <= e.n) {
+          held.template read<true>(e, at);
+          renew(b, held.template step<true>(e, at, r, of(ms, b), of(vs, b)));
+        } else {
+          held.template read<false>(e, at);
+          renew(b, held.template step<false>(e, at, r, of(ms, b), of(vs, b)));
+        }
+      }
+      if (lane < blocks) e.ms[first + lane] = ms, e.vs[first + lane] = vs;
+    } else if (e.wide && at + 256 <= e.n) {
+      held.template read<true>(e, at);
+      held.template step<true>(e, at, r, 0.f, 0.f);
+    } else {
+      held.template read<false>(e, at);
+      held.template step<false>(e, at, r, 0.f, 0.f);
+    }
   }
 }
 
@@ -315,6 +411,11 @@ cudaError_t launch_n(const AdamwArgs& a, const AdamwParams<1>& common, int from,
   p.lr = common.lr, p.decay = common.decay, p.lnb1 = common.lnb1, p.lnb2 = common.lnb2;
   p.step = common.step, p.lr_dev = common.lr_dev, p.step_dev = common.step_dev;
   p.grad_scale = common.grad_scale;
+  // a warp's piece: a block; eight (8-bit states) where that still leaves the GPU full
+  long long all = 0;
+  for (int i = from; i < from + count; ++i) all += (a.tensors[i].n + 255) >> 8;
+  p.span = BITS8 && all >= 8LL * 32 * num_sms() ? 8 : 1;
+  const long long piece = 256LL * p.span;
   long long pieces = 0;
   for (int i = from; i < from + count; ++i) {
     const mgg_adamw_tensor& t = a.tensors[i];
@@ -326,18 +427,18 @@ cudaError_t launch_n(const AdamwArgs& a, const AdamwParams<1>& common, int from,
     e.wide = aligned(t.param, 8 * sizeof(P)) && aligned(t.grad, 8 * sizeof(G)) &&
              (!MASTER || aligned(t.master, 32)) && aligned(t.exp_avg, BITS8 ? 8 : 32) &&
              aligned(t.exp_avg_sq, BITS8 ? 8 : 32);
-    pieces += (t.n + kPiece - 1) / kPiece;
+    pieces += (t.n + piece - 1) / piece;
   }
   if (pieces == 0) return cudaSuccess;
   if (pieces > 0x7fffffff) return cudaErrorInvalidValue;
   p.pieces = static_cast<int>(pieces);
   p.first[p.count] = p.pieces;
-  const int blocks = static_cast<int>(std::min<long long>(pieces, 16LL * num_sms()));
+  const int blocks = static_cast<int>(std::min<long long>((pieces + kWarps - 1) / kWarps, 16LL * num_sms()));
   for (int g = 0, k = 0; g < kGroups; ++g) {
     // the first block b of the group has b * kGroups / blocks = g
     const long long b = (static_cast<long long>(g) * blocks + kGroups - 1) / kGroups;
-    const long long piece = b * pieces / blocks;
-    while (k + 1 < p.count && p.first[k + 1] <= piece) ++k;
+    const long long at = b * pieces / blocks;
+    while (k + 1 < p.count && p.first[k + 1] <= at) ++k;
     p.hint[g] = static_cast<unsigned short>(k);
   }
   return launch_pdl(adamw_kernel<P, G, MASTER, BITS8, N>, dim3(blocks), dim3(kThreads), 0, st, p);

@@ -89,24 +89,35 @@ __device__ __forceinline__ float rcp(float v) {
   return r;
 }
 
-// A token's logits (NV pieces of VEC in each of its lanes) to probabilities;
-// rest[]: of sigmoid scores 1 - a_te, else left.  As in the choice of the experts
-// NaN, -inf and the type's lowest value mask an expert (p = 0) and +inf is the
-// largest finite number.  Sigmoids are taken relative to the token's largest where
-// that is below a half (c = min(0, top)): a e^-c = 1 / (e^c + e^(c - z)), so that a
-// token whose scores all vanish in f32 keeps its distribution.
-template <typename T, bool SOFTMAX, int N>
-__device__ __forceinline__ void probabilities(float (&z)[N], float (&rest)[SOFTMAX ? 1 : N], int lanes) {
+// v joined over a token's lanes (WARP: all 32, as with more than one piece a lane; a
+// loop over their number cost a third of the instructions).
+template <bool WARP, typename F>
+__device__ __forceinline__ float over_lanes(float v, int lanes, F join) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2)
+    if (WARP || o < lanes) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// A token's logits (NV pieces of VEC in each of its lanes) to scores s and the
+// inverse of their sum over the token: p = s r.  rest[]: of sigmoid scores 1 - a_te,
+// else left.  As in the choice of the experts NaN, -inf and the type's lowest value
+// mask an expert (s = 0) and +inf is the largest finite number.  Sigmoids are taken
+// relative to the token's largest where that is below a half (c = min(0, top)):
+// a e^-c = 1 / (e^c + e^(c - z)), so that a token whose scores all vanish in f32
+// keeps its distribution.
+template <typename T, bool SOFTMAX, bool WARP, int N>
+__device__ __forceinline__ float scores(float (&z)[N], float (&rest)[SOFTMAX ? 1 : N], int lanes) {
   constexpr float kLow = sizeof(T) == 4 ? -3.402823466e38f : -3.389531390e38f;
   constexpr float kMost = 3.402823466e38f;
   constexpr float kLog2e = 1.4426950408889634f;
   float top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    z[i] = z[i] > kLow ? fminf(z[i], kMost) : -INFINITY;
+    z[i] = z[i] > kLow ? SOFTMAX ? fminf(z[i], kMost) : z[i] : -INFINITY;
     top = fmaxf(top, z[i]);
   }
-  for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = over_lanes<WARP>(top, lanes, [](float a, float b) { return fmaxf(a, b); });
   if constexpr (SOFTMAX) {
     const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
@@ -127,10 +138,22 @@ __device__ __forceinline__ void probabilities(float (&z)[N], float (&rest)[SOFTM
       sum += z[i];
     }
   }
-  for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float r = sum > 0.f ? 1.f / sum : 0.f;
+  sum = over_lanes<WARP>(sum, lanes, [](float a, float b) { return a + b; });
+  return sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+}
+
+// NV pieces of a row, `stride` elements apart, those from `width` on as `fill`.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_row(const T* row, float fill, int width, int stride, float* v) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) z[i] *= r;
+  for (int j = 0; j < NV; ++j) {
+    if (j * stride < width) {
+      load_vec<T, VEC>(row + j * stride, v + j * VEC);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j * VEC + i] = fill;
+    }
+  }
 }
 
 // E hits / (k n^2 live), 0 of a sequence without tokens
@@ -159,8 +182,9 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   if (blockIdx.x == 0 && threadIdx.x == 0 && !p.alone) *p.ticket = 0;
   for (int e = threadIdx.x; e < p.E; e += kFwdThreads) hits[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
-  const int sub = lane & (p.lanes - 1), per = 32 / p.lanes;  // place in the token, tokens of a warp
-  const int step = kWarps * per;
+  const int sub = lane & (p.lanes - 1), place = lane / p.lanes;  // in the token, of the token in the warp
+  const int per = 32 / p.lanes, step = kWarps * per;
+  const int width = p.E - sub * VEC;  // columns from this lane's first on
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
@@ -170,26 +194,18 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
     bool on[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * step + lane / p.lanes;
-      on[u] = t < t1 && (!p.mask || p.mask[t]);
-      const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = (j * p.lanes + sub) * VEC;
-        if (t < t1 && e < p.E) {
-          load_vec<T, VEC>(row + e, &z[u][j * VEC]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) z[u][j * VEC + i] = -INFINITY;
-        }
-      }
+      const int t = min(tb + u * step + place, t1 - 1);  // (past the end: a token that is not used)
+      on[u] = tb + u * step + place < t1 && (!p.mask || p.mask[t]);
+      load_row<T, VEC, NV>(static_cast<const T*>(p.logits) + t * p.ldl + sub * VEC, -INFINITY, width, VEC * p.lanes,
+                           z[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float rest[SOFTMAX ? 1 : N];
-      probabilities<T, SOFTMAX, N>(z[u], rest, p.lanes);
+      const float r = scores<T, SOFTMAX, (NV > 1), N>(z[u], rest, p.lanes);
+      const float w = on[u] ? r : 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] += on[u] ? z[u][i] : 0.f;
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(z[u][i], w, acc[i]);
       mine += on[u] && sub == 0;
     }
   }
@@ -274,10 +290,14 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cols = cdiv(p.E, 32), items = cols * p.sequences;
   int live = 0;
-  for (int b = threadIdx.x; b < p.sequences; b += kJoinThreads) {
-    int n = 0;
-    for (int c = 0; c < p.chunks; ++c) n |= p.tokens[b * p.chunks + c];
-    live += n != 0;
+  if (p.chunks == 1) {
+    for (int b = threadIdx.x; b < p.sequences; b += kJoinThreads) live += p.tokens[b] != 0;
+  } else {  // (few sequences: a warp each)
+    for (int b = warp; b < p.sequences; b += 8) {
+      bool any = false;
+      for (int c = lane; c < p.chunks; c += 32) any |= p.tokens[b * p.chunks + c] != 0;
+      live += __any_sync(0xffffffffu, any) && lane == 0;
+    }
   }
   live = __reduce_add_sync(0xffffffffu, live);
   if (lane == 0) s_live[warp] = live;
@@ -286,18 +306,18 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
     const int b = it / cols, e = (it % cols) * 32 + lane;
     float sum = 0.f;
     int hit = 0, n = 0;
-    for (int c = warp; c < p.chunks; c += 32) {
-      float f[4];
-      int h[4];
+    for (int c = warp; c < p.chunks; c += 64) {
+      float f[8];
+      int h[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const bool any = c + 8 * u < p.chunks && e < p.E;
         const long long at = (static_cast<long long>(b) * p.chunks + c + 8 * u) * p.E + e;
         f[u] = any ? p.sums[at] : 0.f;
         h[u] = any ? p.hits[at] : 0;
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sum += f[u], hit += h[u];
+      for (int u = 0; u < 8; ++u) sum += f[u], hit += h[u];
     }
     for (int c = threadIdx.x; c < p.chunks; c += kJoinThreads) n += p.tokens[b * p.chunks + c];
     n = __reduce_add_sync(0xffffffffu, n);
@@ -339,60 +359,62 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
 }
 
 template <typename T, bool SOFTMAX, int VEC, int NV>
-__global__ void __launch_bounds__(kBwdThreads) balance_grad_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(kBwdThreads, VEC* NV <= 8 ? 4 : 1) balance_grad_kernel(const BalanceParams p) {
   constexpr int N = VEC * NV, U = N >= 16 ? 1 : 2;
+  constexpr int SV = VEC > 1 ? 4 : 1;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane & (p.lanes - 1), per = 32 / p.lanes;
+  const int sub = lane & (p.lanes - 1), place = lane / p.lanes, per = 32 / p.lanes;
   const int warps = gridDim.x * (kBwdThreads / 32), step = warps * per;
+  const int width = p.E - sub * VEC, stride = VEC * p.lanes;
   const float g = *p.dloss;
   for (int tb = (blockIdx.x * (kBwdThreads / 32) + warp) * per; tb < p.T; tb += U * step) {
-    float z[U][N], s[U][N];
+    float z[U][N];
     bool on[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * step + lane / p.lanes;
-      const bool any = t < p.T;
-      on[u] = any && (!p.mask || p.mask[t]);
-      const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
-      const float* slope = p.slope + static_cast<long long>(any ? t / p.len : 0) * p.E;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = (j * p.lanes + sub) * VEC;
-        if (any && e < p.E) {
-          load_vec<T, VEC>(row + e, &z[u][j * VEC]);
-#pragma unroll
-          for (int i = 0; i < VEC; i += VEC > 1 ? 4 : 1)
-            load_vec<float, (VEC > 1 ? 4 : 1)>(slope + e + i, &s[u][j * VEC + i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) z[u][j * VEC + i] = -INFINITY, s[u][j * VEC + i] = 0.f;
-        }
-      }
+      const int t = min(tb + u * step + place, p.T - 1);  // (past the end: a token that is not stored)
+      on[u] = !p.mask || p.mask[t];
+      load_row<T, VEC, NV>(static_cast<const T*>(p.logits) + t * p.ldl + sub * VEC, -INFINITY, width, stride, z[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * step + lane / p.lanes;
+      const int t = tb + u * step + place;
+      // (the same rows again and again: they lie in L1)
+      const float* slope = p.slope + sub * VEC;
+      if (p.sequences > 1) slope += static_cast<long long>(min(t, p.T - 1) / p.len) * p.E;
+      float s[N];
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; i += SV) {
+          if (j * stride < width) {
+            load_vec<float, SV>(slope + j * stride + i, &s[j * VEC + i]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < SV; ++q) s[j * VEC + i + q] = 0.f;
+          }
+        }
       float rest[SOFTMAX ? 1 : N];
-      probabilities<T, SOFTMAX, N>(z[u], rest, p.lanes);
+      const float r = scores<T, SOFTMAX, (NV > 1), N>(z[u], rest, p.lanes);
       float dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) dot = fmaf(z[u][i], s[u][i], dot);
-      for (int o = p.lanes >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      for (int i = 0; i < N; ++i) dot = fmaf(z[u][i], s[i], dot);
+      dot = over_lanes<(NV > 1)>(dot, p.lanes, [](float a, float b) { return a + b; });
+      dot *= r;
+      const float w = on[u] ? r * g : 0.f;
       if (t >= p.T) continue;
-      T* out = static_cast<T*>(p.dlogits) + static_cast<long long>(t) * p.E;
+      T* out = static_cast<T*>(p.dlogits) + static_cast<long long>(t) * p.E + sub * VEC;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float d = z[u][i] * (s[u][i] - dot);
+        float d = (z[u][i] * w) * (s[i] - dot);
         if constexpr (!SOFTMAX) d *= rest[i];
-        z[u][i] = on[u] && z[u][i] > 0.f ? d * g : 0.f;
+        z[u][i] = d;
       }
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = (j * p.lanes + sub) * VEC;
-        if (e < p.E) store_vec<T, VEC>(out + e, &z[u][j * VEC]);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (j * stride < width) store_vec<T, VEC>(out + j * stride, &z[u][j * VEC]);
     }
   }
 }

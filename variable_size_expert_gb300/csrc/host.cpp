@@ -502,13 +502,16 @@ struct List {
   List(const List&) = delete;
   List& operator=(const List&) = delete;
   bool given() const { return fast != nullptr; }
-  // the i-th: of this dtype and number of elements, dense, on the device
-  void* at(Py_ssize_t i, ScalarType t, int64_t n, const at::Device& dev) const {
-    const Tensor& x = tensor(PySequence_Fast_GET_ITEM(fast, i), what);
-    if (x.scalar_type() != t) fail(PyExc_TypeError, "%s: the tensors' dtype differs or is not supported", what);
-    if (x.numel() != n) fail(PyExc_ValueError, "%s: a tensor has %ld elements, not %ld", what, x.numel(), n);
-    if (x.device() != dev) fail(PyExc_ValueError, "%s must be on the first parameter's device", what);
-    if (!x.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", what);
+  const Tensor& get(Py_ssize_t i) const { return tensor(PySequence_Fast_ITEMS(fast)[i], what); }
+  // the i-th: of this dtype and number of elements, dense, on the device (a
+  // training step checks a thousand of these: one look at the tensor's own fields)
+  void* at(Py_ssize_t i, caffe2::TypeMeta t, int64_t n, c10::Device dev) const {
+    const Tensor& x = get(i);
+    const c10::TensorImpl* p = x.unsafeGetTensorImpl();
+    if (p->dtype() != t) fail(PyExc_TypeError, "%s: the tensors' dtype differs or is not supported", what);
+    if (p->numel() != n) fail(PyExc_ValueError, "%s: a tensor has %ld elements, not %ld", what, x.numel(), n);
+    if (p->device() != dev) fail(PyExc_ValueError, "%s must be on the first parameter's device", what);
+    if (!p->is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", what);
     return x.data_ptr();
   }
   PyObject* fast = nullptr;
@@ -527,35 +530,43 @@ PyObject* adamw_step(PyObject* const* a) {
   const double lr = THPVariable_Check(a[5]) ? 0.0 : number(a[5]);
   const long long step = THPVariable_Check(a[4]) ? 0 : wide_integer(a[4]);
   if (n == 0) return none();
-  const Tensor& first = tensor(PySequence_Fast_GET_ITEM(params.fast, 0), "params");
+  const Tensor& first = params.get(0);
   on_gpu(first);
-  const at::Device dev = first.device();
+  const c10::Device dev = first.device();
   const OnDevice on(first, {{a[4], "step"}, {a[5], "lr"}, {a[13], "grad_scale"}});
   const float* lr_dev = THPVariable_Check(a[5]) ? scalar_f32(tensor(a[5], "lr"), "lr") : nullptr;
-  const int32_t* step_dev = THPVariable_Check(a[4]) ? status_word(a[4]) : nullptr;
+  const int32_t* step_dev = nullptr;
+  if (THPVariable_Check(a[4])) {
+    const Tensor& s = tensor(a[4], "step");
+    if (s.scalar_type() != at::kInt || s.numel() != 1) fail(PyExc_ValueError, "%s must be int32 [1]", "step");
+    on_gpu(s);
+    step_dev = static_cast<const int32_t*>(s.data_ptr());
+  }
   const float* gs = a[13] == Py_None ? nullptr : scalar_f32(tensor(a[13], "grad_scale"), "grad_scale");
   const ScalarType pt = first.scalar_type(),
-                   gt = tensor(PySequence_Fast_GET_ITEM(grads.fast, 0), "grads").scalar_type();
+                   gt = grads.get(0).scalar_type();
   const mgg_dtype pc = code(pt), gc = code(gt);
-  const ScalarType state = ms.given() ? at::kFloat8_e4m3fn : at::kFloat;
+  const caffe2::TypeMeta state = c10::scalarTypeToTypeMeta(ms.given() ? at::kFloat8_e4m3fn : at::kFloat),
+                         f32 = c10::scalarTypeToTypeMeta(at::kFloat), pm = c10::scalarTypeToTypeMeta(pt),
+                         gm = c10::scalarTypeToTypeMeta(gt);
   std::vector<mgg_adamw_tensor> t(static_cast<size_t>(n));
   std::vector<std::pair<const char*, int64_t>> spans;
   spans.reserve(t.size());
   for (Py_ssize_t i = 0; i < n; ++i) {
-    const int64_t size = tensor(PySequence_Fast_GET_ITEM(params.fast, i), "params").numel();
+    const int64_t size = params.get(i).numel();
     const int64_t blocks = (size + MGG_ADAMW_BLOCK - 1) / MGG_ADAMW_BLOCK;
     mgg_adamw_tensor& e = t[static_cast<size_t>(i)];
     e.n = size;
-    e.param = params.at(i, pt, size, dev);
-    e.grad = grads.at(i, gt, size, dev);
+    e.param = params.at(i, pm, size, dev);
+    e.grad = grads.at(i, gm, size, dev);
     e.exp_avg = m.at(i, state, size, dev);
     e.exp_avg_sq = v.at(i, state, size, dev);
-    e.master = masters.given() ? static_cast<float*>(masters.at(i, at::kFloat, size, dev)) : nullptr;
-    e.exp_avg_scale = ms.given() ? static_cast<float*>(ms.at(i, at::kFloat, blocks, dev)) : nullptr;
-    e.exp_avg_sq_scale = ms.given() ? static_cast<float*>(vs.at(i, at::kFloat, blocks, dev)) : nullptr;
+    e.master = masters.given() ? static_cast<float*>(masters.at(i, f32, size, dev)) : nullptr;
+    e.exp_avg_scale = ms.given() ? static_cast<float*>(ms.at(i, f32, blocks, dev)) : nullptr;
+    e.exp_avg_sq_scale = ms.given() ? static_cast<float*>(vs.at(i, f32, blocks, dev)) : nullptr;
     if (size) spans.emplace_back(static_cast<const char*>(e.param), size * (pt == at::kFloat ? 4 : 2));
   }
-  std::sort(spans.begin(), spans.end());
+  if (!std::is_sorted(spans.begin(), spans.end())) std::sort(spans.begin(), spans.end());
   for (size_t i = 1; i < spans.size(); ++i)
     if (spans[i - 1].first + spans[i - 1].second > spans[i].first)
       fail(PyExc_ValueError, "%s must not overlap (is one of them listed twice?)", "params");
