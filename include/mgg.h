@@ -59,6 +59,9 @@
  *   MGG_FFN_BWD_SPLIT="a,b"  mgg_moe_ffn_backward's GEMMs side by side on
  *                      shares a (dh) and b (dx) of the CTA pairs (default:
  *                      one after the other)
+ *   MGG_VOCAB_PIECE    columns of the vocabulary (rounded up to 64) that
+ *                      mgg_linear_cross_entropy_backward takes at a time
+ *                      (default: as many as give its bf16 piece 256 MB)
  */
 #ifndef MGG_H
 #define MGG_H
@@ -722,7 +725,8 @@ mgg_status mgg_linear_backward(const void* dy, mgg_dtype dy_dtype, int64_t lddy,
  * Logits mask experts as in mgg_select_experts (p = 0; a token with no expert
  * left adds nothing to p, its choices count).  An id outside [0, E) sets
  * MGG_DEV_BAD_EXPERT_ID and is not counted.  Sums are f32, in a fixed order.
- * ws: mgg_workspace_bytes(MGG_OP_BALANCE, T, sequences, E, 0, 0, ...).
+ * ws: mgg_workspace_bytes(MGG_OP_BALANCE, T, sequences, E, 0, 0, ...); 0 for small
+ * calls, which then need none.
  * Errors: MGG_ERR_INVALID_ARG (null, T < 0, E < 1, E > MGG_MAX_EXPERTS, k < 1,
  * k > MGG_MAX_TOPK, ldl < E, sequences < 1 or not dividing T, a scoring other
  * than MGG_SCORE_SOFTMAX and MGG_SCORE_SIGMOID), MGG_ERR_DTYPE,

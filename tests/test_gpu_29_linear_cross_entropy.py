@@ -75,13 +75,32 @@ def test_forward_backward(T, K, V, reduction):
     _check(x, W, t, reduction, (0.0, 1e-3)[h % 2], g)
 
 
-# pieces of the vocabulary (a piece takes 64 MB at these sizes, 2048 columns at
-# least): two of them, and the last one narrow
-@pytest.mark.parametrize("T,K,V,reduction", [(16500, 64, 2056, "mean"), (16500, 40, 4111, "none"),
-                                             (20000, 24, 2049, "sum")])
-def test_pieces(T, K, V, reduction):
+# pieces of the vocabulary: two to eight, the last one narrow, one slice of dx in it
+# or several; few tokens (d in two parts) and many
+@pytest.mark.parametrize("T,K,V,piece,reduction", [(300, 64, 1000, 256, "mean"), (1, 40, 2000, 1024, "none"),
+                                                   (128, 72, 515, 64, "sum"), (129, 200, 4097, 2048, "mean"),
+                                                   (700, 136, 3000, 1500, "none")])
+def test_pieces(T, K, V, piece, reduction, monkeypatch):
+    monkeypatch.setenv("MGG_VOCAB_PIECE", str(piece))
     x, W, t, g = _inputs(T, K, V, T)
     _check(x, W, t, reduction, 1e-4, g)
+
+
+def test_pieces_of_the_default_size():
+    x, W, t, g = _inputs(70000, 8, 2049, 1)
+    _check(x, W, t, "mean", 0.0, g)
+
+
+# rows off 64-byte lines: x is copied from 256 tokens on, W's pieces from 2048 on
+@pytest.mark.parametrize("T,K,V", [(256, 72, 500), (2050, 40, 700), (2300, 264, 900)])
+def test_rows_off_lines(T, K, V, monkeypatch):
+    x, W, t, g = _inputs(T, K, V, T)
+    _check(x, W, t, "mean", 0.0, g)
+    monkeypatch.setenv("MGG_VOCAB_PIECE", "320")
+    _check(x, W, t, "none", 0.0, g)
+    wide = torch.zeros(T, K + 8, dtype=BF, device=DEV)
+    wide[:, 8:] = x
+    _check(wide[:, 8:], W, t, "sum", 0.0, g)
 
 
 @pytest.mark.parametrize("scale", [0.0, 40.0, 1000.0])

@@ -479,8 +479,8 @@ size_t mgg_workspace_bytes(mgg_op op, int T, int k, int E, int N, int K, mgg_dty
       if (T < 1 || E < 1 || E > kMaxExperts || k < 1 || T % k != 0) return 0;
       return balance_ws_bytes(T, E, k);
     case MGG_OP_VOCAB_FORWARD:
-      if (T < 1 || N < 1) return 0;
-      return vocab_fwd_ws_bytes(T, N);
+      if (T < 1 || N < 1 || K < 1) return 0;
+      return vocab_fwd_ws_bytes(T, K, N);
     case MGG_OP_VOCAB_BACKWARD:
       if (T < 1 || N < 1 || K < 1) return 0;
       return vocab_bwd_ws_bytes(T, K, N);

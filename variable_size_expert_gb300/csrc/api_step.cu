@@ -59,7 +59,8 @@ mgg_status mgg_balance_loss(const void* logits, mgg_dtype dtype, int64_t ldl,
   if (!aligned(logits, size_of(dtype)) || !aligned(expert_ids, 4)) return MGG_ERR_ALIGNMENT;
   s = check_arch();
   if (s != MGG_OK) return s;
-  if (!ws || !aligned(ws, 256) || ws_bytes < balance_ws_bytes(T, E, sequences)) return MGG_ERR_WORKSPACE;
+  const size_t need = balance_ws_bytes(T, E, sequences);
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return MGG_ERR_WORKSPACE;
   BalanceArgs a{};
   a.logits = logits, a.f32 = dtype == MGG_F32, a.ldl = ldl, a.ids = expert_ids, a.mask = mask;
   a.T = T, a.E = E, a.k = k, a.sequences = sequences, a.softmax = scoring == MGG_SCORE_SOFTMAX;
@@ -108,7 +109,7 @@ mgg_status mgg_linear_cross_entropy(const void* x, int64_t ldx, const void* W, c
   }
   s = check_arch();
   if (s != MGG_OK) return s;
-  if (T > 0 && (!ws || !aligned(ws, 256) || ws_bytes < vocab_fwd_ws_bytes(T, V))) return MGG_ERR_WORKSPACE;
+  if (T > 0 && (!ws || !aligned(ws, 256) || ws_bytes < vocab_fwd_ws_bytes(T, K, V))) return MGG_ERR_WORKSPACE;
   VocabForward a{};
   a.x = x, a.ldx = ldx, a.W = W, a.targets = targets, a.i64 = targets_i64 != 0, a.ignore = ignore_index;
   a.T = T, a.K = K, a.V = V, a.reduction = reduction, a.z_loss = z_loss;

@@ -477,6 +477,7 @@ constexpr int kJoinBlocks = 1024;  // at most
 
 size_t balance_ws_bytes(int T, int E, int sequences) {
   const size_t blocks = static_cast<size_t>(sequences) * plan_chunks(T, E, sequences);
+  if (blocks == 1) return 0;
   return 2 * round256(blocks * E * 4) + round256(blocks * 4) + round256(kJoinBlocks * 4) + 256;
 }
 

@@ -397,12 +397,14 @@ PyObject* balance_loss_forward(PyObject* const* a) {
   const mgg_dtype lc = code(l.scalar_type());
   Tensor loss = empty({}, at::kFloat, l), counts = empty({runs, r.cols}, at::kInt, l),
          slope = empty({runs, r.cols}, at::kFloat, l);
-  Tensor ws = room(a[6], mgg_workspace_bytes(MGG_OP_BALANCE, r.rows, runs, r.cols, 0, 0, lc), l);
+  const size_t need = mgg_workspace_bytes(MGG_OP_BALANCE, r.rows, runs, r.cols, 0, 0, lc);
+  Tensor ws;
+  if (need) ws = room(a[6], need, l);
   check(mgg_balance_loss(r.ptr, lc, r.ld, static_cast<const int32_t*>(ip), mp, r.rows, r.cols, k, runs,
                          static_cast<mgg_scoring>(integer(a[2], "scoring")),
                          static_cast<float*>(loss.data_ptr()), static_cast<int32_t*>(counts.data_ptr()),
-                         static_cast<float*>(slope.data_ptr()), status_word(a[5]), ws.data_ptr(), ws.nbytes(),
-                         stream(l)),
+                         static_cast<float*>(slope.data_ptr()), status_word(a[5]), need ? ws.data_ptr() : nullptr,
+                         need ? ws.nbytes() : 0, stream(l)),
         "mgg_balance_loss");
   return tuple({loss, counts, slope});
 }

@@ -292,7 +292,7 @@ struct VocabBackward {
   int32_t* dev_status;
   long long wait_limit;
 };
-size_t vocab_fwd_ws_bytes(int T, int V);
+size_t vocab_fwd_ws_bytes(int T, int K, int V);
 size_t vocab_bwd_ws_bytes(int T, int K, int V);
 cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t st);
 cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t st);

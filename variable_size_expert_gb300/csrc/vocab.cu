@@ -23,6 +23,8 @@
 //             tokens there are no many roundings for one token's to vanish among
 //             (one token: dW off by up to 2^-8 in its target's row, now by the
 //             rounding of the result alone).
+#include <stdlib.h>
+
 #include "pair.cuh"
 
 namespace mgg {
@@ -643,17 +645,42 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 // Tokens up to which d is kept in two parts.
 constexpr int kSplitTokens = 128;
 
-// [x; x], rows dense: the other operand of d's two parts in dW.
-__global__ void __launch_bounds__(256) vocab_twice_kernel(const uint4* x, long long ldx, int T, int K8, uint4* out) {
+// Rows whose pitch is no multiple of 64 bytes cost: an operand's 128-byte rows then
+// lie across three or more 64-byte pieces of the L2, whose way to the SMs is what the
+// pair kernel is closest to (loss of 8192 x 2040 x 32768 758 us, with x copied to rows
+// on 128-byte boundaries 594; gradients 2117, with both copied 1790).  x is copied
+// where there are enough tokens to gain from it, a piece of W where its copy (134 MB
+// take 40 us) is a few percent of the products.
+constexpr int kCopyTokens = 256, kCopyWTokens = 2048;
+bool off_lines(const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % 64 || ld % 32; }
+int line_ld(int K) { return (K + 63) / 64 * 64; }
+
+// rows x K8 16-byte pieces, `ld` apart, to rows `out_ld` apart; `copies` of all, one
+// behind the other ([x; x] is the other operand of d's two parts in dW).
+__global__ void __launch_bounds__(256) vocab_copy_kernel(const uint4* x, long long ld, int rows, int K8,
+                                                         int out_ld, int copies, uint4* out) {
   pdl_trigger();
   pdl_wait();
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < T * K8; i += gridDim.x * 256) {
-    const int t = i / K8, k = i - t * K8;
-    const uint4 v = x[t * ldx + k];
-    out[i] = v;
-    out[T * K8 + i] = v;
+  const long long n = static_cast<long long>(rows) * K8, step = static_cast<long long>(gridDim.x) * 256;
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+    const long long t = i / K8;
+    const int k = static_cast<int>(i - t * K8);
+    const uint4 v = x[t * ld + k];
+    for (int c = 0; c < copies; ++c) out[(c * rows + t) * out_ld + k] = v;
   }
 }
+// o's rows to `to`, on 128-byte boundaries
+cudaError_t copy_rows(DenseOperand* o, void* to, int copies, cudaStream_t st) {
+  const int ld = line_ld(o->cols);
+  const long long n = static_cast<long long>(o->rows) * (o->cols / 8);
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((n + 255) / 256, 16 * num_sms()));
+  const cudaError_t e = launch_pdl(vocab_copy_kernel, dim3(blocks), dim3(256), 0, st,
+                                   static_cast<const uint4*>(o->ptr), o->ld / 8, o->rows, o->cols / 8, ld / 8,
+                                   copies, static_cast<uint4*>(to));
+  *o = DenseOperand{to, o->rows, o->cols, ld};
+  return e;
+}
+
 // dx = the sum of its parts, [parts][T K]
 __global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, int parts, long long n4,
                                                             uint2* dx) {
@@ -669,20 +696,23 @@ __global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, i
   }
 }
 
-// Columns of a piece of the backward: d takes rows x that many bfloat16 values.
+// Columns of a piece of the backward: as many as give d 256 MB (4096 x 2048 x 32768 in
+// pieces of 64 MB 1031 us, 128 1013, 256 987), at least 2048; MGG_VOCAB_PIECE sets it.
 int piece_columns(int T, int V) {
-  const long long most = 64LL << 20;  // bytes of d
+  const long long most = 256LL << 20;
   const int rows = T <= kSplitTokens ? 2 * T : T;
-  const long long cols = std::max<long long>(2048, most / (2LL * rows) / 256 * 256);
+  long long cols = std::max<long long>(2048, most / (2LL * rows) / 256 * 256);
+  if (const char* s = getenv("MGG_VOCAB_PIECE"))
+    if (const long long n = atoll(s); n > 0) cols = (std::min(n, 1LL << 30) + 63) / 64 * 64;
   return static_cast<int>(std::min<long long>(cols, (V + 7) / 8 * 8));
 }
 // What the backward keeps: d; f32 sums of dx (over pieces, of its slices and parts);
-// [x; x].
+// x or [x; x]; a piece of W.
 struct BackLayout {
   int cols;
-  bool split;
-  int slices;                // of dx's contraction in a piece
-  size_t sum, twice, total;  // offsets of the second and third
+  bool split, copy_w;
+  int slices;              // of dx's contraction in a piece
+  size_t sum, x, w, total; // offsets of the second and on
 };
 BackLayout back_layout(int T, int K, int V) {
   BackLayout l;
@@ -698,17 +728,20 @@ BackLayout back_layout(int T, int K, int V) {
   l.slices = static_cast<int>(std::min<long long>(32, (blocks + most - 1) / most));
   const size_t sums = static_cast<size_t>(rows) * l.slices;
   l.sum = round256(static_cast<size_t>(rows) * l.cols * 2);
-  l.twice = l.sum + (l.split || l.slices > 1 || l.cols < V ? round256(sums * K * 4) : 0);
-  l.total = l.twice + (l.split ? round256(static_cast<size_t>(rows) * K * 2) : 0);
+  l.copy_w = T >= kCopyWTokens && K % 32;
+  l.x = l.sum + (l.split || l.slices > 1 || l.cols < V ? round256(sums * K * 4) : 0);
+  l.w = l.x + (l.split || T >= kCopyTokens ? round256(static_cast<size_t>(rows) * line_ld(K) * 2) : 0);
+  l.total = l.w + (l.copy_w ? round256(static_cast<size_t>(l.cols) * line_ld(K) * 2) : 0);
   return l;
 }
 
 }  // namespace
 
-// forward: the tiles' pairs, the targets' logits, the joining blocks' sums, their ticket
-size_t vocab_fwd_ws_bytes(int T, int V) {
+// forward: the tiles' pairs, the targets' logits, the joining blocks' sums, their ticket, x
+size_t vocab_fwd_ws_bytes(int T, int K, int V) {
   return round256(static_cast<size_t>(cdiv(V, tile_columns(T))) * T * 8) + round256(static_cast<size_t>(T) * 4) +
-         round256(static_cast<size_t>(cdiv(T, 32)) * 8) + 256;
+         round256(static_cast<size_t>(cdiv(T, 32)) * 8) + 256 +
+         (T >= kCopyTokens ? round256(static_cast<size_t>(T) * line_ld(K) * 2) : 0);
 }
 size_t vocab_bwd_ws_bytes(int T, int K, int V) { return back_layout(T, K, V).total; }
 
@@ -733,7 +766,10 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t s
   j.blocks = reinterpret_cast<float2*>(take(static_cast<size_t>(cdiv(a.T, 32)) * 8));
   p.ticket = reinterpret_cast<int*>(take(4));
   p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
-  cudaError_t e = launch_tiles<false>(DenseOperand{a.x, a.T, a.K, a.ldx}, DenseOperand{a.W, a.V, a.K, a.K}, p, st);
+  DenseOperand x{a.x, a.T, a.K, a.ldx};
+  cudaError_t e = cudaSuccess;
+  if (a.T >= kCopyTokens && off_lines(a.x, a.ldx)) e = copy_rows(&x, at, 1, st);
+  if (e == cudaSuccess) e = launch_tiles<false>(x, DenseOperand{a.W, a.V, a.K, a.K}, p, st);
   if (e != cudaSuccess) return e;
   j.part = p.part, j.tiles = tn, j.T = a.T, j.vocab = a.V, j.target_z = p.target_z;
   j.targets = a.targets, j.i64 = a.i64, j.ignore = a.ignore, j.zc = a.z_loss, j.reduction = a.reduction;
@@ -748,17 +784,13 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
   __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(base);
   float* sum = reinterpret_cast<float*>(base + l.sum);
   const int rows = l.split ? 2 * a.T : a.T;
-  const DenseOperand x{a.x, a.T, a.K, a.ldx};
-  DenseOperand xd = x;  // beside d's rows
+  DenseOperand x{a.x, a.T, a.K, a.ldx};
   const float* const scale = a.per_token ? nullptr : a.dloss;
   cudaError_t e = cudaSuccess;
-  if (l.split && a.dW) {
-    void* twice = base + l.twice;
-    const int K8 = a.K / 8;
-    e = launch_pdl(vocab_twice_kernel, dim3(cdiv(a.T * K8, 256)), dim3(256), 0, st,
-                   static_cast<const uint4*>(a.x), a.ldx / 8, a.T, K8, static_cast<uint4*>(twice));
-    xd = DenseOperand{twice, rows, a.K, a.K};
-  }
+  if ((l.split && a.dW) || (a.T >= kCopyTokens && off_lines(a.x, a.ldx)))
+    e = copy_rows(&x, base + l.x, l.split ? 2 : 1, st);
+  DenseOperand xd = x;  // beside d's rows
+  xd.rows = rows;
   for (int v0 = 0; e == cudaSuccess && v0 < a.V; v0 += l.cols) {
     const int n = std::min(l.cols, a.V - v0);
     const char* W = static_cast<const char*>(a.W) + static_cast<size_t>(v0) * a.K * 2;
@@ -768,8 +800,10 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     p.lse = a.lse, p.z2 = 2.f * a.z_loss, p.gtok = a.per_token ? a.dloss : nullptr, p.weight = a.weight;
     p.d = d, p.ldd = l.cols, p.split = l.split;
     p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
-    const DenseOperand Wp{W, n, a.K, a.K}, dp{d, rows, n, l.cols};
-    e = launch_tiles<true>(x, Wp, p, st);
+    DenseOperand Wp{W, n, a.K, a.K};
+    const DenseOperand dp{d, rows, n, l.cols};
+    if (l.copy_w) e = copy_rows(&Wp, base + l.w, 1, st);
+    if (e == cudaSuccess) e = launch_tiles<true>(x, Wp, p, st);
     if (e != cudaSuccess) return e;
     const bool parts = l.split || l.slices > 1;
     const bool first = v0 == 0, direct = v0 + n == a.V && !parts;  // dx in place
