@@ -260,7 +260,7 @@ __device__ __forceinline__ float put_moments(const Entry& e, long long i, uint32
 }
 
 // ---------------------------------------------------------------- the step
-// One instruction each, within 2 ulp; second moments below 1e-38 count as 0.
+// One instruction each, within 2 ulp; a second moment below 1e-38 counts as 0 here.
 __device__ __forceinline__ float root(float v) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -270,6 +270,13 @@ __device__ __forceinline__ float inverse(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
+}
+// a + b, each rounded by itself.  (add2 of two products is contracted to fma2.)
+__device__ __forceinline__ F2 sum2(F2 a, F2 b) {
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
 }
 struct Rates {
   float b1, c1, b2, c2, eps, keep, rate, root, gs;
@@ -309,20 +316,27 @@ struct Held {
     const long long i = at + (WIDE ? 8 * lane : lane), n = e.n;
     if constexpr (WIDE && sizeof(G) == 2) bf16s(gc, g);
     if constexpr (BITS8) {
-      decode8(mc, ms * r.b1, m);  // b1 m
+      decode8(mc, ms, m);
       decode8(vc, vs, v);
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       const F2 x = mul2(pack2(g[j], g[j + 1]), both(r.gs));
-      F2 mm = pack2(m[j], m[j + 1]), vv = pack2(v[j], v[j + 1]);
-      if constexpr (!BITS8) mm = mul2(mm, both(r.b1));
-      mm = fma2(x, both(r.c1), mm);
-      if constexpr (BITS8) vv = mul2(vv, vv);
-      vv = fma2(mul2(x, x), both(r.c2), mul2(vv, both(r.b2)));
-      float v0, v1, d0, d1, p0, p1;
-      unpack2(vv, v0, v1);
-      const float r0 = root(v0), r1 = root(v1);
+      F2 mm = mul2(pack2(m[j], m[j + 1]), both(r.b1)), vv = pack2(v[j], v[j + 1]);
+      float v0, v1, r0, r1, d0, d1, p0, p1;
+      if constexpr (BITS8) {
+        // each operation rounded by itself, as the formula is written: the codes are
+        // then the same wherever they are computed in f32
+        mm = sum2(mm, mul2(x, both(r.c1)));
+        vv = sum2(mul2(mul2(vv, vv), both(r.b2)), mul2(mul2(x, x), both(r.c2)));
+        unpack2(vv, v0, v1);
+        r0 = __fsqrt_rn(v0), r1 = __fsqrt_rn(v1);
+      } else {
+        mm = fma2(x, both(r.c1), mm);
+        vv = fma2(mul2(x, x), both(r.c2), mul2(vv, both(r.b2)));
+        unpack2(vv, v0, v1);
+        r0 = root(v0), r1 = root(v1);
+      }
       unpack2(fma2(pack2(r0, r1), both(r.root), both(r.eps)), d0, d1);
       const F2 u = mul2(mm, pack2(inverse(d0), inverse(d1)));
       unpack2(fma2(both(-r.rate), u, mul2(pack2(p[j], p[j + 1]), both(r.keep))), p0, p1);
