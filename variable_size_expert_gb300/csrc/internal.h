@@ -181,7 +181,8 @@ struct DenseProduct {
   bool out_vec;     // rows of out start on 16-byte boundaries (set by the launcher)
   bool epilogue;    // bias, activation, residual, z kept
   int slices;       // pieces of the contraction, each with an f32 output [M, N] of its own,
-                    // one behind the other (0: one)
+                    // one behind the other (0: one; more only with `pairs`)
+  bool pairs;       // on CTA pairs, whatever the estimate
   int tiles;        // set by the launcher
 };
 struct DenseParams {

@@ -1083,10 +1083,13 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
   }
   p.pre_vec = p.pre && vec_rows(p.pre, p.pr[0].N, false);
   const int pairs = std::min(dense_pair_count(), total);
-  auto blocks = [&](int q) { return q < n ? cdiv(cdiv(p.pr[q].Kc, BK), p.pr[q].slices) : 0; };
-  p.longer = blocks(1) > blocks(0);
+  // a tile's time in blocks of the contraction: its own and storing it (see use_pairs)
+  auto cost = [&](int q) {
+    return q < n ? std::max(cdiv(cdiv(p.pr[q].Kc, BK), p.pr[q].slices) + 4, 9) : 0;
+  };
+  p.longer = cost(1) > cost(0);
   p.deal_pairs = p.pr[p.longer].tiles % pairs;
-  p.deal = n > 1 && p.deal_pairs ? (2 * blocks(p.longer) + blocks(1 - p.longer)) / (2 * blocks(1 - p.longer)) : 0;
+  p.deal = n > 1 && p.deal_pairs ? (2 * cost(p.longer) + cost(1 - p.longer)) / (2 * cost(1 - p.longer)) : 0;
   p.res_tma = p.residual && p.res_vec && p.pr[0].out_f32;
   if (p.res_tma && !encode_tmap_residual(&maps.res, p.residual, p.res_f32, p.pr[0].slices * p.pr[0].M, p.pr[0].N, p.ldr))
     return cudaErrorInvalidValue;
@@ -1295,7 +1298,7 @@ cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, 
     if (!pr[i].out) continue;
     p.pr[n] = pr[i];
     const CtaPlan plan = plan_cta(pr[i]);
-    if (pr[i].slices > 1 || use_pairs(pr[i], plan)) {
+    if (pr[i].pairs || use_pairs(pr[i], plan)) {
       pa[n] = a[i], pb[n] = b[i];
       ++n;
       continue;

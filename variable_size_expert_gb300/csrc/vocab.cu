@@ -308,14 +308,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 64 tokens the weights' bytes are the bound: tiles of 128 rows of W by N
-// tokens (16..64), W's rows on the rows of the accumulator, two blocks an SM with a
-// ring each, so that 190 KB an SM are in flight.  (Pair tiles, whose 256 token rows
-// are mostly empty, take 42 us for 16 x 2048 x 32768.)  A lane then holds a vocabulary
-// entry, not a token: the forward turns the tile through shared memory and reduces a
-// token with a warp, the backward stores d as it lies.  Runs of the contraction have
-// an accumulator each and meet in f32 (see kRunBlocks).
-constexpr int kFewTokens = 64, kFewThreads = 192, kFewSlots = 6;
+// Up to 32 tokens the weights' bytes are the bound: tiles of 128 rows of W by N
+// tokens (16 or 32), W's rows on the rows of the accumulator, two blocks an SM with a
+// ring each, so that 190 KB an SM are in flight.  (On pair tiles every SM asks for
+// the same few rows of x at once: the loss of 16 x 2048 x 32768 40 us, here 30; of 64
+// tokens 32 there, 34 here.)  A lane then holds a vocabulary entry, not a token: the
+// forward turns the tile through shared memory and reduces a token with a warp, the
+// backward stores d as it lies.  Runs of the contraction have an accumulator each
+// and meet in f32 (see kRunBlocks).
+constexpr int kFewTokens = 32, kFewThreads = 192, kFewSlots = 6;
 constexpr int kFewMeta = 256;
 struct FewParams {
   int N;          // tokens, rounded up to 16
@@ -688,6 +689,7 @@ __global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, i
   pdl_wait();
   for (long long i = blockIdx.x * 256 + threadIdx.x; i < n4; i += gridDim.x * 256) {
     float4 a = sum[i];
+#pragma unroll 8
     for (int k = 1; k < parts; ++k) {
       const float4 b = sum[k * n4 + i];
       a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
@@ -723,7 +725,7 @@ BackLayout back_layout(int T, int K, int V) {
   // no tile takes longer than half of what a pair has to do (1111 x 1160 over 50257:
   // 25 tiles, 240 us on single-CTA tiles)
   const long long blocks = cdiv(l.cols, BK), tk = cdiv(K, 256);
-  const long long work = cdiv(rows, 256) * tk * blocks + cdiv(l.cols, 256) * tk * (cdiv(rows, BK) + 4);
+  const long long work = cdiv(rows, 256) * tk * (blocks + 4) + cdiv(l.cols, 256) * tk * std::max(cdiv(rows, BK) + 4, 9);
   const long long most = std::max<long long>(16, work / (num_sms() / 2) / 2);
   l.slices = static_cast<int>(std::min<long long>(32, (blocks + most - 1) / most));
   const size_t sums = static_cast<size_t>(rows) * l.slices;
@@ -816,7 +818,10 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     dx.out = !a.dx ? nullptr : direct ? a.dx : sum;
     dx.out_f32 = !direct, dx.epilogue = !first;
     dx.slices = std::min(l.slices, cdiv(n, BK));  // (a last piece may be narrow)
+    dx.pairs = dx.slices > 1;
     dW.M = n, dW.N = a.K, dW.Kc = rows, dW.a_mn = dW.b_mn = true;
+    // (beside dx's slices; of 32 rows alone 59 us on single-CTA tiles, 34 on pairs)
+    dW.pairs = dx.pairs;
     dW.out = a.dW ? static_cast<char*>(a.dW) + static_cast<size_t>(v0) * a.K * 2 : nullptr;
     if (!first) {
       q.residual = sum;
