@@ -726,7 +726,7 @@ BackLayout back_layout(int T, int K, int V) {
   // 25 tiles, 240 us on single-CTA tiles)
   const long long blocks = cdiv(l.cols, BK), tk = cdiv(K, 256);
   const long long work = cdiv(rows, 256) * tk * (blocks + 4) + cdiv(l.cols, 256) * tk * std::max(cdiv(rows, BK) + 4, 9);
-  const long long most = std::max<long long>(16, work / (num_sms() / 2) / 2);
+  const long long most = std::max<long long>(16, work / std::max(1, num_sms() / 2) / 2);
   l.slices = static_cast<int>(std::min<long long>(32, (blocks + most - 1) / most));
   const size_t sums = static_cast<size_t>(rows) * l.slices;
   l.sum = round256(static_cast<size_t>(rows) * l.cols * 2);
