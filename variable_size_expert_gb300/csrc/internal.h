@@ -163,7 +163,8 @@ struct MaskedParams {
 };
 
 // Activations of the dense products (the values of mgg_activation; the last one,
-// for the library's own calls, multiplies every product by *scale0 * *scale1).
+// for the library's own calls on CTA pairs, multiplies every product by *scale0 *
+// *scale1).
 enum DenseAct { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActScale = 4 };
 
 // A bf16 operand [rows][cols], row stride ld elements.
@@ -180,9 +181,6 @@ struct DenseProduct {
   bool out_f32;     // else bf16
   bool out_vec;     // rows of out start on 16-byte boundaries (set by the launcher)
   bool epilogue;    // bias, activation, residual, z kept
-  int slices;       // pieces of the contraction, each with an f32 output [M, N] of its own,
-                    // one behind the other (0: one; more only with `pairs`)
-  bool pairs;       // on CTA pairs, whatever the estimate
   int tiles;        // set by the launcher
 };
 struct DenseParams {
@@ -196,8 +194,6 @@ struct DenseParams {
   long long ldr;
   void* pre;             // bf16 z [M, N] or null
   bool pre_vec;          // rows on 16-byte boundaries (set by the launcher)
-  const float *scale0, *scale1;  // of kActScale
-  int longer, deal_pairs, deal;  // the tiles' order, set by the launcher
   int32_t* dev_status;
   long long wait_limit;
 };
@@ -256,8 +252,15 @@ cudaError_t launch_select_bwd(const float* g, const void* logits, bool f32, long
 size_t dense_bwd_ws_bytes(int T, int N);
 cudaError_t launch_dense_forward(const DenseParams& p, const DenseOperand& x,
                                  const DenseOperand& W, cudaStream_t st);
-cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, const DenseOperand* a,
-                                  const DenseOperand* b, cudaStream_t st);
+// What the library's own products on CTA pairs can have beside.
+struct PairOptions {
+  bool always;                   // on pairs, whatever the estimate says
+  int slices[2];                 // pieces of a product's contraction, each with an f32 output
+                                 // [M, N] of its own, one behind the other (0: one)
+  const float *scale0, *scale1;  // of kActScale
+};
+cudaError_t launch_dense_products(const DenseParams& q, const PairOptions& opt, const DenseProduct* pr,
+                                  const DenseOperand* a, const DenseOperand* b, cudaStream_t st);
 cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t st);
 
 int dense_pair_count();  // co-resident clusters of two (persistent grid)

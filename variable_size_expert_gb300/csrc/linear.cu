@@ -125,9 +125,6 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
   else if (act == kActGelu) act_n<kActGelu>(v);
 }
 
-// The factor of every product (kActScale): two words, as a loss's gradient and
-// its tokens' weight come.
-__device__ __forceinline__ float factor(const DenseParams& p) { return *p.scale0 * *p.scale1; }
 template <int N>
 __device__ __forceinline__ void scale_all(float scale, float (&v)[N]) {
 #pragma unroll
@@ -226,25 +223,31 @@ struct PairMaps {
   CUtensorMap a[2], b[2], res;
 };
 
+// The tiles' order and the options of a launch of the pair kernel.
+struct PairExtra {
+  int slices[2];
+  int longer, deal_pairs, deal;  // see tile_of
+  const float *scale0, *scale1;  // of kActScale
+};
 struct PTile {
   int q;           // product
   int m0, n0;      // first row and column
   int slice;       // of the contraction
   int kb0, nkb;    // its blocks
 };
-__device__ __forceinline__ PTile decode_pair(const DenseParams& p, int tau) {
+__device__ __forceinline__ PTile decode_pair(const DenseParams& p, const PairExtra& x, int tau) {
   PTile t;
   t.q = tau >= p.pr[0].tiles ? 1 : 0;
   const DenseProduct& d = p.pr[t.q];
   int local = tau - (t.q ? p.pr[0].tiles : 0);
-  const int blocks = cdiv(d.Kc, BK);
+  const int blocks = cdiv(d.Kc, BK), slices = x.slices[t.q];
   t.slice = 0, t.kb0 = 0, t.nkb = blocks;
-  if (d.slices > 1) {
-    const int per = d.tiles / d.slices;
+  if (slices > 1) {
+    const int per = d.tiles / slices;
     t.slice = local / per;
     local -= t.slice * per;
-    t.kb0 = static_cast<int>(static_cast<long long>(t.slice) * blocks / d.slices);
-    t.nkb = static_cast<int>(static_cast<long long>(t.slice + 1) * blocks / d.slices) - t.kb0;
+    t.kb0 = static_cast<int>(static_cast<long long>(t.slice) * blocks / slices);
+    t.nkb = static_cast<int>(static_cast<long long>(t.slice + 1) * blocks / slices) - t.kb0;
   }
   band_tile(local, d.M, d.N, t.m0, t.n0);
   return t;
@@ -255,21 +258,20 @@ __device__ __forceinline__ PTile decode_pair(const DenseParams& p, int tau) {
 // about as long as that one, before those are dealt out in turn too.  (Dealt out by
 // their number alone, 128 tiles of 128 blocks and 256 of 64 gave four pairs 512
 // blocks of 431 on average; so none has more than 448.)
-__device__ __forceinline__ int tile_of(const DenseParams& p, int pair, int npairs, int i) {
-  const int f = p.longer, head = p.pr[f].tiles, tail = p.pr[1 - f].tiles;
-  const int base0 = f ? p.pr[0].tiles : 0, base1 = f ? 0 : p.pr[0].tiles;
-  const int mine = pair < head ? (head - 1 - pair) / npairs + 1 : 0;
-  if (i < mine) return base0 + pair + i * npairs;
-  i -= mine;
-  const int few = npairs - p.deal_pairs;  // pairs with one fewer
-  int t;
-  if (pair >= p.deal_pairs && i < p.deal) {
-    t = i * few + pair - p.deal_pairs;
+__device__ __forceinline__ int tile_of(const DenseParams& p, const PairExtra& x, int pair, int npairs, int i) {
+  const int f = x.longer, head = p.pr[f].tiles, tail = p.pr[1 - f].tiles;
+  int t = pair + i * npairs;
+  if (t < head) return f ? p.pr[0].tiles + t : t;
+  if (tail == 0) return -1;
+  i -= pair < head ? (head - 1 - pair) / npairs + 1 : 0;
+  const int few = npairs - x.deal_pairs;  // pairs with one fewer
+  if (pair >= x.deal_pairs && i < x.deal) {
+    t = i * few + pair - x.deal_pairs;
   } else {
-    if (pair >= p.deal_pairs) i -= p.deal;
-    t = p.deal * few + i * npairs + pair;
+    if (pair >= x.deal_pairs) i -= x.deal;
+    t = x.deal * few + i * npairs + pair;
   }
-  return t < tail ? base1 + t : -1;
+  return t < tail ? (f ? t : p.pr[0].tiles + t) : -1;
 }
 
 // ACT is a template argument and the column loop is not unrolled: with the
@@ -277,7 +279,8 @@ __device__ __forceinline__ int tile_of(const DenseParams& p, int pair, int npair
 // outgrew the instruction cache, which the lone producer and MMA threads share.
 template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ DenseParams p) {
+    dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ DenseParams p,
+                      const __grid_constant__ PairExtra x) {
   extern __shared__ uint8_t smem_raw[];
   const PSmem m = carve_pair(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -310,8 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ TMA
     Ring r{0, 0, 0};
     bool ok = true;
-    for (int i = 0, tau; ok && (tau = tile_of(p, pair, npairs, i)) >= 0; ++i) {
-      const PTile t = decode_pair(p, tau);
+    for (int i = 0, tau; ok && (tau = tile_of(p, x, pair, npairs, i)) >= 0; ++i) {
+      const PTile t = decode_pair(p, x, tau);
       const DenseProduct& d = p.pr[t.q];
       const int ar = t.m0 + static_cast<int>(rank) * kHalf;
       const int br = t.n0 + static_cast<int>(rank) * kHalf;
@@ -332,20 +335,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int tcount = 0;
       Ring r{0, 0, 0};
       bool ok = true;
-      for (int i = 0, tau; ok && (tau = tile_of(p, pair, npairs, i)) >= 0; ++i) {
-        const PTile t = decode_pair(p, tau);
-        const DenseProduct& d = p.pr[t.q];
+      for (int i = 0, tau; ok && (tau = tile_of(p, x, pair, npairs, i)) >= 0; ++i) {
+        // (of the tile only its product and length: this warp is what tiles wait for)
+        const int q = tau >= p.pr[0].tiles;
+        const DenseProduct& d = p.pr[q];
+        const int nkb = x.slices[q] > 1 ? decode_pair(p, x, tau).nkb : cdiv(d.Kc, BK);
         const int acc = tcount & 1;
         if (!__all_sync(0xffffffffu, wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)))
           break;
         tc_fence_after();
         const uint32_t dt = tmem_base + acc * 256;
         if (d.a_mn)
-          ok = multiply<true, true>(m, dt, t.nkb, r, wc);
+          ok = multiply<true, true>(m, dt, nkb, r, wc);
         else if (d.b_mn)
-          ok = multiply<false, true>(m, dt, t.nkb, r, wc);
+          ok = multiply<false, true>(m, dt, nkb, r, wc);
         else
-          ok = multiply<false, false>(m, dt, t.nkb, r, wc);
+          ok = multiply<false, false>(m, dt, nkb, r, wc);
         if (!ok) break;
         if (elect_one()) tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
         ++tcount;
@@ -370,9 +375,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int row_w = static_cast<int>(rank) * kHalf + quad * 32;
     int tcount = 0, res_n = 0;
     bool res_open = false;  // a residual block is on its way
-    const float scale = ACT == kActScale ? factor(p) : 1.f;
-    for (int i = 0, tau; (tau = tile_of(p, pair, npairs, i)) >= 0; ++i) {
-      const PTile t = decode_pair(p, tau);
+    const float scale = ACT == kActScale ? *x.scale0 * *x.scale1 : 1.f;
+    for (int i = 0, tau; (tau = tile_of(p, x, pair, npairs, i)) >= 0; ++i) {
+      const PTile t = decode_pair(p, x, tau);
       const DenseProduct& d = p.pr[t.q];
       const int row0 = t.m0 + row_w;
       const int acc = tcount & 1;
@@ -551,7 +556,6 @@ __device__ __forceinline__ void finish16(const CtaParams& c, const DenseParams& 
   const DenseProduct& d = c.d;
   const long long o = static_cast<long long>(col0) * d.N + row;
   const int nv = end - col0;
-  if (p.act == kActScale) scale_all<16>(factor(p), v);
   auto store = [&](void* out, bool f32) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -834,7 +838,6 @@ __global__ void __launch_bounds__(kCtaThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[16 * k + i] = h[i];
       }
-      if (p.act == kActScale) scale_all<32>(factor(p), v);
       if (d.epilogue && p.bias) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // (past BN: columns that are not stored)
@@ -1053,17 +1056,19 @@ int dense_pair_count() {  // (one block per SM, whatever the activation)
 namespace {
 
 template <int ACT>
-cudaError_t launch_pairs_act(const PairMaps& maps, const DenseParams& p, int total,
+cudaError_t launch_pairs_act(const PairMaps& maps, const DenseParams& p, const PairExtra& x, int total,
                              cudaStream_t st) {
   static bool done[64] = {};
   cudaError_t e = allow_smem(dense_pair_kernel<ACT>, kPairSmem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(dense_pair_kernel<ACT>, dim3(2 * std::min(dense_pair_count(), total)),
-                    dim3(kPairThreads), kPairSmem, st, maps, p);
+                    dim3(kPairThreads), kPairSmem, st, maps, p, x);
 }
 
-cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperand* b, int n,
-                         cudaStream_t st) {
+cudaError_t launch_pairs(DenseParams p, const PairOptions& opt, const DenseOperand* a, const DenseOperand* b,
+                         int n, cudaStream_t st) {
+  PairExtra x{};
+  x.scale0 = opt.scale0, x.scale1 = opt.scale1;
   PairMaps maps;
   memset(&maps, 0, sizeof(maps));
   int total = 0;
@@ -1073,8 +1078,8 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
       d.tiles = 0;
       continue;
     }
-    d.slices = std::max(1, d.slices);
-    d.tiles = cdiv(d.M, 256) * cdiv(d.N, 256) * d.slices;
+    x.slices[q] = std::max(1, opt.slices[q]);
+    d.tiles = cdiv(d.M, 256) * cdiv(d.N, 256) * x.slices[q];
     total += d.tiles;
     d.out_vec = vec_rows(d.out, d.N, d.out_f32);
     if (!tmap_operand(&maps.a[q], a[q], d.a_mn, kHalf) ||
@@ -1085,19 +1090,19 @@ cudaError_t launch_pairs(DenseParams p, const DenseOperand* a, const DenseOperan
   const int pairs = std::min(dense_pair_count(), total);
   // a tile's time in blocks of the contraction: its own and storing it (see use_pairs)
   auto cost = [&](int q) {
-    return q < n ? std::max(cdiv(cdiv(p.pr[q].Kc, BK), p.pr[q].slices) + 4, 9) : 0;
+    return q < n ? std::max(cdiv(cdiv(p.pr[q].Kc, BK), x.slices[q]) + 4, 9) : 0;
   };
-  p.longer = cost(1) > cost(0);
-  p.deal_pairs = p.pr[p.longer].tiles % pairs;
-  p.deal = n > 1 && p.deal_pairs ? (2 * cost(p.longer) + cost(1 - p.longer)) / (2 * cost(1 - p.longer)) : 0;
+  x.longer = cost(1) > cost(0);
+  x.deal_pairs = p.pr[x.longer].tiles % pairs;
+  x.deal = n > 1 && x.deal_pairs ? (2 * cost(x.longer) + cost(1 - x.longer)) / (2 * cost(1 - x.longer)) : 0;
   p.res_tma = p.residual && p.res_vec && p.pr[0].out_f32;
-  if (p.res_tma && !encode_tmap_residual(&maps.res, p.residual, p.res_f32, p.pr[0].slices * p.pr[0].M, p.pr[0].N, p.ldr))
+  if (p.res_tma && !encode_tmap_residual(&maps.res, p.residual, p.res_f32, x.slices[0] * p.pr[0].M, p.pr[0].N, p.ldr))
     return cudaErrorInvalidValue;
-  if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, total, st);
-  if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, total, st);
-  if (p.act == kActGelu) return launch_pairs_act<kActGelu>(maps, p, total, st);
-  if (p.act == kActScale) return launch_pairs_act<kActScale>(maps, p, total, st);
-  return launch_pairs_act<kActNone>(maps, p, total, st);
+  if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, x, total, st);
+  if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, x, total, st);
+  if (p.act == kActGelu) return launch_pairs_act<kActGelu>(maps, p, x, total, st);
+  if (p.act == kActScale) return launch_pairs_act<kActScale>(maps, p, x, total, st);
+  return launch_pairs_act<kActNone>(maps, p, x, total, st);
 }
 
 // The kernel for a product, by estimated time in us, fitted to sweeps of 16 to
@@ -1283,22 +1288,24 @@ size_t dense_bwd_ws_bytes(int T, int N) {
 cudaError_t launch_dense_forward(const DenseParams& p, const DenseOperand& x,
                                  const DenseOperand& W, cudaStream_t st) {
   const CtaPlan plan = plan_cta(p.pr[0]);
-  return use_pairs(p.pr[0], plan) ? launch_pairs(p, &x, &W, 1, st)
+  return use_pairs(p.pr[0], plan) ? launch_pairs(p, PairOptions{}, &x, &W, 1, st)
                                   : launch_cta(p, 0, plan, x, W, st);
 }
 
 // Up to two products (those with an output): one launch where both take 256 x
 // 256 tiles.  The epilogue's operands in p are the first one's.
-cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, const DenseOperand* a,
-                                  const DenseOperand* b, cudaStream_t st) {
+cudaError_t launch_dense_products(const DenseParams& q, const PairOptions& opt, const DenseProduct* pr,
+                                  const DenseOperand* a, const DenseOperand* b, cudaStream_t st) {
   DenseParams p = q;
+  PairOptions o = opt;
   DenseOperand pa[2], pb[2];
   int n = 0;
   for (int i = 0; i < 2; ++i) {
     if (!pr[i].out) continue;
     p.pr[n] = pr[i];
-    const CtaPlan plan = plan_cta(pr[i]);
-    if (pr[i].pairs || use_pairs(pr[i], plan)) {
+    o.slices[n] = opt.slices[i];
+    const CtaPlan plan = opt.always ? CtaPlan{} : plan_cta(pr[i]);
+    if (opt.always || use_pairs(pr[i], plan)) {
       pa[n] = a[i], pb[n] = b[i];
       ++n;
       continue;
@@ -1306,7 +1313,7 @@ cudaError_t launch_dense_products(const DenseParams& q, const DenseProduct* pr, 
     const cudaError_t e = launch_cta(p, n, plan, a[i], b[i], st);
     if (e != cudaSuccess) return e;
   }
-  return n ? launch_pairs(p, pa, pb, n, st) : cudaSuccess;
+  return n ? launch_pairs(p, o, pa, pb, n, st) : cudaSuccess;
 }
 
 // Up to four launches: dz, then dx and dW (one launch where both take 256 x
@@ -1348,7 +1355,7 @@ cudaError_t launch_dense_backward(const DenseBackward& a, void* ws, cudaStream_t
   dW.M = a.N, dW.N = a.K, dW.Kc = a.T, dW.a_mn = dW.b_mn = true, dW.out = a.dW;
   const DenseProduct pr[2] = {dx, dW};
   const DenseOperand oa[2] = {z, z}, ob[2] = {W, x};
-  if (e == cudaSuccess) e = launch_dense_products(p, pr, oa, ob, st);
+  if (e == cudaSuccess) e = launch_dense_products(p, PairOptions{}, pr, oa, ob, st);
   if (e == cudaSuccess && part_out)
     e = launch_column_sums(part, parts, a.N, a.db, nullptr, a.db_f32, st);
   return e;

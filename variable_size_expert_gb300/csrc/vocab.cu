@@ -811,17 +811,15 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     const bool first = v0 == 0, direct = v0 + n == a.V && !parts;  // dx in place
     // every product is multiplied by the loss's gradient as it leaves
     DenseParams q{};
-    q.scale0 = scale, q.scale1 = a.weight;
     q.dev_status = a.dev_status, q.wait_limit = a.wait_limit;
     DenseProduct dx{}, dW{};
     dx.M = rows, dx.N = a.K, dx.Kc = n, dx.b_mn = true;
     dx.out = !a.dx ? nullptr : direct ? a.dx : sum;
     dx.out_f32 = !direct, dx.epilogue = !first;
-    dx.slices = std::min(l.slices, cdiv(n, BK));  // (a last piece may be narrow)
-    dx.pairs = dx.slices > 1;
     dW.M = n, dW.N = a.K, dW.Kc = rows, dW.a_mn = dW.b_mn = true;
-    // (beside dx's slices; of 32 rows alone 59 us on single-CTA tiles, 34 on pairs)
-    dW.pairs = dx.pairs;
+    // (on pairs in any case, which know a factor of the product; of 32 rows dW takes 59
+    // us on single-CTA tiles, 34 on pairs)
+    const PairOptions opt{true, {std::min(l.slices, cdiv(n, BK)), 1}, scale, a.weight};  // (a last piece may be narrow)
     dW.out = a.dW ? static_cast<char*>(a.dW) + static_cast<size_t>(v0) * a.K * 2 : nullptr;
     if (!first) {
       q.residual = sum;
@@ -831,7 +829,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     q.act = scale ? kActScale : kActNone;
     const DenseOperand oa[2] = {dp, dp}, ob[2] = {Wp, xd};
     const DenseProduct pr[2] = {dx, dW};
-    e = launch_dense_products(q, pr, oa, ob, st);
+    e = launch_dense_products(q, opt, pr, oa, ob, st);
   }
   if (e == cudaSuccess && (l.split || l.slices > 1) && a.dx) {
     const long long n4 = static_cast<long long>(a.T) * a.K / 4;
