@@ -23,6 +23,10 @@
 //             tokens there are no many roundings for one token's to vanish among
 //             (one token: dW off by up to 2^-8 in its target's row, now by the
 //             rounding of the result alone).
+//
+// Bound by the matrix units at the power limit: loss of 8192 x 2048 x 32768 632 us
+// (1740 TFLOP/s), gradients of 4096 x 2048 x 32768 974 us (1690); with few tokens by
+// the weights' bytes.
 #include <stdlib.h>
 
 #include "pair.cuh"
@@ -229,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (!ok) break;
           const uint32_t taddr = taddr0 + (tcount & 1) * 256;
           // (sixteen columns at a time: 64 sums and 32 more do not fit a thread's 96
-          // registers, and spilled ones cost 876 us instead of 6xx)
+          // registers, and with spilled ones 8192 x 2048 x 32768 takes 876 us, not 632)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float x[16];
@@ -310,9 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------- few tokens
 // Up to 32 tokens the weights' bytes are the bound: tiles of 128 rows of W by N
 // tokens (16 or 32), W's rows on the rows of the accumulator, two blocks an SM with a
-// ring each, so that 190 KB an SM are in flight.  (On pair tiles every SM asks for
-// the same few rows of x at once: the loss of 16 x 2048 x 32768 40 us, here 30; of 64
-// tokens 32 there, 34 here.)  A lane then holds a vocabulary entry, not a token: the
+// ring each, so that 190 KB an SM are in flight: the loss of 16 x 2048 x 32768 29 us
+// (134 MB, 68% of the measured copy rate; start, last epilogue and the joining kernel
+// are 9 of it).  On pair tiles every SM asks for the same few rows of x at once, 40
+// us (of 64 tokens 32 there, 34 here); one block an SM that walks over the tiles with
+// two accumulators 31.6.  A lane then holds a vocabulary entry, not a token: the
 // forward turns the tile through shared memory and reduces a token with a warp, the
 // backward stores d as it lies.  Runs of the contraction have an accumulator each
 // and meet in f32 (see kRunBlocks).
@@ -514,7 +520,11 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinPara
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int t = blockIdx.x * 32 + lane;
+  // (the token that this warp finishes: its target is on its way meanwhile)
+  const int own = blockIdx.x * 32 + warp;
+  const int y = own < p.T ? target_of(p.targets, p.i64, p.ignore, p.vocab, own) : -1;
+  const float z = y >= 0 ? p.target_z[own] : 0.f;
+  const int t = blockIdx.x * 32 + lane;
   float c = -INFINITY, s = 0.f;
   if (t < p.T) {
     for (int i = warp; i < p.tiles; i += 4 * kJoinWarps) {
@@ -530,7 +540,6 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinPara
   sh[warp][lane] = make_float2(c, s);
   __syncthreads();
   // warp w: the block's token w
-  t = blockIdx.x * 32 + warp;
   const float2 q = sh[lane][warp];
   c = q.x, s = q.y;
 #pragma unroll
@@ -538,32 +547,44 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinPara
     join(c, s, __shfl_xor_sync(0xffffffffu, c, o), __shfl_xor_sync(0xffffffffu, s, o));
   if (lane == 0) {
     float loss = 0.f, n = 0.f;
-    if (t < p.T) {
+    if (own < p.T) {
       const float lse = kLn2 * (c + log2f(s));
-      p.lse[t] = lse;
-      const int y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
+      p.lse[own] = lse;
       if (y >= 0) {
-        loss = lse - p.target_z[t] + p.zc * lse * lse;
+        loss = lse - z + p.zc * lse * lse;
         n = 1.f;
       } else if (y == -2) {
         atomicOr(p.dev_status, kDevBadTarget);
       }
-      if (p.reduction == MGG_REDUCE_NONE) p.losses[t] = loss;
+      if (p.reduction == MGG_REDUCE_NONE) p.losses[own] = loss;
     }
     each[warp] = make_float2(loss, n);
   }
   __syncthreads();
-  if (warp == 0) {
-    float2 e = each[lane];
+  auto over_warps = [&](float2 e) {
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
       e.x += __shfl_xor_sync(0xffffffffu, e.x, o);
       e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
     }
+    return e;
+  };
+  auto finish = [&](float2 e) {
+    const float w = p.reduction == MGG_REDUCE_MEAN ? 1.f / fmaxf(e.y, 1.f) : 1.f;
+    if (p.reduction != MGG_REDUCE_NONE) *p.total = e.x * w;
+    *p.weight = w;
+  };
+  if (warp == 0) {
+    const float2 e = over_warps(each[lane]);
     if (lane == 0) {
-      p.blocks[blockIdx.x] = e;
-      __threadfence();
-      last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+      last = false;
+      if (gridDim.x == 1) {
+        finish(e);
+      } else {
+        p.blocks[blockIdx.x] = e;
+        __threadfence();
+        last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+      }
     }
   }
   __syncthreads();
@@ -574,25 +595,12 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_join_kernel(const JoinPara
     const float2 b = __ldcg(p.blocks + i);
     e.x += b.x, e.y += b.y;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) {
-    e.x += __shfl_xor_sync(0xffffffffu, e.x, o);
-    e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
-  }
+  e = over_warps(e);
   if (lane == 0) each[warp] = e;
   __syncthreads();
   if (warp == 0) {
-    e = each[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-      e.x += __shfl_xor_sync(0xffffffffu, e.x, o);
-      e.y += __shfl_xor_sync(0xffffffffu, e.y, o);
-    }
-    if (lane == 0) {
-      const float w = p.reduction == MGG_REDUCE_MEAN ? 1.f / fmaxf(e.y, 1.f) : 1.f;
-      if (p.reduction != MGG_REDUCE_NONE) *p.total = e.x * w;
-      *p.weight = w;
-    }
+    e = over_warps(each[lane]);
+    if (lane == 0) finish(e);
   }
 }
 
@@ -615,7 +623,7 @@ cudaError_t launch_few(const DenseOperand& x, const DenseOperand& W, const Vocab
   // half of an SM's shared memory and tensor memory
   f.slots = std::min({kFewSlots, (112 * 1024 - 1024 - kFewMeta) / (OPER + f.N * 128), nkb});
   f.run = std::max(BACK ? nkb : cdiv(nkb, 256 / f.N), 1);
-  if (!BACK) f.run = std::max(f.run, std::min(nkb, 4));
+  if (!BACK) f.run = std::max(f.run, std::min(nkb, kRunBlocks));
   f.runs = cdiv(nkb, f.run);
   f.tmem_cols = 32;
   while (f.tmem_cols < f.runs * f.N) f.tmem_cols *= 2;
