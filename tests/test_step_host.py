@@ -219,6 +219,14 @@ def test_autograd_of_the_losses(monkeypatch):
             (g.square().sum() + x.pow(3).sum()).backward()
 
 
+def test_adamw_state_of_any_iterable():
+    ps = [torch.zeros(3, 5), torch.zeros(300), torch.zeros(0)]
+    for bits, blocks in ((32, None), (8, [1, 2, 0])):
+        m, v, ms, vs = mgg.adamw_state(iter(ps), bits)
+        assert [x.shape for x in m] == [x.shape for x in v] == [x.shape for x in ps]
+        assert ms is None and vs is None if blocks is None else [len(x) for x in ms] == [len(x) for x in vs] == blocks
+
+
 def test_adamw_class_keeps_its_own_count(monkeypatch):
     calls = []
     monkeypatch.setattr(step, "adamw_step", lambda *a: calls.append(a))

@@ -144,6 +144,7 @@ def adamw_state(params, bits: int = 32):
     scale for each 256 elements, else float32 and None for the scales."""
     if bits not in (8, 32):
         raise ValueError("bits must be 8 or 32")
+    params = list(params)
     dtype = torch.float32 if bits == 32 else torch.float8_e4m3fn
     m, v = ([torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(dtype) if bits == 8
              else torch.zeros(p.shape, dtype=dtype, device=p.device) for p in params] for _ in range(2))
