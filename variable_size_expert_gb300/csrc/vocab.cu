@@ -38,10 +38,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The matrix units cut every sum they add to off: over 2048 terms a logit loses 1.3e-5
 // of 6 or so, always towards zero, and a loss, which averages many, keeps that (1.6e-6
-// of it, ten times the error of f32 sums).  The forward therefore has them add up eight
-// blocks (512 terms) at a time and adds those sums in f32, in the registers of the
-// epilogue, under the next eight blocks' products.  (For d a logit need not be as good.)
-constexpr int kRunBlocks = 8;
+// of it, ten times the error of f32 sums).  The forward therefore has them add up a
+// run of blocks at a time and adds those sums in f32, in the registers of the epilogue,
+// under the next run's products.  Runs of eight blocks (512 terms) leave 3e-7 to 5e-7
+// of a mean over many tokens; of 8192 x 2048 x 32768 they take 636 us, of four 670, of
+// two 754.  With up to 256 tokens, where W's bytes are the bound and few tokens average
+// less away, four (two with up to 32) cost nothing.  (For d a logit need not be as good.)
+constexpr int kRunBlocks = 8, kRunFew = 4, kRunFewest = 2;
 
 struct VocabMaps {
   CUtensorMap a, b;
@@ -56,6 +59,7 @@ struct VocabParams {
   float2* part;         // [tiles along V][T]: (c, sum)
   float* target_z;      // [T]
   int* ticket;          // zeroed for the joining kernel
+  int run;              // see kRunBlocks
   // backward
   const float* lse;
   float z2;             // 2 c
@@ -113,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
   const int total = cdiv(p.T, 256) * cdiv(p.V, 256), nkb = cdiv(p.K, BK);
   // blocks of the contraction that one accumulator adds up
-  const int kRun = BACK ? nkb : kRunBlocks;
+  const int run = BACK ? nkb : p.run;
   const uint32_t full_l = mapa_shared(m.full, 0);
   const uint32_t acc_empty_l = mapa_shared(m.acc_empty, 0);
   if (!BACK && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
@@ -137,12 +141,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       Ring r{0, 0, 0};
       bool ok = true;
       for (int tau = pair; ok && tau < total; tau += npairs) {
-        for (int kb = 0; ok && kb < nkb; kb += kRun, ++tcount) {
+        for (int kb = 0; ok && kb < nkb; kb += run, ++tcount) {
           const int acc = tcount & 1;
           ok = __all_sync(0xffffffffu, wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc));
           if (!ok) break;
           tc_fence_after();
-          ok = multiply<false, false>(m, tmem_base + acc * 256, min(kRun, nkb - kb), r, wc);
+          ok = multiply<false, false>(m, tmem_base + acc * 256, min(run, nkb - kb), r, wc);
           if (ok && elect_one()) tc_commit_cg2_mc(m.acc_full + 8 * acc, 0x3);
         }
       }
@@ -228,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       } else {
         float v[64];
         bool ok = true;
-        for (int kb = 0; ok && kb < nkb; kb += kRun) {
+        for (int kb = 0; ok && kb < nkb; kb += run) {
           ok = arrived();
           if (!ok) break;
           const uint32_t taddr = taddr0 + (tcount & 1) * 256;
@@ -622,8 +626,7 @@ cudaError_t launch_few(const DenseOperand& x, const DenseOperand& W, const Vocab
   const int nkb = cdiv(p.K, BK);
   // half of an SM's shared memory and tensor memory
   f.slots = std::min({kFewSlots, (112 * 1024 - 1024 - kFewMeta) / (OPER + f.N * 128), nkb});
-  f.run = std::max(BACK ? nkb : cdiv(nkb, 256 / f.N), 1);
-  if (!BACK) f.run = std::max(f.run, std::min(nkb, kRunBlocks));
+  f.run = BACK ? nkb : std::max(cdiv(nkb, 256 / f.N), p.run);
   f.runs = cdiv(nkb, f.run);
   f.tmem_cols = 32;
   while (f.tmem_cols < f.runs * f.N) f.tmem_cols *= 2;
@@ -775,6 +778,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t s
   JoinParams j{};
   j.blocks = reinterpret_cast<float2*>(take(static_cast<size_t>(cdiv(a.T, 32)) * 8));
   p.ticket = reinterpret_cast<int*>(take(4));
+  p.run = a.T <= kFewTokens ? kRunFewest : a.T <= 256 ? kRunFew : kRunBlocks;
   p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
   DenseOperand x{a.x, a.T, a.K, a.ldx};
   cudaError_t e = cudaSuccess;
