@@ -235,12 +235,13 @@ struct PTile {
   int slice;       // of the contraction
   int kb0, nkb;    // its blocks
 };
+template <bool EXTRA>
 __device__ __forceinline__ PTile decode_pair(const DenseParams& p, const PairExtra& x, int tau) {
   PTile t;
-  t.q = tau >= p.pr[0].tiles ? 1 : 0;
+  t.q = EXTRA && tau >= p.pr[0].tiles ? 1 : 0;
   const DenseProduct& d = p.pr[t.q];
   int local = tau - (t.q ? p.pr[0].tiles : 0);
-  const int blocks = cdiv(d.Kc, BK), slices = x.slices[t.q];
+  const int blocks = cdiv(d.Kc, BK), slices = EXTRA ? x.slices[t.q] : 1;
   t.slice = 0, t.kb0 = 0, t.nkb = blocks;
   if (slices > 1) {
     const int per = d.tiles / slices;
@@ -277,7 +278,9 @@ __device__ __forceinline__ int tile_of(const DenseParams& p, const PairExtra& x,
 // ACT is a template argument and the column loop is not unrolled: with the
 // activations as runtime branches of an unrolled loop the epilogue's code
 // outgrew the instruction cache, which the lone producer and MMA threads share.
-template <int ACT>
+// EXTRA: two products, slices or a factor; a single product's tiles go by their number
+// (the order by length costs 4% where a tile is two blocks, 8192 x 128 x 8192).
+template <int ACT, bool EXTRA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     dense_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ DenseParams p,
                       const __grid_constant__ PairExtra x) {
@@ -306,6 +309,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_wait();
   pdl_trigger();
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
+  const int total = p.pr[0].tiles;
+  // the i-th tile of this pair after `tau`
+  auto next = [&](int i, int& tau) {
+    if constexpr (EXTRA) {
+      tau = tile_of(p, x, pair, npairs, i);
+      return tau >= 0;
+    } else {
+      tau = i ? tau + npairs : pair;
+      return tau < total;
+    }
+  };
   const uint32_t full_l = mapa_shared(m.full, 0);
   const uint32_t acc_empty_l = mapa_shared(m.acc_empty, 0);
 
@@ -313,8 +327,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ TMA
     Ring r{0, 0, 0};
     bool ok = true;
-    for (int i = 0, tau; ok && (tau = tile_of(p, x, pair, npairs, i)) >= 0; ++i) {
-      const PTile t = decode_pair(p, x, tau);
+    for (int i = 0, tau = 0; ok && next(i, tau); ++i) {
+      const PTile t = decode_pair<EXTRA>(p, x, tau);
       const DenseProduct& d = p.pr[t.q];
       const int ar = t.m0 + static_cast<int>(rank) * kHalf;
       const int br = t.n0 + static_cast<int>(rank) * kHalf;
@@ -335,11 +349,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int tcount = 0;
       Ring r{0, 0, 0};
       bool ok = true;
-      for (int i = 0, tau; ok && (tau = tile_of(p, x, pair, npairs, i)) >= 0; ++i) {
+      for (int i = 0, tau = 0; ok && next(i, tau); ++i) {
         // (of the tile only its product and length: this warp is what tiles wait for)
-        const int q = tau >= p.pr[0].tiles;
+        const int q = EXTRA && tau >= p.pr[0].tiles ? 1 : 0;
         const DenseProduct& d = p.pr[q];
-        const int nkb = x.slices[q] > 1 ? decode_pair(p, x, tau).nkb : cdiv(d.Kc, BK);
+        const int nkb = EXTRA && x.slices[q] > 1 ? decode_pair<EXTRA>(p, x, tau).nkb : cdiv(d.Kc, BK);
         const int acc = tcount & 1;
         if (!__all_sync(0xffffffffu, wait_bar(m.acc_empty + 8 * acc, ((tcount >> 1) & 1) ^ 1, wc)))
           break;
@@ -376,8 +390,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int tcount = 0, res_n = 0;
     bool res_open = false;  // a residual block is on its way
     const float scale = ACT == kActScale ? *x.scale0 * *x.scale1 : 1.f;
-    for (int i = 0, tau; (tau = tile_of(p, x, pair, npairs, i)) >= 0; ++i) {
-      const PTile t = decode_pair(p, x, tau);
+    for (int i = 0, tau = 0; next(i, tau); ++i) {
+      const PTile t = decode_pair<EXTRA>(p, x, tau);
       const DenseProduct& d = p.pr[t.q];
       const int row0 = t.m0 + row_w;
       const int acc = tcount & 1;
@@ -1046,7 +1060,7 @@ int dense_pair_count() {  // (one block per SM, whatever the activation)
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<kActNone>, &cfg) != cudaSuccess || n < 1)
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<kActNone, false>, &cfg) != cudaSuccess || n < 1)
     n = num_sms() / 2;
   n = std::min(n, num_sms() / 2);
   if (dev < 64) cache[dev] = n;
@@ -1055,13 +1069,13 @@ int dense_pair_count() {  // (one block per SM, whatever the activation)
 
 namespace {
 
-template <int ACT>
+template <int ACT, bool EXTRA>
 cudaError_t launch_pairs_act(const PairMaps& maps, const DenseParams& p, const PairExtra& x, int total,
                              cudaStream_t st) {
   static bool done[64] = {};
-  cudaError_t e = allow_smem(dense_pair_kernel<ACT>, kPairSmem, done);
+  cudaError_t e = allow_smem(dense_pair_kernel<ACT, EXTRA>, kPairSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(dense_pair_kernel<ACT>, dim3(2 * std::min(dense_pair_count(), total)),
+  return launch_pdl(dense_pair_kernel<ACT, EXTRA>, dim3(2 * std::min(dense_pair_count(), total)),
                     dim3(kPairThreads), kPairSmem, st, maps, p, x);
 }
 
@@ -1098,11 +1112,15 @@ cudaError_t launch_pairs(DenseParams p, const PairOptions& opt, const DenseOpera
   p.res_tma = p.residual && p.res_vec && p.pr[0].out_f32;
   if (p.res_tma && !encode_tmap_residual(&maps.res, p.residual, p.res_f32, x.slices[0] * p.pr[0].M, p.pr[0].N, p.ldr))
     return cudaErrorInvalidValue;
-  if (p.act == kActRelu) return launch_pairs_act<kActRelu>(maps, p, x, total, st);
-  if (p.act == kActSilu) return launch_pairs_act<kActSilu>(maps, p, x, total, st);
-  if (p.act == kActGelu) return launch_pairs_act<kActGelu>(maps, p, x, total, st);
-  if (p.act == kActScale) return launch_pairs_act<kActScale>(maps, p, x, total, st);
-  return launch_pairs_act<kActNone>(maps, p, x, total, st);
+  if (p.act == kActScale) return launch_pairs_act<kActScale, true>(maps, p, x, total, st);
+  if (n > 1 || x.slices[0] > 1) {  // (gradients: no activation)
+    if (p.act != kActNone) return cudaErrorInvalidValue;
+    return launch_pairs_act<kActNone, true>(maps, p, x, total, st);
+  }
+  if (p.act == kActRelu) return launch_pairs_act<kActRelu, false>(maps, p, x, total, st);
+  if (p.act == kActSilu) return launch_pairs_act<kActSilu, false>(maps, p, x, total, st);
+  if (p.act == kActGelu) return launch_pairs_act<kActGelu, false>(maps, p, x, total, st);
+  return launch_pairs_act<kActNone, false>(maps, p, x, total, st);
 }
 
 // The kernel for a product, by estimated time in us, fitted to sweeps of 16 to
