@@ -136,6 +136,17 @@ def test_what_is_not_finite_stays_where_it_is():
             assert torch.isfinite(s.float()[~odd]).all() and not torch.isfinite(s.float()[odd]).any()
 
 
+def test_a_state_that_is_not_a_number_stays_one():
+    """A code of NaN in either moment, as a step on a NaN gradient left it."""
+    for at in (2, 3):
+        case = _case([512], F, F, False, 8, 7)
+        case[at][0].view(torch.uint8)[300] = 0x7F
+        mgg.adamw_step(case[0], case[1], case[2], case[3], 4, **OPT, exp_avg_scale=case[4], exp_avg_sq_scale=case[5])
+        for s in (case[0][0], case[at][0]):
+            odd = ~torch.isfinite(s.float())
+            assert odd[300] and int(odd.sum()) == 1
+
+
 def test_second_moment_of_eight_bits_never_vanishes():
     """A gradient far below its block's largest: sqrt(v) stays a code above zero,
     so that its element does not leap."""

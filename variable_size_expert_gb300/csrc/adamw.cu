@@ -156,25 +156,34 @@ __device__ __forceinline__ void decode8(uint2 w, float scale, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; j += 2) unpack2(mul2(pack2(v[j], v[j + 1]), both(scale)), v[j], v[j + 1]);
 }
-// The largest magnitude of the block, as bits; odd: some value is not finite, and
-// the largest is that of the others (an element that is not finite becomes NaN and
-// leaves its neighbours alone).  SIGNED: the values may be negative.
-template <bool SIGNED>
-__device__ __forceinline__ uint32_t largest(const float (&v)[8], bool& odd) {
-  auto bits = [](float x) { return __float_as_uint(SIGNED ? fabsf(x) : x); };
+// The largest magnitudes of a block's moments m and r (its root, not negative).  odd:
+// a value is not finite, and the largest are those of the others (an element that is
+// not finite becomes NaN and leaves its neighbours alone); of m its sum tells.
+__device__ __forceinline__ bool largest(const float (&m)[8], const float (&r)[8], float& tm, float& tr) {
   uint32_t top = 0;
+  tm = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, bits(v[j]));
+  for (int j = 0; j < 8; ++j) {
+    top = max(top, __float_as_uint(r[j]));  // (as whole numbers, which keep NaN)
+    tm = fmaxf(tm, fabsf(m[j]));
+  }
+  float s0, s1;
+  unpack2(add2(add2(pack2(m[0], m[1]), pack2(m[2], m[3])), add2(pack2(m[4], m[5]), pack2(m[6], m[7]))), s0, s1);
+  if (!isfinite(s0 + s1)) top = 0xffffffffu;
   top = __reduce_max_sync(0xffffffffu, top);
-  odd = top >= 0x7f800000u;  // (the same in every lane)
+  const bool odd = top >= 0x7f800000u;  // (the same in every lane)
   if (odd) {
-    top = 0;
+    top = 0, tm = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (bits(v[j]) < 0x7f800000u) top = max(top, bits(v[j]));
+    for (int j = 0; j < 8; ++j) {
+      if (__float_as_uint(r[j]) < 0x7f800000u) top = max(top, __float_as_uint(r[j]));
+      if (isfinite(m[j])) tm = fmaxf(tm, fabsf(m[j]));
+    }
     top = __reduce_max_sync(0xffffffffu, top);
   }
-  return top;
+  tr = __uint_as_float(top);
+  tm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(tm)));
+  return odd;
 }
 // v's codes: |v| / scale as the bits of a number with four exponent and three
 // mantissa bits (times 2^-120, so that e4m3's denormals are float's), 20 bits below
@@ -187,8 +196,10 @@ __device__ __forceinline__ uint2 codes(float inv, float tiny, bool odd, const ui
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     float y0, y1;
-    if (ONE) {
-      unpack2(mul2(pack2(fabsf(v[j]), fabsf(v[j + 1])), both(tiny)), y0, y1);
+    if (ONE && ROOT) {
+      unpack2(mul2(pack2(v[j], v[j + 1]), both(tiny)), y0, y1);
+    } else if (ONE) {
+      y0 = fabsf(v[j]) * tiny, y1 = fabsf(v[j + 1]) * tiny;
     } else {
       y0 = (fabsf(v[j]) * inv) * 0x1p-120f, y1 = (fabsf(v[j + 1]) * inv) * 0x1p-120f;
     }
@@ -245,8 +256,8 @@ __device__ __forceinline__ void put_codes(void* base, long long i, long long n, 
 template <bool WIDE>
 __device__ __forceinline__ float put_moments(const Entry& e, long long i, uint32_t walk, const float (&m)[8],
                                              const float (&r)[8]) {
-  bool odd_m, odd_r;
-  const float tm = __uint_as_float(largest<true>(m, odd_m)), tr = __uint_as_float(largest<false>(r, odd_r));
+  float tm, tr;
+  const bool odd = largest(m, r, tm, tr);
   const int lane = threadIdx.x & 31;
   const float t = lane & 1 ? tr : tm;
   const float q = __fdiv_rn(lane & 2 ? 448.f : t, lane & 2 ? t : 448.f);
@@ -257,10 +268,10 @@ __device__ __forceinline__ float put_moments(const Entry& e, long long i, uint32
   uint32_t w[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] = (walk + static_cast<uint32_t>(WIDE ? j : 32 * j) * kWalkI) >> 12;
-  put_codes<WIDE, false>(e.m, i, e.n, im, odd_m, w, m);
+  put_codes<WIDE, false>(e.m, i, e.n, im, odd, w, m);
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] ^= kSaltV >> 12;
-  put_codes<WIDE, true>(e.v, i, e.n, ir, odd_r, w, r);
+  put_codes<WIDE, true>(e.v, i, e.n, ir, odd, w, r);
   return q;
 }
 
