@@ -253,18 +253,18 @@ __device__ __forceinline__ PTile decode_pair(const DenseParams& p, const PairExt
   band_tile(local, d.M, d.N, t.m0, t.n0);
   return t;
 }
-// The i-th tile of a pair, -1 after its last.  The tiles of the product with the
-// longer contraction are dealt out one after the other; the pairs left with one
-// fewer of them (from p.deal_pairs on) then take p.deal tiles of the other product,
-// about as long as that one, before those are dealt out in turn too.  (Dealt out by
-// their number alone, 128 tiles of 128 blocks and 256 of 64 gave four pairs 512
+// The i-th tile of a pair, -1 after its last; `mine` of them are of the product with
+// the longer contraction.  Its tiles are dealt out one after the other; the pairs left
+// with one fewer of them (from x.deal_pairs on) then take x.deal tiles of the other
+// product, about as long as that one, before those are dealt out in turn too.  (Dealt
+// out by their number alone, 128 tiles of 128 blocks and 256 of 64 gave four pairs 512
 // blocks of 431 on average; so none has more than 448.)
-__device__ __forceinline__ int tile_of(const DenseParams& p, const PairExtra& x, int pair, int npairs, int i) {
-  const int f = x.longer, head = p.pr[f].tiles, tail = p.pr[1 - f].tiles;
-  int t = pair + i * npairs;
-  if (t < head) return f ? p.pr[0].tiles + t : t;
-  if (tail == 0) return -1;
-  i -= pair < head ? (head - 1 - pair) / npairs + 1 : 0;
+__device__ __forceinline__ int tile_of(const DenseParams& p, const PairExtra& x, int pair, int npairs, int mine,
+                                       int i) {
+  const int f = x.longer, tail = p.pr[1 - f].tiles;
+  if (i < mine) return (f ? p.pr[0].tiles : 0) + pair + i * npairs;
+  i -= mine;
+  int t;
   const int few = npairs - x.deal_pairs;  // pairs with one fewer
   if (pair >= x.deal_pairs && i < x.deal) {
     t = i * few + pair - x.deal_pairs;
@@ -310,10 +310,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_trigger();
   const WaitCtl wc{m.abort_flag, p.dev_status, p.wait_limit};
   const int total = p.pr[0].tiles;
+  // this pair's tiles of the product with the longer contraction
+  const int head = EXTRA ? p.pr[x.longer].tiles : 0;
+  const int mine = pair < head ? (head - 1 - pair) / npairs + 1 : 0;
   // the i-th tile of this pair after `tau`
   auto next = [&](int i, int& tau) {
     if constexpr (EXTRA) {
-      tau = tile_of(p, x, pair, npairs, i);
+      tau = tile_of(p, x, pair, npairs, mine, i);
       return tau >= 0;
     } else {
       tau = i ? tau + npairs : pair;
