@@ -86,6 +86,26 @@ def test_pieces(T, K, V, piece, reduction, monkeypatch):
     _check(x, W, t, reduction, 1e-4, g)
 
 
+# up to 4 tokens the gradients leave one kernel: columns that do not fill its blocks,
+# rows that do not fill its chunks, several chunks a block; 5 tokens, the first beyond
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("K,V,reduction", [(1032, 17, "none"), (8, 20000, "mean"), (264, 1999, "sum"),
+                                           (2056, 16384, "mean")])
+def test_very_few_tokens(T, K, V, reduction, monkeypatch):
+    monkeypatch.setenv("MGG_VOCAB_PIECE", "640")
+    x, W, t, g = _inputs(T, K, V, T + K, ignored=0.1)
+    wide = torch.full((T, K + 16), math.nan, dtype=BF, device=DEV)
+    wide[:, 8:-8] = x
+    loss, lse, dx, dW = _check(wide[:, 8:-8], W, t, reduction, 1e-3, g)
+    if reduction != "none":
+        w = 1 / max(int((t >= 0).sum()), 1) if reduction == "mean" else 1.0
+        args = (torch.tensor(1.7, device=DEV), x, W, t, lse, torch.tensor(w, device=DEV))
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV).fill_(0xFF)
+        ax, none = mgg.linear_cross_entropy_backward(*args, z_loss=1e-3, need_dW=False, workspace=ws)
+        none2, aW = mgg.linear_cross_entropy_backward(*args, z_loss=1e-3, need_dx=False, workspace=ws)
+        assert none is None and none2 is None and torch.equal(dx, ax) and torch.equal(dW, aW)
+
+
 def test_pieces_of_the_default_size():
     x, W, t, g = _inputs(70000, 8, 2049, 1)
     _check(x, W, t, "mean", 0.0, g)

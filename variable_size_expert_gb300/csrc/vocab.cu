@@ -68,6 +68,7 @@ struct VocabParams {
   __nv_bfloat16* d;     // [T][ldd], 16-byte rows
   int ldd;
   bool split;           // d in two parts, rows t and T + t
+  float* df;            // or d in f32, [T][ldd] (few tokens)
   int32_t* dev_status;
   long long wait_limit;
 };
@@ -449,7 +450,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           float d = exp2_f(fmaf(v[i], kLog2e, -lse * kLog2e)) * ((1.f + p.z2 * lse) * g);
           if (y == p.v0 + row) d -= g;
           if (y < 0) d = 0.f;
-          if (row < p.V) {
+          if (row < p.V && p.df) {
+            p.df[static_cast<long long>(t) * p.ldd + row] = d;
+          } else if (row < p.V) {
             const __nv_bfloat16 hi = __float2bfloat16_rn(d);
             p.d[static_cast<long long>(t) * p.ldd + row] = hi;
             if (p.split)
@@ -693,20 +696,212 @@ cudaError_t copy_rows(DenseOperand* o, void* to, int copies, cudaStream_t st) {
   return e;
 }
 
-// dx = the sum of its parts, [parts][T K]
+// dx = scale (the sum of its parts, [parts][T K]).  Eight groups of threads share the
+// parts of 32 x 4 values, so that many parts are not as many latencies.
 __global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, int parts, long long n4,
-                                                            uint2* dx) {
+                                                            const float* scale0, const float* scale1, uint2* dx) {
+  __shared__ float4 sh[8][32];
   pdl_trigger();
   pdl_wait();
-  for (long long i = blockIdx.x * 256 + threadIdx.x; i < n4; i += gridDim.x * 256) {
-    float4 a = sum[i];
+  const float g = scale0 ? *scale0 * *scale1 : 1.f;
+  const int group = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = min(8, parts);
+  // (the same number of rounds in every thread of the block)
+  for (long long base = static_cast<long long>(blockIdx.x) * 32; base < n4; base += static_cast<long long>(gridDim.x) * 32) {
+    const long long i = base + lane;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n4) {
 #pragma unroll 8
-    for (int k = 1; k < parts; ++k) {
-      const float4 b = sum[k * n4 + i];
-      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+      for (int k = group; k < parts; k += 8) {
+        const float4 b = sum[k * n4 + i];
+        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+      }
     }
-    dx[i] = make_uint2(cvt_bf16x2(a.x, a.y), cvt_bf16x2(a.z, a.w));
+    sh[group][lane] = a;
+    __syncthreads();
+    if (group == 0 && i < n4) {
+      for (int k = 1; k < groups; ++k) {
+        const float4 b = sh[k][lane];
+        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+      }
+      dx[i] = make_uint2(cvt_bf16x2(a.x * g, a.y * g), cvt_bf16x2(a.z * g, a.w * g));
+    }
+    __syncthreads();
   }
+}
+cudaError_t join_dx(const float* sum, int parts, int T, int K, const float* scale0, const float* scale1, void* dx,
+                    cudaStream_t st) {
+  const long long n4 = static_cast<long long>(T) * K / 4;
+  return launch_pdl(vocab_join_dx_kernel, dim3(static_cast<unsigned>(std::min<long long>((n4 + 31) / 32, 64 * num_sms()))),
+                    dim3(256), 0, st, reinterpret_cast<const float4*>(sum), parts, n4, scale0, scale1,
+                    static_cast<uint2*>(dx));
+}
+
+// ---------------------------------------------------------------- both gradients of very few tokens
+// Up to 4 tokens dx and dW are sums of a few products an element, bound by W read and
+// dW written once: no tensor cores, d in f32.  A thread holds eight columns of every
+// token's x and of its sum of dx, and walks down rows of W: each is read, added to dx
+// with d's column, and leaves as dW's.  Its rows wait in a ring of its own in shared
+// memory (only the thread that copied them reads them: no barrier), 16 under way.  The
+// blocks take chunks of rows from W's end, which d's kernel has read last and L2 still
+// holds, and write dW past it.  The blocks' sums of dx meet afterwards.  d, dx and dW of
+// 1, 2 and 4 x 2048 x 32768 take 75, 76 and 78 us (on pair tiles, of one contraction
+// block each, 97 to 99; with four loads under way a thread 112 to 121), of 2 x 4096 x
+// 131072 513 (627), of 2 x 64 x 512 7.1 (10.3).  From 8 tokens their products bound it:
+// 8 x 2048 x 32768 112 us, on pair tiles 99.
+constexpr int kThinTokens = 4, kThinRows = 16, kThinStages = 16;  // rows of a chunk; of the ring
+struct ThinParams {
+  const float* d;            // [T][ldd]
+  int ldd;
+  const __nv_bfloat16 *x, *W;
+  long long ldx;
+  int T, K, V;
+  float* sums;               // [gridDim.y][T][K], or null: no dx
+  __nv_bfloat16* dW;         // or null
+  const float *scale0, *scale1;  // of dW, or null
+};
+__device__ __forceinline__ void pairs_of(const uint4& q, F2 (&v)[4]) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+template <int TT>
+__global__ void __launch_bounds__(128) vocab_thin_kernel(const ThinParams p) {
+  __shared__ uint4 ring[kThinStages][128];
+  __shared__ float sd[2][kThinRows][TT];
+  pdl_trigger();
+  pdl_wait();
+  const int k0 = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
+  const bool in = k0 < p.K;
+  const int chunks = (p.V + kThinRows - 1) / kThinRows;
+  const int mine = (chunks - static_cast<int>(blockIdx.y) + gridDim.y - 1) / gridDim.y;  // chunks, >= 1
+  // the i-th of them, from W's end
+  auto first_row = [&](int i) { return (chunks - 1 - (static_cast<int>(blockIdx.y) + i * static_cast<int>(gridDim.y))) * kThinRows; };
+  constexpr int S = kThinStages, R = kThinRows, U = 4;
+  static_assert(S == R, "the ring holds a chunk");
+  const float g = p.scale0 ? *p.scale0 * *p.scale1 : 1.f;
+  // rows u .. u+3 of a chunk into the ring (rows behind V stay what they were, unread)
+  auto fetch = [&](int i, int u) {
+    if (i < mine && in) {
+      const int r = first_row(i) + u;
+#pragma unroll
+      for (int a = 0; a < U; ++a)
+        if (r + a < p.V)
+          cp_async_16_full(smem_u32(&ring[u + a][threadIdx.x]), p.W + static_cast<long long>(r + a) * p.K + k0);
+    }
+    cp_async_commit();
+  };
+  // d of a chunk: up to PER values a thread, through registers to the buffer read next
+  constexpr int PER = (R * TT + 31) / 32;
+  float dn[PER];
+  auto load_d = [&](int i) {
+#pragma unroll
+    for (int a = 0; a < PER; ++a) {
+      const int e = threadIdx.x + a * blockDim.x, t = e / R, r = e % R;
+      dn[a] = 0.f;
+      if (i < mine && e < R * TT && t < p.T && first_row(i) + r < p.V)
+        dn[a] = p.d[static_cast<long long>(t) * p.ldd + first_row(i) + r];
+    }
+  };
+  auto store_d = [&](int b) {
+#pragma unroll
+    for (int a = 0; a < PER; ++a) {
+      const int e = threadIdx.x + a * blockDim.x;
+      if (e < R * TT) sd[b][e % R][e / R] = dn[a];
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < R; u += U) fetch(0, u);
+  load_d(0);
+  F2 x[TT][4], acc[TT][4];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (in && t < p.T) q = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + k0);
+    pairs_of(q, x[t]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[t][i] = both(0.f);
+  }
+  store_d(0);
+  __syncthreads();
+  for (int c = 0; c < mine; ++c) {
+    load_d(c + 1);
+    const int rb = first_row(c);
+#pragma unroll 1
+    for (int u = 0; u < R; u += U) {
+      cp_async_wait<R / U - 1>();
+      uint4 w[U];
+#pragma unroll
+      for (int a = 0; a < U; ++a) w[a] = ring[u + a][threadIdx.x];
+      fetch(c + 1, u);
+#pragma unroll
+      for (int a = 0; a < U; ++a) {
+        if (rb + u + a >= p.V || !in) break;
+        F2 wv[4], out[4];
+        pairs_of(w[a], wv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = both(0.f);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const F2 d = both(sd[c & 1][u + a][t]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[t][i] = fma2(d, wv[i], acc[t][i]);
+            out[i] = fma2(d, x[t][i], out[i]);
+          }
+        }
+        if (p.dW) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float e, f;
+            unpack2(out[i], e, f);
+            o[i] = cvt_bf16x2(e * g, f * g);
+          }
+          __stcs(reinterpret_cast<uint4*>(p.dW + static_cast<long long>(rb + u + a) * p.K + k0),
+                 make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      }
+    }
+    // (the other buffer: its readers are past the barrier before this chunk)
+    store_d((c + 1) & 1);
+    __syncthreads();
+  }
+  cp_async_wait<0>();
+  if (!in || !p.sums) return;
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    if (t >= p.T) break;
+    float* to = p.sums + (static_cast<long long>(blockIdx.y) * p.T + t) * p.K + k0;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(acc[t][i], v[2 * i], v[2 * i + 1]);
+    reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+// Threads of a block, blocks along the columns and down the rows: as many as an SM's
+// registers hold (of 128 threads six for up to 2 tokens, four for 4: of 4 x 2048 x 32768
+// on two 108 us, four 78, six, of which not all fit, 83), with two chunks or more where
+// that leaves 64 ranges (2 x 2048 x 8192 29 us, with one 31; 2 x 64 x 512 8.4 and 7.1).
+struct ThinPlan {
+  int threads, slabs, ranges;
+};
+ThinPlan plan_thin(int T, int K, int V) {
+  ThinPlan l;
+  l.threads = std::min(128, cdiv(K / 8, 32) * 32);
+  l.slabs = cdiv(K, 8 * l.threads);
+  const int blocks = std::max(1, (T <= 2 ? 6 : 4) * num_sms());
+  const int chunks = cdiv(V, kThinRows);
+  l.ranges = std::max(1, std::min(blocks / l.slabs, std::min(chunks, std::max(64, chunks / 2))));
+  return l;
+}
+template <int TT>
+cudaError_t launch_thin_t(const ThinPlan& l, const ThinParams& p, cudaStream_t st) {
+  return launch_pdl(vocab_thin_kernel<TT>, dim3(l.slabs, l.ranges), dim3(l.threads), 0, st, p);
+}
+cudaError_t launch_thin(const ThinPlan& l, const ThinParams& p, cudaStream_t st) {
+  return p.T <= 2 ? launch_thin_t<2>(l, p, st) : launch_thin_t<4>(l, p, st);
 }
 
 // Columns of a piece of the backward: as many as give d 256 MB (4096 x 2048 x 32768 in
@@ -756,7 +951,12 @@ size_t vocab_fwd_ws_bytes(int T, int K, int V) {
          round256(static_cast<size_t>(cdiv(T, 32)) * 8) + 256 +
          (T >= kCopyTokens ? round256(static_cast<size_t>(T) * line_ld(K) * 2) : 0);
 }
-size_t vocab_bwd_ws_bytes(int T, int K, int V) { return back_layout(T, K, V).total; }
+size_t vocab_bwd_ws_bytes(int T, int K, int V) {
+  if (T <= kThinTokens)
+    return round256(static_cast<size_t>(T) * ((V + 7) / 8 * 8) * 4) +
+           round256(static_cast<size_t>(plan_thin(T, K, V).ranges) * T * K * 4);
+  return back_layout(T, K, V).total;
+}
 
 cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t st) {
   if (a.T == 0) {
@@ -792,7 +992,29 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t s
   return launch_pdl(vocab_join_kernel, dim3(cdiv(a.T, 32)), dim3(kJoinThreads), 0, st, j);
 }
 
+// Up to 4 tokens: the whole vocabulary at once (d is a few rows), three launches.
+static cudaError_t backward_thin(const VocabBackward& a, void* ws, cudaStream_t st) {
+  VocabParams p{};
+  p.T = a.T, p.V = a.V, p.K = a.K, p.vocab = a.V;
+  p.targets = a.targets, p.i64 = a.i64, p.ignore = a.ignore;
+  p.lse = a.lse, p.z2 = 2.f * a.z_loss, p.gtok = a.per_token ? a.dloss : nullptr, p.weight = a.weight;
+  p.df = static_cast<float*>(ws), p.ldd = (a.V + 7) / 8 * 8;
+  p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
+  cudaError_t e = launch_tiles<true>(DenseOperand{a.x, a.T, a.K, a.ldx}, DenseOperand{a.W, a.V, a.K, a.K}, p, st);
+  if (e != cudaSuccess) return e;
+  const ThinPlan l = plan_thin(a.T, a.K, a.V);
+  ThinParams t{};
+  t.d = p.df, t.ldd = p.ldd, t.x = static_cast<const __nv_bfloat16*>(a.x);
+  t.W = static_cast<const __nv_bfloat16*>(a.W), t.ldx = a.ldx, t.T = a.T, t.K = a.K, t.V = a.V;
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(static_cast<size_t>(a.T) * p.ldd * 4));
+  t.sums = a.dx ? sums : nullptr, t.dW = static_cast<__nv_bfloat16*>(a.dW);
+  t.scale0 = a.per_token ? nullptr : a.dloss, t.scale1 = a.weight;
+  e = launch_thin(l, t, st);
+  return e == cudaSuccess && a.dx ? join_dx(sums, l.ranges, a.T, a.K, t.scale0, t.scale1, a.dx, st) : e;
+}
+
 cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t st) {
+  if (a.T <= kThinTokens) return backward_thin(a, ws, st);
   const BackLayout l = back_layout(a.T, a.K, a.V);
   char* const base = static_cast<char*>(ws);
   __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(base);
@@ -843,12 +1065,9 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     const DenseProduct pr[2] = {dx, dW};
     e = launch_dense_products(q, opt, pr, oa, ob, st);
   }
-  if (e == cudaSuccess && (l.split || l.slices > 1) && a.dx) {
-    const long long n4 = static_cast<long long>(a.T) * a.K / 4;
-    e = launch_pdl(vocab_join_dx_kernel, dim3(static_cast<unsigned>(std::min<long long>((n4 + 255) / 256, 16 * num_sms()))),
-                   dim3(256), 0, st, reinterpret_cast<const float4*>(sum), (l.split ? 2 : 1) * l.slices, n4,
-                    static_cast<uint2*>(a.dx));
-  }
+  // (its parts have the factor already)
+  if (e == cudaSuccess && (l.split || l.slices > 1) && a.dx)
+    e = join_dx(sum, (l.split ? 2 : 1) * l.slices, a.T, a.K, nullptr, nullptr, a.dx, st);
   return e;
 }
 
