@@ -197,6 +197,25 @@ def test_class_mixes_types_and_skips_what_has_no_gradient():
     assert all(p.grad is None for p in params)
 
 
+def test_a_graph_that_kept_the_old_parameters_notices():
+    params = [torch.nn.Parameter(torch.randn(300, device=DEV).to(dt)) for dt in (BF, F)]
+    opt = mgg.AdamW(params, **OPT)
+    kept = sum(p.square().float().sum() for p in params)
+    for p in params:
+        p.grad = torch.ones_like(p)
+    at = [p._version for p in params]
+    opt.step()
+    assert all(p._version > a for p, a in zip(params, at))
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.backward()
+    with torch.inference_mode():  # a tensor without versions
+        q, g = torch.ones(40, device=DEV), torch.ones(40, device=DEV)
+        m, v, _, _ = mgg.adamw_state([q])
+        mgg.adamw_step([q], [g], m, v, 1)
+        assert not q.eq(1).any()
+    mgg.adamw_step([q], [g], m, v, 2)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_captured_steps_count_on(bits):
     def fresh():

@@ -1,8 +1,8 @@
 // Python entry to the C ABI of the layers around the experts (block.py) and of a
-// training step's losses and optimiser (step.py): the argument checks, output allocation and the call, in one C function each.  A
-// decode step's calls take the GPU 4 to 8 us; these take the host 3.6 to 5 (the
-// products' gradients 8 to 9), where the same steps in Python and ctypes took 11
-// to 13.5.  No computation happens here.
+// training step's losses and optimiser (step.py): the argument checks, output
+// allocation and the call, in one C function each.  A decode step's calls take the
+// GPU 4 to 8 us; these take the host 3.6 to 5 (the products' gradients 8 to 9), where
+// the same steps in Python and ctypes took 11 to 13.5.  No computation happens here.
 #include <Python.h>
 
 #include <algorithm>
@@ -521,6 +521,11 @@ struct List {
   const char* what;
 };
 
+void written(const Tensor& t) {
+  c10::TensorImpl* p = t.unsafeGetTensorImpl();
+  if (!p->is_inference()) p->bump_version();
+}
+
 // params, grads, exp_avg, exp_avg_sq, step, lr, beta1, beta2, eps, weight_decay, masters,
 // exp_avg_scale, exp_avg_sq_scale, grad_scale
 PyObject* adamw_step(PyObject* const* a) {
@@ -575,6 +580,9 @@ PyObject* adamw_step(PyObject* const* a) {
   check(mgg_adamw_step(t.data(), static_cast<int>(n), pc, gc, ms.given() ? 8 : 32, lr, lr_dev, number(a[6]),
                        number(a[7]), number(a[8]), number(a[9]), step, step_dev, gs, stream(first)),
         "mgg_adamw_step");
+  // written in place: a backward pass that kept the old values has to notice (6 ns
+  // a tensor; masters are in no graph)
+  for (Py_ssize_t i = 0; i < n; ++i) written(params.get(i));
   return none();
 }
 

@@ -173,8 +173,10 @@ class AdamW:
     """AdamW over ``params`` with their state: step() updates those that have a
     gradient, in one launch for each mix of dtypes among them.  ``bits`` 8 holds
     the moments in 8 bits.  ``master`` keeps float32 copies of bfloat16
-    params.  ``capturable``: each parameter's count of steps lives on the GPU, so that
-    a captured step() counts its replays; ``lr`` may then be a float32 tensor."""
+    params.  One count of steps holds for all of them: a gradient that first
+    comes later is corrected as one that was zero until then.  ``capturable``:
+    the count lives on the GPU, so that a captured step() counts its replays;
+    ``lr`` may then be a float32 tensor."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
                  bits: int = 32, master: bool = True, capturable: bool = False):
