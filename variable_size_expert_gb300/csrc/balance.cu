@@ -21,7 +21,7 @@
 namespace mgg {
 namespace {
 
-constexpr int kFwdThreads = 512, kBwdThreads = 256, kJoinThreads = 256;
+constexpr int kFwdThreads = 512, kBwdThreads = 256, kJoinThreads = 1024;
 
 struct BalanceParams {
   const void* logits;
@@ -182,6 +182,15 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   if (blockIdx.x == 0 && threadIdx.x == 0 && !p.alone) *p.ticket = 0;
   for (int e = threadIdx.x; e < p.E; e += kFwdThreads) hits[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
+  // the choices of the block's tokens, those that count; each thread's first one is read
+  // ahead of the logits
+  const int choices = (t1 - t0) * p.k;
+  auto choice = [&](int i, int* e) {
+    *e = p.ids[static_cast<long long>(t0) * p.k + i];
+    return !p.mask || p.mask[t0 + i / p.k] != 0;
+  };
+  int first = 0;
+  const bool any = static_cast<int>(threadIdx.x) < choices && choice(threadIdx.x, &first);
   const int sub = lane & (p.lanes - 1), place = lane / p.lanes;  // in the token, of the token in the warp
   const int per = 32 / p.lanes, step = kWarps * per;
   const int width = p.E - sub * VEC;  // columns from this lane's first on
@@ -216,10 +225,9 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   mine = __reduce_add_sync(0xffffffffu, mine);
   __syncthreads();  // (hits, tokens are zero)
   if (lane == 0 && mine) atomicAdd(&tokens, mine);
-  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kFwdThreads) {
-    const int t = t0 + i / p.k;
-    const int e = p.ids[static_cast<long long>(t0) * p.k + i];
-    if (p.mask && !p.mask[t]) continue;
+  for (int i = threadIdx.x; i < choices; i += kFwdThreads) {
+    int e = first;
+    if (i < kFwdThreads ? !any : !choice(i, &e)) continue;
     if (e < 0 || e >= p.E)
       atomicOr(p.dev_status, kDevBadExpertId);
     else
@@ -279,57 +287,64 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
 }
 
 // An item is 32 experts of one sequence: a lane each, the chunks dealt out to the
-// eight warps.
+// warps, so that those of the most blocks that the sums take are read at once.
+constexpr int kJoinWarps = kJoinThreads / 32, kJoinAhead = 10;
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const BalanceParams p) {
-  __shared__ float s_sum[8][32];
-  __shared__ int s_hit[8][32];
-  __shared__ int s_n[8], s_live[8];
+  __shared__ float s_sum[kJoinWarps][32];
+  __shared__ int s_hit[kJoinWarps][32];
+  __shared__ int s_n[kJoinWarps], s_live[kJoinWarps];
   __shared__ bool last;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cols = cdiv(p.E, 32), items = cols * p.sequences;
-  int live = 0;
-  if (p.chunks == 1) {
-    for (int b = threadIdx.x; b < p.sequences; b += kJoinThreads) live += p.tokens[b] != 0;
-  } else {  // (few sequences: a warp each)
-    for (int b = warp; b < p.sequences; b += 8) {
-      bool any = false;
-      for (int c = lane; c < p.chunks; c += 32) any |= p.tokens[b * p.chunks + c] != 0;
-      live += __any_sync(0xffffffffu, any) && lane == 0;
-    }
-  }
-  live = __reduce_add_sync(0xffffffffu, live);
-  if (lane == 0) s_live[warp] = live;
   float share = 0.f;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const int b = it / cols, e = (it % cols) * 32 + lane;
     float sum = 0.f;
     int hit = 0, n = 0;
-    for (int c = warp; c < p.chunks; c += 64) {
-      float f[8];
-      int h[8];
+    for (int c = threadIdx.x; c < p.chunks; c += kJoinThreads) n += p.tokens[b * p.chunks + c];
+    for (int c = warp; c < p.chunks; c += kJoinAhead * kJoinWarps) {
+      float f[kJoinAhead];
+      int h[kJoinAhead];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const bool any = c + 8 * u < p.chunks && e < p.E;
-        const long long at = (static_cast<long long>(b) * p.chunks + c + 8 * u) * p.E + e;
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const bool any = c + kJoinWarps * u < p.chunks && e < p.E;
+        const long long at = (static_cast<long long>(b) * p.chunks + c + kJoinWarps * u) * p.E + e;
         f[u] = any ? p.sums[at] : 0.f;
         h[u] = any ? p.hits[at] : 0;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) sum += f[u], hit += h[u];
+      for (int u = 0; u < kJoinAhead; ++u) sum += f[u], hit += h[u];
     }
-    for (int c = threadIdx.x; c < p.chunks; c += kJoinThreads) n += p.tokens[b * p.chunks + c];
     n = __reduce_add_sync(0xffffffffu, n);
     s_sum[warp][lane] = sum;
     s_hit[warp][lane] = hit;
     if (lane == 0) s_n[warp] = n;
+    if (it == blockIdx.x) {  // sequences with tokens
+      int live = 0;
+      if (p.sequences == 1) {
+        live = lane == 0 && n != 0;
+      } else if (p.chunks == 1) {
+        for (int s = threadIdx.x; s < p.sequences; s += kJoinThreads) live += p.tokens[s] != 0;
+      } else {  // (few sequences: a warp each)
+        for (int s = warp; s < p.sequences; s += kJoinWarps) {
+          bool any = false;
+          for (int c = lane; c < p.chunks; c += 32) any |= p.tokens[s * p.chunks + c] != 0;
+          live += __any_sync(0xffffffffu, any) && lane == 0;
+        }
+      }
+      live = __reduce_add_sync(0xffffffffu, live);
+      if (lane == 0) s_live[warp] = live;
+    }
     __syncthreads();
     if (warp == 0) {
-      live = 0, n = 0, sum = 0.f, hit = 0;
+      int live = __reduce_add_sync(0xffffffffu, s_live[lane]);
+      if (p.sequences == 1) live = live != 0;
+      n = __reduce_add_sync(0xffffffffu, s_n[lane]);
+      sum = 0.f, hit = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w)
-        live += s_live[w], n += s_n[w], sum += s_sum[w][lane], hit += s_hit[w][lane];
+      for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w][lane], hit += s_hit[w][lane];
       const float slope = slope_of(hit, p.E, p.k, n, live);
       if (e < p.E) {
         p.counts[static_cast<long long>(b) * p.E + e] = hit;
@@ -342,7 +357,10 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
   if (warp == 0) {
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) share += __shfl_xor_sync(0xffffffffu, share, o);
-    if (lane == 0) {
+    if (gridDim.x == 1) {
+      if (lane == 0) *p.loss = share;
+      last = false;
+    } else if (lane == 0) {
       p.parts[blockIdx.x] = share;
       __threadfence();
       last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
@@ -423,11 +441,11 @@ __global__ void __launch_bounds__(kBwdThreads, VEC* NV <= 8 ? 4 : 1) balance_gra
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Blocks of a sequence's sums: two an SM in all, of at least 32 tokens each; one
-// alone where it needs no more than two steps of its 512 threads' lanes (512 x 8
-// in one launch 3 us less than in two).
+// alone up to 16384 logits (256 x 64 in one launch 6.0 us, called one after the other
+// 6.2; in two 8.1 and 9.3; 512 x 64 9.9 and 8.5).
 int plan_chunks(int T, int E, int sequences) {
   const int len = T / sequences;
-  if (sequences == 1 && static_cast<long long>(T) * E <= 8192) return 1;
+  if (sequences == 1 && static_cast<long long>(T) * E <= 16384) return 1;
   return std::max(1, std::min(cdiv(2 * num_sms(), sequences), cdiv(len, 32)));
 }
 
