@@ -18,7 +18,8 @@
 //             multiplies the accumulators: (p - 1) rounds to bfloat16 better
 //             than any multiple of it, and a small g does not leave the type's
 //             range.  (g of each token its own multiplies d before.)
-//             Up to 128 tokens d is kept in two bfloat16 parts, as further rows of
+//             Up to 4 tokens d is kept in f32 and both gradients leave one pass over
+//             W.  Up to 128 d is kept in two bfloat16 parts, as further rows of
 //             both products: a tile of 256 rows has room for them, and with few
 //             tokens there are no many roundings for one token's to vanish among
 //             (one token: dW off by up to 2^-8 in its target's row, now by the
@@ -657,7 +658,7 @@ cudaError_t launch_tiles(const DenseOperand& x, const DenseOperand& W, const Voc
 
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Tokens up to which d is kept in two parts.
+// Tokens up to which d, in bfloat16, is kept in two parts.
 constexpr int kSplitTokens = 128;
 
 // Rows whose pitch is no multiple of 64 bytes cost: an operand's 128-byte rows then
