@@ -68,6 +68,27 @@ def test_sequences(sequences, length, E, scoring):
     _check(logits, ids, scoring, None, sequences)
 
 
+# one cluster of blocks, two launches: either side of the limit, few blocks' sums to join
+# and many, sequences that share a cluster and a number of them that does not, blocks
+# without a token
+@pytest.mark.parametrize("T,E,sequences", [(1024, 8, 1), (1032, 8, 1), (2048, 64, 1), (2056, 64, 1), (521, 251, 1),
+                                           (523, 251, 1), (9, 1024, 1), (17, 1000, 1), (1032, 10, 2), (1032, 10, 4),
+                                           (1032, 10, 8), (1032, 10, 3), (16, 600, 8), (20000, 11, 4), (1600, 129, 16)])
+def test_blocks_clusters_and_launches(T, E, sequences):
+    logits, ids, g = _inputs(T, E, 3, (F, BF)[T % 2], T + E)
+    length = T // sequences
+    at = (length * torch.rand(sequences, generator=g, device=DEV)).long()
+    at[-1] = 0 if sequences > 1 else length // 3
+    mask = (torch.arange(length, device=DEV)[None] < at[:, None]).flatten()
+    for m in (None, mask):
+        a = _check(logits, ids, "softmax", m, sequences)
+        b = _check(logits, ids, "softmax", m, sequences)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    _check(logits, ids, "sigmoid", mask, sequences)
+    ids[T // 3, 1], ids[T - 1, 2] = -(1 << 31), E
+    _check(logits, ids, "softmax", None, sequences, want_status=L.MGG_DEV_BAD_EXPERT_ID)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [F, BF])
 def test_masked_experts_and_padding(scoring, dtype):

@@ -12,7 +12,8 @@
 // time), forms the slopes and the loss.  A token's logits lie in the registers of
 // `lanes` lanes (a power of two, 32 from 128 experts on), so that a softmax is
 // log2(lanes) shuffles and small gates fill their warps with tokens.  A call that one
-// block gets through in two steps (512 tokens of 8 experts) is one launch.
+// cluster of blocks gets through is one launch without a workspace: the blocks read one
+// another's sums from shared memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,7 +22,7 @@
 namespace mgg {
 namespace {
 
-constexpr int kFwdThreads = 512, kBwdThreads = 256, kJoinThreads = 1024;
+constexpr int kFwdThreads = 512, kBwdThreads = 256;
 
 struct BalanceParams {
   const void* logits;
@@ -31,7 +32,7 @@ struct BalanceParams {
   int T, E, k, len, sequences;  // len: tokens of a sequence
   int lanes;
   int chunks, rows;             // of a sequence: blocks, and tokens of one
-  bool alone;                   // one block, which finishes by itself
+  bool joined;                  // the blocks are one cluster, which finishes by itself
   float* sums;                  // [sequences * chunks][E]
   int32_t* hits;                // [sequences * chunks][E]
   int32_t* tokens;              // [sequences * chunks]
@@ -163,6 +164,18 @@ __device__ __forceinline__ float slope_of(int hits, int E, int k, int n, int liv
          (static_cast<float>(n) * static_cast<float>(n)) / static_cast<float>(live);
 }
 
+constexpr int kCluster = 8;  // blocks of the one launch, at most
+__device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ int ld_cluster_s32(uint32_t at) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 // tokens that a lane has in flight
 template <int N>
 constexpr int kUnroll = N >= 32 ? 1 : N >= 16 ? 2 : 4;
@@ -179,7 +192,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int seq = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int t0 = seq * p.len + chunk * p.rows, t1 = min(t0 + p.rows, (seq + 1) * p.len);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.alone) *p.ticket = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.joined) *p.ticket = 0;
   for (int e = threadIdx.x; e < p.E; e += kFwdThreads) hits[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
   // the choices of the block's tokens, those that count; each thread's first one is read
@@ -255,62 +268,113 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   if (warp < kWarps / 2) put(warp);
   __syncthreads();
   const long long out = static_cast<long long>(blockIdx.x) * p.E;
-  float share = 0.f;
   for (int e = threadIdx.x; e < p.E; e += kFwdThreads) {
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps / 2; ++w) s += sums[w * p.E + e];
-    if (p.alone) {
-      const float slope = slope_of(hits[e], p.E, p.k, tokens, 1);
-      p.counts[e] = hits[e];
-      p.slope[e] = slope;
-      share += slope * s;
+    if (p.joined) {
+      sums[e] = s;  // (which no other thread reads before the barrier)
     } else {
       p.sums[out + e] = s;
       p.hits[out + e] = hits[e];
     }
   }
-  if (p.alone) {
-    __shared__ float shares[kWarps];
+  if (!p.joined) {
+    if (threadIdx.x == 0) p.tokens[blockIdx.x] = tokens;
+    return;
+  }
+  // the cluster's blocks share the columns out and read one another's sums
+  __shared__ float shares[kWarps], total[kCluster];
+  __shared__ int s_n[kCluster], s_live;
+  const int rank = blockIdx.x, blocks = gridDim.x;
+  cluster_sync_all();
+  if (warp == 0) {
+    const int mine = lane < blocks ? ld_cluster_s32(mapa_shared(smem_u32(&tokens), lane)) : 0;
+    int n = 0;
+    for (int c = 0; c < p.chunks; ++c) n += __shfl_sync(0xffffffffu, mine, (lane * p.chunks + c) & 31);
+    if (lane < p.sequences) s_n[lane] = n;
+    const uint32_t live = __ballot_sync(0xffffffffu, lane < p.sequences && n != 0);
+    if (lane == 0) s_live = __popc(live);
+  }
+  __syncthreads();
+  float share = 0.f;
+  for (int i = rank * kFwdThreads + threadIdx.x; i < p.sequences * p.E; i += blocks * kFwdThreads) {
+    const int b = i / p.E, e = i - b * p.E;
+    float f[kCluster];
+    int h[kCluster];
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) share += __shfl_xor_sync(0xffffffffu, share, o);
-    if (lane == 0) shares[warp] = share;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      share = 0.f;
-      for (int w = 0; w < kWarps; ++w) share += shares[w];
-      *p.loss = share;
-    }
-  } else if (threadIdx.x == 0) {
-    p.tokens[blockIdx.x] = tokens;
+    for (int c = 0; c < kCluster; ++c)
+      if (c < p.chunks) {
+        f[c] = ld_cluster_f32(mapa_shared(smem_u32(&sums[e]), b * p.chunks + c));
+        h[c] = ld_cluster_s32(mapa_shared(smem_u32(&hits[e]), b * p.chunks + c));
+      }
+    float sum = 0.f;
+    int hit = 0;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c)
+      if (c < p.chunks) sum += f[c], hit += h[c];
+    const float slope = slope_of(hit, p.E, p.k, s_n[b], s_live);
+    p.counts[i] = hit;
+    p.slope[i] = slope;
+    share += slope * sum;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) share += __shfl_xor_sync(0xffffffffu, share, o);
+  if (lane == 0) shares[warp] = share;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    share = 0.f;
+    for (int w = 0; w < kWarps; ++w) share += shares[w];
+    st_cluster_s32(mapa_shared(smem_u32(&total[rank]), 0), __float_as_int(share));
+  }
+  cluster_sync_all();  // (no block leaves before the others have read its sums)
+  if (rank == 0 && threadIdx.x == 0) {
+    share = 0.f;
+    for (int r = 0; r < blocks; ++r) share += total[r];
+    *p.loss = share;
   }
 }
 
 // An item is 32 experts of one sequence: a lane each, the chunks dealt out to the
-// warps, so that those of the most blocks that the sums take are read at once.
-constexpr int kJoinWarps = kJoinThreads / 32, kJoinAhead = 10;
-__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const BalanceParams p) {
-  __shared__ float s_sum[kJoinWarps][32];
-  __shared__ int s_hit[kJoinWarps][32];
-  __shared__ int s_n[kJoinWarps], s_live[kJoinWarps];
+// warps, which read theirs at once: 8 warps up to 80 chunks, 32 beyond (38 chunks of 8
+// sequences x 256 10.3 us with 8, 11.1 with 32; 304 of 16384 x 8 10.3 and 6.9).
+constexpr int kJoinFew = 8, kJoinMany = 32, kJoinAhead = 10;
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) balance_join_kernel(const BalanceParams p) {
+  constexpr int kThreads = WARPS * 32;
+  __shared__ float s_sum[WARPS][32];
+  __shared__ int s_hit[WARPS][32];
+  __shared__ int s_n[WARPS], s_live[WARPS];
   __shared__ bool last;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cols = cdiv(p.E, 32), items = cols * p.sequences;
+  int live = 0;  // sequences with tokens
+  if (p.chunks == 1) {
+    for (int b = threadIdx.x; b < p.sequences; b += kThreads) live += p.tokens[b] != 0;
+  } else if (p.sequences > 1) {  // (few: a warp each)
+    for (int b = warp; b < p.sequences; b += WARPS) {
+      bool any = false;
+      for (int c = lane; c < p.chunks; c += 32) any |= p.tokens[b * p.chunks + c] != 0;
+      live += __any_sync(0xffffffffu, any) && lane == 0;
+    }
+  }
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) s_live[warp] = live;
   float share = 0.f;
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const int b = it / cols, e = (it % cols) * 32 + lane;
     float sum = 0.f;
     int hit = 0, n = 0;
-    for (int c = threadIdx.x; c < p.chunks; c += kJoinThreads) n += p.tokens[b * p.chunks + c];
-    for (int c = warp; c < p.chunks; c += kJoinAhead * kJoinWarps) {
+    for (int c = threadIdx.x; c < p.chunks; c += kThreads) n += p.tokens[b * p.chunks + c];
+    for (int c = warp; c < p.chunks; c += kJoinAhead * WARPS) {
       float f[kJoinAhead];
       int h[kJoinAhead];
 #pragma unroll
       for (int u = 0; u < kJoinAhead; ++u) {
-        const bool any = c + kJoinWarps * u < p.chunks && e < p.E;
-        const long long at = (static_cast<long long>(b) * p.chunks + c + kJoinWarps * u) * p.E + e;
+        const bool any = c + WARPS * u < p.chunks && e < p.E;
+        const long long at = (static_cast<long long>(b) * p.chunks + c + WARPS * u) * p.E + e;
         f[u] = any ? p.sums[at] : 0.f;
         h[u] = any ? p.hits[at] : 0;
       }
@@ -321,30 +385,14 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
     s_sum[warp][lane] = sum;
     s_hit[warp][lane] = hit;
     if (lane == 0) s_n[warp] = n;
-    if (it == blockIdx.x) {  // sequences with tokens
-      int live = 0;
-      if (p.sequences == 1) {
-        live = lane == 0 && n != 0;
-      } else if (p.chunks == 1) {
-        for (int s = threadIdx.x; s < p.sequences; s += kJoinThreads) live += p.tokens[s] != 0;
-      } else {  // (few sequences: a warp each)
-        for (int s = warp; s < p.sequences; s += kJoinWarps) {
-          bool any = false;
-          for (int c = lane; c < p.chunks; c += 32) any |= p.tokens[s * p.chunks + c] != 0;
-          live += __any_sync(0xffffffffu, any) && lane == 0;
-        }
-      }
-      live = __reduce_add_sync(0xffffffffu, live);
-      if (lane == 0) s_live[warp] = live;
-    }
     __syncthreads();
     if (warp == 0) {
-      int live = __reduce_add_sync(0xffffffffu, s_live[lane]);
-      if (p.sequences == 1) live = live != 0;
-      n = __reduce_add_sync(0xffffffffu, s_n[lane]);
+      live = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_live[lane] : 0);
+      n = __reduce_add_sync(0xffffffffu, lane < WARPS ? s_n[lane] : 0);
+      if (p.sequences == 1) live = n != 0;
       sum = 0.f, hit = 0;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w][lane], hit += s_hit[w][lane];
+      for (int w = 0; w < WARPS; ++w) sum += s_sum[w][lane], hit += s_hit[w][lane];
       const float slope = slope_of(hit, p.E, p.k, n, live);
       if (e < p.E) {
         p.counts[static_cast<long long>(b) * p.E + e] = hit;
@@ -440,12 +488,20 @@ __global__ void __launch_bounds__(kBwdThreads, VEC* NV <= 8 ? 4 : 1) balance_gra
 // ---------------------------------------------------------------- host
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Blocks of a sequence's sums: two an SM in all, of at least 32 tokens each; one
-// alone up to 16384 logits (256 x 64 in one launch 6.0 us, called one after the other
-// 6.2; in two 8.1 and 9.3; 512 x 64 9.9 and 8.5).
-int plan_chunks(int T, int E, int sequences) {
+// Blocks of a sequence's sums: one cluster of eight in all up to 131072 logits
+// (*joined), else two an SM, of at least 32 tokens each.  In a graph and called one
+// after the other, us:
+//   logits        one block   one cluster   two launches
+//   512 x 8       4.4, 5.3    4.5, 5.2      5.9, 8.4
+//   1024 x 64    18.4, 18.8   5.5, 5.7      9.0, 9.0
+//   16384 x 8    33.5, 34.0   7.5, 7.8      6.8, 8.4
+//   2048 x 64    33.8, 34.2   7.4, 7.7      9.1, 9.1
+//   4096 x 64    64.6, 65.0  11.5, 11.7     9.2, 9.9
+int plan_chunks(int T, int E, int sequences, bool* joined) {
   const int len = T / sequences;
-  if (sequences == 1 && static_cast<long long>(T) * E <= 16384) return 1;
+  const long long n = static_cast<long long>(T) * E;
+  *joined = n <= 131072 && sequences <= kCluster && (sequences & (sequences - 1)) == 0;
+  if (*joined) return kCluster / sequences;
   return std::max(1, std::min(cdiv(2 * num_sms(), sequences), cdiv(len, 32)));
 }
 
@@ -494,17 +550,17 @@ BalanceParams params(const BalanceArgs& a) {
 constexpr int kJoinBlocks = 1024;  // at most
 
 size_t balance_ws_bytes(int T, int E, int sequences) {
-  const size_t blocks = static_cast<size_t>(sequences) * plan_chunks(T, E, sequences);
-  if (blocks == 1) return 0;
+  bool joined;
+  const size_t blocks = static_cast<size_t>(sequences) * plan_chunks(T, E, sequences, &joined);
+  if (joined) return 0;
   return 2 * round256(blocks * E * 4) + round256(blocks * 4) + round256(kJoinBlocks * 4) + 256;
 }
 
 cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st) {
   BalanceParams p = params(a);
-  p.chunks = plan_chunks(a.T, a.E, a.sequences);
+  p.chunks = plan_chunks(a.T, a.E, a.sequences, &p.joined);
   p.rows = cdiv(p.len, p.chunks);
   const size_t blocks = static_cast<size_t>(a.sequences) * p.chunks;
-  p.alone = blocks == 1;
   char* at = static_cast<char*>(ws);
   p.sums = reinterpret_cast<float*>(at), at += round256(blocks * a.E * 4);
   p.hits = reinterpret_cast<int32_t*>(at), at += round256(blocks * a.E * 4);
@@ -515,14 +571,26 @@ cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st) {
     using T = decltype(type);
     return by_layout(a, false, &p.lanes, [&](auto wide, auto nv) {
       constexpr int VEC = wide() == 1 ? 1 : 16 / sizeof(T), NV = VEC == 8 && nv() > 4 ? 4 : nv();
-      return launch_pdl(balance_sums_kernel<T, softmax(), VEC, NV>, dim3(static_cast<unsigned>(blocks)),
-                        dim3(kFwdThreads), 0, st, p);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+      cfg.blockDim = dim3(kFwdThreads);
+      cfg.stream = st;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
+      attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = p.joined ? 2 : 1;
+      return cudaLaunchKernelEx(&cfg, balance_sums_kernel<T, softmax(), VEC, NV>, p);
     });
   });
-  if (e != cudaSuccess || p.alone) return e;
+  if (e != cudaSuccess || p.joined) return e;
   const long long items = static_cast<long long>(cdiv(a.E, 32)) * a.sequences;
-  return launch_pdl(balance_join_kernel, dim3(static_cast<unsigned>(std::min<long long>(items, kJoinBlocks))),
-                    dim3(kJoinThreads), 0, st, p);
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(items, kJoinBlocks)));
+  return p.chunks <= kJoinFew * kJoinAhead ? launch_pdl(balance_join_kernel<kJoinFew>, grid, dim3(kJoinFew * 32), 0, st, p)
+                                           : launch_pdl(balance_join_kernel<kJoinMany>, grid, dim3(kJoinMany * 32), 0, st, p);
 }
 
 cudaError_t launch_balance_bwd(const BalanceArgs& a, cudaStream_t st) {
