@@ -238,13 +238,22 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sums_kernel(const Balance
   mine = __reduce_add_sync(0xffffffffu, mine);
   __syncthreads();  // (hits, tokens are zero)
   if (lane == 0 && mine) atomicAdd(&tokens, mine);
-  for (int i = threadIdx.x; i < choices; i += kFwdThreads) {
-    int e = first;
-    if (i < kFwdThreads ? !any : !choice(i, &e)) continue;
+  auto count = [&](bool on, int e) {
+    if (!on) return;
     if (e < 0 || e >= p.E)
       atomicOr(p.dev_status, kDevBadExpertId);
     else
       atomicAdd(&hits[e], 1);
+  };
+  // (four on their way at a time: 16384 choices a block 11.8 to 9.4 us)
+  count(any, first);
+  for (int i = threadIdx.x + kFwdThreads; i < choices; i += 4 * kFwdThreads) {
+    int e[4];
+    bool on[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) on[u] = i + u * kFwdThreads < choices && choice(i + u * kFwdThreads, &e[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) count(on[u], e[u]);
   }
   // the warps' sums meet in two steps, in the warps' order
   auto put = [&](int w) {
@@ -494,8 +503,8 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 //   logits        one block   one cluster   two launches
 //   512 x 8       4.4, 5.3    4.5, 5.2      5.9, 8.4
 //   1024 x 64    18.4, 18.8   5.5, 5.7      9.0, 9.0
-//   16384 x 8    33.5, 34.0   7.5, 7.8      6.8, 8.4
-//   2048 x 64    33.8, 34.2   7.4, 7.7      9.1, 9.1
+//   16384 x 8    33.5, 34.0   7.0, 7.2      6.8, 8.4
+//   2048 x 64    33.8, 34.2   7.2, 7.6      9.1, 9.1
 //   4096 x 64    64.6, 65.0  11.5, 11.7     9.2, 9.9
 int plan_chunks(int T, int E, int sequences, bool* joined) {
   const int len = T / sequences;
