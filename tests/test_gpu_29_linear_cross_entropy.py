@@ -75,6 +75,21 @@ def test_forward_backward(T, K, V, reduction):
     _check(x, W, t, reduction, (0.0, 1e-3)[h % 2], g)
 
 
+# few tiles: groups of 32 tokens, the contraction shared out in a cluster of two, four or
+# eight (parts of one length and not; d in f32, in two parts, in one); and sizes of the
+# same kind with too many tiles for that
+@pytest.mark.parametrize("T,K,V", [(3, 1040, 700), (5, 4096, 300), (31, 2056, 5000), (32, 1032, 128), (100, 1224, 1111),
+                                   (129, 576, 130), (640, 520, 1700), (1025, 2600, 7), (32, 520, 20001), (33, 136, 20001),
+                                   (100, 72, 9999), (129, 64, 9000), (300, 264, 5003), (1300, 200, 1030),
+                                   (4000, 72, 400)])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+def test_few_tiles(T, K, V, reduction):
+    x, W, t, g = _inputs(T, K, V, T + K, dtype=(torch.int64, torch.int32)[T % 2])
+    a = _check(x, W, t, reduction, 1e-3, g)
+    loss, lse, w = mgg.linear_cross_entropy_forward(x, W, t, reduction=reduction, z_loss=1e-3)
+    assert torch.equal(loss, a[0]) and torch.equal(lse, a[1])
+
+
 # pieces of the vocabulary: two to eight, the last one narrow, one slice of dx in it
 # or several; few tokens (d in two parts) and many
 @pytest.mark.parametrize("T,K,V,piece,reduction", [(300, 64, 1000, 256, "mean"), (1, 40, 2000, 1024, "none"),

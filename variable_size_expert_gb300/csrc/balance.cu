@@ -165,16 +165,6 @@ __device__ __forceinline__ float slope_of(int hits, int E, int k, int n, int liv
 }
 
 constexpr int kCluster = 8;  // blocks of the one launch, at most
-__device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ int ld_cluster_s32(uint32_t at) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
 
 // tokens that a lane has in flight
 template <int N>
@@ -580,19 +570,11 @@ cudaError_t launch_balance(const BalanceArgs& a, void* ws, cudaStream_t st) {
     using T = decltype(type);
     return by_layout(a, false, &p.lanes, [&](auto wide, auto nv) {
       constexpr int VEC = wide() == 1 ? 1 : 16 / sizeof(T), NV = VEC == 8 && nv() > 4 ? 4 : nv();
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-      cfg.blockDim = dim3(kFwdThreads);
-      cfg.stream = st;
-      cudaLaunchAttribute attr[2];
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-      attr[1].id = cudaLaunchAttributeClusterDimension;
-      attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
-      attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = p.joined ? 2 : 1;
-      return cudaLaunchKernelEx(&cfg, balance_sums_kernel<T, softmax(), VEC, NV>, p);
+      const dim3 grid(static_cast<unsigned>(blocks)), block(kFwdThreads);
+      if (p.joined)
+        return launch_pdl_clusters(balance_sums_kernel<T, softmax(), VEC, NV>, grid, block, 0, static_cast<int>(blocks),
+                                   st, p);
+      return launch_pdl(balance_sums_kernel<T, softmax(), VEC, NV>, grid, block, 0, st, p);
     });
   });
   if (e != cudaSuccess || p.joined) return e;

@@ -322,7 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // tokens (16 or 32), W's rows on the rows of the accumulator, two blocks an SM with a
 // ring each, so that 190 KB an SM are in flight: the loss of 16 x 2048 x 32768 29 us
 // (134 MB, 68% of the measured copy rate; start, last epilogue and the joining kernel
-// are 9 of it).  On pair tiles every SM asks for the same few rows of x at once, 40
+// are 9 of it).  A vocabulary of few tiles leaves SMs idle: the blocks of a cluster then share
+// a tile's contraction out, leave their sums in shared memory and finish a share of its
+// tokens each.  On pair tiles every SM asks for the same few rows of x at once, 40
 // us (of 64 tokens 32 there, 34 here); one block an SM that walks over the tiles with
 // two accumulators 31.6.  A lane then holds a vocabulary entry, not a token: the
 // forward turns the tile through shared memory and reduces a token with a warp, the
@@ -331,13 +333,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 constexpr int kFewTokens = 32, kFewThreads = 192, kFewSlots = 6;
 constexpr int kFewMeta = 256;
 struct FewParams {
-  int N;          // tokens, rounded up to 16
-  int slots, run, runs, tmem_cols;
+  int N;          // tokens of a block, rounded up to 16
+  int split;      // blocks of a cluster that share the contraction out
+  int slots, run, tmem_cols;
 };
 size_t few_smem(int N, int slots) {
   return 1024 + std::max(static_cast<size_t>(slots) * (OPER + N * 128), static_cast<size_t>(N) * 132 * 4) + kFewMeta;
 }
-template <bool BACK>
+template <bool BACK, bool SPLIT>
 __global__ void __launch_bounds__(kFewThreads, 2)
     vocab_few_kernel(const __grid_constant__ VocabMaps maps, const __grid_constant__ VocabParams p,
                      const __grid_constant__ FewParams f) {
@@ -351,7 +354,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ring + 16 * kFewSlots + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * 128, nkb = cdiv(p.K, BK);
+  const int split = SPLIT ? f.split : 1, tile = blockIdx.x / split, rank = blockIdx.x % split;
+  const int n0 = tile * 128, t0 = SPLIT ? blockIdx.y * kFewTokens : 0;
+  const int kb0 = cdiv(p.K, BK) * rank / split, nkb = cdiv(p.K, BK) * (rank + 1) / split - kb0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < f.slots; ++s) {
@@ -375,18 +380,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   pdl_wait();
   pdl_trigger();
   const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
-  if (!BACK && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+  if (!BACK && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ticket = 0;
 
   if (warp == 4) {
     Ring r{0, 0, 0};
 #pragma unroll 1
-    for (int k = 0; k < nkb * BK; k += BK) {
+    for (int k = kb0 * BK; k < (kb0 + nkb) * BK; k += BK) {
       if (r.it >= f.slots && !__all_sync(0xffffffffu, wait_bar(empty + 8 * r.s, r.ph ^ 1, wc))) break;
       if (elect_one()) {
         const uint32_t a = base + r.s * stage;
         mbar_arrive_expect_tx(full + 8 * r.s, stage);
         tma_load_2d(a, &maps.b, full + 8 * r.s, k, n0);
-        tma_load_2d(a + OPER, &maps.a, full + 8 * r.s, k, 0);
+        tma_load_2d(a + OPER, &maps.a, full + 8 * r.s, k, t0);
       }
       r.next(f.slots);
     }
@@ -425,7 +430,28 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();  // every MMA is done; all warps, no wait of their own
   tc_fence_after();
   const bool ok = *abort_flag == 0;
-  const int tl = warp * 32 + lane, row = n0 + tl;
+  const int tl = warp * 32 + lane, row = n0 + tl, tokens = min(kFewTokens, p.T - t0);
+  const int runs = cdiv(nkb, f.run);
+  // the logit of the block's token i and this thread's row of W to its gradient
+  auto store_d = [&](int i, float z) {
+    const int t = t0 + i;
+    const int y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
+    const float lse = p.lse[t];
+    const float g = y < 0 ? 0.f : p.gtok ? p.gtok[t] * *p.weight : 1.f;
+    if (y == -2 && p.v0 + row == 0) atomicOr(p.dev_status, kDevBadTarget);
+    float d = exp2_f(fmaf(z, kLog2e, -lse * kLog2e)) * ((1.f + p.z2 * lse) * g);
+    if (y == p.v0 + row) d -= g;
+    if (y < 0) d = 0.f;
+    if (row < p.V && p.df) {
+      p.df[static_cast<long long>(t) * p.ldd + row] = d;
+    } else if (row < p.V) {
+      const __nv_bfloat16 hi = __float2bfloat16_rn(d);
+      p.d[static_cast<long long>(t) * p.ldd + row] = hi;
+      if (p.split)
+        p.d[static_cast<long long>(p.T + t) * p.ldd + row] = __float2bfloat16_rn(d - __bfloat162float(hi));
+    }
+  };
+  constexpr bool kTurned = !BACK || SPLIT;  // the tile goes through shared memory
   if (ok && warp < 4) {
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
@@ -433,46 +459,43 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       float v[16], x[16];
       tmem_ld16(taddr + j, v);
       tmem_ld_wait();
-      for (int k = 1; k < f.runs; ++k) {
+      for (int k = 1; k < runs; ++k) {
         tmem_ld16(taddr + k * f.N + j, x);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] += x[i];
       }
-      if constexpr (BACK) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = j + i;
-          if (t >= p.T) break;
-          const int y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
-          const float lse = p.lse[t];
-          const float g = y < 0 ? 0.f : p.gtok ? p.gtok[t] * *p.weight : 1.f;
-          if (y == -2 && p.v0 + row == 0) atomicOr(p.dev_status, kDevBadTarget);
-          float d = exp2_f(fmaf(v[i], kLog2e, -lse * kLog2e)) * ((1.f + p.z2 * lse) * g);
-          if (y == p.v0 + row) d -= g;
-          if (y < 0) d = 0.f;
-          if (row < p.V && p.df) {
-            p.df[static_cast<long long>(t) * p.ldd + row] = d;
-          } else if (row < p.V) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(d);
-            p.d[static_cast<long long>(t) * p.ldd + row] = hi;
-            if (p.split)
-              p.d[static_cast<long long>(p.T + t) * p.ldd + row] = __float2bfloat16_rn(d - __bfloat162float(hi));
-          }
-        }
-      } else {
+      if constexpr (kTurned) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) st_shared_f32(base + ((j + i) * 132 + tl) * 4, row < p.V ? v[i] : -INFINITY);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (j + i >= tokens) break;
+          store_d(j + i, v[i]);
+        }
       }
     }
   }
-  if (!BACK) {
-    __syncthreads();
-    for (int t = warp; ok && t < p.T; t += kFewThreads / 32) {
+  // the parts of a sum lie in the cluster's blocks, which share the tokens out
+  if (SPLIT) cluster_sync_all();
+  else if (!BACK) __syncthreads();
+  auto logit = [&](int t, int r) {
+    const uint32_t at = base + (t * 132 + r) * 4;
+    if (!SPLIT) return ld_shared_f32(at);
+    float z = 0.f;
+    for (int c = 0; c < split; ++c) z += ld_cluster_f32(mapa_shared(at, c));
+    return z;
+  };
+  if (BACK) {
+    if (SPLIT && ok && warp < 4)
+      for (int t = rank; t < tokens; t += split) store_d(t, logit(t, tl));
+  } else {
+    for (int t = rank + warp * split; ok && t < tokens; t += kFewThreads / 32 * split) {
       float v[4], top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = ld_shared_f32(base + (t * 132 + 32 * i + lane) * 4);
+        v[i] = logit(t, 32 * i + lane);
         top = fmaxf(top, v[i]);
       }
 #pragma unroll
@@ -483,13 +506,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       for (int i = 0; i < 4; ++i) s += exp2_f(fmaf(v[i], kLog2e, -r));
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) {
-        p.part[static_cast<long long>(blockIdx.x) * p.T + t] = make_float2(c, s);
-        const int at = target_of(p.targets, p.i64, p.ignore, p.vocab, t) - n0;
-        if (at >= 0 && at < 128) p.target_z[t] = ld_shared_f32(base + (t * 132 + at) * 4);
-      }
+      const int at = target_of(p.targets, p.i64, p.ignore, p.vocab, t0 + t) - n0;
+      if (lane == 0) p.part[static_cast<long long>(tile) * p.T + t0 + t] = make_float2(c, s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at == 32 * i + lane) p.target_z[t0 + t] = v[i];
     }
   }
+  if (SPLIT) cluster_sync_all();  // (no block leaves before the others have read its sums)
   tc_fence_before();
   __syncthreads();
   if (warp == 5) {
@@ -617,33 +641,56 @@ __global__ void vocab_empty_kernel(float* total, float* weight) {
   *weight = 1.f;
 }
 
+// Blocks of a cluster that share a tile's contraction out: as many as find room, with four
+// of its steps or more, of contractions of 1024 on (the loss of 16 x 4096 x 2048 23.1 us
+// without, 9.0 on clusters of eight; of 16 x 1024 x 2048 9.8 and 7.4; of 16 x 512 x 4096 7.8
+// and, of two, 8.4).
+int few_split(int T, int K, int V) {
+  const long long blocks = static_cast<long long>(cdiv(T, kFewTokens)) * cdiv(V, 128);
+  int split = 1;
+  while (split < 8 && 2 * split * blocks <= 2 * num_sms() && cdiv(K, BK) >= std::max(16, 8 * split)) split *= 2;
+  return split;
+}
+// More tokens go by groups of 32 where that leaves clusters of four: 256 x 256 tiles would
+// leave most SMs idle (loss, gradients of 64 x 4096 x 2048 25 and 43 us on them, 11 and 28
+// so; of 128 x 2048 x 2048 17 and 32, 13 and 27; of 128 x 1024 x 4096, clusters of two, 13
+// and 27, 14 and 30).
+bool by_few(int T, int K, int V) { return T <= kFewTokens || few_split(T, K, V) >= 4; }
 // Rows of W that one pair (c, s) of the forward stands for.
-int tile_columns(int T) { return T <= kFewTokens ? 128 : 256; }
+int tile_columns(int T, int K, int V) { return by_few(T, K, V) ? 128 : 256; }
 
+template <bool BACK, bool SPLIT>
+cudaError_t launch_few_as(const VocabMaps& maps, const VocabParams& p, const FewParams& f, cudaStream_t st) {
+  static bool done[64] = {};
+  const cudaError_t e = allow_smem(vocab_few_kernel<BACK, SPLIT>, 116 * 1024, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(cdiv(p.V, 128) * f.split, cdiv(p.T, kFewTokens));
+  const size_t smem = few_smem(f.N, f.slots);
+  if (SPLIT)
+    return launch_pdl_clusters(vocab_few_kernel<BACK, SPLIT>, grid, dim3(kFewThreads), smem, f.split, st, maps, p, f);
+  return launch_pdl(vocab_few_kernel<BACK, SPLIT>, grid, dim3(kFewThreads), smem, st, maps, p, f);
+}
 template <bool BACK>
 cudaError_t launch_few(const DenseOperand& x, const DenseOperand& W, const VocabParams& p, cudaStream_t st) {
-  static bool done[64] = {};
-  cudaError_t e = allow_smem(vocab_few_kernel<BACK>, 116 * 1024, done);
-  if (e != cudaSuccess) return e;
   FewParams f;
-  f.N = (p.T + 15) / 16 * 16;
-  const int nkb = cdiv(p.K, BK);
+  f.N = (std::min(p.T, kFewTokens) + 15) / 16 * 16;
+  f.split = few_split(p.T, p.K, p.V);
+  const int nkb = cdiv(cdiv(p.K, BK), f.split);
   // half of an SM's shared memory and tensor memory
   f.slots = std::min({kFewSlots, (112 * 1024 - 1024 - kFewMeta) / (OPER + f.N * 128), nkb});
   f.run = BACK ? nkb : std::max(cdiv(nkb, 256 / f.N), p.run);
-  f.runs = cdiv(nkb, f.run);
+  const int runs = cdiv(nkb, f.run);
   f.tmem_cols = 32;
-  while (f.tmem_cols < f.runs * f.N) f.tmem_cols *= 2;
+  while (f.tmem_cols < runs * f.N) f.tmem_cols *= 2;
   VocabMaps maps;
   if (!tmap_operand(&maps.a, x, false, f.N) || !tmap_operand(&maps.b, W, false, 128)) return cudaErrorInvalidValue;
-  return launch_pdl(vocab_few_kernel<BACK>, dim3(cdiv(p.V, 128)), dim3(kFewThreads), few_smem(f.N, f.slots), st,
-                    maps, p, f);
+  return f.split > 1 ? launch_few_as<BACK, true>(maps, p, f, st) : launch_few_as<BACK, false>(maps, p, f, st);
 }
 
 template <bool BACK>
 cudaError_t launch_tiles(const DenseOperand& x, const DenseOperand& W, const VocabParams& p,
                          cudaStream_t st) {
-  if (p.T <= kFewTokens) return launch_few<BACK>(x, W, p, st);
+  if (by_few(p.T, p.K, p.V)) return launch_few<BACK>(x, W, p, st);
   static bool done[64] = {};
   cudaError_t e = allow_smem(vocab_pair_kernel<BACK>, kPairSmem, done);
   if (e != cudaSuccess) return e;
@@ -697,45 +744,56 @@ cudaError_t copy_rows(DenseOperand* o, void* to, int copies, cudaStream_t st) {
   return e;
 }
 
-// dx = scale (the sum of its parts, [parts][T K]).  Eight groups of threads share the
-// parts of 32 x 4 values, so that many parts are not as many latencies.
-__global__ void __launch_bounds__(256) vocab_join_dx_kernel(const float4* sum, int parts, long long n4,
+// dx = scale (the sum of its parts, [parts][T K]).  GROUPS groups of threads share the
+// parts of a block's values: eight for few values of many parts, which otherwise are as
+// many latencies (gradients of 32 x 256 x 131072 95 us with one, 84 with eight; of 512 x
+// 4096 x 2048 44 with one, 53 with eight), 32 from 65 parts on.
+template <int GROUPS>
+constexpr int kJoinDxThreads = GROUPS == 1 ? 256 : GROUPS * 32;
+template <int GROUPS>
+__global__ void __launch_bounds__(kJoinDxThreads<GROUPS>) vocab_join_dx_kernel(const float4* sum, int parts, long long n4,
                                                             const float* scale0, const float* scale1, uint2* dx) {
-  __shared__ float4 sh[8][32];
+  constexpr int kWide = kJoinDxThreads<GROUPS> / GROUPS;
+  __shared__ float4 sh[GROUPS > 1 ? GROUPS : 1][GROUPS > 1 ? kWide : 1];
   pdl_trigger();
   pdl_wait();
   const float g = scale0 ? *scale0 * *scale1 : 1.f;
-  const int group = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = min(8, parts);
+  const int group = threadIdx.x / kWide, lane = threadIdx.x % kWide;
   // (the same number of rounds in every thread of the block)
-  for (long long base = static_cast<long long>(blockIdx.x) * 32; base < n4; base += static_cast<long long>(gridDim.x) * 32) {
-    const long long i = base + lane;
+  for (long long at = static_cast<long long>(blockIdx.x) * kWide; at < n4; at += static_cast<long long>(gridDim.x) * kWide) {
+    const long long i = at + lane;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < n4) {
-#pragma unroll 8
-      for (int k = group; k < parts; k += 8) {
-        const float4 b = sum[k * n4 + i];
-        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-      }
+    for (int k = group; i < n4 && k < parts; k += 8 * GROUPS) {
+      float4 b[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        b[u] = k + u * GROUPS < parts ? sum[(k + u * GROUPS) * n4 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a.x += b[u].x, a.y += b[u].y, a.z += b[u].z, a.w += b[u].w;
     }
-    sh[group][lane] = a;
-    __syncthreads();
-    if (group == 0 && i < n4) {
-      for (int k = 1; k < groups; ++k) {
+    if constexpr (GROUPS > 1) {
+      sh[group][lane] = a;
+      __syncthreads();
+      for (int k = 1; group == 0 && k < GROUPS; ++k) {
         const float4 b = sh[k][lane];
         a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
       }
-      dx[i] = make_uint2(cvt_bf16x2(a.x * g, a.y * g), cvt_bf16x2(a.z * g, a.w * g));
+      __syncthreads();
     }
-    __syncthreads();
+    if (group == 0 && i < n4) dx[i] = make_uint2(cvt_bf16x2(a.x * g, a.y * g), cvt_bf16x2(a.z * g, a.w * g));
   }
 }
 cudaError_t join_dx(const float* sum, int parts, int T, int K, const float* scale0, const float* scale1, void* dx,
                     cudaStream_t st) {
   const long long n4 = static_cast<long long>(T) * K / 4;
-  return launch_pdl(vocab_join_dx_kernel, dim3(static_cast<unsigned>(std::min<long long>((n4 + 31) / 32, 64 * num_sms()))),
-                    dim3(256), 0, st, reinterpret_cast<const float4*>(sum), parts, n4, scale0, scale1,
-                    static_cast<uint2*>(dx));
+  auto launch = [&](auto kernel, long long blocks, int threads) {
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, st,
+                      reinterpret_cast<const float4*>(sum), parts, n4, scale0, scale1, static_cast<uint2*>(dx));
+  };
+  if (n4 > 65536 || parts < 8)
+    return launch(vocab_join_dx_kernel<1>, std::min<long long>((n4 + 255) / 256, 16 * num_sms()), kJoinDxThreads<1>);
+  return parts <= 64 ? launch(vocab_join_dx_kernel<8>, (n4 + 31) / 32, kJoinDxThreads<8>)
+                     : launch(vocab_join_dx_kernel<32>, (n4 + 31) / 32, kJoinDxThreads<32>);
 }
 
 // ---------------------------------------------------------------- both gradients of very few tokens
@@ -746,10 +804,10 @@ cudaError_t join_dx(const float* sum, int parts, int T, int K, const float* scal
 // memory (only the thread that copied them reads them: no barrier), 16 under way.  The
 // blocks take chunks of rows from W's end, which d's kernel has read last and L2 still
 // holds, and write dW past it.  The blocks' sums of dx meet afterwards.  d, dx and dW of
-// 1, 2 and 4 x 2048 x 32768 take 75, 76 and 78 us (on pair tiles, of one contraction
-// block each, 97 to 99; with four loads under way a thread 112 to 121), of 2 x 4096 x
-// 131072 513 (627), of 2 x 64 x 512 7.1 (10.3).  From 8 tokens their products bound it:
-// 8 x 2048 x 32768 112 us, on pair tiles 99.
+// 1, 2 and 4 x 2048 x 32768 take 70, 71 and 74 us (on pair tiles, of one contraction
+// block each, 97 to 99; with four loads under way a thread 112 to 121), of 2 x 2048 x
+// 8192 23 (39), of 2 x 512 x 4096 12.3 (18.6).  From 8 tokens their products bound it: 8 x
+// 2048 x 32768 112 us, on pair tiles 99.
 constexpr int kThinTokens = 4, kThinRows = 16, kThinStages = 16;  // rows of a chunk; of the ring
 struct ThinParams {
   const float* d;            // [T][ldd]
@@ -948,7 +1006,7 @@ BackLayout back_layout(int T, int K, int V) {
 
 // forward: the tiles' pairs, the targets' logits, the joining blocks' sums, their ticket, x
 size_t vocab_fwd_ws_bytes(int T, int K, int V) {
-  return round256(static_cast<size_t>(cdiv(V, tile_columns(T))) * T * 8) + round256(static_cast<size_t>(T) * 4) +
+  return round256(static_cast<size_t>(cdiv(V, tile_columns(T, K, V))) * T * 8) + round256(static_cast<size_t>(T) * 4) +
          round256(static_cast<size_t>(cdiv(T, 32)) * 8) + 256 +
          (T >= kCopyTokens ? round256(static_cast<size_t>(T) * line_ld(K) * 2) : 0);
 }
@@ -970,7 +1028,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t s
     at += round256(bytes);
     return r;
   };
-  const int tn = cdiv(a.V, tile_columns(a.T));
+  const int tn = cdiv(a.V, tile_columns(a.T, a.K, a.V));
   VocabParams p{};
   p.T = a.T, p.V = a.V, p.K = a.K, p.vocab = a.V;
   p.targets = a.targets, p.i64 = a.i64, p.ignore = a.ignore;
