@@ -381,6 +381,20 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   pdl_trigger();
   const WaitCtl wc{abort_flag, p.dev_status, p.wait_limit};
   if (!BACK && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ticket = 0;
+  // the backward's: what token `lane` of the block brings to d, under the products (read
+  // for each in the epilogue, gradients of 32 x 256 x 131072 84 us; so 73)
+  const int tokens = min(kFewTokens, p.T - t0);
+  int own_y = -1;
+  float own_lse = 0.f, own_g = 0.f, own_f = 0.f;
+  if (BACK && warp < 4 && lane < tokens) {
+    const int t = t0 + lane;
+    own_y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
+    const float lse = p.lse[t];
+    own_lse = -lse * kLog2e;
+    own_g = own_y < 0 ? 0.f : p.gtok ? p.gtok[t] * *p.weight : 1.f;
+    own_f = (1.f + p.z2 * lse) * own_g;
+    if (own_y == -2 && p.v0 + n0 == 0 && rank == 0 && warp == 0) atomicOr(p.dev_status, kDevBadTarget);
+  }
 
   if (warp == 4) {
     Ring r{0, 0, 0};
@@ -430,25 +444,22 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();  // every MMA is done; all warps, no wait of their own
   tc_fence_after();
   const bool ok = *abort_flag == 0;
-  const int tl = warp * 32 + lane, row = n0 + tl, tokens = min(kFewTokens, p.T - t0);
+  const int tl = warp * 32 + lane, row = n0 + tl;
   const int runs = cdiv(nkb, f.run);
   // the logit of the block's token i and this thread's row of W to its gradient
   auto store_d = [&](int i, float z) {
-    const int t = t0 + i;
-    const int y = target_of(p.targets, p.i64, p.ignore, p.vocab, t);
-    const float lse = p.lse[t];
-    const float g = y < 0 ? 0.f : p.gtok ? p.gtok[t] * *p.weight : 1.f;
-    if (y == -2 && p.v0 + row == 0) atomicOr(p.dev_status, kDevBadTarget);
-    float d = exp2_f(fmaf(z, kLog2e, -lse * kLog2e)) * ((1.f + p.z2 * lse) * g);
+    const long long t = t0 + i;
+    const int y = __shfl_sync(0xffffffffu, own_y, i);
+    const float g = __shfl_sync(0xffffffffu, own_g, i);
+    float d = exp2_f(fmaf(z, kLog2e, __shfl_sync(0xffffffffu, own_lse, i))) * __shfl_sync(0xffffffffu, own_f, i);
     if (y == p.v0 + row) d -= g;
     if (y < 0) d = 0.f;
     if (row < p.V && p.df) {
-      p.df[static_cast<long long>(t) * p.ldd + row] = d;
+      p.df[t * p.ldd + row] = d;
     } else if (row < p.V) {
       const __nv_bfloat16 hi = __float2bfloat16_rn(d);
-      p.d[static_cast<long long>(t) * p.ldd + row] = hi;
-      if (p.split)
-        p.d[static_cast<long long>(p.T + t) * p.ldd + row] = __float2bfloat16_rn(d - __bfloat162float(hi));
+      p.d[t * p.ldd + row] = hi;
+      if (p.split) p.d[(p.T + t) * p.ldd + row] = __float2bfloat16_rn(d - __bfloat162float(hi));
     }
   };
   constexpr bool kTurned = !BACK || SPLIT;  // the tile goes through shared memory
