@@ -727,7 +727,7 @@ mgg_status mgg_linear_backward(const void* dy, mgg_dtype dy_dtype, int64_t lddy,
  * MGG_DEV_BAD_EXPERT_ID and is not counted.  Sums are f32, in a fixed order.
  * ws: mgg_workspace_bytes(MGG_OP_BALANCE, T, sequences, E, 0, 0, ...); 0 for small
  * calls, which then need none.
- * Errors: MGG_ERR_INVALID_ARG (null, T < 0, E < 1, E > MGG_MAX_EXPERTS, k < 1,
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, T > 2^30, E < 1, E > MGG_MAX_EXPERTS, k < 1,
  * k > MGG_MAX_TOPK, ldl < E, sequences < 1 or not dividing T, a scoring other
  * than MGG_SCORE_SOFTMAX and MGG_SCORE_SIGMOID), MGG_ERR_DTYPE,
  * MGG_ERR_ALIGNMENT, MGG_ERR_WORKSPACE, MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
@@ -766,8 +766,8 @@ mgg_status mgg_balance_loss_backward(const float* dloss, const void* logits, mgg
  * K % 8 == 0, ldx % 8 == 0, x and W 16-byte aligned; any V >= 1.  f32
  * accumulation and statistics; equal inputs give equal bits.
  * ws: mgg_workspace_bytes(MGG_OP_VOCAB_FORWARD, T, 0, 0, V, K, MGG_BF16).
- * Errors: MGG_ERR_INVALID_ARG (null, T < 0, K < 1, V < 1, ldx < K, z_loss
- * negative or not finite, unknown reduction), MGG_ERR_ALIGNMENT,
+ * Errors: MGG_ERR_INVALID_ARG (null, T < 0, K < 1, V < 1, one of them over 2^30,
+ * ldx < K, z_loss negative or not finite, unknown reduction), MGG_ERR_ALIGNMENT,
  * MGG_ERR_WORKSPACE, MGG_ERR_UNSUPPORTED_ARCH, MGG_ERR_CUDA.
  */
 mgg_status mgg_linear_cross_entropy(const void* x, int64_t ldx, const void* W, const void* targets,
@@ -783,8 +783,8 @@ mgg_status mgg_linear_cross_entropy(const void* x, int64_t ldx, const void* W, c
  *   dx [T, K] bf16 = g d W,  dW [V, K] bf16 = g d^T x; either may be NULL
  *   g = dloss[0] weight[0], or with per_token dloss[t] weight[0] (dloss [T])
  * The vocabulary is taken in pieces: the logits again, d in bf16 (the products'
- * operand), both products; dx is summed in f32 over the pieces.  dloss and weight
- * are read on the device.
+ * operand; up to 128 tokens in two bf16 parts, up to 4 in f32), both products; dx is
+ * summed in f32 over the pieces.  dloss and weight are read on the device.
  * ws: mgg_workspace_bytes(MGG_OP_VOCAB_BACKWARD, T, 0, 0, V, K, MGG_BF16).
  * Errors as for the forward.
  */

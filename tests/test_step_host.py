@@ -35,7 +35,7 @@ def test_balance_refusals(lib):
                      (dict(slope=None), inv), (dict(st=None), inv), (dict(T=-1), inv), (dict(E=0), inv),
                      (dict(E=1025, ldl=1025), inv), (dict(k=0), inv), (dict(k=33), inv), (dict(ldl=15), inv),
                      (dict(B=0), inv), (dict(B=3), inv), (dict(sc=2), inv), (dict(sc=0x100), inv), (dict(d=2), dt),
-                     (dict(l=FAKE + 2), al), (dict(ids=FAKE + 1), al), (dict(slope=FAKE + 2), al)):
+                     (dict(l=FAKE + 2), al), (dict(ids=FAKE + 1), al), (dict(slope=FAKE + 2), al), (dict(T=(1 << 30) + 1), inv)):
         assert f(**kw) == want, kw
 
     def b(g=FAKE, l=FAKE, d=1, slope=FAKE, T=4, E=16, B=1, sc=0, out=FAKE):
@@ -62,7 +62,8 @@ def test_cross_entropy_refusals(lib):
                      (dict(K=0), inv), (dict(V=0), inv), (dict(ldx=56), inv), (dict(red=3), inv), (dict(red=-1), inv),
                      (dict(zl=-1.0), inv), (dict(zl=math.nan), inv), (dict(zl=math.inf), inv), (dict(K=60), al),
                      (dict(ldx=68), al), (dict(x=FAKE + 8), al), (dict(W=FAKE + 8), al), (dict(t=FAKE + 4), al),
-                     (dict(i64=0, t=FAKE + 2), al), (dict(lse=FAKE + 2), al)):
+                     (dict(i64=0, t=FAKE + 2), al), (dict(lse=FAKE + 2), al), (dict(T=(1 << 30) + 1), inv),
+                     (dict(V=(1 << 30) + 1), inv), (dict(K=(1 << 30) + 8, ldx=1 << 31), inv)):
         assert f(**kw) == want, kw
 
     def b(g=FAKE, w=FAKE, x=FAKE, W=FAKE, t=FAKE, lse=FAKE, T=4, K=64, V=24, zl=0.0, dx=FAKE, dW=FAKE, st=FAKE):

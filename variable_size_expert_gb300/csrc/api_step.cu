@@ -3,6 +3,8 @@
 // entropy over a vocabulary and the AdamW step.
 #include <math.h>
 
+#include <algorithm>
+
 #include "../../include/mgg.h"
 #include "common.cuh"
 #include "internal.h"
@@ -19,16 +21,20 @@ mgg_status zero(void* p, size_t bytes, cudaStream_t st) {
   return p && bytes ? from_cuda(cudaMemsetAsync(p, 0, bytes, st)) : MGG_OK;
 }
 
+// The kernels count rows in 32 bits and step past a side's end.
+constexpr int kMostRows = 1 << 30;
+
 mgg_status check_balance(mgg_dtype dtype, int64_t ldl, int T, int E, int sequences,
                          mgg_scoring scoring) {
-  if (T < 0 || E < 1 || E > kMaxExperts || ldl < E || sequences < 1 || T % sequences != 0)
+  if (T < 0 || T > kMostRows || E < 1 || E > kMaxExperts || ldl < E || sequences < 1 || T % sequences != 0)
     return MGG_ERR_INVALID_ARG;
   if (scoring != MGG_SCORE_SOFTMAX && scoring != MGG_SCORE_SIGMOID) return MGG_ERR_INVALID_ARG;
   return float_type(dtype) ? MGG_OK : MGG_ERR_DTYPE;
 }
 
 mgg_status check_vocab(int64_t ldx, int T, int K, int V, float z_loss) {
-  if (T < 0 || K < 1 || V < 1 || ldx < K || !(z_loss >= 0.f) || !isfinite(z_loss))
+  if (T < 0 || K < 1 || V < 1 || ldx < K || !(z_loss >= 0.f) || !isfinite(z_loss) ||
+      std::max({T, K, V}) > kMostRows)
     return MGG_ERR_INVALID_ARG;
   return K % 8 == 0 && ldx % 8 == 0 ? MGG_OK : MGG_ERR_ALIGNMENT;
 }
