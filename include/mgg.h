@@ -784,7 +784,8 @@ mgg_status mgg_linear_cross_entropy(const void* x, int64_t ldx, const void* W, c
  *   g = dloss[0] weight[0], or with per_token dloss[t] weight[0] (dloss [T])
  * The vocabulary is taken in pieces: the logits again, d in bf16 (the products'
  * operand; up to 128 tokens in two bf16 parts, up to 4 in f32), both products; dx is
- * summed in f32 over the pieces.  dloss and weight are read on the device.
+ * summed in f32 over the pieces.  dloss and weight are read on the device.  What the
+ * rows of x hold of tokens that do not count (NaN, infinities) reaches neither result.
  * ws: mgg_workspace_bytes(MGG_OP_VOCAB_BACKWARD, T, 0, 0, V, K, MGG_BF16).
  * Errors as for the forward.
  */

@@ -24,6 +24,11 @@
 //             tokens there are no many roundings for one token's to vanish among
 //             (one token: dW off by up to 2^-8 in its target's row, now by the
 //             rounding of the result alone).
+//             Tokens that do not count have d = 0, which is not enough for dW: 0 times
+//             a NaN or an infinity in their rows of x would be NaN in all of it.  dW's
+//             x is therefore a copy in which their rows are zeros: gradients of 4096 x
+//             2048 x 32768 979 us, 987 with x as it lies; of 1111 x 1160 x 50257 341 and
+//             339 (few tokens and rows off 64-byte lines were copied before, too).
 //
 // Bound by the matrix units at the power limit: loss of 8192 x 2048 x 32768 632 us
 // (1740 TFLOP/s), gradients of 4096 x 2048 x 32768 974 us (1690); with few tokens by
@@ -730,27 +735,31 @@ bool off_lines(const void* p, long long ld) { return reinterpret_cast<uintptr_t>
 int line_ld(int K) { return (K + 63) / 64 * 64; }
 
 // rows x K8 16-byte pieces, `ld` apart, to rows `out_ld` apart; `copies` of all, one
-// behind the other ([x; x] is the other operand of d's two parts in dW).
+// behind the other ([x; x] is the other operand of d's two parts in dW).  With targets
+// (of a vocabulary of `vocab`) the rows of tokens that do not count become zeros.
 __global__ void __launch_bounds__(256) vocab_copy_kernel(const uint4* x, long long ld, int rows, int K8,
-                                                         int out_ld, int copies, uint4* out) {
+                                                         int out_ld, int copies, const void* targets, bool i64,
+                                                         long long ignore, int vocab, uint4* out) {
   pdl_trigger();
   pdl_wait();
   const long long n = static_cast<long long>(rows) * K8, step = static_cast<long long>(gridDim.x) * 256;
   for (long long i = blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
     const long long t = i / K8;
     const int k = static_cast<int>(i - t * K8);
-    const uint4 v = x[t * ld + k];
+    uint4 v = x[t * ld + k];
+    if (targets && target_of(targets, i64, ignore, vocab, static_cast<int>(t)) < 0) v = make_uint4(0, 0, 0, 0);
     for (int c = 0; c < copies; ++c) out[(c * rows + t) * out_ld + k] = v;
   }
 }
-// o's rows to `to`, on 128-byte boundaries
-cudaError_t copy_rows(DenseOperand* o, void* to, int copies, cudaStream_t st) {
+// o's rows to `to`, on 128-byte boundaries; with `a` x's, those that do not count as zeros
+cudaError_t copy_rows(DenseOperand* o, void* to, int copies, const VocabBackward* a, cudaStream_t st) {
   const int ld = line_ld(o->cols);
   const long long n = static_cast<long long>(o->rows) * (o->cols / 8);
   const unsigned blocks = static_cast<unsigned>(std::min<long long>((n + 255) / 256, 16 * num_sms()));
   const cudaError_t e = launch_pdl(vocab_copy_kernel, dim3(blocks), dim3(256), 0, st,
                                    static_cast<const uint4*>(o->ptr), o->ld / 8, o->rows, o->cols / 8, ld / 8,
-                                   copies, static_cast<uint4*>(to));
+                                   copies, a ? a->targets : nullptr, a && a->i64, a ? a->ignore : 0LL,
+                                   a ? a->V : 0, static_cast<uint4*>(to));
   *o = DenseOperand{to, o->rows, o->cols, ld};
   return e;
 }
@@ -826,6 +835,9 @@ struct ThinParams {
   const __nv_bfloat16 *x, *W;
   long long ldx;
   int T, K, V;
+  const void* targets;       // as in VocabParams
+  bool i64;
+  long long ignore;
   float* sums;               // [gridDim.y][T][K], or null: no dx
   __nv_bfloat16* dW;         // or null
   const float *scale0, *scale1;  // of dW, or null
@@ -887,7 +899,9 @@ __global__ void __launch_bounds__(128) vocab_thin_kernel(const ThinParams p) {
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     uint4 q = make_uint4(0, 0, 0, 0);
-    if (in && t < p.T) q = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + k0);
+    // (a token that does not count: zeros, whatever its row holds)
+    if (in && t < p.T && target_of(p.targets, p.i64, p.ignore, p.V, t) >= 0)
+      q = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + k0);
     pairs_of(q, x[t]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = both(0.f);
@@ -985,7 +999,7 @@ int piece_columns(int T, int V) {
   return static_cast<int>(std::min<long long>(cols, (V + 7) / 8 * 8));
 }
 // What the backward keeps: d; f32 sums of dx (over pieces, of its slices and parts);
-// x or [x; x]; a piece of W.
+// a copy of x or [x; x]; of a piece of W.
 struct BackLayout {
   int cols;
   bool split, copy_w;
@@ -1008,7 +1022,7 @@ BackLayout back_layout(int T, int K, int V) {
   l.sum = round256(static_cast<size_t>(rows) * l.cols * 2);
   l.copy_w = T >= kCopyWTokens && K % 32;
   l.x = l.sum + (l.split || l.slices > 1 || l.cols < V ? round256(sums * K * 4) : 0);
-  l.w = l.x + (l.split || T >= kCopyTokens ? round256(static_cast<size_t>(rows) * line_ld(K) * 2) : 0);
+  l.w = l.x + round256(static_cast<size_t>(rows) * line_ld(K) * 2);
   l.total = l.w + (l.copy_w ? round256(static_cast<size_t>(l.cols) * line_ld(K) * 2) : 0);
   return l;
 }
@@ -1052,7 +1066,7 @@ cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t s
   p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
   DenseOperand x{a.x, a.T, a.K, a.ldx};
   cudaError_t e = cudaSuccess;
-  if (a.T >= kCopyTokens && off_lines(a.x, a.ldx)) e = copy_rows(&x, at, 1, st);
+  if (a.T >= kCopyTokens && off_lines(a.x, a.ldx)) e = copy_rows(&x, at, 1, nullptr, st);
   if (e == cudaSuccess) e = launch_tiles<false>(x, DenseOperand{a.W, a.V, a.K, a.K}, p, st);
   if (e != cudaSuccess) return e;
   j.part = p.part, j.tiles = tn, j.T = a.T, j.vocab = a.V, j.target_z = p.target_z;
@@ -1076,6 +1090,7 @@ static cudaError_t backward_thin(const VocabBackward& a, void* ws, cudaStream_t 
   ThinParams t{};
   t.d = p.df, t.ldd = p.ldd, t.x = static_cast<const __nv_bfloat16*>(a.x);
   t.W = static_cast<const __nv_bfloat16*>(a.W), t.ldx = a.ldx, t.T = a.T, t.K = a.K, t.V = a.V;
+  t.targets = a.targets, t.i64 = a.i64, t.ignore = a.ignore;
   float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(static_cast<size_t>(a.T) * p.ldd * 4));
   t.sums = a.dx ? sums : nullptr, t.dW = static_cast<__nv_bfloat16*>(a.dW);
   t.scale0 = a.per_token ? nullptr : a.dloss, t.scale1 = a.weight;
@@ -1093,8 +1108,8 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
   DenseOperand x{a.x, a.T, a.K, a.ldx};
   const float* const scale = a.per_token ? nullptr : a.dloss;
   cudaError_t e = cudaSuccess;
-  if ((l.split && a.dW) || (a.T >= kCopyTokens && off_lines(a.x, a.ldx)))
-    e = copy_rows(&x, base + l.x, l.split ? 2 : 1, st);
+  if (a.dW || (a.T >= kCopyTokens && off_lines(a.x, a.ldx)))
+    e = copy_rows(&x, base + l.x, l.split ? 2 : 1, &a, st);
   DenseOperand xd = x;  // beside d's rows
   xd.rows = rows;
   for (int v0 = 0; e == cudaSuccess && v0 < a.V; v0 += l.cols) {
@@ -1108,7 +1123,7 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
     DenseOperand Wp{W, n, a.K, a.K};
     const DenseOperand dp{d, rows, n, l.cols};
-    if (l.copy_w) e = copy_rows(&Wp, base + l.w, 1, st);
+    if (l.copy_w) e = copy_rows(&Wp, base + l.w, 1, nullptr, st);
     if (e == cudaSuccess) e = launch_tiles<true>(x, Wp, p, st);
     if (e != cudaSuccess) return e;
     const bool parts = l.split || l.slices > 1;

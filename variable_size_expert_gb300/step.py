@@ -103,7 +103,8 @@ def linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, W: torch
                                   workspace: torch.Tensor | None = None):
     """Gradients of linear_cross_entropy_forward from its lse and weight: (dx
     [T, K], dW [V, K]) bfloat16.  dloss float32 on the GPU: a scalar, or [T]
-    after reduction "none"."""
+    after reduction "none".  Whatever x holds of tokens that do not count
+    reaches neither."""
     st = status if status is not None else new_status(x.device)
     return block._host.linear_cross_entropy_backward(dloss, x, W, targets, lse, weight, ignore_index, z_loss,
                                                      need_dx, need_dW, st, workspace)
