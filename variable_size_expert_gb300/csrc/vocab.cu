@@ -333,14 +333,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // us (of 64 tokens 32 there, 34 here); one block an SM that walks over the tiles with
 // two accumulators 31.6.  A lane then holds a vocabulary entry, not a token: the
 // forward turns the tile through shared memory and reduces a token with a warp, the
-// backward stores d as it lies.  Runs of the contraction have an accumulator each
-// and meet in f32 (see kRunBlocks).
-constexpr int kFewTokens = 32, kFewThreads = 192, kFewSlots = 6;
-constexpr int kFewMeta = 256;
+// backward stores d as it lies.  The forward's runs of the contraction have an
+// accumulator each and meet in f32 (see kRunBlocks); runs beyond half of the tensor
+// memory (contractions over 2048, over 1024 from 17 tokens on) take the accumulators in
+// turn, and the epilogue's warps empty one while the next are multiplied (16 x 2048 x
+// 32768, where both ways are open, 29.1 us so, 28.2 with all read at the end).  With
+// longer runs in place of more of them 32 tokens' lse of 32 x 16384 x 19500 were 7.7e-6
+// of 11.9 too low on average (positive terms: 1.5e-4 of 74); so 7e-7 and 1e-6, as at any
+// other length.
+constexpr int kFewTokens = 32, kFewThreads = 192, kFewSlots = 6, kFewAccs = 16;
+constexpr int kFewMeta = 512;
 struct FewParams {
   int N;          // tokens of a block, rounded up to 16
   int split;      // blocks of a cluster that share the contraction out
   int slots, run, tmem_cols;
+  int accs;       // accumulators, up to kFewAccs
 };
 size_t few_smem(int N, int slots) {
   return 1024 + std::max(static_cast<size_t>(slots) * (OPER + N * 128), static_cast<size_t>(N) * 132 * 4) + kFewMeta;
@@ -358,10 +365,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t full = base + ring, empty = full + 8 * kFewSlots, done = empty + 8 * kFewSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ring + 16 * kFewSlots + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t acc_full = done + 16, acc_empty = acc_full + 8 * kFewAccs;  // (forward)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = SPLIT ? f.split : 1, tile = blockIdx.x / split, rank = blockIdx.x % split;
   const int n0 = tile * 128, t0 = SPLIT ? blockIdx.y * kFewTokens : 0;
   const int kb0 = cdiv(p.K, BK) * rank / split, nkb = cdiv(p.K, BK) * (rank + 1) / split - kb0;
+  const int runs = cdiv(nkb, f.run);
+  const bool in_turn = !BACK && runs > f.accs;  // (the backward has one run)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < f.slots; ++s) {
@@ -373,6 +383,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     fence_mbar_init();
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
+  }
+  if (in_turn && warp == 1 && lane < f.accs) {
+    mbar_init(acc_full + 8 * lane, 1);
+    mbar_init(acc_empty + 8 * lane, 4);
+    fence_mbar_init();
   }
   if (warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), f.tmem_cols);
@@ -421,22 +436,31 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   } else if (warp == 5) {
     const uint32_t idesc = idesc_bf16_f32(128, f.N, false, false);
     const uint64_t a0 = sw128_desc(base, 16, 1024), b0 = sw128_desc(base + OPER, 16, 1024);
-    Ring r{0, 0, 0};
+    Ring r{0, 0, 0}, a{0, 0, 0};  // the operands' slots, the accumulators
     bool ok = true;
 #pragma unroll 1
-    for (int kb = 0; kb < nkb; ++kb) {
+    for (int kb = 0, in = 0; kb < nkb; ++kb) {
+      if (in == 0 && a.it >= f.accs) {
+        ok = __all_sync(0xffffffffu, wait_bar(acc_empty + 8 * a.s, a.ph ^ 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+      }
       ok = __all_sync(0xffffffffu, wait_bar(full + 8 * r.s, r.ph, wc));
       if (!ok) break;
       tc_fence_after();
-      const int run = kb / f.run;
       const uint64_t ad = a0 + r.s * (stage >> 4), bd = b0 + r.s * (stage >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          tc_mma_bf16(tmem_base + run * f.N, ad + kk * 2, bd + kk * 2, idesc, kb != run * f.run || kk);
+          tc_mma_bf16(tmem_base + a.s * f.N, ad + kk * 2, bd + kk * 2, idesc, in || kk);
         tc_commit(empty + 8 * r.s);
       }
       r.next(f.slots);
+      if (++in == f.run || kb + 1 == nkb) {
+        if (in_turn && elect_one()) tc_commit(acc_full + 8 * a.s);
+        a.next(f.accs);
+        in = 0;
+      }
     }
     if (elect_one()) {
       tc_commit(done);
@@ -445,12 +469,34 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     __syncwarp();
   }
+  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  float sums[BACK ? 1 : kFewTokens];  // of this thread's row of W and each token
+  if (!BACK && in_turn && warp < 4) {
+    Ring a{0, 0, 0};
+#pragma unroll 1
+    while (a.it < runs) {
+      if (!__all_sync(0xffffffffu, wait_bar(acc_full + 8 * a.s, a.ph, wc))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < kFewTokens; j += 16) {
+        if (j >= f.N) break;
+        float x[16];
+        tmem_ld16(taddr + a.s * f.N + j, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[j + i] = a.it ? sums[j + i] + x[i] : x[i];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + 8 * a.s);
+      a.next(f.accs);
+    }
+  }
   // ------------------------------------------------ epilogue
   __syncthreads();  // every MMA is done; all warps, no wait of their own
   tc_fence_after();
   const bool ok = *abort_flag == 0;
   const int tl = warp * 32 + lane, row = n0 + tl;
-  const int runs = cdiv(nkb, f.run);
   // the logit of the block's token i and this thread's row of W to its gradient
   auto store_d = [&](int i, float z) {
     const long long t = t0 + i;
@@ -467,9 +513,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       if (p.split) p.d[(p.T + t) * p.ldd + row] = __float2bfloat16_rn(d - __bfloat162float(hi));
     }
   };
-  constexpr bool kTurned = !BACK || SPLIT;  // the tile goes through shared memory
-  if (ok && warp < 4) {
-    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+  auto turn = [&](int i, float z) { st_shared_f32(base + (i * 132 + tl) * 4, row < p.V ? z : -INFINITY); };
+  if (in_turn && ok && warp < 4) {
+#pragma unroll
+    for (int i = 0; i < kFewTokens; ++i)
+      if (i < f.N) turn(i, sums[BACK ? 0 : i]);
+  } else if (ok && warp < 4) {
 #pragma unroll 1
     for (int j = 0; j < f.N; j += 16) {
       float v[16], x[16];
@@ -481,9 +530,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] += x[i];
       }
-      if constexpr (kTurned) {
+      if constexpr (!BACK || SPLIT) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st_shared_f32(base + ((j + i) * 132 + tl) * 4, row < p.V ? v[i] : -INFINITY);
+        for (int i = 0; i < 16; ++i) turn(j + i, v[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -694,10 +743,10 @@ cudaError_t launch_few(const DenseOperand& x, const DenseOperand& W, const Vocab
   const int nkb = cdiv(cdiv(p.K, BK), f.split);
   // half of an SM's shared memory and tensor memory
   f.slots = std::min({kFewSlots, (112 * 1024 - 1024 - kFewMeta) / (OPER + f.N * 128), nkb});
-  f.run = BACK ? nkb : std::max(cdiv(nkb, 256 / f.N), p.run);
-  const int runs = cdiv(nkb, f.run);
+  f.run = BACK ? nkb : p.run;
+  f.accs = std::min(256 / f.N, cdiv(nkb, f.run));
   f.tmem_cols = 32;
-  while (f.tmem_cols < runs * f.N) f.tmem_cols *= 2;
+  while (f.tmem_cols < f.accs * f.N) f.tmem_cols *= 2;
   VocabMaps maps;
   if (!tmap_operand(&maps.a, x, false, f.N) || !tmap_operand(&maps.b, W, false, 128)) return cudaErrorInvalidValue;
   return f.split > 1 ? launch_few_as<BACK, true>(maps, p, f, st) : launch_few_as<BACK, false>(maps, p, f, st);
