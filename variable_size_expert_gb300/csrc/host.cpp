@@ -527,8 +527,9 @@ void written(const Tensor& t) {
 }
 
 // params, grads, exp_avg, exp_avg_sq, step, lr, beta1, beta2, eps, weight_decay, masters,
-// exp_avg_scale, exp_avg_sq_scale, grad_scale
-PyObject* adamw_step(PyObject* const* a) {
+// exp_avg_scale, exp_avg_sq_scale, grad_scale.  `only_check`: everything but the step,
+// whose refusals are then known before any of several calls has updated anything.
+PyObject* adamw(PyObject* const* a, bool only_check) {
   const List params(a[0], "params", -1, false);
   const Py_ssize_t n = params.count;
   const List grads(a[1], "grads", n, false), m(a[2], "exp_avg", n, false), v(a[3], "exp_avg_sq", n, false),
@@ -577,14 +578,18 @@ PyObject* adamw_step(PyObject* const* a) {
   for (size_t i = 1; i < spans.size(); ++i)
     if (spans[i - 1].first + spans[i - 1].second > spans[i].first)
       fail(PyExc_ValueError, "%s must not overlap (is one of them listed twice?)", "params");
-  check(mgg_adamw_step(t.data(), static_cast<int>(n), pc, gc, ms.given() ? 8 : 32, lr, lr_dev, number(a[6]),
-                       number(a[7]), number(a[8]), number(a[9]), step, step_dev, gs, stream(first)),
+  // (with no tensors the library checks the numbers alone)
+  check(mgg_adamw_step(t.data(), only_check ? 0 : static_cast<int>(n), pc, gc, ms.given() ? 8 : 32, lr, lr_dev,
+                       number(a[6]), number(a[7]), number(a[8]), number(a[9]), step, step_dev, gs, stream(first)),
         "mgg_adamw_step");
+  if (only_check) return none();
   // written in place: a backward pass that kept the old values has to notice (15 ns
   // a tensor; masters are in no graph)
   for (Py_ssize_t i = 0; i < n; ++i) written(params.get(i));
   return none();
 }
+PyObject* adamw_step(PyObject* const* a) { return adamw(a, false); }
+PyObject* adamw_check(PyObject* const* a) { return adamw(a, true); }
 
 #define MGG_ENTRY(f, n)                                                               \
   {                                                                                   \
@@ -602,6 +607,7 @@ PyMethodDef methods[] = {MGG_ENTRY(layer_norm_forward, 5),
                          MGG_ENTRY(linear_cross_entropy_forward, 8),
                          MGG_ENTRY(linear_cross_entropy_backward, 12),
                          MGG_ENTRY(adamw_step, 14),
+                         MGG_ENTRY(adamw_check, 14),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", nullptr, -1, methods};
 

@@ -166,18 +166,23 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     tensors of one element (int32, float32), which a captured call reads anew.
     ``grad_scale`` (float32 [1] on the GPU) multiplies the gradients
     (mgg_adamw_step)."""
-    block._host.adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], eps, weight_decay,
-                           masters, exp_avg_scale, exp_avg_sq_scale, grad_scale)
+    block._host.adamw_step(*_host_args(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay,
+                                       masters, exp_avg_scale, exp_avg_sq_scale, grad_scale))
+
+
+def _host_args(params, grads, exp_avg, exp_avg_sq, step, lr, betas, *rest):
+    return params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], *rest
 
 
 class AdamW:
     """AdamW over ``params`` with their state: step() updates those that have a
-    gradient, in one launch for each mix of dtypes among them.  ``bits`` 8 holds
-    the moments in 8 bits.  ``master`` keeps float32 copies of bfloat16
-    params.  One count of steps holds for all of them: a gradient that first
-    comes later is corrected as one that was zero until then.  ``capturable``:
-    the count lives on the GPU, so that a captured step() counts its replays;
-    ``lr`` may then be a float32 tensor."""
+    gradient, in one launch for each mix of dtypes among them; a step that is
+    refused has updated and counted nothing.  ``bits`` 8 holds the moments in 8
+    bits.  ``master`` keeps float32 copies of bfloat16 params.  One count of
+    steps holds for all of them: a gradient that first comes later is corrected
+    as one that was zero until then.  ``capturable``: the count lives on the
+    GPU, so that a captured step() counts its replays; ``lr`` may then be a
+    float32 tensor."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
                  bits: int = 32, master: bool = True, capturable: bool = False):
@@ -192,18 +197,30 @@ class AdamW:
 
     @torch.no_grad()
     def step(self, grad_scale: torch.Tensor | None = None) -> None:
-        self.count += 1
         mixes: dict = {}
         for i, p in enumerate(self.params):
             if p.grad is not None:
                 mixes.setdefault((p.dtype, p.grad.dtype, self.masters[i] is None), []).append(i)
+        count = self.count if self.capturable else self.count + 1
+        calls = []
         for (_, _, alone), at in mixes.items():
             def pick(t):
                 return None if t is None else [t[i] for i in at]
-            adamw_step(pick(self.params), [self.params[i].grad for i in at], pick(self.exp_avg),
-                       pick(self.exp_avg_sq), self.count, self.lr, self.betas, self.eps, self.weight_decay,
-                       None if alone else pick(self.masters), pick(self.exp_avg_scale),
-                       pick(self.exp_avg_sq_scale), grad_scale)
+            calls.append((pick(self.params), [self.params[i].grad for i in at], pick(self.exp_avg),
+                          pick(self.exp_avg_sq), count, self.lr, self.betas, self.eps, self.weight_decay,
+                          None if alone else pick(self.masters), pick(self.exp_avg_scale),
+                          pick(self.exp_avg_sq_scale), grad_scale))
+        # One call refuses before it updates anything.  Where something precedes a call
+        # (another mix, the count on the GPU), all are checked first.  (Without a GPU
+        # the first call refuses.)
+        if (self.capturable or len(calls) > 1) and any(c[0][0].is_cuda for c in calls):
+            for c in calls:
+                block._host.adamw_check(*_host_args(*c))
+        if self.capturable:
+            self.count += 1
+        for c in calls:
+            adamw_step(*c)
+        self.count = count
 
     def zero_grad(self) -> None:
         for p in self.params:
