@@ -47,3 +47,34 @@ def test_the_check_refuses_what_the_step_refuses(host):
             kinds.append((e.type, str(e.value)))
         assert kinds[0] == kinds[1], at
     assert host.adamw_check(*([[]] * 4), *good[4:]) is None
+
+
+def test_masters_take_over_what_was_written(monkeypatch):
+    monkeypatch.setattr(step, "adamw_step", lambda *a: None)
+    ps = _params() + [torch.nn.Parameter(torch.ones(5).bfloat16())]
+    opt = mgg.AdamW(ps)
+    assert [m is None for m in opt.masters] == [False, True, False]
+    opt.masters[0].add_(1e-4)                  # (bits that bfloat16 does not hold)
+    low = opt.masters[0].clone()
+    assert torch.equal(low.bfloat16(), ps[0].detach())
+    opt.step()
+    assert torch.equal(opt.masters[0], low)    # nothing was written
+    with torch.no_grad():
+        ps[0][1, 2] = 7.0
+        ps[2].fill_(2.0)
+    opt.step()
+    low[1, 2] = 7.0
+    assert torch.equal(opt.masters[0], low)
+    assert (opt.masters[2] == 1).all()         # (no gradient yet: when one comes)
+    ps[2].grad = torch.ones(5).bfloat16()
+    opt.step()
+    assert (opt.masters[2] == 2).all()
+    ps[0].data.fill_(3.0)                      # (counts no version)
+    opt.step()
+    assert torch.equal(opt.masters[0], low)
+    opt.sync_masters()
+    assert (opt.masters[0] == 3).all()
+    with torch.inference_mode():
+        q = torch.ones(4).bfloat16()
+        q.grad = torch.ones(4).bfloat16()
+        mgg.AdamW([q]).step()

@@ -174,11 +174,18 @@ def _host_args(params, grads, exp_avg, exp_avg_sq, step, lr, betas, *rest):
     return params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], *rest
 
 
+def _version(t: torch.Tensor) -> int:
+    """How often t was written in place (a tensor of inference mode does not count)."""
+    return 0 if t.is_inference() else t._version
+
+
 class AdamW:
     """AdamW over ``params`` with their state: step() updates those that have a
     gradient, in one launch for each mix of dtypes among them; a step that is
     refused has updated and counted nothing.  ``bits`` 8 holds the moments in 8
-    bits.  ``master`` keeps float32 copies of bfloat16 params.  One count of
+    bits.  ``master`` keeps float32 copies of bfloat16 params; they take over
+    what was written into their params since the last step (weights that were
+    loaded), found by the tensors' versions: see sync_masters.  One count of
     steps holds for all of them: a gradient that first comes later is corrected
     as one that was zero until then.  ``capturable``: the count lives on the
     GPU, so that a captured step() counts its replays; ``lr`` may then be a
@@ -191,6 +198,7 @@ class AdamW:
         self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = adamw_state(self.params, bits)
         self.masters = [p.detach().float() if master and p.dtype == torch.bfloat16 else None
                         for p in self.params]
+        self._seen = [_version(p) for p in self.params]     # versions that the masters stand for
         self.capturable = capturable
         device = self.params[0].device if self.params else "cpu"
         self.count = torch.zeros(1, dtype=torch.int32, device=device) if capturable else 0
@@ -201,6 +209,9 @@ class AdamW:
         for i, p in enumerate(self.params):
             if p.grad is not None:
                 mixes.setdefault((p.dtype, p.grad.dtype, self.masters[i] is None), []).append(i)
+        for i in (i for at in mixes.values() for i in at):
+            if self.masters[i] is not None and self._seen[i] != _version(self.params[i]):
+                self._take_over(i)
         count = self.count if self.capturable else self.count + 1
         calls = []
         for (_, _, alone), at in mixes.items():
@@ -221,6 +232,25 @@ class AdamW:
         for c in calls:
             adamw_step(*c)
         self.count = count
+        for i in (i for at in mixes.values() for i in at):
+            self._seen[i] = _version(self.params[i])
+
+    def _take_over(self, i: int) -> None:
+        p, w = self.params[i].detach(), self.masters[i]
+        # (what a param holds unchanged is its master rounded: that keeps its bits)
+        w.copy_(torch.where(w.to(p.dtype) == p, w, p.to(w.dtype)))
+        self._seen[i] = _version(self.params[i])
+
+    @torch.no_grad()
+    def sync_masters(self) -> None:
+        """Masters take over every element of their params that is not the
+        master's own, rounded.  step() does so for params whose version has
+        changed; to be called after writes that count no version (through
+        ``.data``, by a captured graph) and after writes that replays of a
+        captured step are to see."""
+        for i, w in enumerate(self.masters):
+            if w is not None:
+                self._take_over(i)
 
     def zero_grad(self) -> None:
         for p in self.params:
