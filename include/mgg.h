@@ -193,6 +193,8 @@ mgg_status mgg_tile_config(mgg_op op, mgg_dtype dtype, int* BM, int* BN, int* BK
  *   MGG_OP_FFN_BACKWARD          : T, k, E, N = H, K = F, dtype (bf16)
  *   MGG_OP_LAYER_NORM_BACKWARD   : T, K
  *   MGG_OP_LINEAR_BACKWARD       : T, N
+ *   MGG_OP_BALANCE               : T, k = the sequences, E
+ *   MGG_OP_VOCAB_FORWARD, MGG_OP_VOCAB_BACKWARD : T, N = V, K
  */
 size_t mgg_workspace_bytes(mgg_op op, int T, int k, int E, int N, int K, mgg_dtype dtype);
 

@@ -476,13 +476,13 @@ size_t mgg_workspace_bytes(mgg_op op, int T, int k, int E, int N, int K, mgg_dty
       if (T < 1 || N < 1) return 0;
       return dense_bwd_ws_bytes(T, N);
     case MGG_OP_BALANCE:  // k: the sequences
-      if (T < 1 || E < 1 || E > kMaxExperts || k < 1 || T % k != 0) return 0;
+      if (T < 1 || T > kMostRows || E < 1 || E > kMaxExperts || k < 1 || T % k != 0) return 0;
       return balance_ws_bytes(T, E, k);
     case MGG_OP_VOCAB_FORWARD:
-      if (T < 1 || N < 1 || K < 1) return 0;
+      if (T < 1 || N < 1 || K < 1 || std::max({T, N, K}) > kMostRows) return 0;
       return vocab_fwd_ws_bytes(T, K, N);
     case MGG_OP_VOCAB_BACKWARD:
-      if (T < 1 || N < 1 || K < 1) return 0;
+      if (T < 1 || N < 1 || K < 1 || std::max({T, N, K}) > kMostRows) return 0;
       return vocab_bwd_ws_bytes(T, K, N);
   }
   return 0;

@@ -21,9 +21,6 @@ mgg_status zero(void* p, size_t bytes, cudaStream_t st) {
   return p && bytes ? from_cuda(cudaMemsetAsync(p, 0, bytes, st)) : MGG_OK;
 }
 
-// The kernels count rows in 32 bits and step past a side's end.
-constexpr int kMostRows = 1 << 30;
-
 mgg_status check_balance(mgg_dtype dtype, int64_t ldl, int T, int E, int sequences,
                          mgg_scoring scoring) {
   if (T < 0 || T > kMostRows || E < 1 || E > kMaxExperts || ldl < E || sequences < 1 || T % sequences != 0)

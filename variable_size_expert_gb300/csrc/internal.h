@@ -301,6 +301,10 @@ size_t vocab_bwd_ws_bytes(int T, int K, int V);
 cudaError_t launch_vocab_forward(const VocabForward& a, void* ws, cudaStream_t st);
 cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t st);
 
+// Longest side of the balance loss and the vocabulary's products: the kernels count
+// rows in 32 bits and step past a side's end.
+constexpr int kMostRows = 1 << 30;
+
 // balance.cu
 struct BalanceArgs {
   const void* logits;
