@@ -6,6 +6,7 @@ import torch
 
 import variable_size_expert_gb300 as mgg
 from tests import block_ref as R
+from tests.test_gpu_29_linear_cross_entropy import _check, _inputs
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -35,3 +36,16 @@ def test_no_bias_grows_with_the_contraction(T, K, V):
     tol = 8 * 2.0 ** -23 * z + 3 * R.U * ref.mean() + 8 * R.U
     err = (lse.double() - ref).mean()
     assert err.abs() <= tol, (float(err), float(tol))
+
+
+# more runs than accumulators (16 up to 16 tokens, else 8), whole rounds of them and not,
+# a last run of one block; blocks of their own and clusters
+@pytest.mark.parametrize("T,K,V", [(17, 1032, 20001), (32, 1024 + 64, 20001), (20, 2056, 19600), (32, 2048, 19500),
+                                   (16, 2056, 20001), (9, 2048 + 128, 19500), (1, 4104, 19500), (32, 8200, 700),
+                                   (70, 8200, 300), (16, 16392, 600)])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+def test_accumulators_in_turn(T, K, V, reduction):
+    x, W, t, g = _inputs(T, K, V, T + K)
+    a = _check(x, W, t, reduction, 1e-3, g)
+    b = mgg.linear_cross_entropy_forward(x, W, t, reduction=reduction, z_loss=1e-3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
