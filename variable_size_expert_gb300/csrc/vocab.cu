@@ -26,9 +26,7 @@
 //             rounding of the result alone).
 //             Tokens that do not count have d = 0, which is not enough for dW: 0 times
 //             a NaN or an infinity in their rows of x would be NaN in all of it.  dW's
-//             x is therefore a copy in which their rows are zeros: gradients of 4096 x
-//             2048 x 32768 979 us, 987 with x as it lies; of 1111 x 1160 x 50257 341 and
-//             339 (few tokens and rows off 64-byte lines were copied before, too).
+//             x is therefore a copy in which their rows are zeros.
 //
 // Bound by the matrix units at the power limit: loss of 8192 x 2048 x 32768 632 us
 // (1740 TFLOP/s), gradients of 4096 x 2048 x 32768 974 us (1690); with few tokens by
@@ -74,6 +72,9 @@ struct VocabParams {
   __nv_bfloat16* d;     // [T][ldd], 16-byte rows
   int ldd;
   bool split;           // d in two parts, rows t and T + t
+  const uint4* x;       // rows ldx8 16-byte pieces apart, to copy as dW's operand,
+  uint4* x_out;         // out_ld8 apart; or null
+  long long ldx8, out_ld8;
   float* df;            // or d in f32, [T][ldd] (few tokens)
   int32_t* dev_status;
   long long wait_limit;
@@ -86,6 +87,32 @@ __device__ __forceinline__ int target_of(const void* targets, bool i64, long lon
                           : static_cast<long long>(static_cast<const int32_t*>(targets)[t]);
   if (y == ignore) return -1;
   return y >= 0 && y < vocab ? static_cast<int>(y) : -2;
+}
+
+// Thread `at` of `step`: its share of the copy of rows x K8 16-byte pieces, `ld` apart, to
+// rows `out_ld` apart; `copies` of all, one behind the other.  With targets the rows of
+// tokens that do not count become zeros.  Four pieces are under way a thread.
+__device__ __forceinline__ void copy_pieces(const uint4* x, long long ld, int rows, int K8, uint4* out,
+                                            long long out_ld, int copies, const void* targets, bool i64,
+                                            long long ignore, int vocab, int at, int step) {
+  const int dt = step / K8, dk = step % K8;
+  int t = at / K8, k = at % K8;
+  while (t < rows) {
+    uint4 v[4];
+    long long to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      to[u] = t < rows ? t * out_ld + k : -1;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (t < rows && (!targets || target_of(targets, i64, ignore, vocab, t) >= 0)) v[u] = x[t * ld + k];
+      t += dt, k += dk;
+      if (k >= K8) k -= K8, ++t;
+    }
+    for (int c = 0; c < copies; ++c)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (to[u] >= 0) out[c * rows * out_ld + to[u]] = v[u];
+  }
 }
 
 // Joins (c, s) and (c2, s2), sums relative to 2^c.
@@ -172,6 +199,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // (forward) the groups' statistics, two tiles' in turn: [tile][group][row]
     const uint32_t stat = m.sEpi + quad * 2048 + lane * 8;
     int tcount = 0, parity = 0;
+    // dW's x, while the first tile is multiplied.  (A launch of its own costs 3 us:
+    // gradients of 512 x 2048 x 32768 153 us with it, 149 so and without any copy; a dW of
+    // eight tiles, which waits for its operands, reads the copy slower than what the
+    // products for d have just read, 16384 x 64 x 2048 113 and 100.)
+    if (BACK && p.x_out)
+      copy_pieces(p.x, p.ldx8, p.T, p.K >> 3, p.x_out, p.out_ld8, 1, p.targets, p.i64, p.ignore, p.vocab,
+                  (blockIdx.x * kEpiWarps + ew) * 32 + lane, gridDim.x * kEpiWarps * 32);
     for (int tau = pair; tau < total; tau += npairs, parity ^= 1) {
       int m0, n0;
       band_tile(tau, p.T, p.V, m0, n0);
@@ -783,28 +817,20 @@ constexpr int kCopyTokens = 256, kCopyWTokens = 2048;
 bool off_lines(const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % 64 || ld % 32; }
 int line_ld(int K) { return (K + 63) / 64 * 64; }
 
-// rows x K8 16-byte pieces, `ld` apart, to rows `out_ld` apart; `copies` of all, one
-// behind the other ([x; x] is the other operand of d's two parts in dW).  With targets
-// (of a vocabulary of `vocab`) the rows of tokens that do not count become zeros.
+// ([x; x], copied twice, is the other operand of d's two parts in dW.)
 __global__ void __launch_bounds__(256) vocab_copy_kernel(const uint4* x, long long ld, int rows, int K8,
                                                          int out_ld, int copies, const void* targets, bool i64,
                                                          long long ignore, int vocab, uint4* out) {
   pdl_trigger();
   pdl_wait();
-  const long long n = static_cast<long long>(rows) * K8, step = static_cast<long long>(gridDim.x) * 256;
-  for (long long i = blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-    const long long t = i / K8;
-    const int k = static_cast<int>(i - t * K8);
-    uint4 v = x[t * ld + k];
-    if (targets && target_of(targets, i64, ignore, vocab, static_cast<int>(t)) < 0) v = make_uint4(0, 0, 0, 0);
-    for (int c = 0; c < copies; ++c) out[(c * rows + t) * out_ld + k] = v;
-  }
+  copy_pieces(x, ld, rows, K8, out, out_ld, copies, targets, i64, ignore, vocab, blockIdx.x * 256 + threadIdx.x,
+              gridDim.x * 256);
 }
 // o's rows to `to`, on 128-byte boundaries; with `a` x's, those that do not count as zeros
 cudaError_t copy_rows(DenseOperand* o, void* to, int copies, const VocabBackward* a, cudaStream_t st) {
   const int ld = line_ld(o->cols);
   const long long n = static_cast<long long>(o->rows) * (o->cols / 8);
-  const unsigned blocks = static_cast<unsigned>(std::min<long long>((n + 255) / 256, 16 * num_sms()));
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((n + 255) / 256, 8 * num_sms()));
   const cudaError_t e = launch_pdl(vocab_copy_kernel, dim3(blocks), dim3(256), 0, st,
                                    static_cast<const uint4*>(o->ptr), o->ld / 8, o->rows, o->cols / 8, ld / 8,
                                    copies, a ? a->targets : nullptr, a && a->i64, a ? a->ignore : 0LL,
@@ -1157,10 +1183,14 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
   DenseOperand x{a.x, a.T, a.K, a.ldx};
   const float* const scale = a.per_token ? nullptr : a.dloss;
   cudaError_t e = cudaSuccess;
-  if (a.dW || (a.T >= kCopyTokens && off_lines(a.x, a.ldx)))
-    e = copy_rows(&x, base + l.x, l.split ? 2 : 1, &a, st);
+  // x is copied for its lines, for d's two parts, or for dW alone, which the pair kernel
+  // does on its way
+  const bool own_copy = l.split ? a.dW != nullptr : a.T >= kCopyTokens && off_lines(a.x, a.ldx);
+  const bool on_way = a.dW && !own_copy && !by_few(a.T, a.K, std::min(l.cols, a.V));
+  if (own_copy || (a.dW && !on_way)) e = copy_rows(&x, base + l.x, l.split ? 2 : 1, &a, st);
   DenseOperand xd = x;  // beside d's rows
   xd.rows = rows;
+  if (on_way) xd.ptr = base + l.x, xd.ld = line_ld(a.K);
   for (int v0 = 0; e == cudaSuccess && v0 < a.V; v0 += l.cols) {
     const int n = std::min(l.cols, a.V - v0);
     const char* W = static_cast<const char*>(a.W) + static_cast<size_t>(v0) * a.K * 2;
@@ -1169,6 +1199,10 @@ cudaError_t launch_vocab_backward(const VocabBackward& a, void* ws, cudaStream_t
     p.targets = a.targets, p.i64 = a.i64, p.ignore = a.ignore;
     p.lse = a.lse, p.z2 = 2.f * a.z_loss, p.gtok = a.per_token ? a.dloss : nullptr, p.weight = a.weight;
     p.d = d, p.ldd = l.cols, p.split = l.split;
+    if (on_way && v0 == 0) {
+      p.x = static_cast<const uint4*>(a.x), p.ldx8 = a.ldx / 8;
+      p.x_out = reinterpret_cast<uint4*>(base + l.x), p.out_ld8 = line_ld(a.K) / 8;
+    }
     p.dev_status = a.dev_status, p.wait_limit = a.wait_limit;
     DenseOperand Wp{W, n, a.K, a.K};
     const DenseOperand dp{d, rows, n, l.cols};
