@@ -166,17 +166,16 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr=1e-3, betas=(0.9, 0.
     tensors of one element (int32, float32), which a captured call reads anew.
     ``grad_scale`` (float32 [1] on the GPU) multiplies the gradients
     (mgg_adamw_step)."""
-    block._host.adamw_step(*_host_args(params, grads, exp_avg, exp_avg_sq, step, lr, betas, eps, weight_decay,
-                                       masters, exp_avg_scale, exp_avg_sq_scale, grad_scale))
+    block._host.adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], eps, weight_decay,
+                           masters, exp_avg_scale, exp_avg_sq_scale, grad_scale)
 
 
-def _host_args(params, grads, exp_avg, exp_avg_sq, step, lr, betas, *rest):
-    return params, grads, exp_avg, exp_avg_sq, step, lr, betas[0], betas[1], *rest
-
-
-def _version(t: torch.Tensor) -> int:
-    """How often t was written in place (a tensor of inference mode does not count)."""
-    return 0 if t.is_inference() else t._version
+def _versions(tensors) -> list:
+    """How often each was written in place (a tensor of inference mode does not count)."""
+    try:
+        return [t._version for t in tensors]
+    except RuntimeError:
+        return [0 if t.is_inference() else t._version for t in tensors]
 
 
 class AdamW:
@@ -198,48 +197,52 @@ class AdamW:
         self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = adamw_state(self.params, bits)
         self.masters = [p.detach().float() if master and p.dtype == torch.bfloat16 else None
                         for p in self.params]
-        self._seen = [_version(p) for p in self.params]     # versions that the masters stand for
+        self._seen = _versions(self.params)     # the params' versions that their masters stand for
         self.capturable = capturable
         device = self.params[0].device if self.params else "cpu"
         self.count = torch.zeros(1, dtype=torch.int32, device=device) if capturable else 0
 
     @torch.no_grad()
     def step(self, grad_scale: torch.Tensor | None = None) -> None:
+        grads = [p.grad for p in self.params]
         mixes: dict = {}
-        for i, p in enumerate(self.params):
-            if p.grad is not None:
-                mixes.setdefault((p.dtype, p.grad.dtype, self.masters[i] is None), []).append(i)
-        for i in (i for at in mixes.values() for i in at):
-            if self.masters[i] is not None and self._seen[i] != _version(self.params[i]):
+        for i, (p, g, w) in enumerate(zip(self.params, grads, self.masters)):
+            if g is not None:
+                mixes.setdefault((p.dtype, g.dtype, w is None), []).append(i)
+        seen = _versions(self.params)
+        late = [] if seen == self._seen else [i for i, (a, b) in enumerate(zip(seen, self._seen)) if a != b]
+        for i in late:
+            if grads[i] is not None and self.masters[i] is not None:
                 self._take_over(i)
         count = self.count if self.capturable else self.count + 1
         calls = []
         for (_, _, alone), at in mixes.items():
             def pick(t):
-                return None if t is None else [t[i] for i in at]
-            calls.append((pick(self.params), [self.params[i].grad for i in at], pick(self.exp_avg),
-                          pick(self.exp_avg_sq), count, self.lr, self.betas, self.eps, self.weight_decay,
-                          None if alone else pick(self.masters), pick(self.exp_avg_scale),
-                          pick(self.exp_avg_sq_scale), grad_scale))
+                return t if t is None or len(at) == len(t) else [t[i] for i in at]
+            calls.append((pick(self.params), pick(grads), pick(self.exp_avg), pick(self.exp_avg_sq), count, self.lr,
+                          self.betas, self.eps, self.weight_decay, None if alone else pick(self.masters),
+                          pick(self.exp_avg_scale), pick(self.exp_avg_sq_scale), grad_scale))
         # One call refuses before it updates anything.  Where something precedes a call
         # (another mix, the count on the GPU), all are checked first.  (Without a GPU
         # the first call refuses.)
         if (self.capturable or len(calls) > 1) and any(c[0][0].is_cuda for c in calls):
             for c in calls:
-                block._host.adamw_check(*_host_args(*c))
+                block._host.adamw_check(*c[:6], c[6][0], c[6][1], *c[7:])
         if self.capturable:
             self.count += 1
         for c in calls:
             adamw_step(*c)
         self.count = count
-        for i in (i for at in mixes.values() for i in at):
-            self._seen[i] = _version(self.params[i])
+        seen = _versions(self.params)
+        for i in late:
+            if grads[i] is None:        # (to be taken over when one comes)
+                seen[i] = self._seen[i]
+        self._seen = seen
 
     def _take_over(self, i: int) -> None:
         p, w = self.params[i].detach(), self.masters[i]
         # (what a param holds unchanged is its master rounded: that keeps its bits)
         w.copy_(torch.where(w.to(p.dtype) == p, w, p.to(w.dtype)))
-        self._seen[i] = _version(self.params[i])
 
     @torch.no_grad()
     def sync_masters(self) -> None:
@@ -251,6 +254,7 @@ class AdamW:
         for i, w in enumerate(self.masters):
             if w is not None:
                 self._take_over(i)
+        self._seen = _versions(self.params)
 
     def zero_grad(self) -> None:
         for p in self.params:
