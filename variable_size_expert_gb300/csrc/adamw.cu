@@ -2,8 +2,8 @@
 //   g = grad * scale;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
 //   p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
 // Bound by its bytes: 28 an element with bfloat16 weights and gradients, float32
-// masters and moments (60M elements 252 us, 98% of the measured copy rate); 14 with
-// float32 weights, bfloat16 gradients and 8-bit moments (120M elements 299 us, 83%:
+// masters and moments (60M elements 253 us, 98% of the measured copy rate); 14 with
+// float32 weights, bfloat16 gradients and 8-bit moments (120M elements 297 us, 84%:
 // the codes' instructions).  Many small tensors: the host, whose
 // checks take 0.1 us a tensor.
 //
