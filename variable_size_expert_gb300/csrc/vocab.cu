@@ -202,9 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t stat = m.sEpi + quad * 2048 + lane * 8;
     int tcount = 0, parity = 0;
     // dW's x, while the first tile is multiplied.  (A launch of its own costs 3 us:
-    // gradients of 512 x 2048 x 32768 153 us with it, 149 so and without any copy; a dW of
-    // eight tiles, which waits for its operands, reads the copy slower than what the
-    // products for d have just read, 16384 x 64 x 2048 113 and 100.)
+    // gradients of 512 x 2048 x 32768 153 us with it, 149 so and without any copy; with few
+    // columns, whose products are no longer than the copy, 16384 x 512 x 1024 101 and 95.)
     if (BACK && p.x_out)
       copy_pieces(p.x, p.ldx8, p.T, p.K >> 3, p.x_out, p.out_ld8, 1, p.targets, p.i64, p.ignore, p.vocab,
                   (blockIdx.x * kEpiWarps + ew) * 32 + lane, gridDim.x * kEpiWarps * 32);
